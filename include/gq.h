@@ -90,7 +90,7 @@ const char *gq_last_error_message(void);
  * bounds check of a GQ_DEBUG build failed (a library bug; those builds check the
  * indices the kernels derive from their arguments and never trap), else
  * GQ_ERR_INVALID_ARG if a length or position read on the device was out of range
- * (the INT8 KV-cache calls), else GQ_OK; reading clears it and, after a timeout, re-zeroes the
+ * (the KV-cache calls), else GQ_OK; reading clears it and, after a timeout, re-zeroes the
  * workspace counters of the device.  Synchronizes the current device first. */
 gq_status gq_last_error(void);
 
@@ -407,6 +407,113 @@ gq_status gq_attn_decode_i8(const float *q, const int8_t *k, const float *k_scal
                             const int8_t *v, const float *v_scale, const int32_t *lens,
                             float *out, int64_t B, int64_t Hq, int64_t Hkv, int64_t Tcap,
                             int64_t D, float softmax_scale, cudaStream_t stream);
+
+/* ---- 8-bit KV cache in pages: append, attention, eviction ---------------------------
+ *
+ * The second form of the cache: the codes are held in 8 bits (INT8, or the 8-bit
+ * floating-point type e4m3) with ONE f32 scale for each block of tokens and head, and
+ * the block -- a page of P tokens of one (sequence, KV head) -- is also the unit in
+ * which memory is handed out and tokens are dropped.  (xFasterTransformer, "2.2
+ * Effective KV cache Optimization", gives the 8-bit cache with a scale per token and
+ * head, above; pages, their scale, the score options and eviction are this library's.)
+ *
+ * gq_kv_pages describes one layer's cache.  It is read on the host during a call (the
+ * library keeps no pointer to it); the arrays are DEVICE pointers, 16-byte aligned:
+ *   k, v    codes [pages][P][D], one byte each; page x belongs to one (sequence, KV
+ *           head), which its table row says.  A code c stands for c * scale.
+ *   ks, vs  f32 [pages]: the page's scale for keys and for values
+ *   table   int32 [B][Hkv][NB]: the pages of (b, h) in order: slot s (the s-th token
+ *           held) is row s % P of page table[b][h][s / P].  All NB entries of a row
+ *           are pages that (b, h) owns; the caller fills them once.
+ *   base    int32 [B][Hkv][NB]: position of the page's first token (written by append);
+ *           the tokens of a page have consecutive positions
+ *   held    int32 [B]: tokens of the sequence in the cache BEFORE the step
+ *   seen    int32 [B]: position of the step's first token; held[b] without eviction,
+ *           more after it.  Positions stay below 2^30.
+ * A step's new tokens come packed: sequence b has rows cu[b] .. cu[b+1] - 1 of k, v, q
+ * and out (cu int32 [B+1], cu[0] = 0, T = cu[B] rows, at most max_n per sequence, zero
+ * allowed).  They take slots held[b], held[b]+1, .. and positions seen[b], seen[b]+1, ..
+ * Every call of a step reads held and seen as they were before it; the caller adds the
+ * new tokens to both once the step's layers are done.
+ * Sizes: D is 64 or 128; P is 16, 32, 64 or 128; NB * P < 2^30, B * Hkv * NB < 2^31,
+ * pages < 2^31, pages * P * D <= 2^37.  Lengths, table entries and cu are read on the
+ * device: a sequence for which they are out of range (held < 0, held + new > NB * P,
+ * new > max_n, cu decreasing or past T) is skipped by append and gives zero rows in the
+ * attention; a page outside [0, pages) is skipped, its tokens are seen by nobody;
+ * either makes the next gq_last_error() return GQ_ERR_INVALID_ARG. */
+typedef enum { GQ_KV_I8 = 0, GQ_KV_E4M3 = 1 } gq_kv_kind;
+
+typedef struct gq_kv_pages {
+    int64_t kind;   /* gq_kv_kind */
+    int64_t B, Hkv, D, P, NB, pages;
+    void *k, *v;
+    float *ks, *vs;
+    int32_t *table, *base;
+    const int32_t *held, *seen;
+} gq_kv_pages;
+
+/* Writes the step's keys and values k, v (f32; row t at k + t * ldk, [Hkv][D] inside; ldk,
+ * ldv multiples of 4, at least Hkv * D: slices of one product's output are fine).  For
+ * each page that gets tokens,
+ *     scale = max(old scale, amax / top)     top = 127 (INT8) or 448 (e4m3)
+ * with amax the largest magnitude of the new tokens in it, in f32; a page whose first
+ * token is written by this step has no old scale.  Every code of the page is the 8-bit
+ * value nearest to value / scale (of the exact quotient; ties to the even code; 0 when
+ * the scale is 0), where value is the f32 input for a new token and code * old scale for
+ * one held before: a page's held tokens are coded again when its scale grows, and stay
+ * as they are when it does not.  Appending the same step twice changes nothing. */
+gq_status gq_kv_pages_append(const gq_kv_pages *cache, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                             const int32_t *cu, int64_t T, int64_t max_n, cudaStream_t stream);
+
+/* Reads slots back as f32: the slots start[b] .. start[b] + cu[b+1] - cu[b] - 1 of
+ * sequence b into rows cu[b] .. of k and v ([T][Hkv][D], either may be NULL), as
+ * code * scale.  start int32 [B]; slots must lie in [0, NB * P). */
+gq_status gq_kv_pages_read(const gq_kv_pages *cache, const int32_t *start, const int32_t *cu, int64_t T, int64_t max_n,
+                           float *k, float *v, cudaStream_t stream);
+
+/* Which keys a query sees, and what is done to its scores.  A query at position p sees the
+ * key at position x if
+ *     x >= first  and  (x < prefix  or  (x <= p and (window == 0 or p - x < window)))
+ * and its score is  z = scale * (q . key);  z = cap * tanh(z / cap) if cap > 0;
+ * z -= slopes[head] * |p - x| if slopes is given.  Read on the host during the call. */
+typedef struct gq_attn_scores {
+    float scale;            /* usually 1 / sqrt(D) */
+    float cap;              /* 0: none */
+    int64_t window;         /* 0: none */
+    const float *slopes;    /* f32 [Hq], or NULL */
+    const int32_t *first;   /* int32 [T]: first position of each query's document, or NULL (0) */
+    const int32_t *prefix;  /* int32 [T]: end of the positions that all see, or NULL (0) */
+} gq_attn_scores;
+
+/* Attention of the step's queries (f32; row t at q + t * ldq, [Hq][D] inside, Hq = G * Hkv,
+ * G 1 .. 64; query head h reads KV head h / G) over the cache, the step's own tokens
+ * included (append them first): out row t at out + t * ldo, [Hq][D] inside, overwritten;
+ * ldq, ldo multiples of 4 and at least Hq * D.  A query that sees nothing gives a zero row.
+ * Arithmetic is f32 throughout: the 8-bit codes are widened exactly, query and softmax
+ * weights enter the tensor cores as two fp16 terms each.  Results are deterministic.
+ * weights_out (f32 [B][Hkv][NB], or NULL for none) receives, for the pages in use after
+ * the step, decay * weights_in + the page's share of the softmax summed over the step's
+ * queries and the G heads, and 0 for the other entries; weights_in may be weights_out,
+ * or NULL (0).  Uses the stream's workspace (grown on demand, as for the products;
+ * GQ_ERR_NO_MEMORY when that is not possible, e.g. while the stream is captured: run the
+ * call once before capturing). */
+gq_status gq_attn_pages(const gq_kv_pages *cache, const gq_attn_scores *scores, const float *q, int64_t ldq,
+                        const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
+                        const float *weights_in, float *weights_out, float decay, cudaStream_t stream);
+
+/* Drops pages by gathered weight.  For each (b, h) with n = ceil(held[b] / P) pages in use
+ * and n > budget: the first keep_first and the last keep_last pages stay, and of the others
+ * the budget - keep_first - keep_last with the largest weights (equal ones: the lower
+ * index).  Rows of table and base are reordered: the pages that stay, in order, then the
+ * dropped ones, in order (their memory is used again by later appends), then the unused
+ * ones; weights likewise, with 0 for the dropped.  held_out[b] = held[b] less the dropped
+ * tokens.  Rows with n <= budget are copied.  The outputs may be the inputs themselves
+ * (table_out = cache->table, ...) or separate arrays of the same shape, not overlapping
+ * otherwise.  weights are f32 [B][Hkv][NB], finite.  keep_first >= 0, keep_last >= 1 (the
+ * page being filled stays), keep_first + keep_last <= budget, NB <= 16384. */
+gq_status gq_kv_pages_evict(const gq_kv_pages *cache, const float *weights, int64_t budget, int64_t keep_first,
+                            int64_t keep_last, int32_t *table_out, int32_t *base_out, float *weights_out,
+                            int32_t *held_out, cudaStream_t stream);
 
 /* ---- verification --------------------------------------------------------------- */
 

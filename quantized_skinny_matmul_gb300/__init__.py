@@ -48,6 +48,21 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int64
 _S = ctypes.c_int
 
+GQ_KV_I8 = 0
+GQ_KV_E4M3 = 1
+
+
+class KVPagesStruct(ctypes.Structure):
+    """gq_kv_pages."""
+    _fields_ = ([(n, _I) for n in ("kind", "B", "Hkv", "D", "P", "NB", "pages")]
+                + [(n, _P) for n in ("k", "v", "ks", "vs", "table", "base", "held", "seen")])
+
+
+class AttnScoresStruct(ctypes.Structure):
+    """gq_attn_scores."""
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", _I),
+                ("slopes", _P), ("first", _P), ("prefix", _P)]
+
 # name -> (argtypes, restype); the signatures of include/gq.h
 SIGNATURES = {
     "gq_debug_wait_timeout": ([ctypes.c_uint32, _P], _S),
@@ -55,6 +70,11 @@ SIGNATURES = {
     "gq_kv_quantize_i8": ([_P, _P, _P, _I, _I, _P], _S),
     "gq_kv_append_i8": ([_P, _P, _P, _P, _I, _I, _I, _I, _P], _S),
     "gq_attn_decode_i8": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P], _S),
+    "gq_kv_pages_append": ([ctypes.POINTER(KVPagesStruct), _P, _I, _P, _I, _P, _I, _I, _P], _S),
+    "gq_kv_pages_read": ([ctypes.POINTER(KVPagesStruct), _P, _P, _I, _I, _P, _P, _P], _S),
+    "gq_attn_pages": ([ctypes.POINTER(KVPagesStruct), ctypes.POINTER(AttnScoresStruct), _P, _I, _P, _I, _I, _I, _P, _I,
+                       _P, _P, ctypes.c_float, _P], _S),
+    "gq_kv_pages_evict": ([ctypes.POINTER(KVPagesStruct), _P, _I, _I, _I, _P, _P, _P, _P, _P], _S),
     "gq_abi_version": ([], ctypes.c_int),
     "gq_status_string": ([_S], ctypes.c_char_p),
     "gq_last_error_message": ([], ctypes.c_char_p),
@@ -368,6 +388,119 @@ def gq_attn_decode_i8(q, k, k_scale, v, v_scale, lens, out, B: int, Hq: int, Hkv
            "gq_attn_decode_i8")
 
 
+def gq_kv_pages_append(cache, k, ldk: int, v, ldv: int, cu, T: int, max_n: int, stream=None) -> None:
+    """``cache``: a KVPages; k, v: packed rows (first row's tensor or address) of row strides ldk, ldv."""
+    _check(lib().gq_kv_pages_append(_struct(cache), _rows_ptr(k), ldk, _rows_ptr(v), ldv, _ptr(cu), T, max_n,
+                                    _stream(stream)), "gq_kv_pages_append")
+
+
+def gq_kv_pages_read(cache, start, cu, T: int, max_n: int, k, v, stream=None) -> None:
+    _check(lib().gq_kv_pages_read(_struct(cache), _ptr(start), _ptr(cu), T, max_n, _ptr(k), _ptr(v), _stream(stream)),
+           "gq_kv_pages_read")
+
+
+def gq_attn_pages(cache, scores, q, ldq: int, cu, T: int, max_n: int, Hq: int, out, ldo: int, weights_in, weights_out,
+                  decay: float, stream=None) -> None:
+    _check(lib().gq_attn_pages(_struct(cache), _struct(scores), _rows_ptr(q), ldq, _ptr(cu), T, max_n, Hq,
+                               _rows_ptr(out), ldo, _ptr(weights_in), _ptr(weights_out), decay, _stream(stream)),
+           "gq_attn_pages")
+
+
+def gq_kv_pages_evict(cache, weights, budget: int, keep_first: int, keep_last: int, table_out, base_out, weights_out,
+                      held_out, stream=None) -> None:
+    _check(lib().gq_kv_pages_evict(_struct(cache), _ptr(weights), budget, keep_first, keep_last, _ptr(table_out),
+                                   _ptr(base_out), _ptr(weights_out), _ptr(held_out), _stream(stream)),
+           "gq_kv_pages_evict")
+
+
+def _struct(x):
+    return x if x is None else x.by_ref
+
+
+def _rows_ptr(t) -> int:
+    """Address of packed rows: each row contiguous, any stride between rows."""
+    if t is None:
+        return 0
+    if isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _row_stride(x, width: int, name: str) -> int:
+    """The stride between the packed f32 rows of x ([T, width] or [T, heads, D])."""
+    import torch
+    if x.dtype != torch.float32:
+        raise ValueError(f"{name}: expected float32, got {x.dtype}")
+    n = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{name}: each row must be contiguous")
+        n *= size
+    if n != width:
+        raise ValueError(f"{name}: rows of {n} values, expected {width}")
+    return x.stride(0) if x.shape[0] > 1 else width
+
+
+class KVPages:
+    """One layer's 8-bit KV cache in pages (gq_kv_pages): the tensors, kept alive, and their struct.
+
+    k, v: one-byte codes [pages, P, D]; ks, vs: f32 [pages]; table, base: int32 [B, Hkv, NB];
+    held, seen: int32 [B], the tokens held and the next position before the step.
+    """
+
+    def __init__(self, kind, k, v, ks, vs, table, base, held, seen):
+        pages, P, D = k.shape
+        B, Hkv, NB = table.shape
+        _shape(k, (pages, P, D), None, "k")
+        _shape(v, (pages, P, D), None, "v")
+        for t, name in ((ks, "ks"), (vs, "vs")):
+            _shape(t, (pages,), "float32", name)
+        for t, name in ((table, "table"), (base, "base")):
+            _shape(t, (B, Hkv, NB), "int32", name)
+        for t, name in ((held, "held"), (seen, "seen")):
+            _shape(t, (B,), "int32", name)
+        self.kind, self.B, self.Hkv, self.D, self.P, self.NB, self.pages = kind, B, Hkv, D, P, NB, pages
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        self.table, self.base, self.held, self.seen = table, base, held, seen
+        self.struct = KVPagesStruct(kind, B, Hkv, D, P, NB, pages, *(_ptr(t) for t in (k, v, ks, vs, table, base, held,
+                                                                                    seen)))
+        self.by_ref = ctypes.pointer(self.struct)
+
+    @classmethod
+    def empty(cls, B: int, Hkv: int, D: int, tokens: int, page: int = 32, kind: int = GQ_KV_I8, device="cuda"):
+        """A cache with room for `tokens` tokens per sequence, each head owning its pages."""
+        import torch
+        NB = -(-tokens // page)
+        n = B * Hkv * NB
+        codes = [torch.zeros((n, page, D), dtype=torch.int8 if kind == GQ_KV_I8 else torch.uint8, device=device)
+                 for _ in range(2)]
+        scales = [torch.zeros(n, dtype=torch.float32, device=device) for _ in range(2)]
+        table = torch.arange(n, dtype=torch.int32, device=device).reshape(B, Hkv, NB)
+        ints = [torch.zeros(B, dtype=torch.int32, device=device) for _ in range(2)]
+        return cls(kind, *codes, *scales, table, torch.zeros_like(table), *ints)
+
+
+class AttnScores:
+    """What attn_pages does to scores (gq_attn_scores); tensors are kept alive here."""
+
+    def __init__(self, scale: float, cap: float = 0.0, window: int = 0, slopes=None, first=None, prefix=None):
+        for t, dtype, name in ((slopes, "float32", "slopes"), (first, "int32", "first"), (prefix, "int32", "prefix")):
+            if t is not None:
+                _shape(t, tuple(t.shape), dtype, name)
+        self.slopes, self.first, self.prefix = slopes, first, prefix
+        self.struct = AttnScoresStruct(scale, cap, window, _ptr(slopes), _ptr(first), _ptr(prefix))
+        self.by_ref = ctypes.pointer(self.struct)
+
+
+def _shape(t, shape, dtype, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is None and t.element_size() != 1 or dtype is not None and str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name}: wrong dtype {t.dtype}")
+
+
 # ---------------------------------------------------------------------------
 # allocating helpers (torch tensors in, torch tensors out)
 # ---------------------------------------------------------------------------
@@ -570,3 +703,56 @@ def attn_decode_i8(q, k, k_scale, v, v_scale, lens, softmax_scale=None, out=None
         out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
     gq_attn_decode_i8(q, k, k_scale, v, v_scale, lens, out, B, Hq, Hkv, Tcap, D, softmax_scale)
     return out
+
+
+def kv_pages_append(cache: KVPages, k, v, cu, max_n: int) -> None:
+    """Write a step's packed keys and values (f32 [T, Hkv * D] or [T, Hkv, D], rows may be strided)."""
+    T, width = k.shape[0], cache.Hkv * cache.D
+    if v.shape[0] != T:
+        raise ValueError(f"v has {v.shape[0]} rows, k {T}")
+    _shape(cu, (cache.B + 1,), "int32", "cu")
+    gq_kv_pages_append(cache, k, _row_stride(k, width, "k"), v, _row_stride(v, width, "v"), cu, T, max_n)
+
+
+def kv_pages_read(cache: KVPages, start, cu, T: int, max_n: int):
+    """Slots start[b] .. of each sequence as f32: (k, v), each [T, Hkv, D], packed by cu."""
+    import torch
+    _shape(start, (cache.B,), "int32", "start")
+    _shape(cu, (cache.B + 1,), "int32", "cu")
+    k, v = (torch.empty((T, cache.Hkv, cache.D), dtype=torch.float32, device=cache.k.device) for _ in range(2))
+    gq_kv_pages_read(cache, start, cu, T, max_n, k, v)
+    return k, v
+
+
+def attn_pages(cache: KVPages, q, cu, max_n: int, scores: AttnScores, weights=None, decay: float = 1.0, out=None):
+    """Attention of a step's packed queries (f32 [T, Hq * D] or [T, Hq, D]) over the cache: f32 [T, Hq, D].
+
+    With ``weights`` (f32 [B, Hkv, NB], what each page gathered so far) the result is
+    (out, new weights), the new ones being decay * weights + this step's shares.
+    """
+    import torch
+    T = q.shape[0]
+    width = q[0].numel()
+    Hq = width // cache.D
+    _shape(cu, (cache.B + 1,), "int32", "cu")
+    for t, n, name in ((scores.slopes, Hq, "slopes"), (scores.first, T, "first"), (scores.prefix, T, "prefix")):
+        if t is not None:
+            _shape(t, (n,), str(t.dtype)[6:], name)
+    if out is None:
+        out = torch.empty((T, Hq, cache.D), dtype=torch.float32, device=q.device)
+    new = None
+    if weights is not None:
+        _shape(weights, (cache.B, cache.Hkv, cache.NB), "float32", "weights")
+        new = torch.empty_like(weights)
+    gq_attn_pages(cache, scores, q, _row_stride(q, Hq * cache.D, "q"), cu, T, max_n, Hq, out,
+                  _row_stride(out, Hq * cache.D, "out"), weights, new, decay)
+    return out if weights is None else (out, new)
+
+
+def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, keep_last: int = 1):
+    """Drop the pages that gathered least until `budget` are left: (table, base, weights, held), new tensors."""
+    import torch
+    _shape(weights, (cache.B, cache.Hkv, cache.NB), "float32", "weights")
+    outs = [torch.empty_like(t) for t in (cache.table, cache.base, weights, cache.held)]
+    gq_kv_pages_evict(cache, weights, budget, keep_first, keep_last, *outs)
+    return tuple(outs)

@@ -1,0 +1,837 @@
+// attn_pages.cu -- attention over the paged 8-bit KV cache, for few query rows per KV head.
+//
+// For a query at position p and the keys at positions x it sees (definition: gq.h),
+//     z_x = f(scale * q . k_x, p, x),   out = sum_x softmax(z)_x v_x,
+// with k_x = code * (the page's scale).  One pass over the cache with a running maximum and
+// sum: a unit of 32 tokens gives scores z (base 2), the maximum m grows to m', the sums so
+// far are scaled by 2^(m - m'), and the unit's 2^(z - m') join the denominator and, times
+// the values, the output.
+//
+// Both products run as m16n8k16 fp16 MMAs with f32 accumulation at f32 accuracy: the codes
+// widen to fp16 exactly, and a query row (scaled by a power of two) or a row of weights is
+// carried as two fp16 terms, hi + lo.  The 16 MMA rows are 8 query rows' hi terms and the
+// same rows' lo terms, so the accumulator fragment of the scores (a lane holds hi and lo of
+// the same row and tokens) turns into the A fragment of the weights in registers.  The order
+// in which the MMAs take positions within a row (D) and tokens within a unit is chosen so
+// that every lane reads its 16-byte chunks of codes as they lie in shared memory.
+//
+// Work is divided evenly, not by sequence: the (sequence, head, row tile) items' units are
+// laid out in a line, every CTA takes an equal piece of it, and items cut at a piece's end
+// are joined by the CTA that finishes last, in the order of the pieces (so the result does
+// not depend on timing).  A producer warp streams the units' pages through a ring of
+// shared-memory slots (tensor copies, 128-byte swizzle) and puts each unit's scales and
+// positions beside them; four consumer warps take the units in turn, each with its own
+// running maximum and sums, joined at the end of the item.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gq_common.cuh"
+#include "gq_internal.h"
+#include "kv_pages.cuh"
+
+namespace gq {
+namespace {
+
+#define KV_TRY(expr)                  \
+    do {                              \
+        gq_status _st = (expr);       \
+        if (_st != GQ_OK) return _st; \
+    } while (0)
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int UNIT = 32;                    // tokens per unit
+constexpr int W = 4;                        // consumer warps
+constexpr int CONSUMERS = W * 32, THREADS = CONSUMERS + 32;
+constexpr int ROWS = 8;                     // query rows of an item
+
+struct RowsParams {
+    PagesView c;
+    const float *q;
+    float *out;
+    const int32_t *cu;
+    const float *slopes;
+    const int32_t *first, *prefix;
+    float *parts;               // [CTA][2][ROWS][D] sums, then [CTA][2][ROWS][2] maximum and denominator
+    float *part_ml;
+    int *counters;              // per CTA: pieces of the item cut at its end that are done
+    float *glse;                // [T * Hq][NG] log2 of the weight sums by group, or null
+    float *lse;                 // [T * Hq] log2 of the denominators
+    int64_t ldq, ldo, window;
+    int T, max_n, Hq, G, NG, lgP, lgGroup;
+    float scale, cap;
+};
+
+__host__ __device__ constexpr int slots_of(int D) { return D == 128 ? 11 : 24; }   // two CTAs per SM
+
+struct UnitMeta {               // beside each slot: scales and first positions of the two halves
+    float ks[2], vs[2];
+    int base[2];
+    int live;                   // tokens of the unit that are held (0 .. 32)
+    int lost;                   // bit i: half i has no usable page
+};
+
+struct RowsSmem {
+    uint64_t full[24], empty[24];
+    UnitMeta meta[24];
+    float ml[2][W][ROWS][2];    // [parity]: maximum and denominator of each warp
+    int64_t start, total;       // line position of the sequence that the CTA starts in
+    int start_b, last;
+    int64_t warp_sum[THREADS / 32];
+};
+
+template <int D>
+__host__ __device__ constexpr size_t rows_smem_bytes() {
+    return 1024 + (size_t)slots_of(D) * UNIT * D * 2 + (size_t)W * ROWS * D * 4 + sizeof(RowsSmem);
+}
+
+__device__ __forceinline__ uint4 sh_ld128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 sh_ld64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh: the continued fraction x / (1 + x^2 / (3 + x^2 / (5 + ...))) cut after the fifth level for
+// |x| <= 1 (off by 1e-7 relative at 1, less below), 1 - 2 / (e^2x + 1) beyond.
+__device__ __forceinline__ float tanh_f32(float x) {
+    const float u = x * x;
+    const float small = x * fmaf(u, 105.0f + u, 945.0f) * __frcp_rn(fmaf(u, fmaf(15.0f, u, 420.0f), 945.0f));
+    const float a = fabsf(x);
+    if (a <= 1.0f) return small;
+    const float t = 1.0f - 2.0f * __frcp_rn(ex2(2.0f * LOG2E * a) + 1.0f);
+    return x < 0.0f ? -t : t;
+}
+
+// The two fp16 terms of two values.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// The four codes of a word as two exact fp16 pairs.
+template <int KIND>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &p01, uint32_t &p23) {
+    if constexpr (KIND == GQ_KV_I8) q8_to_f16x2(w, p01, p23);
+    else e4m3x4_to_f16x2(w, p01, p23);
+}
+// Byte j of x and byte j of y as one exact fp16 pair, j = 0 .. 3.
+template <int KIND>
+__device__ __forceinline__ void widen_pairs(uint32_t x, uint32_t y, uint32_t (&o)[4]) {
+    if constexpr (KIND == GQ_KV_I8) {
+        x ^= 0x80808080u;
+        y ^= 0x80808080u;
+        const uint32_t i01 = __byte_perm(x, y, 0x5140), i23 = __byte_perm(x, y, 0x7362);
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+        uint32_t t[4] = {__byte_perm(i01, 0x64646464u, 0x4140), __byte_perm(i01, 0x64646464u, 0x4342),
+                         __byte_perm(i23, 0x64646464u, 0x4140), __byte_perm(i23, 0x64646464u, 0x4342)};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t[i]), off);
+            o[i] = *reinterpret_cast<uint32_t *>(&h);
+        }
+    } else {
+        e4m3x4_to_f16x2(__byte_perm(x, y, 0x5140), o[0], o[1]);
+        e4m3x4_to_f16x2(__byte_perm(x, y, 0x7362), o[2], o[3]);
+    }
+}
+
+// ---- the units of a sequence ------------------------------------------------------------
+// Slots that some query of the step can see lie in [0, pre) and [start, n): key positions are
+// at least their slot number and distinct, below seen + n, so the slots whose position is at
+// least X number at most seen + new - X.
+struct Span {
+    int pre, start, units;   // units [0, pre) and [start, pre's end ..): `units` in all
+};
+
+__device__ __forceinline__ Span span_of(const RowsParams &p, const SeqStep &s) {
+    Span r;
+    const int n = s.held + s.n, end = (n + UNIT - 1) >> 5;
+    int lo = 0, pre = 0, first = 0;
+    if (s.n <= ROWS) {   // few tokens: look at each one's own range
+        if (p.first) {
+            first = 0x7fffffff;
+            for (int i = 0; i < s.n; i++) first = min(first, p.first[s.t0 + i]);
+        }
+        if (p.prefix)
+            for (int i = 0; i < s.n; i++) pre = max(pre, p.prefix[s.t0 + i]);
+    } else if (p.prefix) {
+        pre = n;
+    }
+    if (first > 0) lo = (int)max((int64_t)0, (int64_t)s.held - s.seen + first);
+    if (p.window > 0) lo = (int)max((int64_t)lo, (int64_t)s.held - p.window + 1);
+    r.start = min(lo, n - 1) >> 5;
+    r.pre = min((min(max(pre, 0), n) + UNIT - 1) >> 5, r.start);
+    r.units = r.pre + end - r.start;
+    return r;
+}
+
+// Where a piece of work is: the item (sequence b, head h, row tile) and its sequence's data.
+struct Cursor {
+    int b, h, tile, tiles;
+    SeqStep s;
+    Span u;
+};
+
+__device__ __forceinline__ void load_seq(const RowsParams &p, Cursor &k) {
+    k.s = seq_step(p.c, p.cu, k.b, p.T, p.max_n);
+    if (k.s.bad) {   // rows of an unusable sequence: one unit that nobody sees, a zero output
+        const int t1 = p.cu[k.b + 1];
+        const bool rows = k.s.t0 >= 0 && t1 > k.s.t0 && t1 <= p.T && t1 - k.s.t0 <= p.max_n;
+        k.s.n = rows ? t1 - k.s.t0 : 0;
+        k.s.held = -k.s.n;   // no tokens
+        k.s.seen = 0;
+        k.u.pre = k.u.start = 0;
+        k.u.units = 1;
+    } else if (k.s.n > 0) {
+        k.u = span_of(p, k.s);
+    }
+    k.tiles = (k.s.n * p.G + ROWS - 1) / ROWS;
+}
+
+__device__ __forceinline__ void next_item(const RowsParams &p, Cursor &k) {
+    if (++k.tile < k.tiles) return;
+    k.tile = 0;
+    if (++k.h < p.c.Hkv) return;
+    k.h = 0;
+    do {
+        if (++k.b >= p.c.B) return;
+        load_seq(p, k);
+    } while (k.tiles == 0);
+}
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(THREADS, 2)
+    attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                           const RowsParams p) {
+    constexpr int SLOTS = slots_of(D), HALF = UNIT * D;      // bytes of a unit's keys
+    constexpr int KS = D / 16;                               // MMA steps of a score
+    constexpr int RUN = D / 4;                               // positions per lane
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *red = reinterpret_cast<float *>(ring + (size_t)SLOTS * 2 * HALF);          // [W][ROWS][D]
+    RowsSmem &sm = *reinterpret_cast<RowsSmem *>(red + W * ROWS * D);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PagesView &c = p.c;
+
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int s = 0; s < SLOTS; s++) {
+            mbar_init(smem_addr(sm.full + s), 1);
+            mbar_init(smem_addr(sm.empty + s), 1);
+        }
+        fence_barrier_init();
+    }
+    pdl_wait();
+
+    // ---- this CTA's piece of the line of units
+    {
+        const int per = (c.B + THREADS - 1) / THREADS, b0 = tid * per, b1 = min(c.B, b0 + per);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; b++) {
+            Cursor k;
+            k.b = b;
+            load_seq(p, k);
+            if (k.s.bad) atomicOr(c.status, STATUS_RANGE);
+            if (k.tiles) mine += (int64_t)k.tiles * c.Hkv * k.u.units;
+        }
+        int64_t inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t t = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += t;
+        }
+        if (lane == 31) sm.warp_sum[warp] = inc;
+        if (tid == 0) sm.start_b = -1;
+        __syncthreads();
+        int64_t before = inc - mine, total = 0;
+        for (int w = 0; w < THREADS / 32; w++) {
+            if (w < warp) before += sm.warp_sum[w];
+            total += sm.warp_sum[w];
+        }
+        const int64_t piece = max((int64_t)W, (total + gridDim.x - 1) / gridDim.x), lo = piece * blockIdx.x;
+        if (lo >= before && lo < before + mine) {
+            for (int b = b0; b < b1; b++) {
+                Cursor k;
+                k.b = b;
+                load_seq(p, k);
+                const int64_t u = k.tiles ? (int64_t)k.tiles * c.Hkv * k.u.units : 0;
+                if (lo < before + u) {
+                    sm.start_b = b;
+                    sm.start = before;
+                    break;
+                }
+                before += u;
+            }
+        }
+        if (tid == 0) sm.total = total;
+        __syncthreads();
+    }
+    const int64_t total = sm.total, piece = max((int64_t)W, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t lo = piece * blockIdx.x, hi = min(total, lo + piece);
+    if (lo >= hi) return;
+    Cursor k;
+    k.b = sm.start_b;
+    load_seq(p, k);
+    int64_t item0;   // line position of the item's first unit
+    {
+        const int64_t i = (lo - sm.start) / k.u.units;
+        k.tile = (int)(i % k.tiles);
+        k.h = (int)(i / k.tiles);
+        item0 = sm.start + i * k.u.units;
+    }
+
+    // ---------------------------------------------------------------- producer
+    if (warp == W) {
+        const uint64_t policy = l2_evict_first_policy();
+        int count = 0;
+        bool ok = true;
+        const int rows16 = D / 8;   // 128-byte pool rows of 16 tokens
+        for (int64_t at = lo; at < hi && ok;) {
+            const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
+            const int64_t trow = ((int64_t)k.b * c.Hkv + k.h) * c.NB;
+            const int n = k.s.held + k.s.n;
+            for (int ub = u0; ub < u1 && ok; ub += 32) {
+                // each lane looks up one unit: its pages, their scales and positions
+                const int u = ub + lane;
+                const int slot = (u < k.u.pre ? u : k.u.start + u - k.u.pre) * UNIT;
+                UnitMeta m;
+                int page[2] = {-1, -1};
+                m.lost = 0;
+                m.live = u < u1 ? max(0, min(UNIT, n - slot)) : 0;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    m.ks[i] = m.vs[i] = 0.0f;
+                    m.base[i] = 0;
+                    if (m.live > 16 * i) {
+                        const int j = (slot + 16 * i) >> p.lgP;
+                        const int pg = __ldg(c.table + trow + j);
+                        if ((unsigned)pg < (unsigned)c.pages) {
+                            page[i] = pg;
+                            m.ks[i] = __ldg(c.ks + pg);
+                            m.vs[i] = __ldg(c.vs + pg);
+                            m.base[i] = __ldg(c.base + trow + j) + ((slot + 16 * i) & (c.P - 1));
+                        } else {
+                            atomicOr(c.status, STATUS_RANGE);
+                            m.base[i] = 0x7f000000;   // a position nobody sees
+                            m.lost |= 1 << i;
+                        }
+                    }
+                }
+                const int todo = min(32, u1 - ub);
+                for (int i = 0; i < todo; i++) {
+                    const int sl = count % SLOTS;
+                    if (count >= SLOTS)
+                        ok = mbar_wait(smem_addr(sm.empty + sl), (uint32_t)((count / SLOTS - 1) & 1), c.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == i) {
+                        const uint32_t bar = smem_addr(sm.full + sl);
+                        const uint32_t dst = smem_addr(ring + (size_t)sl * 2 * HALF);
+                        sm.meta[sl] = m;
+                        const int inpage = slot & (c.P - 1);
+                        if (c.P >= UNIT) {
+                            mbar_arrive_expect_tx(bar, page[0] >= 0 ? 2 * HALF : 0);
+                            if (page[0] >= 0) {
+                                const int row = (int)(((int64_t)page[0] * c.P + inpage) * D / 128);
+                                tma_rows(dst, &kmap, row, bar, policy);
+                                tma_rows(dst + HALF, &vmap, row, bar, policy);
+                            }
+                        } else {
+                            mbar_arrive_expect_tx(bar, ((page[0] >= 0) + (page[1] >= 0)) * HALF);
+#pragma unroll
+                            for (int g = 0; g < 2; g++)
+                                if (page[g] >= 0) {
+                                    const int row = (int)((int64_t)page[g] * rows16);
+                                    tma_rows(dst + g * (HALF / 2), &kmap, row, bar, policy);
+                                    tma_rows(dst + HALF + g * (HALF / 2), &vmap, row, bar, policy);
+                                }
+                        }
+                    }
+                    __syncwarp();
+                    count++;
+                }
+            }
+            at = item0 + u1;
+            if (u1 == k.u.units) {
+                item0 += k.u.units;
+                if (at < hi) next_item(p, k);
+            }
+        }
+        // stay until every copy issued has landed: the CTA never ends with a copy in flight
+        for (int i = max(0, count - SLOTS); i < count; i++)
+            mbar_wait(smem_addr(sm.full + i % SLOTS), (uint32_t)((i / SLOTS) & 1), c.status);
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int g8 = lane >> 2, t = lane & 3;
+    int count = 0, parity = 0;
+    bool failed = false;
+    for (int64_t at = lo; at < hi;) {
+        const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
+        // ---- the query row of this lane: row tile * 8 + g8 is token r / G, head r % G of the group
+        const int r = k.tile * ROWS + g8;
+        const bool real = r < k.s.n * p.G;
+        const int ti = k.s.t0 + (real ? r / p.G : 0), head = k.h * p.G + (real ? r % p.G : 0);
+        const int qpos = k.s.seen + ti - k.s.t0;
+        int seelo = 0, pre = 0;   // sees x >= first and (x < pre or seelo <= x <= qpos)
+        int firstp = 0;
+        float slope = 0.0f;
+        if (p.first) firstp = __ldg(p.first + ti);
+        if (p.prefix) pre = min(__ldg(p.prefix + ti), 1 << 30);
+        if (p.slopes) slope = __ldg(p.slopes + head) * LOG2E;
+        if (p.window > 0) seelo = (int)max((int64_t)0, (int64_t)qpos - p.window + 1);
+        seelo = max(seelo, firstp);
+        uint32_t qa[KS][4];
+        float f;   // what turns a raw product into z (base 2), or into z / cap
+        {
+            const float4 *qr = reinterpret_cast<const float4 *>(p.q + (int64_t)ti * p.ldq + (int64_t)head * D + RUN * t);
+            float4 v[KS];
+            float am = 0.0f;
+#pragma unroll
+            for (int i = 0; i < KS; i++) {
+                v[i] = real ? __ldg(qr + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                am = fmaxf(am, absmax4(v[i]));
+            }
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            // a power of two takes the row's largest magnitude into [2^14, 2^15)
+            const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255u) - 126, -100), 126);
+            const float up = __uint_as_float((uint32_t)(15 - ex + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < KS; i++) {
+                split2(v[i].x * up, v[i].y * up, qa[i][0], qa[i][1]);
+                split2(v[i].z * up, v[i].w * up, qa[i][2], qa[i][3]);
+            }
+            f = __uint_as_float((uint32_t)(ex - 15 + 127) << 23) * p.scale;
+            f = p.cap > 0.0f ? f / p.cap : f * LOG2E;
+        }
+        const float cap2 = p.cap * LOG2E;
+        // a unit with all positions in [see_all_lo, see_all_hi] is seen whole by every row
+        int all_lo = real ? seelo : 0, all_hi = real ? qpos : 0x7fffffff;
+#pragma unroll
+        for (int m = 4; m <= 16; m <<= 1) {
+            all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, m));
+            all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, m));
+        }
+        float o[2 * KS][4];
+#pragma unroll
+        for (int i = 0; i < 2 * KS; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float mrow = -INFINITY, lrow = 0.0f;
+        int vex = -100;   // the sums are in units of 2^(vex - 14)
+
+        // unit u of the item is unit count + u - u0 of this CTA; warp w takes every fourth
+        for (int u = u0 + ((warp - count) & (W - 1)); u < u1; u += W) {
+            const int i = count + u - u0, sl = i % SLOTS;
+            if (failed) break;   // a wait gave up: no further ones
+            const bool got = mbar_wait(smem_addr(sm.full + sl), (uint32_t)((i / SLOTS) & 1), c.status);
+            failed = !__all_sync(0xffffffffu, got);
+            if (failed) break;
+            const uint32_t kb = smem_addr(ring + (size_t)sl * 2 * HALF), vb = kb + HALF;
+            const UnitMeta &m = sm.meta[sl];
+            const int live = m.live;
+            // ---- scores: columns 8j + n are the unit's tokens, k the positions in chunk order
+            float s[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const int tok = 8 * j + g8;
+#pragma unroll
+                for (int hh = 0; hh < D / 64; hh++) {
+                    uint32_t a;
+                    if (D == 128) a = kb + tok * 128 + (((2 * t + hh) ^ (tok & 7)) << 4);
+                    else a = kb + (tok >> 1) * 128 + (((4 * (tok & 1) + t) ^ ((tok >> 1) & 7)) << 4);
+                    const uint4 w4 = sh_ld128(a);
+                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        uint32_t b0, b1;
+                        widen4<KIND>(w[x], b0, b1);
+                        mma_f16_16x8x16(acc, qa[4 * hh + x][0], qa[4 * hh + x][1], qa[4 * hh + x][2], qa[4 * hh + x][3], b0, b1);
+                    }
+                }
+                s[j][0] = acc[0] + acc[2];
+                s[j][1] = acc[1] + acc[3];
+            }
+            // ---- scale, cap, bias, mask
+            const int base0 = m.base[0], base1 = m.base[1];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float fk = f * m.ks[j >> 1];
+                const int x0 = (j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    float z = s[j][e] * fk;
+                    if (p.cap > 0.0f) z = cap2 * tanh_f32(z);
+                    if (p.slopes) z -= slope * (float)abs(qpos - (x0 + e));
+                    s[j][e] = z;
+                }
+            }
+            const bool whole = live == UNIT && base0 >= all_lo && base1 >= all_lo && base0 + 15 <= all_hi &&
+                               base1 + 15 <= all_hi;   // warp-uniform
+            if (!whole) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int x = (j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t + e;
+                        const bool see = 8 * j + 2 * t + e < live && x >= firstp && (x < pre || (x >= seelo && x <= qpos));
+                        s[j][e] = see ? s[j][e] : -INFINITY;
+                    }
+            }
+            // ---- the running maximum
+            float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])),
+                             fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mnew = fmaxf(mrow, mx), msafe = mnew == -INFINITY ? 0.0f : mnew;
+            const float vs0 = m.vs[0], vs1 = m.vs[1];
+            const int ve = max(vex, min(max((int)((__float_as_uint(fmaxf(vs0, vs1)) >> 23) & 255u) - 126, -100), 126));
+            if (__any_sync(0xffffffffu, mnew > mrow) || ve != vex) {
+                const float a = ex2(mrow - msafe);   // 0 while nothing was seen
+                lrow *= a;
+                // 2^(vex - ve): exact, 0 when it would underflow
+                const float av = a * (vex - ve < -126 ? 0.0f : __uint_as_float((uint32_t)(vex - ve + 127) << 23));
+#pragma unroll
+                for (int n = 0; n < 2 * KS; n++) {
+                    o[n][0] *= av;
+                    o[n][1] *= av;
+                    o[n][2] *= av;
+                    o[n][3] *= av;
+                }
+                mrow = mnew;
+                vex = ve;
+            }
+            float gsum[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                s[j][0] = ex2(s[j][0] - msafe);
+                s[j][1] = ex2(s[j][1] - msafe);
+                gsum[j >> 1] += s[j][0] + s[j][1];
+            }
+            lrow += gsum[0] + gsum[1];
+            if (p.glse) {   // log2 of the weight sums by group of min(P, 32) tokens
+#pragma unroll
+                for (int i2 = 0; i2 < 2; i2++) {
+                    gsum[i2] += __shfl_xor_sync(0xffffffffu, gsum[i2], 1);
+                    gsum[i2] += __shfl_xor_sync(0xffffffffu, gsum[i2], 2);
+                }
+                if (real && t == 0) {
+                    const int slot = (u < k.u.pre ? u : k.u.start + u - k.u.pre) * UNIT;
+                    float *gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (slot >> p.lgGroup);
+                    if (p.lgGroup == 4) {
+                        gl[0] = __log2f(gsum[0]) + msafe;
+                        if (live > 16) gl[1] = __log2f(gsum[1]) + msafe;
+                    } else {
+                        gl[0] = __log2f(gsum[0] + gsum[1]) + msafe;
+                    }
+                }
+            }
+            // ---- weights times value scales, in units of 2^(vex - 14), as two fp16 terms
+            const float vu = __uint_as_float((uint32_t)(14 - vex + 127) << 23);
+            const float v0 = vs0 * vu, v1 = vs1 * vu;
+            uint32_t pa[4][2];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float vv = j < 2 ? v0 : v1;
+                split2(s[j][0] * vv, s[j][1] * vv, pa[j][0], pa[j][1]);
+            }
+            // ---- values: k the 16 tokens of a step, column n of tile x the x-th position of chunk n
+#pragma unroll
+            for (int st = 0; st < 2; st++) {
+                uint32_t w[4][D / 32];   // this lane's chunk of tokens r0, r0 + 1, r0 + 8, r0 + 9
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const int tok = 16 * st + 2 * t + (x & 1) + 8 * (x >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 q4 = sh_ld128(vb + tok * 128 + ((g8 ^ (tok & 7)) << 4));
+                        w[x][0] = q4.x;
+                        w[x][1] = q4.y;
+                        w[x][2] = q4.z;
+                        w[x][3] = q4.w;
+                    } else {
+                        const uint2 q2 = sh_ld64(vb + (tok >> 1) * 128 +
+                                                 (((4 * (tok & 1) + (g8 >> 1)) ^ ((tok >> 1) & 7)) << 4) + 8 * (g8 & 1));
+                        w[x][0] = q2.x;
+                        w[x][1] = q2.y;
+                    }
+                    // slots past the last token may hold any bytes, NaN codes among them
+                    if (KIND == GQ_KV_E4M3 && !whole && (tok >= live || ((m.lost >> st) & 1)))
+#pragma unroll
+                        for (int y = 0; y < D / 32; y++) w[x][y] = 0u;
+                }
+#pragma unroll
+                for (int y = 0; y < D / 32; y++) {
+                    uint32_t b0[4], b1[4];
+                    widen_pairs<KIND>(w[0][y], w[1][y], b0);
+                    widen_pairs<KIND>(w[2][y], w[3][y], b1);
+#pragma unroll
+                    for (int x = 0; x < 4; x++)
+                        mma_f16_16x8x16(o[4 * y + x], pa[2 * st][0], pa[2 * st][1], pa[2 * st + 1][0], pa[2 * st + 1][1],
+                                        b0[x], b1[x]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(sm.empty + sl));
+        }
+        count += u1 - u0;
+
+        // ---- join the four warps
+        lrow += __shfl_xor_sync(0xffffffffu, lrow, 1);
+        lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
+        if (t == 0) {
+            sm.ml[parity][warp][g8][0] = mrow;
+            sm.ml[parity][warp][g8][1] = lrow;
+        }
+        consumer_sync();
+        {
+            float mt = sm.ml[parity][0][g8][0];
+#pragma unroll
+            for (int w = 1; w < W; w++) mt = fmaxf(mt, sm.ml[parity][w][g8][0]);
+            const float a = mrow == -INFINITY ? 0.0f : ex2(mrow - mt) * __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
+            // lane (g8, t): n-tile x, column 2t (+1) is position (2t (+1)) * RUN / 2 + x
+            float4 *dst = reinterpret_cast<float4 *>(red + ((size_t)warp * ROWS + g8) * D + RUN * t);
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+#pragma unroll
+                for (int x = 0; x < 2 * KS; x += 4)
+                    dst[e * (KS / 2) + x / 4] = make_float4((o[x][e] + o[x][e + 2]) * a, (o[x + 1][e] + o[x + 1][e + 2]) * a,
+                                                            (o[x + 2][e] + o[x + 2][e + 2]) * a,
+                                                            (o[x + 3][e] + o[x + 3][e + 2]) * a);
+        }
+        consumer_sync();
+        const bool cut0 = u0 > 0, cut1 = u1 < k.u.units;   // the item began before, goes on after this CTA
+        const int rows = min(ROWS, k.s.n * p.G - k.tile * ROWS);
+        auto row_ptr = [&](int rr) {   // output row of tile row rr
+            const int x = k.tile * ROWS + rr;
+            return p.out + (int64_t)(k.s.t0 + x / p.G) * p.ldo + (int64_t)(k.h * p.G + x % p.G) * D;
+        };
+        auto row_index = [&](int rr) {
+            const int x = k.tile * ROWS + rr;
+            return (int64_t)(k.s.t0 + x / p.G) * p.Hq + k.h * p.G + x % p.G;
+        };
+        const int piece_slot = blockIdx.x * 2 + (cut0 ? 0 : 1);
+        for (int x = tid; x < rows * (D / 4); x += CONSUMERS) {
+            const int rr = x / (D / 4), d4 = x % (D / 4);
+            float mt = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; w++) mt = fmaxf(mt, sm.ml[parity][w][rr][0]);
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < W; w++) {
+                const float mw = sm.ml[parity][w][rr][0];
+                if (mw != -INFINITY) l += sm.ml[parity][w][rr][1] * ex2(mw - mt);
+                const float4 v = reinterpret_cast<const float4 *>(red + ((size_t)w * ROWS + rr) * D)[d4];
+                a.x += v.x;
+                a.y += v.y;
+                a.z += v.z;
+                a.w += v.w;
+            }
+            if (!cut0 && !cut1) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                reinterpret_cast<float4 *>(row_ptr(rr))[d4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                if (p.lse && d4 == 0) p.lse[row_index(rr)] = l > 0.0f ? mt + log2f(l) : INFINITY;
+            } else {
+                reinterpret_cast<float4 *>(p.parts + ((int64_t)piece_slot * ROWS + rr) * D)[d4] = a;
+                if (d4 == 0) {
+                    p.part_ml[((int64_t)piece_slot * ROWS + rr) * 2] = mt;
+                    p.part_ml[((int64_t)piece_slot * ROWS + rr) * 2 + 1] = l;
+                }
+            }
+        }
+        if (cut0 || cut1) {
+            // the pieces of this item: CTAs c0 .. c1; the one that finishes last joins them in order
+            const int c0 = (int)(item0 / piece), c1 = (int)((item0 + k.u.units - 1) / piece);
+            __threadfence();
+            consumer_sync();
+            if (tid == 0) {
+                const int done = atomicAdd(p.counters + c0, 1);
+                sm.last = done == c1 - c0;
+                if (done == c1 - c0) p.counters[c0] = 0;   // left at zero for the next launch
+            }
+            consumer_sync();
+            if (sm.last) {
+                __threadfence();
+                for (int x = tid; x < rows * (D / 4); x += CONSUMERS) {
+                    const int rr = x / (D / 4), d4 = x % (D / 4);
+                    // the item begins in CTA c0 (its slot 1); it is the first item of the others (slot 0)
+                    float mt = -INFINITY;
+                    for (int q = c0; q <= c1; q++)
+                        mt = fmaxf(mt, __ldcg(p.part_ml + ((int64_t)(q * 2 + (q == c0)) * ROWS + rr) * 2));
+                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float l = 0.0f;
+                    if (mt != -INFINITY)
+#pragma unroll 4
+                        for (int q = c0; q <= c1; q++) {
+                            const int64_t pr = (int64_t)(q * 2 + (q == c0)) * ROWS + rr;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + pr * 2));
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.parts + pr * D) + d4);
+                            const float e = ex2(ml.x - mt);
+                            l += e * ml.y;
+                            a.x += e * v.x;
+                            a.y += e * v.y;
+                            a.z += e * v.z;
+                            a.w += e * v.w;
+                        }
+                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                    reinterpret_cast<float4 *>(row_ptr(rr))[d4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                    if (p.lse && d4 == 0) p.lse[row_index(rr)] = l > 0.0f ? mt + log2f(l) : INFINITY;
+                }
+            }
+        }
+        parity ^= 1;
+        at = item0 + u1;
+        if (u1 == k.u.units) {
+            item0 += k.u.units;
+            if (at < hi) next_item(p, k);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The weight that each page gathered: decay * in + sum over the step's query rows of
+// 2^(log2 of the page's weight sum - log2 of the row's denominator).
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(128) attn_pages_weights_kernel(const RowsParams p, const float *w_in, float *w_out,
+                                                                 float decay) {
+    const PagesView &c = p.c;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tiles = (c.NB + 127) / 128, bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
+    const int j = (blockIdx.x % tiles) * 128 + threadIdx.x;
+    if (j >= c.NB) return;
+    Cursor k;
+    k.b = b;
+    load_seq(p, k);
+    const int64_t at = (int64_t)bh * c.NB + j;
+    const int64_t slot = (int64_t)j << p.lgP;
+    if (slot >= k.s.held + k.s.n) {
+        w_out[at] = 0.0f;
+        return;
+    }
+    float sum = 0.0f;
+    if (k.s.n > 0) {
+        const int per = 1 << (p.lgP - p.lgGroup), end = k.s.held + k.s.n;
+        for (int g = 0; g < per; g++) {
+            const int s0 = (int)slot + (g << p.lgGroup), u = s0 / UNIT;
+            if (s0 >= end || (u >= k.u.pre && u < k.u.start)) continue;   // nobody looked there
+            const float *gl = p.glse + ((int64_t)k.s.t0 * p.Hq + h * p.G) * p.NG + (s0 >> p.lgGroup);
+            const float *ls = p.lse + (int64_t)k.s.t0 * p.Hq + h * p.G;
+            for (int i = 0; i < k.s.n; i++)
+                for (int x = 0; x < p.G; x++) {
+                    const int64_t r = (int64_t)i * p.Hq + x;
+                    sum += ex2(gl[r * p.NG] - ls[r]);
+                }
+        }
+    }
+    w_out[at] = (w_in ? decay * w_in[at] : 0.0f) + sum;
+}
+
+int log2_of(int64_t x) {
+    int l = 0;
+    while ((1LL << l) < x) l++;
+    return l;
+}
+
+template <int KIND, int D>
+gq_status launch_rows(RowsParams p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
+                      cudaStream_t s) {
+    auto kernel = attn_pages_rows_kernel<KIND, D>;
+    constexpr size_t smem = rows_smem_bytes<D>();
+    static std::atomic<bool> smem_set[64];
+    int dev = 0;
+    KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
+    if (dev < 0 || dev >= 64) return fail(GQ_ERR_UNSUPPORTED_DEVICE, "device index %d", dev);
+    if (!smem_set[dev].load(std::memory_order_acquire)) {
+        KV_TRY(check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                          "paged attention shared-memory attribute"));
+        smem_set[dev].store(true, std::memory_order_release);
+    }
+    const int grid = 2 * sm_count();
+    const size_t parts = (size_t)grid * 2 * ROWS * D * 4, mls = (size_t)grid * 2 * ROWS * 8;
+    const size_t lse = w_out ? ((size_t)T * p.Hq * 4 + 255) / 256 * 256 : 0;
+    const size_t glse = w_out ? (size_t)T * p.Hq * p.NG * 4 : 0;
+    Workspace ws{};
+    KV_TRY(get_workspace(s, (size_t)grid * sizeof(int), parts + mls + lse + glse, &ws));
+    p.counters = reinterpret_cast<int *>(ws.counters);
+    p.parts = reinterpret_cast<float *>(ws.data);
+    p.part_ml = reinterpret_cast<float *>(ws.data + parts);
+    p.lse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls) : nullptr;
+    p.glse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls + lse) : nullptr;
+    alignas(64) CUtensorMap kmap, vmap;
+    const int64_t rows = c.pages * c.P * c.D / 128;
+    const int box = (int)(std::min<int64_t>(c.P, UNIT) * D / 128);
+    KV_TRY(byte_rows_map(&kmap, c.k, rows, box));
+    KV_TRY(byte_rows_map(&vmap, c.v, rows, box));
+    void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
+    KV_TRY(launch_pdl((const void *)kernel, dim3((unsigned)grid), dim3(THREADS), smem, s, args, "paged attention launch"));
+    if (w_out) {
+        const int64_t wgrid = c.B * c.Hkv * ((c.NB + 127) / 128);
+        void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
+        KV_TRY(launch_pdl((const void *)attn_pages_weights_kernel, dim3((unsigned)wgrid), dim3(128), 0, s, wargs,
+                          "paged attention weights launch"));
+    }
+    return GQ_OK;
+}
+
+}  // namespace
+
+gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, const float *q, int64_t ldq,
+                            const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
+                            const float *w_in, float *w_out, float decay, cudaStream_t s) {
+    RowsParams p{};
+    KV_TRY(pages_view(c, &p.c));
+    p.q = q;
+    p.out = out;
+    p.cu = cu;
+    p.slopes = sc.slopes;
+    p.first = sc.first;
+    p.prefix = sc.prefix;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.window = sc.window;
+    p.T = (int)T;
+    p.max_n = (int)max_n;
+    p.Hq = (int)Hq;
+    p.G = (int)(Hq / c.Hkv);
+    p.lgP = log2_of(c.P);
+    p.lgGroup = std::min(p.lgP, 5);
+    p.NG = (int)((c.NB * c.P) >> p.lgGroup);
+    p.scale = sc.scale;
+    p.cap = sc.cap;
+    if (c.kind == GQ_KV_I8)
+        return c.D == 64 ? launch_rows<GQ_KV_I8, 64>(p, c, T, w_in, w_out, decay, s)
+                         : launch_rows<GQ_KV_I8, 128>(p, c, T, w_in, w_out, decay, s);
+    return c.D == 64 ? launch_rows<GQ_KV_E4M3, 64>(p, c, T, w_in, w_out, decay, s)
+                     : launch_rows<GQ_KV_E4M3, 128>(p, c, T, w_in, w_out, decay, s);
+}
+
+}  // namespace gq

@@ -743,3 +743,128 @@ gq_status gq_attn_decode_i8(const float *q, const int8_t *k, const float *k_scal
 }
 
 }  // extern "C"
+
+namespace {
+gq_status check_pages(const gq_kv_pages *c) {
+    if (!c) return fail(GQ_ERR_INVALID_ARG, "cache is NULL");
+    if (c->kind != GQ_KV_I8 && c->kind != GQ_KV_E4M3)
+        return fail(GQ_ERR_INVALID_ARG, "cache kind %lld is neither GQ_KV_I8 nor GQ_KV_E4M3", (long long)c->kind);
+    if (c->D != 64 && c->D != 128) return fail(GQ_ERR_INVALID_ARG, "D must be 64 or 128 (got %lld)", (long long)c->D);
+    if (c->P != 16 && c->P != 32 && c->P != 64 && c->P != 128)
+        return fail(GQ_ERR_INVALID_ARG, "P must be 16, 32, 64 or 128 tokens (got %lld)", (long long)c->P);
+    const int64_t lim = 1LL << 31;
+    if (c->B <= 0 || c->Hkv <= 0 || c->NB <= 0 || c->pages <= 0)
+        return fail(GQ_ERR_INVALID_ARG, "B, Hkv, NB and pages must be positive (got %lld, %lld, %lld, %lld)",
+                    (long long)c->B, (long long)c->Hkv, (long long)c->NB, (long long)c->pages);
+    if (c->B >= lim || c->Hkv >= lim || c->NB >= lim || c->pages >= lim || c->NB * c->P >= (1LL << 30) ||
+        c->B * c->Hkv >= lim || c->B * c->Hkv * c->NB >= lim || c->pages * c->P * c->D > (1LL << 37))
+        return fail(GQ_ERR_INVALID_ARG, "cache too large (B=%lld Hkv=%lld NB=%lld pages=%lld)", (long long)c->B,
+                    (long long)c->Hkv, (long long)c->NB, (long long)c->pages);
+    GQ_TRY(check_ptr(c->k, "cache k"));
+    GQ_TRY(check_ptr(c->v, "cache v"));
+    GQ_TRY(check_ptr(c->ks, "cache ks"));
+    GQ_TRY(check_ptr(c->vs, "cache vs"));
+    GQ_TRY(check_ptr(c->table, "cache table"));
+    GQ_TRY(check_ptr(c->base, "cache base"));
+    GQ_TRY(check_ptr(c->held, "cache held"));
+    return check_ptr(c->seen, "cache seen");
+}
+
+// the packed rows of a step: T rows in all, at most max_n of one sequence
+gq_status check_packed(const gq_kv_pages *c, const int32_t *cu, int64_t T, int64_t max_n) {
+    if (T <= 0 || T >= (1LL << 30)) return fail(GQ_ERR_INVALID_ARG, "T must be in [1, 2^30) (got %lld)", (long long)T);
+    if (max_n <= 0 || max_n > T)
+        return fail(GQ_ERR_INVALID_ARG, "max_n must be in [1, T] (got %lld, T=%lld)", (long long)max_n, (long long)T);
+    if (max_n > c->NB * c->P)
+        return fail(GQ_ERR_INVALID_ARG, "max_n=%lld tokens do not fit NB * P = %lld", (long long)max_n,
+                    (long long)(c->NB * c->P));
+    return check_ptr(cu, "cu");
+}
+
+gq_status check_rows(int64_t ld, int64_t heads, int64_t D, const char *name) {
+    if (ld % 4 != 0 || ld < heads * D || ld >= (1LL << 31))
+        return fail(GQ_ERR_INVALID_ARG, "%s=%lld must be a multiple of 4 and at least %lld", name, (long long)ld,
+                    (long long)(heads * D));
+    return GQ_OK;
+}
+}  // namespace
+
+extern "C" {
+
+gq_status gq_kv_pages_append(const gq_kv_pages *cache, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                             const int32_t *cu, int64_t T, int64_t max_n, cudaStream_t stream) {
+    GQ_TRY(check_pages(cache));
+    GQ_TRY(check_packed(cache, cu, T, max_n));
+    GQ_TRY(check_rows(ldk, cache->Hkv, cache->D, "ldk"));
+    GQ_TRY(check_rows(ldv, cache->Hkv, cache->D, "ldv"));
+    GQ_TRY(check_ptr(k, "k"));
+    GQ_TRY(check_ptr(v, "v"));
+    GQ_TRY(check_device());
+    GQ_TRY(launch_kv_pages_append(*cache, k, ldk, v, ldv, cu, T, max_n, stream));
+    return ok();
+}
+
+gq_status gq_kv_pages_read(const gq_kv_pages *cache, const int32_t *start, const int32_t *cu, int64_t T, int64_t max_n,
+                           float *k, float *v, cudaStream_t stream) {
+    GQ_TRY(check_pages(cache));
+    GQ_TRY(check_packed(cache, cu, T, max_n));
+    GQ_TRY(check_ptr(start, "start"));
+    if (!k && !v) return fail(GQ_ERR_INVALID_ARG, "k and v are both NULL");
+    if (k) GQ_TRY(check_ptr(k, "k"));
+    if (v) GQ_TRY(check_ptr(v, "v"));
+    GQ_TRY(check_device());
+    GQ_TRY(launch_kv_pages_read(*cache, start, cu, T, max_n, k, v, stream));
+    return ok();
+}
+
+gq_status gq_attn_pages(const gq_kv_pages *cache, const gq_attn_scores *scores, const float *q, int64_t ldq,
+                        const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
+                        const float *weights_in, float *weights_out, float decay, cudaStream_t stream) {
+    GQ_TRY(check_pages(cache));
+    GQ_TRY(check_packed(cache, cu, T, max_n));
+    if (!scores) return fail(GQ_ERR_INVALID_ARG, "scores is NULL");
+    if (Hq <= 0 || Hq % cache->Hkv != 0 || Hq / cache->Hkv > 64)
+        return fail(GQ_ERR_INVALID_ARG, "Hq=%lld is not 1 to 64 times Hkv=%lld", (long long)Hq, (long long)cache->Hkv);
+    GQ_TRY(check_rows(ldq, Hq, cache->D, "ldq"));
+    GQ_TRY(check_rows(ldo, Hq, cache->D, "ldo"));
+    if (!std::isfinite(scores->scale)) return fail(GQ_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(scores->cap) || scores->cap < 0.0f)
+        return fail(GQ_ERR_INVALID_ARG, "cap must be finite and not negative (0: none)");
+    if (scores->window < 0) return fail(GQ_ERR_INVALID_ARG, "window must not be negative (0: none)");
+    if (scores->slopes) GQ_TRY(check_ptr(scores->slopes, "slopes"));
+    if (scores->first) GQ_TRY(check_ptr(scores->first, "first"));
+    if (scores->prefix) GQ_TRY(check_ptr(scores->prefix, "prefix"));
+    GQ_TRY(check_ptr(q, "q"));
+    GQ_TRY(check_ptr(out, "out"));
+    if (weights_in && !weights_out) return fail(GQ_ERR_INVALID_ARG, "weights_in without weights_out");
+    if (weights_in) GQ_TRY(check_ptr(weights_in, "weights_in"));
+    if (weights_out) GQ_TRY(check_ptr(weights_out, "weights_out"));
+    if (!std::isfinite(decay)) return fail(GQ_ERR_INVALID_ARG, "decay is not finite");
+    GQ_TRY(check_device());
+    GQ_TRY(launch_attn_pages(*cache, *scores, q, ldq, cu, T, max_n, Hq, out, ldo, weights_in, weights_out, decay,
+                             stream));
+    return ok();
+}
+
+gq_status gq_kv_pages_evict(const gq_kv_pages *cache, const float *weights, int64_t budget, int64_t keep_first,
+                            int64_t keep_last, int32_t *table_out, int32_t *base_out, float *weights_out,
+                            int32_t *held_out, cudaStream_t stream) {
+    GQ_TRY(check_pages(cache));
+    if (cache->NB > 16384)
+        return fail(GQ_ERR_INVALID_ARG, "NB must be at most 16384 for eviction (got %lld)", (long long)cache->NB);
+    if (keep_first < 0 || keep_last < 1 || keep_first > (1LL << 31) || keep_last > (1LL << 31) ||
+        budget < keep_first + keep_last)
+        return fail(GQ_ERR_INVALID_ARG, "need keep_first >= 0, keep_last >= 1 and keep_first + keep_last <= budget "
+                    "(got %lld, %lld, %lld)", (long long)keep_first, (long long)keep_last, (long long)budget);
+    GQ_TRY(check_ptr(weights, "weights"));
+    GQ_TRY(check_ptr(table_out, "table_out"));
+    GQ_TRY(check_ptr(base_out, "base_out"));
+    GQ_TRY(check_ptr(weights_out, "weights_out"));
+    GQ_TRY(check_ptr(held_out, "held_out"));
+    GQ_TRY(check_device());
+    GQ_TRY(launch_kv_pages_evict(*cache, weights, budget, keep_first, keep_last, table_out, base_out, weights_out,
+                                 held_out, stream));
+    return ok();
+}
+
+}  // extern "C"

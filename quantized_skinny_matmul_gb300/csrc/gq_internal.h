@@ -103,6 +103,17 @@ gq_status f16_tile_map(void *map, const void *base, int64_t N, int64_t K);
 // The F16 product over row-major weights through the GEMV pipeline of the repacked tiles.
 gq_status launch_gemv_f16_rowmajor(const void *w16, const float *x, float *dst, int64_t M, int64_t N, int64_t K,
                                    cudaStream_t s);
+// 8-bit KV cache in pages: append and read back, the attention over it, eviction (arguments validated).
+gq_status launch_kv_pages_append(const gq_kv_pages &c, const float *k, int64_t ldk, const float *v, int64_t ldv,
+                                 const int32_t *cu, int64_t T, int64_t max_n, cudaStream_t s);
+gq_status launch_kv_pages_read(const gq_kv_pages &c, const int32_t *start, const int32_t *cu, int64_t T, int64_t max_n,
+                               float *k, float *v, cudaStream_t s);
+gq_status launch_kv_pages_evict(const gq_kv_pages &c, const float *w, int64_t budget, int64_t keep_first,
+                                int64_t keep_last, int32_t *table_out, int32_t *base_out, float *w_out,
+                                int32_t *held_out, cudaStream_t s);
+gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, const float *q, int64_t ldq,
+                            const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
+                            const float *w_in, float *w_out, float decay, cudaStream_t s);
 gq_status launch_block_dots_q4_0(const void *rep, const void *q8, int32_t *sumi, int64_t M,
                                  int64_t N, int64_t K, cudaStream_t s);
 
