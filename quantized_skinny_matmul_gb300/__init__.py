@@ -150,10 +150,28 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+def _torch_stream():
+    """A function that gives the handle of torch's current stream (3 us for the Stream object, 0.1 us raw)."""
+    import torch
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
+def _current_stream() -> int:
+    global _current
+    if _current is None:
+        _current = _torch_stream()
+    return _current()
+
+
+_current = None
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -428,19 +446,52 @@ def _rows_ptr(t) -> int:
     return t.data_ptr()
 
 
-def _row_stride(x, width: int, name: str) -> int:
-    """The stride between the packed f32 rows of x ([T, width] or [T, heads, D])."""
-    import torch
-    if x.dtype != torch.float32:
+def _f32():
+    global _float32
+    if _float32 is None:
+        import torch
+        _float32 = torch.float32
+    return _float32
+
+
+_float32 = None
+
+
+def _lengths(cu, n: int, name: str = "cu") -> int:
+    """The address of int32 [n] on the device."""
+    if cu.shape != (n,) or not cu.is_cuda or not cu.is_contiguous() or str(cu.dtype) != "torch.int32":
+        raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of {n} values, got {cu.dtype} {tuple(cu.shape)}")
+    return cu.data_ptr()
+
+
+def _page_weights(cache, w) -> int:
+    """The address of f32 [B, Hkv, NB] on the device."""
+    if (w.shape != (cache.B, cache.Hkv, cache.NB) or w.dtype is not _f32() or not w.is_cuda or not w.is_contiguous()):
+        raise ValueError(f"weights: expected a contiguous CUDA float32 tensor of shape "
+                         f"{(cache.B, cache.Hkv, cache.NB)}, got {w.dtype} {tuple(w.shape)}")
+    return w.data_ptr()
+
+
+def _packed(x, D: int, name: str):
+    """(rows, heads, row stride) of packed f32 rows: [T, heads * D] or [T, heads, D], each row contiguous."""
+    shape, stride = x.shape, x.stride()
+    if not x.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if x.dtype is not _f32():
         raise ValueError(f"{name}: expected float32, got {x.dtype}")
-    n = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if size != 1 and stride != n:
-            raise ValueError(f"{name}: each row must be contiguous")
-        n *= size
-    if n != width:
-        raise ValueError(f"{name}: rows of {n} values, expected {width}")
-    return x.stride(0) if x.shape[0] > 1 else width
+    if len(shape) == 2:
+        heads, rest = divmod(shape[1], D)
+        if rest:
+            raise ValueError(f"{name}: rows of {shape[1]} values are not a multiple of D = {D}")
+        whole = stride[1] == 1 or shape[1] == 1
+    elif len(shape) == 3 and shape[2] == D:
+        heads = shape[1]
+        whole = stride[2] == 1 and (stride[1] == D or heads == 1)
+    else:
+        raise ValueError(f"{name}: expected shape [T, heads * {D}] or [T, heads, {D}], got {tuple(shape)}")
+    if not whole:
+        raise ValueError(f"{name}: each row must be contiguous")
+    return shape[0], heads, stride[0] if shape[0] > 1 else heads * D
 
 
 class KVPages:
@@ -495,7 +546,7 @@ class AttnScores:
 
 
 def _shape(t, shape, dtype, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is None and t.element_size() != 1 or dtype is not None and str(t.dtype) != "torch." + dtype:
         raise ValueError(f"{name}: wrong dtype {t.dtype}")
@@ -707,20 +758,20 @@ def attn_decode_i8(q, k, k_scale, v, v_scale, lens, softmax_scale=None, out=None
 
 def kv_pages_append(cache: KVPages, k, v, cu, max_n: int) -> None:
     """Write a step's packed keys and values (f32 [T, Hkv * D] or [T, Hkv, D], rows may be strided)."""
-    T, width = k.shape[0], cache.Hkv * cache.D
-    if v.shape[0] != T:
-        raise ValueError(f"v has {v.shape[0]} rows, k {T}")
-    _shape(cu, (cache.B + 1,), "int32", "cu")
-    gq_kv_pages_append(cache, k, _row_stride(k, width, "k"), v, _row_stride(v, width, "v"), cu, T, max_n)
+    T, heads, ldk = _packed(k, cache.D, "k")
+    Tv, heads_v, ldv = _packed(v, cache.D, "v")
+    if T != Tv or heads != cache.Hkv or heads_v != heads:
+        raise ValueError(f"expected {cache.Hkv} heads in the rows of k and v, and as many rows in both: got {heads} "
+                         f"and {heads_v} heads, {T} and {Tv} rows")
+    _check(lib().gq_kv_pages_append(cache.by_ref, k.data_ptr(), ldk, v.data_ptr(), ldv, _lengths(cu, cache.B + 1), T, max_n,
+                                    _current_stream()), "gq_kv_pages_append")
 
 
 def kv_pages_read(cache: KVPages, start, cu, T: int, max_n: int):
     """Slots start[b] .. of each sequence as f32: (k, v), each [T, Hkv, D], packed by cu."""
-    import torch
-    _shape(start, (cache.B,), "int32", "start")
-    _shape(cu, (cache.B + 1,), "int32", "cu")
-    k, v = (torch.empty((T, cache.Hkv, cache.D), dtype=torch.float32, device=cache.k.device) for _ in range(2))
-    gq_kv_pages_read(cache, start, cu, T, max_n, k, v)
+    k, v = cache.ks.new_empty((2, T, cache.Hkv, cache.D)).unbind(0)
+    _check(lib().gq_kv_pages_read(cache.by_ref, _lengths(start, cache.B, "start"), _lengths(cu, cache.B + 1), T, max_n,
+                                  k.data_ptr(), v.data_ptr(), _current_stream()), "gq_kv_pages_read")
     return k, v
 
 
@@ -730,29 +781,32 @@ def attn_pages(cache: KVPages, q, cu, max_n: int, scores: AttnScores, weights=No
     With ``weights`` (f32 [B, Hkv, NB], what each page gathered so far) the result is
     (out, new weights), the new ones being decay * weights + this step's shares.
     """
-    import torch
-    T = q.shape[0]
-    width = q[0].numel()
-    Hq = width // cache.D
-    _shape(cu, (cache.B + 1,), "int32", "cu")
-    for t, n, name in ((scores.slopes, Hq, "slopes"), (scores.first, T, "first"), (scores.prefix, T, "prefix")):
-        if t is not None:
-            _shape(t, (n,), str(t.dtype)[6:], name)
+    T, Hq, ldq = _packed(q, cache.D, "q")
+    if scores.slopes is not None and scores.slopes.shape[0] != Hq:
+        raise ValueError(f"slopes: expected {Hq} values, got {scores.slopes.shape[0]}")
+    for t, name in ((scores.first, "first"), (scores.prefix, "prefix")):
+        if t is not None and t.shape[0] != T:
+            raise ValueError(f"{name}: expected {T} values, got {t.shape[0]}")
     if out is None:
-        out = torch.empty((T, Hq, cache.D), dtype=torch.float32, device=q.device)
-    new = None
+        out, ldo = cache.ks.new_empty((T, Hq, cache.D)), Hq * cache.D
+    else:
+        To, Ho, ldo = _packed(out, cache.D, "out")
+        if To != T or Ho != Hq:
+            raise ValueError(f"out: expected {T} rows of {Hq} heads, got {To} and {Ho}")
+    new = w_in = w_out = None
     if weights is not None:
-        _shape(weights, (cache.B, cache.Hkv, cache.NB), "float32", "weights")
-        new = torch.empty_like(weights)
-    gq_attn_pages(cache, scores, q, _row_stride(q, Hq * cache.D, "q"), cu, T, max_n, Hq, out,
-                  _row_stride(out, Hq * cache.D, "out"), weights, new, decay)
+        w_in, new = _page_weights(cache, weights), weights.new_empty(weights.shape)
+        w_out = new.data_ptr()
+    _check(lib().gq_attn_pages(cache.by_ref, scores.by_ref, q.data_ptr(), ldq, _lengths(cu, cache.B + 1), T, max_n, Hq,
+                               out.data_ptr(), ldo, w_in, w_out, decay, _current_stream()), "gq_attn_pages")
     return out if weights is None else (out, new)
 
 
 def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, keep_last: int = 1):
     """Drop the pages that gathered least until `budget` are left: (table, base, weights, held), new tensors."""
-    import torch
-    _shape(weights, (cache.B, cache.Hkv, cache.NB), "float32", "weights")
-    outs = [torch.empty_like(t) for t in (cache.table, cache.base, weights, cache.held)]
-    gq_kv_pages_evict(cache, weights, budget, keep_first, keep_last, *outs)
-    return tuple(outs)
+    w = _page_weights(cache, weights)
+    table, base = cache.table.new_empty((2,) + cache.table.shape).unbind(0)
+    new, held = weights.new_empty(weights.shape), cache.held.new_empty(cache.held.shape)
+    _check(lib().gq_kv_pages_evict(cache.by_ref, w, budget, keep_first, keep_last, table.data_ptr(), base.data_ptr(),
+                                   new.data_ptr(), held.data_ptr(), _current_stream()), "gq_kv_pages_evict")
+    return table, base, new, held

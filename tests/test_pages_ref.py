@@ -109,6 +109,25 @@ def test_refused_evictions(lib):
     assert ev(c=cache(NB=16385, pages=1 << 20, P=16)) == 1
 
 
+class OnGpu:
+    """What the packed-row checks look at, of a tensor that says it lives on the GPU."""
+
+    def __init__(self, t):
+        self.shape, self.dtype, self.is_cuda, self.stride = t.shape, t.dtype, True, t.stride
+
+
+def test_binding_refuses_wrong_rows():
+    import torch
+    for bad, why in ((torch.zeros((3, 8, 32))[:, :, ::2], "contiguous"), (torch.zeros((3, 40)), "multiple"),
+                     (torch.zeros((3, 2, 8)), "shape"), (torch.zeros((3, 32), dtype=torch.float16), "float32")):
+        with pytest.raises(ValueError, match=why):
+            gq._packed(OnGpu(bad), 16, "q")
+    with pytest.raises(ValueError, match="CUDA"):
+        gq._packed(torch.zeros((3, 32)), 16, "q")
+    assert gq._packed(OnGpu(torch.zeros((3, 64))[:, 8:40]), 16, "q") == (3, 2, 64)
+    assert gq._packed(OnGpu(torch.zeros((1, 2, 16))), 16, "q") == (1, 2, 32)
+
+
 def test_binding_refuses_wrong_tensors():
     import torch
     ok = dict(kind=0, k=torch.zeros((4, 16, 64), dtype=torch.int8), v=torch.zeros((4, 16, 64), dtype=torch.int8),
@@ -124,8 +143,4 @@ def test_binding_refuses_wrong_tensors():
             gq.KVPages(**{**ok, name: bad})
     with pytest.raises(ValueError, match="slopes"):
         gq.AttnScores(1.0, slopes=torch.zeros(4, dtype=torch.float64))
-    with pytest.raises(ValueError, match="contiguous"):
-        gq._row_stride(torch.zeros((3, 8, 2))[:, :, 0], 8, "q")
-    assert gq._row_stride(torch.zeros((3, 64))[:, 8:40], 32, "q") == 64
-    assert gq._row_stride(torch.zeros((1, 2, 16)), 32, "q") == 32
     assert ctypes.sizeof(gq.KVPagesStruct) == 15 * 8 and ctypes.sizeof(gq.AttnScoresStruct) == 40
