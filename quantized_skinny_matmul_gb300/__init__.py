@@ -805,7 +805,7 @@ def attn_pages(cache: KVPages, q, cu, max_n: int, scores: AttnScores, weights=No
 def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, keep_last: int = 1):
     """Drop the pages that gathered least until `budget` are left: (table, base, weights, held), new tensors."""
     w = _page_weights(cache, weights)
-    table, base = cache.table.new_empty((2,) + cache.table.shape).unbind(0)
+    table, base = cache.table.new_empty(cache.table.shape), cache.base.new_empty(cache.base.shape)
     new, held = weights.new_empty(weights.shape), cache.held.new_empty(cache.held.shape)
     _check(lib().gq_kv_pages_evict(cache.by_ref, w, budget, keep_first, keep_last, table.data_ptr(), base.data_ptr(),
                                    new.data_ptr(), held.data_ptr(), _current_stream()), "gq_kv_pages_evict")

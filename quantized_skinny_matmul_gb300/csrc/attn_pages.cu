@@ -30,9 +30,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "attn_pages.cuh"
 #include "gq_common.cuh"
 #include "gq_internal.h"
-#include "kv_pages.cuh"
 
 namespace gq {
 namespace {
@@ -43,28 +43,10 @@ namespace {
         if (_st != GQ_OK) return _st; \
     } while (0)
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr int UNIT = 32;                    // tokens per unit
 constexpr int W = 4;                        // consumer warps
 constexpr int CONSUMERS = W * 32, THREADS = CONSUMERS + 32;
 constexpr int ROWS = 8;                     // query rows of an item
-
-struct RowsParams {
-    PagesView c;
-    const float *q;
-    float *out;
-    const int32_t *cu;
-    const float *slopes;
-    const int32_t *first, *prefix;
-    float *parts;               // [CTA][2][ROWS][D] sums, then [CTA][2][ROWS][2] maximum and denominator
-    float *part_ml;
-    int *counters;              // per CTA: pieces of the item cut at its end that are done
-    float *glse;                // [T * Hq][NG] log2 of the weight sums by group, or null
-    float *lse;                 // [T * Hq] log2 of the denominators
-    int64_t ldq, ldo, window;
-    int T, max_n, Hq, G, NG, lgP, lgGroup;
-    float scale, cap;
-};
 
 __host__ __device__ constexpr int slots_of(int D) { return D == 128 ? 11 : 24; }   // two CTAs per SM
 
@@ -89,59 +71,8 @@ __host__ __device__ constexpr size_t rows_smem_bytes() {
     return 1024 + (size_t)slots_of(D) * UNIT * D * 2 + (size_t)W * ROWS * D * 4 + sizeof(RowsSmem);
 }
 
-__device__ __forceinline__ uint4 sh_ld128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 sh_ld64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
-
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int row, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar), "l"(policy)
-        : "memory");
-}
-
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory"); }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// tanh: the continued fraction x / (1 + x^2 / (3 + x^2 / (5 + ...))) cut after the fifth level for
-// |x| <= 1 (off by 1e-7 relative at 1, less below), 1 - 2 / (e^2x + 1) beyond.
-__device__ __forceinline__ float tanh_f32(float x) {
-    const float u = x * x;
-    const float small = x * fmaf(u, 105.0f + u, 945.0f) * __frcp_rn(fmaf(u, fmaf(15.0f, u, 420.0f), 945.0f));
-    const float a = fabsf(x);
-    if (a <= 1.0f) return small;
-    const float t = 1.0f - 2.0f * __frcp_rn(ex2(2.0f * LOG2E * a) + 1.0f);
-    return x < 0.0f ? -t : t;
-}
-
-// The two fp16 terms of two values.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-}
-
-// The four codes of a word as two exact fp16 pairs.
-template <int KIND>
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &p01, uint32_t &p23) {
-    if constexpr (KIND == GQ_KV_I8) q8_to_f16x2(w, p01, p23);
-    else e4m3x4_to_f16x2(w, p01, p23);
-}
 // Byte j of x and byte j of y as one exact fp16 pair, j = 0 .. 3.
 template <int KIND>
 __device__ __forceinline__ void widen_pairs(uint32_t x, uint32_t y, uint32_t (&o)[4]) {
@@ -171,7 +102,7 @@ struct Span {
     int pre, start, units;   // units [0, pre) and [start, pre's end ..): `units` in all
 };
 
-__device__ __forceinline__ Span span_of(const RowsParams &p, const SeqStep &s) {
+__device__ __forceinline__ Span span_of(const AttnParams8 &p, const SeqStep &s) {
     Span r;
     const int n = s.held + s.n, end = (n + UNIT - 1) >> 5;
     int lo = 0, pre = 0, first = 0;
@@ -200,23 +131,18 @@ struct Cursor {
     Span u;
 };
 
-__device__ __forceinline__ void load_seq(const RowsParams &p, Cursor &k) {
-    k.s = seq_step(p.c, p.cu, k.b, p.T, p.max_n);
-    if (k.s.bad) {   // rows of an unusable sequence: one unit that nobody sees, a zero output
-        const int t1 = p.cu[k.b + 1];
-        const bool rows = k.s.t0 >= 0 && t1 > k.s.t0 && t1 <= p.T && t1 - k.s.t0 <= p.max_n;
-        k.s.n = rows ? t1 - k.s.t0 : 0;
-        k.s.held = -k.s.n;   // no tokens
-        k.s.seen = 0;
+__device__ __forceinline__ void load_seq(const AttnParams8 &p, Cursor &k) {
+    k.s = attn_step(p, k.b);
+    if (k.s.bad) {   // one unit that nobody sees
         k.u.pre = k.u.start = 0;
         k.u.units = 1;
     } else if (k.s.n > 0) {
         k.u = span_of(p, k.s);
     }
-    k.tiles = (k.s.n * p.G + ROWS - 1) / ROWS;
+    k.tiles = k.s.n * p.G > p.rows_over ? 0 : (k.s.n * p.G + ROWS - 1) / ROWS;
 }
 
-__device__ __forceinline__ void next_item(const RowsParams &p, Cursor &k) {
+__device__ __forceinline__ void next_item(const AttnParams8 &p, Cursor &k) {
     if (++k.tile < k.tiles) return;
     k.tile = 0;
     if (++k.h < p.c.Hkv) return;
@@ -230,7 +156,7 @@ __device__ __forceinline__ void next_item(const RowsParams &p, Cursor &k) {
 template <int KIND, int D>
 __global__ void __launch_bounds__(THREADS, 2)
     attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                           const RowsParams p) {
+                           const AttnParams8 p) {
     constexpr int SLOTS = slots_of(D), HALF = UNIT * D;      // bytes of a unit's keys
     constexpr int KS = D / 16;                               // MMA steps of a score
     constexpr int RUN = D / 4;                               // positions per lane
@@ -718,41 +644,49 @@ __global__ void __launch_bounds__(THREADS, 2)
 
 // ---------------------------------------------------------------------------
 // The weight that each page gathered: decay * in + sum over the step's query rows of
-// 2^(log2 of the page's weight sum - log2 of the row's denominator).
+// 2^(log2 of the page's weight sum - log2 of the row's denominator).  A CTA takes 32 pages
+// of one (sequence, head), a lane per page; its warps share the rows and are added in order.
+// The sums of groups that a row cannot see were never written: they are passed over.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(128) attn_pages_weights_kernel(const RowsParams p, const float *w_in, float *w_out,
-                                                                 float decay) {
+constexpr int WW = 8;   // warps
+
+__global__ void __launch_bounds__(WW * 32) attn_pages_weights_kernel(const AttnParams8 p, const float *w_in, float *w_out,
+                                                                     float decay) {
+    __shared__ float part[WW][32];
     const PagesView &c = p.c;
     pdl_launch_dependents();
+    const int tiles = (c.NB + 31) / 32, bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = (blockIdx.x % tiles) * 32 + lane;
     pdl_wait();
-    const int tiles = (c.NB + 127) / 128, bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
-    const int j = (blockIdx.x % tiles) * 128 + threadIdx.x;
-    if (j >= c.NB) return;
-    Cursor k;
-    k.b = b;
-    load_seq(p, k);
+    const SeqStep s = seq_step(c, p.cu, b, p.T, p.max_n);
+    const int end = s.bad ? 0 : s.held + s.n;
     const int64_t at = (int64_t)bh * c.NB + j;
-    const int64_t slot = (int64_t)j << p.lgP;
-    if (slot >= k.s.held + k.s.n) {
-        w_out[at] = 0.0f;
-        return;
-    }
+    const bool used = j < c.NB && ((int64_t)j << p.lgP) < end;
     float sum = 0.0f;
-    if (k.s.n > 0) {
-        const int per = 1 << (p.lgP - p.lgGroup), end = k.s.held + k.s.n;
-        for (int g = 0; g < per; g++) {
-            const int s0 = (int)slot + (g << p.lgGroup), u = s0 / UNIT;
-            if (s0 >= end || (u >= k.u.pre && u < k.u.start)) continue;   // nobody looked there
-            const float *gl = p.glse + ((int64_t)k.s.t0 * p.Hq + h * p.G) * p.NG + (s0 >> p.lgGroup);
-            const float *ls = p.lse + (int64_t)k.s.t0 * p.Hq + h * p.G;
-            for (int i = 0; i < k.s.n; i++)
-                for (int x = 0; x < p.G; x++) {
-                    const int64_t r = (int64_t)i * p.Hq + x;
-                    sum += ex2(gl[r * p.NG] - ls[r]);
-                }
+    if (used) {
+        const int base = c.base[at], slot = j << p.lgP;
+        const int groups = (min(c.P, end - slot) + (1 << p.lgGroup) - 1) >> p.lgGroup, size = 1 << p.lgGroup;
+        const float *gl = p.glse + (slot >> p.lgGroup);
+        for (int x = warp; x < s.n * p.G; x += WW) {
+            const int i = x / p.G, qpos = s.seen + i;
+            const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? __ldg(p.prefix + s.t0 + i) : 0;
+            const int lo = p.window > 0 ? (int)max((int64_t)first, (int64_t)qpos - p.window + 1) : first;
+            const int64_t r = (int64_t)(s.t0 + i) * p.Hq + h * p.G + (x - i * p.G);
+            const float l = __ldcg(p.lse + r);
+            for (int g = 0; g < groups; g++) {
+                const int x0 = base + g * size, x1 = x0 + size - 1;
+                if ((x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre))
+                    sum += ex2(__ldcg(gl + r * p.NG + g) - l);
+            }
         }
     }
-    w_out[at] = (w_in ? decay * w_in[at] : 0.0f) + sum;
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && j < c.NB) {
+        float total = part[0][lane];
+        for (int w = 1; w < WW; w++) total += part[w][lane];
+        w_out[at] = used ? (w_in ? decay * w_in[at] : 0.0f) + total : 0.0f;
+    }
 }
 
 int log2_of(int64_t x) {
@@ -761,8 +695,12 @@ int log2_of(int64_t x) {
     return l;
 }
 
+// Which kernel: a tile of the tensor-memory kernel holds 128 query rows of one KV head; sequences
+// with at most ROWS_MAX rows leave most of it idle and take the row kernel.
+constexpr int ROWS_MAX = 32;
+
 template <int KIND, int D>
-gq_status launch_rows(RowsParams p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
+gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
                       cudaStream_t s) {
     auto kernel = attn_pages_rows_kernel<KIND, D>;
     constexpr size_t smem = rows_smem_bytes<D>();
@@ -778,25 +716,34 @@ gq_status launch_rows(RowsParams p, const gq_kv_pages &c, int64_t T, const float
     const int grid = 2 * sm_count();
     const size_t parts = (size_t)grid * 2 * ROWS * D * 4, mls = (size_t)grid * 2 * ROWS * 8;
     const size_t lse = w_out ? ((size_t)T * p.Hq * 4 + 255) / 256 * 256 : 0;
-    const size_t glse = w_out ? (size_t)T * p.Hq * p.NG * 4 : 0;
+    const size_t glse = w_out ? ((size_t)T * p.Hq * p.NG * 4 + 255) / 256 * 256 : 0;
+    const bool tiles = (int64_t)p.max_n * p.G > ROWS_MAX;
+    // every sequence may still be small; with equal lengths, or one sequence, none is
+    const bool rows = !tiles || (c.B > 1 && T < c.B * (int64_t)p.max_n);
+    const size_t plan = tiles ? attn_pages_tc_workspace(c, T, p.G) : 0;
     Workspace ws{};
-    KV_TRY(get_workspace(s, (size_t)grid * sizeof(int), parts + mls + lse + glse, &ws));
+    KV_TRY(get_workspace(s, (size_t)grid * sizeof(int), parts + mls + lse + glse + plan, &ws));
     p.counters = reinterpret_cast<int *>(ws.counters);
     p.parts = reinterpret_cast<float *>(ws.data);
     p.part_ml = reinterpret_cast<float *>(ws.data + parts);
     p.lse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls) : nullptr;
     p.glse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls + lse) : nullptr;
-    alignas(64) CUtensorMap kmap, vmap;
-    const int64_t rows = c.pages * c.P * c.D / 128;
-    const int box = (int)(std::min<int64_t>(c.P, UNIT) * D / 128);
-    KV_TRY(byte_rows_map(&kmap, c.k, rows, box));
-    KV_TRY(byte_rows_map(&vmap, c.v, rows, box));
-    void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
-    KV_TRY(launch_pdl((const void *)kernel, dim3((unsigned)grid), dim3(THREADS), smem, s, args, "paged attention launch"));
+    p.rows_over = tiles ? ROWS_MAX : INT32_MAX;
+    if (tiles) KV_TRY(launch_attn_pages_tc(p, c, ws.data + parts + mls + lse + glse, s));
+    if (rows) {
+        alignas(64) CUtensorMap kmap, vmap;
+        const int64_t pool_rows = c.pages * c.P * c.D / 128;
+        const int box = (int)(std::min<int64_t>(c.P, UNIT) * D / 128);
+        KV_TRY(byte_rows_map(&kmap, c.k, pool_rows, box));
+        KV_TRY(byte_rows_map(&vmap, c.v, pool_rows, box));
+        void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
+        KV_TRY(launch_pdl((const void *)kernel, dim3((unsigned)grid), dim3(THREADS), smem, s, args,
+                          "paged attention launch"));
+    }
     if (w_out) {
-        const int64_t wgrid = c.B * c.Hkv * ((c.NB + 127) / 128);
+        const int64_t wgrid = c.B * c.Hkv * ((c.NB + 31) / 32);
         void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
-        KV_TRY(launch_pdl((const void *)attn_pages_weights_kernel, dim3((unsigned)wgrid), dim3(128), 0, s, wargs,
+        KV_TRY(launch_pdl((const void *)attn_pages_weights_kernel, dim3((unsigned)wgrid), dim3(WW * 32), 0, s, wargs,
                           "paged attention weights launch"));
     }
     return GQ_OK;
@@ -807,7 +754,7 @@ gq_status launch_rows(RowsParams p, const gq_kv_pages &c, int64_t T, const float
 gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, const float *q, int64_t ldq,
                             const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
                             const float *w_in, float *w_out, float decay, cudaStream_t s) {
-    RowsParams p{};
+    AttnParams8 p{};
     KV_TRY(pages_view(c, &p.c));
     p.q = q;
     p.out = out;

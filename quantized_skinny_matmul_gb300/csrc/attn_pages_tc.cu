@@ -1,0 +1,925 @@
+// attn_pages_tc.cu -- attention over the paged 8-bit KV cache for many query rows per KV head
+// (prompts and prompt chunks), on the 5th-generation tensor cores.
+//
+// The mathematics is attn_pages.cu's: a running maximum and sum over the cache, codes widened
+// to fp16 exactly, queries and softmax weights carried as two fp16 terms.  Per 128 query rows
+// and 128 tokens that is four 128 x 128 x D products: S = Qhi K + Qlo K, then
+// O += Phi V + Plo V: the bound is the tensor pipe at twice the arithmetic of the formula.
+//
+// One CTA per SM holds two tiles of 128 rows (row r = token r / G, head r % G of one KV head):
+//   warps 0-3, 4-7   softmax of tile 0 and tile 1, a thread per row: the scores come from
+//                    tensor memory, the weights' two terms go back in their place (the A
+//                    operand of the second product); also the query's conversion and the
+//                    output.  The output stays in tensor memory; it is rescaled only when a
+//                    row's maximum has grown by more than 2^8 (the weights have that room);
+//   warps 8-11       widen the codes of a block of 128 tokens from the raw copies into the
+//                    128-byte-swizzled operands (K by rows for the first product; the same
+//                    layout of V is the token-major B operand of the second);
+//   warp 12          chooses items and blocks, looks up pages, scales and positions, and
+//                    streams the raw codes in (tensor copies);
+//   warp 13          issues the MMAs: for block j and tile t, P_t(j) V(j), then Q_t K(j + 1),
+//                    so that the softmax of one tile runs beside the products of the other.
+// Tensor memory: S of both tiles (2 x 128 columns), O of both (2 x D).
+// Items (sequence, head, pair of tiles) are taken from a list that a small kernel lays out, in
+// turn, longest first within a sequence; which CTA takes which does not change any result.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attn_pages.cuh"
+#include "gq_common.cuh"
+#include "gq_internal.h"
+
+namespace gq {
+namespace {
+
+#define KV_TRY(expr)                  \
+    do {                              \
+        gq_status _st = (expr);       \
+        if (_st != GQ_OK) return _st; \
+    } while (0)
+
+constexpr int BR = 128;                     // query rows of a tile
+constexpr int BT = 128;                     // tokens of a block
+constexpr int GROUPS = BT / 16;             // scales and positions come by 16 tokens
+constexpr int METAS = 4;                    // blocks whose data is kept
+constexpr int THREADS = 512;
+enum : int { F_TILE0 = 1, F_TILE1 = 2, F_FIRST = 4, F_LAST = 8, F_EXIT = 16 };
+
+struct BlockMeta {
+    int flags;
+    int b, h, pair;             // the item
+    SeqStep s;
+    int slot, live;             // first slot of the block, tokens of it that are held
+    int lost;                   // bit i: group i has no usable page
+    float ks[GROUPS], vs[GROUPS];
+    int base[GROUPS];           // position of the group's first token
+};
+
+enum : int {
+    META_FULL = 0, META_EMPTY = META_FULL + METAS,
+    RAWK_FULL = META_EMPTY + METAS, RAWK_EMPTY, RAWV_FULL, RAWV_EMPTY,
+    K_FULL, K_EMPTY, V_FULL, V_EMPTY,
+    Q_FULL, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
+    ALL_DONE = O_FULL + 2, NUM_BARS
+};
+
+struct TileSmem {
+    uint64_t bars[NUM_BARS];
+    BlockMeta meta[METAS];
+    uint32_t tmem;
+};
+
+template <int D>
+struct TileLayout {
+    static constexpr int ATOM = BR * 128;                  // 128 rows x 64 halves: 16 KB
+    static constexpr int OPERAND = BR * D * 2;             // a tile of 128 x D halves
+    static constexpr int RAW = BT * D;
+    static constexpr int q = 0;                            // [tile][hi, lo]
+    static constexpr int k = q + 4 * OPERAND;
+    static constexpr int v = k + OPERAND;
+    static constexpr int rawk = v + OPERAND;
+    static constexpr int rawv = rawk + RAW;
+    static constexpr int ctl = rawv + RAW;
+    static constexpr int total = ctl + (int)sizeof(TileSmem);
+    static_assert(total + 1024 <= 227 * 1024, "shared memory");
+};
+
+constexpr uint32_t TM_S = 0, TM_O = 256;    // tensor-memory columns: S of tile t at 128 t, O at 256 + 128 t
+
+struct PlanView {
+    int2 *list;                 // (sequence, pair of tiles)
+    int *count, *next;          // entries, items taken
+};
+
+// ---- tcgen05 ---------------------------------------------------------------------------
+// Shared-memory matrix descriptors of 128-byte-swizzled operands.  Both operands lie as atoms
+// of 64 halves x rows (128 bytes a row, 8-row groups 1024 bytes apart).  Read by rows (K-major)
+// a K step of 16 is 32 bytes inside the atom; read token-major (V: N the positions, K the
+// tokens) the atoms are the leading offset and the 8-token groups the stride.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t leading) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(leading >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+    return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's lanes.  tm_wait ties the registers to the wait: nothing reads them before.
+__device__ __forceinline__ void tm_ld32(uint32_t a, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_wait(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
+                   "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                   "+f"(v[30]), "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const float *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Waits of one role: after one gave up, the role waits no more and leaves.
+struct Waiter {
+    unsigned int *status;
+    uint64_t *bars;
+    bool failed;
+    __device__ __forceinline__ bool operator()(int bar, int phase) {
+        if (!failed && !mbar_wait(smem_addr(bars + bar), (uint32_t)(phase & 1), status)) failed = true;
+        return !failed;
+    }
+    // the same for a whole warp, so that its lanes agree
+    __device__ __forceinline__ bool warp(int bar, int phase) {
+        (*this)(bar, phase);
+        failed = __any_sync(0xffffffffu, failed);
+        return !failed;
+    }
+    __device__ __forceinline__ void arrive(int bar) { mbar_arrive(smem_addr(bars + bar)); }
+};
+
+__device__ __forceinline__ int exponent_of(float x) {   // x < 2^e, clamped to [-100, 126]
+    return min(max((int)((__float_as_uint(x) >> 23) & 255u) - 126, -100), 126);
+}
+__device__ __forceinline__ float pow2i(int e) {         // 2^e, 0 below 2^-126
+    return e < -126 ? 0.0f : __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// ---- the list of items --------------------------------------------------------------------
+__global__ void __launch_bounds__(256) attn_pages_plan_kernel(const AttnParams8 p, const PlanView plan) {
+    __shared__ int sums[8];
+    __shared__ int carry;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < p.c.B; b0 += 256) {
+        const int b = b0 + tid;
+        int pairs = 0;
+        if (b < p.c.B) {
+            const SeqStep s = attn_step(p, b);
+            if (s.bad) atomicOr(p.c.status, STATUS_RANGE);
+            if (s.n * p.G > p.rows_over) pairs = (s.n * p.G + 2 * BR - 1) / (2 * BR);
+        }
+        int inc = pairs;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += t;
+        }
+        if (lane == 31) sums[warp] = inc;
+        __syncthreads();
+        int at = carry + inc - pairs, all = 0;
+        for (int w = 0; w < 8; w++) {
+            if (w < warp) at += sums[w];
+            all += sums[w];
+        }
+        for (int i = 0; i < pairs; i++) plan.list[at + i] = make_int2(b, pairs - 1 - i);
+        __syncthreads();
+        if (tid == 0) carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        *plan.count = carry;
+        *plan.next = 0;
+    }
+}
+
+// ---- warp 12: items, blocks, raw copies ---------------------------------------------------
+struct Item {
+    int b, h, pair;
+    SeqStep s;
+};
+
+template <int KIND, int D>
+__device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &plan, const CUtensorMap &kmap,
+                                          const CUtensorMap &vmap, uint8_t *smem, TileSmem &sm, Waiter &wait, int lane) {
+    using L = TileLayout<D>;
+    const PagesView &c = p.c;
+    const int items = *plan.count * c.Hkv;   // below 2^31: checked on the host
+    const uint32_t rawk = smem_addr(smem + L::rawk), rawv = smem_addr(smem + L::rawv);
+    const uint64_t policy = l2_evict_first_policy();
+    const int per = c.P / 16;                // groups per page
+    int nmeta = 0, nraw = 0;
+
+    auto publish = [&](const Item &x, int flags, int slot, int live, int lost, float ks, float vs, int base) {
+        const int st = nmeta % METAS;
+        if (nmeta >= METAS && !wait.warp(META_EMPTY + st, nmeta / METAS - 1)) return;
+        BlockMeta &d = sm.meta[st];
+        if (lane < GROUPS) {
+            d.ks[lane] = ks;
+            d.vs[lane] = vs;
+            d.base[lane] = base;
+        }
+        if (lane == 0) {
+            d.flags = flags;
+            d.b = x.b;
+            d.h = x.h;
+            d.pair = x.pair;
+            d.s = x.s;
+            d.slot = slot;
+            d.live = live;
+            d.lost = lost;
+        }
+        __syncwarp();
+        if (lane == 0) wait.arrive(META_FULL + st);
+        nmeta++;
+    };
+
+    while (!wait.failed) {
+        int item = 0;
+        if (lane == 0) item = atomicAdd(plan.next, 1);
+        item = __shfl_sync(0xffffffffu, item, 0);
+        Item x{0, 0, 0, {0, 0, 0, 0, false}};
+        if (item >= items) {
+            publish(x, F_EXIT, 0, 0, 0, 0.0f, 0.0f, 0);
+            break;
+        }
+        const int2 e = __ldcg(plan.list + item / c.Hkv);
+        x.b = e.x;
+        x.h = item % c.Hkv;
+        x.pair = e.y;
+        x.s = attn_step(p, x.b);
+        const int end = x.s.held + x.s.n;    // slots in use (0 for an unusable sequence)
+        // what the rows of each tile can see: positions lo .. hi, and those below pre
+        int lo[2] = {0, 0}, hi[2] = {-1, -1}, pre[2] = {0, 0}, lomin = 0x7fffffff, premax = 0, imax = 0;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            const int r0 = (x.pair * 2 + t) * BR, r1 = min(x.s.n * p.G, r0 + BR);
+            if (r0 >= r1) continue;
+            const int i0 = r0 / p.G, i1 = (r1 - 1) / p.G;
+            int l = 0x7fffffff, q = 0;
+            for (int i = i0 + lane; i <= i1; i += 32) {
+                int f = p.first ? __ldg(p.first + x.s.t0 + i) : 0;
+                if (p.window > 0) f = (int)max((int64_t)f, (int64_t)x.s.seen + i - p.window + 1);
+                l = min(l, f);
+                if (p.prefix) q = max(q, min(__ldg(p.prefix + x.s.t0 + i), 1 << 30));
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) {
+                l = min(l, __shfl_xor_sync(0xffffffffu, l, d));
+                q = max(q, __shfl_xor_sync(0xffffffffu, q, d));
+            }
+            lo[t] = max(l, 0);
+            hi[t] = x.s.seen + i1;
+            pre[t] = q;
+            lomin = min(lomin, lo[t]);
+            premax = max(premax, q);
+            imax = max(imax, i1);
+        }
+        // blocks [0, bp) and [b0, b1).  Positions are at least their slot, and distinct below
+        // seen + n: a position of at least X is in a slot of at least held - seen + X.
+        int b0 = 0, b1 = 0, bp = 0;
+        if (end > 0) {
+            const int top = max(x.s.held + imax + 1, min(end, premax));
+            const int low = (int)min((int64_t)(end - 1), max((int64_t)0, (int64_t)x.s.held - x.s.seen + lomin));
+            b1 = (top + BT - 1) / BT;
+            b0 = min(low / BT, b1);
+            bp = min((min(end, premax) + BT - 1) / BT, b0);
+        }
+        const int blocks = bp + b1 - b0;
+        const int64_t trow = ((int64_t)x.b * c.Hkv + x.h) * c.NB;
+        // A block that some row sees is sent once the next one is known, so that the last can say
+        // so.  The values of the one that waits (w...): lane g holds those of group g.
+        int wflags = 0, wslot = 0, wlive = 0, wlost = 0, wbase = 0, wpage = -1;
+        float wks = 0.0f, wvs = 0.0f;
+        bool first = true;
+        for (int i = 0; i <= blocks && !wait.failed; i++) {
+            const bool done = i == blocks;
+            float ks = 0.0f, vs = 0.0f;
+            int base = 0x7f000000, page = -1, active = 0, slot = 0, live = 0, lost = 0;   // a position nobody sees
+            if (!done) {
+                slot = (i < bp ? i : b0 + i - bp) * BT;
+                live = min(BT, end - slot);
+                bool bad = false;
+                if (lane < GROUPS && 16 * lane < live) {
+                    const int at = slot + 16 * lane, j = at >> p.lgP;
+                    page = __ldg(c.table + trow + j);
+                    bad = (unsigned)page >= (unsigned)c.pages;
+                    if (bad) {
+                        atomicOr(c.status, STATUS_RANGE);
+                        page = -1;
+                    } else {
+                        ks = __ldg(c.ks + page);
+                        vs = __ldg(c.vs + page);
+                        base = __ldg(c.base + trow + j) + (at & (c.P - 1));
+                    }
+                }
+                lost = (int)__ballot_sync(0xffffffffu, bad);
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const bool see = page >= 0 && hi[t] >= 0 && ((base + 15 >= lo[t] && base <= hi[t]) || base < pre[t]);
+                    if (__any_sync(0xffffffffu, see)) active |= F_TILE0 << t;
+                }
+                if (!active) continue;
+            }
+            if (wflags || done) {   // (with no block at all: one that says only that the item is over)
+                publish(x, wflags | (first ? F_FIRST : 0) | (done ? F_LAST : 0), wslot, wlive, wlost, wks, wvs, wbase);
+                first = false;
+                if (wflags && !wait.failed) {
+                    if (nraw > 0) {
+                        wait.warp(RAWK_EMPTY, nraw - 1);
+                        wait.warp(RAWV_EMPTY, nraw - 1);
+                    }
+                    if (wait.failed) break;
+                    const bool mine = lane < GROUPS && wpage >= 0 && lane % per == 0;
+                    const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * c.P * D);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(smem_addr(sm.bars + RAWK_FULL), bytes);
+                        mbar_arrive_expect_tx(smem_addr(sm.bars + RAWV_FULL), bytes);
+                    }
+                    __syncwarp();
+                    if (mine) {
+                        const int row = (int)((int64_t)wpage * c.P * D / 128);
+                        tma_rows(rawk + lane * 16 * D, &kmap, row, smem_addr(sm.bars + RAWK_FULL), policy);
+                        tma_rows(rawv + lane * 16 * D, &vmap, row, smem_addr(sm.bars + RAWV_FULL), policy);
+                    }
+                    nraw++;
+                }
+            }
+            wflags = active;
+            wslot = slot;
+            wlive = live;
+            wlost = lost;
+            wks = ks;
+            wvs = vs;
+            wbase = base;
+            wpage = page;
+        }
+    }
+    // stay until every copy issued has landed
+    if (nraw > 0) {
+        mbar_wait(smem_addr(sm.bars + RAWK_FULL), (uint32_t)((nraw - 1) & 1), c.status);
+        mbar_wait(smem_addr(sm.bars + RAWV_FULL), (uint32_t)((nraw - 1) & 1), c.status);
+    }
+}
+
+// ---- warp 13: the products ------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem, int lane) {
+    using L = TileLayout<D>;
+    constexpr uint32_t idq = idesc_f16(BR, BT, false), idp = idesc_f16(BR, D, true);
+    const uint32_t qa = smem_addr(smem + L::q), ka = smem_addr(smem + L::k), va = smem_addr(smem + L::v);
+    int nk = 0, nv = 0, nitem = 0, np0 = 0, np1 = 0;   // blocks, products with V, items, weights of each tile so far
+    int prev = 0, started = 0;    // tiles whose weights wait for V; tiles with a product in this item
+
+    auto commit = [&](int bar) {
+        if (lane == 0) mma_commit(smem_addr(sm.bars + bar));
+        __syncwarp();
+    };
+    // P_t V of the block before; the item's first one overwrites O_t
+    auto pv = [&](int t) {
+        if (t == 0) wait.warp(P_FULL, np0++);
+        else wait.warp(P_FULL + 1, np1++);
+        if (wait.failed) return;
+        tc_after();
+        if (lane == 0) {
+            const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
+            const uint64_t vd = desc_sw128(va, L::ATOM);
+            const uint32_t keep = (started >> t) & 1;
+#pragma unroll
+            for (int term = 0; term < 2; term++)
+#pragma unroll
+                for (int kk = 0; kk < BT / 16; kk++)
+                    mma_ts(o, s + 32 * (kk >> 1) + 16 * term + 8 * (kk & 1), vd + (uint64_t)(2048 * kk >> 4), idp, term | kk ? 1u : keep);
+        }
+        __syncwarp();
+        started |= 1 << t;
+    };
+    auto qk = [&](int t) {
+        if (lane == 0) {
+            const uint64_t kd = desc_sw128(ka, 16);
+#pragma unroll
+            for (int term = 0; term < 2; term++) {
+                const uint64_t qd = desc_sw128(qa + (2 * t + term) * L::OPERAND, 16);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; kk++) {
+                    const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
+                    mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term | kk ? 1u : 0u);
+                }
+            }
+            mma_commit(smem_addr(sm.bars + S_FULL + t));
+        }
+        __syncwarp();
+    };
+
+    for (int i = 0;; i++) {
+        const int st = i % METAS;
+        if (!wait.warp(META_FULL + st, i / METAS)) return;
+        const int flags = sm.meta[st].flags, now = flags & (F_TILE0 | F_TILE1);
+        __syncwarp();
+        if (lane == 0) wait.arrive(META_EMPTY + st);
+        if (flags & F_EXIT) return;
+        if (flags & F_FIRST) {
+            wait.warp(Q_FULL, nitem);
+            wait.warp(Q_FULL + 1, nitem);
+            nitem++;
+            started = 0;
+        }
+        if (prev) wait.warp(V_FULL, nv);
+        bool have_k = false;
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            if (wait.failed) return;
+            if ((prev >> t) & 1) {
+                pv(t);
+                if (wait.failed) return;
+                if (t == 1 || !(prev & F_TILE1)) commit(V_EMPTY);
+            }
+            if ((now >> t) & 1) {
+                if (!have_k) wait.warp(K_FULL, nk);
+                have_k = true;
+                if (wait.failed) return;
+                tc_after();
+                qk(t);
+            }
+        }
+        if (prev) nv++;
+        if (now) {
+            commit(K_EMPTY);
+            nk++;
+        }
+        prev = now;
+        if (flags & F_LAST) {
+            if (prev) {
+                wait.warp(V_FULL, nv++);
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    if (wait.failed) return;
+                    if ((prev >> t) & 1) pv(t);
+                    if (wait.failed) return;
+                    if ((started >> t) & 1) commit(O_FULL + t);
+                }
+                commit(V_EMPTY);
+            }
+            prev = 0;
+        }
+    }
+}
+
+// ---- warps 8-11: codes to operands, a thread per token ----------------------------------------
+template <int KIND, int D>
+__device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t op, int tok, bool dead) {
+    using L = TileLayout<D>;
+#pragma unroll
+    for (int ch = 0; ch < D / 16; ch++) {
+        uint32_t a;
+        if (D == 128) a = raw + tok * 128 + ((ch ^ (tok & 7)) << 4);
+        else a = raw + (tok >> 1) * 128 + (((4 * (tok & 1) + ch) ^ ((tok >> 1) & 7)) << 4);
+        uint4 w = sh_ld128(a);
+        if (dead) w = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t o[8];
+        widen4<KIND>(w.x, o[0], o[1]);
+        widen4<KIND>(w.y, o[2], o[3]);
+        widen4<KIND>(w.z, o[4], o[5]);
+        widen4<KIND>(w.w, o[6], o[7]);
+        const uint32_t dst = op + (ch >> 2) * L::ATOM + tok * 128;
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((((ch & 3) * 2 + x) ^ (tok & 7)) << 4)),
+                         "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+                         : "memory");
+    }
+}
+
+template <int KIND, int D>
+__device__ __forceinline__ void widen_role(uint8_t *smem, TileSmem &sm, Waiter &wait, int tok, int lane) {
+    using L = TileLayout<D>;
+    int n = 0;
+    for (int i = 0;; i++) {
+        const int st = i % METAS;
+        if (!wait.warp(META_FULL + st, i / METAS)) return;
+        const BlockMeta &m = sm.meta[st];
+        const int flags = m.flags;
+        // slots past the last token, and lost pages, may hold any bytes (NaN codes among them)
+        const bool dead = tok >= m.live || ((m.lost >> (tok >> 4)) & 1);
+        __syncwarp();
+        if (lane == 0) wait.arrive(META_EMPTY + st);
+        if (flags & F_EXIT) return;
+        if (!(flags & (F_TILE0 | F_TILE1))) continue;
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+            wait.warp(kv ? RAWV_FULL : RAWK_FULL, n);
+            if (n > 0) wait.warp(kv ? V_EMPTY : K_EMPTY, n - 1);
+            if (wait.failed) return;
+            widen_tile<KIND, D>(smem_addr(smem + (kv ? L::rawv : L::rawk)), smem_addr(smem + (kv ? L::v : L::k)), tok, dead);
+            fence_proxy_async_shared();   // the MMAs (async proxy) read what these threads wrote
+            __syncwarp();
+            if (lane == 0) {
+                wait.arrive(kv ? V_FULL : K_FULL);
+                wait.arrive(kv ? RAWV_EMPTY : RAWK_EMPTY);
+            }
+        }
+        n++;
+    }
+}
+
+// ---- warps 0-7: softmax, a thread per row ------------------------------------------------------
+template <int D>
+__device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem,
+                                             int t, int row, int lane) {
+    using L = TileLayout<D>;
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16;   // this warp's tensor-memory lanes
+    const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
+    const float cap2 = p.cap * LOG2E;
+    int ns = 0, no = 0;
+    // the row
+    bool real = false, any = false;
+    int ti = 0, head = 0, qpos = 0, seelo = 0, firstp = 0, pre = 0, all_lo = 0, all_hi = 0, vex = 0;
+    float f = 0.0f, slope = 0.0f, mrow = -INFINITY, lrow = 0.0f;
+
+    for (int i = 0;; i++) {
+        const int st = i % METAS;
+        if (!wait.warp(META_FULL + st, i / METAS)) return;
+        const BlockMeta &m = sm.meta[st];
+        const int flags = m.flags;
+        if (flags & F_EXIT) return;
+        if (flags & F_FIRST) {
+            const SeqStep s = m.s;
+            const int r = (m.pair * 2 + t) * BR + row;
+            real = r < s.n * p.G;
+            ti = s.t0 + (real ? r / p.G : 0);
+            head = m.h * p.G + (real ? r % p.G : 0);
+            qpos = s.seen + ti - s.t0;
+            firstp = p.first ? __ldg(p.first + ti) : 0;
+            pre = p.prefix ? min(__ldg(p.prefix + ti), 1 << 30) : 0;
+            slope = p.slopes ? __ldg(p.slopes + head) * LOG2E : 0.0f;
+            seelo = p.window > 0 ? (int)max((int64_t)firstp, (int64_t)qpos - p.window + 1) : firstp;
+            all_lo = real ? seelo : 0;
+            all_hi = real ? qpos : 0x7fffffff;
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) {
+                all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, d));
+                all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, d));
+            }
+            mrow = -INFINITY;
+            lrow = 0.0f;
+            any = false;
+            // the query row, scaled by a power of two into [2^14, 2^15), as two fp16 terms
+            const float4 *q = reinterpret_cast<const float4 *>(p.q + (int64_t)ti * p.ldq + (int64_t)head * D);
+            float am = 0.0f;
+#pragma unroll 8
+            for (int x = 0; x < D / 4; x++)
+                if (real) am = fmaxf(am, absmax4(__ldg(q + x)));
+            const int ex = exponent_of(am);
+            const float up = real ? pow2i(15 - ex) : 0.0f;
+            const uint32_t qs = smem_addr(smem + L::q) + 2 * t * L::OPERAND + row * 128;
+#pragma unroll 4
+            for (int x = 0; x < D / 8; x++) {   // read again, from L1
+                const float4 v0 = __ldg(q + 2 * x), v1 = __ldg(q + 2 * x + 1);
+                uint32_t hi[4], lo[4];
+                split2(v0.x * up, v0.y * up, hi[0], lo[0]);
+                split2(v0.z * up, v0.w * up, hi[1], lo[1]);
+                split2(v1.x * up, v1.y * up, hi[2], lo[2]);
+                split2(v1.z * up, v1.w * up, hi[3], lo[3]);
+                const uint32_t a = qs + (x >> 3) * L::ATOM + (((x & 7) ^ (row & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
+                             "r"(hi[3])
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + L::OPERAND), "r"(lo[0]), "r"(lo[1]),
+                             "r"(lo[2]), "r"(lo[3])
+                             : "memory");
+            }
+            f = pow2i(ex - 15) * p.scale;
+            f = p.cap > 0.0f ? f / p.cap : f * LOG2E;
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) wait.arrive(Q_FULL + t);
+        }
+        if (flags & (F_TILE0 << t)) {
+            const int live = m.live;
+            bool whole = live == BT;   // every row sees every token (warp-uniform)
+            float vmax = 0.0f;
+#pragma unroll
+            for (int g = 0; g < GROUPS; g++) {
+                whole = whole && m.base[g] >= all_lo && m.base[g] + 15 <= all_hi;
+                vmax = fmaxf(vmax, m.vs[g]);
+            }
+            const bool simple = whole && p.cap == 0.0f && !p.slopes;
+            if (!wait.warp(S_FULL + t, ns++)) return;
+            tc_after();
+            // ---- the block's maximum.  Where more than the scales is to be applied, the finished
+            // scores go back to tensor memory, so that it is done once.
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (simple) {
+#pragma unroll
+                for (int x = 0; x < BT; x += 64) {
+                    float s0[32], s1[32];
+                    tm_ld32(ts + x, s0);
+                    tm_ld32(ts + x + 32, s1);
+                    tm_wait(s0);
+                    tm_wait(s1);
+#pragma unroll
+                    for (int g = 0; g < 2; g++) {
+                        const float f0 = f * m.ks[x / 16 + g], f1 = f * m.ks[x / 16 + 2 + g];
+                        float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            a0 = fmaxf(a0, s0[16 * g + e] * f0);
+                            a1 = fmaxf(a1, s1[16 * g + e] * f1);
+                        }
+                        mx[2 * g] = fmaxf(mx[2 * g], a0);
+                        mx[2 * g + 1] = fmaxf(mx[2 * g + 1], a1);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int x = 0; x < BT; x += 32) {
+                    float s[32];
+                    tm_ld32(ts + x, s);
+                    tm_wait(s);
+#pragma unroll
+                    for (int g = 0; g < 2; g++) {
+                        const float fk = f * m.ks[x / 16 + g];
+                        const int base = m.base[x / 16 + g];
+#pragma unroll
+                        for (int e = 0; e < 16; e++) s[16 * g + e] *= fk;
+                        if (p.cap > 0.0f) {
+#pragma unroll
+                            for (int e = 0; e < 16; e++) s[16 * g + e] = cap2 * tanh_f32(s[16 * g + e]);
+                        }
+                        if (p.slopes) {
+#pragma unroll
+                            for (int e = 0; e < 16; e++) s[16 * g + e] -= slope * (float)abs(qpos - (base + e));
+                        }
+                        if (!whole) {
+#pragma unroll
+                            for (int e = 0; e < 16; e++) {
+                                const int y = base + e;
+                                const bool see = x + 16 * g + e < live && y >= firstp && (y < pre || (y >= seelo && y <= qpos));
+                                s[16 * g + e] = see ? s[16 * g + e] : -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; e++) mx[e & 3] = fmaxf(mx[e & 3], s[16 * g + e]);
+                    }
+                    tm_st32(ts + x, s);
+                }
+                tm_wait_st();
+            }
+            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // The sums are relative to mrow, which may lag behind the maximum by 8 (the weights
+            // then reach 2^8), and O to 2^(vex - 4), where a value scale may exceed 2^vex by 8
+            // times: weights times scales stay below 2^15.
+            const int ve = exponent_of(vmax);
+            const bool grow = mb > mrow + 8.0f || (mrow == -INFINITY && mb != -INFINITY);
+            const int vnew = !any || ve > vex + 3 ? ve : vex;
+            if (__any_sync(0xffffffffu, grow) || vnew != vex) {
+                const float mnew = grow ? mb : mrow;
+                const float a = mnew == mrow ? 1.0f : ex2(mrow - mnew);
+                lrow *= a;
+                if (any) {
+                    const float ao = a * pow2i(vex - vnew);
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        float o[32];
+                        tm_ld32(to + x, o);
+                        tm_wait(o);
+#pragma unroll
+                        for (int y = 0; y < 32; y++) o[y] *= ao;
+                        tm_st32(to + x, o);
+                    }
+                }
+                mrow = mnew;
+                vex = vnew;
+            }
+            any = true;
+            // ---- the weights: 32 tokens at a time, their two terms in the columns of their scores
+            // (columns 0 .. 15 of each 32 the first term, 16 .. 31 the second)
+            const float msafe = mrow == -INFINITY ? 0.0f : mrow, vu = pow2i(4 - vex);
+            float *gl = nullptr;
+            if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
+#pragma unroll
+            for (int x = 0; x < BT; x += 32) {
+                float s[32], sum[2];
+                uint32_t hi[16], lo[16];
+                tm_ld32(ts + x, s);
+                tm_wait(s);
+#pragma unroll
+                for (int g = 0; g < 2; g++) {
+                    const float vv = m.vs[x / 16 + g] * vu, fk = simple ? f * m.ks[x / 16 + g] : 1.0f;
+                    float q[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float p0 = ex2(fmaf(s[16 * g + e], fk, -msafe)), p1 = ex2(fmaf(s[16 * g + e + 1], fk, -msafe));
+                        q[0] += p0;
+                        q[1] += p1;
+                        split2(p0 * vv, p1 * vv, hi[8 * g + e / 2], lo[8 * g + e / 2]);
+                    }
+                    sum[g] = q[0] + q[1];
+                }
+                lrow += sum[0] + sum[1];
+                if (gl && real && x < live) {
+                    if (p.lgGroup == 4) {
+                        gl[x / 16] = __log2f(sum[0]) + msafe;
+                        if (x + 16 < live) gl[x / 16 + 1] = __log2f(sum[1]) + msafe;
+                    } else {
+                        gl[x / 32] = __log2f(sum[0] + sum[1]) + msafe;
+                    }
+                }
+                tm_st16(ts + x, hi);
+                tm_st16(ts + x + 16, lo);
+            }
+            tm_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) wait.arrive(P_FULL + t);
+        }
+        if (flags & F_LAST) {
+            const float l = lrow;
+            const float inv = l > 0.0f ? pow2i(vex - 4) / l : 0.0f;
+            float4 *out = reinterpret_cast<float4 *>(p.out + (int64_t)ti * p.ldo + (int64_t)head * D);
+            if (any) {
+                if (!wait.warp(O_FULL + t, no++)) return;
+                tc_after();
+            }
+#pragma unroll
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                if (any) {
+                    tm_ld32(to + x, o);
+                    tm_wait(o);
+                }
+                if (real)
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4)
+                        out[(x + y) / 4] = any && l > 0.0f ? make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv)
+                                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            tc_before();   // O is overwritten only after these loads (the next item's P_FULL)
+            if (p.lse && real) p.lse[(int64_t)ti * p.Hq + head] = l > 0.0f ? mrow + log2f(l) : INFINITY;
+        }
+        __syncwarp();
+        if (lane == 0) wait.arrive(META_EMPTY + st);
+    }
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
+template <int KIND, int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_pages_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                           const AttnParams8 p, const PlanView plan) {
+    using L = TileLayout<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TileSmem &sm = *reinterpret_cast<TileSmem *>(smem + L::ctl);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PagesView &c = p.c;
+    Waiter wait{c.status, sm.bars, false};
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        auto init = [&](int bar, int n) { mbar_init(smem_addr(sm.bars + bar), (uint32_t)n); };
+        for (int i = 0; i < METAS; i++) {
+            init(META_FULL + i, 1);
+            init(META_EMPTY + i, 13);      // 8 softmax warps, 4 widening warps, the MMA warp
+        }
+        init(RAWK_FULL, 1);
+        init(RAWV_FULL, 1);
+        init(RAWK_EMPTY, 4);
+        init(RAWV_EMPTY, 4);
+        init(K_FULL, 4);
+        init(V_FULL, 4);
+        init(K_EMPTY, 1);
+        init(V_EMPTY, 1);
+        for (int t = 0; t < 2; t++) {
+            init(Q_FULL + t, 4);
+            init(S_FULL + t, 1);
+            init(P_FULL + t, 4);
+            init(O_FULL + t, 1);
+        }
+        init(ALL_DONE, 1);
+        fence_barrier_init();
+    }
+    if (warp == 13) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sm.tmem;
+    pdl_wait();
+
+    if (warp >= 12) {
+        if (warp == 12) lead_role<KIND, D>(p, plan, kmap, vmap, smem, sm, wait, lane);
+        if (warp == 13) {
+            mma_role<D>(smem, sm, wait, tmem, lane);
+            // the products issued have completed before shared and tensor memory are given up
+            if (lane == 0) mma_commit(smem_addr(sm.bars + ALL_DONE));
+            __syncwarp();
+            mbar_wait(smem_addr(sm.bars + ALL_DONE), 0u, c.status);
+        }
+    } else if (warp >= 8) {
+        widen_role<KIND, D>(smem, sm, wait, threadIdx.x - 256, lane);
+    } else {
+        softmax_role<D>(p, smem, sm, wait, tmem, warp >> 2, threadIdx.x & 127, lane);
+    }
+    __syncthreads();
+    if (warp == 13) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+template <int KIND, int D>
+gq_status launch_tiles(const AttnParams8 &p, const gq_kv_pages &c, const PlanView &plan, int64_t items, cudaStream_t s) {
+    auto kernel = attn_pages_tile_kernel<KIND, D>;
+    constexpr int smem = TileLayout<D>::total + 1024;
+    static std::atomic<bool> smem_set[64];
+    int dev = 0;
+    KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
+    if (dev < 0 || dev >= 64) return fail(GQ_ERR_UNSUPPORTED_DEVICE, "device index %d", dev);
+    if (!smem_set[dev].load(std::memory_order_acquire)) {
+        KV_TRY(check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                          "paged attention shared-memory attribute"));
+        smem_set[dev].store(true, std::memory_order_release);
+    }
+    alignas(64) CUtensorMap kmap, vmap;
+    const int64_t rows = c.pages * c.P * c.D / 128;
+    const int box = (int)(c.P * D / 128);
+    KV_TRY(byte_rows_map(&kmap, c.k, rows, box));
+    KV_TRY(byte_rows_map(&vmap, c.v, rows, box));
+    void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p, (void *)&plan};
+    return launch_pdl((const void *)kernel, dim3((unsigned)std::min<int64_t>(items, sm_count())), dim3(THREADS), smem, s,
+                      args, "paged attention (tiles) launch");
+}
+
+// At most so many pairs of tiles: the rows of all sequences, and a last pair of each.
+int64_t most_pairs(const gq_kv_pages &c, int64_t T, int64_t G) { return T * G / (2 * BR) + std::min(c.B, T) + 1; }
+
+}  // namespace
+
+size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t T, int64_t G) {
+    return 256 + (size_t)most_pairs(c, T, G) * sizeof(int2);
+}
+
+gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8_t *work, cudaStream_t s) {
+    PlanView plan{};
+    plan.count = reinterpret_cast<int *>(work);
+    plan.next = plan.count + 1;
+    plan.list = reinterpret_cast<int2 *>(work + 256);
+    const int64_t items = most_pairs(c, p.T, p.G) * c.Hkv;
+    if (items > INT32_MAX) return fail(GQ_ERR_INVALID_ARG, "attention grid too large");
+    void *args[] = {(void *)&p, (void *)&plan};
+    KV_TRY(launch_pdl((const void *)attn_pages_plan_kernel, dim3(1), dim3(256), 0, s, args, "paged attention plan launch"));
+    if (c.kind == GQ_KV_I8)
+        return c.D == 64 ? launch_tiles<GQ_KV_I8, 64>(p, c, plan, items, s) : launch_tiles<GQ_KV_I8, 128>(p, c, plan, items, s);
+    return c.D == 64 ? launch_tiles<GQ_KV_E4M3, 64>(p, c, plan, items, s)
+                     : launch_tiles<GQ_KV_E4M3, 128>(p, c, plan, items, s);
+}
+
+}  // namespace gq

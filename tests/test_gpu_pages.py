@@ -196,6 +196,9 @@ SHAPES = [
     (1, 2, 2, 128, 64, [40, 0, 129], [33, 64, 7], True),         # prompt chunks
     (0, 1, 64, 64, 128, [90], [2], False),
     (0, 5, 1, 64, 16, [3] * 200, [1] * 200, False),              # many short sequences
+    (0, 1, 4, 128, 32, [150], [100], False),                     # tiles of 128 rows: two pairs
+    (1, 2, 1, 64, 16, [0, 700, 3], [290, 33, 1], True),          # and rows, in one batch
+    (0, 1, 3, 64, 128, [260, 5], [86, 200], True),
 ]
 
 
