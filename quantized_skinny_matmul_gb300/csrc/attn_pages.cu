@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     constexpr int KS = D / 16;                               // MMA steps of a score
     constexpr int RUN = D / 4;                               // positions per lane
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
     float *red = reinterpret_cast<float *>(ring + (size_t)SLOTS * 2 * HALF);          // [W][ROWS][D]
     RowsSmem &sm = *reinterpret_cast<RowsSmem *>(red + W * ROWS * D);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

@@ -47,7 +47,16 @@ constexpr int BR = 128;                     // query rows of a tile
 constexpr int BT = 128;                     // tokens of a block
 constexpr int GROUPS = BT / 16;             // scales and positions come by 16 tokens
 constexpr int METAS = 4;                    // blocks whose data is kept
+// The tensor cores add to their f32 accumulators with truncation: after N products an output is
+// off by about N 2^-26 of itself, one way.  Every FLUSH blocks (16 products each) a tile's O is
+// added to a running sum in memory, rounded to nearest, and begun anew: without it a row over 4,500
+// tokens was off by 8e-6.
+constexpr int FLUSH = 8;
 constexpr int THREADS = 512;
+// Registers per thread of the four warpgroups: they add up to the 4 x 128 of the launch.
+constexpr int REGS_SOFTMAX = 168, REGS_REST = 88;
+static_assert(2 * REGS_SOFTMAX + 2 * REGS_REST <= 4 * 65536 / THREADS, "register split");
+
 enum : int { F_TILE0 = 1, F_TILE1 = 2, F_FIRST = 4, F_LAST = 8, F_EXIT = 16 };
 
 struct BlockMeta {
@@ -63,9 +72,9 @@ struct BlockMeta {
 enum : int {
     META_FULL = 0, META_EMPTY = META_FULL + METAS,
     RAWK_FULL = META_EMPTY + METAS, RAWK_EMPTY, RAWV_FULL, RAWV_EMPTY,
-    K_FULL, K_EMPTY, V_FULL, V_EMPTY,
+    K_FULL, V_FULL, V_EMPTY,   // (K is free once the scores of the block's last tile are there)
     Q_FULL, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
-    ALL_DONE = O_FULL + 2, NUM_BARS
+    TILE_SYNC = O_FULL + 2, ALL_DONE = TILE_SYNC + 2, NUM_BARS
 };
 
 struct TileSmem {
@@ -94,6 +103,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256;    // tensor-memory columns: S of tile 
 struct PlanView {
     int2 *list;                 // (sequence, pair of tiles)
     int *count, *next;          // entries, items taken
+    float *sums;                // [CTA][2][D / 4][BR][4]: the tiles' flushed output sums
 };
 
 // ---- tcgen05 ---------------------------------------------------------------------------
@@ -169,6 +179,50 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *v) {
         : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two f32 at a time.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
 
 // Waits of one role: after one gave up, the role waits no more and leaves.
 struct Waiter {
@@ -251,7 +305,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
     const uint32_t rawk = smem_addr(smem + L::rawk), rawv = smem_addr(smem + L::rawv);
     const uint64_t policy = l2_evict_first_policy();
     const int per = c.P / 16;                // groups per page
-    int nmeta = 0, nraw = 0;
+    int nmeta = 0, nk = 0, nraw = 0;   // blocks published, copies of keys and of values issued
 
     auto publish = [&](const Item &x, int flags, int slot, int live, int lost, float ks, float vs, int base) {
         const int st = nmeta % METAS;
@@ -368,23 +422,18 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
                 publish(x, wflags | (first ? F_FIRST : 0) | (done ? F_LAST : 0), wslot, wlive, wlost, wks, wvs, wbase);
                 first = false;
                 if (wflags && !wait.failed) {
-                    if (nraw > 0) {
-                        wait.warp(RAWK_EMPTY, nraw - 1);
-                        wait.warp(RAWV_EMPTY, nraw - 1);
-                    }
-                    if (wait.failed) break;
                     const bool mine = lane < GROUPS && wpage >= 0 && lane % per == 0;
                     const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * c.P * D);
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(smem_addr(sm.bars + RAWK_FULL), bytes);
-                        mbar_arrive_expect_tx(smem_addr(sm.bars + RAWV_FULL), bytes);
-                    }
+                    const int row = (int)((int64_t)wpage * c.P * D / 128);
+                    if (nraw > 0 && !wait.warp(RAWK_EMPTY, nraw - 1)) break;
+                    if (lane == 0) mbar_arrive_expect_tx(smem_addr(sm.bars + RAWK_FULL), bytes);
                     __syncwarp();
-                    if (mine) {
-                        const int row = (int)((int64_t)wpage * c.P * D / 128);
-                        tma_rows(rawk + lane * 16 * D, &kmap, row, smem_addr(sm.bars + RAWK_FULL), policy);
-                        tma_rows(rawv + lane * 16 * D, &vmap, row, smem_addr(sm.bars + RAWV_FULL), policy);
-                    }
+                    if (mine) tma_rows(rawk + lane * 16 * D, &kmap, row, smem_addr(sm.bars + RAWK_FULL), policy);
+                    nk++;
+                    if (nraw > 0 && !wait.warp(RAWV_EMPTY, nraw - 1)) break;
+                    if (lane == 0) mbar_arrive_expect_tx(smem_addr(sm.bars + RAWV_FULL), bytes);
+                    __syncwarp();
+                    if (mine) tma_rows(rawv + lane * 16 * D, &vmap, row, smem_addr(sm.bars + RAWV_FULL), policy);
                     nraw++;
                 }
             }
@@ -399,10 +448,8 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         }
     }
     // stay until every copy issued has landed
-    if (nraw > 0) {
-        mbar_wait(smem_addr(sm.bars + RAWK_FULL), (uint32_t)((nraw - 1) & 1), c.status);
-        mbar_wait(smem_addr(sm.bars + RAWV_FULL), (uint32_t)((nraw - 1) & 1), c.status);
-    }
+    if (nk > 0) mbar_wait(smem_addr(sm.bars + RAWK_FULL), (uint32_t)((nk - 1) & 1), c.status);
+    if (nraw > 0) mbar_wait(smem_addr(sm.bars + RAWV_FULL), (uint32_t)((nraw - 1) & 1), c.status);
 }
 
 // ---- warp 13: the products ------------------------------------------------------------------
@@ -411,15 +458,16 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
     using L = TileLayout<D>;
     constexpr uint32_t idq = idesc_f16(BR, BT, false), idp = idesc_f16(BR, D, true);
     const uint32_t qa = smem_addr(smem + L::q), ka = smem_addr(smem + L::k), va = smem_addr(smem + L::v);
-    int nk = 0, nv = 0, nitem = 0, np0 = 0, np1 = 0;   // blocks, products with V, items, weights of each tile so far
-    int prev = 0, started = 0;    // tiles whose weights wait for V; tiles with a product in this item
+    int nk = 0, nv = 0, nitem = 0, np0 = 0, np1 = 0, no0 = 0, no1 = 0;   // blocks, products with V, items, weights of each tile, those of the item
+    int prev = 0, started = 0, fresh_q = 0;    // tiles whose weights wait for V; tiles with a product in this item; queries not yet waited for
 
     auto commit = [&](int bar) {
         if (lane == 0) mma_commit(smem_addr(sm.bars + bar));
         __syncwarp();
     };
-    // P_t V of the block before; the item's first one overwrites O_t
+    // P_t V of the block before; the item's first one, and the first after a flush, overwrites O_t
     auto pv = [&](int t) {
+        const int in_item = t == 0 ? no0++ : no1++;
         if (t == 0) wait.warp(P_FULL, np0++);
         else wait.warp(P_FULL + 1, np1++);
         if (wait.failed) return;
@@ -427,7 +475,7 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
         if (lane == 0) {
             const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
             const uint64_t vd = desc_sw128(va, L::ATOM);
-            const uint32_t keep = (started >> t) & 1;
+            const uint32_t keep = in_item % FLUSH ? 1u : 0u;
 #pragma unroll
             for (int term = 0; term < 2; term++)
 #pragma unroll
@@ -441,12 +489,12 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
         if (lane == 0) {
             const uint64_t kd = desc_sw128(ka, 16);
 #pragma unroll
-            for (int term = 0; term < 2; term++) {
+            for (int term = 1; term >= 0; term--) {   // the small terms first: less is lost to truncation
                 const uint64_t qd = desc_sw128(qa + (2 * t + term) * L::OPERAND, 16);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk++) {
                     const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term | kk ? 1u : 0u);
+                    mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term == 0 || kk ? 1u : 0u);
                 }
             }
             mma_commit(smem_addr(sm.bars + S_FULL + t));
@@ -462,10 +510,9 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
         if (lane == 0) wait.arrive(META_EMPTY + st);
         if (flags & F_EXIT) return;
         if (flags & F_FIRST) {
-            wait.warp(Q_FULL, nitem);
-            wait.warp(Q_FULL + 1, nitem);
             nitem++;
-            started = 0;
+            started = no0 = no1 = 0;
+            fresh_q = F_TILE0 | F_TILE1;
         }
         if (prev) wait.warp(V_FULL, nv);
         bool have_k = false;
@@ -480,16 +527,15 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
             if ((now >> t) & 1) {
                 if (!have_k) wait.warp(K_FULL, nk);
                 have_k = true;
+                if ((fresh_q >> t) & 1) wait.warp(Q_FULL + t, nitem - 1);
+                fresh_q &= ~(1 << t);
                 if (wait.failed) return;
                 tc_after();
                 qk(t);
             }
         }
         if (prev) nv++;
-        if (now) {
-            commit(K_EMPTY);
-            nk++;
-        }
+        if (now) nk++;
         prev = now;
         if (flags & F_LAST) {
             if (prev) {
@@ -512,7 +558,7 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
 template <int KIND, int D>
 __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t op, int tok, bool dead) {
     using L = TileLayout<D>;
-#pragma unroll
+#pragma unroll 2
     for (int ch = 0; ch < D / 16; ch++) {
         uint32_t a;
         if (D == 128) a = raw + tok * 128 + ((ch ^ (tok & 7)) << 4);
@@ -536,7 +582,7 @@ __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t op, int tok, b
 template <int KIND, int D>
 __device__ __forceinline__ void widen_role(uint8_t *smem, TileSmem &sm, Waiter &wait, int tok, int lane) {
     using L = TileLayout<D>;
-    int n = 0;
+    int n = 0, ns0 = 0, ns1 = 0, last = 0;   // blocks, scores of each tile, the last tile of the block before
     for (int i = 0;; i++) {
         const int st = i % METAS;
         if (!wait.warp(META_FULL + st, i / METAS)) return;
@@ -548,10 +594,13 @@ __device__ __forceinline__ void widen_role(uint8_t *smem, TileSmem &sm, Waiter &
         if (lane == 0) wait.arrive(META_EMPTY + st);
         if (flags & F_EXIT) return;
         if (!(flags & (F_TILE0 | F_TILE1))) continue;
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; kv++) {
             wait.warp(kv ? RAWV_FULL : RAWK_FULL, n);
-            if (n > 0) wait.warp(kv ? V_EMPTY : K_EMPTY, n - 1);
+            if (n > 0) {
+                if (kv) wait.warp(V_EMPTY, n - 1);
+                else wait.warp(S_FULL + last, (last ? ns1 : ns0) - 1);
+            }
             if (wait.failed) return;
             widen_tile<KIND, D>(smem_addr(smem + (kv ? L::rawv : L::rawk)), smem_addr(smem + (kv ? L::v : L::k)), tok, dead);
             fence_proxy_async_shared();   // the MMAs (async proxy) read what these threads wrote
@@ -562,22 +611,39 @@ __device__ __forceinline__ void widen_role(uint8_t *smem, TileSmem &sm, Waiter &
             }
         }
         n++;
+        ns0 += flags & F_TILE0 ? 1 : 0;
+        ns1 += flags & F_TILE1 ? 1 : 0;
+        last = flags & F_TILE1 ? 1 : 0;
     }
 }
 
 // ---- warps 0-7: softmax, a thread per row ------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem,
-                                             int t, int row, int lane) {
+                                             float *sums, int t, int row, int lane) {
     using L = TileLayout<D>;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;   // this warp's tensor-memory lanes
     const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
     const float cap2 = p.cap * LOG2E;
     int ns = 0, no = 0;
     // the row
-    bool real = false, any = false;
+    bool real = false;
     int ti = 0, head = 0, qpos = 0, seelo = 0, firstp = 0, pre = 0, all_lo = 0, all_hi = 0, vex = 0;
     float f = 0.0f, slope = 0.0f, mrow = -INFINITY, lrow = 0.0f;
+    // the running sum of flushed parts: this thread's float4s, D / 4 of them, BR apart; in units of
+    // 2^gex, relative to gmax
+    float4 *sum = reinterpret_cast<float4 *>(sums) + ((size_t)blockIdx.x * 2 + t) * (D / 4) * BR + row;
+    int blocks = 0, gex = 0;       // blocks of the item so far
+    float gmax = -INFINITY;
+    // the four warps of the tile, with a bounded wait
+    int nsync = 0;
+    auto sync_tile = [&]() {
+        __syncwarp();
+        if (lane == 0) wait.arrive(TILE_SYNC + t);
+        return wait.warp(TILE_SYNC + t, nsync++);
+    };
+    // what takes the running sum to the present units
+    auto carry = [&]() { return blocks <= FLUSH ? 0.0f : (gmax == mrow ? 1.0f : ex2(gmax - mrow)) * pow2i(gex - vex); };
 
     for (int i = 0;; i++) {
         const int st = i % METAS;
@@ -605,33 +671,61 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             }
             mrow = -INFINITY;
             lrow = 0.0f;
-            any = false;
-            // the query row, scaled by a power of two into [2^14, 2^15), as two fp16 terms
-            const float4 *q = reinterpret_cast<const float4 *>(p.q + (int64_t)ti * p.ldq + (int64_t)head * D);
-            float am = 0.0f;
-#pragma unroll 8
-            for (int x = 0; x < D / 4; x++)
-                if (real) am = fmaxf(am, absmax4(__ldg(q + x)));
-            const int ex = exponent_of(am);
-            const float up = real ? pow2i(15 - ex) : 0.0f;
-            const uint32_t qs = smem_addr(smem + L::q) + 2 * t * L::OPERAND + row * 128;
-#pragma unroll 4
-            for (int x = 0; x < D / 8; x++) {   // read again, from L1
-                const float4 v0 = __ldg(q + 2 * x), v1 = __ldg(q + 2 * x + 1);
-                uint32_t hi[4], lo[4];
-                split2(v0.x * up, v0.y * up, hi[0], lo[0]);
-                split2(v0.z * up, v0.w * up, hi[1], lo[1]);
-                split2(v1.x * up, v1.y * up, hi[2], lo[2]);
-                split2(v1.z * up, v1.w * up, hi[3], lo[3]);
-                const uint32_t a = qs + (x >> 3) * L::ATOM + (((x & 7) ^ (row & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
-                             "r"(hi[3])
-                             : "memory");
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a + L::OPERAND), "r"(lo[0]), "r"(lo[1]),
-                             "r"(lo[2]), "r"(lo[3])
-                             : "memory");
+            blocks = 0;
+            // The query rows of this warp, each scaled by a power of two into [2^14, 2^15), as two fp16
+            // terms.  A row is read by D / 4 lanes together (whole lines: a lane per row costs 32 L1
+            // accesses an instruction), and the row's thread is told its power.
+            constexpr int LPR = D / 4, RPI = 32 / LPR, BATCH = 16;
+            const int64_t mine = real ? (int64_t)ti * p.ldq + (int64_t)head * D : -1;
+            const int part = lane / LPR, col = lane % LPR;
+            const uint32_t qs = smem_addr(smem + L::q) + 2 * t * L::OPERAND + (col >> 4) * L::ATOM + (col & 1) * 8;
+            int ex = 0;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += BATCH * RPI) {
+                float4 v[BATCH];
+#pragma unroll
+                for (int x = 0; x < BATCH; x++) {
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, r0 + x * RPI + part);
+                    v[x] = at >= 0 ? __ldg(reinterpret_cast<const float4 *>(p.q + at) + col) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                // the maxima of BATCH rows over LPR lanes: each exchange halves the rows a lane holds
+                float am[BATCH];
+#pragma unroll
+                for (int x = 0; x < BATCH; x++) am[x] = absmax4(v[x]);
+#pragma unroll
+                for (int h = BATCH / 2, d = LPR / 2; d >= 1; d >>= 1, h >>= 1) {
+                    if (h >= 1) {
+                        const bool up = (col & d) != 0;
+#pragma unroll
+                        for (int x = 0; x < BATCH / 2; x++)
+                            if (x < h) {
+                                const float send = up ? am[x] : am[x + h], keep = up ? am[x + h] : am[x];
+                                am[x] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, d));
+                            }
+                    } else {
+                        am[0] = fmaxf(am[0], __shfl_xor_sync(0xffffffffu, am[0], d));
+                    }
+                }
+                // lane (part, col) holds row x = col / (LPR / BATCH) of its part
+                const int e0 = exponent_of(am[0]);
+#pragma unroll
+                for (int x = 0; x < BATCH; x++) {
+                    const int e = __shfl_sync(0xffffffffu, e0, part * LPR + x * (LPR / BATCH));
+                    const int rr = r0 + x * RPI + part, R = (row & ~31) + rr;
+                    const float up = p.scale < 0.0f ? -pow2i(15 - e) : pow2i(15 - e);   // f is not negative
+                    uint32_t h0, h1, l0, l1;
+                    split2(v[x].x * up, v[x].y * up, h0, l0);
+                    split2(v[x].z * up, v[x].w * up, h1, l1);
+                    const uint32_t at = qs + R * 128 + ((((col & 15) >> 1) ^ (R & 7)) << 4);
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(h0), "r"(h1) : "memory");
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::OPERAND), "r"(l0), "r"(l1) : "memory");
+                }
+                // the row's own thread: row lane = r0 + x RPI + y is held by part y, row x
+                const int x = (lane - r0) / RPI, y = (lane - r0) % RPI;
+                const int ey = __shfl_sync(0xffffffffu, e0, (y * LPR + x * (LPR / BATCH)) & 31);
+                if (lane >= r0 && lane < r0 + BATCH * RPI) ex = ey;
             }
-            f = pow2i(ex - 15) * p.scale;
+            f = pow2i(ex - 15) * fabsf(p.scale);
             f = p.cap > 0.0f ? f / p.cap : f * LOG2E;
             fence_proxy_async_shared();
             __syncwarp();
@@ -652,8 +746,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // ---- the block's maximum.  Where more than the scales is to be applied, the finished
             // scores go back to tensor memory, so that it is done once.
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (simple) {
-#pragma unroll
+            if (simple) {   // f is not negative: a group's largest raw score is its largest score
+#pragma unroll 1
                 for (int x = 0; x < BT; x += 64) {
                     float s0[32], s1[32];
                     tm_ld32(ts + x, s0);
@@ -662,15 +756,16 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                     tm_wait(s1);
 #pragma unroll
                     for (int g = 0; g < 2; g++) {
-                        const float f0 = f * m.ks[x / 16 + g], f1 = f * m.ks[x / 16 + 2 + g];
-                        float a0 = -INFINITY, a1 = -INFINITY;
+                        float a0 = s0[16 * g], a1 = s1[16 * g];
 #pragma unroll
-                        for (int e = 0; e < 16; e++) {
-                            a0 = fmaxf(a0, s0[16 * g + e] * f0);
-                            a1 = fmaxf(a1, s1[16 * g + e] * f1);
+                        for (int e = 1; e < 15; e += 2) {
+                            a0 = max3(a0, s0[16 * g + e], s0[16 * g + e + 1]);
+                            a1 = max3(a1, s1[16 * g + e], s1[16 * g + e + 1]);
                         }
-                        mx[2 * g] = fmaxf(mx[2 * g], a0);
-                        mx[2 * g + 1] = fmaxf(mx[2 * g + 1], a1);
+                        a0 = fmaxf(a0, s0[16 * g + 15]);
+                        a1 = fmaxf(a1, s1[16 * g + 15]);
+                        mx[2 * g] = fmaxf(mx[2 * g], a0 * (f * m.ks[x / 16 + g]));
+                        mx[2 * g + 1] = fmaxf(mx[2 * g + 1], a1 * (f * m.ks[x / 16 + 2 + g]));
                     }
                 }
             } else {
@@ -714,12 +809,33 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // times: weights times scales stay below 2^15.
             const int ve = exponent_of(vmax);
             const bool grow = mb > mrow + 8.0f || (mrow == -INFINITY && mb != -INFINITY);
-            const int vnew = !any || ve > vex + 3 ? ve : vex;
+            // (this block's scores come after the products of the block before: O is complete up to it)
+            if (blocks > 0 && blocks % FLUSH == 0) {
+                const float cs = carry();
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    float o[32];
+                    tm_ld32(to + x, o);
+                    tm_wait(o);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4) {
+                        float4 *at = sum + (x + y) / 4 * BR;
+                        float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (blocks > FLUSH) g = __ldcg(at);
+                        __stcg(at, make_float4(fmaf(g.x, cs, o[y]), fmaf(g.y, cs, o[y + 1]), fmaf(g.z, cs, o[y + 2]),
+                                               fmaf(g.w, cs, o[y + 3])));
+                    }
+                }
+                gmax = mrow;
+                gex = vex;
+            }
+            const bool have_o = blocks % FLUSH != 0;
+            const int vnew = blocks == 0 || ve > vex + 3 ? ve : vex;
             if (__any_sync(0xffffffffu, grow) || vnew != vex) {
                 const float mnew = grow ? mb : mrow;
                 const float a = mnew == mrow ? 1.0f : ex2(mrow - mnew);
                 lrow *= a;
-                if (any) {
+                if (have_o) {
                     const float ao = a * pow2i(vex - vnew);
 #pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
@@ -734,30 +850,44 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 mrow = mnew;
                 vex = vnew;
             }
-            any = true;
+            blocks++;
             // ---- the weights: 32 tokens at a time, their two terms in the columns of their scores
             // (columns 0 .. 15 of each 32 the first term, 16 .. 31 the second)
             const float msafe = mrow == -INFINITY ? 0.0f : mrow, vu = pow2i(4 - vex);
             float *gl = nullptr;
             if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
-#pragma unroll
-            for (int x = 0; x < BT; x += 32) {
-                float s[32], sum[2];
+            const uint64_t nm = pack2(-msafe, -msafe);
+            float s[2][32];
+            tm_ld32(ts, s[0]);
+            // 32 tokens from s[cur] while the next 32 are on their way
+            auto weigh = [&](int x, float (&cur)[32], float (&next)[32]) {
+                tm_wait(cur);
+                if (x + 32 < BT) tm_ld32(ts + x + 32, next);
                 uint32_t hi[16], lo[16];
-                tm_ld32(ts + x, s);
-                tm_wait(s);
+                float sum[2];
 #pragma unroll
                 for (int g = 0; g < 2; g++) {
                     const float vv = m.vs[x / 16 + g] * vu, fk = simple ? f * m.ks[x / 16 + g] : 1.0f;
-                    float q[2] = {0.0f, 0.0f};
+                    const uint64_t vv2 = pack2(vv, vv), fk2 = pack2(fk, fk);
+                    uint64_t q = 0ull;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float p0 = ex2(fmaf(s[16 * g + e], fk, -msafe)), p1 = ex2(fmaf(s[16 * g + e + 1], fk, -msafe));
-                        q[0] += p0;
-                        q[1] += p1;
-                        split2(p0 * vv, p1 * vv, hi[8 * g + e / 2], lo[8 * g + e / 2]);
+                        float p0, p1;
+                        unpack2(fma2(pack2(cur[16 * g + e], cur[16 * g + e + 1]), fk2, nm), p0, p1);
+                        const uint64_t w = pack2(ex2(p0), ex2(p1));
+                        q = add2(q, w);
+                        // the first term: the leading 11 bits; the second: the rest, exact in f32
+                        const uint64_t y = mul2(w, vv2);
+                        unpack2(y, p0, p1);
+                        p0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
+                        p1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
+                        hi[8 * g + e / 2] = half2_of(p0, p1);
+                        unpack2(add2(y, pack2(-p0, -p1)), p0, p1);
+                        lo[8 * g + e / 2] = half2_of(p0, p1);
                     }
-                    sum[g] = q[0] + q[1];
+                    float q0, q1;
+                    unpack2(q, q0, q1);
+                    sum[g] = q0 + q1;
                 }
                 lrow += sum[0] + sum[1];
                 if (gl && real && x < live) {
@@ -770,6 +900,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 }
                 tm_st16(ts + x, hi);
                 tm_st16(ts + x + 16, lo);
+            };
+#pragma unroll 1   // (code that fits the instruction caches: five roles run different parts of it)
+            for (int x = 0; x < BT; x += 64) {
+                weigh(x, s[0], s[1]);
+                weigh(x + 32, s[1], s[0]);
             }
             tm_wait_st();
             tc_before();
@@ -779,24 +914,47 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
         if (flags & F_LAST) {
             const float l = lrow;
             const float inv = l > 0.0f ? pow2i(vex - 4) / l : 0.0f;
-            float4 *out = reinterpret_cast<float4 *>(p.out + (int64_t)ti * p.ldo + (int64_t)head * D);
-            if (any) {
+            const float cs = carry() * inv;
+            if (blocks > 0) {
                 if (!wait.warp(O_FULL + t, no++)) return;
                 tc_after();
             }
-#pragma unroll
+            // out by way of the query's memory (every product that read it is done): a row is stored
+            // by D / 4 lanes together.  Each warp has a quarter of it: 32 rows of D f32, 16-byte
+            // chunk x of row r at chunk x ^ (r mod 8).
+            constexpr int LPR = D / 4, RPI = 32 / LPR;
+            const uint32_t stage = smem_addr(smem + L::q) + 2 * t * L::OPERAND + (row >> 5) * (L::OPERAND / 2);
+            if (!sync_tile()) return;   // the four warps' products: all of them are done
+#pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 float o[32];
-                if (any) {
+                if (blocks > 0) {
                     tm_ld32(to + x, o);
                     tm_wait(o);
                 }
-                if (real)
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4)
-                        out[(x + y) / 4] = any && l > 0.0f ? make_float4(o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv)
-                                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int y = 0; y < 32; y += 4) {
+                    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f), g = r;
+                    if (blocks > FLUSH) g = __ldcg(sum + (x + y) / 4 * BR);
+                    if (l > 0.0f)
+                        r = make_float4(fmaf(g.x, cs, o[y] * inv), fmaf(g.y, cs, o[y + 1] * inv),
+                                        fmaf(g.z, cs, o[y + 2] * inv), fmaf(g.w, cs, o[y + 3] * inv));
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * D * 4 + ((((x + y) / 4) ^ (lane & 7)) << 4)),
+                                 "f"(r.x), "f"(r.y), "f"(r.z), "f"(r.w)
+                                 : "memory");
+                }
             }
+            __syncwarp();
+            const int64_t mine = real ? (int64_t)ti * p.ldo + (int64_t)head * D : -1;
+            const int part = lane / LPR, col = lane % LPR;
+#pragma unroll 4
+            for (int r0 = 0; r0 < 32; r0 += RPI) {
+                const int rr = r0 + part;
+                const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
+                const uint4 v = sh_ld128(stage + rr * D * 4 + ((col ^ (rr & 7)) << 4));
+                if (at >= 0) *(reinterpret_cast<uint4 *>(p.out + at) + col) = v;
+            }
+            if (!sync_tile()) return;   // the next item's queries go into the same memory
             tc_before();   // O is overwritten only after these loads (the next item's P_FULL)
             if (p.lse && real) p.lse[(int64_t)ti * p.Hq + head] = l > 0.0f ? mrow + log2f(l) : INFINITY;
         }
@@ -812,7 +970,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                            const AttnParams8 p, const PlanView plan) {
     using L = TileLayout<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
     TileSmem &sm = *reinterpret_cast<TileSmem *>(smem + L::ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const PagesView &c = p.c;
@@ -831,13 +989,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         init(RAWV_EMPTY, 4);
         init(K_FULL, 4);
         init(V_FULL, 4);
-        init(K_EMPTY, 1);
         init(V_EMPTY, 1);
         for (int t = 0; t < 2; t++) {
             init(Q_FULL + t, 4);
             init(S_FULL + t, 1);
             init(P_FULL + t, 4);
             init(O_FULL + t, 1);
+            init(TILE_SYNC + t, 4);
         }
         init(ALL_DONE, 1);
         fence_barrier_init();
@@ -855,6 +1013,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_wait();
 
     if (warp >= 12) {
+        regs_dec<REGS_REST>();
         if (warp == 12) lead_role<KIND, D>(p, plan, kmap, vmap, smem, sm, wait, lane);
         if (warp == 13) {
             mma_role<D>(smem, sm, wait, tmem, lane);
@@ -864,9 +1023,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_wait(smem_addr(sm.bars + ALL_DONE), 0u, c.status);
         }
     } else if (warp >= 8) {
+        regs_dec<REGS_REST>();
         widen_role<KIND, D>(smem, sm, wait, threadIdx.x - 256, lane);
     } else {
-        softmax_role<D>(p, smem, sm, wait, tmem, warp >> 2, threadIdx.x & 127, lane);
+        regs_inc<REGS_SOFTMAX>();
+        softmax_role<D>(p, smem, sm, wait, tmem, plan.sums, warp >> 2, threadIdx.x & 127, lane);
     }
     __syncthreads();
     if (warp == 13) {
@@ -904,7 +1065,8 @@ int64_t most_pairs(const gq_kv_pages &c, int64_t T, int64_t G) { return T * G / 
 }  // namespace
 
 size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t T, int64_t G) {
-    return 256 + (size_t)most_pairs(c, T, G) * sizeof(int2);
+    return 256 + ((size_t)most_pairs(c, T, G) * sizeof(int2) + 255) / 256 * 256 +
+           (size_t)sm_count() * 2 * c.D * BR * sizeof(float);
 }
 
 gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8_t *work, cudaStream_t s) {
@@ -912,6 +1074,7 @@ gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8
     plan.count = reinterpret_cast<int *>(work);
     plan.next = plan.count + 1;
     plan.list = reinterpret_cast<int2 *>(work + 256);
+    plan.sums = reinterpret_cast<float *>(work + 256 + ((size_t)most_pairs(c, p.T, p.G) * sizeof(int2) + 255) / 256 * 256);
     const int64_t items = most_pairs(c, p.T, p.G) * c.Hkv;
     if (items > INT32_MAX) return fail(GQ_ERR_INVALID_ARG, "attention grid too large");
     void *args[] = {(void *)&p, (void *)&plan};
