@@ -44,11 +44,18 @@ namespace {
     } while (0)
 
 constexpr int UNIT = 32;                    // tokens per unit
-constexpr int W = 4;                        // consumer warps
+// Consumer warps: two CTAs of 7 + 1 warps at 128 registers fill an SM.  (With 4 + 1 at 168, the
+// query's fragments in registers, the warps' own latency bound the kernel: 128 sequences of up to
+// 2,048 tokens on 32 heads took 324 us.)
+constexpr int W = 7;
 constexpr int CONSUMERS = W * 32, THREADS = CONSUMERS + 32;
 constexpr int ROWS = 8;                     // query rows of an item
+constexpr int ITEMS = 2;                    // items whose data is kept
 
-__host__ __device__ constexpr int slots_of(int D) { return D == 128 ? 11 : 24; }   // two CTAs per SM
+// Slots of the ring (56 KB).  A multiple of W: the warp that takes a slot's unit also takes the next
+// one in that slot.  Otherwise a warp could wait for a slot's next phase before the present one is
+// over (copies land in any order), and a parity wait two phases ahead passes at once.
+__host__ __device__ constexpr int slots_of(int D) { return D == 128 ? W : 2 * W; }
 
 struct UnitMeta {               // beside each slot: scales and first positions of the two halves
     float ks[2], vs[2];
@@ -57,21 +64,48 @@ struct UnitMeta {               // beside each slot: scales and first positions 
     int lost;                   // bit i: half i has no usable page
 };
 
+// A stretch of an item's units that this CTA works on, put there by the producer.
+struct ItemRec {
+    int64_t item0;              // line position of the item's first unit
+    int u0, u1, units;          // units of the stretch, units of the item
+    int pre, start;             // its span
+    int rows;                   // query rows (0 .. ROWS)
+    int ti[ROWS], head[ROWS], qpos[ROWS];   // of each row: token, query head, position
+    int first[ROWS], prefix[ROWS];
+    float slope[ROWS];          // times log2 e
+};
+
 struct RowsSmem {
-    uint64_t full[24], empty[24];
-    UnitMeta meta[24];
-    float ml[2][W][ROWS][2];    // [parity]: maximum and denominator of each warp
+    uint64_t full[2 * W], empty[2 * W], item_full[ITEMS], item_empty[ITEMS];
+    UnitMeta meta[2 * W];
+    ItemRec item[ITEMS];
+    float ml[W][ROWS][2];       // maximum and denominator of each warp
     int64_t start, total;       // line position of the sequence that the CTA starts in
     int start_b, last;
     int64_t warp_sum[THREADS / 32];
 };
 
 template <int D>
-__host__ __device__ constexpr size_t rows_smem_bytes() {
-    return 1024 + (size_t)slots_of(D) * UNIT * D * 2 + (size_t)W * ROWS * D * 4 + sizeof(RowsSmem);
-}
+struct RowsLayout {
+    static constexpr int ring = 0;                                     // units: keys, values
+    static constexpr int q = ring + slots_of(D) * UNIT * D * 2;        // [ITEMS][ROWS][D] f32
+    static constexpr int frag = q + ITEMS * ROWS * D * 4;              // the query's MMA fragments
+    static constexpr int red = frag + D * 32;                          // [W][ROWS][D] f32
+    static constexpr int ctl = red + W * ROWS * D * 4;
+    static constexpr int total = ctl + (int)sizeof(RowsSmem);
+    static_assert(2 * (total + 2048) <= 228 * 1024, "two CTAs per SM");
+};
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory"); }
+// The same, with the answer whether any thread said yes.
+__device__ __forceinline__ bool consumer_any(bool yes) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes), "n"(CONSUMERS)
+                 : "memory");
+    return r != 0;
+}
 
 // Byte j of x and byte j of y as one exact fp16 pair, j = 0 .. 3.
 template <int KIND>
@@ -153,17 +187,69 @@ __device__ __forceinline__ void next_item(const AttnParams8 &p, Cursor &k) {
     } while (k.tiles == 0);
 }
 
+// Joins the pieces of an item that several CTAs worked on, in their order, into its output rows:
+// a warp per row, a lane per D / 32 columns.  The lanes first take 32 pieces' maxima and
+// denominators each; then every piece's weight goes from its lane to all.
+template <int D>
+__device__ __forceinline__ void join_pieces(const AttnParams8 &p, const ItemRec &it, int c0, int c1, int warp, int lane) {
+    constexpr int V = D / 32;
+    const int n = c1 - c0 + 1;
+    for (int rr = warp; rr < it.rows; rr += W) {
+        // the item begins in CTA c0 (its slot 1); it is the first item of the others (slot 0)
+        auto piece = [&](int i) { return ((int64_t)(c0 + i) * 2 + (i == 0)) * ROWS + rr; };
+        float mt = -INFINITY;
+        for (int i = lane; i < n; i += 32) mt = fmaxf(mt, __ldcg(p.part_ml + piece(i) * 2));
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
+        float a[V], l = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) a[v] = 0.0f;
+        for (int i0 = 0; i0 < n && mt != -INFINITY; i0 += 32) {
+            float e = 0.0f, el = 0.0f;
+            if (i0 + lane < n) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + piece(i0 + lane) * 2));
+                e = ex2(ml.x - mt);
+                el = e * ml.y;
+            }
+            const int m = min(32, n - i0);
+#pragma unroll 8
+            for (int i = 0; i < m; i++) {
+                const float w = __shfl_sync(0xffffffffu, e, i);
+                l += __shfl_sync(0xffffffffu, el, i);
+                const float *src = p.parts + piece(i0 + i) * D + V * lane;
+                if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+                    a[0] = fmaf(w, x.x, a[0]);
+                    a[1] = fmaf(w, x.y, a[1]);
+                    a[2] = fmaf(w, x.z, a[2]);
+                    a[3] = fmaf(w, x.w, a[3]);
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+                    a[0] = fmaf(w, x.x, a[0]);
+                    a[1] = fmaf(w, x.y, a[1]);
+                }
+            }
+        }
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        float *out = p.out + (int64_t)it.ti[rr] * p.ldo + (int64_t)it.head[rr] * D + V * lane;
+        if constexpr (V == 4) *reinterpret_cast<float4 *>(out) = make_float4(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+        else *reinterpret_cast<float2 *>(out) = make_float2(a[0] * inv, a[1] * inv);
+        if (p.lse && lane == 0) p.lse[(int64_t)it.ti[rr] * p.Hq + it.head[rr]] = l > 0.0f ? mt + log2f(l) : INFINITY;
+    }
+}
+
 template <int KIND, int D>
 __global__ void __launch_bounds__(THREADS, 2)
     attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const AttnParams8 p) {
+    using L = RowsLayout<D>;
     constexpr int SLOTS = slots_of(D), HALF = UNIT * D;      // bytes of a unit's keys
     constexpr int KS = D / 16;                               // MMA steps of a score
     constexpr int RUN = D / 4;                               // positions per lane
+    static_assert(SLOTS % W == 0, "a slot belongs to one warp");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
-    float *red = reinterpret_cast<float *>(ring + (size_t)SLOTS * 2 * HALF);          // [W][ROWS][D]
-    RowsSmem &sm = *reinterpret_cast<RowsSmem *>(red + W * ROWS * D);
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
+    RowsSmem &sm = *reinterpret_cast<RowsSmem *>(smem + L::ctl);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagesView &c = p.c;
 
@@ -172,6 +258,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         for (int s = 0; s < SLOTS; s++) {
             mbar_init(smem_addr(sm.full + s), 1);
             mbar_init(smem_addr(sm.empty + s), 1);
+        }
+        for (int s = 0; s < ITEMS; s++) {
+            mbar_init(smem_addr(sm.item_full + s), 1);
+            mbar_init(smem_addr(sm.item_empty + s), W);
         }
         fence_barrier_init();
     }
@@ -223,27 +313,66 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int64_t total = sm.total, piece = max((int64_t)W, (total + gridDim.x - 1) / gridDim.x);
     const int64_t lo = piece * blockIdx.x, hi = min(total, lo + piece);
     if (lo >= hi) return;
-    Cursor k;
-    k.b = sm.start_b;
-    load_seq(p, k);
-    int64_t item0;   // line position of the item's first unit
-    {
-        const int64_t i = (lo - sm.start) / k.u.units;
-        k.tile = (int)(i % k.tiles);
-        k.h = (int)(i / k.tiles);
-        item0 = sm.start + i * k.u.units;
-    }
 
     // ---------------------------------------------------------------- producer
     if (warp == W) {
+        Cursor k;
+        k.b = sm.start_b;
+        load_seq(p, k);
+        int64_t item0;   // line position of the item's first unit
+        {
+            const int64_t i = (lo - sm.start) / k.u.units;
+            k.tile = (int)(i % k.tiles);
+            k.h = (int)(i / k.tiles);
+            item0 = sm.start + i * k.u.units;
+        }
         const uint64_t policy = l2_evict_first_policy();
-        int count = 0;
+        int count = 0, items = 0;
         bool ok = true;
         const int rows16 = D / 8;   // 128-byte pool rows of 16 tokens
         for (int64_t at = lo; at < hi && ok;) {
             const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
             const int64_t trow = ((int64_t)k.b * c.Hkv + k.h) * c.NB;
             const int n = k.s.held + k.s.n;
+            // ---- the item: its rows (row r is token r / G, head r % G of the group) and queries
+            {
+                const int st = items % ITEMS, rows = min(ROWS, k.s.n * p.G - k.tile * ROWS);
+                const int r = k.tile * ROWS + (lane < rows ? lane : 0), i = r / p.G;
+                const int ti = k.s.t0 + i, head = k.h * p.G + r - i * p.G;
+                const int first = p.first ? __ldg(p.first + ti) : 0, pre = p.prefix ? min(__ldg(p.prefix + ti), 1 << 30) : 0;
+                const float slope = p.slopes ? __ldg(p.slopes + head) * LOG2E : 0.0f;
+                if (items >= ITEMS)
+                    ok = mbar_wait(smem_addr(sm.item_empty + st), (uint32_t)((items / ITEMS - 1) & 1), c.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ItemRec &it = sm.item[st];
+                if (lane < ROWS) {
+                    it.ti[lane] = ti;
+                    it.head[lane] = head;
+                    it.qpos[lane] = k.s.seen + i;
+                    it.first[lane] = first;
+                    it.prefix[lane] = pre;
+                    it.slope[lane] = slope;
+                }
+                if (lane == 0) {
+                    it.item0 = item0;
+                    it.u0 = u0;
+                    it.u1 = u1;
+                    it.units = k.u.units;
+                    it.pre = k.u.pre;
+                    it.start = k.u.start;
+                    it.rows = rows;
+                }
+                __syncwarp();
+                const uint32_t bar = smem_addr(sm.item_full + st);
+                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(rows * D * 4));
+                __syncwarp();
+                if (lane < rows)   // (a lane per row)
+                    bulk_g2s(smem_addr(smem + L::q + (st * ROWS + lane) * D * 4), p.q + (int64_t)ti * p.ldq + (int64_t)head * D,
+                             (uint32_t)(D * 4), bar);
+                __syncwarp();
+                items++;
+            }
             for (int ub = u0; ub < u1 && ok; ub += 32) {
                 // each lane looks up one unit: its pages, their scales and positions
                 const int u = ub + lane;
@@ -280,7 +409,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     if (!ok) break;
                     if (lane == i) {
                         const uint32_t bar = smem_addr(sm.full + sl);
-                        const uint32_t dst = smem_addr(ring + (size_t)sl * 2 * HALF);
+                        const uint32_t dst = smem_addr(smem + L::ring + (size_t)sl * 2 * HALF);
                         sm.meta[sl] = m;
                         const int inpage = slot & (c.P - 1);
                         if (c.P >= UNIT) {
@@ -314,54 +443,59 @@ __global__ void __launch_bounds__(THREADS, 2)
         // stay until every copy issued has landed: the CTA never ends with a copy in flight
         for (int i = max(0, count - SLOTS); i < count; i++)
             mbar_wait(smem_addr(sm.full + i % SLOTS), (uint32_t)((i / SLOTS) & 1), c.status);
+        for (int i = max(0, items - ITEMS); i < items; i++)
+            mbar_wait(smem_addr(sm.item_full + i % ITEMS), (uint32_t)((i / ITEMS) & 1), c.status);
         return;
     }
 
     // ---------------------------------------------------------------- consumers
     const int g8 = lane >> 2, t = lane & 3;
-    int count = 0, parity = 0;
+    const uint32_t frag = smem_addr(smem + L::frag) + lane * 16;
+    float *red = reinterpret_cast<float *>(smem + L::red);
+    int count = 0;
     bool failed = false;
-    for (int64_t at = lo; at < hi;) {
-        const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
-        // ---- the query row of this lane: row tile * 8 + g8 is token r / G, head r % G of the group
-        const int r = k.tile * ROWS + g8;
-        const bool real = r < k.s.n * p.G;
-        const int ti = k.s.t0 + (real ? r / p.G : 0), head = k.h * p.G + (real ? r % p.G : 0);
-        const int qpos = k.s.seen + ti - k.s.t0;
-        int seelo = 0, pre = 0;   // sees x >= first and (x < pre or seelo <= x <= qpos)
-        int firstp = 0;
-        float slope = 0.0f;
-        if (p.first) firstp = __ldg(p.first + ti);
-        if (p.prefix) pre = min(__ldg(p.prefix + ti), 1 << 30);
-        if (p.slopes) slope = __ldg(p.slopes + head) * LOG2E;
-        if (p.window > 0) seelo = (int)max((int64_t)0, (int64_t)qpos - p.window + 1);
-        seelo = max(seelo, firstp);
-        uint32_t qa[KS][4];
-        float f;   // what turns a raw product into z (base 2), or into z / cap
+    int64_t at = lo;
+    for (int items = 0; at < hi; items++) {
+        const int st = items % ITEMS;
+        const ItemRec &it = sm.item[st];
+        failed = failed || !mbar_wait(smem_addr(sm.item_full + st), (uint32_t)((items / ITEMS) & 1), c.status);
+        // ---- the query row of this lane, scaled by a power of two into [2^14, 2^15); the warps share
+        // the work of splitting it: fragment x goes to shared memory from warp x mod W
+        const bool real = !failed && g8 < it.rows;
+        float f = 0.0f;   // what turns a raw product into z (base 2), or into z / cap
         {
-            const float4 *qr = reinterpret_cast<const float4 *>(p.q + (int64_t)ti * p.ldq + (int64_t)head * D + RUN * t);
-            float4 v[KS];
+            const uint32_t qr = smem_addr(smem + L::q + (st * ROWS + g8) * D * 4) + RUN * 4 * t;
             float am = 0.0f;
 #pragma unroll
             for (int i = 0; i < KS; i++) {
-                v[i] = real ? __ldg(qr + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                am = fmaxf(am, absmax4(v[i]));
+                const uint4 v = real ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+                am = fmaxf(am, absmax4(make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                                   __uint_as_float(v.w))));
             }
             am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
             am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            // a power of two takes the row's largest magnitude into [2^14, 2^15)
             const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255u) - 126, -100), 126);
             const float up = __uint_as_float((uint32_t)(15 - ex + 127) << 23);
-#pragma unroll
-            for (int i = 0; i < KS; i++) {
-                split2(v[i].x * up, v[i].y * up, qa[i][0], qa[i][1]);
-                split2(v[i].z * up, v[i].w * up, qa[i][2], qa[i][3]);
+            for (int i = warp; i < KS; i += W) {
+                const uint4 v = real ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t h0, l0, h1, l1;
+                split2(__uint_as_float(v.x) * up, __uint_as_float(v.y) * up, h0, l0);
+                split2(__uint_as_float(v.z) * up, __uint_as_float(v.w) * up, h1, l1);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(frag + 512 * i), "r"(h0), "r"(l0), "r"(h1), "r"(l1)
+                             : "memory");
             }
             f = __uint_as_float((uint32_t)(ex - 15 + 127) << 23) * p.scale;
             f = p.cap > 0.0f ? f / p.cap : f * LOG2E;
         }
+        // a wait that gave up ends the work of all the warps here
+        if (consumer_any(failed)) return;
+        const int u0 = it.u0, u1 = it.u1, rows = it.rows;
+        const int qpos = real ? it.qpos[g8] : 0, firstp = real ? it.first[g8] : 0, pre = real ? it.prefix[g8] : 0;
+        const float slope = real ? it.slope[g8] : 0.0f;
+        // the row sees x >= firstp and (x < pre or seelo <= x <= qpos)
+        const int seelo = p.window > 0 ? (int)max((int64_t)firstp, (int64_t)qpos - p.window + 1) : firstp;
         const float cap2 = p.cap * LOG2E;
-        // a unit with all positions in [see_all_lo, see_all_hi] is seen whole by every row
+        // a unit with all positions in [all_lo, all_hi] is seen whole by every row
         int all_lo = real ? seelo : 0, all_hi = real ? qpos : 0x7fffffff;
 #pragma unroll
         for (int m = 4; m <= 16; m <<= 1) {
@@ -374,51 +508,74 @@ __global__ void __launch_bounds__(THREADS, 2)
         float mrow = -INFINITY, lrow = 0.0f;
         int vex = -100;   // the sums are in units of 2^(vex - 14)
 
-        // unit u of the item is unit count + u - u0 of this CTA; warp w takes every fourth
-        for (int u = u0 + ((warp - count) & (W - 1)); u < u1; u += W) {
+        // unit u of the item is unit count + u - u0 of this CTA; warp w takes every W-th
+        for (int u = u0 + (warp + W - count % W) % W; u < u1; u += W) {
             const int i = count + u - u0, sl = i % SLOTS;
             if (failed) break;   // a wait gave up: no further ones
             const bool got = mbar_wait(smem_addr(sm.full + sl), (uint32_t)((i / SLOTS) & 1), c.status);
             failed = !__all_sync(0xffffffffu, got);
             if (failed) break;
-            const uint32_t kb = smem_addr(ring + (size_t)sl * 2 * HALF), vb = kb + HALF;
+            const uint32_t kb = smem_addr(smem + L::ring) + (uint32_t)sl * 2 * HALF, vb = kb + HALF;
             const UnitMeta &m = sm.meta[sl];
             const int live = m.live;
             // ---- scores: columns 8j + n are the unit's tokens, k the positions in chunk order
             float s[4][2];
+            {
+                float acc[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                const int tok = 8 * j + g8;
+                for (int j = 0; j < 4; j++) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
 #pragma unroll
                 for (int hh = 0; hh < D / 64; hh++) {
-                    uint32_t a;
-                    if (D == 128) a = kb + tok * 128 + (((2 * t + hh) ^ (tok & 7)) << 4);
-                    else a = kb + (tok >> 1) * 128 + (((4 * (tok & 1) + t) ^ ((tok >> 1) & 7)) << 4);
-                    const uint4 w4 = sh_ld128(a);
-                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int tok = 8 * j + g8;
+                        uint32_t a;
+                        if (D == 128) a = kb + tok * 128 + (((2 * t + hh) ^ g8) << 4);
+                        else a = kb + (tok >> 1) * 128 + (((4 * (tok & 1) + t) ^ ((tok >> 1) & 7)) << 4);
+                        const uint4 w4 = sh_ld128(a);
+                        w[j][0] = w4.x;
+                        w[j][1] = w4.y;
+                        w[j][2] = w4.z;
+                        w[j][3] = w4.w;
+                    }
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
-                        uint32_t b0, b1;
-                        widen4<KIND>(w[x], b0, b1);
-                        mma_f16_16x8x16(acc, qa[4 * hh + x][0], qa[4 * hh + x][1], qa[4 * hh + x][2], qa[4 * hh + x][3], b0, b1);
+                        const uint4 q = sh_ld128(frag + 512 * (4 * hh + x));
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            uint32_t b0, b1;
+                            widen4<KIND>(w[j][x], b0, b1);
+                            mma_f16_16x8x16(acc[j], q.x, q.y, q.z, q.w, b0, b1);
+                        }
                     }
                 }
-                s[j][0] = acc[0] + acc[2];
-                s[j][1] = acc[1] + acc[3];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    s[j][0] = acc[j][0] + acc[j][2];
+                    s[j][1] = acc[j][1] + acc[j][3];
+                }
             }
             // ---- scale, cap, bias, mask
             const int base0 = m.base[0], base1 = m.base[1];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const float fk = f * m.ks[j >> 1];
-                const int x0 = (j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t;
+                s[j][0] *= fk;
+                s[j][1] *= fk;
+            }
+            if (p.cap > 0.0f) {
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    float z = s[j][e] * fk;
-                    if (p.cap > 0.0f) z = cap2 * tanh_f32(z);
-                    if (p.slopes) z -= slope * (float)abs(qpos - (x0 + e));
-                    s[j][e] = z;
+                for (int j = 0; j < 4; j++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) s[j][e] = cap2 * tanh_f32(s[j][e]);
+            }
+            if (p.slopes) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int d = qpos - ((j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t);
+                    s[j][0] -= slope * (float)abs(d);
+                    s[j][1] -= slope * (float)abs(d - 1);
                 }
             }
             const bool whole = live == UNIT && base0 >= all_lo && base1 >= all_lo && base0 + 15 <= all_hi &&
@@ -438,11 +595,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                              fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mnew = fmaxf(mrow, mx), msafe = mnew == -INFINITY ? 0.0f : mnew;
+            const float mnew = fmaxf(mrow, mx);
             const float vs0 = m.vs[0], vs1 = m.vs[1];
             const int ve = max(vex, min(max((int)((__float_as_uint(fmaxf(vs0, vs1)) >> 23) & 255u) - 126, -100), 126));
             if (__any_sync(0xffffffffu, mnew > mrow) || ve != vex) {
-                const float a = ex2(mrow - msafe);   // 0 while nothing was seen
+                const float a = mnew > mrow ? ex2(mrow - mnew) : 1.0f;   // 0 while nothing was seen
                 lrow *= a;
                 // 2^(vex - ve): exact, 0 when it would underflow
                 const float av = a * (vex - ve < -126 ? 0.0f : __uint_as_float((uint32_t)(vex - ve + 127) << 23));
@@ -456,6 +613,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 mrow = mnew;
                 vex = ve;
             }
+            const float msafe = mrow == -INFINITY ? 0.0f : mrow;
             float gsum[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -471,8 +629,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                     gsum[i2] += __shfl_xor_sync(0xffffffffu, gsum[i2], 2);
                 }
                 if (real && t == 0) {
-                    const int slot = (u < k.u.pre ? u : k.u.start + u - k.u.pre) * UNIT;
-                    float *gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (slot >> p.lgGroup);
+                    const int slot = (u < it.pre ? u : it.start + u - it.pre) * UNIT;
+                    float *gl = p.glse + ((int64_t)it.ti[g8] * p.Hq + it.head[g8]) * p.NG + (slot >> p.lgGroup);
                     if (p.lgGroup == 4) {
                         gl[0] = __log2f(gsum[0]) + msafe;
                         if (live > 16) gl[1] = __log2f(gsum[1]) + msafe;
@@ -492,11 +650,11 @@ __global__ void __launch_bounds__(THREADS, 2)
             }
             // ---- values: k the 16 tokens of a step, column n of tile x the x-th position of chunk n
 #pragma unroll
-            for (int st = 0; st < 2; st++) {
+            for (int step = 0; step < 2; step++) {
                 uint32_t w[4][D / 32];   // this lane's chunk of tokens r0, r0 + 1, r0 + 8, r0 + 9
 #pragma unroll
                 for (int x = 0; x < 4; x++) {
-                    const int tok = 16 * st + 2 * t + (x & 1) + 8 * (x >> 1);
+                    const int tok = 16 * step + 2 * t + (x & 1) + 8 * (x >> 1);
                     if constexpr (D == 128) {
                         const uint4 q4 = sh_ld128(vb + tok * 128 + ((g8 ^ (tok & 7)) << 4));
                         w[x][0] = q4.x;
@@ -510,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                         w[x][1] = q2.y;
                     }
                     // slots past the last token may hold any bytes, NaN codes among them
-                    if (KIND == GQ_KV_E4M3 && !whole && (tok >= live || ((m.lost >> st) & 1)))
+                    if (KIND == GQ_KV_E4M3 && !whole && (tok >= live || ((m.lost >> step) & 1)))
 #pragma unroll
                         for (int y = 0; y < D / 32; y++) w[x][y] = 0u;
                 }
@@ -521,70 +679,61 @@ __global__ void __launch_bounds__(THREADS, 2)
                     widen_pairs<KIND>(w[2][y], w[3][y], b1);
 #pragma unroll
                     for (int x = 0; x < 4; x++)
-                        mma_f16_16x8x16(o[4 * y + x], pa[2 * st][0], pa[2 * st][1], pa[2 * st + 1][0], pa[2 * st + 1][1],
+                        mma_f16_16x8x16(o[4 * y + x], pa[2 * step][0], pa[2 * step][1], pa[2 * step + 1][0], pa[2 * step + 1][1],
                                         b0[x], b1[x]);
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(sm.empty + sl));
+            __syncwarp();
         }
         count += u1 - u0;
 
-        // ---- join the four warps
+        // ---- join the warps
         lrow += __shfl_xor_sync(0xffffffffu, lrow, 1);
         lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
         if (t == 0) {
-            sm.ml[parity][warp][g8][0] = mrow;
-            sm.ml[parity][warp][g8][1] = lrow;
+            sm.ml[warp][g8][0] = mrow;
+            sm.ml[warp][g8][1] = lrow;
         }
-        consumer_sync();
         {
-            float mt = sm.ml[parity][0][g8][0];
-#pragma unroll
-            for (int w = 1; w < W; w++) mt = fmaxf(mt, sm.ml[parity][w][g8][0]);
-            const float a = mrow == -INFINITY ? 0.0f : ex2(mrow - mt) * __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
-            // lane (g8, t): n-tile x, column 2t (+1) is position (2t (+1)) * RUN / 2 + x
-            float4 *dst = reinterpret_cast<float4 *>(red + ((size_t)warp * ROWS + g8) * D + RUN * t);
+            // in units of 2^0, relative to the warp's own maximum.  Lane (g8, t): n-tile x, column
+            // 2t (+1) is position (2t (+1)) * RUN / 2 + x; 16-byte chunk y of row r lies at y ^ r
+            const float a = __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
+            const uint32_t dst = smem_addr(red) + (uint32_t)((warp * ROWS + g8) * D * 4);
 #pragma unroll
             for (int e = 0; e < 2; e++)
 #pragma unroll
                 for (int x = 0; x < 2 * KS; x += 4)
-                    dst[e * (KS / 2) + x / 4] = make_float4((o[x][e] + o[x][e + 2]) * a, (o[x + 1][e] + o[x + 1][e + 2]) * a,
-                                                            (o[x + 2][e] + o[x + 2][e + 2]) * a,
-                                                            (o[x + 3][e] + o[x + 3][e + 2]) * a);
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((RUN / 4 * t + e * (KS / 2) + x / 4) ^ g8) << 4)),
+                                 "f"((o[x][e] + o[x][e + 2]) * a), "f"((o[x + 1][e] + o[x + 1][e + 2]) * a),
+                                 "f"((o[x + 2][e] + o[x + 2][e + 2]) * a), "f"((o[x + 3][e] + o[x + 3][e + 2]) * a)
+                                 : "memory");
         }
         consumer_sync();
-        const bool cut0 = u0 > 0, cut1 = u1 < k.u.units;   // the item began before, goes on after this CTA
-        const int rows = min(ROWS, k.s.n * p.G - k.tile * ROWS);
-        auto row_ptr = [&](int rr) {   // output row of tile row rr
-            const int x = k.tile * ROWS + rr;
-            return p.out + (int64_t)(k.s.t0 + x / p.G) * p.ldo + (int64_t)(k.h * p.G + x % p.G) * D;
-        };
-        auto row_index = [&](int rr) {
-            const int x = k.tile * ROWS + rr;
-            return (int64_t)(k.s.t0 + x / p.G) * p.Hq + k.h * p.G + x % p.G;
-        };
+        const bool cut0 = u0 > 0, cut1 = u1 < it.units;   // the item began before, goes on after this CTA
         const int piece_slot = blockIdx.x * 2 + (cut0 ? 0 : 1);
         for (int x = tid; x < rows * (D / 4); x += CONSUMERS) {
             const int rr = x / (D / 4), d4 = x % (D / 4);
             float mt = -INFINITY, l = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; w++) mt = fmaxf(mt, sm.ml[parity][w][rr][0]);
+            for (int w = 0; w < W; w++) mt = fmaxf(mt, sm.ml[w][rr][0]);
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < W; w++) {
-                const float mw = sm.ml[parity][w][rr][0];
-                if (mw != -INFINITY) l += sm.ml[parity][w][rr][1] * ex2(mw - mt);
-                const float4 v = reinterpret_cast<const float4 *>(red + ((size_t)w * ROWS + rr) * D)[d4];
-                a.x += v.x;
-                a.y += v.y;
-                a.z += v.z;
-                a.w += v.w;
+                const float mw = sm.ml[w][rr][0], e = mw == -INFINITY ? 0.0f : ex2(mw - mt);
+                l += sm.ml[w][rr][1] * e;
+                const float4 v = *reinterpret_cast<const float4 *>(red + (w * ROWS + rr) * D + 4 * (d4 ^ rr));
+                a.x = fmaf(v.x, e, a.x);
+                a.y = fmaf(v.y, e, a.y);
+                a.z = fmaf(v.z, e, a.z);
+                a.w = fmaf(v.w, e, a.w);
             }
             if (!cut0 && !cut1) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                reinterpret_cast<float4 *>(row_ptr(rr))[d4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                if (p.lse && d4 == 0) p.lse[row_index(rr)] = l > 0.0f ? mt + log2f(l) : INFINITY;
+                reinterpret_cast<float4 *>(p.out + (int64_t)it.ti[rr] * p.ldo + (int64_t)it.head[rr] * D)[d4] =
+                    make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+                if (p.lse && d4 == 0) p.lse[(int64_t)it.ti[rr] * p.Hq + it.head[rr]] = l > 0.0f ? mt + log2f(l) : INFINITY;
             } else {
                 reinterpret_cast<float4 *>(p.parts + ((int64_t)piece_slot * ROWS + rr) * D)[d4] = a;
                 if (d4 == 0) {
@@ -595,7 +744,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         if (cut0 || cut1) {
             // the pieces of this item: CTAs c0 .. c1; the one that finishes last joins them in order
-            const int c0 = (int)(item0 / piece), c1 = (int)((item0 + k.u.units - 1) / piece);
+            const int64_t item0 = it.item0;
+            const int c0 = (int)(item0 / piece), c1 = (int)((item0 + it.units - 1) / piece);
             __threadfence();
             consumer_sync();
             if (tid == 0) {
@@ -606,39 +756,13 @@ __global__ void __launch_bounds__(THREADS, 2)
             consumer_sync();
             if (sm.last) {
                 __threadfence();
-                for (int x = tid; x < rows * (D / 4); x += CONSUMERS) {
-                    const int rr = x / (D / 4), d4 = x % (D / 4);
-                    // the item begins in CTA c0 (its slot 1); it is the first item of the others (slot 0)
-                    float mt = -INFINITY;
-                    for (int q = c0; q <= c1; q++)
-                        mt = fmaxf(mt, __ldcg(p.part_ml + ((int64_t)(q * 2 + (q == c0)) * ROWS + rr) * 2));
-                    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    float l = 0.0f;
-                    if (mt != -INFINITY)
-#pragma unroll 4
-                        for (int q = c0; q <= c1; q++) {
-                            const int64_t pr = (int64_t)(q * 2 + (q == c0)) * ROWS + rr;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + pr * 2));
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.parts + pr * D) + d4);
-                            const float e = ex2(ml.x - mt);
-                            l += e * ml.y;
-                            a.x += e * v.x;
-                            a.y += e * v.y;
-                            a.z += e * v.z;
-                            a.w += e * v.w;
-                        }
-                    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                    reinterpret_cast<float4 *>(row_ptr(rr))[d4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                    if (p.lse && d4 == 0) p.lse[row_index(rr)] = l > 0.0f ? mt + log2f(l) : INFINITY;
-                }
+                join_pieces<D>(p, it, c0, c1, warp, lane);
             }
         }
-        parity ^= 1;
-        at = item0 + u1;
-        if (u1 == k.u.units) {
-            item0 += k.u.units;
-            if (at < hi) next_item(p, k);
-        }
+        at = it.item0 + u1;
+        consumer_sync();   // the item's data, the warps' sums and the fragments are free
+        if (lane == 0) mbar_arrive(smem_addr(sm.item_empty + st));
+        __syncwarp();
     }
 }
 
@@ -703,7 +827,7 @@ template <int KIND, int D>
 gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
                       cudaStream_t s) {
     auto kernel = attn_pages_rows_kernel<KIND, D>;
-    constexpr size_t smem = rows_smem_bytes<D>();
+    constexpr size_t smem = RowsLayout<D>::total + 1024;
     static std::atomic<bool> smem_set[64];
     int dev = 0;
     KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));

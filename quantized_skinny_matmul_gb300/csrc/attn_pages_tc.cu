@@ -538,6 +538,10 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
         if (now) nk++;
         prev = now;
         if (flags & F_LAST) {
+            // the queries of a tile that saw nothing: every phase of a barrier is waited for
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+                if ((fresh_q >> t) & 1) wait.warp(Q_FULL + t, nitem - 1);
             if (prev) {
                 wait.warp(V_FULL, nv++);
 #pragma unroll
