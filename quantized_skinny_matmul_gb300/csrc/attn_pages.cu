@@ -8,12 +8,14 @@
 // the values, the output.
 //
 // Both products run as m16n8k16 fp16 MMAs with f32 accumulation at f32 accuracy: the codes
-// widen to fp16 exactly, and a query row (scaled by a power of two) or a row of weights is
-// carried as two fp16 terms, hi + lo.  The 16 MMA rows are 8 query rows' hi terms and the
-// same rows' lo terms, so the accumulator fragment of the scores (a lane holds hi and lo of
-// the same row and tokens) turns into the A fragment of the weights in registers.  The order
-// in which the MMAs take positions within a row (D) and tokens within a unit is chosen so
-// that every lane reads its 16-byte chunks of codes as they lie in shared memory.
+// widen to fp16 exactly and are the 16-row operand; a query row (scaled by a power of two) or a
+// row of weights is carried as two fp16 terms, hi + lo, in two of the 8 columns.  So an MMA
+// serves 4 query rows; items have up to 4 (one column tile) or up to 8 (two), and with one, half
+// the accumulators of a layout with the query as the 16-row operand.  A lane's scores are those
+// of its row (lane mod 4) for tokens g and g + 8 of 16 (g = lane / 4); the values' product takes
+// tokens in the order (t, t + 8), (t + 4, t + 12) .., so that a weight pair moves to its place
+// with one shuffle a term.  The order in which the MMAs take positions within a row (D) is
+// chosen so that every lane reads its 16-byte chunks of codes as they lie in shared memory.
 //
 // Work is divided evenly, not by sequence: the (sequence, head, row tile) items' units are
 // laid out in a line, every CTA takes an equal piece of it, and items cut at a piece's end
@@ -44,18 +46,18 @@ namespace {
     } while (0)
 
 constexpr int UNIT = 32;                    // tokens per unit
-// Consumer warps: two CTAs of 7 + 1 warps at 128 registers fill an SM.  (With 4 + 1 at 168, the
-// query's fragments in registers, the warps' own latency bound the kernel: 128 sequences of up to
-// 2,048 tokens on 32 heads took 324 us.)
-constexpr int W = 7;
-constexpr int CONSUMERS = W * 32, THREADS = CONSUMERS + 32;
-constexpr int ROWS = 8;                     // query rows of an item
+// Consumer warps, and query rows of an item, for 1 or 2 column tiles: two CTAs of W + 1 warps fill
+// an SM's registers.
+__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 9 : 7; }
+__host__ __device__ constexpr int rows_of(int NN) { return 4 * NN; }
+constexpr int ROWS_MOST = 8;
 constexpr int ITEMS = 2;                    // items whose data is kept
 
-// Slots of the ring (56 KB).  A multiple of W: the warp that takes a slot's unit also takes the next
-// one in that slot.  Otherwise a warp could wait for a slot's next phase before the present one is
-// over (copies land in any order), and a parity wait two phases ahead passes at once.
-__host__ __device__ constexpr int slots_of(int D) { return D == 128 ? W : 2 * W; }
+// Slots of the ring, of 8 KB (D = 128) or 4.  A multiple of W: the warp that takes a slot's unit also
+// takes the next one in that slot.  Otherwise a warp could wait for a slot's next phase before the
+// present one is over (copies land in any order), and a parity wait two phases ahead passes at once.
+__host__ __device__ constexpr int slots_of(int D, int NN) { return warps_of(NN) * (D == 128 ? 1 : 2); }
+constexpr int MAX_SLOTS = 18;
 
 struct UnitMeta {               // beside each slot: scales and first positions of the two halves
     float ks[2], vs[2];
@@ -69,42 +71,37 @@ struct ItemRec {
     int64_t item0;              // line position of the item's first unit
     int u0, u1, units;          // units of the stretch, units of the item
     int pre, start;             // its span
-    int rows;                   // query rows (0 .. ROWS)
-    int ti[ROWS], head[ROWS], qpos[ROWS];   // of each row: token, query head, position
-    int first[ROWS], prefix[ROWS];
-    float slope[ROWS];          // times log2 e
+    int rows;                   // query rows
+    int ti[ROWS_MOST], head[ROWS_MOST], qpos[ROWS_MOST];   // of each row: token, query head, position
+    int first[ROWS_MOST], prefix[ROWS_MOST];
+    float slope[ROWS_MOST];          // times log2 e
 };
 
 struct RowsSmem {
-    uint64_t full[2 * W], empty[2 * W], item_full[ITEMS], item_empty[ITEMS];
-    UnitMeta meta[2 * W];
+    uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], item_full[ITEMS], item_empty[ITEMS];
+    UnitMeta meta[MAX_SLOTS];
     ItemRec item[ITEMS];
-    float ml[W][ROWS][2];       // maximum and denominator of each warp
+    float ml[warps_of(1)][ROWS_MOST][2];    // maximum and denominator of each warp
     int64_t start, total;       // line position of the sequence that the CTA starts in
-    int start_b, last;
-    int64_t warp_sum[THREADS / 32];
+    int start_b, last, failed;
+    int64_t warp_sum[warps_of(1) + 1];
 };
 
-template <int D>
+template <int D, int NN>
 struct RowsLayout {
+    static constexpr int W = warps_of(NN), ROWS = rows_of(NN);
     static constexpr int ring = 0;                                     // units: keys, values
-    static constexpr int q = ring + slots_of(D) * UNIT * D * 2;        // [ITEMS][ROWS][D] f32
+    static constexpr int q = ring + slots_of(D, NN) * UNIT * D * 2;    // [ITEMS][ROWS][D] f32
     static constexpr int frag = q + ITEMS * ROWS * D * 4;              // the query's MMA fragments
-    static constexpr int red = frag + D * 32;                          // [W][ROWS][D] f32
+    static constexpr int red = frag + D * 16 * NN;                     // [W][ROWS][D] f32
     static constexpr int ctl = red + W * ROWS * D * 4;
     static constexpr int total = ctl + (int)sizeof(RowsSmem);
     static_assert(2 * (total + 2048) <= 228 * 1024, "two CTAs per SM");
 };
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory"); }
-// The same, with the answer whether any thread said yes.
-__device__ __forceinline__ bool consumer_any(bool yes) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r)
-                 : "r"((uint32_t)yes), "n"(CONSUMERS)
-                 : "memory");
-    return r != 0;
+template <int N>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
 // Byte j of x and byte j of y as one exact fp16 pair, j = 0 .. 3.
@@ -140,7 +137,7 @@ __device__ __forceinline__ Span span_of(const AttnParams8 &p, const SeqStep &s) 
     Span r;
     const int n = s.held + s.n, end = (n + UNIT - 1) >> 5;
     int lo = 0, pre = 0, first = 0;
-    if (s.n <= ROWS) {   // few tokens: look at each one's own range
+    if (s.n <= ROWS_MOST) {   // few tokens: look at each one's own range
         if (p.first) {
             first = 0x7fffffff;
             for (int i = 0; i < s.n; i++) first = min(first, p.first[s.t0 + i]);
@@ -160,6 +157,7 @@ __device__ __forceinline__ Span span_of(const AttnParams8 &p, const SeqStep &s) 
 
 // Where a piece of work is: the item (sequence b, head h, row tile) and its sequence's data.
 struct Cursor {
+    int rows;                   // of an item
     int b, h, tile, tiles;
     SeqStep s;
     Span u;
@@ -173,7 +171,7 @@ __device__ __forceinline__ void load_seq(const AttnParams8 &p, Cursor &k) {
     } else if (k.s.n > 0) {
         k.u = span_of(p, k.s);
     }
-    k.tiles = k.s.n * p.G > p.rows_over ? 0 : (k.s.n * p.G + ROWS - 1) / ROWS;
+    k.tiles = k.s.n * p.G > p.rows_over ? 0 : (k.s.n * p.G + k.rows - 1) / k.rows;
 }
 
 __device__ __forceinline__ void next_item(const AttnParams8 &p, Cursor &k) {
@@ -190,7 +188,7 @@ __device__ __forceinline__ void next_item(const AttnParams8 &p, Cursor &k) {
 // Joins the pieces of an item that several CTAs worked on, in their order, into its output rows:
 // a warp per row, a lane per D / 32 columns.  The lanes first take 32 pieces' maxima and
 // denominators each; then every piece's weight goes from its lane to all.
-template <int D>
+template <int D, int W, int ROWS>
 __device__ __forceinline__ void join_pieces(const AttnParams8 &p, const ItemRec &it, int c0, int c1, int warp, int lane) {
     constexpr int V = D / 32;
     const int n = c1 - c0 + 1;
@@ -238,14 +236,16 @@ __device__ __forceinline__ void join_pieces(const AttnParams8 &p, const ItemRec 
     }
 }
 
-template <int KIND, int D>
-__global__ void __launch_bounds__(THREADS, 2)
+template <int KIND, int D, int NN>
+__global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
     attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const AttnParams8 p) {
-    using L = RowsLayout<D>;
-    constexpr int SLOTS = slots_of(D), HALF = UNIT * D;      // bytes of a unit's keys
+    using L = RowsLayout<D, NN>;
+    constexpr int W = L::W, ROWS = L::ROWS, CONSUMERS = W * 32, THREADS = CONSUMERS + 32;
+    constexpr int SLOTS = slots_of(D, NN), HALF = UNIT * D;  // bytes of a unit's keys
     constexpr int KS = D / 16;                               // MMA steps of a score
-    constexpr int RUN = D / 4;                               // positions per lane
+    constexpr int RUN = D / 4;                               // positions per lane of a score
+    constexpr int MT = D / 16;                               // row tiles of the output
     static_assert(SLOTS % W == 0, "a slot belongs to one warp");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         int64_t mine = 0;
         for (int b = b0; b < b1; b++) {
             Cursor k;
+            k.rows = ROWS;
             k.b = b;
             load_seq(p, k);
             if (k.s.bad) atomicOr(c.status, STATUS_RANGE);
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             if (lane >= d) inc += t;
         }
         if (lane == 31) sm.warp_sum[warp] = inc;
-        if (tid == 0) sm.start_b = -1;
+        if (tid == 0) sm.failed = 0;
         __syncthreads();
         int64_t before = inc - mine, total = 0;
         for (int w = 0; w < THREADS / 32; w++) {
@@ -296,6 +297,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (lo >= before && lo < before + mine) {
             for (int b = b0; b < b1; b++) {
                 Cursor k;
+                k.rows = ROWS;
                 k.b = b;
                 load_seq(p, k);
                 const int64_t u = k.tiles ? (int64_t)k.tiles * c.Hkv * k.u.units : 0;
@@ -317,6 +319,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // ---------------------------------------------------------------- producer
     if (warp == W) {
         Cursor k;
+        k.rows = ROWS;
         k.b = sm.start_b;
         load_seq(p, k);
         int64_t item0;   // line position of the item's first unit
@@ -450,25 +453,36 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     // ---------------------------------------------------------------- consumers
     const int g8 = lane >> 2, t = lane & 3;
-    const uint32_t frag = smem_addr(smem + L::frag) + lane * 16;
+    const uint32_t frag = smem_addr(smem + L::frag) + lane * 8;
     float *red = reinterpret_cast<float *>(smem + L::red);
     int count = 0;
     bool failed = false;
     int64_t at = lo;
+    // where this lane's chunks of key rows g8 and of value rows t lie in 16 tokens (D = 64: two rows a
+    // 128-byte line)
+    uint32_t koff[D / 64], voff;
+#pragma unroll
+    for (int hh = 0; hh < D / 64; hh++)
+        koff[hh] = D == 128 ? g8 * 128 + (((2 * t + hh) ^ g8) << 4) : (g8 >> 1) * 128 + (((4 * (g8 & 1) + t) ^ (g8 >> 1)) << 4);
+    voff = D == 128 ? t * 128 + ((g8 ^ t) << 4) : (t >> 1) * 128 + (((4 * (t & 1) + (g8 >> 1)) ^ (t >> 1)) << 4) + 8 * (g8 & 1);
     for (int items = 0; at < hi; items++) {
         const int st = items % ITEMS;
         const ItemRec &it = sm.item[st];
         failed = failed || !mbar_wait(smem_addr(sm.item_full + st), (uint32_t)((items / ITEMS) & 1), c.status);
-        // ---- the query row of this lane, scaled by a power of two into [2^14, 2^15); the warps share
-        // the work of splitting it: fragment x goes to shared memory from warp x mod W
-        const bool real = !failed && g8 < it.rows;
-        float f = 0.0f;   // what turns a raw product into z (base 2), or into z / cap
-        {
-            const uint32_t qr = smem_addr(smem + L::q + (st * ROWS + g8) * D * 4) + RUN * 4 * t;
+        // ---- the query rows, scaled by powers of two into [2^14, 2^15), as MMA columns (row r: its hi
+        // term column 2r, its lo term 2r + 1).  Lane (g8, t) makes column g8 of each tile, positions
+        // RUN t ..; the warps share the work.
+        const int nrows = failed ? 0 : it.rows;
+        float f[NN];   // of row 4 nn + t: what turns a raw product into z (base 2), or into z / cap
+#pragma unroll
+        for (int nn = 0; nn < NN; nn++) {
+            const int r = 4 * nn + (g8 >> 1);
+            const bool there = r < nrows;
+            const uint32_t qr = smem_addr(smem + L::q + (st * ROWS + r) * D * 4) + RUN * 4 * t;
             float am = 0.0f;
 #pragma unroll
             for (int i = 0; i < KS; i++) {
-                const uint4 v = real ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = there ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
                 am = fmaxf(am, absmax4(make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
                                                    __uint_as_float(v.w))));
             }
@@ -477,35 +491,62 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int ex = min(max((int)((__float_as_uint(am) >> 23) & 255u) - 126, -100), 126);
             const float up = __uint_as_float((uint32_t)(15 - ex + 127) << 23);
             for (int i = warp; i < KS; i += W) {
-                const uint4 v = real ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = there ? sh_ld128(qr + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
                 uint32_t h0, l0, h1, l1;
                 split2(__uint_as_float(v.x) * up, __uint_as_float(v.y) * up, h0, l0);
                 split2(__uint_as_float(v.z) * up, __uint_as_float(v.w) * up, h1, l1);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(frag + 512 * i), "r"(h0), "r"(l0), "r"(h1), "r"(l1)
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(frag + 256 * (i * NN + nn)), "r"(g8 & 1 ? l0 : h0),
+                             "r"(g8 & 1 ? l1 : h1)
                              : "memory");
             }
-            f = __uint_as_float((uint32_t)(ex - 15 + 127) << 23) * p.scale;
-            f = p.cap > 0.0f ? f / p.cap : f * LOG2E;
+            // the factor of row 4 nn + t comes from a lane that made its column
+            const float fr = __uint_as_float((uint32_t)(ex - 15 + 127) << 23) * p.scale;
+            f[nn] = __shfl_sync(0xffffffffu, p.cap > 0.0f ? fr / p.cap : fr * LOG2E, 8 * t);
         }
         // a wait that gave up ends the work of all the warps here
-        if (consumer_any(failed)) return;
-        const int u0 = it.u0, u1 = it.u1, rows = it.rows;
-        const int qpos = real ? it.qpos[g8] : 0, firstp = real ? it.first[g8] : 0, pre = real ? it.prefix[g8] : 0;
-        const float slope = real ? it.slope[g8] : 0.0f;
-        // the row sees x >= firstp and (x < pre or seelo <= x <= qpos)
-        const int seelo = p.window > 0 ? (int)max((int64_t)firstp, (int64_t)qpos - p.window + 1) : firstp;
-        const float cap2 = p.cap * LOG2E;
-        // a unit with all positions in [all_lo, all_hi] is seen whole by every row
-        int all_lo = real ? seelo : 0, all_hi = real ? qpos : 0x7fffffff;
+        if (failed) sm.failed = 1;
+        consumer_sync<CONSUMERS>();
+        if (*(volatile int *)&sm.failed) return;
+        const int u0 = it.u0, u1 = it.u1;
+        // rows 4 nn + t of this lane: what they see, x >= firstp and (x < pre or seelo <= x <= qpos)
+        int qpos[NN], firstp[NN], pre[NN], seelo[NN], all_lo = 0, all_hi = 0x7fffffff;
+        float slope[NN];
 #pragma unroll
-        for (int m = 4; m <= 16; m <<= 1) {
+        for (int nn = 0; nn < NN; nn++) {
+            const int r = 4 * nn + t;
+            const bool real = r < nrows;
+            qpos[nn] = real ? it.qpos[r] : 0;
+            firstp[nn] = real ? it.first[r] : 0;
+            pre[nn] = real ? it.prefix[r] : 0;
+            slope[nn] = real ? it.slope[r] : 0.0f;
+            seelo[nn] = p.window > 0 ? (int)max((int64_t)firstp[nn], (int64_t)qpos[nn] - p.window + 1) : firstp[nn];
+            // a unit with all positions in [all_lo, all_hi] is seen whole by every row
+            if (real) {
+                all_lo = max(all_lo, seelo[nn]);
+                all_hi = min(all_hi, qpos[nn]);
+            }
+        }
+#pragma unroll
+        for (int m = 1; m <= 2; m <<= 1) {
             all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, m));
             all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, m));
         }
-        float o[2 * KS][4];
+        const float cap2 = p.cap * LOG2E;
+        uint2 qb[NN == 1 ? KS : 1];   // the query's fragments: in registers where there is room
+        if (NN == 1)
 #pragma unroll
-        for (int i = 0; i < 2 * KS; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float mrow = -INFINITY, lrow = 0.0f;
+            for (int i = 0; i < KS; i++) qb[NN == 1 ? i : 0] = sh_ld64(frag + 256 * i);
+        float o[MT][NN][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int nn = 0; nn < NN; nn++) o[m][nn][0] = o[m][nn][1] = o[m][nn][2] = o[m][nn][3] = 0.0f;
+        float mrow[NN], lrow[NN];
+#pragma unroll
+        for (int nn = 0; nn < NN; nn++) {
+            mrow[nn] = -INFINITY;
+            lrow[nn] = 0.0f;
+        }
         int vex = -100;   // the sums are in units of 2^(vex - 14)
 
         // unit u of the item is unit count + u - u0 of this CTA; warp w takes every W-th
@@ -518,169 +559,180 @@ __global__ void __launch_bounds__(THREADS, 2)
             const uint32_t kb = smem_addr(smem + L::ring) + (uint32_t)sl * 2 * HALF, vb = kb + HALF;
             const UnitMeta &m = sm.meta[sl];
             const int live = m.live;
-            // ---- scores: columns 8j + n are the unit's tokens, k the positions in chunk order
-            float s[4][2];
-            {
-                float acc[4][4];
+            // ---- scores of tokens 16 mt + g8 and + 8, rows 4 nn + t
+            float s[2][NN][2];
 #pragma unroll
-                for (int j = 0; j < 4; j++) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+            for (int mt = 0; mt < 2; mt++) {
+                float acc[NN][4];
+#pragma unroll
+                for (int nn = 0; nn < NN; nn++) acc[nn][0] = acc[nn][1] = acc[nn][2] = acc[nn][3] = 0.0f;
 #pragma unroll
                 for (int hh = 0; hh < D / 64; hh++) {
-                    uint32_t w[4][4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int tok = 8 * j + g8;
-                        uint32_t a;
-                        if (D == 128) a = kb + tok * 128 + (((2 * t + hh) ^ g8) << 4);
-                        else a = kb + (tok >> 1) * 128 + (((4 * (tok & 1) + t) ^ ((tok >> 1) & 7)) << 4);
-                        const uint4 w4 = sh_ld128(a);
-                        w[j][0] = w4.x;
-                        w[j][1] = w4.y;
-                        w[j][2] = w4.z;
-                        w[j][3] = w4.w;
-                    }
+                    const uint4 wa = sh_ld128(kb + koff[hh] + mt * 16 * D);
+                    // (D = 64: eight rows on, the line's number changes by 4 and with it bit 6 of the chunk)
+                    const uint4 wb = sh_ld128(kb + (D == 128 ? koff[hh] : koff[hh] ^ 64u) + mt * 16 * D + 8 * D);
+                    const uint32_t av[4] = {wa.x, wa.y, wa.z, wa.w}, bv[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
-                        const uint4 q = sh_ld128(frag + 512 * (4 * hh + x));
+                        uint32_t a0, a1, a2, a3;
+                        widen4<KIND>(av[x], a0, a2);
+                        widen4<KIND>(bv[x], a1, a3);
 #pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            uint32_t b0, b1;
-                            widen4<KIND>(w[j][x], b0, b1);
-                            mma_f16_16x8x16(acc[j], q.x, q.y, q.z, q.w, b0, b1);
+                        for (int nn = 0; nn < NN; nn++) {
+                            const uint2 q = NN == 1 ? qb[NN == 1 ? 4 * hh + x : 0] : sh_ld64(frag + 256 * ((4 * hh + x) * NN + nn));
+                            mma_f16_16x8x16(acc[nn], a0, a1, a2, a3, q.x, q.y);
                         }
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    s[j][0] = acc[j][0] + acc[j][2];
-                    s[j][1] = acc[j][1] + acc[j][3];
+                for (int nn = 0; nn < NN; nn++) {
+                    const float fk = f[nn] * m.ks[mt];
+                    s[mt][nn][0] = (acc[nn][0] + acc[nn][1]) * fk;
+                    s[mt][nn][1] = (acc[nn][2] + acc[nn][3]) * fk;
                 }
             }
-            // ---- scale, cap, bias, mask
-            const int base0 = m.base[0], base1 = m.base[1];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float fk = f * m.ks[j >> 1];
-                s[j][0] *= fk;
-                s[j][1] *= fk;
-            }
+            // ---- cap, bias, mask
             if (p.cap > 0.0f) {
 #pragma unroll
-                for (int j = 0; j < 4; j++)
+                for (int mt = 0; mt < 2; mt++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) s[j][e] = cap2 * tanh_f32(s[j][e]);
+                    for (int nn = 0; nn < NN; nn++) {
+                        s[mt][nn][0] = cap2 * tanh_f32(s[mt][nn][0]);
+                        s[mt][nn][1] = cap2 * tanh_f32(s[mt][nn][1]);
+                    }
             }
             if (p.slopes) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int d = qpos - ((j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t);
-                    s[j][0] -= slope * (float)abs(d);
-                    s[j][1] -= slope * (float)abs(d - 1);
-                }
+                for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                    for (int nn = 0; nn < NN; nn++) {
+                        const int d = qpos[nn] - (m.base[mt] + g8);
+                        s[mt][nn][0] -= slope[nn] * (float)abs(d);
+                        s[mt][nn][1] -= slope[nn] * (float)abs(d - 8);
+                    }
             }
-            const bool whole = live == UNIT && base0 >= all_lo && base1 >= all_lo && base0 + 15 <= all_hi &&
-                               base1 + 15 <= all_hi;   // warp-uniform
+            const bool whole = live == UNIT && m.base[0] >= all_lo && m.base[1] >= all_lo && m.base[0] + 15 <= all_hi &&
+                               m.base[1] + 15 <= all_hi;   // warp-uniform
             if (!whole) {
 #pragma unroll
-                for (int j = 0; j < 4; j++)
+                for (int mt = 0; mt < 2; mt++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const int x = (j < 2 ? base0 + 8 * j : base1 + 8 * (j - 2)) + 2 * t + e;
-                        const bool see = 8 * j + 2 * t + e < live && x >= firstp && (x < pre || (x >= seelo && x <= qpos));
-                        s[j][e] = see ? s[j][e] : -INFINITY;
-                    }
+                    for (int nn = 0; nn < NN; nn++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int x = m.base[mt] + g8 + 8 * e;
+                            const bool see = 16 * mt + g8 + 8 * e < live && x >= firstp[nn] &&
+                                             (x < pre[nn] || (x >= seelo[nn] && x <= qpos[nn]));
+                            s[mt][nn][e] = see ? s[mt][nn][e] : -INFINITY;
+                        }
             }
-            // ---- the running maximum
-            float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])),
-                             fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mnew = fmaxf(mrow, mx);
+            // ---- the running maxima
             const float vs0 = m.vs[0], vs1 = m.vs[1];
             const int ve = max(vex, min(max((int)((__float_as_uint(fmaxf(vs0, vs1)) >> 23) & 255u) - 126, -100), 126));
-            if (__any_sync(0xffffffffu, mnew > mrow) || ve != vex) {
-                const float a = mnew > mrow ? ex2(mrow - mnew) : 1.0f;   // 0 while nothing was seen
-                lrow *= a;
-                // 2^(vex - ve): exact, 0 when it would underflow
-                const float av = a * (vex - ve < -126 ? 0.0f : __uint_as_float((uint32_t)(vex - ve + 127) << 23));
+            float mnew[NN];
+            bool grow = ve != vex;
 #pragma unroll
-                for (int n = 0; n < 2 * KS; n++) {
-                    o[n][0] *= av;
-                    o[n][1] *= av;
-                    o[n][2] *= av;
-                    o[n][3] *= av;
+            for (int nn = 0; nn < NN; nn++) {
+                float mx = fmaxf(fmaxf(s[0][nn][0], s[0][nn][1]), fmaxf(s[1][nn][0], s[1][nn][1]));
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                mnew[nn] = fmaxf(mrow[nn], mx);
+                grow = grow || mnew[nn] > mrow[nn];
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+                // 2^(vex - ve): exact, 0 when it would underflow
+                const float ov = vex - ve < -126 ? 0.0f : __uint_as_float((uint32_t)(vex - ve + 127) << 23);
+#pragma unroll
+                for (int nn = 0; nn < NN; nn++) {
+                    const float a = mnew[nn] > mrow[nn] ? ex2(mrow[nn] - mnew[nn]) : 1.0f;   // 0 while nothing was seen
+                    lrow[nn] *= a;
+                    const float av = a * ov;
+#pragma unroll
+                    for (int y = 0; y < MT; y++) {
+                        o[y][nn][0] *= av;
+                        o[y][nn][1] *= av;
+                        o[y][nn][2] *= av;
+                        o[y][nn][3] *= av;
+                    }
+                    mrow[nn] = mnew[nn];
                 }
-                mrow = mnew;
                 vex = ve;
             }
-            const float msafe = mrow == -INFINITY ? 0.0f : mrow;
-            float gsum[2] = {0.0f, 0.0f};
+            // ---- weights; times value scales, in units of 2^(vex - 14), as two fp16 terms, moved to the
+            // lanes that multiply them: column g8 is row g8 / 2's hi (even) or lo term
+            const float vu = __uint_as_float((uint32_t)(14 - vex + 127) << 23);
+            uint32_t pb[2][NN][2];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                s[j][0] = ex2(s[j][0] - msafe);
-                s[j][1] = ex2(s[j][1] - msafe);
-                gsum[j >> 1] += s[j][0] + s[j][1];
-            }
-            lrow += gsum[0] + gsum[1];
-            if (p.glse) {   // log2 of the weight sums by group of min(P, 32) tokens
+            for (int nn = 0; nn < NN; nn++) {
+                const float msafe = mrow[nn] == -INFINITY ? 0.0f : mrow[nn];
+                float gsum[2];
 #pragma unroll
-                for (int i2 = 0; i2 < 2; i2++) {
-                    gsum[i2] += __shfl_xor_sync(0xffffffffu, gsum[i2], 1);
-                    gsum[i2] += __shfl_xor_sync(0xffffffffu, gsum[i2], 2);
+                for (int mt = 0; mt < 2; mt++) {
+                    const float p0 = ex2(s[mt][nn][0] - msafe), p1 = ex2(s[mt][nn][1] - msafe), vv = (mt ? vs1 : vs0) * vu;
+                    gsum[mt] = p0 + p1;
+                    uint32_t hi, lo;
+                    split2(p0 * vv, p1 * vv, hi, lo);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int from = (t + 4 * e) * 4 + (g8 >> 1);
+                        const uint32_t h = __shfl_sync(0xffffffffu, hi, from), l = __shfl_sync(0xffffffffu, lo, from);
+                        pb[mt][nn][e] = g8 & 1 ? l : h;
+                    }
                 }
-                if (real && t == 0) {
-                    const int slot = (u < it.pre ? u : it.start + u - it.pre) * UNIT;
-                    float *gl = p.glse + ((int64_t)it.ti[g8] * p.Hq + it.head[g8]) * p.NG + (slot >> p.lgGroup);
-                    if (p.lgGroup == 4) {
-                        gl[0] = __log2f(gsum[0]) + msafe;
-                        if (live > 16) gl[1] = __log2f(gsum[1]) + msafe;
-                    } else {
-                        gl[0] = __log2f(gsum[0] + gsum[1]) + msafe;
+                lrow[nn] += gsum[0] + gsum[1];
+                if (p.glse) {   // log2 of the weight sums by group of min(P, 32) tokens
+#pragma unroll
+                    for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) gsum[mt] += __shfl_xor_sync(0xffffffffu, gsum[mt], d);
+                    const int r = 4 * nn + t;
+                    if (g8 == 0 && r < nrows) {
+                        const int slot = (u < it.pre ? u : it.start + u - it.pre) * UNIT;
+                        float *gl = p.glse + ((int64_t)it.ti[r] * p.Hq + it.head[r]) * p.NG + (slot >> p.lgGroup);
+                        if (p.lgGroup == 4) {
+                            gl[0] = __log2f(gsum[0]) + msafe;
+                            if (live > 16) gl[1] = __log2f(gsum[1]) + msafe;
+                        } else {
+                            gl[0] = __log2f(gsum[0] + gsum[1]) + msafe;
+                        }
                     }
                 }
             }
-            // ---- weights times value scales, in units of 2^(vex - 14), as two fp16 terms
-            const float vu = __uint_as_float((uint32_t)(14 - vex + 127) << 23);
-            const float v0 = vs0 * vu, v1 = vs1 * vu;
-            uint32_t pa[4][2];
+            // ---- values: k the 16 tokens of a step in the order (t, t + 8), (t + 4, t + 12); row g8 of
+            // tile x is the 2x-th position of chunk g8, row g8 + 8 the next one
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float vv = j < 2 ? v0 : v1;
-                split2(s[j][0] * vv, s[j][1] * vv, pa[j][0], pa[j][1]);
-            }
-            // ---- values: k the 16 tokens of a step, column n of tile x the x-th position of chunk n
-#pragma unroll
-            for (int step = 0; step < 2; step++) {
-                uint32_t w[4][D / 32];   // this lane's chunk of tokens r0, r0 + 1, r0 + 8, r0 + 9
+            for (int mt = 0; mt < 2; mt++) {
+                uint32_t w[4][D / 32];   // this lane's chunk of tokens t, t + 8, t + 4, t + 12
 #pragma unroll
                 for (int x = 0; x < 4; x++) {
-                    const int tok = 16 * step + 2 * t + (x & 1) + 8 * (x >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 q4 = sh_ld128(vb + tok * 128 + ((g8 ^ (tok & 7)) << 4));
+                    const int up = 8 * (x & 1) + 4 * (x >> 1), tok = 16 * mt + t + up;
+                    if constexpr (D == 128) {   // (four rows on: the chunk's bit 2 changes, eight: nothing)
+                        const uint4 q4 = sh_ld128(vb + (x >> 1 ? voff ^ 64u : voff) + (16 * mt + up) * 128);
                         w[x][0] = q4.x;
                         w[x][1] = q4.y;
                         w[x][2] = q4.z;
                         w[x][3] = q4.w;
-                    } else {
-                        const uint2 q2 = sh_ld64(vb + (tok >> 1) * 128 +
-                                                 (((4 * (tok & 1) + (g8 >> 1)) ^ ((tok >> 1) & 7)) << 4) + 8 * (g8 & 1));
+                    } else {   // (four rows on: two lines, the chunk's bit 1 changes; eight: its bit 2)
+                        const uint2 q2 = sh_ld64(vb + (voff ^ (x >> 1 ? 32u : 0u) ^ (x & 1 ? 64u : 0u)) + (16 * mt + up) * 64);
                         w[x][0] = q2.x;
                         w[x][1] = q2.y;
                     }
                     // slots past the last token may hold any bytes, NaN codes among them
-                    if (KIND == GQ_KV_E4M3 && !whole && (tok >= live || ((m.lost >> step) & 1)))
+                    if (KIND == GQ_KV_E4M3 && !whole && (tok >= live || ((m.lost >> mt) & 1)))
 #pragma unroll
                         for (int y = 0; y < D / 32; y++) w[x][y] = 0u;
                 }
 #pragma unroll
                 for (int y = 0; y < D / 32; y++) {
-                    uint32_t b0[4], b1[4];
+                    uint32_t b0[4], b1[4];   // positions 4y .. 4y + 3 of tokens (t, t + 8) and (t + 4, t + 12)
                     widen_pairs<KIND>(w[0][y], w[1][y], b0);
                     widen_pairs<KIND>(w[2][y], w[3][y], b1);
 #pragma unroll
-                    for (int x = 0; x < 4; x++)
-                        mma_f16_16x8x16(o[4 * y + x], pa[2 * step][0], pa[2 * step][1], pa[2 * step + 1][0], pa[2 * step + 1][1],
-                                        b0[x], b1[x]);
+                    for (int x = 0; x < 2; x++)
+#pragma unroll
+                        for (int nn = 0; nn < NN; nn++)
+                            mma_f16_16x8x16(o[2 * y + x][nn], b0[2 * x], b0[2 * x + 1], b1[2 * x], b1[2 * x + 1], pb[mt][nn][0],
+                                            pb[mt][nn][1]);
                 }
             }
             __syncwarp();
@@ -689,28 +741,28 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         count += u1 - u0;
 
-        // ---- join the warps
-        lrow += __shfl_xor_sync(0xffffffffu, lrow, 1);
-        lrow += __shfl_xor_sync(0xffffffffu, lrow, 2);
-        if (t == 0) {
-            sm.ml[warp][g8][0] = mrow;
-            sm.ml[warp][g8][1] = lrow;
-        }
-        {
-            // in units of 2^0, relative to the warp's own maximum.  Lane (g8, t): n-tile x, column
-            // 2t (+1) is position (2t (+1)) * RUN / 2 + x; 16-byte chunk y of row r lies at y ^ r
-            const float a = __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
-            const uint32_t dst = smem_addr(red) + (uint32_t)((warp * ROWS + g8) * D * 4);
+        // ---- join the warps: sums in units of 2^0, relative to the warp's own maximum.  Lane (g8, t)
+        // holds positions D / 8 g8 .. of row 4 nn + t; 16-byte chunk y of row r lies at y ^ r
+        const float vscale = __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
 #pragma unroll
-            for (int e = 0; e < 2; e++)
+        for (int nn = 0; nn < NN; nn++) {
 #pragma unroll
-                for (int x = 0; x < 2 * KS; x += 4)
-                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((RUN / 4 * t + e * (KS / 2) + x / 4) ^ g8) << 4)),
-                                 "f"((o[x][e] + o[x][e + 2]) * a), "f"((o[x + 1][e] + o[x + 1][e + 2]) * a),
-                                 "f"((o[x + 2][e] + o[x + 2][e + 2]) * a), "f"((o[x + 3][e] + o[x + 3][e + 2]) * a)
-                                 : "memory");
+            for (int d = 4; d <= 16; d <<= 1) lrow[nn] += __shfl_xor_sync(0xffffffffu, lrow[nn], d);
+            const int r = 4 * nn + t;
+            if (g8 == 0) {
+                sm.ml[warp][r][0] = mrow[nn];
+                sm.ml[warp][r][1] = lrow[nn];
+            }
+            const uint32_t dst = smem_addr(red) + (uint32_t)((warp * ROWS + r) * D * 4);
+#pragma unroll
+            for (int x = 0; x < MT; x += 2)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((D / 32 * g8 + x / 2) ^ r) << 4)),
+                             "f"((o[x][nn][0] + o[x][nn][1]) * vscale), "f"((o[x][nn][2] + o[x][nn][3]) * vscale),
+                             "f"((o[x + 1][nn][0] + o[x + 1][nn][1]) * vscale), "f"((o[x + 1][nn][2] + o[x + 1][nn][3]) * vscale)
+                             : "memory");
         }
-        consumer_sync();
+        consumer_sync<CONSUMERS>();
+        const int rows = nrows;
         const bool cut0 = u0 > 0, cut1 = u1 < it.units;   // the item began before, goes on after this CTA
         const int piece_slot = blockIdx.x * 2 + (cut0 ? 0 : 1);
         for (int x = tid; x < rows * (D / 4); x += CONSUMERS) {
@@ -747,20 +799,20 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int64_t item0 = it.item0;
             const int c0 = (int)(item0 / piece), c1 = (int)((item0 + it.units - 1) / piece);
             __threadfence();
-            consumer_sync();
+            consumer_sync<CONSUMERS>();
             if (tid == 0) {
                 const int done = atomicAdd(p.counters + c0, 1);
                 sm.last = done == c1 - c0;
                 if (done == c1 - c0) p.counters[c0] = 0;   // left at zero for the next launch
             }
-            consumer_sync();
+            consumer_sync<CONSUMERS>();
             if (sm.last) {
                 __threadfence();
-                join_pieces<D>(p, it, c0, c1, warp, lane);
+                join_pieces<D, W, ROWS>(p, it, c0, c1, warp, lane);
             }
         }
         at = it.item0 + u1;
-        consumer_sync();   // the item's data, the warps' sums and the fragments are free
+        consumer_sync<CONSUMERS>();   // the item's data, the warps' sums and the fragments are free
         if (lane == 0) mbar_arrive(smem_addr(sm.item_empty + st));
         __syncwarp();
     }
@@ -823,11 +875,12 @@ int log2_of(int64_t x) {
 // with at most ROWS_MAX rows leave most of it idle and take the row kernel.
 constexpr int ROWS_MAX = 32;
 
-template <int KIND, int D>
+template <int KIND, int D, int NN>
 gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
                       cudaStream_t s) {
-    auto kernel = attn_pages_rows_kernel<KIND, D>;
-    constexpr size_t smem = RowsLayout<D>::total + 1024;
+    auto kernel = attn_pages_rows_kernel<KIND, D, NN>;
+    constexpr size_t smem = RowsLayout<D, NN>::total + 1024;
+    constexpr int ROWS = rows_of(NN), THREADS = (warps_of(NN) + 1) * 32;
     static std::atomic<bool> smem_set[64];
     int dev = 0;
     KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
@@ -898,11 +951,20 @@ gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, cons
     p.NG = (int)((c.NB * c.P) >> p.lgGroup);
     p.scale = sc.scale;
     p.cap = sc.cap;
-    if (c.kind == GQ_KV_I8)
-        return c.D == 64 ? launch_rows<GQ_KV_I8, 64>(p, c, T, w_in, w_out, decay, s)
-                         : launch_rows<GQ_KV_I8, 128>(p, c, T, w_in, w_out, decay, s);
-    return c.D == 64 ? launch_rows<GQ_KV_E4M3, 64>(p, c, T, w_in, w_out, decay, s)
-                     : launch_rows<GQ_KV_E4M3, 128>(p, c, T, w_in, w_out, decay, s);
+    // items of up to 4 rows, where a sequence's rows of a KV head are no more, else of up to 8
+    const bool few = (int64_t)max_n * p.G <= 4;
+    if (c.kind == GQ_KV_I8) {
+        if (c.D == 64)
+            return few ? launch_rows<GQ_KV_I8, 64, 1>(p, c, T, w_in, w_out, decay, s)
+                       : launch_rows<GQ_KV_I8, 64, 2>(p, c, T, w_in, w_out, decay, s);
+        return few ? launch_rows<GQ_KV_I8, 128, 1>(p, c, T, w_in, w_out, decay, s)
+                   : launch_rows<GQ_KV_I8, 128, 2>(p, c, T, w_in, w_out, decay, s);
+    }
+    if (c.D == 64)
+        return few ? launch_rows<GQ_KV_E4M3, 64, 1>(p, c, T, w_in, w_out, decay, s)
+                   : launch_rows<GQ_KV_E4M3, 64, 2>(p, c, T, w_in, w_out, decay, s);
+    return few ? launch_rows<GQ_KV_E4M3, 128, 1>(p, c, T, w_in, w_out, decay, s)
+               : launch_rows<GQ_KV_E4M3, 128, 2>(p, c, T, w_in, w_out, decay, s);
 }
 
 }  // namespace gq
