@@ -48,18 +48,28 @@ namespace {
 constexpr int UNIT = 32;                    // tokens per unit
 // Consumer warps, and query rows of an item, for 1 or 2 column tiles: two CTAs of W + 1 warps fill
 // an SM's registers.
-__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 9 : 7; }
+__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 8 : 6; }
 __host__ __device__ constexpr int rows_of(int NN) { return 4 * NN; }
 constexpr int ROWS_MOST = 8;
 constexpr int ITEMS = 2;                    // items whose data is kept
 
-// Slots of the ring, of 8 KB (D = 128) or 4.  A multiple of W: the warp that takes a slot's unit also
-// takes the next one in that slot.  Otherwise a warp could wait for a slot's next phase before the
-// present one is over (copies land in any order), and a parity wait two phases ahead passes at once.
-__host__ __device__ constexpr int slots_of(int D, int NN) { return warps_of(NN) * (D == 128 ? 1 : 2); }
-constexpr int MAX_SLOTS = 18;
+// The ring's slots hold two units, 64 tokens' keys and values: the producer's time for a slot (a
+// wait, a count of bytes, the copies) is what limits a CTA when slots are small.  They are filled in
+// order and read by any warps.  A slot's next phase may be waited for only when the present one is
+// over (a parity wait two phases ahead passes at once), and copies land in any order: so a warp
+// first waits until the slot's last contents were given back.  That wait itself is never two phases
+// ahead: a warp's units are W apart, which is at most W / 2 + 1 slots within an item (its first and
+// last slot may hold one unit), and the slot before was filled when the one `slots` earlier was
+// given back; and items end together.
+__host__ __device__ constexpr int slots_of(int D, int NN) { return (NN == 1 ? 5 : 4) * (D == 128 ? 1 : 2); }
+static_assert(slots_of(128, 1) >= warps_of(1) / 2 + 1 && slots_of(128, 2) >= warps_of(2) / 2 + 1, "see above");
+constexpr int MAX_SLOTS = 10;
+// Places for units' data, taken 32 at a time (the last of an item may be few).  What the producer
+// overwrites is done: either two items have begun since (ITEMS), or 32 units of one.
+constexpr int METAS = 128;
+static_assert(ITEMS == 2 && 16 >= MAX_SLOTS, "a unit's data stays until it is done");
 
-struct UnitMeta {               // beside each slot: scales and first positions of the two halves
+struct UnitMeta {               // of a unit: scales and first positions of the two halves
     float ks[2], vs[2];
     int base[2];
     int live;                   // tokens of the unit that are held (0 .. 32)
@@ -79,7 +89,7 @@ struct ItemRec {
 
 struct RowsSmem {
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], item_full[ITEMS], item_empty[ITEMS];
-    UnitMeta meta[MAX_SLOTS];
+    UnitMeta meta[METAS];       // of unit u of an item at (its first unit's place + u) mod METAS
     ItemRec item[ITEMS];
     float ml[warps_of(1)][ROWS_MOST][2];    // maximum and denominator of each warp
     int64_t start, total;       // line position of the sequence that the CTA starts in
@@ -90,8 +100,8 @@ struct RowsSmem {
 template <int D, int NN>
 struct RowsLayout {
     static constexpr int W = warps_of(NN), ROWS = rows_of(NN);
-    static constexpr int ring = 0;                                     // units: keys, values
-    static constexpr int q = ring + slots_of(D, NN) * UNIT * D * 2;    // [ITEMS][ROWS][D] f32
+    static constexpr int ring = 0;                                     // [slot]: keys, values of 64 tokens
+    static constexpr int q = ring + slots_of(D, NN) * UNIT * D * 4;    // [ITEMS][ROWS][D] f32
     static constexpr int frag = q + ITEMS * ROWS * D * 4;              // the query's MMA fragments
     static constexpr int red = frag + D * 16 * NN;                     // [W][ROWS][D] f32
     static constexpr int ctl = red + W * ROWS * D * 4;
@@ -149,8 +159,9 @@ __device__ __forceinline__ Span span_of(const AttnParams8 &p, const SeqStep &s) 
     }
     if (first > 0) lo = (int)max((int64_t)0, (int64_t)s.held - s.seen + first);
     if (p.window > 0) lo = (int)max((int64_t)lo, (int64_t)s.held - p.window + 1);
-    r.start = min(lo, n - 1) >> 5;
-    r.pre = min((min(max(pre, 0), n) + UNIT - 1) >> 5, r.start);
+    // (whole slots of two units)
+    r.start = (min(lo, n - 1) >> 6) * 2;
+    r.pre = min(((min(max(pre, 0), n) + 2 * UNIT - 1) >> 6) * 2, r.start);
     r.units = r.pre + end - r.start;
     return r;
 }
@@ -246,7 +257,6 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
     constexpr int KS = D / 16;                               // MMA steps of a score
     constexpr int RUN = D / 4;                               // positions per lane of a score
     constexpr int MT = D / 16;                               // row tiles of the output
-    static_assert(SLOTS % W == 0, "a slot belongs to one warp");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);   // (an offset: the compiler keeps the address space)
     RowsSmem &sm = *reinterpret_cast<RowsSmem *>(smem + L::ctl);
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
     if (tid == 0) {
         for (int s = 0; s < SLOTS; s++) {
             mbar_init(smem_addr(sm.full + s), 1);
-            mbar_init(smem_addr(sm.empty + s), 1);
+            mbar_init(smem_addr(sm.empty + s), 2);   // a slot's two units
         }
         for (int s = 0; s < ITEMS; s++) {
             mbar_init(smem_addr(sm.item_full + s), 1);
@@ -330,9 +340,14 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
             item0 = sm.start + i * k.u.units;
         }
         const uint64_t policy = l2_evict_first_policy();
-        int count = 0, items = 0;
+        int count = 0, meta = 0, items = 0;   // slots filled, places for units' data, items
         bool ok = true;
-        const int rows16 = D / 8;   // 128-byte pool rows of 16 tokens
+        // Lane l < 8 copies group l mod 4 (16 tokens) of a slot, keys or values (l / 4); where a page holds
+        // more, the first group's copy brings up to 64 tokens of it.
+        const int per = min(c.P, 2 * UNIT), g = lane & 3;
+        const uint32_t copy_bytes = (uint32_t)(per * D), my_dst = (uint32_t)((lane >> 2) * 2 * HALF + g * 16 * D);
+        const bool copier = lane < 8 && g * 16 % per == 0;
+        const CUtensorMap *my_map = lane < 4 ? &kmap : &vmap;
         for (int64_t at = lo; at < hi && ok;) {
             const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
             const int64_t trow = ((int64_t)k.b * c.Hkv + k.h) * c.NB;
@@ -376,26 +391,26 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
                 __syncwarp();
                 items++;
             }
-            for (int ub = u0; ub < u1 && ok; ub += 32) {
+            for (int ub = u0 & ~1; ub < u1 && ok; ub += 32) {
                 // each lane looks up one unit: its pages, their scales and positions
                 const int u = ub + lane;
                 const int slot = (u < k.u.pre ? u : k.u.start + u - k.u.pre) * UNIT;
                 UnitMeta m;
-                int page[2] = {-1, -1};
+                int row[2] = {-1, -1};   // pool rows (128 bytes) of the halves
                 m.lost = 0;
-                m.live = u < u1 ? max(0, min(UNIT, n - slot)) : 0;
+                m.live = u >= u0 && u < u1 ? max(0, min(UNIT, n - slot)) : 0;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     m.ks[i] = m.vs[i] = 0.0f;
                     m.base[i] = 0;
                     if (m.live > 16 * i) {
-                        const int j = (slot + 16 * i) >> p.lgP;
+                        const int j = (slot + 16 * i) >> p.lgP, inpage = (slot + 16 * i) & (c.P - 1);
                         const int pg = __ldg(c.table + trow + j);
                         if ((unsigned)pg < (unsigned)c.pages) {
-                            page[i] = pg;
+                            row[i] = (int)(((int64_t)pg * c.P + inpage) * D / 128);
                             m.ks[i] = __ldg(c.ks + pg);
                             m.vs[i] = __ldg(c.vs + pg);
-                            m.base[i] = __ldg(c.base + trow + j) + ((slot + 16 * i) & (c.P - 1));
+                            m.base[i] = __ldg(c.base + trow + j) + inpage;
                         } else {
                             atomicOr(c.status, STATUS_RANGE);
                             m.base[i] = 0x7f000000;   // a position nobody sees
@@ -404,35 +419,31 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
                     }
                 }
                 const int todo = min(32, u1 - ub);
-                for (int i = 0; i < todo; i++) {
+                if (lane < todo) sm.meta[(meta + lane) % METAS] = m;   // (what was there is done: METAS)
+                meta += 32;
+                __syncwarp();
+                for (int i = 0; i < todo; i += 2) {   // units ub + i and the next one
+                    // the group's row; where one copy brings all, from the first group that is there
+                    const int from = i + (g >> 1);
+                    const int ra = __shfl_sync(0xffffffffu, row[0], from), rb = __shfl_sync(0xffffffffu, row[1], from);
+                    int r = g & 1 ? rb : ra;
+                    if (per == 2 * UNIT) {
+                        const uint32_t there = __ballot_sync(0xffffffffu, lane < 4 && r >= 0);
+                        const int first = there ? __ffs(there) - 1 : 0;
+                        r = __shfl_sync(0xffffffffu, r, first);
+                        r = there ? r - first * 16 * D / 128 : -1;
+                    }
+                    const bool mine = copier && r >= 0;
+                    const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * copy_bytes;
                     const int sl = count % SLOTS;
                     if (count >= SLOTS)
                         ok = mbar_wait(smem_addr(sm.empty + sl), (uint32_t)((count / SLOTS - 1) & 1), c.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if (lane == i) {
-                        const uint32_t bar = smem_addr(sm.full + sl);
-                        const uint32_t dst = smem_addr(smem + L::ring + (size_t)sl * 2 * HALF);
-                        sm.meta[sl] = m;
-                        const int inpage = slot & (c.P - 1);
-                        if (c.P >= UNIT) {
-                            mbar_arrive_expect_tx(bar, page[0] >= 0 ? 2 * HALF : 0);
-                            if (page[0] >= 0) {
-                                const int row = (int)(((int64_t)page[0] * c.P + inpage) * D / 128);
-                                tma_rows(dst, &kmap, row, bar, policy);
-                                tma_rows(dst + HALF, &vmap, row, bar, policy);
-                            }
-                        } else {
-                            mbar_arrive_expect_tx(bar, ((page[0] >= 0) + (page[1] >= 0)) * HALF);
-#pragma unroll
-                            for (int g = 0; g < 2; g++)
-                                if (page[g] >= 0) {
-                                    const int row = (int)((int64_t)page[g] * rows16);
-                                    tma_rows(dst + g * (HALF / 2), &kmap, row, bar, policy);
-                                    tma_rows(dst + HALF + g * (HALF / 2), &vmap, row, bar, policy);
-                                }
-                        }
-                    }
+                    const uint32_t bar = smem_addr(sm.full + sl);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (mine) tma_rows(smem_addr(smem + L::ring) + (uint32_t)(sl * 4 * HALF) + my_dst, my_map, r, bar, policy);
                     __syncwarp();
                     count++;
                 }
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
     const int g8 = lane >> 2, t = lane & 3;
     const uint32_t frag = smem_addr(smem + L::frag) + lane * 8;
     float *red = reinterpret_cast<float *>(smem + L::red);
-    int count = 0;
+    int count = 0, slots = 0, metas = 0;   // units, slots, places of units' data before the item
     bool failed = false;
     int64_t at = lo;
     // where this lane's chunks of key rows g8 and of value rows t lie in 16 tokens (D = 64: two rows a
@@ -551,13 +562,14 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
 
         // unit u of the item is unit count + u - u0 of this CTA; warp w takes every W-th
         for (int u = u0 + (warp + W - count % W) % W; u < u1; u += W) {
-            const int i = count + u - u0, sl = i % SLOTS;
+            const int i = slots + (u >> 1) - (u0 >> 1), sl = i % SLOTS, phase = i / SLOTS;
             if (failed) break;   // a wait gave up: no further ones
-            const bool got = mbar_wait(smem_addr(sm.full + sl), (uint32_t)((i / SLOTS) & 1), c.status);
+            bool got = phase == 0 || mbar_wait(smem_addr(sm.empty + sl), (uint32_t)((phase - 1) & 1), c.status);
+            got = got && mbar_wait(smem_addr(sm.full + sl), (uint32_t)(phase & 1), c.status);
             failed = !__all_sync(0xffffffffu, got);
             if (failed) break;
-            const uint32_t kb = smem_addr(smem + L::ring) + (uint32_t)sl * 2 * HALF, vb = kb + HALF;
-            const UnitMeta &m = sm.meta[sl];
+            const uint32_t kb = smem_addr(smem + L::ring) + (uint32_t)(sl * 4 * HALF + (u & 1) * HALF), vb = kb + 2 * HALF;
+            const UnitMeta &m = sm.meta[(metas + u - (u0 & ~1)) % METAS];
             const int live = m.live;
             // ---- scores of tokens 16 mt + g8 and + 8, rows 4 nn + t
             float s[2][NN][2];
@@ -736,10 +748,16 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(sm.empty + sl));
+            if (lane == 0) {
+                mbar_arrive(smem_addr(sm.empty + sl));
+                // a slot's only unit gives both halves back
+                if ((u == u0 && (u & 1)) || (u == u1 - 1 && !(u & 1))) mbar_arrive(smem_addr(sm.empty + sl));
+            }
             __syncwarp();
         }
         count += u1 - u0;
+        slots += ((u1 - 1) >> 1) - (u0 >> 1) + 1;
+        metas += (u1 - (u0 & ~1) + 31) & ~31;
 
         // ---- join the warps: sums in units of 2^0, relative to the warp's own maximum.  Lane (g8, t)
         // holds positions D / 8 g8 .. of row 4 nn + t; 16-byte chunk y of row r lies at y ^ r
@@ -910,7 +928,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
     if (rows) {
         alignas(64) CUtensorMap kmap, vmap;
         const int64_t pool_rows = c.pages * c.P * c.D / 128;
-        const int box = (int)(std::min<int64_t>(c.P, UNIT) * D / 128);
+        const int box = (int)(std::min<int64_t>(c.P, 2 * UNIT) * D / 128);
         KV_TRY(byte_rows_map(&kmap, c.k, pool_rows, box));
         KV_TRY(byte_rows_map(&vmap, c.v, pool_rows, box));
         void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
