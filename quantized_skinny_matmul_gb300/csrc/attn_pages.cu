@@ -48,7 +48,7 @@ namespace {
 constexpr int UNIT = 32;                    // tokens per unit
 // Consumer warps, and query rows of an item, for 1 or 2 column tiles: two CTAs of W + 1 warps fill
 // an SM's registers.
-__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 8 : 6; }
+__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 7 : 7; }
 __host__ __device__ constexpr int rows_of(int NN) { return 4 * NN; }
 constexpr int ROWS_MOST = 8;
 constexpr int ITEMS = 2;                    // items whose data is kept
@@ -838,48 +838,51 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
 
 // ---------------------------------------------------------------------------
 // The weight that each page gathered: decay * in + sum over the step's query rows of
-// 2^(log2 of the page's weight sum - log2 of the row's denominator).  A CTA takes 32 pages
-// of one (sequence, head), a lane per page; its warps share the rows and are added in order.
+// 2^(log2 of the page's weight sum - log2 of the row's denominator).  A CTA takes 32 groups of
+// tokens of one (sequence, head), a lane per group; its warps share the rows and are added in order.
 // The sums of groups that a row cannot see were never written: they are passed over.
 // ---------------------------------------------------------------------------
-constexpr int WW = 8;   // warps
+constexpr int WW = 16;   // warps
 
 __global__ void __launch_bounds__(WW * 32) attn_pages_weights_kernel(const AttnParams8 p, const float *w_in, float *w_out,
                                                                      float decay) {
     __shared__ float part[WW][32];
     const PagesView &c = p.c;
     pdl_launch_dependents();
-    const int tiles = (c.NB + 31) / 32, bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = (blockIdx.x % tiles) * 32 + lane;
+    const int per = p.lgP - p.lgGroup;   // log2 of the groups of a page
+    const int tiles = (((c.NB << per) + 31) / 32), bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = (blockIdx.x % tiles) * 32 + lane, j = g >> per;
+    const int size = 1 << p.lgGroup;
     pdl_wait();
     const SeqStep s = seq_step(c, p.cu, b, p.T, p.max_n);
-    const int end = s.bad ? 0 : s.held + s.n;
+    const int end = s.bad ? 0 : s.held + s.n, slot = g << p.lgGroup;
     const int64_t at = (int64_t)bh * c.NB + j;
-    const bool used = j < c.NB && ((int64_t)j << p.lgP) < end;
+    const bool used = slot < end;        // (a page is in use if its first group is)
     float sum = 0.0f;
-    if (used) {
-        const int base = c.base[at], slot = j << p.lgP;
-        const int groups = (min(c.P, end - slot) + (1 << p.lgGroup) - 1) >> p.lgGroup, size = 1 << p.lgGroup;
-        const float *gl = p.glse + (slot >> p.lgGroup);
-        for (int x = warp; x < s.n * p.G; x += WW) {
+    if (__any_sync(0xffffffffu, used)) {
+        const int x0 = used ? c.base[at] + (slot & (c.P - 1)) : 0x7f000000, x1 = used ? x0 + size - 1 : 0x7f000000;
+        const float *gl = p.glse + (used ? g : 0);
+        const int rows = s.n * p.G;
+        const int64_t r0 = (int64_t)s.t0 * p.Hq + h * p.G;
+        // (loads of rows and groups that were never written are within the buffer, and passed over)
+#pragma unroll 4
+        for (int x = warp; x < rows; x += WW) {
             const int i = x / p.G, qpos = s.seen + i;
+            const int64_t r = r0 + (int64_t)i * p.Hq + (x - i * p.G);
+            const float v = __ldcg(gl + r * p.NG), l = __ldcg(p.lse + r);
             const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? __ldg(p.prefix + s.t0 + i) : 0;
             const int lo = p.window > 0 ? (int)max((int64_t)first, (int64_t)qpos - p.window + 1) : first;
-            const int64_t r = (int64_t)(s.t0 + i) * p.Hq + h * p.G + (x - i * p.G);
-            const float l = __ldcg(p.lse + r);
-            for (int g = 0; g < groups; g++) {
-                const int x0 = base + g * size, x1 = x0 + size - 1;
-                if ((x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre))
-                    sum += ex2(__ldcg(gl + r * p.NG + g) - l);
-            }
+            const bool see = (x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre);
+            sum += see ? ex2(v - l) : 0.0f;
         }
     }
     part[warp][lane] = sum;
     __syncthreads();
-    if (warp == 0 && j < c.NB) {
+    if (warp == 0) {
         float total = part[0][lane];
         for (int w = 1; w < WW; w++) total += part[w][lane];
-        w_out[at] = used ? (w_in ? decay * w_in[at] : 0.0f) + total : 0.0f;
+        for (int d = 1; d < 1 << per; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+        if (j < c.NB && (g & ((1 << per) - 1)) == 0) w_out[at] = used ? (w_in ? decay * w_in[at] : 0.0f) + total : 0.0f;
     }
 }
 
@@ -936,7 +939,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
                           "paged attention launch"));
     }
     if (w_out) {
-        const int64_t wgrid = c.B * c.Hkv * ((c.NB + 31) / 32);
+        const int64_t wgrid = c.B * c.Hkv * ((p.NG + 31) / 32);
         void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
         KV_TRY(launch_pdl((const void *)attn_pages_weights_kernel, dim3((unsigned)wgrid), dim3(WW * 32), 0, s, wargs,
                           "paged attention weights launch"));

@@ -34,28 +34,26 @@ namespace {
 // ---------------------------------------------------------------------------
 struct Scale8 {
     float d, r, m;   // the scale times m, 1 / d (0 for a zero scale), m = 1 or 2^64
+    bool small;      // m is not 1
 };
 
 __device__ __forceinline__ Scale8 scale8(float s) {
     Scale8 q;
-    q.m = s < 0x1p-60f ? 0x1p64f : 1.0f;
+    q.small = s < 0x1p-60f;
+    q.m = q.small ? 0x1p64f : 1.0f;
     q.d = s * q.m;
     q.r = q.d == 0.0f ? 0.0f : 1.0f / q.d;
     return q;
 }
 
 // Is y too near a border between codes for its rounding to be trusted?  (y is off by at most
-// 2 units in its last place: for INT8 at most 2^-16; for e4m3 two steps of the 20 bits that
-// the three mantissa bits leave, or 2^-20 of a step below 2^-6, where the step is fixed.)
+// 3 units in its last place: for INT8 at most 2^-15; for e4m3 of the 20 bits that the three
+// mantissa bits leave.  Below 2^-6, where e4m3 steps are fixed, every value is looked at.)
 template <int KIND>
 __device__ __forceinline__ bool code_unsure(float y) {
-    if constexpr (KIND == GQ_KV_I8) {
-        return !(fabsf(y - rintf(y)) < 0.5f - 0x1p-15f);
-    } else {
-        const uint32_t b = __float_as_uint(y) & 0x7fffffffu;
-        const float t = fabsf(y) * 512.0f;
-        return b >= 0x3C800000u ? ((b & 0xFFFFFu) - 0x80000u + 4u) < 8u : !(fabsf(t - rintf(t)) < 0.5f - 0x1p-15f);
-    }
+    if constexpr (KIND == GQ_KV_I8) return !(fabsf(y - rintf(y)) < 0.5f - 0x1p-15f);
+    const uint32_t b = __float_as_uint(y) & 0x7fffffffu;
+    return b < 0x3C800000u || ((b - 0x7FFFCu) & 0xFFFFFu) < 8u;
 }
 
 // The 8-bit value (not the code) nearest to (a + ae) / d, given y near that quotient.
@@ -96,19 +94,49 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 __device__ __forceinline__ int clamp127(float v) { return (int)fminf(fmaxf(v, -127.0f), 127.0f); }
 
-// Four codes from four values v (+ remainders e, for held tokens), already times s.m.
+// Four codes from four values v (+ remainders e, for held tokens), already times s.m: the nearest
+// codes of the quotients, and, where some lane of the warp has one next to a border, the exact
+// ones in their place (a few warps in a hundred; all 32 lanes call this).  Scales next to the
+// smallest, where INT8 quotients may pass 127, always take the second way.
 template <int KIND>
-__device__ __forceinline__ uint32_t encode4(float4 v, float4 e, const Scale8 &s) {
-    float y[4] = {v.x * s.r, v.y * s.r, v.z * s.r, v.w * s.r};
-    const float a[4] = {v.x, v.y, v.z, v.w}, ae[4] = {e.x, e.y, e.z, e.w};
-    if (s.r == 0.0f) return 0u;
+__device__ __forceinline__ uint32_t encode4(float4 v, float4 e, const Scale8 &s, bool live) {
+    const float y[4] = {v.x * s.r, v.y * s.r, v.z * s.r, v.w * s.r};
+    uint32_t code;
+    bool unsure;
+    if constexpr (KIND == GQ_KV_I8) {
+        // the nearest integer in the low mantissa bits of y + 1.5 * 2^23
+        uint32_t t[4];
+        float off = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-        if (code_unsure<KIND>(y[i])) y[i] = value_exact<KIND>(y[i], a[i], ae[i], s.d);
-    if constexpr (KIND == GQ_KV_I8)
-        return pack_bytes(clamp127(rintf(y[0])), clamp127(rintf(y[1])), clamp127(rintf(y[2])), clamp127(rintf(y[3])));
-    else
-        return e4m3x4(y[0], y[1], y[2], y[3]);
+        for (int i = 0; i < 4; i++) {
+            const float z = y[i] + 12582912.0f;
+            t[i] = __float_as_uint(z);
+            off = fmaxf(off, fabsf(y[i] - (z - 12582912.0f)));
+        }
+        code = pack_bytes((int)t[0], (int)t[1], (int)t[2], (int)t[3]);
+        unsure = !(off < 0.5f - 0x1p-15f) || s.small;
+    } else {
+        uint32_t least = 0x7fffffffu, near = 0xFFFFFu;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t b = __float_as_uint(y[i]) & 0x7fffffffu;
+            least = min(least, b);
+            near = min(near, (b - 0x7FFFCu) & 0xFFFFFu);
+        }
+        code = e4m3x4(y[0], y[1], y[2], y[3]);
+        unsure = least < 0x3C800000u || near < 8u;
+    }
+    if (__any_sync(0xffffffffu, unsure && live)) {
+        const float a[4] = {v.x, v.y, v.z, v.w}, ae[4] = {e.x, e.y, e.z, e.w};
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[i] = code_unsure<KIND>(y[i]) ? value_exact<KIND>(y[i], a[i], ae[i], s.d) : y[i];
+        if constexpr (KIND == GQ_KV_I8)
+            code = pack_bytes(clamp127(rintf(x[0])), clamp127(rintf(x[1])), clamp127(rintf(x[2])), clamp127(rintf(x[3])));
+        else
+            code = e4m3x4(x[0], x[1], x[2], x[3]);
+    }
+    return s.r == 0.0f ? 0u : code;
 }
 
 // The values of four codes.
@@ -196,17 +224,21 @@ __global__ void __launch_bounds__(AP_THREADS) kv_pages_append_kernel(const Appen
     for (int i = 0; i < R; i++) {
         const int r = r0 + i * RP;
         uint32_t *at = reinterpret_cast<uint32_t *>(codes + r * D);
-        if (r < fill) {
-            if (!grow) continue;
-            const float4 k = decode4<KIND>(*at);
+        const bool fresh = r >= fill && r < end;
+        const float4 a = make_float4(v[i].x * s.m, v[i].y * s.m, v[i].z * s.m, v[i].w * s.m);
+        const uint32_t code = encode4<KIND>(a, zero, s, fresh);
+        if (fresh) *at = code;
+    }
+    if (grow)   // held tokens, coded again
+        for (int i = 0; i < R; i++) {
+            const int r = r0 + i * RP;
+            uint32_t *at = reinterpret_cast<uint32_t *>(codes + r * D);
+            const float4 k = decode4<KIND>(r < fill ? *at : 0u);
             const float4 a = make_float4(k.x * om, k.y * om, k.z * om, k.w * om);
             const float4 e = make_float4(fmaf(k.x, om, -a.x), fmaf(k.y, om, -a.y), fmaf(k.z, om, -a.z), fmaf(k.w, om, -a.w));
-            *at = encode4<KIND>(a, e, s);
-        } else if (r < end) {
-            const float4 a = make_float4(v[i].x * s.m, v[i].y * s.m, v[i].z * s.m, v[i].w * s.m);
-            *at = encode4<KIND>(a, zero, s);
+            const uint32_t code = encode4<KIND>(a, e, s, r < fill);
+            if (r < fill) *at = code;
         }
-    }
     if (threadIdx.x == 0) {
         *scale = snew;
         if (kv == 0 && fill == 0) c.base[(int64_t)bh * c.NB + j] = q.seen + s0 - q.held;
@@ -214,8 +246,9 @@ __global__ void __launch_bounds__(AP_THREADS) kv_pages_append_kernel(const Appen
 }
 
 // ---------------------------------------------------------------------------
-// Read back: a thread turns 4 codes into 4 f32; a CTA takes RD_TOKENS tokens of a sequence,
-// all heads.  Bound by the f32 stores.
+// Read back.  A warp takes RD_TOKENS tokens of one head, keys or values: their pages (two at most,
+// as a page holds 16 tokens and more), then all their codes at once, then the f32 rows.  Bound by
+// the f32 stores.
 // ---------------------------------------------------------------------------
 constexpr int RD_THREADS = 256, RD_TOKENS = 8;
 
@@ -223,61 +256,72 @@ struct ReadParams {
     PagesView c;
     float *out[2];
     const int32_t *start, *cu;
-    int T, max_n, tiles;
+    int T, max_n, tiles, heads;   // tiles of tokens, groups of RD_THREADS / 32 heads
 };
 
-template <int KIND>
-__global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadParams p, int logP, int logQ) {
+template <int KIND, int D>
+__global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadParams p, int logP) {
+    constexpr int Q = D / 4, PER = 32 / Q, N = RD_TOKENS / PER;   // columns of 4, tokens per access, accesses
     const PagesView &c = p.c;
     pdl_launch_dependents();
-    const int tile = blockIdx.x % p.tiles, b = blockIdx.x / p.tiles;
+    const int hg = blockIdx.x % p.heads, tile = blockIdx.x / p.heads % p.tiles, b = blockIdx.x / p.heads / p.tiles;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = hg * (RD_THREADS / 32) + warp;
+    float *out = p.out[blockIdx.y];
     pdl_wait();
-    const int t0 = p.cu[b], n = p.cu[b + 1] - t0, s0 = p.start[b];
-    const int64_t cap = (int64_t)c.NB << logP;
-    if (t0 < 0 || n < 0 || n > p.max_n || (int64_t)t0 + n > p.T || s0 < 0 || (int64_t)s0 + n > cap) {
+    const int t0 = p.cu[b], t1 = p.cu[b + 1], s0 = p.start[b];
+    const int64_t n = (int64_t)t1 - t0;
+    if (t0 < 0 || n < 0 || n > p.max_n || t1 > p.T || s0 < 0 || s0 + n > ((int64_t)c.NB << logP)) {
         if (threadIdx.x == 0 && tile == 0) atomicOr(c.status, STATUS_RANGE);
         return;
     }
-    const int i0 = tile * RD_TOKENS, ni = min(RD_TOKENS, n - i0);
-    if (ni <= 0) return;
-    float *out = p.out[blockIdx.y];
-    if (!out) return;
+    const int i0 = tile * RD_TOKENS, ni = min(RD_TOKENS, (int)n - i0), slot = s0 + i0;
+    if (ni <= 0 || !out || h >= c.Hkv) return;
     const uint8_t *pool = blockIdx.y ? c.v : c.k;
     const float *scale = blockIdx.y ? c.vs : c.ks;
-    const int D = 4 << logQ, per = c.Hkv << logQ;   // 4-value columns per token
-    const int total = ni * per;
-    bool bad = false;
-#pragma unroll 4
-    for (int x = threadIdx.x; x < total; x += RD_THREADS) {
-        const int i = x / per, y = x - i * per, h = y >> logQ, col = y & ((1 << logQ) - 1);
-        const int slot = s0 + i0 + i;
-        const int page = __ldg(c.table + ((int64_t)b * c.Hkv + h) * c.NB + (slot >> logP));
-        if ((unsigned)page >= (unsigned)c.pages) {
-            bad = true;
-            continue;
-        }
-        const float s = __ldg(scale + page);
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(
-            pool + (((int64_t)page << logP) + (slot & ((1 << logP) - 1))) * D + 4 * col));
-        float4 f = decode4<KIND>(w);
-        f.x *= s;
-        f.y *= s;
-        f.z *= s;
-        f.w *= s;
-        *reinterpret_cast<float4 *>(out + ((int64_t)(t0 + i0 + i) * c.Hkv + h) * D + 4 * col) = f;
+    const int j0 = slot >> logP, j1 = (slot + ni - 1) >> logP;   // the pages of the first and of the last token
+    const int32_t *row = c.table + ((int64_t)b * c.Hkv + h) * c.NB;
+    int page[2] = {__ldg(row + j0), __ldg(row + j1)};
+    float s[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        const bool bad = (unsigned)page[e] >= (unsigned)c.pages;
+        if (bad && lane == 0) atomicOr(c.status, STATUS_RANGE);
+        if (bad) page[e] = -1;   // its tokens are left out
+        s[e] = bad ? 0.0f : __ldg(scale + page[e]);
     }
-    if (bad) atomicOr(c.status, STATUS_RANGE);
+    const int col = lane % Q, part = lane / Q;
+    uint32_t w[N];
+#pragma unroll
+    for (int x = 0; x < N; x++) {
+        const int i = x * PER + part, sl = slot + i, pg = sl >> logP == j0 ? page[0] : page[1];
+        w[x] = 0u;
+        if (i < ni && pg >= 0)
+            w[x] = __ldg(reinterpret_cast<const uint32_t *>(pool + (((int64_t)pg << logP) + (sl & ((1 << logP) - 1))) * D) + col);
+    }
+#pragma unroll
+    for (int x = 0; x < N; x++) {
+        const int i = x * PER + part, sl = slot + i, e = sl >> logP == j0 ? 0 : 1;
+        float4 f = decode4<KIND>(w[x]);
+        f.x *= s[e];
+        f.y *= s[e];
+        f.z *= s[e];
+        f.w *= s[e];
+        if (i < ni && page[e] >= 0)
+            reinterpret_cast<float4 *>(out + ((int64_t)(t0 + i0 + i) * c.Hkv + h) * D)[col] = f;
+    }
 }
 
 // ---------------------------------------------------------------------------
-// Eviction.  One CTA per (sequence, KV head).  The row's weights become ordered integer
-// keys in shared memory; a radix selection (four passes of 8 bits, counts in shared memory)
-// finds the key of the last page that stays; then one pass over the row, in order, gives
-// every page its place: the pages that stay first, the dropped ones behind them.  Integer
-// counts only: the result does not depend on timing.  All of the row is in shared memory
-// before anything is written, so the outputs may be the inputs.
+// Eviction.  One CTA per (sequence, KV head).  The row's weights become ordered integer keys in
+// shared memory; the key of the last page that stays is found from the top, two bits a step: the
+// warps count the keys at or above three candidates (no histogram: equal weights, which are
+// common, would meet in one counter).  Then each warp places its stretch of the row: a page's
+// place among those that stay follows from how many before it are larger or must stay, and how
+// many are equal.  Counts only: the result does not depend on timing.  All of the row is in
+// shared memory before anything is written, so the outputs may be the inputs.  Bound by latency
+// (few rows) or by the 24 bytes a page.
 // ---------------------------------------------------------------------------
-constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
+constexpr int EV_MAX_WARPS = 32;
 
 struct EvictParams {
     const int32_t *table, *base, *held;
@@ -299,12 +343,13 @@ __device__ __forceinline__ int pages_in_use(int held, int P, int NB, bool &bad) 
     return bad ? 0 : (held + P - 1) / P;
 }
 
-__global__ void __launch_bounds__(EV_THREADS) kv_pages_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(EV_MAX_WARPS * 32) kv_pages_evict_kernel(const EvictParams p) {
     extern __shared__ uint32_t ev_smem[];
-    __shared__ int hist[256], warp_a[EV_WARPS], warp_b[EV_WARPS], pick[2];
+    __shared__ int count[2][3][EV_MAX_WARPS], sure[EV_MAX_WARPS], ties[EV_MAX_WARPS];
     uint32_t *key = ev_smem;
     int32_t *tab = reinterpret_cast<int32_t *>(ev_smem + p.NB), *bas = tab + p.NB;
     const int bh = blockIdx.x, b = bh / p.Hkv, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int threads = blockDim.x, warps = threads >> 5;
     const int64_t row = (int64_t)bh * p.NB;
     pdl_launch_dependents();
     pdl_wait();
@@ -315,96 +360,86 @@ __global__ void __launch_bounds__(EV_THREADS) kv_pages_evict_kernel(const EvictP
     const bool evict = n > p.budget;
     if (tid == 0 && bh % p.Hkv == 0 && p.write_held) p.held_out[b] = evict ? held - (n - p.budget) * p.P : held;
     // the tail, and whole rows that lose nothing, are copied
-    for (int i = (evict ? n : 0) + tid; i < p.NB; i += EV_THREADS) {
+    for (int i = (evict ? n : 0) + tid; i < p.NB; i += threads) {
         if (p.table_out != p.table) p.table_out[row + i] = p.table[row + i];
         if (p.base_out != p.base) p.base_out[row + i] = p.base[row + i];
         if (p.w_out != p.w) p.w_out[row + i] = p.w[row + i];
     }
     if (!evict) return;
-    for (int i = tid; i < n; i += EV_THREADS) {
+#pragma unroll 4
+    for (int i = tid; i < n; i += threads) {
         key[i] = order_key(p.w[row + i]);
         tab[i] = p.table[row + i];
         bas[i] = p.base[row + i];
     }
-    // the key of rank `want` among the middle pages, digit by digit from the top
-    const int m0 = p.first, m1 = n - p.last;
-    int want = p.budget - p.first - p.last;   // middle pages that stay; 0: none
-    uint32_t prefix = 0;
-    if (want > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += EV_THREADS) hist[i] = 0;
-            __syncthreads();
-            for (int i = m0 + tid; i < m1; i += EV_THREADS)
-                if (shift == 24 || (key[i] >> (shift + 8)) == (prefix >> (shift + 8)))
-                    atomicAdd(&hist[(key[i] >> shift) & 255], 1);
-            __syncthreads();
-            if (wid == 0) {   // counts from the top: lane l owns digits 255 - 8l .. 248 - 8l
-                int c[8], sum = 0;
-#pragma unroll
-                for (int i = 0; i < 8; i++) sum += c[i] = hist[255 - 8 * lane - i];
-                int inc = sum;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int t = __shfl_up_sync(0xffffffffu, inc, d);
-                    if (lane >= d) inc += t;
-                }
-                int above = inc - sum;
-                if (above < want && inc >= want) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        if (above < want && above + c[i] >= want) {
-                            pick[0] = 255 - 8 * lane - i;
-                            pick[1] = want - above;
-                            break;
-                        }
-                        above += c[i];
-                    }
-                }
+    __syncthreads();
+    // ---- the want-th largest key among the middle pages
+    const int m0 = p.first, m1 = n - p.last, want = p.budget - p.first - p.last;
+    uint32_t cut = 0;   // the largest key with at least `want` keys at or above it
+    if (want > 0)
+        for (int shift = 30, step = 0; shift >= 0; shift -= 2, step ^= 1) {
+            int c1 = 0, c2 = 0, c3 = 0;
+            const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
+            for (int i = m0 + tid; i < m1; i += threads) {
+                const uint32_t k = key[i];
+                c1 += k >= t1;
+                c2 += k >= t2;
+                c3 += k >= t3;
             }
-            __syncthreads();
-            prefix |= (uint32_t)pick[0] << shift;
-            want = pick[1];   // of the pages that share this prefix, so many stay
+            c1 = __reduce_add_sync(0xffffffffu, c1);
+            c2 = __reduce_add_sync(0xffffffffu, c2);
+            c3 = __reduce_add_sync(0xffffffffu, c3);
+            if (lane == 0) {
+                count[step][0][wid] = c1;
+                count[step][1][wid] = c2;
+                count[step][2][wid] = c3;
+            }
+            __syncthreads();   // (the counts of the step before are read by all by then: two sets)
+            const bool in = lane < warps;
+            c1 = __reduce_add_sync(0xffffffffu, in ? count[step][0][lane] : 0);
+            c2 = __reduce_add_sync(0xffffffffu, in ? count[step][1][lane] : 0);
+            c3 = __reduce_add_sync(0xffffffffu, in ? count[step][2][lane] : 0);
+            cut = c3 >= want ? t3 : c2 >= want ? t2 : c1 >= want ? t1 : cut;
         }
-    } else {
-        __syncthreads();
+    // ---- places.  Warp w has the pages from w * span on.
+    const int span = ((n + warps - 1) / warps + 31) & ~31, i0 = wid * span, i1 = min(n, i0 + span);
+    auto kind = [&](int i) {   // 2: stays for sure, 1: equal to the cut, 0: dropped
+        const uint32_t k = key[i];
+        return i < m0 || i >= m1 ? 2 : want <= 0 ? 0 : k > cut ? 2 : k == cut ? 1 : 0;
+    };
+    int larger = 0, sures = 0, equal = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const int k = kind(i);
+        sures += k == 2;
+        equal += k == 1;
     }
-    const bool some = p.budget > p.first + p.last;
-    // places, in order: EV_THREADS pages at a time with running totals
-    int ties = 0, kept = 0;   // equal keys seen, pages kept, before this chunk
-    for (int i0 = 0; i0 < n; i0 += EV_THREADS) {
-        const int i = i0 + tid;
-        const bool in = i < n, mid = in && i >= m0 && i < m1;
-        const uint32_t k = in ? key[i] : 0u;
-        const bool tie = some && mid && k == prefix;
-        const uint32_t tmask = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) warp_a[wid] = __popc(tmask);
-        __syncthreads();
-        int before = ties, all = 0;
-        for (int w = 0; w < EV_WARPS; w++) {
-            if (w < wid) before += warp_a[w];
-            all += warp_a[w];
-        }
-        ties += all;
-        before += __popc(tmask & ((1u << lane) - 1u));
-        const bool keep = in && (!mid || (some && (k > prefix || (tie && before < want))));
-        const uint32_t kmask = __ballot_sync(0xffffffffu, keep);
-        if (lane == 0) warp_b[wid] = __popc(kmask);
-        __syncthreads();
-        int place = kept, total = 0;
-        for (int w = 0; w < EV_WARPS; w++) {
-            if (w < wid) place += warp_b[w];
-            total += warp_b[w];
-        }
-        place += __popc(kmask & ((1u << lane) - 1u));   // pages kept before this one
-        kept += total;
-        if (in) {
-            const int at = keep ? place : p.budget + (i - place);
+    sures = __reduce_add_sync(0xffffffffu, sures);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+        sure[wid] = sures;
+        ties[wid] = equal;
+    }
+    __syncthreads();
+    const int s_all = __reduce_add_sync(0xffffffffu, lane < warps ? sure[lane] : 0);
+    larger = __reduce_add_sync(0xffffffffu, lane < wid ? sure[lane] : 0);    // before this warp's stretch
+    equal = __reduce_add_sync(0xffffffffu, lane < wid ? ties[lane] : 0);
+    const int room = p.budget - s_all;   // of the equal ones, so many stay: the first
+    for (int c0 = i0; c0 < i1; c0 += 32) {
+        const int i = c0 + lane;
+        const int k = i < i1 ? kind(i) : 0;
+        const uint32_t ms = __ballot_sync(0xffffffffu, k == 2), mt = __ballot_sync(0xffffffffu, k == 1);
+        const uint32_t below = (1u << lane) - 1u;
+        const int eq = equal + __popc(mt & below), before = larger + __popc(ms & below) + min(eq, room);
+        const bool keep = k == 2 || (k == 1 && eq < room);
+        if (i < i1) {
+            const int at = keep ? before : p.budget + (i - before);
             p.table_out[row + at] = tab[i];
             p.base_out[row + at] = bas[i];
-            const uint32_t fb = k & 0x80000000u ? k & 0x7fffffffu : ~k;
+            const uint32_t q = key[i], fb = q & 0x80000000u ? q & 0x7fffffffu : ~q;
             p.w_out[row + at] = keep ? __uint_as_float(fb) : 0.0f;
         }
-        __syncthreads();   // warp_a is rewritten by the next chunk
+        larger += __popc(ms);
+        equal += __popc(mt);
     }
 }
 
@@ -505,13 +540,16 @@ gq_status launch_kv_pages_read(const gq_kv_pages &c, const int32_t *start, const
     p.T = (int)T;
     p.max_n = (int)max_n;
     p.tiles = (int)((max_n + RD_TOKENS - 1) / RD_TOKENS);
-    const int64_t grid = c.B * p.tiles;
+    p.heads = (int)((c.Hkv + RD_THREADS / 32 - 1) / (RD_THREADS / 32));
+    const int64_t grid = c.B * p.tiles * p.heads;
     if (grid > INT32_MAX) return fail(GQ_ERR_INVALID_ARG, "read grid too large");
-    int logP = log2_of(c.P), logQ = log2_of(c.D / 4);
-    void *args[] = {(void *)&p, (void *)&logP, (void *)&logQ};
-    return launch_pdl(c.kind == GQ_KV_I8 ? (const void *)kv_pages_read_kernel<GQ_KV_I8>
-                                         : (const void *)kv_pages_read_kernel<GQ_KV_E4M3>,
-                      dim3((unsigned)grid, 2), dim3(RD_THREADS), 0, s, args, "paged read launch");
+    int logP = log2_of(c.P);
+    void *args[] = {(void *)&p, (void *)&logP};
+    const void *fn = c.kind == GQ_KV_I8
+                         ? (c.D == 64 ? (const void *)kv_pages_read_kernel<GQ_KV_I8, 64> : (const void *)kv_pages_read_kernel<GQ_KV_I8, 128>)
+                         : (c.D == 64 ? (const void *)kv_pages_read_kernel<GQ_KV_E4M3, 64>
+                                      : (const void *)kv_pages_read_kernel<GQ_KV_E4M3, 128>);
+    return launch_pdl(fn, dim3((unsigned)grid, 2), dim3(RD_THREADS), 0, s, args, "paged read launch");
 }
 
 gq_status launch_kv_pages_evict(const gq_kv_pages &c, const float *w, int64_t budget, int64_t keep_first,
@@ -537,6 +575,8 @@ gq_status launch_kv_pages_evict(const gq_kv_pages &c, const float *w, int64_t bu
     // the rows of one sequence all read held[b]: in place it is written by a launch of its own
     p.write_held = held_out != c.held;
     const size_t smem = (size_t)c.NB * 12;
+    // eight pages a thread; many small CTAs hide each other's latency (2,048 pages: 24 KB, 8 CTAs an SM)
+    const unsigned threads = (unsigned)std::min<int64_t>(EV_MAX_WARPS * 32, std::max<int64_t>(64, (c.NB / 8 + 31) / 32 * 32));
     static std::atomic<bool> smem_set[64];
     int dev = 0;
     KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
@@ -548,7 +588,7 @@ gq_status launch_kv_pages_evict(const gq_kv_pages &c, const float *w, int64_t bu
         smem_set[dev].store(true, std::memory_order_release);
     }
     void *args[] = {(void *)&p};
-    KV_TRY(launch_pdl((const void *)kv_pages_evict_kernel, dim3((unsigned)(c.B * c.Hkv)), dim3(EV_THREADS), smem, s, args,
+    KV_TRY(launch_pdl((const void *)kv_pages_evict_kernel, dim3((unsigned)(c.B * c.Hkv)), dim3(threads), smem, s, args,
                       "eviction launch"));
     if (!p.write_held) {
         const int32_t *held = c.held;
