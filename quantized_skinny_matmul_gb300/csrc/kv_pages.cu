@@ -313,9 +313,10 @@ __global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadPar
 
 // ---------------------------------------------------------------------------
 // Eviction.  One CTA per (sequence, KV head).  The row's weights become ordered integer keys in
-// shared memory; the key of the last page that stays is found from the top, two bits a step: the
-// warps count the keys at or above three candidates (no histogram: equal weights, which are
-// common, would meet in one counter).  Then each warp places its stretch of the row: a page's
+// shared memory; the key of the last page that stays is found from the top, a byte a pass: counts
+// of the byte's values among the keys that share the bytes before, which every warp then reads for
+// itself (one barrier a pass; 16 passes of 2 bits by comparing, without counters in shared memory,
+// cost 2.5 times the instructions).  Then each warp places its stretch of the row: a page's
 // place among those that stay follows from how many before it are larger or must stay, and how
 // many are equal.  Counts only: the result does not depend on timing.  All of the row is in
 // shared memory before anything is written, so the outputs may be the inputs.  Bound by latency
@@ -345,7 +346,8 @@ __device__ __forceinline__ int pages_in_use(int held, int P, int NB, bool &bad) 
 
 __global__ void __launch_bounds__(EV_MAX_WARPS * 32) kv_pages_evict_kernel(const EvictParams p) {
     extern __shared__ uint32_t ev_smem[];
-    __shared__ int count[2][3][EV_MAX_WARPS], sure[EV_MAX_WARPS], ties[EV_MAX_WARPS];
+    __shared__ __align__(16) int hist[4][256];
+    __shared__ int sure[EV_MAX_WARPS], ties[EV_MAX_WARPS];
     uint32_t *key = ev_smem;
     int32_t *tab = reinterpret_cast<int32_t *>(ev_smem + p.NB), *bas = tab + p.NB;
     const int bh = blockIdx.x, b = bh / p.Hkv, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(EV_MAX_WARPS * 32) kv_pages_evict_kernel(const
         if (p.w_out != p.w) p.w_out[row + i] = p.w[row + i];
     }
     if (!evict) return;
+    for (int i = tid; i < 4 * 256; i += threads) hist[i >> 8][i & 255] = 0;
 #pragma unroll 4
     for (int i = tid; i < n; i += threads) {
         key[i] = order_key(p.w[row + i]);
@@ -375,32 +378,45 @@ __global__ void __launch_bounds__(EV_MAX_WARPS * 32) kv_pages_evict_kernel(const
     __syncthreads();
     // ---- the want-th largest key among the middle pages
     const int m0 = p.first, m1 = n - p.last, want = p.budget - p.first - p.last;
-    uint32_t cut = 0;   // the largest key with at least `want` keys at or above it
-    if (want > 0)
-        for (int shift = 30, step = 0; shift >= 0; shift -= 2, step ^= 1) {
-            int c1 = 0, c2 = 0, c3 = 0;
-            const uint32_t t1 = cut | (1u << shift), t2 = cut | (2u << shift), t3 = cut | (3u << shift);
+    uint32_t cut = 0;
+    if (want > 0) {
+        int left = want;   // among the keys that share the bytes found so far
+#pragma unroll 1
+        for (int pass = 0; pass < 4; pass++) {
+            const int shift = 24 - 8 * pass;
             for (int i = m0 + tid; i < m1; i += threads) {
                 const uint32_t k = key[i];
-                c1 += k >= t1;
-                c2 += k >= t2;
-                c3 += k >= t3;
+                if (pass == 0 || (k ^ cut) >> (shift + 8) == 0) atomicAdd(&hist[pass][(k >> shift) & 255u], 1);
             }
-            c1 = __reduce_add_sync(0xffffffffu, c1);
-            c2 = __reduce_add_sync(0xffffffffu, c2);
-            c3 = __reduce_add_sync(0xffffffffu, c3);
-            if (lane == 0) {
-                count[step][0][wid] = c1;
-                count[step][1][wid] = c2;
-                count[step][2][wid] = c3;
+            __syncthreads();
+            // lane l has the counts of the bytes 255 - 8 l .. 248 - 8 l, from the top
+            const int4 lo = *reinterpret_cast<const int4 *>(&hist[pass][248 - 8 * lane]);
+            const int4 hi = *reinterpret_cast<const int4 *>(&hist[pass][252 - 8 * lane]);
+            const int c[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum += c[i];
+            int inc = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += t;
             }
-            __syncthreads();   // (the counts of the step before are read by all by then: two sets)
-            const bool in = lane < warps;
-            c1 = __reduce_add_sync(0xffffffffu, in ? count[step][0][lane] : 0);
-            c2 = __reduce_add_sync(0xffffffffu, in ? count[step][1][lane] : 0);
-            c3 = __reduce_add_sync(0xffffffffu, in ? count[step][2][lane] : 0);
-            cut = c3 >= want ? t3 : c2 >= want ? t2 : c1 >= want ? t1 : cut;
+            int above = inc - sum, digit = 0, rest = 0;
+            const bool here = above < left && inc >= left;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                if (above < left && above + c[i] >= left) {
+                    digit = 255 - 8 * lane - i;
+                    rest = left - above;
+                }
+                above += c[i];
+            }
+            const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+            cut |= (uint32_t)__shfl_sync(0xffffffffu, digit, from) << shift;
+            left = __shfl_sync(0xffffffffu, rest, from);
         }
+    }
     // ---- places.  Warp w has the pages from w * span on.
     const int span = ((n + warps - 1) / warps + 31) & ~31, i0 = wid * span, i1 = min(n, i0 + span);
     auto kind = [&](int i) {   // 2: stays for sure, 1: equal to the cut, 0: dropped
