@@ -769,7 +769,9 @@ def kv_pages_append(cache: KVPages, k, v, cu, max_n: int) -> None:
 
 def kv_pages_read(cache: KVPages, start, cu, T: int, max_n: int):
     """Slots start[b] .. of each sequence as f32: (k, v), each [T, Hkv, D], packed by cu."""
-    k, v = cache.ks.new_empty((2, T, cache.Hkv, cache.D)).unbind(0)
+    import torch
+    shape = (T, cache.Hkv, cache.D)
+    k, v = (torch.empty(shape, dtype=torch.float32, device=cache.ks.device) for _ in range(2))
     _check(lib().gq_kv_pages_read(cache.by_ref, _lengths(start, cache.B, "start"), _lengths(cu, cache.B + 1), T, max_n,
                                   k.data_ptr(), v.data_ptr(), _current_stream()), "gq_kv_pages_read")
     return k, v
@@ -788,14 +790,16 @@ def attn_pages(cache: KVPages, q, cu, max_n: int, scores: AttnScores, weights=No
         if t is not None and t.shape[0] != T:
             raise ValueError(f"{name}: expected {T} values, got {t.shape[0]}")
     if out is None:
-        out, ldo = cache.ks.new_empty((T, Hq, cache.D)), Hq * cache.D
+        import torch
+        out, ldo = torch.empty((T, Hq, cache.D), dtype=torch.float32, device=cache.ks.device), Hq * cache.D
     else:
         To, Ho, ldo = _packed(out, cache.D, "out")
         if To != T or Ho != Hq:
             raise ValueError(f"out: expected {T} rows of {Hq} heads, got {To} and {Ho}")
     new = w_in = w_out = None
     if weights is not None:
-        w_in, new = _page_weights(cache, weights), weights.new_empty(weights.shape)
+        import torch
+        w_in, new = _page_weights(cache, weights), torch.empty_like(weights)
         w_out = new.data_ptr()
     _check(lib().gq_attn_pages(cache.by_ref, scores.by_ref, q.data_ptr(), ldq, _lengths(cu, cache.B + 1), T, max_n, Hq,
                                out.data_ptr(), ldo, w_in, w_out, decay, _current_stream()), "gq_attn_pages")
@@ -805,8 +809,8 @@ def attn_pages(cache: KVPages, q, cu, max_n: int, scores: AttnScores, weights=No
 def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, keep_last: int = 1):
     """Drop the pages that gathered least until `budget` are left: (table, base, weights, held), new tensors."""
     w = _page_weights(cache, weights)
-    table, base = cache.table.new_empty(cache.table.shape), cache.base.new_empty(cache.base.shape)
-    new, held = weights.new_empty(weights.shape), cache.held.new_empty(cache.held.shape)
+    from torch import empty_like
+    table, base, new, held = empty_like(cache.table), empty_like(cache.base), empty_like(weights), empty_like(cache.held)
     _check(lib().gq_kv_pages_evict(cache.by_ref, w, budget, keep_first, keep_last, table.data_ptr(), base.data_ptr(),
                                    new.data_ptr(), held.data_ptr(), _current_stream()), "gq_kv_pages_evict")
     return table, base, new, held
