@@ -73,7 +73,7 @@ enum : int {
     META_FULL = 0, META_EMPTY = META_FULL + METAS,
     RAWK_FULL = META_EMPTY + METAS, RAWK_EMPTY, RAWV_FULL, RAWV_EMPTY,
     K_FULL, V_FULL, V_EMPTY,   // (K is free once the scores of the block's last tile are there)
-    Q_FULL, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 2,
+    Q_FULL, S_FULL = Q_FULL + 2, P_FULL = S_FULL + 2, O_FULL = P_FULL + 4,   // P: [half][tile]; a half's phases pass one by one
     TILE_SYNC = O_FULL + 2, ALL_DONE = TILE_SYNC + 2, NUM_BARS
 };
 
@@ -242,6 +242,13 @@ struct Waiter {
     __device__ __forceinline__ void arrive(int bar) { mbar_arrive(smem_addr(bars + bar)); }
 };
 
+// The bits lo .. hi of 16 (none where hi < lo).
+__device__ __forceinline__ uint32_t bits16(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 15);
+    return hi < lo ? 0u : (2u << hi) - (1u << lo);
+}
+
 __device__ __forceinline__ int exponent_of(float x) {   // x < 2^e, clamped to [-100, 126]
     return min(max((int)((__float_as_uint(x) >> 23) & 255u) - 126, -100), 126);
 }
@@ -307,14 +314,15 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
     const int per = c.P / 16;                // groups per page
     int nmeta = 0, nk = 0, nraw = 0;   // blocks published, copies of keys and of values issued
 
-    auto publish = [&](const Item &x, int flags, int slot, int live, int lost, float ks, float vs, int base) {
+    // (the values of a block's groups are in the eight lanes from 8 q on)
+    auto publish = [&](const Item &x, int flags, int slot, int live, int lost, int q, float ks, float vs, int base) {
         const int st = nmeta % METAS;
         if (nmeta >= METAS && !wait.warp(META_EMPTY + st, nmeta / METAS - 1)) return;
         BlockMeta &d = sm.meta[st];
-        if (lane < GROUPS) {
-            d.ks[lane] = ks;
-            d.vs[lane] = vs;
-            d.base[lane] = base;
+        if (lane >> 3 == q) {
+            d.ks[lane & 7] = ks;
+            d.vs[lane & 7] = vs;
+            d.base[lane & 7] = base;
         }
         if (lane == 0) {
             d.flags = flags;
@@ -337,7 +345,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         item = __shfl_sync(0xffffffffu, item, 0);
         Item x{0, 0, 0, {0, 0, 0, 0, false}};
         if (item >= items) {
-            publish(x, F_EXIT, 0, 0, 0, 0.0f, 0.0f, 0);
+            publish(x, F_EXIT, 0, 0, 0, 0, 0.0f, 0.0f, 0);
             break;
         }
         const int2 e = __ldcg(plan.list + item / c.Hkv);
@@ -345,6 +353,10 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         x.h = item % c.Hkv;
         x.pair = e.y;
         x.s = attn_step(p, x.b);
+        // the queries, on their way to L2 while the item before is finished (read from there, they hold
+        // the start of an item up by 10 us less than from device memory)
+        for (int i = x.pair * 2 * BR / p.G + lane; i < x.s.n && i * p.G < (x.pair + 1) * 2 * BR; i += 32)
+            bulk_prefetch_l2(p.q + (int64_t)(x.s.t0 + i) * p.ldq + (int64_t)x.h * p.G * D, (uint32_t)(p.G * D * 4));
         const int end = x.s.held + x.s.n;    // slots in use (0 for an unusable sequence)
         // what the rows of each tile can see: positions lo .. hi, and those below pre
         int lo[2] = {0, 0}, hi[2] = {-1, -1}, pre[2] = {0, 0}, lomin = 0x7fffffff, premax = 0, imax = 0;
@@ -384,67 +396,91 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         }
         const int blocks = bp + b1 - b0;
         const int64_t trow = ((int64_t)x.b * c.Hkv + x.h) * c.NB;
+        // Blocks are looked up four at a time, a lane per group of 16 tokens; the pages of the next four,
+        // and then their scales, are under way while these are worked on (one by one, these dependent
+        // loads were what a block took longest).
+        struct Look {
+            int page, base, live;   // page -1: none, -2: not usable
+            float ks, vs;
+        };
+        auto slot_of = [&](int i) { return (i < bp ? i : b0 + i - bp) * BT; };
+        auto pages = [&](int i0, Look &l) {
+            const int i = i0 + (lane >> 3), at = slot_of(i) + 16 * (lane & 7);
+            l.page = -1;
+            l.base = 0x7f000000;   // a position nobody sees
+            l.live = i < blocks ? min(BT, end - slot_of(i)) : 0;
+            if (16 * (lane & 7) < l.live) {
+                l.page = __ldg(c.table + trow + (at >> p.lgP));
+                l.base = __ldg(c.base + trow + (at >> p.lgP)) + (at & (c.P - 1));
+            }
+        };
+        auto scales = [&](Look &l) {
+            l.ks = l.vs = 0.0f;
+            if (l.page == -1) return;
+            if ((unsigned)l.page >= (unsigned)c.pages) {
+                atomicOr(c.status, STATUS_RANGE);
+                l.page = -2;
+                l.base = 0x7f000000;
+            } else {
+                l.ks = __ldg(c.ks + l.page);
+                l.vs = __ldg(c.vs + l.page);
+            }
+        };
+        Look now, next, later;
+        pages(0, now);
+        pages(4, next);
+        scales(now);
         // A block that some row sees is sent once the next one is known, so that the last can say
-        // so.  The values of the one that waits (w...): lane g holds those of group g.
-        int wflags = 0, wslot = 0, wlive = 0, wlost = 0, wbase = 0, wpage = -1;
-        float wks = 0.0f, wvs = 0.0f;
+        // so.  w...: the one that waits, its groups' values in the lanes from 8 wq on.
+        int wflags = 0, wslot = 0, wlive = 0, wlost = 0, wq = 0;
+        Look w = now;
         bool first = true;
         for (int i = 0; i <= blocks && !wait.failed; i++) {
             const bool done = i == blocks;
-            float ks = 0.0f, vs = 0.0f;
-            int base = 0x7f000000, page = -1, active = 0, slot = 0, live = 0, lost = 0;   // a position nobody sees
+            const int q = i & 3;
+            if (q == 0) {
+                if (i > 0) now = next;
+                if (i > 0) next = later;
+                scales(next);
+                pages(i + 8, later);
+            }
+            int active = 0, lost = 0;
             if (!done) {
-                slot = (i < bp ? i : b0 + i - bp) * BT;
-                live = min(BT, end - slot);
-                bool bad = false;
-                if (lane < GROUPS && 16 * lane < live) {
-                    const int at = slot + 16 * lane, j = at >> p.lgP;
-                    page = __ldg(c.table + trow + j);
-                    bad = (unsigned)page >= (unsigned)c.pages;
-                    if (bad) {
-                        atomicOr(c.status, STATUS_RANGE);
-                        page = -1;
-                    } else {
-                        ks = __ldg(c.ks + page);
-                        vs = __ldg(c.vs + page);
-                        base = __ldg(c.base + trow + j) + (at & (c.P - 1));
-                    }
-                }
-                lost = (int)__ballot_sync(0xffffffffu, bad);
+                lost = (int)(__ballot_sync(0xffffffffu, now.page == -2) >> (8 * q)) & 255;
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
-                    const bool see = page >= 0 && hi[t] >= 0 && ((base + 15 >= lo[t] && base <= hi[t]) || base < pre[t]);
-                    if (__any_sync(0xffffffffu, see)) active |= F_TILE0 << t;
+                    const bool see = now.page >= 0 && hi[t] >= 0 &&
+                                     ((now.base + 15 >= lo[t] && now.base <= hi[t]) || now.base < pre[t]);
+                    if ((__ballot_sync(0xffffffffu, see) >> (8 * q)) & 255u) active |= F_TILE0 << t;
                 }
                 if (!active) continue;
             }
             if (wflags || done) {   // (with no block at all: one that says only that the item is over)
-                publish(x, wflags | (first ? F_FIRST : 0) | (done ? F_LAST : 0), wslot, wlive, wlost, wks, wvs, wbase);
+                publish(x, wflags | (first ? F_FIRST : 0) | (done ? F_LAST : 0), wslot, wlive, wlost, wq, w.ks, w.vs, w.base);
                 first = false;
                 if (wflags && !wait.failed) {
-                    const bool mine = lane < GROUPS && wpage >= 0 && lane % per == 0;
+                    const bool mine = lane >> 3 == wq && w.page >= 0 && (lane & 7) % per == 0;
                     const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * c.P * D);
-                    const int row = (int)((int64_t)wpage * c.P * D / 128);
+                    const int row = (int)((int64_t)w.page * c.P * D / 128);
+                    const uint32_t to = (uint32_t)((lane & 7) * 16 * D);
                     if (nraw > 0 && !wait.warp(RAWK_EMPTY, nraw - 1)) break;
                     if (lane == 0) mbar_arrive_expect_tx(smem_addr(sm.bars + RAWK_FULL), bytes);
                     __syncwarp();
-                    if (mine) tma_rows(rawk + lane * 16 * D, &kmap, row, smem_addr(sm.bars + RAWK_FULL), policy);
+                    if (mine) tma_rows(rawk + to, &kmap, row, smem_addr(sm.bars + RAWK_FULL), policy);
                     nk++;
                     if (nraw > 0 && !wait.warp(RAWV_EMPTY, nraw - 1)) break;
                     if (lane == 0) mbar_arrive_expect_tx(smem_addr(sm.bars + RAWV_FULL), bytes);
                     __syncwarp();
-                    if (mine) tma_rows(rawv + lane * 16 * D, &vmap, row, smem_addr(sm.bars + RAWV_FULL), policy);
+                    if (mine) tma_rows(rawv + to, &vmap, row, smem_addr(sm.bars + RAWV_FULL), policy);
                     nraw++;
                 }
             }
             wflags = active;
-            wslot = slot;
-            wlive = live;
+            wslot = slot_of(i);
+            wlive = min(BT, end - wslot);
             wlost = lost;
-            wks = ks;
-            wvs = vs;
-            wbase = base;
-            wpage = page;
+            wq = q;
+            w = now;
         }
     }
     // stay until every copy issued has landed
@@ -453,83 +489,75 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
 }
 
 // ---- warp 13: the products ------------------------------------------------------------------
+// One thread.  Few MMAs can be queued, so what it does between two groups of them is time that the
+// tensor pipe stands still: no votes, and the waits that may be over early come early.
 template <int D>
-__device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem, int lane) {
+__device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem) {
     using L = TileLayout<D>;
     constexpr uint32_t idq = idesc_f16(BR, BT, false), idp = idesc_f16(BR, D, true);
-    const uint32_t qa = smem_addr(smem + L::q), ka = smem_addr(smem + L::k), va = smem_addr(smem + L::v);
-    int nk = 0, nv = 0, nitem = 0, np0 = 0, np1 = 0, no0 = 0, no1 = 0;   // blocks, products with V, items, weights of each tile, those of the item
+    const uint64_t qd0 = desc_sw128(smem_addr(smem + L::q), 16), kd = desc_sw128(smem_addr(smem + L::k), 16);
+    const uint64_t vd = desc_sw128(smem_addr(smem + L::v), L::ATOM);
+    int nk = 0, nv = 0, nitem = 0, np[2] = {0, 0}, no[2] = {0, 0};   // blocks, products with V, items, weights of each tile, those of the item
     int prev = 0, started = 0, fresh_q = 0;    // tiles whose weights wait for V; tiles with a product in this item; queries not yet waited for
 
-    auto commit = [&](int bar) {
-        if (lane == 0) mma_commit(smem_addr(sm.bars + bar));
-        __syncwarp();
-    };
+    auto commit = [&](int bar) { mma_commit(smem_addr(sm.bars + bar)); };
     // P_t V of the block before; the item's first one, and the first after a flush, overwrites O_t
     auto pv = [&](int t) {
-        const int in_item = t == 0 ? no0++ : no1++;
-        if (t == 0) wait.warp(P_FULL, np0++);
-        else wait.warp(P_FULL + 1, np1++);
-        if (wait.failed) return;
-        tc_after();
-        if (lane == 0) {
-            const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
-            const uint64_t vd = desc_sw128(va, L::ATOM);
-            const uint32_t keep = in_item % FLUSH ? 1u : 0u;
+        const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
+#pragma unroll
+        for (int half = 0; half < 2; half++) {   // 64 tokens' weights at a time, as they come
+            if (!wait(P_FULL + 2 * half + t, np[t])) return;
+            tc_after();
+            const uint32_t keep = no[t] % FLUSH || half ? 1u : 0u;
 #pragma unroll
             for (int term = 0; term < 2; term++)
 #pragma unroll
-                for (int kk = 0; kk < BT / 16; kk++)
-                    mma_ts(o, s + 32 * (kk >> 1) + 16 * term + 8 * (kk & 1), vd + (uint64_t)(2048 * kk >> 4), idp, term | kk ? 1u : keep);
+                for (int kk = 4 * half; kk < 4 * half + 4; kk++)
+                    mma_ts(o, s + 32 * (kk >> 1) + 16 * term + 8 * (kk & 1), vd + (uint64_t)(2048 * kk >> 4), idp,
+                           term || kk > 4 * half ? 1u : keep);
         }
-        __syncwarp();
+        np[t]++;
+        no[t]++;
         started |= 1 << t;
     };
     auto qk = [&](int t) {
-        if (lane == 0) {
-            const uint64_t kd = desc_sw128(ka, 16);
 #pragma unroll
-            for (int term = 1; term >= 0; term--) {   // the small terms first: less is lost to truncation
-                const uint64_t qd = desc_sw128(qa + (2 * t + term) * L::OPERAND, 16);
+        for (int term = 1; term >= 0; term--) {   // the small terms first: less is lost to truncation
+            const uint64_t qd = qd0 + (uint64_t)((2 * t + term) * L::OPERAND >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; kk++) {
-                    const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
-                    mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term == 0 || kk ? 1u : 0u);
-                }
+            for (int kk = 0; kk < D / 16; kk++) {
+                const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
+                mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term == 0 || kk ? 1u : 0u);
             }
-            mma_commit(smem_addr(sm.bars + S_FULL + t));
         }
-        __syncwarp();
+        commit(S_FULL + t);
     };
 
     for (int i = 0;; i++) {
         const int st = i % METAS;
-        if (!wait.warp(META_FULL + st, i / METAS)) return;
+        if (!wait(META_FULL + st, i / METAS)) return;
         const int flags = sm.meta[st].flags, now = flags & (F_TILE0 | F_TILE1);
-        __syncwarp();
-        if (lane == 0) wait.arrive(META_EMPTY + st);
+        wait.arrive(META_EMPTY + st);
         if (flags & F_EXIT) return;
         if (flags & F_FIRST) {
             nitem++;
-            started = no0 = no1 = 0;
+            started = no[0] = no[1] = 0;
             fresh_q = F_TILE0 | F_TILE1;
         }
-        if (prev) wait.warp(V_FULL, nv);
+        if (prev && !wait(V_FULL, nv)) return;
         bool have_k = false;
 #pragma unroll
         for (int t = 0; t < 2; t++) {
-            if (wait.failed) return;
             if ((prev >> t) & 1) {
                 pv(t);
                 if (wait.failed) return;
                 if (t == 1 || !(prev & F_TILE1)) commit(V_EMPTY);
             }
             if ((now >> t) & 1) {
-                if (!have_k) wait.warp(K_FULL, nk);
+                if (!have_k && !wait(K_FULL, nk)) return;
                 have_k = true;
-                if ((fresh_q >> t) & 1) wait.warp(Q_FULL + t, nitem - 1);
+                if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
                 fresh_q &= ~(1 << t);
-                if (wait.failed) return;
                 tc_after();
                 qk(t);
             }
@@ -541,12 +569,11 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
             // the queries of a tile that saw nothing: every phase of a barrier is waited for
 #pragma unroll
             for (int t = 0; t < 2; t++)
-                if ((fresh_q >> t) & 1) wait.warp(Q_FULL + t, nitem - 1);
+                if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
             if (prev) {
-                wait.warp(V_FULL, nv++);
+                if (!wait(V_FULL, nv++)) return;
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
-                    if (wait.failed) return;
                     if ((prev >> t) & 1) pv(t);
                     if (wait.failed) return;
                     if ((started >> t) & 1) commit(O_FULL + t);
@@ -792,13 +819,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
 #pragma unroll
                             for (int e = 0; e < 16; e++) s[16 * g + e] -= slope * (float)abs(qpos - (base + e));
                         }
-                        if (!whole) {
+                        if (!whole) {   // bit e: the group's token e is there and seen
+                            const uint32_t see = (bits16(seelo - base, qpos - base) | bits16(firstp - base, pre - 1 - base)) &
+                                                 bits16(0, live - x - 16 * g - 1);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) {
-                                const int y = base + e;
-                                const bool see = x + 16 * g + e < live && y >= firstp && (y < pre || (y >= seelo && y <= qpos));
-                                s[16 * g + e] = see ? s[16 * g + e] : -INFINITY;
-                            }
+                            for (int e = 0; e < 16; e++)
+                                if (!(see & (1u << e))) s[16 * g + e] = -INFINITY;
                         }
 #pragma unroll
                         for (int e = 0; e < 16; e++) mx[e & 3] = fmaxf(mx[e & 3], s[16 * g + e]);
@@ -909,11 +935,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             for (int x = 0; x < BT; x += 64) {
                 weigh(x, s[0], s[1]);
                 weigh(x + 32, s[1], s[0]);
+                // half of the weights are there: their product may begin
+                tm_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) wait.arrive(P_FULL + (x >> 5) + t);   // x = 0: the first half, 64: the second
             }
-            tm_wait_st();
-            tc_before();
-            __syncwarp();
-            if (lane == 0) wait.arrive(P_FULL + t);
         }
         if (flags & F_LAST) {
             const float l = lrow;
@@ -998,6 +1025,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             init(Q_FULL + t, 4);
             init(S_FULL + t, 1);
             init(P_FULL + t, 4);
+            init(P_FULL + 2 + t, 4);
             init(O_FULL + t, 1);
             init(TILE_SYNC + t, 4);
         }
@@ -1020,11 +1048,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         regs_dec<REGS_REST>();
         if (warp == 12) lead_role<KIND, D>(p, plan, kmap, vmap, smem, sm, wait, lane);
         if (warp == 13) {
-            mma_role<D>(smem, sm, wait, tmem, lane);
-            // the products issued have completed before shared and tensor memory are given up
-            if (lane == 0) mma_commit(smem_addr(sm.bars + ALL_DONE));
+            if (lane == 0) {
+                mma_role<D>(smem, sm, wait, tmem);
+                // the products issued have completed before shared and tensor memory are given up
+                mma_commit(smem_addr(sm.bars + ALL_DONE));
+                mbar_wait(smem_addr(sm.bars + ALL_DONE), 0u, c.status);
+            }
             __syncwarp();
-            mbar_wait(smem_addr(sm.bars + ALL_DONE), 0u, c.status);
         }
     } else if (warp >= 8) {
         regs_dec<REGS_REST>();
