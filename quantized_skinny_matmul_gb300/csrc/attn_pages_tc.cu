@@ -160,6 +160,18 @@ __device__ __forceinline__ void tm_wait(float *v) {
                    "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                    "+f"(v[30]), "+f"(v[31])::"memory");
 }
+__device__ __forceinline__ void tm_ld16(uint32_t a, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_wait16(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])::"memory");
+}
 __device__ __forceinline__ void tm_st32(uint32_t a, const float *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -426,23 +438,24 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
                 l.vs = __ldg(c.vs + l.page);
             }
         };
-        Look now, next, later;
-        pages(0, now);
-        pages(4, next);
-        scales(now);
+        Look now{-1, 0, 0, 0.0f, 0.0f}, next = now, later = now;
         // A block that some row sees is sent once the next one is known, so that the last can say
         // so.  w...: the one that waits, its groups' values in the lanes from 8 wq on.
         int wflags = 0, wslot = 0, wlive = 0, wlost = 0, wq = 0;
         Look w = now;
         bool first = true;
-        for (int i = 0; i <= blocks && !wait.failed; i++) {
+        for (int i = -8; i <= blocks && !wait.failed; i++) {
             const bool done = i == blocks;
             const int q = i & 3;
             if (q == 0) {
-                if (i > 0) now = next;
-                if (i > 0) next = later;
+                now = next;
+                next = later;
                 scales(next);
                 pages(i + 8, later);
+            }
+            if (i < 0) {
+                i += 3;
+                continue;
             }
             int active = 0, lost = 0;
             if (!done) {
@@ -497,91 +510,87 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
     constexpr uint32_t idq = idesc_f16(BR, BT, false), idp = idesc_f16(BR, D, true);
     const uint64_t qd0 = desc_sw128(smem_addr(smem + L::q), 16), kd = desc_sw128(smem_addr(smem + L::k), 16);
     const uint64_t vd = desc_sw128(smem_addr(smem + L::v), L::ATOM);
-    int nk = 0, nv = 0, nitem = 0, np[2] = {0, 0}, no[2] = {0, 0};   // blocks, products with V, items, weights of each tile, those of the item
+    // blocks, products with V, items; of tile 0 in the low half of a word and tile 1 in the high half:
+    // weights multiplied, and those of the item
+    int nk = 0, nv = 0, nitem = 0;
+    uint32_t np = 0, no = 0;
     int prev = 0, started = 0, fresh_q = 0;    // tiles whose weights wait for V; tiles with a product in this item; queries not yet waited for
 
     auto commit = [&](int bar) { mma_commit(smem_addr(sm.bars + bar)); };
-    // P_t V of the block before; the item's first one, and the first after a flush, overwrites O_t
-    auto pv = [&](int t) {
-        const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
-#pragma unroll
-        for (int half = 0; half < 2; half++) {   // 64 tokens' weights at a time, as they come
-            if (!wait(P_FULL + 2 * half + t, np[t])) return;
-            tc_after();
-            const uint32_t keep = no[t] % FLUSH || half ? 1u : 0u;
-#pragma unroll
-            for (int term = 0; term < 2; term++)
-#pragma unroll
-                for (int kk = 4 * half; kk < 4 * half + 4; kk++)
-                    mma_ts(o, s + 32 * (kk >> 1) + 16 * term + 8 * (kk & 1), vd + (uint64_t)(2048 * kk >> 4), idp,
-                           term || kk > 4 * half ? 1u : keep);
-        }
-        np[t]++;
-        no[t]++;
-        started |= 1 << t;
-    };
-    auto qk = [&](int t) {
-#pragma unroll
-        for (int term = 1; term >= 0; term--) {   // the small terms first: less is lost to truncation
-            const uint64_t qd = qd0 + (uint64_t)((2 * t + term) * L::OPERAND >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; kk++) {
-                const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
-                mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term == 0 || kk ? 1u : 0u);
-            }
-        }
-        commit(S_FULL + t);
-    };
-
     for (int i = 0;; i++) {
         const int st = i % METAS;
         if (!wait(META_FULL + st, i / METAS)) return;
-        const int flags = sm.meta[st].flags, now = flags & (F_TILE0 | F_TILE1);
+        const int flags = sm.meta[st].flags;
         wait.arrive(META_EMPTY + st);
         if (flags & F_EXIT) return;
         if (flags & F_FIRST) {
             nitem++;
-            started = no[0] = no[1] = 0;
+            no = 0;
+            started = 0;
             fresh_q = F_TILE0 | F_TILE1;
         }
-        if (prev && !wait(V_FULL, nv)) return;
-        bool have_k = false;
+        // A pass: for each tile P V of the block before, then Q K of this one.  After an item's last
+        // block one more, for its P V.  (One copy of the code.)
+        const int passes = flags & F_LAST ? 2 : 1;
+#pragma unroll 1
+        for (int pass = 0; pass < passes; pass++) {
+            const int now = pass == 0 ? flags & (F_TILE0 | F_TILE1) : 0;
+            if (prev && !wait(V_FULL, nv)) return;
+            bool have_k = false;
+#pragma unroll 1
+            for (int t = 0; t < 2; t++) {
+                const uint32_t one = 1u << (16 * t);
+                if ((prev >> t) & 1) {
+                    // the item's first product, and the first after a flush, overwrites O_t
+                    const uint32_t s = tmem + TM_S + 128 * t, o = tmem + TM_O + 128 * t;
+                    const int ph = (int)(np >> (16 * t)) & 0xffff;
+                    uint32_t keep = (no >> (16 * t)) % FLUSH ? 1u : 0u;   // (FLUSH divides 2^16)
+#pragma unroll 1
+                    for (int half = 0; half < 2; half++) {   // 64 tokens' weights at a time, as they come
+                        if (!wait(P_FULL + 2 * half + t, ph)) return;
+                        tc_after();
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-            if ((prev >> t) & 1) {
-                pv(t);
-                if (wait.failed) return;
-                if (t == 1 || !(prev & F_TILE1)) commit(V_EMPTY);
+                        for (int term = 0; term < 2; term++)
+#pragma unroll
+                            for (int kk = 0; kk < 4; kk++) {
+                                mma_ts(o, s + 64 * half + 32 * (kk >> 1) + 16 * term + 8 * (kk & 1),
+                                       vd + (uint64_t)((8192 * half + 2048 * kk) >> 4), idp, term || kk ? 1u : keep);
+                            }
+                        keep = 1u;
+                    }
+                    np = t ? np + one : (np & 0xffff0000u) | ((np + 1) & 0xffffu);
+                    no = t ? no + one : (no & 0xffff0000u) | ((no + 1) & 0xffffu);
+                    started |= 1 << t;
+                    if (t == 1 || !(prev & F_TILE1)) commit(V_EMPTY);
+                }
+                if (pass == 1 && ((started >> t) & 1)) commit(O_FULL + t);
+                if ((now >> t) & 1) {
+                    if (!have_k && !wait(K_FULL, nk)) return;
+                    have_k = true;
+                    if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
+                    fresh_q &= ~(1 << t);
+                    tc_after();
+                    uint64_t qd = qd0 + (uint64_t)((2 * t + 1) * L::OPERAND >> 4);
+                    // the small terms first: less is lost to truncation
+#pragma unroll
+                    for (int term = 1; term >= 0; term--) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; kk++) {
+                            const uint64_t step = (uint64_t)(((kk >> 2) * L::ATOM + (kk & 3) * 32) >> 4);
+                            mma_ss(tmem + TM_S + 128 * t, qd + step, kd + step, idq, term == 0 || kk ? 1u : 0u);
+                        }
+                        qd -= (uint64_t)(L::OPERAND >> 4);
+                    }
+                    commit(S_FULL + t);
+                }
             }
-            if ((now >> t) & 1) {
-                if (!have_k && !wait(K_FULL, nk)) return;
-                have_k = true;
-                if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
-                fresh_q &= ~(1 << t);
-                tc_after();
-                qk(t);
-            }
+            if (prev) nv++;
+            if (now) nk++;
+            prev = now;
         }
-        if (prev) nv++;
-        if (now) nk++;
-        prev = now;
-        if (flags & F_LAST) {
-            // the queries of a tile that saw nothing: every phase of a barrier is waited for
-#pragma unroll
+        if (flags & F_LAST)   // the queries of a tile that saw nothing: every phase of a barrier is waited for
             for (int t = 0; t < 2; t++)
                 if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
-            if (prev) {
-                if (!wait(V_FULL, nv++)) return;
-#pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    if ((prev >> t) & 1) pv(t);
-                    if (wait.failed) return;
-                    if ((started >> t) & 1) commit(O_FULL + t);
-                }
-                commit(V_EMPTY);
-            }
-            prev = 0;
-        }
     }
 }
 
@@ -706,7 +715,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // The query rows of this warp, each scaled by a power of two into [2^14, 2^15), as two fp16
             // terms.  A row is read by D / 4 lanes together (whole lines: a lane per row costs 32 L1
             // accesses an instruction), and the row's thread is told its power.
-            constexpr int LPR = D / 4, RPI = 32 / LPR, BATCH = 16;
+            constexpr int LPR = D / 4, RPI = 32 / LPR, BATCH = 8;
             const int64_t mine = real ? (int64_t)ti * p.ldq + (int64_t)head * D : -1;
             const int part = lane / LPR, col = lane % LPR;
             const uint32_t qs = smem_addr(smem + L::q) + 2 * t * L::OPERAND + (col >> 4) * L::ATOM + (col & 1) * 8;
@@ -801,35 +810,35 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 }
             } else {
 #pragma unroll 1
-                for (int x = 0; x < BT; x += 32) {
-                    float s[32];
-                    tm_ld32(ts + x, s);
-                    tm_wait(s);
+                for (int g = 0; g < GROUPS; g++) {
+                    float s[16];
+                    tm_ld16(ts + 16 * g, s);
+                    tm_wait16(s);
+                    const float fk = f * m.ks[g];
+                    const int base = m.base[g];
 #pragma unroll
-                    for (int g = 0; g < 2; g++) {
-                        const float fk = f * m.ks[x / 16 + g];
-                        const int base = m.base[x / 16 + g];
+                    for (int e = 0; e < 16; e++) s[e] *= fk;
+                    if (p.cap > 0.0f) {
 #pragma unroll
-                        for (int e = 0; e < 16; e++) s[16 * g + e] *= fk;
-                        if (p.cap > 0.0f) {
-#pragma unroll
-                            for (int e = 0; e < 16; e++) s[16 * g + e] = cap2 * tanh_f32(s[16 * g + e]);
-                        }
-                        if (p.slopes) {
-#pragma unroll
-                            for (int e = 0; e < 16; e++) s[16 * g + e] -= slope * (float)abs(qpos - (base + e));
-                        }
-                        if (!whole) {   // bit e: the group's token e is there and seen
-                            const uint32_t see = (bits16(seelo - base, qpos - base) | bits16(firstp - base, pre - 1 - base)) &
-                                                 bits16(0, live - x - 16 * g - 1);
-#pragma unroll
-                            for (int e = 0; e < 16; e++)
-                                if (!(see & (1u << e))) s[16 * g + e] = -INFINITY;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; e++) mx[e & 3] = fmaxf(mx[e & 3], s[16 * g + e]);
+                        for (int e = 0; e < 16; e++) s[e] = cap2 * tanh_f32(s[e]);
                     }
-                    tm_st32(ts + x, s);
+                    if (p.slopes) {
+#pragma unroll
+                        for (int e = 0; e < 16; e++) s[e] -= slope * (float)abs(qpos - (base + e));
+                    }
+                    if (!whole) {   // bit e: the group's token e is there and seen
+                        const uint32_t see = (bits16(seelo - base, qpos - base) | bits16(firstp - base, pre - 1 - base)) &
+                                             bits16(0, live - 16 * g - 1);
+#pragma unroll
+                        for (int e = 0; e < 16; e++)
+                            if (!(see & (1u << e))) s[e] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e++) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
+                    uint32_t u[16];
+#pragma unroll
+                    for (int e = 0; e < 16; e++) u[e] = __float_as_uint(s[e]);
+                    tm_st16(ts + 16 * g, u);
                 }
                 tm_wait_st();
             }
@@ -887,11 +896,14 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             float *gl = nullptr;
             if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
             const uint64_t nm = pack2(-msafe, -msafe);
-            float s[2][32];
-            tm_ld32(ts, s[0]);
-            // 32 tokens from s[cur] while the next 32 are on their way
-            auto weigh = [&](int x, float (&cur)[32], float (&next)[32]) {
-                tm_wait(cur);
+            float cur[32], next[32];
+            tm_ld32(ts, cur);
+            tm_wait(cur);
+            // 32 tokens at a time, while the next 32 are on their way.  (One copy of this code: the five
+            // roles' loops together have to fit the instruction caches; unrolled, waiting for instructions
+            // was a third of the stalls.)
+#pragma unroll 1
+            for (int x = 0; x < BT; x += 32) {
                 if (x + 32 < BT) tm_ld32(ts + x + 32, next);
                 uint32_t hi[16], lo[16];
                 float sum[2];
@@ -930,16 +942,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 }
                 tm_st16(ts + x, hi);
                 tm_st16(ts + x + 16, lo);
-            };
-#pragma unroll 1   // (code that fits the instruction caches: five roles run different parts of it)
-            for (int x = 0; x < BT; x += 64) {
-                weigh(x, s[0], s[1]);
-                weigh(x + 32, s[1], s[0]);
-                // half of the weights are there: their product may begin
-                tm_wait_st();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) wait.arrive(P_FULL + (x >> 5) + t);   // x = 0: the first half, 64: the second
+                if (x & 32) {   // half of the weights are there: their product may begin
+                    tm_wait_st();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) wait.arrive(P_FULL + (x >> 6) * 2 + t);
+                }
+                if (x + 32 < BT) {
+                    tm_wait(next);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) cur[e] = next[e];
+                }
             }
         }
         if (flags & F_LAST) {
