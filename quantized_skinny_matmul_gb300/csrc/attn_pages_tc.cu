@@ -514,7 +514,7 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
     // weights multiplied, and those of the item
     int nk = 0, nv = 0, nitem = 0;
     uint32_t np = 0, no = 0;
-    int prev = 0, started = 0, fresh_q = 0;    // tiles whose weights wait for V; tiles with a product in this item; queries not yet waited for
+    int prev = 0, fresh_q = 0;    // tiles whose weights wait for V; queries not yet waited for
 
     auto commit = [&](int bar) { mma_commit(smem_addr(sm.bars + bar)); };
     for (int i = 0;; i++) {
@@ -526,7 +526,6 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
         if (flags & F_FIRST) {
             nitem++;
             no = 0;
-            started = 0;
             fresh_q = F_TILE0 | F_TILE1;
         }
         // A pass: for each tile P V of the block before, then Q K of this one.  After an item's last
@@ -560,10 +559,14 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
                     }
                     np = t ? np + one : (np & 0xffff0000u) | ((np + 1) & 0xffffu);
                     no = t ? no + one : (no & 0xffff0000u) | ((no + 1) & 0xffffu);
-                    started |= 1 << t;
                     if (t == 1 || !(prev & F_TILE1)) commit(V_EMPTY);
                 }
-                if (pass == 1 && ((started >> t) & 1)) commit(O_FULL + t);
+                if (pass == 1) {
+                    // a tile that saw nothing too: its queries are waited for, and its next ones come
+                    // only after O_FULL (else they come phases ahead of this wait)
+                    if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
+                    commit(O_FULL + t);
+                }
                 if ((now >> t) & 1) {
                     if (!have_k && !wait(K_FULL, nk)) return;
                     have_k = true;
@@ -588,9 +591,6 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
             if (now) nk++;
             prev = now;
         }
-        if (flags & F_LAST)   // the queries of a tile that saw nothing: every phase of a barrier is waited for
-            for (int t = 0; t < 2; t++)
-                if (((fresh_q >> t) & 1) && !wait(Q_FULL + t, nitem - 1)) return;
     }
 }
 
@@ -959,10 +959,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             const float l = lrow;
             const float inv = l > 0.0f ? pow2i(vex - 4) / l : 0.0f;
             const float cs = carry() * inv;
-            if (blocks > 0) {
-                if (!wait.warp(O_FULL + t, no++)) return;
-                tc_after();
-            }
+            if (!wait.warp(O_FULL + t, no++)) return;
+            tc_after();
             // out by way of the query's memory (every product that read it is done): a row is stored
             // by D / 4 lanes together.  Each warp has a quarter of it: 32 rows of D f32, 16-byte
             // chunk x of row r at chunk x ^ (r mod 8).

@@ -199,6 +199,7 @@ SHAPES = [
     (0, 1, 4, 128, 32, [150], [100], False),                     # tiles of 128 rows: two pairs
     (1, 2, 1, 64, 16, [0, 700, 3], [290, 33, 1], True),          # and rows, in one batch
     (0, 1, 3, 64, 128, [260, 5], [86, 200], True),
+    (0, 2, 2, 64, 16, [5] * 330, [20] * 330, False),             # a first tile each, and no second one
 ]
 
 
