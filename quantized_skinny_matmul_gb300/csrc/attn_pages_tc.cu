@@ -62,6 +62,7 @@ enum : int { F_TILE0 = 1, F_TILE1 = 2, F_FIRST = 4, F_LAST = 8, F_EXIT = 16 };
 struct BlockMeta {
     int flags;
     int b, h, pair;             // the item
+    int place;                  // of its share's outputs; -1: it has all keys
     SeqStep s;
     int slot, live;             // first slot of the block, tokens of it that are held
     int lost;                   // bit i: group i has no usable page
@@ -101,7 +102,10 @@ struct TileLayout {
 constexpr uint32_t TM_S = 0, TM_O = 256;    // tensor-memory columns: S of tile t at 128 t, O at 256 + 128 t
 
 struct PlanView {
-    int2 *list;                 // (sequence, pair of tiles)
+    int4 *list;                 // (sequence, pair of tiles, share, shares)
+    float *parts;               // [place][2 BR][D]: a share's outputs; null: nothing is shared
+    float *part_lse;            // [place][2 BR]: log2 of its denominators (infinity: nothing seen)
+    int places;
     int *count, *next;          // entries, items taken
     float *sums;                // [CTA][2][D / 4][BR][4]: the tiles' flushed output sums
 };
@@ -269,49 +273,66 @@ __device__ __forceinline__ float pow2i(int e) {         // 2^e, 0 below 2^-126
 }
 
 // ---- the list of items --------------------------------------------------------------------
+// Where the items leave most SMs idle, the keys of long ones are shared out, as far as all shares
+// run at once and none has under SHARE_BLOCKS blocks; attn_pages_join_kernel joins them.  64 rows of
+// one head on 32768 tokens, 64 shares: 61 us (16 shares: 107); 8 heads on 4096: 42 us (3 blocks: 43).
+constexpr int SHARE_BLOCKS = 4, MOST_SHARES = 64;
+
 __global__ void __launch_bounds__(256) attn_pages_plan_kernel(const AttnParams8 p, const PlanView plan) {
     __shared__ int sums[8];
-    __shared__ int carry;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) carry = 0;
-    __syncthreads();
-    for (int b0 = 0; b0 < p.c.B; b0 += 256) {
-        const int b = b0 + tid;
-        int pairs = 0;
-        if (b < p.c.B) {
-            const SeqStep s = attn_step(p, b);
-            if (s.bad) atomicOr(p.c.status, STATUS_RANGE);
-            if (s.n * p.G > p.rows_over) pairs = (s.n * p.G + 2 * BR - 1) / (2 * BR);
-        }
-        int inc = pairs;
+    // the CTA's sum of x, and of those of the threads before
+    auto scan = [&](int x, int &before) {
+        int inc = x;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int t = __shfl_up_sync(0xffffffffu, inc, d);
             if (lane >= d) inc += t;
         }
+        __syncthreads();
         if (lane == 31) sums[warp] = inc;
         __syncthreads();
-        int at = carry + inc - pairs, all = 0;
+        int all = 0;
+        before = inc - x;
         for (int w = 0; w < 8; w++) {
-            if (w < warp) at += sums[w];
+            if (w < warp) before += sums[w];
             all += sums[w];
         }
-        for (int i = 0; i < pairs; i++) plan.list[at + i] = make_int2(b, pairs - 1 - i);
-        __syncthreads();
-        if (tid == 0) carry += all;
-        __syncthreads();
+        return all;
+    };
+    int at = 0, total = 0, most = 1;
+    for (int phase = 0; phase < 2; phase++) {   // count the pairs, then write the list
+        for (int b0 = 0; b0 < p.c.B; b0 += 256) {
+            const int b = b0 + tid;
+            int pairs = 0, splits = 1, before;
+            if (b < p.c.B) {
+                const SeqStep s = attn_step(p, b);
+                if (s.bad && phase == 0) atomicOr(p.c.status, STATUS_RANGE);
+                if (s.n * p.G > p.rows_over) pairs = (s.n * p.G + 2 * BR - 1) / (2 * BR);
+                int keys = s.held + s.n;
+                if (p.window > 0) keys = (int)min((int64_t)keys, p.window + 2 * BR / p.G);
+                splits = max(1, min(most, keys / (SHARE_BLOCKS * BT)));
+            }
+            const int all = scan(phase ? pairs * splits : pairs, before);
+            if (phase)
+                for (int i = 0; i < pairs * splits; i++)
+                    plan.list[at + before + i] = make_int4(b, pairs - 1 - i / splits, i % splits, splits);
+            if (phase) at += all;
+            else total += all;
+        }
+        if (phase == 0 && plan.parts && total > 0) most = max(1, min(MOST_SHARES, plan.places / max(1, total * p.c.Hkv)));
     }
     if (tid == 0) {
-        *plan.count = carry;
+        *plan.count = at;
         *plan.next = 0;
     }
 }
 
 // ---- warp 12: items, blocks, raw copies ---------------------------------------------------
 struct Item {
-    int b, h, pair;
+    int b, h, pair, z, splits, place;
     SeqStep s;
 };
 
@@ -341,6 +362,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
             d.b = x.b;
             d.h = x.h;
             d.pair = x.pair;
+            d.place = x.place;
             d.s = x.s;
             d.slot = slot;
             d.live = live;
@@ -355,15 +377,18 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         int item = 0;
         if (lane == 0) item = atomicAdd(plan.next, 1);
         item = __shfl_sync(0xffffffffu, item, 0);
-        Item x{0, 0, 0, {0, 0, 0, 0, false}};
+        Item x{0, 0, 0, 0, 1, -1, {0, 0, 0, 0, false}};
         if (item >= items) {
             publish(x, F_EXIT, 0, 0, 0, 0, 0.0f, 0.0f, 0);
             break;
         }
-        const int2 e = __ldcg(plan.list + item / c.Hkv);
+        const int4 e = __ldcg(plan.list + item / c.Hkv);
         x.b = e.x;
         x.h = item % c.Hkv;
         x.pair = e.y;
+        x.z = e.z;
+        x.splits = e.w;
+        x.place = x.splits > 1 ? item : -1;
         x.s = attn_step(p, x.b);
         // the queries, on their way to L2 while the item before is finished (read from there, they hold
         // the start of an item up by 10 us less than from device memory)
@@ -406,7 +431,8 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
             b0 = min(low / BT, b1);
             bp = min((min(end, premax) + BT - 1) / BT, b0);
         }
-        const int blocks = bp + b1 - b0;
+        const int all = bp + b1 - b0, ib = (int)((int64_t)all * x.z / x.splits);   // this share's first block
+        const int blocks = (int)((int64_t)all * (x.z + 1) / x.splits) - ib;
         const int64_t trow = ((int64_t)x.b * c.Hkv + x.h) * c.NB;
         // Blocks are looked up four at a time, a lane per group of 16 tokens; the pages of the next four,
         // and then their scales, are under way while these are worked on (one by one, these dependent
@@ -415,7 +441,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
             int page, base, live;   // page -1: none, -2: not usable
             float ks, vs;
         };
-        auto slot_of = [&](int i) { return (i < bp ? i : b0 + i - bp) * BT; };
+        auto slot_of = [&](int i) { return (ib + i < bp ? ib + i : b0 + ib + i - bp) * BT; };
         auto pages = [&](int i0, Look &l) {
             const int i = i0 + (lane >> 3), at = slot_of(i) + 16 * (lane & 7);
             l.page = -1;
@@ -660,7 +686,7 @@ __device__ __forceinline__ void widen_role(uint8_t *smem, TileSmem &sm, Waiter &
 // ---- warps 0-7: softmax, a thread per row ------------------------------------------------------
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem, TileSmem &sm, Waiter &wait, uint32_t tmem,
-                                             float *sums, int t, int row, int lane) {
+                                             const PlanView &plan, int t, int row, int lane) {
     using L = TileLayout<D>;
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;   // this warp's tensor-memory lanes
     const uint32_t ts = tmem + lanes + TM_S + 128 * t, to = tmem + lanes + TM_O + 128 * t;
@@ -672,7 +698,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
     float f = 0.0f, slope = 0.0f, mrow = -INFINITY, lrow = 0.0f;
     // the running sum of flushed parts: this thread's float4s, D / 4 of them, BR apart; in units of
     // 2^gex, relative to gmax
-    float4 *sum = reinterpret_cast<float4 *>(sums) + ((size_t)blockIdx.x * 2 + t) * (D / 4) * BR + row;
+    float4 *sum = reinterpret_cast<float4 *>(plan.sums) + ((size_t)blockIdx.x * 2 + t) * (D / 4) * BR + row;
     int blocks = 0, gex = 0;       // blocks of the item so far
     float gmax = -INFINITY;
     // the four warps of the tile, with a bounded wait
@@ -987,18 +1013,20 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 }
             }
             __syncwarp();
-            const int64_t mine = real ? (int64_t)ti * p.ldo + (int64_t)head * D : -1;
+            const int64_t to_part = ((int64_t)m.place * 2 + t) * BR + row;
+            const int64_t mine = !real ? -1 : m.place >= 0 ? to_part * D : (int64_t)ti * p.ldo + (int64_t)head * D;
+            float *out = m.place >= 0 ? plan.parts : p.out, *lse = m.place >= 0 ? plan.part_lse + to_part : p.lse + (int64_t)ti * p.Hq + head;
             const int part = lane / LPR, col = lane % LPR;
 #pragma unroll 4
             for (int r0 = 0; r0 < 32; r0 += RPI) {
                 const int rr = r0 + part;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
                 const uint4 v = sh_ld128(stage + rr * D * 4 + ((col ^ (rr & 7)) << 4));
-                if (at >= 0) *(reinterpret_cast<uint4 *>(p.out + at) + col) = v;
+                if (at >= 0) *(reinterpret_cast<uint4 *>(out + at) + col) = v;
             }
             if (!sync_tile()) return;   // the next item's queries go into the same memory
+            if (real && (p.lse || m.place >= 0)) *lse = l > 0.0f ? mrow + log2f(l) : INFINITY;
             tc_before();   // O is overwritten only after these loads (the next item's P_FULL)
-            if (p.lse && real) p.lse[(int64_t)ti * p.Hq + head] = l > 0.0f ? mrow + log2f(l) : INFINITY;
         }
         __syncwarp();
         if (lane == 0) wait.arrive(META_EMPTY + st);
@@ -1072,12 +1100,59 @@ __global__ void __launch_bounds__(THREADS, 1)
         widen_role<KIND, D>(smem, sm, wait, threadIdx.x - 256, lane);
     } else {
         regs_inc<REGS_SOFTMAX>();
-        softmax_role<D>(p, smem, sm, wait, tmem, plan.sums, warp >> 2, threadIdx.x & 127, lane);
+        softmax_role<D>(p, smem, sm, wait, tmem, plan, warp >> 2, threadIdx.x & 127, lane);
     }
     __syncthreads();
     if (warp == 13) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// ---- shares of an item joined -------------------------------------------------------------------
+// A row of D / 4 lanes at a time: the shares' outputs by their denominators, in order.
+constexpr int JOIN_ROWS = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_pages_join_kernel(const AttnParams8 p, const PlanView plan) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int Hkv = (int)p.c.Hkv, place = blockIdx.y;
+    if (place / Hkv >= __ldcg(plan.count)) return;
+    const int4 e = __ldcg(plan.list + place / Hkv);
+    const int splits = e.w;
+    if (splits == 1 || e.z > 0) return;   // (the first share's blocks join)
+    const SeqStep s = attn_step(p, e.x);
+    constexpr int LPR = D / 4, RPI = 256 / LPR;
+    const int col = threadIdx.x % LPR;
+#pragma unroll
+    for (int r0 = 0; r0 < JOIN_ROWS; r0 += RPI) {
+        const int row = blockIdx.x * JOIN_ROWS + r0 + threadIdx.x / LPR, r = e.y * 2 * BR + row;
+        if (r >= s.n * p.G) return;
+        float lse = -INFINITY, sum = 0.0f;
+        auto part = [&](int z) { return (int64_t)(place + z * Hkv) * 2 * BR + row; };
+#pragma unroll 8
+        for (int z = 0; z < splits; z++) {
+            const float x = __ldcg(plan.part_lse + part(z));
+            if (x != INFINITY) lse = fmaxf(lse, x);
+        }
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int z = 0; z < splits; z++) {   // (a share that saw nothing has zeros)
+            const float x = __ldcg(plan.part_lse + part(z));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(plan.parts + part(z) * D) + col);
+            const float w = x == INFINITY ? 0.0f : ex2(x - lse);
+            sum += w;
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const int ti = s.t0 + r / p.G;
+        const int64_t head = (int64_t)(place % Hkv) * p.G + r % p.G;
+        reinterpret_cast<float4 *>(p.out + ti * p.ldo + head * D)[col] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (p.lse && col == 0) p.lse[(int64_t)ti * p.Hq + head] = sum > 0.0f ? lse + log2f(sum) : INFINITY;
     }
 }
 
@@ -1109,25 +1184,42 @@ int64_t most_pairs(const gq_kv_pages &c, int64_t T, int64_t G) { return T * G / 
 
 }  // namespace
 
+// Whether the rows, if all are in tiles, may leave half of the SMs idle: places for shares' outputs.
+static int share_places(const gq_kv_pages &c, int64_t T, int64_t G) {
+    return T * G / (2 * BR) * c.Hkv * 2 > sm_count() ? 0 : sm_count();
+}
+
+static size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
 size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t T, int64_t G) {
-    return 256 + ((size_t)most_pairs(c, T, G) * sizeof(int2) + 255) / 256 * 256 +
-           (size_t)sm_count() * 2 * c.D * BR * sizeof(float);
+    const size_t places = (size_t)share_places(c, T, G);
+    return 256 + round_up(((size_t)most_pairs(c, T, G) + places) * sizeof(int4)) +
+           (size_t)sm_count() * 2 * c.D * BR * 4 + places * 2 * BR * (c.D + 1) * 4;
 }
 
 gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8_t *work, cudaStream_t s) {
     PlanView plan{};
+    plan.places = share_places(c, p.T, p.G);
+    const int64_t entries = most_pairs(c, p.T, p.G) + plan.places;
     plan.count = reinterpret_cast<int *>(work);
     plan.next = plan.count + 1;
-    plan.list = reinterpret_cast<int2 *>(work + 256);
-    plan.sums = reinterpret_cast<float *>(work + 256 + ((size_t)most_pairs(c, p.T, p.G) * sizeof(int2) + 255) / 256 * 256);
-    const int64_t items = most_pairs(c, p.T, p.G) * c.Hkv;
-    if (items > INT32_MAX) return fail(GQ_ERR_INVALID_ARG, "attention grid too large");
+    plan.list = reinterpret_cast<int4 *>(work + 256);
+    plan.sums = reinterpret_cast<float *>(work + 256 + round_up((size_t)entries * sizeof(int4)));
+    plan.parts = plan.places ? plan.sums + (size_t)sm_count() * 2 * c.D * BR : nullptr;
+    plan.part_lse = plan.places ? plan.parts + (size_t)plan.places * 2 * BR * c.D : nullptr;
+    if (entries * c.Hkv > INT32_MAX) return fail(GQ_ERR_INVALID_ARG, "attention grid too large");
     void *args[] = {(void *)&p, (void *)&plan};
     KV_TRY(launch_pdl((const void *)attn_pages_plan_kernel, dim3(1), dim3(256), 0, s, args, "paged attention plan launch"));
+    const int64_t items = entries * c.Hkv;
+    gq_status st;
     if (c.kind == GQ_KV_I8)
-        return c.D == 64 ? launch_tiles<GQ_KV_I8, 64>(p, c, plan, items, s) : launch_tiles<GQ_KV_I8, 128>(p, c, plan, items, s);
-    return c.D == 64 ? launch_tiles<GQ_KV_E4M3, 64>(p, c, plan, items, s)
-                     : launch_tiles<GQ_KV_E4M3, 128>(p, c, plan, items, s);
+        st = c.D == 64 ? launch_tiles<GQ_KV_I8, 64>(p, c, plan, items, s) : launch_tiles<GQ_KV_I8, 128>(p, c, plan, items, s);
+    else
+        st = c.D == 64 ? launch_tiles<GQ_KV_E4M3, 64>(p, c, plan, items, s)
+                       : launch_tiles<GQ_KV_E4M3, 128>(p, c, plan, items, s);
+    if (st != GQ_OK || !plan.places) return st;
+    return launch_pdl(c.D == 64 ? (const void *)attn_pages_join_kernel<64> : (const void *)attn_pages_join_kernel<128>,
+                      dim3(2 * BR / JOIN_ROWS, (unsigned)plan.places), dim3(256), 0, s, args, "paged attention join launch");
 }
 
 }  // namespace gq

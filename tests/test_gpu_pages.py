@@ -200,6 +200,9 @@ SHAPES = [
     (1, 2, 1, 64, 16, [0, 700, 3], [290, 33, 1], True),          # and rows, in one batch
     (0, 1, 3, 64, 128, [260, 5], [86, 200], True),
     (0, 2, 2, 64, 16, [5] * 330, [20] * 330, False),             # a first tile each, and no second one
+    (0, 2, 3, 64, 16, [5] * 330, [20] * 330, False),
+    (0, 1, 4, 128, 32, [2500, 0], [40, 100], False),             # few tiles, many keys: shares of one sequence's keys
+    (1, 1, 8, 64, 16, [5000], [17], True),
 ]
 
 
