@@ -838,20 +838,22 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
 
 // ---------------------------------------------------------------------------
 // The weight that each page gathered: decay * in + sum over the step's query rows of
-// 2^(log2 of the page's weight sum - log2 of the row's denominator).  A CTA takes 32 groups of
-// tokens of one (sequence, head), a lane per group; its warps share the rows and are added in order.
-// The sums of groups that a row cannot see were never written: they are passed over.
+// 2^(log2 of the page's weight sum - log2 of the row's denominator).  A cluster of CL CTAs takes 32
+// groups of tokens of one (sequence, head), a lane per group; its CTAs' WW warps share the tokens
+// and are added in order.  The sums of groups that a row cannot see were never written: they are
+// passed over.  Bound by the latency of the loads, so many rows want many warps: 4 sequences of
+// up to 1000 tokens x 2 heads each, 8 KV heads: 72 us with one CTA each.
 // ---------------------------------------------------------------------------
-constexpr int WW = 16;   // warps
-
-__global__ void __launch_bounds__(WW * 32) attn_pages_weights_kernel(const AttnParams8 p, const float *w_in, float *w_out,
-                                                                     float decay) {
+template <int WW, int CL>
+__global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
+    attn_pages_weights_kernel(const AttnParams8 p, const float *w_in, float *w_out, float decay) {
     __shared__ float part[WW][32];
     const PagesView &c = p.c;
     pdl_launch_dependents();
     const int per = p.lgP - p.lgGroup;   // log2 of the groups of a page
-    const int tiles = (((c.NB << per) + 31) / 32), bh = blockIdx.x / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = (blockIdx.x % tiles) * 32 + lane, j = g >> per;
+    const int tiles = (((c.NB << per) + 31) / 32), item = blockIdx.x / CL, rank = blockIdx.x % CL;
+    const int bh = item / tiles, b = bh / c.Hkv, h = bh % c.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = (item % tiles) * 32 + lane, j = g >> per;
     const int size = 1 << p.lgGroup;
     pdl_wait();
     const SeqStep s = seq_step(c, p.cu, b, p.T, p.max_n);
@@ -862,29 +864,50 @@ __global__ void __launch_bounds__(WW * 32) attn_pages_weights_kernel(const AttnP
     if (__any_sync(0xffffffffu, used)) {
         const int x0 = used ? c.base[at] + (slot & (c.P - 1)) : 0x7f000000, x1 = used ? x0 + size - 1 : 0x7f000000;
         const float *gl = p.glse + (used ? g : 0);
-        const int rows = s.n * p.G;
-        const int64_t r0 = (int64_t)s.t0 * p.Hq + h * p.G;
         // (loads of rows and groups that were never written are within the buffer, and passed over)
-#pragma unroll 4
-        for (int x = warp; x < rows; x += WW) {
-            const int i = x / p.G, qpos = s.seen + i;
-            const int64_t r = r0 + (int64_t)i * p.Hq + (x - i * p.G);
+        auto row = [&](int i, int y) {
+            const int64_t r = (int64_t)(s.t0 + i) * p.Hq + h * p.G + y;
+            const int qpos = s.seen + i;
             const float v = __ldcg(gl + r * p.NG), l = __ldcg(p.lse + r);
             const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? __ldg(p.prefix + s.t0 + i) : 0;
             const int lo = p.window > 0 ? (int)max((int64_t)first, (int64_t)qpos - p.window + 1) : first;
             const bool see = (x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre);
             sum += see ? ex2(v - l) : 0.0f;
+        };
+        if (CL == 1) {      // few rows
+            for (int x = warp; x < s.n * p.G; x += WW) row(x / p.G, x % p.G);
+        } else {
+            for (int y = 0; y < p.G; y++)
+#pragma unroll 8
+                for (int i = rank * WW + warp; i < s.n; i += WW * CL) row(i, y);
         }
     }
     part[warp][lane] = sum;
     __syncthreads();
+    float total = 0.0f;
     if (warp == 0) {
-        float total = part[0][lane];
+        total = part[0][lane];
         for (int w = 1; w < WW; w++) total += part[w][lane];
+    }
+    if (CL > 1) {
+        if (warp == 0) part[0][lane] = total;
+        cluster_sync();
+        if (warp == 0 && rank == 0) {
+            float other[CL];
+#pragma unroll
+            for (int r = 1; r < CL; r++) other[r] = ld_shared_cluster_f32(map_shared_rank(&part[0][lane], r));
+#pragma unroll
+            for (int r = 1; r < CL; r++) total += other[r];
+        }
+        cluster_sync();   // (shared memory stays until it is read)
+    }
+    if (warp == 0 && rank == 0) {
         for (int d = 1; d < 1 << per; d <<= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
         if (j < c.NB && (g & ((1 << per) - 1)) == 0) w_out[at] = used ? (w_in ? decay * w_in[at] : 0.0f) + total : 0.0f;
     }
 }
+
+constexpr int WROWS_FEW = 32;   // rows of a KV head that 4 warps take
 
 int log2_of(int64_t x) {
     int l = 0;
@@ -942,9 +965,12 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
                           "paged attention launch"));
     }
     if (w_out) {
-        const int64_t wgrid = c.B * c.Hkv * ((p.NG + 31) / 32);
+        // a cluster from 2 rows a warp on
+        const int64_t items = c.B * c.Hkv * ((p.NG + 31) / 32);
         void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
-        KV_TRY(launch_pdl((const void *)attn_pages_weights_kernel, dim3((unsigned)wgrid), dim3(WW * 32), 0, s, wargs,
+        const bool many = (int64_t)p.max_n * p.G > WROWS_FEW;
+        KV_TRY(launch_pdl(many ? (const void *)attn_pages_weights_kernel<16, 8> : (const void *)attn_pages_weights_kernel<4, 1>,
+                          dim3((unsigned)(many ? 8 * items : items)), dim3(many ? 512 : 128), 0, s, wargs,
                           "paged attention weights launch"));
     }
     return GQ_OK;
