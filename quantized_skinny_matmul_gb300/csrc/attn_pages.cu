@@ -841,8 +841,10 @@ __global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
 // 2^(log2 of the page's weight sum - log2 of the row's denominator).  A cluster of CL CTAs takes 32
 // groups of tokens of one (sequence, head), a lane per group; its CTAs' WW warps share the tokens
 // and are added in order.  The sums of groups that a row cannot see were never written: they are
-// passed over.  Bound by the latency of the loads, so many rows want many warps: 4 sequences of
-// up to 1000 tokens x 2 heads each, 8 KV heads: 72 us with one CTA each.
+// passed over.  Bound by the latency of the loads, so many rows want many warps, unless the items
+// fill the GPU by themselves.  The whole step, 4 sequences of up to 1000 tokens x 2 heads of 8 KV heads
+// (64 items): 74 us, 109 with one CTA an item; 8 x 8 tokens x 8 heads on 4096 (512 items): 89 us with 4
+// warps an item, 170 with 8 x 16.
 // ---------------------------------------------------------------------------
 template <int WW, int CL>
 __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
             const bool see = (x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre);
             sum += see ? ex2(v - l) : 0.0f;
         };
-        if (CL == 1) {      // few rows
+        if (WW == 4) {      // few rows
             for (int x = warp; x < s.n * p.G; x += WW) row(x / p.G, x % p.G);
         } else {
             for (int y = 0; y < p.G; y++)
@@ -907,7 +909,9 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
     }
 }
 
-constexpr int WROWS_FEW = 32;   // rows of a KV head that 4 warps take
+// Page weights: up to WROWS_FEW rows of a KV head are left to 4 warps; more to 16, and to 16 of each of
+// WCTAS CTAs where all of them fit the GPU at once.
+constexpr int WROWS_FEW = 64, WCTAS = 8;
 
 int log2_of(int64_t x) {
     int l = 0;
@@ -965,12 +969,13 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
                           "paged attention launch"));
     }
     if (w_out) {
-        // a cluster from 2 rows a warp on
         const int64_t items = c.B * c.Hkv * ((p.NG + 31) / 32);
         void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
-        const bool many = (int64_t)p.max_n * p.G > WROWS_FEW;
-        KV_TRY(launch_pdl(many ? (const void *)attn_pages_weights_kernel<16, 8> : (const void *)attn_pages_weights_kernel<4, 1>,
-                          dim3((unsigned)(many ? 8 * items : items)), dim3(many ? 512 : 128), 0, s, wargs,
+        const bool few = (int64_t)p.max_n * p.G <= WROWS_FEW, spread = !few && items * WCTAS <= 4 * sm_count();
+        const void *weigh = few      ? (const void *)attn_pages_weights_kernel<4, 1>
+                            : spread ? (const void *)attn_pages_weights_kernel<16, WCTAS>
+                                     : (const void *)attn_pages_weights_kernel<16, 1>;
+        KV_TRY(launch_pdl(weigh, dim3((unsigned)(spread ? WCTAS * items : items)), dim3(few ? 128 : 512), 0, s, wargs,
                           "paged attention weights launch"));
     }
     return GQ_OK;

@@ -49,9 +49,10 @@ constexpr int GROUPS = BT / 16;             // scales and positions come by 16 t
 constexpr int METAS = 4;                    // blocks whose data is kept
 // The tensor cores add to their f32 accumulators with truncation: after N products an output is
 // off by about N 2^-26 of itself, one way.  Every FLUSH blocks (16 products each) a tile's O is
-// added to a running sum in memory, rounded to nearest, and begun anew: without it a row over 4,500
-// tokens was off by 8e-6.
-constexpr int FLUSH = 8;
+// added to a running sum in memory, rounded to nearest, and begun anew.  A row over 4,500 tokens is
+// off by 8e-6 without it, by 2.5e-6 every 8 blocks, 1.4e-6 every 4 and 0.9e-6 every 2 (elementary
+// operations in f32: 1.2e-6); a prompt of 4096 takes 288, 300 and 320 us with 8, 4 and 2.
+constexpr int FLUSH = 4;
 constexpr int THREADS = 512;
 // Registers per thread of the four warpgroups: they add up to the 4 x 128 of the launch.
 constexpr int REGS_SOFTMAX = 168, REGS_REST = 88;
@@ -195,6 +196,10 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *v) {
         : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void red_add4(float4 *at, float a, float b, float c, float d) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -877,6 +882,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // (this block's scores come after the products of the block before: O is complete up to it)
             if (blocks > 0 && blocks % FLUSH == 0) {
                 const float cs = carry();
+                // the sum is in the same units as O (nearly always): added without being read
+                const bool add = blocks > FLUSH && __all_sync(0xffffffffu, cs == 1.0f);
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
                     float o[32];
@@ -885,6 +892,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
 #pragma unroll
                     for (int y = 0; y < 32; y += 4) {
                         float4 *at = sum + (x + y) / 4 * BR;
+                        if (add) {
+                            red_add4(at, o[y], o[y + 1], o[y + 2], o[y + 3]);
+                            continue;
+                        }
                         float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         if (blocks > FLUSH) g = __ldcg(at);
                         __stcg(at, make_float4(fmaf(g.x, cs, o[y]), fmaf(g.y, cs, o[y + 1]), fmaf(g.z, cs, o[y + 2]),
