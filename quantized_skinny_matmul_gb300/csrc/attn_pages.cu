@@ -22,7 +22,7 @@
 // are joined by the CTA that finishes last, in the order of the pieces (so the result does
 // not depend on timing).  A producer warp streams the units' pages through a ring of
 // shared-memory slots (tensor copies, 128-byte swizzle) and puts each unit's scales and
-// positions beside them; four consumer warps take the units in turn, each with its own
+// positions beside them; seven consumer warps take the units in turn, each with its own
 // running maximum and sums, joined at the end of the item.
 #include <algorithm>
 #include <atomic>
@@ -46,9 +46,13 @@ namespace {
     } while (0)
 
 constexpr int UNIT = 32;                    // tokens per unit
-// Consumer warps, and query rows of an item, for 1 or 2 column tiles: two CTAs of W + 1 warps fill
-// an SM's registers.
-__host__ __device__ constexpr int warps_of(int NN) { return NN == 1 ? 7 : 7; }
+// Consumer warps, and query rows of an item for 1 or 2 column tiles.  Two CTAs of 8 warps fill an
+// SM's registers.  128 sequences x 32 heads on 2048 tokens, a row each: 303 us with the query as the
+// 16-row operand, 274 with the codes there and slots of 32 tokens, 235 as it is (85% of a copy's
+// rate; bound by memory).  Short ones are bound by the steps of an item (about 1 us each: the
+// first slot, the query's fragments, the warps' sums joined, the pieces joined): 1 x 500 tokens of 32
+// heads takes 13.5 us, 1 x 32768 of 8 heads 28.
+constexpr int WARPS = 7;
 __host__ __device__ constexpr int rows_of(int NN) { return 4 * NN; }
 constexpr int ROWS_MOST = 8;
 constexpr int ITEMS = 2;                    // items whose data is kept
@@ -62,7 +66,7 @@ constexpr int ITEMS = 2;                    // items whose data is kept
 // last slot may hold one unit), and the slot before was filled when the one `slots` earlier was
 // given back; and items end together.
 __host__ __device__ constexpr int slots_of(int D, int NN) { return (NN == 1 ? 5 : 4) * (D == 128 ? 1 : 2); }
-static_assert(slots_of(128, 1) >= warps_of(1) / 2 + 1 && slots_of(128, 2) >= warps_of(2) / 2 + 1, "see above");
+static_assert(slots_of(128, 2) >= WARPS / 2 + 1, "see above");
 constexpr int MAX_SLOTS = 10;
 // Places for units' data, taken 32 at a time (the last of an item may be few).  What the producer
 // overwrites is done: either two items have begun since (ITEMS), or 32 units of one.
@@ -91,15 +95,15 @@ struct RowsSmem {
     uint64_t full[MAX_SLOTS], empty[MAX_SLOTS], item_full[ITEMS], item_empty[ITEMS];
     UnitMeta meta[METAS];       // of unit u of an item at (its first unit's place + u) mod METAS
     ItemRec item[ITEMS];
-    float ml[warps_of(1)][ROWS_MOST][2];    // maximum and denominator of each warp
+    float ml[WARPS][ROWS_MOST][2];    // maximum and denominator of each warp
     int64_t start, total;       // line position of the sequence that the CTA starts in
     int start_b, last, failed;
-    int64_t warp_sum[warps_of(1) + 1];
+    int64_t warp_sum[WARPS + 1];
 };
 
 template <int D, int NN>
 struct RowsLayout {
-    static constexpr int W = warps_of(NN), ROWS = rows_of(NN);
+    static constexpr int W = WARPS, ROWS = rows_of(NN);
     static constexpr int ring = 0;                                     // [slot]: keys, values of 64 tokens
     static constexpr int q = ring + slots_of(D, NN) * UNIT * D * 4;    // [ITEMS][ROWS][D] f32
     static constexpr int frag = q + ITEMS * ROWS * D * 4;              // the query's MMA fragments
@@ -248,7 +252,7 @@ __device__ __forceinline__ void join_pieces(const AttnParams8 &p, const ItemRec 
 }
 
 template <int KIND, int D, int NN>
-__global__ void __launch_bounds__((warps_of(NN) + 1) * 32, 2)
+__global__ void __launch_bounds__((WARPS + 1) * 32, 2)
     attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const AttnParams8 p) {
     using L = RowsLayout<D, NN>;
@@ -931,7 +935,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
                       cudaStream_t s) {
     auto kernel = attn_pages_rows_kernel<KIND, D, NN>;
     constexpr size_t smem = RowsLayout<D, NN>::total + 1024;
-    constexpr int ROWS = rows_of(NN), THREADS = (warps_of(NN) + 1) * 32;
+    constexpr int ROWS = rows_of(NN), THREADS = (WARPS + 1) * 32;
     static std::atomic<bool> smem_set[64];
     int dev = 0;
     KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
@@ -1006,7 +1010,8 @@ gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, cons
     p.NG = (int)((c.NB * c.P) >> p.lgGroup);
     p.scale = sc.scale;
     p.cap = sc.cap;
-    // items of up to 4 rows, where a sequence's rows of a KV head are no more, else of up to 8
+    // items of up to 4 rows, where a sequence's rows of a KV head are no more, else of up to 8: 32
+    // sequences x 8 heads x 4 rows on 2048 tokens take 33 us with one column tile, 41 with two
     const bool few = (int64_t)max_n * p.G <= 4;
     if (c.kind == GQ_KV_I8) {
         if (c.D == 64)
