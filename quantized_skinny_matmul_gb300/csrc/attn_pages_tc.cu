@@ -940,7 +940,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             float *gl = nullptr;
             if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
             const uint64_t nm = pack2(-msafe, -msafe);
-            float cur[32], next[32];
+            float cur[32];
             tm_ld32(ts, cur);
             tm_wait(cur);
             // 32 tokens at a time, while the next 32 are on their way.  (One copy of this code: the five
@@ -948,18 +948,27 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // was a third of the stalls.)
 #pragma unroll 1
             for (int x = 0; x < BT; x += 32) {
-                if (x + 32 < BT) tm_ld32(ts + x + 32, next);
-                uint32_t hi[16], lo[16];
-                float sum[2];
+                uint64_t z[16];
+                float vv[2], sum[2];
 #pragma unroll
                 for (int g = 0; g < 2; g++) {
-                    const float vv = m.vs[x / 16 + g] * vu, fk = simple ? f * m.ks[x / 16 + g] : 1.0f;
-                    const uint64_t vv2 = pack2(vv, vv), fk2 = pack2(fk, fk);
+                    vv[g] = m.vs[x / 16 + g] * vu;
+                    const float fk = simple ? f * m.ks[x / 16 + g] : 1.0f;
+                    const uint64_t fk2 = pack2(fk, fk);
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        z[8 * g + e] = fma2(pack2(cur[16 * g + 2 * e], cur[16 * g + 2 * e + 1]), fk2, nm);
+                }
+                if (x + 32 < BT) tm_ld32(ts + x + 32, cur);
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int g = 0; g < 2; g++) {
+                    const uint64_t vv2 = pack2(vv[g], vv[g]);
                     uint64_t q = 0ull;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float p0, p1;
-                        unpack2(fma2(pack2(cur[16 * g + e], cur[16 * g + e + 1]), fk2, nm), p0, p1);
+                        unpack2(z[8 * g + e / 2], p0, p1);
                         const uint64_t w = pack2(ex2(p0), ex2(p1));
                         q = add2(q, w);
                         // the first term: the leading 11 bits; the second: the rest, exact in f32
@@ -992,11 +1001,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                     __syncwarp();
                     if (lane == 0) wait.arrive(P_FULL + (x >> 6) * 2 + t);
                 }
-                if (x + 32 < BT) {
-                    tm_wait(next);
-#pragma unroll
-                    for (int e = 0; e < 32; e++) cur[e] = next[e];
-                }
+                if (x + 32 < BT) tm_wait(cur);
             }
         }
         if (flags & F_LAST) {

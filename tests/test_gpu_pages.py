@@ -326,6 +326,44 @@ def test_a_step_in_a_graph():
             assert np.array_equal(host(out), want)
 
 
+@pytest.mark.parametrize("kind,Hkv,G,D,P,held,new", [
+    (0, 1, 8, 128, 32, [3000], [30]),                        # shares of one tile's keys, joined
+    (1, 2, 2, 64, 16, [60] * 100, [25] * 100),               # many items of one block, second tiles empty
+    (0, 2, 4, 128, 64, [500, 0, 9], [70, 200, 1]),           # tiles and rows in one batch
+])
+def test_prompts_in_a_graph_and_in_a_row(kind, Hkv, G, D, P, held, new):
+    """Every launch of a long row of them, eager and replayed, gives the first one's bits."""
+    p = ref.problem(12, kind, len(held), Hkv, G, D, P, held, new)
+    c, q, cu, sc = cache_of(p), dev(p["q"]), dev(p["cu"]), gq.AttnScores(ref.SCALE(D))
+    w = dev(p["gen"].random(p["table"].shape).astype(np.float32))
+    out, new_w = torch.empty_like(q), torch.empty_like(w)
+
+    def call():
+        gq.gq_attn_pages(c, sc, q, Hkv * G * D, cu, q.shape[0], max(new), Hkv * G, out, Hkv * G * D, w, new_w, 0.5)
+
+    call()
+    want = out.clone(), new_w.clone()
+    check_attention(p, out, new_w, weights=host(w), decay=0.5)
+    for _ in range(200):
+        call()
+    assert torch.equal(out, want[0]) and torch.equal(new_w, want[1])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        call()
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            call()
+            call()
+        out.zero_()
+        for _ in range(50):
+            graph.replay()
+        st.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(new_w, want[1])
+    assert gq.gq_last_error() == gq.GQ_OK
+
+
 # ---- eviction ------------------------------------------------------------------------------------
 
 
