@@ -61,8 +61,9 @@ constexpr int METAS = 4;                    // blocks whose data is kept
 // operations in f32: 1.2e-6); a prompt of 4096 takes 288, 300 and 320 us with 8, 4 and 2.
 constexpr int FLUSH = 4;
 constexpr int THREADS = 512;
-// Registers per thread of the four warpgroups: they add up to the 4 x 128 of the launch.
-constexpr int REGS_SOFTMAX = 168, REGS_REST = 88;
+// Registers per thread of the four warpgroups: they add up to the 4 x 128 of the launch.  (A prompt
+// of 4096 takes 281 us; 283 with 152 and 104, 286 with 136 and 120.)
+constexpr int REGS_SOFTMAX = 144, REGS_REST = 112;
 static_assert(2 * REGS_SOFTMAX + 2 * REGS_REST <= 4 * 65536 / THREADS, "register split");
 
 enum : int { F_TILE0 = 1, F_TILE1 = 2, F_FIRST = 4, F_LAST = 8, F_EXIT = 16 };
@@ -636,7 +637,7 @@ __device__ __forceinline__ void mma_role(uint8_t *smem, TileSmem &sm, Waiter &wa
 template <int KIND, int D>
 __device__ __forceinline__ void widen_tile(uint32_t raw, uint32_t op, int tok, bool dead) {
     using L = TileLayout<D>;
-#pragma unroll 2
+#pragma unroll 1
     for (int ch = 0; ch < D / 16; ch++) {
         uint32_t a;
         if (D == 128) a = raw + tok * 128 + ((ch ^ (tok & 7)) << 4);
@@ -826,25 +827,22 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (simple) {   // f is not negative: a group's largest raw score is its largest score
 #pragma unroll 1
-                for (int x = 0; x < BT; x += 64) {
-                    float s0[32], s1[32];
-                    tm_ld32(ts + x, s0);
-                    tm_ld32(ts + x + 32, s1);
-                    tm_wait(s0);
-                    tm_wait(s1);
+                for (int x = 0; x < BT; x += 32) {
+                    float s0[16], s1[16];
+                    tm_ld16(ts + x, s0);
+                    tm_ld16(ts + x + 16, s1);
+                    tm_wait16(s0);
+                    tm_wait16(s1);
+                    float a0 = s0[0], a1 = s1[0];
 #pragma unroll
-                    for (int g = 0; g < 2; g++) {
-                        float a0 = s0[16 * g], a1 = s1[16 * g];
-#pragma unroll
-                        for (int e = 1; e < 15; e += 2) {
-                            a0 = max3(a0, s0[16 * g + e], s0[16 * g + e + 1]);
-                            a1 = max3(a1, s1[16 * g + e], s1[16 * g + e + 1]);
-                        }
-                        a0 = fmaxf(a0, s0[16 * g + 15]);
-                        a1 = fmaxf(a1, s1[16 * g + 15]);
-                        mx[2 * g] = fmaxf(mx[2 * g], a0 * (f * m.ks[x / 16 + g]));
-                        mx[2 * g + 1] = fmaxf(mx[2 * g + 1], a1 * (f * m.ks[x / 16 + 2 + g]));
+                    for (int e = 1; e < 15; e += 2) {
+                        a0 = max3(a0, s0[e], s0[e + 1]);
+                        a1 = max3(a1, s1[e], s1[e + 1]);
                     }
+                    a0 = fmaxf(a0, s0[15]);
+                    a1 = fmaxf(a1, s1[15]);
+                    mx[0] = fmaxf(mx[0], a0 * (f * m.ks[x / 16]));
+                    mx[1] = fmaxf(mx[1], a1 * (f * m.ks[x / 16 + 1]));
                 }
             } else {
 #pragma unroll 1
@@ -940,6 +938,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             float *gl = nullptr;
             if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
             const uint64_t nm = pack2(-msafe, -msafe);
+            const uint64_t minus = pack2(-1.0f, -1.0f);
             float cur[32];
             tm_ld32(ts, cur);
             tm_wait(cur);
@@ -977,7 +976,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                         p0 = __uint_as_float(__float_as_uint(p0) & 0xFFFFE000u);
                         p1 = __uint_as_float(__float_as_uint(p1) & 0xFFFFE000u);
                         hi[8 * g + e / 2] = half2_of(p0, p1);
-                        unpack2(add2(y, pack2(-p0, -p1)), p0, p1);
+                        unpack2(fma2(pack2(p0, p1), minus, y), p0, p1);
                         lo[8 * g + e / 2] = half2_of(p0, p1);
                     }
                     float q0, q1;
@@ -1040,7 +1039,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             const int64_t mine = !real ? -1 : m.place >= 0 ? to_part * D : (int64_t)ti * p.ldo + (int64_t)head * D;
             float *out = m.place >= 0 ? plan.parts : p.out, *lse = m.place >= 0 ? plan.part_lse + to_part : p.lse + (int64_t)ti * p.Hq + head;
             const int part = lane / LPR, col = lane % LPR;
-#pragma unroll 4
+#pragma unroll 8
             for (int r0 = 0; r0 < 32; r0 += RPI) {
                 const int rr = r0 + part;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
