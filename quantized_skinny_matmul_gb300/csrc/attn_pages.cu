@@ -925,9 +925,9 @@ int log2_of(int64_t x) {
 
 // Which kernel: a tile of the tensor-memory kernel holds 128 query rows of one KV head, as many as
 // there are; the row kernel's time grows with them.  Sequences with at most ROWS_MAX rows take it.
-// 16 sequences x 8 heads on 2048 tokens: 32 rows 72 us against 85 us in tiles, 64 rows 126 against
-// 85; 3 x 8 heads on 10000: 48 rows 83 against 80, 64 rows 103 against 80; 8 heads on 4096: 64 rows
-// 33 against 42.
+// 16 sequences x 8 heads on 2048 tokens: 32 rows 72 us against 82 in tiles, 64 rows 126 against 82;
+// 3 x 8 heads on 10000: 48 rows 83 against 77, 64 rows 103 against 78; 8 heads on 4096: 64 rows 33
+// against 42.
 constexpr int ROWS_MAX = 40;
 
 template <int KIND, int D, int NN>

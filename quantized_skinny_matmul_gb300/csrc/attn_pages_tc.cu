@@ -23,12 +23,12 @@
 // Items (sequence, head, pair of tiles) are taken from a list that a small kernel lays out, in
 // turn, longest first within a sequence; which CTA takes which does not change any result.
 //
-// A prompt of 4096 tokens x 32 heads (8 KV heads, D = 128): 300 us, 456 TFLOP/s of the formula's
-// operations, 912 of those issued (48% of a library product's rate).  A block of both tiles takes
-// about 7,400 cycles, 4,100 of them products: per tile, 4,700 from scores to weights, then 2,600 for
+// A prompt of 4096 tokens x 32 heads (8 KV heads, D = 128): 281 us, 489 TFLOP/s of the formula's
+// operations, 978 of those issued (52% of a library product's rate).  A block of both tiles takes
+// about 7,000 cycles, 4,100 of them products: per tile, 4,000 from scores to weights, then 2,600 for
 // the second half of its P V and the next Q K, which share the operands' memory with the widening;
-// an item's change takes about 20,000 more (8,000 to 10,000 of them the queries' loads).  Two threads
-// a row halve neither: twice the fixed work in half the registers (312 us).
+// an item's change takes about 25,000 more (14,000 of them the queries' loads).  Two threads a row
+// halve neither: twice the fixed work in half the registers (312 us when this was 288).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -58,7 +58,8 @@ constexpr int METAS = 4;                    // blocks whose data is kept
 // off by about N 2^-26 of itself, one way.  Every FLUSH blocks (16 products each) a tile's O is
 // added to a running sum in memory, rounded to nearest, and begun anew.  A row over 4,500 tokens is
 // off by 8e-6 without it, by 2.5e-6 every 8 blocks, 1.4e-6 every 4 and 0.9e-6 every 2 (elementary
-// operations in f32: 1.2e-6); a prompt of 4096 takes 288, 300 and 320 us with 8, 4 and 2.
+// operations in f32: 1.2e-6); a prompt of 4096 takes 266, 281 and 308 us with 8, 4 and 2 (a tile's
+// sums go out at 32 bytes a cycle: 2,000 cycles).
 constexpr int FLUSH = 4;
 constexpr int THREADS = 512;
 // Registers per thread of the four warpgroups: they add up to the 4 x 128 of the launch.  (A prompt
@@ -403,9 +404,9 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         x.splits = e.w;
         x.place = x.splits > 1 ? item : -1;
         x.s = attn_step(p, x.b);
-        // the queries, on their way to L2 while the item before is finished (read from there, they hold
-        // the start of an item up by 10 us less than from device memory)
-        for (int i = x.pair * 2 * BR / p.G + lane; i < x.s.n && i * p.G < (x.pair + 1) * 2 * BR; i += 32)
+        // the queries, on their way to L2 while the item before is finished (a prompt of 4096: 281 us,
+        // 285 without; the CTA's first ones are needed at once)
+        for (int i = nmeta == 0 ? x.s.n : x.pair * 2 * BR / p.G + lane; i < x.s.n && i * p.G < (x.pair + 1) * 2 * BR; i += 32)
             bulk_prefetch_l2(p.q + (int64_t)(x.s.t0 + i) * p.ldq + (int64_t)x.h * p.G * D, (uint32_t)(p.G * D * 4));
         const int end = x.s.held + x.s.n;    // slots in use (0 for an unusable sequence)
         // what the rows of each tile can see: positions lo .. hi, and those below pre
