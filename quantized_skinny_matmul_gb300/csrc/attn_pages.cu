@@ -847,7 +847,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
 // and are added in order.  The sums of groups that a row cannot see were never written: they are
 // passed over.  Bound by the latency of the loads, so many rows want many warps, unless the items
 // fill the GPU by themselves.  The whole step, 4 sequences of up to 1000 tokens x 2 heads of 8 KV heads
-// (64 items): 74 us, 109 with one CTA an item; 8 x 8 tokens x 8 heads on 4096 (512 items): 89 us with 4
+// (64 items): 74 us, 101 with one CTA an item; 8 x 8 tokens x 8 heads on 4096 (512 items): 91 us with 4
 // warps an item, 170 with 8 x 16.
 // ---------------------------------------------------------------------------
 template <int WW, int CL>
