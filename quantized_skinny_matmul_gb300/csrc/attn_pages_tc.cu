@@ -11,7 +11,7 @@
 //                    tensor memory, the weights' two terms go back in their place (the A
 //                    operand of the second product); also the query's conversion and the
 //                    output.  The output stays in tensor memory; it is rescaled only when a
-//                    row's maximum has grown by more than 2^8 (the weights have that room);
+//                    row's maximum has grown by more than 2^6 (the weights have that room);
 //   warps 8-11       widen the codes of a block of 128 tokens from the raw copies into the
 //                    128-byte-swizzled operands (K by rows for the first product; the same
 //                    layout of V is the token-major B operand of the second);
@@ -880,11 +880,13 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 tm_wait_st();
             }
             const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // The sums are relative to mrow, which may lag behind the maximum by 8 (the weights
-            // then reach 2^8), and O to 2^(vex - 4), where a value scale may exceed 2^vex by 8
-            // times: weights times scales stay below 2^15.
+            // The sums are relative to mrow, which may lag behind the maximum by 6 (the weights then
+            // reach 2^6), and O to 2^(vex - 8), where a value scale may reach 2^(vex + 1): weights times
+            // scales stay below 2^15.  fp16 ends at 2^-25: a weight times its scale is carried to 2^-33
+            // of the largest of both.  (A lag of 4 would carry it to 2^-35, but rescales O too often: a
+            // prompt of 4096 takes 311 us instead of 281; one of 8 saves nothing.)
             const int ve = exponent_of(vmax);
-            const bool grow = mb > mrow + 8.0f || (mrow == -INFINITY && mb != -INFINITY);
+            const bool grow = mb > mrow + 6.0f || (mrow == -INFINITY && mb != -INFINITY);
             // (this block's scores come after the products of the block before: O is complete up to it)
             if (blocks > 0 && blocks % FLUSH == 0) {
                 const float cs = carry();
@@ -912,7 +914,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
                 gex = vex;
             }
             const bool have_o = blocks % FLUSH != 0;
-            const int vnew = blocks == 0 || ve > vex + 3 ? ve : vex;
+            const int vnew = blocks == 0 || ve > vex + 1 ? ve : vex;
             if (__any_sync(0xffffffffu, grow) || vnew != vex) {
                 const float mnew = grow ? mb : mrow;
                 const float a = mnew == mrow ? 1.0f : ex2(mrow - mnew);
@@ -935,7 +937,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             blocks++;
             // ---- the weights: 32 tokens at a time, their two terms in the columns of their scores
             // (columns 0 .. 15 of each 32 the first term, 16 .. 31 the second)
-            const float msafe = mrow == -INFINITY ? 0.0f : mrow, vu = pow2i(4 - vex);
+            const float msafe = mrow == -INFINITY ? 0.0f : mrow, vu = pow2i(8 - vex);
             float *gl = nullptr;
             if (p.glse) gl = p.glse + ((int64_t)ti * p.Hq + head) * p.NG + (m.slot >> p.lgGroup);
             const uint64_t nm = pack2(-msafe, -msafe);
@@ -1006,7 +1008,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
         }
         if (flags & F_LAST) {
             const float l = lrow;
-            const float inv = l > 0.0f ? pow2i(vex - 4) / l : 0.0f;
+            const float inv = l > 0.0f ? pow2i(vex - 8) / l : 0.0f;
             const float cs = carry() * inv;
             if (!wait.warp(O_FULL + t, no++)) return;
             tc_after();

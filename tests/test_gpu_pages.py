@@ -262,6 +262,25 @@ def test_scales_of_every_size():
     check_attention(p, run_attention(p))
 
 
+@pytest.mark.parametrize("new", [1, 20])
+def test_many_weights_far_below_the_largest(new):
+    """2,000 keys of weight e^-18 beside the step's own: each is carried to 2^-33 of the largest."""
+    N, G, D, P = 2000, 8, 64, 16
+    p = ref.problem(10, 0, 1, 1, G, D, P, [N], [new])
+    p["q"][:] = 18.0 / (D * ref.SCALE(D))
+    p["ks"][:] = p["vs"][:] = np.float32(1 / 127)
+    for i in range(N + new):
+        page, slot = p["table"][0, 0, i // P], i % P
+        p["k"][page, slot], p["v"][page, slot] = (0, 100) if i < N else (127, 0)
+    want, *_ = ref.attend(0, P, p["k"], p["ks"], p["v"], p["vs"], p["table"], p["base"], p["held"], p["seen"], p["cu"], p["q"],
+                          ref.SCALE(D))
+    got = host(run_attention(p)).astype(np.float64)
+    # scales of 1/127 < 2^-6 times codes of 100; and z = 18 carries 2^-22 and a few roundings: 1e-4 of a weight
+    bound = N * 2.0 ** (-6 - 33) * 100
+    assert np.all(want > 3 * bound)
+    assert np.all(np.abs(got - want) <= bound + 1e-4 * want)
+
+
 def test_strided_rows_and_streams():
     p = ref.problem(8, 0, 2, 2, 4, 128, 64, [500, 77], [1, 1])
     want = host(run_attention(p))
