@@ -115,7 +115,7 @@ struct PlanView {
     int4 *list;                 // (sequence, pair of tiles, share, shares)
     float *parts;               // [place][2 BR][D]: a share's outputs; null: nothing is shared
     float *part_lse;            // [place][2 BR]: log2 of its denominators (infinity: nothing seen)
-    int places;
+    int places, room;           // room: entries that the list holds
     int *count, *next;          // entries, items taken
     float *sums;                // [CTA][2][D / 4][BR][4]: the tiles' flushed output sums
 };
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(256) attn_pages_plan_kernel(const AttnParams8 
         }
         return all;
     };
-    int at = 0, total = 0, most = 1;
+    int64_t at = 0, total = 0;
+    int most = 1;
     for (int phase = 0; phase < 2; phase++) {   // count the pairs, then write the list
         for (int b0 = 0; b0 < p.c.B; b0 += 256) {
             const int b = b0 + tid;
@@ -331,15 +332,19 @@ __global__ void __launch_bounds__(256) attn_pages_plan_kernel(const AttnParams8 
             }
             const int all = scan(phase ? pairs * splits : pairs, before);
             if (phase)
-                for (int i = 0; i < pairs * splits; i++)
+                for (int i = 0; i < pairs * splits && at + before + i < plan.room; i++)
                     plan.list[at + before + i] = make_int4(b, pairs - 1 - i / splits, i % splits, splits);
             if (phase) at += all;
             else total += all;
         }
-        if (phase == 0 && plan.parts && total > 0) most = max(1, min(MOST_SHARES, plan.places / max(1, total * p.c.Hkv)));
+        // Sequences whose rows are their own have no more pairs than the list holds.  A cu that decreases
+        // can name rows again and again: the pairs beyond are left out.
+        if (phase == 0 && total > plan.room && tid == 0) atomicOr(p.c.status, STATUS_RANGE);
+        if (phase == 0 && plan.parts && total > 0)
+            most = (int)max((int64_t)1, min((int64_t)MOST_SHARES, plan.places / (total * p.c.Hkv)));
     }
     if (tid == 0) {
-        *plan.count = at;
+        *plan.count = (int)min(at, (int64_t)plan.room);
         *plan.next = 0;
     }
 }
@@ -1226,6 +1231,7 @@ gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8
     PlanView plan{};
     plan.places = share_places(c, p.T, p.G);
     const int64_t entries = most_pairs(c, p.T, p.G) + plan.places;
+    plan.room = (int)std::min<int64_t>(entries, INT32_MAX);
     plan.count = reinterpret_cast<int *>(work);
     plan.next = plan.count + 1;
     plan.list = reinterpret_cast<int4 *>(work + 256);

@@ -1,0 +1,35 @@
+"""The paged 8-bit KV cache where a call is unusual: lengths and tables that are out of range, limits of
+positions, masked pages unlike the visible ones, steps of many rows (GPU only).  Bounds as in test_gpu_pages.py."""
+import numpy as np
+import pytest
+import torch
+
+import pages_ref as ref
+import quantized_skinny_matmul_gb300 as gq
+from test_gpu_pages import built, cache_of, check_attention, run_attention  # noqa: F401 (built: a fixture)
+from test_gpu_parity import dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+def repeated(p, times):
+    """The problem of one sequence as the 1st, 3rd, .. of a batch whose cu goes to n and back to 0."""
+    n, B = int(p["cu"][1]), 2 * times - 1
+    q = dict(p, cu=np.array([0, n] * times, np.int32))
+    for name in ("table", "base", "held", "seen"):
+        q[name] = np.repeat(p[name], B, axis=0)
+    return q
+
+
+# ---- lengths, tables and cu that are out of range -------------------------------------------------
+
+
+@pytest.mark.parametrize("Hkv,G,new,times", [(1, 8, 512, 40), (2, 8, 1100, 8)])
+def test_a_cu_that_goes_back_stays_within_the_plan(Hkv, G, new, times):
+    """Far more pairs of tiles than rows: what is written stays in bounds, and the fault is reported."""
+    p = ref.problem(20, 0, 1, Hkv, G, 64, 64, [70], [new])
+    out = run_attention(repeated(p, times))
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    check_attention(p, out)                  # all the sequences that name the rows are the same one
+    check_attention(p, run_attention(p))     # and the next call finds everything as it should be
+    assert gq.gq_last_error() == gq.GQ_OK
