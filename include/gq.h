@@ -437,9 +437,9 @@ gq_status gq_attn_decode_i8(const float *q, const int8_t *k, const float *k_scal
  * new tokens to both once the step's layers are done.
  * Sizes: D is 64 or 128; P is 16, 32, 64 or 128; NB * P < 2^30, B * Hkv * NB < 2^31,
  * pages < 2^31, pages * P * D <= 2^37.  Lengths, table entries and cu are read on the
- * device: a sequence for which they are out of range (held < 0, held + new > NB * P,
- * new > max_n, cu decreasing or past T) is skipped by append and gives zero rows in the
- * attention; a page outside [0, pages) is skipped, its tokens are seen by nobody;
+ * device: a sequence for which they are out of range (held < 0, seen < held, held + new >
+ * NB * P, new > max_n, cu decreasing or past T) is skipped by append and gives zero rows in
+ * the attention; a page outside [0, pages) is skipped, its tokens are seen by nobody;
  * either makes the next gq_last_error() return GQ_ERR_INVALID_ARG.  Rows that a cu which
  * decreases gives to several sequences hold what one of them makes of them, or nothing. */
 typedef enum { GQ_KV_I8 = 0, GQ_KV_E4M3 = 1 } gq_kv_kind;

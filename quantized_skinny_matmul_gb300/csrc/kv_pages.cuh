@@ -24,7 +24,8 @@ gq_status pages_view(const gq_kv_pages &c, PagesView *v);
 gq_status launch_pdl(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStream_t s, void **args, const char *what);
 
 // One sequence's part of a step, checked: a sequence whose lengths are out of range has no
-// new tokens (n = 0) and is reported by `bad`.
+// new tokens (n = 0) and is reported by `bad`.  (seen >= held: the attention's choice of slots
+// rests on no position being below its slot.)
 struct SeqStep {
     int t0, n, held, seen;   // first packed row, new tokens, tokens held before, position of the first new one
     bool bad;
@@ -38,7 +39,7 @@ __device__ __forceinline__ SeqStep seq_step(const PagesView &c, const int32_t *c
     s.seen = c.seen[b];
     const int64_t n = (int64_t)t1 - s.t0;
     s.bad = s.t0 < 0 || n < 0 || n > max_n || t1 > T || s.held < 0 || (int64_t)s.held + n > (int64_t)c.NB * c.P ||
-            s.seen < 0 || (int64_t)s.seen + n > (1LL << 30);
+            s.seen < s.held || (int64_t)s.seen + n > (1LL << 30);
     s.n = s.bad ? 0 : (int)n;
     return s;
 }

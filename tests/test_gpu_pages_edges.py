@@ -33,3 +33,25 @@ def test_a_cu_that_goes_back_stays_within_the_plan(Hkv, G, new, times):
     check_attention(p, out)                  # all the sequences that name the rows are the same one
     check_attention(p, run_attention(p))     # and the next call finds everything as it should be
     assert gq.gq_last_error() == gq.GQ_OK
+
+
+@pytest.mark.parametrize("new", [1, 3, 60])
+def test_positions_below_the_slots_are_reported(new):
+    """A next position below the tokens held: skipped, and no slot is sought below the first."""
+    p = ref.problem(21, 0, 2, 1, 2, 64, 16, [100, 40], [new, new])
+    p["seen"][0] = 30
+    before = p["k"].copy()
+    c, x = cache_of(p), np.ones((2 * new, 1, 64), np.float32)
+    gq.kv_pages_append(c, dev(x), dev(x), dev(p["cu"]), new)
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    changed = np.argwhere((host(c.k) != before).any((1, 2)))[:, 0]
+    assert set(changed) <= set(p["table"][1, 0])
+    first = np.where(np.arange(2 * new) < new, 2 ** 31 - 1, 0).astype(np.int32)     # of documents far ahead
+    out, w = run_attention(p, weights=np.ones(p["table"].shape, np.float32), first=first)
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    p["held"][0] = p["seen"][0] = 0          # the reference: a sequence that sees only itself, whose rows are then left out
+    want, ww, E, S, rel = ref.attend(0, 16, p["k"], p["ks"], p["v"], p["vs"], p["table"], p["base"], p["held"], p["seen"],
+                                     p["cu"], p["q"], ref.SCALE(64), weights=np.ones(p["table"].shape), first=first)
+    assert np.all(host(out)[:new] == 0.0) and np.all(host(w)[0] == 0.0)
+    assert np.all(np.abs(host(out) - want)[new:] <= (ref.tolerance(S[..., None], 40 + new) * E)[new:])
+    assert np.all(np.abs(host(w) - ww)[1] <= (ref.tolerance(0, 40 + new) * ww + ref.tolerance(1, 0) * rel)[1])
