@@ -494,30 +494,39 @@ def _packed(x, D: int, name: str):
     return shape[0], heads, stride[0] if shape[0] > 1 else heads * D
 
 
+# the tensors of gq_kv_pages (None: any type of one byte)
+_PAGES_DTYPES = dict(k=None, v=None, ks="float32", vs="float32", table="int32", base="int32", held="int32", seen="int32")
+
+
 class KVPages:
     """One layer's 8-bit KV cache in pages (gq_kv_pages): the tensors, kept alive, and their struct.
 
     k, v: one-byte codes [pages, P, D]; ks, vs: f32 [pages]; table, base: int32 [B, Hkv, NB];
-    held, seen: int32 [B], the tokens held and the next position before the step.
+    held, seen: int32 [B], the tokens held and the next position before the step.  Each may be
+    assigned another tensor of the same shape and type (what was captured into a graph keeps the
+    old one's address).
     """
 
     def __init__(self, kind, k, v, ks, vs, table, base, held, seen):
         pages, P, D = k.shape
         B, Hkv, NB = table.shape
-        _shape(k, (pages, P, D), None, "k")
-        _shape(v, (pages, P, D), None, "v")
-        for t, name in ((ks, "ks"), (vs, "vs")):
-            _shape(t, (pages,), "float32", name)
-        for t, name in ((table, "table"), (base, "base")):
-            _shape(t, (B, Hkv, NB), "int32", name)
-        for t, name in ((held, "held"), (seen, "seen")):
-            _shape(t, (B,), "int32", name)
-        self.kind, self.B, self.Hkv, self.D, self.P, self.NB, self.pages = kind, B, Hkv, D, P, NB, pages
-        self.k, self.v, self.ks, self.vs = k, v, ks, vs
-        self.table, self.base, self.held, self.seen = table, base, held, seen
-        self.struct = KVPagesStruct(kind, B, Hkv, D, P, NB, pages, *(_ptr(t) for t in (k, v, ks, vs, table, base, held,
-                                                                                    seen)))
-        self.by_ref = ctypes.pointer(self.struct)
+        tensors = dict(k=k, v=v, ks=ks, vs=vs, table=table, base=base, held=held, seen=seen)
+        shapes = dict(k=(pages, P, D), v=(pages, P, D), ks=(pages,), vs=(pages,), table=(B, Hkv, NB), base=(B, Hkv, NB),
+                      held=(B,), seen=(B,))
+        for name, t in tensors.items():
+            _shape(t, shapes[name], _PAGES_DTYPES[name], name)
+        struct = KVPagesStruct(kind, B, Hkv, D, P, NB, pages, *(_ptr(t) for t in tensors.values()))
+        vars(self).update(tensors, kind=kind, B=B, Hkv=Hkv, D=D, P=P, NB=NB, pages=pages, struct=struct,
+                          by_ref=ctypes.pointer(struct))
+
+    def __setattr__(self, name, value):
+        """Another tensor in the place of one: checked like the first, and its address goes into the struct."""
+        if name in _PAGES_DTYPES:
+            _shape(value, tuple(getattr(self, name).shape), _PAGES_DTYPES[name], name)
+            setattr(self.struct, name, _ptr(value))
+        elif name in vars(self):
+            raise AttributeError(f"{name}: a cache's kind and sizes are fixed, make another KVPages")
+        vars(self)[name] = value
 
     @classmethod
     def empty(cls, B: int, Hkv: int, D: int, tokens: int, page: int = 32, kind: int = GQ_KV_I8, device="cuda"):
@@ -533,16 +542,28 @@ class KVPages:
         return cls(kind, *codes, *scales, table, torch.zeros_like(table), *ints)
 
 
+# the tensors of gq_attn_scores
+_SCORES_DTYPES = dict(slopes="float32", first="int32", prefix="int32")
+
+
 class AttnScores:
-    """What attn_pages does to scores (gq_attn_scores); tensors are kept alive here."""
+    """What attn_pages does to scores (gq_attn_scores); tensors are kept alive here.  Every field may be assigned."""
 
     def __init__(self, scale: float, cap: float = 0.0, window: int = 0, slopes=None, first=None, prefix=None):
-        for t, dtype, name in ((slopes, "float32", "slopes"), (first, "int32", "first"), (prefix, "int32", "prefix")):
-            if t is not None:
-                _shape(t, tuple(t.shape), dtype, name)
+        struct = AttnScoresStruct()
+        vars(self).update(struct=struct, by_ref=ctypes.pointer(struct))
+        self.scale, self.cap, self.window = scale, cap, window
         self.slopes, self.first, self.prefix = slopes, first, prefix
-        self.struct = AttnScoresStruct(scale, cap, window, _ptr(slopes), _ptr(first), _ptr(prefix))
-        self.by_ref = ctypes.pointer(self.struct)
+
+    def __setattr__(self, name, value):
+        if name in ("struct", "by_ref"):
+            raise AttributeError(f"{name} cannot be assigned")
+        dtype = _SCORES_DTYPES.get(name)
+        if dtype and value is not None:
+            _shape(value, tuple(value.shape), dtype, name)
+        if dtype or name in ("scale", "cap", "window"):
+            setattr(self.struct, name, _ptr(value) if dtype else value)
+        vars(self)[name] = value
 
 
 def _shape(t, shape, dtype, name: str) -> None:

@@ -55,3 +55,21 @@ def test_positions_below_the_slots_are_reported(new):
     assert np.all(host(out)[:new] == 0.0) and np.all(host(w)[0] == 0.0)
     assert np.all(np.abs(host(out) - want)[new:] <= (ref.tolerance(S[..., None], 40 + new) * E)[new:])
     assert np.all(np.abs(host(w) - ww)[1] <= (ref.tolerance(0, 40 + new) * ww + ref.tolerance(1, 0) * rel)[1])
+
+
+def test_an_eviction_s_tensors_assigned_to_the_cache():
+    """The next call works on the new tensors, whatever becomes of the old ones' memory."""
+    p = ref.problem(22, 0, 2, 2, 2, 64, 16, [16 * 9, 16 * 7], [0, 0])
+    w = p["gen"].random(p["table"].shape).astype(np.float32)
+    c = cache_of(p)
+    c.table, c.base, _, c.held = gq.kv_pages_evict(c, dev(w), 4)
+    junk = [torch.full((4096,), 2 ** 30, dtype=torch.int32, device="cuda") for _ in range(64)]     # over the freed ones
+    p["table"], p["base"], _, p["held"] = ref.evict(16, p["table"], p["base"], w, p["held"], 4, 1, 1)
+    p.update(cu=np.array([0, 1, 2], np.int32), q=p["gen"].standard_normal((2, 4, 64)).astype(np.float32))
+    x = p["gen"].standard_normal((2, 2, 64)).astype(np.float32)
+    gq.kv_pages_append(c, dev(x), dev(x), dev(p["cu"]), 1)
+    p.update({n: host(getattr(c, n)) for n in ("k", "v", "ks", "vs", "base")})
+    for b in range(2):                       # the token's page begins where its table row says
+        assert np.all(p["base"][b, :, p["held"][b] // 16] == p["seen"][b])
+    check_attention(p, gq.attn_pages(c, dev(p["q"]), dev(p["cu"]), 1, gq.AttnScores(ref.SCALE(64))))
+    assert len(junk) == 64 and gq.gq_last_error() == gq.GQ_OK
