@@ -875,9 +875,9 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
             const int64_t r = (int64_t)(s.t0 + i) * p.Hq + h * p.G + y;
             const int qpos = s.seen + i;
             const float v = __ldcg(gl + r * p.NG), l = __ldcg(p.lse + r);
-            const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? __ldg(p.prefix + s.t0 + i) : 0;
+            const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? min(__ldg(p.prefix + s.t0 + i), 1 << 30) : 0;
             const int lo = p.window > 0 ? (int)max((int64_t)first, (int64_t)qpos - p.window + 1) : first;
-            const bool see = (x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre);
+            const bool see = used && ((x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre));
             sum += see ? ex2(v - l) : 0.0f;
         };
         if (WW == 4) {      // few rows

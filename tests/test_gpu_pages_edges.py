@@ -73,3 +73,17 @@ def test_an_eviction_s_tensors_assigned_to_the_cache():
         assert np.all(p["base"][b, :, p["held"][b] // 16] == p["seen"][b])
     check_attention(p, gq.attn_pages(c, dev(p["q"]), dev(p["cu"]), 1, gq.AttnScores(ref.SCALE(64))))
     assert len(junk) == 64 and gq.gq_last_error() == gq.GQ_OK
+
+
+# ---- limits of positions ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("new", [1, 50])             # rows, tiles
+@pytest.mark.parametrize("P,held", [(64, 70), (128, 130), (128, 500), (32, 70)])
+def test_a_prefix_without_end(P, held, new):
+    """INT32_MAX, all is seen: a last page whose groups of 32 tokens are partly unused gathers its own share only."""
+    p = ref.problem(23, 0, 2, 2, 1, 64, P, [held, 3], [new, 1])
+    prefix = np.full(new + 1, 2 ** 31 - 1, np.int32)
+    weights = p["gen"].random(p["table"].shape).astype(np.float32)
+    out, w = run_attention(p, weights=weights, decay=0.5, prefix=prefix)
+    check_attention(p, out, w, weights=weights, decay=0.5, prefix=prefix)
