@@ -743,8 +743,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             ti = s.t0 + (real ? r / p.G : 0);
             head = m.h * p.G + (real ? r % p.G : 0);
             qpos = s.seen + ti - s.t0;
-            firstp = p.first ? __ldg(p.first + ti) : 0;
-            pre = p.prefix ? min(__ldg(p.prefix + ti), 1 << 30) : 0;
+            // (positions are in [0, 2^30): within these limits no difference to one wraps)
+            firstp = p.first ? max(__ldg(p.first + ti), 0) : 0;
+            pre = p.prefix ? min(max(__ldg(p.prefix + ti), 0), 1 << 30) : 0;
             slope = p.slopes ? __ldg(p.slopes + head) * LOG2E : 0.0f;
             seelo = p.window > 0 ? (int)max((int64_t)firstp, (int64_t)qpos - p.window + 1) : firstp;
             all_lo = real ? seelo : 0;

@@ -87,3 +87,15 @@ def test_a_prefix_without_end(P, held, new):
     weights = p["gen"].random(p["table"].shape).astype(np.float32)
     out, w = run_attention(p, weights=weights, decay=0.5, prefix=prefix)
     check_attention(p, out, w, weights=weights, decay=0.5, prefix=prefix)
+
+
+@pytest.mark.parametrize("new", [1, 50])
+@pytest.mark.parametrize("least", [-2 ** 31, -2 ** 31 + 5, -1])
+def test_documents_and_prefixes_that_begin_far_below_zero(least, new):
+    """The least int32 as a start or as a prefix's end is as good as none."""
+    p = ref.problem(24, 1, 1, 2, 1, 64, 16, [200], [new])
+    for name in ("first", "prefix"):
+        opt = {name: np.full(new, least, np.int32)}
+        weights = p["gen"].random(p["table"].shape).astype(np.float32)
+        out, w = run_attention(p, weights=weights, window=150, **opt)
+        check_attention(p, out, w, weights=weights, window=150, **opt)
