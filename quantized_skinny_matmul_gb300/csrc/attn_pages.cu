@@ -866,10 +866,12 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
     const int end = s.bad ? 0 : s.held + s.n, slot = g << p.lgGroup;
     const int64_t at = (int64_t)bh * c.NB + j;
     const bool used = slot < end;        // (a page is in use if its first group is)
+    // an entry that is no page: seen by nobody, and its sums may never have been written
+    const bool there = used && (unsigned)c.table[at] < (unsigned)c.pages;
     float sum = 0.0f;
-    if (__any_sync(0xffffffffu, used)) {
-        const int x0 = used ? c.base[at] + (slot & (c.P - 1)) : 0x7f000000, x1 = used ? x0 + size - 1 : 0x7f000000;
-        const float *gl = p.glse + (used ? g : 0);
+    if (__any_sync(0xffffffffu, there)) {
+        const int x0 = there ? c.base[at] + (slot & (c.P - 1)) : 0x7f000000, x1 = there ? x0 + size - 1 : 0x7f000000;
+        const float *gl = p.glse + (there ? g : 0);
         // (loads of rows and groups that were never written are within the buffer, and passed over)
         auto row = [&](int i, int y) {
             const int64_t r = (int64_t)(s.t0 + i) * p.Hq + h * p.G + y;
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
             const float v = __ldcg(gl + r * p.NG), l = __ldcg(p.lse + r);
             const int first = p.first ? __ldg(p.first + s.t0 + i) : 0, pre = p.prefix ? min(__ldg(p.prefix + s.t0 + i), 1 << 30) : 0;
             const int lo = p.window > 0 ? (int)max((int64_t)first, (int64_t)qpos - p.window + 1) : first;
-            const bool see = used && ((x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre));
+            const bool see = there && ((x1 >= lo && x0 <= qpos && lo <= qpos) || (x0 < pre && x1 >= first && first < pre));
             sum += see ? ex2(v - l) : 0.0f;
         };
         if (WW == 4) {      // few rows

@@ -99,3 +99,17 @@ def test_documents_and_prefixes_that_begin_far_below_zero(least, new):
         weights = p["gen"].random(p["table"].shape).astype(np.float32)
         out, w = run_attention(p, weights=weights, window=150, **opt)
         check_attention(p, out, w, weights=weights, window=150, **opt)
+
+
+@pytest.mark.parametrize("new", [2, 50])
+def test_pages_that_are_none_gather_nothing(new):
+    """A block of tokens without a usable page: its weight is what decay leaves of the old one."""
+    p = ref.problem(25, 0, 2, 2, 1, 64, 128, [300, 300], [new, new])
+    weights = p["gen"].random(p["table"].shape).astype(np.float32)
+    run_attention(p, weights=weights)        # (leaves sums of its own where the next call's are kept)
+    q = dict(p, table=p["table"].copy(), base=p["base"].copy())
+    p["table"][0, 0, 1], p["table"][1, 1, 0] = 10 ** 6, -1
+    q["base"][0, 0, 1] = q["base"][1, 1, 0] = 1 << 29        # the reference: positions that nobody sees
+    out, w = run_attention(p, weights=weights, decay=0.5)
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    check_attention(q, out, w, weights=weights, decay=0.5)
