@@ -431,8 +431,9 @@ gq_status gq_attn_decode_i8(const float *q, const int8_t *k, const float *k_scal
  *   seen    int32 [B]: position of the step's first token; held[b] without eviction,
  *           more after it.  Positions stay below 2^30.
  * A step's new tokens come packed: sequence b has rows cu[b] .. cu[b+1] - 1 of k, v, q
- * and out (cu int32 [B+1], cu[0] = 0, T = cu[B] rows, at most max_n per sequence, zero
- * allowed).  They take slots held[b], held[b]+1, .. and positions seen[b], seen[b]+1, ..
+ * and out (cu int32 [B+1], cu[0] = 0, cu[B] of the T rows, at most max_n per sequence, zero
+ * allowed; T > cu[B] pads a step, as a captured one is: rows from cu[B] on are neither read
+ * nor written).  They take slots held[b], held[b]+1, .. and positions seen[b], seen[b]+1, ..
  * Every call of a step reads held and seen as they were before it; the caller adds the
  * new tokens to both once the step's layers are done.
  * Sizes: D is 64 or 128; P is 16, 32, 64 or 128; NB * P < 2^30, B * Hkv * NB < 2^31,

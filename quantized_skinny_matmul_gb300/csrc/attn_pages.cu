@@ -952,7 +952,8 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
     const size_t lse = w_out ? ((size_t)T * p.Hq * 4 + 255) / 256 * 256 : 0;
     const size_t glse = w_out ? ((size_t)T * p.Hq * p.NG * 4 + 255) / 256 * 256 : 0;
     const bool tiles = (int64_t)p.max_n * p.G > ROWS_MAX;
-    // every sequence may still be small; with equal lengths, or one sequence, none is
+    // Some sequence may still be small; with equal lengths, or one sequence, none should be (one that is,
+    // in a step of fewer rows than T, is left to the tiles with the others)
     const bool rows = !tiles || (c.B > 1 && T < c.B * (int64_t)p.max_n);
     const size_t plan = tiles ? attn_pages_tc_workspace(c, T, p.G) : 0;
     Workspace ws{};
@@ -962,7 +963,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
     p.part_ml = reinterpret_cast<float *>(ws.data + parts);
     p.lse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls) : nullptr;
     p.glse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls + lse) : nullptr;
-    p.rows_over = tiles ? ROWS_MAX : INT32_MAX;
+    p.rows_over = !tiles ? INT32_MAX : rows ? ROWS_MAX : 0;
     if (tiles) KV_TRY(launch_attn_pages_tc(p, c, ws.data + parts + mls + lse + glse, s));
     if (rows) {
         alignas(64) CUtensorMap kmap, vmap;

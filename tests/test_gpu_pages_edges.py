@@ -113,3 +113,26 @@ def test_pages_that_are_none_gather_nothing(new):
     out, w = run_attention(p, weights=weights, decay=0.5)
     assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
     check_attention(q, out, w, weights=weights, decay=0.5)
+
+
+@pytest.mark.parametrize("G,T,max_n,cu", [
+    (1, 200, 100, [0, 30, 130]),             # the host's numbers say that both have 100
+    (2, 100, 100, [0, 3]),
+    (1, 100, 100, [0, 0]),
+    (1, 300, 100, [0, 100, 100, 140]),
+])
+def test_fewer_rows_than_the_call_is_made_for(G, T, max_n, cu):
+    """A padded step, as a captured one is: every sequence's rows are worked out, those past cu[B] are left alone."""
+    new = np.diff(cu)
+    p = ref.problem(26, 0, len(new), 2, G, 64, 32, [150] * len(new), new)
+    n, weights = cu[-1], p["gen"].random(p["table"].shape).astype(np.float32)
+    q = torch.randn((T, 2 * G, 64), device="cuda")
+    q[:n] = dev(p["q"])
+    out, w, nan = torch.full((T, 2 * G, 64), 7.0, device="cuda"), dev(weights), np.full(p["table"].shape, np.nan, np.float32)
+    run_attention(p if n else ref.problem(26, 0, 1, 2, G, 64, 32, [0], [1]))
+    for new_w in (dev(nan), dev(nan)):       # (sums of the first call are there in the second)
+        gq.gq_attn_pages(cache_of(p), gq.AttnScores(ref.SCALE(64)), q, 2 * G * 64, dev(p["cu"]), T, max_n, 2 * G, out,
+                         2 * G * 64, w, new_w, 0.5)
+        check_attention(p, out[:n], new_w, weights=weights, decay=0.5)
+        assert torch.all(out[n:] == 7.0)
+    assert gq.gq_last_error() == gq.GQ_OK
