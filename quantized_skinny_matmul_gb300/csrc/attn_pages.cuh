@@ -90,7 +90,7 @@ __device__ __forceinline__ SeqStep attn_step(const AttnParams8 &p, int b) {
     SeqStep s = seq_step(p.c, p.cu, b, p.T, p.max_n);
     if (s.bad) {
         const int t1 = p.cu[b + 1];
-        const bool rows = s.t0 >= 0 && t1 > s.t0 && t1 <= p.T && t1 - s.t0 <= p.max_n;
+        const bool rows = s.t0 >= 0 && t1 > s.t0 && t1 <= p.T;   // (more than max_n too)
         s.n = rows ? t1 - s.t0 : 0;
         s.held = -s.n;
         s.seen = 0;

@@ -136,3 +136,29 @@ def test_fewer_rows_than_the_call_is_made_for(G, T, max_n, cu):
         check_attention(p, out[:n], new_w, weights=weights, decay=0.5)
         assert torch.all(out[n:] == 7.0)
     assert gq.gq_last_error() == gq.GQ_OK
+
+
+@pytest.mark.parametrize("G,T,max_n,cu", [
+    (1, 200, 100, [0, 30, 200]),             # tiles alone, by the host's numbers
+    (1, 250, 100, [0, 30, 200, 250]),        # tiles and rows
+    (2, 5, 2, [0, 1, 4, 5]),                 # rows
+    (1, 170, 100, [0, 170]),
+])
+def test_more_new_tokens_than_said_give_zero_rows(G, T, max_n, cu):
+    new = np.diff(cu)
+    p = ref.problem(27, 1, len(new), 2, G, 64, 32, [150] * len(new), new)
+    weights = p["gen"].random(p["table"].shape).astype(np.float32)
+    want, ww, E, S, rel = ref.attend(1, 32, p["k"], p["ks"], p["v"], p["vs"], p["table"], p["base"], p["held"], p["seen"],
+                                     p["cu"], p["q"], ref.SCALE(64), weights=weights)
+    out = torch.full((T, 2 * G, 64), 7.0, device="cuda")
+    _, w = gq.attn_pages(cache_of(p), dev(p["q"]), dev(p["cu"]), max_n, gq.AttnScores(ref.SCALE(64)), weights=dev(weights),
+                         out=out)
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    out, w, N = host(out), host(w), 150 + max_n
+    for b, n in enumerate(new):
+        rows = slice(cu[b], cu[b + 1])
+        if n > max_n:
+            assert np.all(out[rows] == 0.0) and np.all(w[b] == 0.0)
+        else:
+            assert np.all(np.abs(out - want)[rows] <= (ref.tolerance(S[..., None], N) * E)[rows])
+            assert np.all(np.abs(w - ww)[b] <= (ref.tolerance(0, N) * ww + ref.tolerance(1, 0) * rel)[b])
