@@ -469,7 +469,9 @@ gq_status gq_kv_pages_append(const gq_kv_pages *cache, const float *k, int64_t l
 
 /* Reads slots back as f32: the slots start[b] .. start[b] + cu[b+1] - cu[b] - 1 of
  * sequence b into rows cu[b] .. of k and v ([T][Hkv][D], either may be NULL), as
- * code * scale.  start int32 [B]; slots must lie in [0, NB * P). */
+ * code * scale.  start int32 [B]; slots must lie in [0, NB * P): a sequence for which they do
+ * not, or with more than max_n, gives zero rows, a page outside [0, pages) zeros for its
+ * tokens, and either is reported as above. */
 gq_status gq_kv_pages_read(const gq_kv_pages *cache, const int32_t *start, const int32_t *cu, int64_t T, int64_t max_n,
                            float *k, float *v, cudaStream_t stream);
 

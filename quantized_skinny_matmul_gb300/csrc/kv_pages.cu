@@ -273,6 +273,11 @@ __global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadPar
     const int64_t n = (int64_t)t1 - t0;
     if (t0 < 0 || n < 0 || n > p.max_n || t1 > p.T || s0 < 0 || s0 + n > ((int64_t)c.NB << logP)) {
         if (threadIdx.x == 0 && tile == 0) atomicOr(c.status, STATUS_RANGE);
+        // rows of zeros, if cu itself is sound: this warp's head, the tiles' tokens in turn
+        if (out && h < c.Hkv && t0 >= 0 && t1 <= p.T)
+            for (int64_t i = tile; i < n; i += p.tiles)
+                for (int x = lane; x < Q; x += 32)
+                    reinterpret_cast<float4 *>(out + ((t0 + i) * c.Hkv + h) * D)[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         return;
     }
     const int i0 = tile * RD_TOKENS, ni = min(RD_TOKENS, (int)n - i0), slot = s0 + i0;
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadPar
     for (int e = 0; e < 2; e++) {
         const bool bad = (unsigned)page[e] >= (unsigned)c.pages;
         if (bad && lane == 0) atomicOr(c.status, STATUS_RANGE);
-        if (bad) page[e] = -1;   // its tokens are left out
+        if (bad) page[e] = -1;   // its tokens are zero
         s[e] = bad ? 0.0f : __ldg(scale + page[e]);
     }
     const int col = lane % Q, part = lane / Q;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(RD_THREADS) kv_pages_read_kernel(const ReadPar
         f.y *= s[e];
         f.z *= s[e];
         f.w *= s[e];
-        if (i < ni && page[e] >= 0)
+        if (i < ni)
             reinterpret_cast<float4 *>(out + ((int64_t)(t0 + i0 + i) * c.Hkv + h) * D)[col] = f;
     }
 }

@@ -162,3 +162,29 @@ def test_more_new_tokens_than_said_give_zero_rows(G, T, max_n, cu):
         else:
             assert np.all(np.abs(out - want)[rows] <= (ref.tolerance(S[..., None], N) * E)[rows])
             assert np.all(np.abs(w - ww)[b] <= (ref.tolerance(0, N) * ww + ref.tolerance(1, 0) * rel)[b])
+
+
+@pytest.mark.parametrize("kind", [gq.GQ_KV_I8, gq.GQ_KV_E4M3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_cannot_be_read_back_is_zero(kind, D):
+    """Sequences whose slots are out of range, and pages that are none."""
+    p = ref.problem(28, kind, 5, 2, 1, D, 16, [60] * 5, [0] * 5)
+    NB = p["table"].shape[2]
+    p["table"][3, 1, 1] = 10 ** 6
+    start, n = np.array([-1, 5, NB * 16 - 3, 10, 0], np.int32), [20, 40, 4, 30, 90]
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    T, max_n = int(cu[-1]), 60               # the last one has more than max_n
+    got = [torch.full((T, 2, D), 7.0, device="cuda") for _ in range(2)]
+    gq.gq_kv_pages_read(cache_of(p), dev(start), dev(cu), T, max_n, *got)
+    assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+    for name, r in zip(("k", "v"), got):
+        r = host(r)
+        for b in (0, 2, 4):
+            assert np.all(r[cu[b]:cu[b + 1]] == 0.0), b
+        for b in (1, 3):
+            for i in range(n[b]):
+                s = start[b] + i
+                for h in range(2):
+                    pg = p["table"][b, h, s // 16]
+                    want = 0.0 if pg == 10 ** 6 else ref.decode(kind, p[name][pg, s % 16]) * np.float64(p[name + "s"][pg])
+                    assert np.array_equal(r[cu[b] + i, h], np.broadcast_to(np.float32(want), D)), (b, i, h)
