@@ -562,7 +562,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
             mrow[nn] = -INFINITY;
             lrow[nn] = 0.0f;
         }
-        int vex = -100;   // the sums are in units of 2^(vex - 14)
+        int vex[NN];   // a row's sums are in units of 2^(vex - 14); the largest value scale it has seen is below 2^vex
+#pragma unroll
+        for (int nn = 0; nn < NN; nn++) vex[nn] = -100;
 
         // unit u of the item is unit count + u - u0 of this CTA; warp w takes every W-th
         for (int u = u0 + (warp + W - count % W) % W; u < u1; u += W) {
@@ -629,6 +631,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
             }
             const bool whole = live == UNIT && m.base[0] >= all_lo && m.base[1] >= all_lo && m.base[0] + 15 <= all_hi &&
                                m.base[1] + 15 <= all_hi;   // warp-uniform
+            float vmax[NN];   // the larger value scale of the halves that the row sees some of
+#pragma unroll
+            for (int nn = 0; nn < NN; nn++) vmax[nn] = whole ? fmaxf(m.vs[0], m.vs[1]) : 0.0f;
             if (!whole) {
 #pragma unroll
                 for (int mt = 0; mt < 2; mt++)
@@ -641,25 +646,35 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
                                              (x < pre[nn] || (x >= seelo[nn] && x <= qpos[nn]));
                             s[mt][nn][e] = see ? s[mt][nn][e] : -INFINITY;
                         }
+#pragma unroll
+                for (int mt = 0; mt < 2; mt++)
+#pragma unroll
+                    for (int nn = 0; nn < NN; nn++) {   // x0 .. x1 - 1: the half's positions
+                        const int x0 = m.base[mt], x1 = x0 + min(live - 16 * mt, 16);
+                        const bool some = max(x0, seelo[nn]) < min(x1, qpos[nn] + 1) || max(x0, firstp[nn]) < min(x1, pre[nn]);
+                        // (times a weight of 0, a masked half's scale only has to stay finite: 2^-112 of it counts)
+                        vmax[nn] = fmaxf(vmax[nn], m.vs[mt] * (some ? 1.0f : 0x1p-112f));
+                    }
             }
             // ---- the running maxima
-            const float vs0 = m.vs[0], vs1 = m.vs[1];
-            const int ve = max(vex, min(max((int)((__float_as_uint(fmaxf(vs0, vs1)) >> 23) & 255u) - 126, -100), 126));
+            int ve[NN];
             float mnew[NN];
-            bool grow = ve != vex;
+            bool grow = false;
 #pragma unroll
             for (int nn = 0; nn < NN; nn++) {
                 float mx = fmaxf(fmaxf(s[0][nn][0], s[0][nn][1]), fmaxf(s[1][nn][0], s[1][nn][1]));
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                 mnew[nn] = fmaxf(mrow[nn], mx);
-                grow = grow || mnew[nn] > mrow[nn];
+                ve[nn] = max(vex[nn], min(max((int)((__float_as_uint(vmax[nn]) >> 23) & 255u) - 126, -100), 126));
+                grow = grow || mnew[nn] > mrow[nn] || ve[nn] != vex[nn];
             }
             if (__any_sync(0xffffffffu, grow)) {
-                // 2^(vex - ve): exact, 0 when it would underflow
-                const float ov = vex - ve < -126 ? 0.0f : __uint_as_float((uint32_t)(vex - ve + 127) << 23);
 #pragma unroll
                 for (int nn = 0; nn < NN; nn++) {
+                    // 2^(vex - ve): exact, 0 when it would underflow
+                    const int dv = vex[nn] - ve[nn];
+                    const float ov = dv < -126 ? 0.0f : __uint_as_float((uint32_t)(dv + 127) << 23);
                     const float a = mnew[nn] > mrow[nn] ? ex2(mrow[nn] - mnew[nn]) : 1.0f;   // 0 while nothing was seen
                     lrow[nn] *= a;
                     const float av = a * ov;
@@ -671,20 +686,20 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
                         o[y][nn][3] *= av;
                     }
                     mrow[nn] = mnew[nn];
+                    vex[nn] = ve[nn];
                 }
-                vex = ve;
             }
             // ---- weights; times value scales, in units of 2^(vex - 14), as two fp16 terms, moved to the
             // lanes that multiply them: column g8 is row g8 / 2's hi (even) or lo term
-            const float vu = __uint_as_float((uint32_t)(14 - vex + 127) << 23);
             uint32_t pb[2][NN][2];
 #pragma unroll
             for (int nn = 0; nn < NN; nn++) {
+                const float vu = __uint_as_float((uint32_t)(14 - vex[nn] + 127) << 23);
                 const float msafe = mrow[nn] == -INFINITY ? 0.0f : mrow[nn];
                 float gsum[2];
 #pragma unroll
                 for (int mt = 0; mt < 2; mt++) {
-                    const float p0 = ex2(s[mt][nn][0] - msafe), p1 = ex2(s[mt][nn][1] - msafe), vv = (mt ? vs1 : vs0) * vu;
+                    const float p0 = ex2(s[mt][nn][0] - msafe), p1 = ex2(s[mt][nn][1] - msafe), vv = m.vs[mt] * vu;
                     gsum[mt] = p0 + p1;
                     uint32_t hi, lo;
                     split2(p0 * vv, p1 * vv, hi, lo);
@@ -765,9 +780,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
 
         // ---- join the warps: sums in units of 2^0, relative to the warp's own maximum.  Lane (g8, t)
         // holds positions D / 8 g8 .. of row 4 nn + t; 16-byte chunk y of row r lies at y ^ r
-        const float vscale = __uint_as_float((uint32_t)(vex - 14 + 127) << 23);
 #pragma unroll
         for (int nn = 0; nn < NN; nn++) {
+            const float vscale = __uint_as_float((uint32_t)(vex[nn] - 14 + 127) << 23);
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) lrow[nn] += __shfl_xor_sync(0xffffffffu, lrow[nn], d);
             const int r = 4 * nn + t;

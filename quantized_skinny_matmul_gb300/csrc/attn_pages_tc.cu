@@ -820,12 +820,13 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
         if (flags & (F_TILE0 << t)) {
             const int live = m.live;
             bool whole = live == BT;   // every row sees every token (warp-uniform)
-            float vmax = 0.0f;
+            float vmax = 0.0f;         // the largest value scale of the groups that the row sees some of
 #pragma unroll
             for (int g = 0; g < GROUPS; g++) {
                 whole = whole && m.base[g] >= all_lo && m.base[g] + 15 <= all_hi;
                 vmax = fmaxf(vmax, m.vs[g]);
             }
+            if (!whole) vmax = 0.0f;
             const bool simple = whole && p.cap == 0.0f && !p.slopes;
             if (!wait.warp(S_FULL + t, ns++)) return;
             tc_after();
@@ -875,6 +876,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
 #pragma unroll
                         for (int e = 0; e < 16; e++)
                             if (!(see & (1u << e))) s[e] = -INFINITY;
+                        // (times a weight of 0, a masked group's scale only has to stay finite: 2^-112 of it counts)
+                        vmax = fmaxf(vmax, m.vs[g] * (see ? 1.0f : 0x1p-112f));
                     }
 #pragma unroll
                     for (int e = 0; e < 16; e++) mx[e & 3] = fmaxf(mx[e & 3], s[e]);
@@ -889,8 +892,10 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             // The sums are relative to mrow, which may lag behind the maximum by 6 (the weights then
             // reach 2^6), and O to 2^(vex - 8), where a value scale may reach 2^(vex + 1): weights times
             // scales stay below 2^15.  fp16 ends at 2^-25: a weight times its scale is carried to 2^-33
-            // of the largest of both.  (A lag of 4 would carry it to 2^-35, but rescales O too often: a
-            // prompt of 4096 takes 311 us instead of 281; one of 8 saves nothing.)
+            // of the largest of both among the tokens that the row sees (vex is the row's own: the scales
+            // of masked groups would push small values below that; the whole block's, for all rows alike,
+            // took 282 us where this takes 284).  (A lag of 4 would carry it to 2^-35, but rescales O too
+            // often: a prompt of 4096 takes 311 us instead of 281; one of 8 saves nothing.)
             const int ve = exponent_of(vmax);
             const bool grow = mb > mrow + 6.0f || (mrow == -INFINITY && mb != -INFINITY);
             // (this block's scores come after the products of the block before: O is complete up to it)
@@ -921,7 +926,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams8 &p, uint8_t *smem
             }
             const bool have_o = blocks % FLUSH != 0;
             const int vnew = blocks == 0 || ve > vex + 1 ? ve : vex;
-            if (__any_sync(0xffffffffu, grow) || vnew != vex) {
+            if (__any_sync(0xffffffffu, grow || vnew != vex)) {
                 const float mnew = grow ? mb : mrow;
                 const float a = mnew == mrow ? 1.0f : ex2(mrow - mnew);
                 lrow *= a;

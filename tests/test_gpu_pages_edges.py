@@ -188,3 +188,45 @@ def test_what_cannot_be_read_back_is_zero(kind, D):
                     pg = p["table"][b, h, s // 16]
                     want = 0.0 if pg == 10 ** 6 else ref.decode(kind, p[name][pg, s % 16]) * np.float64(p[name + "s"][pg])
                     assert np.array_equal(r[cu[b] + i, h], np.broadcast_to(np.float32(want), D)), (b, i, h)
+
+
+
+
+# ---- masked pages unlike the visible ones ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", [gq.GQ_KV_I8, gq.GQ_KV_E4M3])
+@pytest.mark.parametrize("Hkv,G,D,P,new,more", [
+    (2, 1, 128, 16, 2, 0), (2, 1, 64, 32, 4, 160), (1, 4, 128, 16, 2, 0), (1, 3, 64, 64, 5, 160),        # rows: alone, and
+    (2, 5, 128, 128, 8, 160), (1, 4, 128, 16, 2, 160),                                                   # many units a warp
+    (2, 1, 128, 16, 60, 0), (1, 4, 64, 32, 40, 0), (1, 8, 128, 128, 70, 0), (1, 2, 64, 16, 300, 0),        # tiles
+])
+@pytest.mark.parametrize("opts", ["first", "window", "prefix"])
+def test_values_of_masked_pages_do_not_matter(kind, Hkv, G, D, P, new, more, opts):
+    """Pages whose values are 2^60 times the others': rows that do not see them keep their own values whole."""
+    # (`more` sequences fill the GPU, so that a CTA has whole items and a warp several units)
+    p = ref.problem(29, kind, 1 + more, Hkv, G, D, P, [300] + [640] * more, [new] + [1] * more)
+    T, qpos = new + more, p["seen"][0] + np.arange(new + more)
+    border = 300 // P * P // 2 // P * P      # the loud pages begin with the sequence and end here
+    for h in range(Hkv):
+        p["vs"][p["table"][0, h, :border // P]] *= np.float32(2.0 ** 60)
+    if opts == "first":                      # every other row sees them
+        opt = dict(first=np.where(np.arange(T) % 2 == 1, 0, border).astype(np.int32))
+    elif opts == "window":                   # the first rows see one token of them, or a few
+        opt = dict(window=int(qpos[0] - border + 1 + min(3, new // 2)))
+    else:                                    # none but the odd rows' prefix
+        opt = dict(window=int(qpos[0] - border), prefix=np.where(np.arange(T) % 2 == 1, border // 2, 0).astype(np.int32))
+    weights = np.ones(p["table"].shape, np.float32)
+    out, w = run_attention(p, weights=weights, **opt)
+    opt = {n: v[:new] if n != "window" else v for n, v in opt.items()}
+    one = dict(p, held=p["held"][:1], seen=p["seen"][:1], cu=p["cu"][:2], q=p["q"][:new], table=p["table"][:1], base=p["base"][:1])
+    names = ("kind", "P", "k", "ks", "v", "vs", "table", "base", "held", "seen", "cu", "q")
+    want, ww, E, S, rel = ref.attend(*(one[n] for n in names), ref.SCALE(D), weights=weights[:1], **opt)
+    # the rows that see none of the loud pages (those that do are bound by them, by a share of 2^-33 at least)
+    start = np.maximum(opt.get("first", np.zeros(new, np.int64)), qpos[:new] - opt.get("window", 10 ** 6) + 1)
+    quiet = (start >= border) & (opt.get("prefix", np.zeros(new)) == 0)
+    assert quiet.sum() >= new // 2
+    N = 300 + new
+    assert np.all(np.abs(host(out)[:new] - want)[quiet] <= (ref.tolerance(S[..., None], N) * E)[quiet])
+    assert np.all(np.abs(host(w)[0] - ww[0]) <= ref.tolerance(0, N) * ww[0] + ref.tolerance(1, 0) * rel[0])
+    assert np.all(np.isfinite(host(out)))
