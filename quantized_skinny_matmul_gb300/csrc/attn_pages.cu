@@ -73,6 +73,15 @@ constexpr int MAX_SLOTS = 10;
 constexpr int METAS = 128;
 static_assert(ITEMS == 2 && 16 >= MAX_SLOTS, "a unit's data stays until it is done");
 
+// The tensor cores add to their f32 accumulators with truncation, one way: values of one sign that a warp
+// sums over 9, 37, 146 and 585 units (a sequence of 2048 .. 131072 tokens in one CTA) came out 0.6, 4, 24
+// and 110 e-6 of themselves too small.  So every FLUSH_UNITS units of a warp its sums are added to sums
+// in shared memory, rounded to nearest, and begun anew: off by 0.5e-6 at every length (16 units: 1.2e-6).
+// 64 sequences x 8 heads on 32768 tokens take 626 us with 4 rows a head and 781 with 8 (without: 623 and
+// 757).  Where no warp can have more than FLUSH_FROM units of an item the kernel does without: the
+// code alone costs 128 sequences on 2048 tokens 240 us for 235, and 1.2e-6 at most is left.
+constexpr int FLUSH_UNITS = 8, FLUSH_FROM = 16;
+
 struct UnitMeta {               // of a unit: scales and first positions of the two halves
     float ks[2], vs[2];
     int base[2];
@@ -96,6 +105,7 @@ struct RowsSmem {
     UnitMeta meta[METAS];       // of unit u of an item at (its first unit's place + u) mod METAS
     ItemRec item[ITEMS];
     float ml[WARPS][ROWS_MOST][2];    // maximum and denominator of each warp
+    float2 sum_unit[WARPS][ROWS_MOST];   // of each warp's flushed sums: the maximum they are relative to, and vex as 2^vex
     int64_t start, total;       // line position of the sequence that the CTA starts in
     int start_b, last, failed;
     int64_t warp_sum[WARPS + 1];
@@ -251,7 +261,7 @@ __device__ __forceinline__ void join_pieces(const AttnParams8 &p, const ItemRec 
     }
 }
 
-template <int KIND, int D, int NN>
+template <int KIND, int D, int NN, bool FLUSH>
 __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
     attn_pages_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const AttnParams8 p) {
@@ -566,8 +576,46 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
 #pragma unroll
         for (int nn = 0; nn < NN; nn++) vex[nn] = -100;
 
+        // Flushed sums of the warp: lane (g8, t) holds positions D / 8 g8 .. of row 4 nn + t, at the place
+        // where the item's end puts them (16-byte chunk y of row r lies at y ^ r).
+        int done = 0;   // units of the item so far
+        const uint32_t mine = smem_addr(red) + (uint32_t)((warp * ROWS + t) * D * 4);
+        auto chunk = [&](int nn, int x) { return mine + (uint32_t)(4 * nn * D * 4) + (((D / 32 * g8 + x / 2) ^ (4 * nn + t)) << 4); };
+        // what takes the flushed sums to the present units: 2^(their maximum - the present one) 2^(their vex - the present one)
+        auto carry = [&](int nn) {
+            const float2 was = sm.sum_unit[warp][4 * nn + t];
+            const float a = was.x == mrow[nn] ? 1.0f : ex2(was.x - mrow[nn]);
+            return a * was.y * __uint_as_float((uint32_t)(127 - vex[nn]) << 23);
+        };
+
         // unit u of the item is unit count + u - u0 of this CTA; warp w takes every W-th
         for (int u = u0 + (warp + W - count % W) % W; u < u1; u += W) {
+            if (FLUSH && done > 0 && done % FLUSH_UNITS == 0) {
+#pragma unroll
+                for (int nn = 0; nn < NN; nn++) {
+                    const float a = done > FLUSH_UNITS ? carry(nn) : 0.0f;
+#pragma unroll
+                    for (int x = 0; x < MT; x += 2) {
+                        const uint32_t at = chunk(nn, x);
+                        const uint4 w = done > FLUSH_UNITS ? sh_ld128(at) : make_uint4(0u, 0u, 0u, 0u);
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                                     "f"(fmaf(__uint_as_float(w.x), a, o[x][nn][0] + o[x][nn][1])),
+                                     "f"(fmaf(__uint_as_float(w.y), a, o[x][nn][2] + o[x][nn][3])),
+                                     "f"(fmaf(__uint_as_float(w.z), a, o[x + 1][nn][0] + o[x + 1][nn][1])),
+                                     "f"(fmaf(__uint_as_float(w.w), a, o[x + 1][nn][2] + o[x + 1][nn][3]))
+                                     : "memory");
+                        o[x][nn][0] = o[x][nn][1] = o[x][nn][2] = o[x][nn][3] = 0.0f;
+                        o[x + 1][nn][0] = o[x + 1][nn][1] = o[x + 1][nn][2] = o[x + 1][nn][3] = 0.0f;
+                    }
+                }
+                __syncwarp();   // (every lane has read the units)
+                if (g8 == 0)
+#pragma unroll
+                    for (int nn = 0; nn < NN; nn++)
+                        sm.sum_unit[warp][4 * nn + t] = make_float2(mrow[nn], __uint_as_float((uint32_t)(vex[nn] + 127) << 23));
+                __syncwarp();
+            }
+            done++;
             const int i = slots + (u >> 1) - (u0 >> 1), sl = i % SLOTS, phase = i / SLOTS;
             if (failed) break;   // a wait gave up: no further ones
             bool got = phase == 0 || mbar_wait(smem_addr(sm.empty + sl), (uint32_t)((phase - 1) & 1), c.status);
@@ -778,8 +826,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
         slots += ((u1 - 1) >> 1) - (u0 >> 1) + 1;
         metas += (u1 - (u0 & ~1) + 31) & ~31;
 
-        // ---- join the warps: sums in units of 2^0, relative to the warp's own maximum.  Lane (g8, t)
-        // holds positions D / 8 g8 .. of row 4 nn + t; 16-byte chunk y of row r lies at y ^ r
+        // ---- join the warps: sums in units of 2^0, relative to the warp's own maximum
 #pragma unroll
         for (int nn = 0; nn < NN; nn++) {
             const float vscale = __uint_as_float((uint32_t)(vex[nn] - 14 + 127) << 23);
@@ -790,13 +837,19 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
                 sm.ml[warp][r][0] = mrow[nn];
                 sm.ml[warp][r][1] = lrow[nn];
             }
-            const uint32_t dst = smem_addr(red) + (uint32_t)((warp * ROWS + r) * D * 4);
+            const bool add = FLUSH && done > FLUSH_UNITS;
+            const float a = add ? carry(nn) : 0.0f;
 #pragma unroll
-            for (int x = 0; x < MT; x += 2)
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((D / 32 * g8 + x / 2) ^ r) << 4)),
-                             "f"((o[x][nn][0] + o[x][nn][1]) * vscale), "f"((o[x][nn][2] + o[x][nn][3]) * vscale),
-                             "f"((o[x + 1][nn][0] + o[x + 1][nn][1]) * vscale), "f"((o[x + 1][nn][2] + o[x + 1][nn][3]) * vscale)
+            for (int x = 0; x < MT; x += 2) {
+                const uint32_t at = chunk(nn, x);
+                const uint4 w = add ? sh_ld128(at) : make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                             "f"(fmaf(__uint_as_float(w.x), a, o[x][nn][0] + o[x][nn][1]) * vscale),
+                             "f"(fmaf(__uint_as_float(w.y), a, o[x][nn][2] + o[x][nn][3]) * vscale),
+                             "f"(fmaf(__uint_as_float(w.z), a, o[x + 1][nn][0] + o[x + 1][nn][1]) * vscale),
+                             "f"(fmaf(__uint_as_float(w.w), a, o[x + 1][nn][2] + o[x + 1][nn][3]) * vscale)
                              : "memory");
+            }
         }
         consumer_sync<CONSUMERS>();
         const int rows = nrows;
@@ -947,19 +1000,23 @@ int log2_of(int64_t x) {
 // against 42.
 constexpr int ROWS_MAX = 40;
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 template <int KIND, int D, int NN>
 gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
                       cudaStream_t s) {
-    auto kernel = attn_pages_rows_kernel<KIND, D, NN>;
     constexpr size_t smem = RowsLayout<D, NN>::total + 1024;
     constexpr int ROWS = rows_of(NN), THREADS = (WARPS + 1) * 32;
+    const void *kernels[2] = {(const void *)attn_pages_rows_kernel<KIND, D, NN, false>,
+                              (const void *)attn_pages_rows_kernel<KIND, D, NN, true>};
     static std::atomic<bool> smem_set[64];
     int dev = 0;
     KV_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
     if (dev < 0 || dev >= 64) return fail(GQ_ERR_UNSUPPORTED_DEVICE, "device index %d", dev);
     if (!smem_set[dev].load(std::memory_order_acquire)) {
-        KV_TRY(check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                          "paged attention shared-memory attribute"));
+        for (const void *kernel : kernels)
+            KV_TRY(check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                              "paged attention shared-memory attribute"));
         smem_set[dev].store(true, std::memory_order_release);
     }
     const int grid = 2 * sm_count();
@@ -987,7 +1044,11 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
         KV_TRY(byte_rows_map(&kmap, c.k, pool_rows, box));
         KV_TRY(byte_rows_map(&vmap, c.v, pool_rows, box));
         void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
-        KV_TRY(launch_pdl((const void *)kernel, dim3((unsigned)grid), dim3(THREADS), smem, s, args,
+        // the units of an item that a CTA can have: the item's, and the CTA's piece of the line
+        const int64_t units = ceil_div(c.NB * c.P, UNIT);
+        const int64_t items = c.B * c.Hkv * ceil_div(std::min<int64_t>((int64_t)p.max_n * p.G, ROWS_MAX), ROWS);
+        const int64_t most = std::min(units, std::max<int64_t>(WARPS, ceil_div(items * units, grid)));
+        KV_TRY(launch_pdl(kernels[most > FLUSH_FROM * WARPS], dim3((unsigned)grid), dim3(THREADS), smem, s, args,
                           "paged attention launch"));
     }
     if (w_out) {

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import pages_accuracy as acc
 import pages_ref as ref
 import quantized_skinny_matmul_gb300 as gq
 from test_gpu_pages import built, cache_of, check_attention, run_attention  # noqa: F401 (built: a fixture)
@@ -230,3 +231,56 @@ def test_values_of_masked_pages_do_not_matter(kind, Hkv, G, D, P, new, more, opt
     assert np.all(np.abs(host(out)[:new] - want)[quiet] <= (ref.tolerance(S[..., None], N) * E)[quiet])
     assert np.all(np.abs(host(w)[0] - ww[0]) <= ref.tolerance(0, N) * ww[0] + ref.tolerance(1, 0) * rel[0])
     assert np.all(np.isfinite(host(out)))
+
+
+# ---- accuracy ---------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", [gq.GQ_KV_I8, gq.GQ_KV_E4M3])
+@pytest.mark.parametrize("G,D,P,new", [(1, 128, 16, 1), (4, 128, 32, 1), (2, 64, 16, 1), (8, 128, 64, 1), (8, 64, 16, 1),   # rows
+                                       (2, 128, 32, 48), (1, 64, 64, 60)])                                                  # tiles
+def test_queries_and_weights_keep_both_terms(kind, G, D, P, new):
+    p = acc.few_keys(40, kind, G, D, P, new)
+    want, _, E, S, _ = acc.reference(p)
+    assert np.all(np.abs(host(run_attention(p)) - want) <= acc.few_keys_bound(D, S, E))
+
+
+def one_sign(kind, D, B, Hkv, G, L, new, gen):
+    """A cache whose values are all positive, and queries of zero: every key weighs the same, and a sum that is
+    not rounded to nearest shows in full.  The outputs of a few rows, and what they should be."""
+    P = 64
+    NB = -(-(L + new) // P)
+    pages = B * Hkv * NB
+    k = torch.zeros((pages, P, D), dtype=torch.int8 if kind == 0 else torch.uint8, device="cuda")
+    lo, hi = (60, 128) if kind == 0 else (0x40, 0x7F)
+    v = torch.randint(lo, hi, (pages, P, D), generator=gen, device="cuda", dtype=k.dtype)
+    vs = torch.rand(pages, generator=gen, device="cuda") / 2 + 0.5
+    table = torch.arange(pages, device="cuda", dtype=torch.int32).reshape(B, Hkv, NB)
+    base = (torch.arange(NB, device="cuda", dtype=torch.int32) * P).expand(B, Hkv, NB).contiguous()
+    held = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    c = gq.KVPages(kind, k, v, torch.ones_like(vs), vs, table, base, held, held.clone())
+    cu = (torch.arange(B + 1, device="cuda") * new).to(torch.int32)
+    out = gq.attn_pages(c, torch.zeros((B * new, Hkv * G, D), device="cuda"), cu, new, gq.AttnScores(1.0))
+    got, want = [], []
+    for b, i in ((0, 0), (B - 1, new - 1)):
+        pg = table[b, 0].long()
+        x = (v[pg] if kind == 0 else v[pg].view(torch.float8_e4m3fn).float()).double() * vs[pg].double()[:, None, None]
+        got.append(out[b * new + i, 0].double())
+        want.append(x.reshape(-1, D)[:L + i + 1].mean(0))
+    assert gq.gq_last_error() == gq.GQ_OK
+    return torch.stack(got), torch.stack(want)
+
+
+@pytest.mark.parametrize("kind", [gq.GQ_KV_I8, gq.GQ_KV_E4M3])
+@pytest.mark.parametrize("D,B,Hkv,G,L,new,steps,adds", [
+    # rows, a sequence in a CTA: 146 units a warp, flushed every 8 of them (2 steps each); 18 flushes and 7 warps to add
+    (64, 304, 1, 1, 32767, 1, 16, 25), (128, 304, 1, 8, 32767, 1, 16, 25),
+    # rows, not flushed: 16 units a warp at most
+    (128, 304, 1, 1, 3500, 1, 32, 7),
+    # tiles: 256 blocks of 8 steps for each of the two terms, flushed every 4
+    (64, 2, 16, 8, 32767, 96, 64, 64), (128, 2, 16, 8, 32767, 96, 64, 64),
+])
+def test_long_sums_are_rounded(kind, D, B, Hkv, G, L, new, steps, adds):
+    """A step is off by at most 2^-23 of the sum so far, an addition by 2^-24; 16 more for the terms and the end."""
+    got, want = one_sign(kind, D, B, Hkv, G, L, new, torch.Generator("cuda").manual_seed(3))
+    assert float(((got - want).abs() / want).max()) <= (2 * steps + adds + 16) * 2.0 ** -24
