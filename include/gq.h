@@ -500,7 +500,9 @@ typedef struct gq_attn_scores {
  * queries and the G heads, and 0 for the other entries; weights_in may be weights_out,
  * or NULL (0).  Uses the stream's workspace (grown on demand, as for the products;
  * GQ_ERR_NO_MEMORY when that is not possible, e.g. while the stream is captured: run the
- * call once before capturing). */
+ * call once before capturing).  With weights that holds 4 T Hq NB P / min(P, 32) bytes of
+ * sums, by the room of the cache; where they are more than 512 MB the rows are worked out
+ * in slices that need no more (but for the sums of a single row). */
 gq_status gq_attn_pages(const gq_kv_pages *cache, const gq_attn_scores *scores, const float *q, int64_t ldq,
                         const int32_t *cu, int64_t T, int64_t max_n, int64_t Hq, float *out, int64_t ldo,
                         const float *weights_in, float *weights_out, float decay, cudaStream_t stream);

@@ -159,7 +159,7 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttnParams8 &p, const SeqStep &s) {
     Span r;
-    const int n = s.held + s.n, end = (n + UNIT - 1) >> 5;
+    const int n = s.end, end = (n + UNIT - 1) >> 5;
     int lo = 0, pre = 0, first = 0;
     if (s.n <= ROWS_MOST) {   // few tokens: look at each one's own range
         if (p.first) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
         for (int64_t at = lo; at < hi && ok;) {
             const int u0 = (int)(at - item0), u1 = (int)min((int64_t)k.u.units, hi - item0);
             const int64_t trow = ((int64_t)k.b * c.Hkv + k.h) * c.NB;
-            const int n = k.s.held + k.s.n;
+            const int n = k.s.end;
             // ---- the item: its rows (row r is token r / G, head r % G of the group) and queries
             {
                 const int st = items % ITEMS, rows = min(ROWS, k.s.n * p.G - k.tile * ROWS);
@@ -930,8 +930,8 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = (item % tiles) * 32 + lane, j = g >> per;
     const int size = 1 << p.lgGroup;
     pdl_wait();
-    const SeqStep s = seq_step(c, p.cu, b, p.T, p.max_n);
-    const int end = s.bad ? 0 : s.held + s.n, slot = g << p.lgGroup;
+    const SeqStep s = attn_step(p, b);
+    const int end = s.end, slot = g << p.lgGroup;
     const int64_t at = (int64_t)bh * c.NB + j;
     const bool used = slot < end;        // (a page is in use if its first group is)
     // an entry that is no page: seen by nobody, and its sums may never have been written
@@ -1000,11 +1000,13 @@ int log2_of(int64_t x) {
 // against 42.
 constexpr int ROWS_MAX = 40;
 
+// Bytes of the row and group sums that a call keeps at most, but for a single row's.
+constexpr int64_t SUMS_MOST = 512ll << 20;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int KIND, int D, int NN>
-gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const float *w_in, float *w_out, float decay,
-                      cudaStream_t s) {
+gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, const float *w_in, float *w_out, float decay, cudaStream_t s) {
     constexpr size_t smem = RowsLayout<D, NN>::total + 1024;
     constexpr int ROWS = rows_of(NN), THREADS = (WARPS + 1) * 32;
     const void *kernels[2] = {(const void *)attn_pages_rows_kernel<KIND, D, NN, false>,
@@ -1021,20 +1023,24 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
     }
     const int grid = 2 * sm_count();
     const size_t parts = (size_t)grid * 2 * ROWS * D * 4, mls = (size_t)grid * 2 * ROWS * 8;
+    const int64_t T = p.row1 - p.row0, max_n = std::min<int64_t>(p.max_n, T);   // of the slice
     const size_t lse = w_out ? ((size_t)T * p.Hq * 4 + 255) / 256 * 256 : 0;
     const size_t glse = w_out ? ((size_t)T * p.Hq * p.NG * 4 + 255) / 256 * 256 : 0;
-    const bool tiles = (int64_t)p.max_n * p.G > ROWS_MAX;
+    const bool tiles = max_n * p.G > ROWS_MAX;
     // Some sequence may still be small; with equal lengths, or one sequence, none should be (one that is,
     // in a step of fewer rows than T, is left to the tiles with the others)
-    const bool rows = !tiles || (c.B > 1 && T < c.B * (int64_t)p.max_n);
+    const bool rows = !tiles || (c.B > 1 && T < c.B * max_n);
     const size_t plan = tiles ? attn_pages_tc_workspace(c, T, p.G) : 0;
     Workspace ws{};
     KV_TRY(get_workspace(s, (size_t)grid * sizeof(int), parts + mls + lse + glse + plan, &ws));
     p.counters = reinterpret_cast<int *>(ws.counters);
     p.parts = reinterpret_cast<float *>(ws.data);
     p.part_ml = reinterpret_cast<float *>(ws.data + parts);
-    p.lse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls) : nullptr;
-    p.glse = w_out ? reinterpret_cast<float *>(ws.data + parts + mls + lse) : nullptr;
+    if (w_out) {   // (the kernels index them by packed rows: from where row 0 would be)
+        const size_t before = (size_t)p.row0 * p.Hq * 4;
+        p.lse = reinterpret_cast<float *>(reinterpret_cast<uintptr_t>(ws.data + parts + mls) - before);
+        p.glse = reinterpret_cast<float *>(reinterpret_cast<uintptr_t>(ws.data + parts + mls + lse) - before * p.NG);
+    }
     p.rows_over = !tiles ? INT32_MAX : rows ? ROWS_MAX : 0;
     if (tiles) KV_TRY(launch_attn_pages_tc(p, c, ws.data + parts + mls + lse + glse, s));
     if (rows) {
@@ -1046,7 +1052,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
         void *args[] = {(void *)&kmap, (void *)&vmap, (void *)&p};
         // the units of an item that a CTA can have: the item's, and the CTA's piece of the line
         const int64_t units = ceil_div(c.NB * c.P, UNIT);
-        const int64_t items = c.B * c.Hkv * ceil_div(std::min<int64_t>((int64_t)p.max_n * p.G, ROWS_MAX), ROWS);
+        const int64_t items = c.B * c.Hkv * ceil_div(std::min<int64_t>(max_n * p.G, ROWS_MAX), ROWS);
         const int64_t most = std::min(units, std::max<int64_t>(WARPS, ceil_div(items * units, grid)));
         KV_TRY(launch_pdl(kernels[most > FLUSH_FROM * WARPS], dim3((unsigned)grid), dim3(THREADS), smem, s, args,
                           "paged attention launch"));
@@ -1054,7 +1060,7 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
     if (w_out) {
         const int64_t items = c.B * c.Hkv * ((p.NG + 31) / 32);
         void *wargs[] = {(void *)&p, (void *)&w_in, (void *)&w_out, (void *)&decay};
-        const bool few = (int64_t)p.max_n * p.G <= WROWS_FEW, spread = !few && items * WCTAS <= 4 * sm_count();
+        const bool few = max_n * p.G <= WROWS_FEW, spread = !few && items * WCTAS <= 4 * sm_count();
         const void *weigh = few      ? (const void *)attn_pages_weights_kernel<4, 1>
                             : spread ? (const void *)attn_pages_weights_kernel<16, WCTAS>
                                      : (const void *)attn_pages_weights_kernel<16, 1>;
@@ -1062,6 +1068,25 @@ gq_status launch_rows(AttnParams8 p, const gq_kv_pages &c, int64_t T, const floa
                           "paged attention weights launch"));
     }
     return GQ_OK;
+}
+
+gq_status launch_slice(const AttnParams8 &p, const gq_kv_pages &c, const float *w_in, float *w_out, float decay,
+                       cudaStream_t s) {
+    // items of up to 4 rows, where a sequence's rows of a KV head are no more, else of up to 8: 32
+    // sequences x 8 heads x 4 rows on 2048 tokens take 33 us with one column tile, 41 with two
+    const bool few = (int64_t)std::min(p.max_n, p.row1 - p.row0) * p.G <= 4;
+    if (c.kind == GQ_KV_I8) {
+        if (c.D == 64)
+            return few ? launch_rows<GQ_KV_I8, 64, 1>(p, c, w_in, w_out, decay, s)
+                       : launch_rows<GQ_KV_I8, 64, 2>(p, c, w_in, w_out, decay, s);
+        return few ? launch_rows<GQ_KV_I8, 128, 1>(p, c, w_in, w_out, decay, s)
+                   : launch_rows<GQ_KV_I8, 128, 2>(p, c, w_in, w_out, decay, s);
+    }
+    if (c.D == 64)
+        return few ? launch_rows<GQ_KV_E4M3, 64, 1>(p, c, w_in, w_out, decay, s)
+                   : launch_rows<GQ_KV_E4M3, 64, 2>(p, c, w_in, w_out, decay, s);
+    return few ? launch_rows<GQ_KV_E4M3, 128, 1>(p, c, w_in, w_out, decay, s)
+               : launch_rows<GQ_KV_E4M3, 128, 2>(p, c, w_in, w_out, decay, s);
 }
 
 }  // namespace
@@ -1089,21 +1114,17 @@ gq_status launch_attn_pages(const gq_kv_pages &c, const gq_attn_scores &sc, cons
     p.NG = (int)((c.NB * c.P) >> p.lgGroup);
     p.scale = sc.scale;
     p.cap = sc.cap;
-    // items of up to 4 rows, where a sequence's rows of a KV head are no more, else of up to 8: 32
-    // sequences x 8 heads x 4 rows on 2048 tokens take 33 us with one column tile, 41 with two
-    const bool few = (int64_t)max_n * p.G <= 4;
-    if (c.kind == GQ_KV_I8) {
-        if (c.D == 64)
-            return few ? launch_rows<GQ_KV_I8, 64, 1>(p, c, T, w_in, w_out, decay, s)
-                       : launch_rows<GQ_KV_I8, 64, 2>(p, c, T, w_in, w_out, decay, s);
-        return few ? launch_rows<GQ_KV_I8, 128, 1>(p, c, T, w_in, w_out, decay, s)
-                   : launch_rows<GQ_KV_I8, 128, 2>(p, c, T, w_in, w_out, decay, s);
+    // The page weights need the sums of every row and group until the step is worked out, as much as the cache
+    // has room for: steps for which that is more than SUMS_MOST are worked out in slices of rows.
+    const int64_t row_bytes = Hq * p.NG * 4;
+    const int64_t slice = w_out ? std::max<int64_t>(1, SUMS_MOST / row_bytes) : T;
+    for (int64_t row0 = 0; row0 < T; row0 += slice) {
+        p.row0 = (int)row0;
+        p.row1 = (int)std::min(T, row0 + slice);
+        // (a later slice adds to what the ones before gathered)
+        KV_TRY(row0 == 0 ? launch_slice(p, c, w_in, w_out, decay, s) : launch_slice(p, c, w_out, w_out, 1.0f, s));
     }
-    if (c.D == 64)
-        return few ? launch_rows<GQ_KV_E4M3, 64, 1>(p, c, T, w_in, w_out, decay, s)
-                   : launch_rows<GQ_KV_E4M3, 64, 2>(p, c, T, w_in, w_out, decay, s);
-    return few ? launch_rows<GQ_KV_E4M3, 128, 1>(p, c, T, w_in, w_out, decay, s)
-               : launch_rows<GQ_KV_E4M3, 128, 2>(p, c, T, w_in, w_out, decay, s);
+    return GQ_OK;
 }
 
 }  // namespace gq

@@ -25,8 +25,9 @@ struct AttnParams8 {
     float *parts;               // row kernel: [CTA][2][ROWS][D] sums, and [CTA][2][ROWS][2] maximum and denominator
     float *part_ml;
     int *counters;              // row kernel, per CTA: pieces of the item cut at its end that are done
-    float *glse;                // [T * Hq][NG] log2 of the weight sums by group, or null
+    float *glse;                // [T * Hq][NG] log2 of the weight sums by group, or null (the slice's rows are there)
     float *lse;                 // [T * Hq] log2 of the denominators
+    int row0, row1;             // the slice of packed rows that is worked out
     int64_t ldq, ldo, window;
     int T, max_n, Hq, G, NG, lgP, lgGroup;
     int rows_over;              // sequences with more query rows per KV head are the tile kernel's
@@ -84,23 +85,28 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &p01, uint32_t &p23)
     if constexpr (KIND == GQ_KV_I8) q8_to_f16x2(w, p01, p23);
     else e4m3x4_to_f16x2(w, p01, p23);
 }
-// A sequence's part of the step.  One whose lengths are out of range keeps its rows, if cu
-// itself is sound, and has no tokens (held + n = 0): its outputs are zero.
+// A sequence's part of the step, as far as the slice goes: its rows there, as if those before
+// had been held already (end is the whole step's).  One whose lengths are out of range keeps its
+// rows, if cu itself is sound, and has no tokens (end = 0): its outputs are zero.
 __device__ __forceinline__ SeqStep attn_step(const AttnParams8 &p, int b) {
     SeqStep s = seq_step(p.c, p.cu, b, p.T, p.max_n);
     if (s.bad) {
         const int t1 = p.cu[b + 1];
         const bool rows = s.t0 >= 0 && t1 > s.t0 && t1 <= p.T;   // (more than max_n too)
         s.n = rows ? t1 - s.t0 : 0;
-        s.held = -s.n;
-        s.seen = 0;
+        s.held = s.seen = 0;
     }
+    const int off = max(0, p.row0 - s.t0);
+    s.n = max(0, min(s.n - off, p.row1 - s.t0 - off));
+    s.t0 += off;
+    s.held += off;
+    s.seen += off;
     return s;
 }
 
 // A call for the sequences with many query rows (attn_pages_tc.cu): those with more than
 // `rows_over` rows per KV head.
-size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t T, int64_t G);
+size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t rows, int64_t G);
 gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8_t *work, cudaStream_t s);
 
 }  // namespace gq

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(256) attn_pages_plan_kernel(const AttnParams8 
                 const SeqStep s = attn_step(p, b);
                 if (s.bad && phase == 0) atomicOr(p.c.status, STATUS_RANGE);
                 if (s.n * p.G > p.rows_over) pairs = (s.n * p.G + 2 * BR - 1) / (2 * BR);
-                int keys = s.held + s.n;
+                int keys = s.end;
                 if (p.window > 0) keys = (int)min((int64_t)keys, p.window + 2 * BR / p.G);
                 splits = max(1, min(most, keys / (SHARE_BLOCKS * BT)));
             }
@@ -396,7 +396,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         int item = 0;
         if (lane == 0) item = atomicAdd(plan.next, 1);
         item = __shfl_sync(0xffffffffu, item, 0);
-        Item x{0, 0, 0, 0, 1, -1, {0, 0, 0, 0, false}};
+        Item x{0, 0, 0, 0, 1, -1, {0, 0, 0, 0, 0, false}};
         if (item >= items) {
             publish(x, F_EXIT, 0, 0, 0, 0, 0.0f, 0.0f, 0);
             break;
@@ -413,7 +413,7 @@ __device__ __forceinline__ void lead_role(const AttnParams8 &p, const PlanView &
         // 285 without; the CTA's first ones are needed at once)
         for (int i = nmeta == 0 ? x.s.n : x.pair * 2 * BR / p.G + lane; i < x.s.n && i * p.G < (x.pair + 1) * 2 * BR; i += 32)
             bulk_prefetch_l2(p.q + (int64_t)(x.s.t0 + i) * p.ldq + (int64_t)x.h * p.G * D, (uint32_t)(p.G * D * 4));
-        const int end = x.s.held + x.s.n;    // slots in use (0 for an unusable sequence)
+        const int end = x.s.end;             // slots in use (0 for an unusable sequence)
         // what the rows of each tile can see: positions lo .. hi, and those below pre
         int lo[2] = {0, 0}, hi[2] = {-1, -1}, pre[2] = {0, 0}, lomin = 0x7fffffff, premax = 0, imax = 0;
 #pragma unroll
@@ -1216,27 +1216,28 @@ gq_status launch_tiles(const AttnParams8 &p, const gq_kv_pages &c, const PlanVie
 }
 
 // At most so many pairs of tiles: the rows of all sequences, and a last pair of each.
-int64_t most_pairs(const gq_kv_pages &c, int64_t T, int64_t G) { return T * G / (2 * BR) + std::min(c.B, T) + 1; }
+int64_t most_pairs(const gq_kv_pages &c, int64_t rows, int64_t G) { return rows * G / (2 * BR) + std::min(c.B, rows) + 1; }
 
 }  // namespace
 
 // Whether the rows, if all are in tiles, may leave half of the SMs idle: places for shares' outputs.
-static int share_places(const gq_kv_pages &c, int64_t T, int64_t G) {
-    return T * G / (2 * BR) * c.Hkv * 2 > sm_count() ? 0 : sm_count();
+static int share_places(const gq_kv_pages &c, int64_t rows, int64_t G) {
+    return rows * G / (2 * BR) * c.Hkv * 2 > sm_count() ? 0 : sm_count();
 }
 
 static size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
-size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t T, int64_t G) {
-    const size_t places = (size_t)share_places(c, T, G);
-    return 256 + round_up(((size_t)most_pairs(c, T, G) + places) * sizeof(int4)) +
+size_t attn_pages_tc_workspace(const gq_kv_pages &c, int64_t rows, int64_t G) {
+    const size_t places = (size_t)share_places(c, rows, G);
+    return 256 + round_up(((size_t)most_pairs(c, rows, G) + places) * sizeof(int4)) +
            (size_t)sm_count() * 2 * c.D * BR * 4 + places * 2 * BR * (c.D + 1) * 4;
 }
 
 gq_status launch_attn_pages_tc(const AttnParams8 &p, const gq_kv_pages &c, uint8_t *work, cudaStream_t s) {
     PlanView plan{};
-    plan.places = share_places(c, p.T, p.G);
-    const int64_t entries = most_pairs(c, p.T, p.G) + plan.places;
+    const int64_t rows = p.row1 - p.row0;
+    plan.places = share_places(c, rows, p.G);
+    const int64_t entries = most_pairs(c, rows, p.G) + plan.places;
     plan.room = (int)std::min<int64_t>(entries, INT32_MAX);
     plan.count = reinterpret_cast<int *>(work);
     plan.next = plan.count + 1;

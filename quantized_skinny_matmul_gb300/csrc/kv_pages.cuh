@@ -28,6 +28,7 @@ gq_status launch_pdl(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStr
 // rests on no position being below its slot.)
 struct SeqStep {
     int t0, n, held, seen;   // first packed row, new tokens, tokens held before, position of the first new one
+    int end;                 // tokens held after
     bool bad;
 };
 
@@ -41,6 +42,7 @@ __device__ __forceinline__ SeqStep seq_step(const PagesView &c, const int32_t *c
     s.bad = s.t0 < 0 || n < 0 || n > max_n || t1 > T || s.held < 0 || (int64_t)s.held + n > (int64_t)c.NB * c.P ||
             s.seen < s.held || (int64_t)s.seen + n > (1LL << 30);
     s.n = s.bad ? 0 : (int)n;
+    s.end = s.bad ? 0 : s.held + s.n;
     return s;
 }
 

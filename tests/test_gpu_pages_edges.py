@@ -284,3 +284,44 @@ def test_long_sums_are_rounded(kind, D, B, Hkv, G, L, new, steps, adds):
     """A step is off by at most 2^-23 of the sum so far, an addition by 2^-24; 16 more for the terms and the end."""
     got, want = one_sign(kind, D, B, Hkv, G, L, new, torch.Generator("cuda").manual_seed(3))
     assert float(((got - want).abs() / want).max()) <= (2 * steps + adds + 16) * 2.0 ** -24
+
+
+# ---- steps whose sums do not fit at once -------------------------------------------------------------
+
+
+def roomy(p, NB):
+    """The same cache with room for NB pages a sequence and head (the entries of the others are never looked at)."""
+    B, Hkv, old = p["table"].shape
+    q = dict(p)
+    for name in ("table", "base"):
+        q[name] = np.zeros((B, Hkv, NB), np.int32)
+        q[name][..., :old] = p[name]
+    return q
+
+
+@pytest.mark.parametrize("kind,Hkv,G,P,held,new,NB,opts", [
+    (0, 1, 16, 16, [40, 0], [400, 200], 20000, ""),                     # 419 rows at a time: within the first sequence
+    (1, 2, 4, 16, [100, 5, 30], [70, 1, 60], 1 << 17, "prefix"),        # 128 rows; keys past the slice's own are seen
+    (0, 1, 8, 32, [300], [150], 1 << 19, "window"),                     # 32 rows
+    (0, 1, 32, 128, [30] * 10, [1] * 10, 1 << 18, "first"),             # 4 rows, of as many sequences
+    (1, 1, 64, 16, [200], [3], 1 << 22, ""),                            # one row's are more than a slice is to have
+])
+def test_weights_in_slices(kind, Hkv, G, P, held, new, NB, opts):
+    p = roomy(ref.problem(31, kind, len(held), Hkv, G, 64, P, held, new), NB)
+    T, opt = int(p["cu"][-1]), {}
+    if opts == "prefix":
+        opt["prefix"] = np.where(np.arange(T) % 2 == 0, 160, 0).astype(np.int32)
+    elif opts == "window":
+        opt["window"] = 45
+    elif opts == "first":
+        opt["first"] = np.where(np.arange(T) % 3 == 0, 25, 0).astype(np.int32)
+    weights = np.zeros(p["table"].shape, np.float32)
+    weights[..., :40] = p["gen"].random((len(held), Hkv, 40))
+    before = torch.cuda.mem_get_info()[0]
+    out, w = run_attention(p, weights=weights, decay=0.75, **opt)
+    used = before - torch.cuda.mem_get_info()[0]
+    check_attention(p, out, w, weights=weights, decay=0.75, **opt)
+    assert gq.gq_last_error() == gq.GQ_OK
+    assert used < 3 << 30                    # (a workspace at least doubles when it grows)
+    again = run_attention(p, weights=weights, decay=0.75, **opt)
+    assert torch.equal(again[0], out) and torch.equal(again[1], w)
