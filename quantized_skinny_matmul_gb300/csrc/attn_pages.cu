@@ -914,12 +914,13 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
 // groups of tokens of one (sequence, head), a lane per group; its CTAs' WW warps share the tokens
 // and are added in order.  The sums of groups that a row cannot see were never written: they are
 // passed over.  Bound by the latency of the loads, so many rows want many warps, unless the items
-// fill the GPU by themselves.  The whole step, 4 sequences of up to 1000 tokens x 2 heads of 8 KV heads
-// (64 items): 74 us, 101 with one CTA an item; 8 x 8 tokens x 8 heads on 4096 (512 items): 91 us with 4
-// warps an item, 170 with 8 x 16.
+// fill the GPU by themselves, and registers for two CTAs of 16 warps an SM (4 sequences of up to 1000
+// tokens x 2 heads of 8 KV heads, 64 items: 68 us the whole step, 86 with 96 registers a thread).  The same
+// with a CTA an item: 101; 8 x 8 tokens x 8 heads on 4096 (512 items): 91 us with 4 warps an item,
+// 170 with 8 x 16.
 // ---------------------------------------------------------------------------
 template <int WW, int CL>
-__global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
+__global__ void __launch_bounds__(WW * 32, WW == 16 ? 2 : 12) __cluster_dims__(CL, 1, 1)
     attn_pages_weights_kernel(const AttnParams8 p, const float *w_in, float *w_out, float decay) {
     __shared__ float part[WW][32];
     const PagesView &c = p.c;
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(WW * 32) __cluster_dims__(CL, 1, 1)
             for (int x = warp; x < s.n * p.G; x += WW) row(x / p.G, x % p.G);
         } else {
             for (int y = 0; y < p.G; y++)
-#pragma unroll 8
+#pragma unroll 4
                 for (int i = rank * WW + warp; i < s.n; i += WW * CL) row(i, y);
         }
     }
