@@ -48,7 +48,7 @@ namespace {
 constexpr int UNIT = 32;                    // tokens per unit
 // Consumer warps, and query rows of an item for 1 or 2 column tiles.  Two CTAs of 8 warps fill an
 // SM's registers.  128 sequences x 32 heads on 2048 tokens, a row each: 303 us with the query as the
-// 16-row operand, 274 with the codes there and slots of 32 tokens, 235 as it is (85% of a copy's
+// 16-row operand, 274 with the codes there and slots of 32 tokens, 236 as it is (84% of a copy's
 // rate; bound by memory).  Short ones are bound by the steps of an item (about 1 us each: the
 // first slot, the query's fragments, the warps' sums joined, the pieces joined): 1 x 500 tokens of 32
 // heads takes 13.5 us, 1 x 32768 of 8 heads 28.
@@ -915,9 +915,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, 2)
 // and are added in order.  The sums of groups that a row cannot see were never written: they are
 // passed over.  Bound by the latency of the loads, so many rows want many warps, unless the items
 // fill the GPU by themselves, and registers for two CTAs of 16 warps an SM (4 sequences of up to 1000
-// tokens x 2 heads of 8 KV heads, 64 items: 68 us the whole step, 86 with 96 registers a thread).  The same
-// with a CTA an item: 101; 8 x 8 tokens x 8 heads on 4096 (512 items): 91 us with 4 warps an item,
-// 170 with 8 x 16.
+// tokens x 2 heads of 8 KV heads, 64 items: 68 us the whole step, 86 with 96 registers a thread; when it
+// was 74, a CTA an item took 101).  8 x 8 tokens x 8 heads on 4096 (512 items): 91 us with 4 warps an
+// item, 170 with 8 x 16.
 // ---------------------------------------------------------------------------
 template <int WW, int CL>
 __global__ void __launch_bounds__(WW * 32, WW == 16 ? 2 : 12) __cluster_dims__(CL, 1, 1)

@@ -23,8 +23,9 @@
 // Items (sequence, head, pair of tiles) are taken from a list that a small kernel lays out, in
 // turn, longest first within a sequence; which CTA takes which does not change any result.
 //
-// A prompt of 4096 tokens x 32 heads (8 KV heads, D = 128): 281 us, 489 TFLOP/s of the formula's
-// operations, 978 of those issued (52% of a library product's rate).  A block of both tiles takes
+// A prompt of 4096 tokens x 32 heads (8 KV heads, D = 128): 285 us, 482 TFLOP/s of the formula's
+// operations, 964 of those issued (51% of a library product's rate; 281 us before a row's unit of
+// values was its own, and in the comparisons below).  A block of both tiles takes
 // about 7,000 cycles, 4,100 of them products: per tile, 4,000 from scores to weights, then 2,600 for
 // the second half of its P V and the next Q K, which share the operands' memory with the widening;
 // an item's change takes about 25,000 more (14,000 of them the queries' loads).  Two threads a row
