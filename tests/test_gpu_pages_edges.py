@@ -325,3 +325,38 @@ def test_weights_in_slices(kind, Hkv, G, P, held, new, NB, opts):
     assert used < 3 << 30                    # (a workspace at least doubles when it grows)
     again = run_attention(p, weights=weights, decay=0.75, **opt)
     assert torch.equal(again[0], out) and torch.equal(again[1], w)
+
+
+@pytest.mark.parametrize("kind,G,D,P,new", [(0, 1, 128, 32, 1), (1, 4, 128, 16, 1), (0, 8, 64, 32, 1), (1, 2, 64, 64, 4),
+                                            (0, 8, 128, 128, 1), (1, 1, 64, 16, 2), (0, 5, 128, 64, 3),
+                                            (0, 1, 128, 32, 48), (1, 4, 64, 16, 12)])       # the last two: tiles
+@pytest.mark.parametrize("opts", ["plain", "grow", "shrink", "masks"])
+def test_flushed_sums_under_changing_maxima_and_scales(kind, G, D, P, new, opts):
+    """Long sequences, sums flushed many times: maxima and value scales that grow or fall on the way."""
+    B, Hkv, pool = 160, 2, 192
+    L = 8000 // P * P - 3
+    p = ref.problem(41, kind, 1, 1, G, D, P, [pool * P], [1], extra=0)       # a pool of pages, shared by the sequences
+    gen, NB = p["gen"], -(-(L + new) // P)
+    table = gen.integers(0, pool, (B, Hkv, NB)).astype(np.int32)
+    if opts in ("grow", "shrink"):           # a page's scales by its number, the numbers in order
+        order = np.sort(table, -1) if opts == "grow" else -np.sort(-table, -1)
+        table = np.ascontiguousarray(order)
+        p["vs"][:] = p["vs"] * np.float32(2.0) ** (np.arange(len(p["vs"])) // 4 - 24)
+        p["ks"][:] = p["ks"] * np.linspace(0.2, 3.0, len(p["ks"])).astype(np.float32)
+    held = np.full(B, L, np.int32)
+    base = np.ascontiguousarray(np.broadcast_to(np.arange(NB, dtype=np.int32) * P, (B, Hkv, NB)))
+    cu = (np.arange(B + 1) * new).astype(np.int32)
+    p.update(table=table, base=base, held=held, seen=held.copy(), cu=cu, q=gen.standard_normal((B * new, Hkv * G, D)).astype(np.float32))
+    opt = {}
+    if opts == "masks":
+        t = np.arange(B * new)
+        opt = dict(cap=20.0, window=6000, prefix=np.where(t % 2 == 0, 700, 0).astype(np.int32),
+                   first=np.where(t % 3 == 0, 150, 0).astype(np.int32), slopes=ref.alibi(Hkv * G) / 64)
+    weights = gen.random(table.shape).astype(np.float32)
+    out, w = run_attention(p, weights=weights, decay=0.5, **opt)
+    assert gq.gq_last_error() == gq.GQ_OK and bool(torch.isfinite(out).all())
+    for b in (0, 77, B - 1):
+        rows = slice(cu[b], cu[b + 1])
+        one = dict(p, held=held[:1], seen=held[:1], cu=cu[:2], q=p["q"][rows], table=table[b:b + 1], base=base[b:b + 1])
+        opt_b = {n: x[rows] if n in ("first", "prefix") else x for n, x in opt.items()}
+        check_attention(one, out[rows], w[b:b + 1], weights=weights[b:b + 1], decay=0.5, **opt_b)
