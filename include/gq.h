@@ -527,6 +527,136 @@ gq_status gq_kv_pages_evict(const gq_kv_pages *cache, const float *weights, int6
                             int64_t keep_last, int32_t *table_out, int32_t *base_out, float *weights_out,
                             int32_t *held_out, cudaStream_t stream);
 
+/* ---- microscaled (MX) formats: 4-bit weights, 8-bit activations, experts -------------------
+ *
+ * Blocks of 32 values along a row share one power of two; the element types are the 4-bit
+ * e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and the 8-bit e4m3 (up to 448).  The
+ * tensor cores of this GPU multiply such blocks as they are, scales included.  (The pages have
+ * no counterpart; the formats are those of the Open Compute Project's MX specification, the
+ * choice of the scale and the layouts are this library's.)
+ *
+ * Rows of K values (a multiple of 32), packed, 16-byte aligned:
+ *   codes   e2m1: K / 2 bytes, value 2i in the low nibble of byte i, value 2i + 1 in the high
+ *           one (bit 3: sign); e4m3: K bytes
+ *   scales  S = gq_mx_scale_cols(K) bytes: byte j is the scale 2^(byte - 127) of values 32 j ..
+ *           32 j + 31; K / 32 of them, the rest (up to a multiple of 16) is padding that is
+ *           written as 0 and read by nobody
+ * The scale is the smallest byte b in 0 .. 254 with amax <= top * 2^(b - 127), top = 6 (e2m1)
+ * or 448 (e4m3), amax the block's largest magnitude: no value is cut off.  Each code is the
+ * element nearest to value / 2^(b - 127), ties to the even code.  A block that holds an
+ * infinity or a NaN gets scale 255 and codes 0: it stands for 32 NaN, and so does every
+ * product that reads it. */
+typedef enum { GQ_MX_E2M1 = 0, GQ_MX_E4M3 = 1 } gq_mx_kind;
+typedef enum { GQ_TYPE_F32 = 0, GQ_TYPE_BF16 = 1 } gq_type;   /* of rows in memory */
+
+size_t gq_mx_scale_cols(int64_t K);   /* ceil(K / 512) * 16; 0 if K <= 0 or K % 32 */
+
+/* Rows x (row m at x + m * ldx values of `type`, each row 16-byte aligned: ldx a multiple of 4,
+ * or of 8 for bf16, at least K) into codes and scales. */
+gq_status gq_quantize_mx(const void *x, int64_t ldx, gq_type type, gq_mx_kind kind, void *codes, uint8_t *scales,
+                         int64_t M, int64_t K, cudaStream_t stream);
+/* The values that codes and scales stand for, into y [M][K] of `type` (exact but for values below
+ * 2^-126 and, in bf16, below 2^-133 steps; NaN for scale 255). */
+gq_status gq_dequantize_mx(const void *codes, const uint8_t *scales, gq_mx_kind kind, void *y, gq_type type,
+                           int64_t M, int64_t K, cudaStream_t stream);
+
+/* Root-mean-square norm.  For each row, h = x + residual (rounded once to `type`; h = x without
+ * one), y_j = h_j * weight_j / sqrt(mean(h^2) + eps).  x, residual and h are rows of `type` at
+ * stride ldx, ldr, ldh (as in gq_quantize_mx); weight f32 [K] or NULL (1).  Outputs, each optional
+ * (at least one): h (NULL: not kept; h may be x or residual), y [M][K] of `ytype`, and the e4m3
+ * blocks of y, codes with scales.  The blocks are those of the exact y: sums and quotients are carried in
+ * two f32 terms (48 bits) up to the choice of scale and code; y itself is rounded once (bf16: twice).
+ * K up to 32768. */
+gq_status gq_rms_norm_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr, gq_type type,
+                         const float *weight, double eps, void *h, int64_t ldh, void *y, gq_type ytype,
+                         void *codes, uint8_t *scales, int64_t M, int64_t K, cudaStream_t stream);
+
+/* 4-bit weights for the products: `count` matrices [N][K] of e2m1 rows, one after the other
+ * (codes [count * N][K / 2], scales [count * N][S]), copied once into tiles of 128 rows x 128
+ * columns: tile (c, g, t) of matrix c, rows 128 g .. and columns 128 t .. is number
+ * (c * ceil(N/128) + g) * ceil(K/128) + t.  First the codes of all tiles, 8192 bytes each (row by
+ * row, 64 bytes), then their scales, 512 bytes each: the four scale bytes of row r at (r % 32) * 16
+ * + (r / 32) * 4.  Padding is 0.  The result must not overlap the inputs. */
+size_t gq_mxfp4_repacked_bytes(int64_t count, int64_t N, int64_t K);   /* 0 for sizes out of range */
+gq_status gq_repack_mxfp4(const void *codes, const uint8_t *scales, void *repacked, int64_t count, int64_t N,
+                          int64_t K, cudaStream_t stream);
+
+/* Activations in e4m3 blocks: `rows` rows of K values. */
+typedef struct gq_mx_rows {
+    int64_t rows;
+    const void *codes;
+    const uint8_t *scales;
+} gq_mx_rows;
+
+/* Which rows go to which expert: row r, offsets[e] <= r < offsets[e + 1], belongs to expert e
+ * (offsets int32 [E + 1] on the device).  R is the room for rows on the host's side; rows from
+ * offsets[E] on are neither read nor written.  With `rows` (int32 [R]) row r of the product reads
+ * row rows[r] of the activations, without it row r.  An expert whose offsets are out of range
+ * (negative, decreasing, past R) has no rows, a row whose index is outside the activations reads
+ * as zeros, and either makes the next gq_last_error() return GQ_ERR_INVALID_ARG.
+ * E 1 .. 1024, R < 2^30. */
+typedef struct gq_expert_rows {
+    int64_t E, R;
+    const int32_t *offsets;
+    const int32_t *rows;
+} gq_expert_rows;
+
+/* dst = X . W^T with X in e4m3 blocks and W in repacked 4-bit blocks: products are exact, sums f32
+ * (the tensor cores' partial sums are taken up by rounded f32 additions every 512 columns).  dst row r
+ * at dst + r * ldd, N values of `type` (rounded once), ldd >= N.  Without a plan W is one matrix and
+ * row m of dst is row m of x; with one W holds E matrices and row r of dst is the product of
+ * its row of x with its expert's matrix.  Results do not depend on timing. */
+gq_status gq_mul_mat_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *dst,
+                              int64_t ldd, gq_type type, int64_t N, int64_t K, cudaStream_t stream);
+
+/* The same for rows of f32 or bf16 (strides as in gq_quantize_mx), quantized to e4m3 blocks inside
+ * the call, in the stream's workspace (grown on demand, as for the products above; GQ_ERR_NO_MEMORY
+ * while the stream is captured: run the call once before capturing). */
+gq_status gq_mul_mat_mxfp4(const void *repacked, const void *x, int64_t ldx, gq_type xtype, void *dst, int64_t ldd,
+                           gq_type type, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
+
+/* A gated unit: gate = X . Wg^T, up = X . Wu^T, and out = silu(gate) * up = gate / (1 + exp(-gate)) * up
+ * in e4m3 blocks (codes [R][F], scales [R][gq_mx_scale_cols(F)]; R the rows of x without a plan).
+ * Repacked weights: for each expert (or once) the matrix Wg [F][K], then Wu [F][K], so 2 E (or 2) matrices in
+ * gq_repack_mxfp4.  F a multiple of 32.  gate and up are f32 sums as above. */
+gq_status gq_swiglu_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *codes,
+                             uint8_t *scales, int64_t F, int64_t K, cudaStream_t stream);
+
+/* Routing.  logits: rows of `type` at stride ldl, E values each.  Scores p = softmax(logits) or
+ * 1 / (1 + exp(-logits)); choice value c = p + bias (bias f32 [E] or NULL).  With top_groups < groups
+ * the experts stand in `groups` equal groups in order; a group's value is the sum of its group_best (1
+ * or 2) largest c, and only experts of the top_groups best groups can be chosen.  The top_k experts with
+ * the largest c are chosen, largest first; equal values: the lower index, of groups too.
+ * Their weights are the scores p, divided by their sum if renormalize is set (left as they are
+ * if the sum is 0), times factor.  The choice is that of exact arithmetic: values that f32 cannot tell
+ * apart are compared in 64 bits.  An expert whose logit is -infinity has score 0; a NaN
+ * logit counts as -infinity; a row without a finite logit has weights 0 (softmax).
+ * E 1 .. 1024, top_k 1 .. 32, 1 to 32 groups that divide E, top_k <= top_groups * E / groups. */
+typedef enum { GQ_SCORE_SOFTMAX = 0, GQ_SCORE_SIGMOID = 1 } gq_score;
+typedef struct gq_router {
+    int64_t E, top_k, score, groups, top_groups, group_best, renormalize;
+    float factor;
+    const float *bias;
+} gq_router;
+
+/* ids int32 [T][top_k], weights f32 [T][top_k]; and, unless all three are NULL, the plan: offsets
+ * int32 [E + 1], rows int32 [T * top_k] (the token of each row: rows sorted by expert, an expert's rows in
+ * the order of the tokens), pos int32 [T][top_k] (the row of each choice).  used (one int32 on the
+ * device, or NULL for T): tokens from *used on are padding: they get ids and pos -1 and weights
+ * 0, and have no rows (a *used outside [0, T] counts as 0 or T and is reported by gq_last_error()).
+ * Uses the stream's workspace, like the products, for T > 32 with a plan. */
+gq_status gq_route(const gq_router *router, const void *logits, int64_t ldl, gq_type type, const int32_t *used,
+                   int32_t *ids, float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, int64_t T,
+                   cudaStream_t stream);
+
+/* out_t = residual_t + sum_j weights[t][j] * y[pos[t][j]] in f32, j in order: y f32 [R][N] (the rows of the down
+ * product), pos and weights as gq_route gives them (a pos outside [0, R) adds nothing), residual (rows of
+ * `rtype` at stride ldr, or NULL), out rows of `type` at stride ldo (may be residual if the types
+ * are equal).  N a multiple of 8; strides as in gq_quantize_mx; top_k 1 .. 32. */
+gq_status gq_experts_combine(const float *y, int64_t R, const int32_t *pos, const float *weights, int64_t top_k,
+                             const void *residual, int64_t ldr, gq_type rtype, void *out, int64_t ldo, gq_type type,
+                             int64_t T, int64_t N, cudaStream_t stream);
+
 /* ---- verification --------------------------------------------------------------- */
 
 /* The integer block dots of the GEMV instruction sequence, for parity tests:

@@ -63,6 +63,31 @@ class AttnScoresStruct(ctypes.Structure):
     _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("window", _I),
                 ("slopes", _P), ("first", _P), ("prefix", _P)]
 
+
+GQ_MX_E2M1 = 0
+GQ_MX_E4M3 = 1
+GQ_TYPE_F32 = 0
+GQ_TYPE_BF16 = 1
+GQ_SCORE_SOFTMAX = 0
+GQ_SCORE_SIGMOID = 1
+
+
+class MXRowsStruct(ctypes.Structure):
+    """gq_mx_rows."""
+    _fields_ = [("rows", _I), ("codes", _P), ("scales", _P)]
+
+
+class ExpertRowsStruct(ctypes.Structure):
+    """gq_expert_rows."""
+    _fields_ = [("E", _I), ("R", _I), ("offsets", _P), ("rows", _P)]
+
+
+class RouterStruct(ctypes.Structure):
+    """gq_router."""
+    _fields_ = ([(n, _I) for n in ("E", "top_k", "score", "groups", "top_groups", "group_best", "renormalize")]
+                + [("factor", ctypes.c_float), ("bias", _P)])
+
+
 # name -> (argtypes, restype); the signatures of include/gq.h
 SIGNATURES = {
     "gq_debug_wait_timeout": ([ctypes.c_uint32, _P], _S),
@@ -75,6 +100,17 @@ SIGNATURES = {
     "gq_attn_pages": ([ctypes.POINTER(KVPagesStruct), ctypes.POINTER(AttnScoresStruct), _P, _I, _P, _I, _I, _I, _P, _I,
                        _P, _P, ctypes.c_float, _P], _S),
     "gq_kv_pages_evict": ([ctypes.POINTER(KVPagesStruct), _P, _I, _I, _I, _P, _P, _P, _P, _P], _S),
+    "gq_mx_scale_cols": ([_I], ctypes.c_size_t),
+    "gq_quantize_mx": ([_P, _I, _S, _S, _P, _P, _I, _I, _P], _S),
+    "gq_dequantize_mx": ([_P, _P, _S, _P, _S, _I, _I, _P], _S),
+    "gq_rms_norm_mx": ([_P, _I, _P, _I, _S, _P, ctypes.c_double, _P, _I, _P, _S, _P, _P, _I, _I, _P], _S),
+    "gq_mxfp4_repacked_bytes": ([_I, _I, _I], ctypes.c_size_t),
+    "gq_repack_mxfp4": ([_P, _P, _P, _I, _I, _I, _P], _S),
+    "gq_mul_mat_mxfp4_mx": ([_P, ctypes.POINTER(MXRowsStruct), ctypes.POINTER(ExpertRowsStruct), _P, _I, _S, _I, _I, _P], _S),
+    "gq_mul_mat_mxfp4": ([_P, _P, _I, _S, _P, _I, _S, _I, _I, _I, _P], _S),
+    "gq_swiglu_mxfp4_mx": ([_P, ctypes.POINTER(MXRowsStruct), ctypes.POINTER(ExpertRowsStruct), _P, _P, _I, _I, _P], _S),
+    "gq_route": ([ctypes.POINTER(RouterStruct), _P, _I, _S, _P, _P, _P, _P, _P, _P, _I, _P], _S),
+    "gq_experts_combine": ([_P, _I, _P, _P, _I, _P, _I, _S, _P, _I, _S, _I, _I, _P], _S),
     "gq_abi_version": ([], ctypes.c_int),
     "gq_status_string": ([_S], ctypes.c_char_p),
     "gq_last_error_message": ([], ctypes.c_char_p),
@@ -429,6 +465,64 @@ def gq_kv_pages_evict(cache, weights, budget: int, keep_first: int, keep_last: i
     _check(lib().gq_kv_pages_evict(_struct(cache), _ptr(weights), budget, keep_first, keep_last, _ptr(table_out),
                                    _ptr(base_out), _ptr(weights_out), _ptr(held_out), _stream(stream)),
            "gq_kv_pages_evict")
+
+
+def gq_mx_scale_cols(K: int) -> int:
+    return lib().gq_mx_scale_cols(K)
+
+
+def gq_quantize_mx(x, ldx: int, type: int, kind: int, codes, scales, M: int, K: int, stream=None) -> None:
+    _check(lib().gq_quantize_mx(_rows_ptr(x), ldx, type, kind, _ptr(codes), _ptr(scales), M, K, _stream(stream)), "gq_quantize_mx")
+
+
+def gq_dequantize_mx(codes, scales, kind: int, y, type: int, M: int, K: int, stream=None) -> None:
+    _check(lib().gq_dequantize_mx(_ptr(codes), _ptr(scales), kind, _ptr(y), type, M, K, _stream(stream)), "gq_dequantize_mx")
+
+
+def gq_rms_norm_mx(x, ldx: int, residual, ldr: int, type: int, weight, eps: float, h, ldh: int, y, ytype: int, codes, scales,
+                   M: int, K: int, stream=None) -> None:
+    _check(lib().gq_rms_norm_mx(_rows_ptr(x), ldx, _rows_ptr(residual), ldr, type, _ptr(weight), eps, _rows_ptr(h), ldh, _ptr(y),
+                                ytype, _ptr(codes), _ptr(scales), M, K, _stream(stream)), "gq_rms_norm_mx")
+
+
+def gq_mxfp4_repacked_bytes(count: int, N: int, K: int) -> int:
+    return lib().gq_mxfp4_repacked_bytes(count, N, K)
+
+
+def gq_repack_mxfp4(codes, scales, repacked, count: int, N: int, K: int, stream=None) -> None:
+    _check(lib().gq_repack_mxfp4(_ptr(codes), _ptr(scales), _ptr(repacked), count, N, K, _stream(stream)), "gq_repack_mxfp4")
+
+
+def gq_mul_mat_mxfp4_mx(repacked, x, plan, dst, ldd: int, type: int, N: int, K: int, stream=None) -> None:
+    """``x``: an MXRowsStruct; ``plan``: an ExpertRowsStruct or None; dst: rows of stride ldd."""
+    _check(lib().gq_mul_mat_mxfp4_mx(_ptr(repacked), _ref(x), _ref(plan), _rows_ptr(dst), ldd, type, N, K, _stream(stream)),
+           "gq_mul_mat_mxfp4_mx")
+
+
+def gq_mul_mat_mxfp4(repacked, x, ldx: int, xtype: int, dst, ldd: int, type: int, M: int, N: int, K: int, stream=None) -> None:
+    _check(lib().gq_mul_mat_mxfp4(_ptr(repacked), _rows_ptr(x), ldx, xtype, _rows_ptr(dst), ldd, type, M, N, K, _stream(stream)),
+           "gq_mul_mat_mxfp4")
+
+
+def gq_swiglu_mxfp4_mx(repacked, x, plan, codes, scales, F: int, K: int, stream=None) -> None:
+    _check(lib().gq_swiglu_mxfp4_mx(_ptr(repacked), _ref(x), _ref(plan), _ptr(codes), _ptr(scales), F, K, _stream(stream)),
+           "gq_swiglu_mxfp4_mx")
+
+
+def gq_route(router, logits, ldl: int, type: int, used, ids, weights, offsets, rows, pos, T: int, stream=None) -> None:
+    """``router``: a RouterStruct."""
+    _check(lib().gq_route(_ref(router), _rows_ptr(logits), ldl, type, _ptr(used), _ptr(ids), _ptr(weights), _ptr(offsets),
+                          _ptr(rows), _ptr(pos), T, _stream(stream)), "gq_route")
+
+
+def gq_experts_combine(y, R: int, pos, weights, top_k: int, residual, ldr: int, rtype: int, out, ldo: int, type: int, T: int,
+                       N: int, stream=None) -> None:
+    _check(lib().gq_experts_combine(_ptr(y), R, _ptr(pos), _ptr(weights), top_k, _rows_ptr(residual), ldr, rtype, _rows_ptr(out),
+                                    ldo, type, T, N, _stream(stream)), "gq_experts_combine")
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 def _struct(x):
@@ -835,3 +929,223 @@ def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, ke
     _check(lib().gq_kv_pages_evict(cache.by_ref, w, budget, keep_first, keep_last, table.data_ptr(), base.data_ptr(),
                                    new.data_ptr(), held.data_ptr(), _current_stream()), "gq_kv_pages_evict")
     return table, base, new, held
+
+
+# ---------------------------------------------------------------------------
+# microscaled formats, routing, experts
+# ---------------------------------------------------------------------------
+def _mx_type(dtype, name: str) -> int:
+    """gq_type of a torch dtype."""
+    if not _types:
+        import torch
+        _types.update({torch.float32: GQ_TYPE_F32, torch.bfloat16: GQ_TYPE_BF16})
+    if dtype not in _types:
+        raise ValueError(f"{name}: expected float32 or bfloat16, got {dtype}")
+    return _types[dtype]
+
+
+_types = {}
+
+
+def _cuda(t, dtype: str, shape, name: str) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape."""
+    if not t.is_cuda or not t.is_contiguous() or str(t.dtype) != "torch." + dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _matrix(x, name: str):
+    """(rows, columns, row stride, gq_type) of a CUDA matrix whose rows are contiguous."""
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name}: expected a CUDA matrix, got {tuple(x.shape)}")
+    (M, K), (ld, one) = x.shape, x.stride()
+    if one != 1 and K > 1:
+        raise ValueError(f"{name}: each row must be contiguous")
+    return M, K, ld if M > 1 else K, _mx_type(x.dtype, name)
+
+
+class MXRows:
+    """Rows in microscaled blocks: codes uint8 [rows, K] (e4m3) or [rows, K / 2] (e2m1), scales uint8 [rows, S]."""
+
+    def __init__(self, codes, scales, kind: int = GQ_MX_E4M3):
+        rows, width = codes.shape
+        self.kind, self.rows, self.K = kind, rows, width * (2 if kind == GQ_MX_E2M1 else 1)
+        c = _cuda(codes, "uint8", codes.shape, "codes")
+        s = _cuda(scales, "uint8", (rows, gq_mx_scale_cols(self.K)), "scales")
+        self.codes, self.scales, self.struct = codes, scales, MXRowsStruct(rows, c, s)
+
+    @classmethod
+    def empty(cls, rows: int, K: int, kind: int = GQ_MX_E4M3, device="cuda"):
+        import torch
+        return cls(torch.empty((rows, K // 2 if kind == GQ_MX_E2M1 else K), dtype=torch.uint8, device=device),
+                   torch.empty((rows, gq_mx_scale_cols(K)), dtype=torch.uint8, device=device), kind)
+
+
+class MXWeights:
+    """`count` repacked 4-bit matrices [N, K] (gq_repack_mxfp4)."""
+
+    def __init__(self, data, count: int, N: int, K: int):
+        self.address = _cuda(data, "uint8", (gq_mxfp4_repacked_bytes(count, N, K),), "data")
+        self.data, self.count, self.N, self.K = data, count, N, K
+
+
+class ExpertPlan:
+    """Rows sorted by expert (gq_expert_rows): offsets int32 [E + 1], the token of each row, the row of each choice [T, top_k]."""
+
+    def __init__(self, offsets, rows, pos):
+        self.offsets, self.rows, self.pos = offsets, rows, pos
+        self.E, self.R = offsets.shape[0] - 1, rows.shape[0]
+        o = _cuda(offsets, "int32", (self.E + 1,), "offsets")
+        r = _cuda(rows, "int32", (self.R,), "rows")
+        _cuda(pos, "int32", pos.shape, "pos")
+        self.gathered, self.in_order = ExpertRowsStruct(self.E, self.R, o, r), ExpertRowsStruct(self.E, self.R, o, None)
+
+
+class Router:
+    """How tokens choose their experts (gq_router)."""
+
+    def __init__(self, E: int, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
+                 group_best: int = 1, renormalize: bool = True, factor: float = 1.0):
+        scores = {"softmax": GQ_SCORE_SOFTMAX, "sigmoid": GQ_SCORE_SIGMOID}
+        if score not in scores:
+            raise ValueError(f"score: expected softmax or sigmoid, got {score}")
+        self.E, self.top_k, self.bias = E, top_k, bias
+        self.struct = RouterStruct(E, top_k, scores[score], groups, top_groups, group_best, renormalize, factor,
+                                   None if bias is None else _cuda(bias, "float32", (E,), "bias"))
+
+
+def quantize_mx(x, kind: int = GQ_MX_E4M3) -> MXRows:
+    """Rows f32 or bf16 [M, K] in microscaled blocks."""
+    M, K, ld, t = _matrix(x, "x")
+    out = MXRows.empty(M, K, kind, x.device)
+    _check(lib().gq_quantize_mx(x.data_ptr(), ld, t, kind, out.struct.codes, out.struct.scales, M, K, _current_stream()),
+           "gq_quantize_mx")
+    return out
+
+
+def dequantize_mx(rows: MXRows, dtype=None):
+    """The values of microscaled rows, f32 (or bf16) [rows, K]."""
+    import torch
+    y = torch.empty((rows.rows, rows.K), dtype=dtype or torch.float32, device=rows.codes.device)
+    _check(lib().gq_dequantize_mx(rows.struct.codes, rows.struct.scales, rows.kind, y.data_ptr(), _mx_type(y.dtype, "dtype"),
+                                  rows.rows, rows.K, _current_stream()), "gq_dequantize_mx")
+    return y
+
+
+def repack_mxfp4(codes, scales, N: int, K: int) -> MXWeights:
+    """e2m1 codes [count * N, K / 2] and scales [count * N, S] as matrices [N, K] for the products."""
+    import torch
+    rows = codes.shape[0]
+    if N <= 0 or rows % N:
+        raise ValueError(f"codes: {rows} rows are not a multiple of N = {N}")
+    c = _cuda(codes, "uint8", (rows, K // 2), "codes")
+    s = _cuda(scales, "uint8", (rows, gq_mx_scale_cols(K)), "scales")
+    data = torch.empty(gq_mxfp4_repacked_bytes(rows // N, N, K), dtype=torch.uint8, device=codes.device)
+    _check(lib().gq_repack_mxfp4(c, s, data.data_ptr(), rows // N, N, K, _current_stream()), "gq_repack_mxfp4")
+    return MXWeights(data, rows // N, N, K)
+
+
+def _operands(w: MXWeights, x: MXRows, plan, gather: bool, parts: int):
+    """(output rows, the plan's struct) of a product, its arguments checked."""
+    if x.kind != GQ_MX_E4M3 or x.K != w.K:
+        raise ValueError(f"x: expected e4m3 rows of K = {w.K}, got kind {x.kind}, K = {x.K}")
+    if w.count != (1 if plan is None else plan.E) * parts:
+        raise ValueError(f"weights: expected {(1 if plan is None else plan.E) * parts} matrices, got {w.count}")
+    if plan is None:
+        if gather:
+            raise ValueError("gather: there is no plan")
+        return x.rows, None
+    return plan.R, ctypes.byref(plan.gathered if gather else plan.in_order)
+
+
+def mul_mat_mxfp4(w: MXWeights, x, plan: ExpertPlan = None, gather: bool = False, dtype=None, out=None):
+    """Rows times 4-bit weights, f32 (or bf16) [rows, N].  x: MXRows, or f32 / bf16 rows (quantized inside).
+
+    With a plan, row r is the product of x's row plan.rows[r] (gather) or r with the weights of its expert;
+    rows from plan.offsets[E] on are left as they are.
+    """
+    import torch
+    if isinstance(x, MXRows):
+        R, ref = _operands(w, x, plan, gather, 1)
+    else:
+        R, K, ldx, xtype = _matrix(x, "x")
+        if plan is not None or K != w.K or w.count != 1:
+            raise ValueError(f"x: expected rows of K = {w.K} and one matrix without a plan, got K = {K} and {w.count}")
+    if out is None:
+        out = torch.empty((R, w.N), dtype=dtype or torch.float32, device=w.data.device)
+    Ro, N, ldd, otype = _matrix(out, "out")
+    if Ro != R or N != w.N:
+        raise ValueError(f"out: expected shape {(R, w.N)}, got {(Ro, N)}")
+    if isinstance(x, MXRows):
+        _check(lib().gq_mul_mat_mxfp4_mx(w.address, ctypes.byref(x.struct), ref, out.data_ptr(), ldd, otype, N, w.K, _current_stream()),
+               "gq_mul_mat_mxfp4_mx")
+    else:
+        _check(lib().gq_mul_mat_mxfp4(w.address, x.data_ptr(), ldx, xtype, out.data_ptr(), ldd, otype, R, N, w.K, _current_stream()),
+               "gq_mul_mat_mxfp4")
+    return out
+
+
+def swiglu_mxfp4(w: MXWeights, x: MXRows, plan: ExpertPlan = None, gather: bool = False) -> MXRows:
+    """silu(x Wg^T) * (x Wu^T) in e4m3 blocks; w holds Wg and Wu, each [F, K], one after the other (for each expert)."""
+    R, ref = _operands(w, x, plan, gather, 2)
+    out = MXRows.empty(R, w.N, GQ_MX_E4M3, w.data.device)
+    _check(lib().gq_swiglu_mxfp4_mx(w.address, ctypes.byref(x.struct), ref, out.struct.codes, out.struct.scales, w.N, w.K,
+                                    _current_stream()), "gq_swiglu_mxfp4_mx")
+    return out
+
+
+def rms_norm_mx(x, weight, eps: float, residual=None, y_dtype=None):
+    """(h, blocks): h = x + residual (x itself without one) and the e4m3 blocks of its norm; with y_dtype (h, blocks, y)."""
+    import torch
+    M, K, ldx, t = _matrix(x, "x")
+    w = None if weight is None else _cuda(weight, "float32", (K,), "weight")
+    h, res, ldr, ldh = x, None, K, K
+    if residual is not None:
+        Mr, Kr, ldr, tr = _matrix(residual, "residual")
+        if (Mr, Kr, tr) != (M, K, t):
+            raise ValueError(f"residual: expected {x.dtype} {(M, K)}, got {residual.dtype} {(Mr, Kr)}")
+        h, res = torch.empty((M, K), dtype=x.dtype, device=x.device), residual.data_ptr()
+    y = None if y_dtype is None else torch.empty((M, K), dtype=y_dtype, device=x.device)
+    out = MXRows.empty(M, K, GQ_MX_E4M3, x.device)
+    _check(lib().gq_rms_norm_mx(x.data_ptr(), ldx, res, ldr, t, w, eps, None if res is None else h.data_ptr(), ldh,
+                                None if y is None else y.data_ptr(), GQ_TYPE_F32 if y is None else _mx_type(y_dtype, "y_dtype"),
+                                out.struct.codes, out.struct.scales, M, K, _current_stream()), "gq_rms_norm_mx")
+    return (h, out) if y is None else (h, out, y)
+
+
+def route(logits, router: Router, used=None):
+    """(ids, weights, plan) of f32 or bf16 logits [T, E]; `used`: int32 [1], tokens from it on are padding."""
+    import torch
+    T, E, ldl, t = _matrix(logits, "logits")
+    if E != router.E:
+        raise ValueError(f"logits: expected {router.E} experts, got {E}")
+    k, dev = router.top_k, logits.device
+    u = None if used is None else _cuda(used, "int32", (1,), "used")
+    ids, pos = (torch.empty((T, k), dtype=torch.int32, device=dev) for _ in range(2))
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    plan = ExpertPlan(torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev), pos)
+    _check(lib().gq_route(ctypes.byref(router.struct), logits.data_ptr(), ldl, t, u, ids.data_ptr(), weights.data_ptr(),
+                          plan.offsets.data_ptr(), plan.rows.data_ptr(), pos.data_ptr(), T, _current_stream()), "gq_route")
+    return ids, weights, plan
+
+
+def experts_combine(y, plan: ExpertPlan, weights, residual=None, dtype=None, out=None):
+    """residual + the weighted sum of each token's rows of y (f32 [R, N]): f32 (or `dtype`) [T, N]."""
+    import torch
+    T, k = plan.pos.shape
+    R, N = y.shape
+    a, w = _cuda(y, "float32", (plan.R, N), "y"), _cuda(weights, "float32", (T, k), "weights")
+    res, ldr, rtype = None, N, GQ_TYPE_F32
+    if residual is not None:
+        Tr, Nr, ldr, rtype = _matrix(residual, "residual")
+        if (Tr, Nr) != (T, N):
+            raise ValueError(f"residual: expected shape {(T, N)}, got {(Tr, Nr)}")
+        res = residual.data_ptr()
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype or torch.float32, device=y.device)
+    To, No, ldo, otype = _matrix(out, "out")
+    if (To, No) != (T, N):
+        raise ValueError(f"out: expected shape {(T, N)}, got {(To, No)}")
+    _check(lib().gq_experts_combine(a, R, plan.pos.data_ptr(), w, k, res, ldr, rtype, out.data_ptr(), ldo, otype, T, N,
+                                    _current_stream()), "gq_experts_combine")
+    return out
