@@ -13,6 +13,7 @@ namespace gq {
 constexpr int MX_TILE = 128;                 // rows and columns of a tile of repacked 4-bit weights
 constexpr int MX_TILE_CODES = MX_TILE * MX_TILE / 2;
 constexpr int MX_TILE_SCALES = MX_TILE * MX_TILE / QK;
+constexpr int MX_TILE_BYTES = MX_TILE_CODES + MX_TILE_SCALES;
 
 // The scale byte of a block whose largest magnitude has these bits: amax = 1.f * 2^(e - 127), and
 // the smallest power of two with amax <= top * power is 2^(e - 127 - 8) for top = 448 = 1.75 * 2^8 and

@@ -5,16 +5,22 @@
 // activations (its N, tensor-memory columns; an MMA is as wide as its tile's rows need, in steps of
 // 16).  kind::mxf8f6f4 multiplies the codes as they are and each block of 32 by its two powers of
 // two, so nothing is converted on the way:
-//   warp 0     copies: the weights' tile by a tensor copy that spreads 16 packed 4-bit codes over 16
-//              bytes (the form in which this kind reads them), its scales by a bulk copy, the
-//              activations' codes by tensor copies of whole rows (gathered four rows at a time where a
-//              plan names them);
-//   warp 1     issues: per stage of 128 columns, copies of the scales into tensor memory and 4 MMAs
-//              (8 for the gated unit, whose gate and up tiles share the activations);
-//   warps 2, 3 bring the activations' scale bytes into the order that tensor memory wants;
+//   warp 0     one thread copies: the weights' tile (packed codes, scales) by a bulk copy, the activations'
+//              codes by a tensor copy;
+//   warps 12 .. 15  spread the weights' codes, each warp every fourth stage (a stage is mostly waiting: for the
+//              copies, for the loads, for the fence, so four of them overlap).  This kind reads 16 4-bit
+//              codes from the first 8 of 16 bytes.  The packed tile arrives in the second half of the 16 KB that it
+//              will take; its first half moves to the free first half, then the second over the place.
+//              (A tensor copy that spreads codes on the way moves 8 bytes a cycle, a quarter of what device
+//              memory gives.)  They also bring the activations' scale bytes into the order that tensor memory
+//              wants, and, where a plan names the rows, their codes, by asynchronous 16-byte copies;
+//   warp 1     one thread issues: per stage of 128 columns, copies of the scales into tensor memory and 4
+//              MMAs (8 for the gated unit, whose gate and up tiles share the activations).  The thread
+//              is elected, not picked by its lane: the compiler then keeps the descriptors in uniform registers,
+//              which halves the cost of an instruction (measured: 80 to 39 cycles per MMA of 16 columns);
 //   warps 4 .. 11  take the sums over: the tensor cores' accumulators cut off what does not fit 24 bits, so
 //              every 4 stages (512 columns) they are added, rounded, to f32 registers, while the
-//              next stages go to the other half of the accumulators; then they store the tile.
+//              next stages go to another set of accumulators; then they store the tile.
 // CTAs take tiles in turn (persistent), those of one expert's weight rows next to each other.  With few
 // tiles a cluster of 2 or 4 CTAs shares a tile's columns; the first adds the others' sums in order.
 #include <cuda.h>
@@ -30,64 +36,73 @@
 namespace gq {
 namespace {
 
-constexpr int THREADS = 384;
+constexpr int THREADS = 512;
 constexpr int EPI_WARPS = 8;
+constexpr int SPREAD_WARPS = 4;              // each takes every fourth stage
 constexpr int FLUSH = 4;                     // stages per take-over of the accumulators
 constexpr int A_BYTES = MX_TILE * MX_TILE;   // a weight tile in shared memory: one byte's room per code
+constexpr int A_SLOT = A_BYTES + 1024;       // and its scales, 1024-aligned
 constexpr int MAX_E = 1024;
-constexpr int MAX_STAGES = 8;
+constexpr int MAX_STAGES = 8, MAX_SETS = 4;
+constexpr int FEW_REGS = 88, MANY_REGS = 168;   // per thread, of 128 at launch: 2 x 88 + 2 x 168 = 4 x 128
 
 // BN: rows of activations per tile.  GATED: two weight tiles (gate, up) per stage.
 template <int BN, bool GATED>
 struct Cfg {
     static constexpr int NA = GATED ? 2 : 1;
     static constexpr int NB = (BN + 127) / 128;             // 512-byte pieces of activation scales
-    static constexpr int ST = GATED ? 4 : BN <= 16 ? 6 : BN <= 64 ? 8 : 5;
-    static constexpr int BOX = BN <= 16 ? 16 : 32;          // activation rows per tensor copy
+    static constexpr int ST = GATED ? 4 : BN <= 64 ? 8 : 5;
+    static constexpr bool BIG = BN > 64;                    // more sums per thread than an even share of registers holds
+    static constexpr int NR = (BN + 31) / 32;               // activation rows of a lane
+    static constexpr int PARTS = BN > 64 ? 2 : 1;           // tensor copies of a tile's activations, BN / PARTS rows each
+    static constexpr int BOX = BN / PARTS;
     static constexpr int CW = BN <= 16 ? 8 : 16;            // columns per read of tensor memory
     static constexpr int CHUNKS = BN / CW;
     static constexpr int MINE = (CHUNKS + 1) / 2;           // chunks of a warpgroup
     static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;
-    // tensor memory: two sets of accumulators, then the scales of every stage
+    // tensor memory: sets of accumulators, then the scales of every stage
     static constexpr int ACC = NA * BN;
-    static constexpr int SF = 2 * ACC;
     static constexpr int SF_STAGE = 4 * (NA + NB);
+    static constexpr int SETS = 4 * ACC + ST * SF_STAGE <= 512 ? 4 : 2;
+    static constexpr int SF = SETS * ACC;
     static constexpr int COLS_USED = SF + ST * SF_STAGE;
     static constexpr int COLS = COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
     static_assert(COLS_USED <= 512, "tensor memory");
+    static_assert(BOX % 8 == 0 && BN % 16 == 0, "tile rows");
     // shared memory from a 1024-aligned base
-    static constexpr int B_STAGE = (BN + BOX - 1) / BOX * BOX * 128;
+    static constexpr int B_STAGE = BN * 128;
     static constexpr int a = 0;
-    static constexpr int b = a + ST * NA * A_BYTES;
-    static constexpr int sfa = b + ST * B_STAGE;
-    static constexpr int sfb = sfa + ST * NA * MX_TILE_SCALES;
+    static constexpr int b = a + ST * NA * A_SLOT;
+    static constexpr int sfb = b + ST * B_STAGE;
     static constexpr int part = sfb + ST * NB * 512;
     static constexpr int PART_BYTES = NA * BN * MX_TILE * 4;
     static constexpr int starts = part + (MAX_SPLIT - 1) * PART_BYTES;
-    static constexpr int bars = starts + (MAX_E + 4) * 4;
-    static constexpr int total = bars + 256;
+    static constexpr int bars = starts + 3 * (MAX_E + 4) * 4;
+    static constexpr int total = bars + 320;
     static_assert(total + 1024 <= 227 * 1024, "shared memory");
     static_assert(ST <= MAX_STAGES, "barriers");
 };
 
 enum : int {
-    FULL = 0,
-    EMPTY = FULL + MAX_STAGES,
+    RAW = 0,                     // a stage's copies have landed
+    FULL = RAW + MAX_STAGES,     // its weights are spread, its activations' scales written
+    EMPTY = FULL + MAX_STAGES,   // its MMAs are done
     ACC_FULL = EMPTY + MAX_STAGES,
-    ACC_EMPTY = ACC_FULL + 2,
-    PART_FULL = ACC_EMPTY + 2,
+    ACC_EMPTY = ACC_FULL + MAX_SETS,
+    PART_FULL = ACC_EMPTY + MAX_SETS,
     PART_EMPTY,
     NUM_BARS
 };
-static_assert(NUM_BARS * 8 + 8 <= 256, "barrier area");
+static_assert(NUM_BARS * 8 + 8 <= 320, "barrier area");
 
 struct MxParams {
-    const uint8_t *w_scales;       // of all tiles
+    const uint8_t *w;              // tiles
     const uint8_t *x_scales;
     const int32_t *offsets, *rows;
     void *dst;
     uint8_t *codes, *scales;       // gated: the output's
     unsigned int *status;
+    const uint8_t *x_codes;        // for gathered rows
     int64_t ldd, x_rows;
     int N, K, KT, G, S, So;        // S, So: scale bytes per row of x and of the gated output
     int E, R, split, bf16;
@@ -105,9 +120,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
-// kind::mxf8f6f4: A e2m1 (5), B e4m3 (0), both K-major, scales ue8m0, f32 sums; scale byte `sf` of both
-__device__ __forceinline__ uint32_t mx_idesc(int n, int sf) {
-    return (uint32_t)sf << 4 | 5u << 7 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24 | (uint32_t)sf << 29;
+// kind::mxf8f6f4: A e2m1 (5), B e4m3 (0), both K-major, scales ue8m0, f32 sums; the scale bytes'
+// places (0 .. 3) go to bits 4 and 29
+__device__ __forceinline__ uint32_t mx_idesc(int n) {
+    return 5u << 7 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24;
 }
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {
@@ -132,17 +148,39 @@ __device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap *map, in
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
-// four rows of 128 bytes
-__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap *map, int c0, int4 r, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(dst), "l"(map), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
-        : "memory");
+// one lane of the warp
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
+// 16 bytes, zeros unless `there`
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+// A place in the ring of stages and the parity of its turn.
+template <int ST>
+struct Ring {
+    int st = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == ST) st = 0, turn ^= 1;
+    }
+};
+// A role's registers (all warps of a warpgroup take the same step).
+template <bool BIG, bool MANY>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (BIG && MANY) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
+    if constexpr (BIG && !MANY) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
+}
+// W columns of this warp's 32 lanes; the values are there after tcgen05.wait::ld
 template <int W>
-__device__ __forceinline__ void read_acc(uint32_t taddr, float (&v)[W]) {
-    uint32_t r[W];
+__device__ __forceinline__ void read_acc(uint32_t taddr, uint32_t (&r)[W]) {
     if constexpr (W == 16)
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -153,9 +191,11 @@ __device__ __forceinline__ void read_acc(uint32_t taddr, float (&v)[W]) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < W; i++) v[i] = __uint_as_float(r[i]);
+}
+// a value read from tensor memory, not used before the wait in front of this
+__device__ __forceinline__ float keep(uint32_t r) {
+    asm volatile("" : "+r"(r));
+    return __uint_as_float(r);
 }
 
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
@@ -174,27 +214,39 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsi
     return false;
 }
 
+// x / (1 + exp(-x)); the exponential and the reciprocal are the fast ones, off by a few units of f32.
+__device__ __forceinline__ float swish(float x) {
+    float e, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return x * r;
+}
+
+// Where tiles lie, in shared memory: starts[e] tiles of BN rows (for one group of weight rows) come before
+// expert e, whose rows are first[e] .. last[e] - 1.
+struct Where {
+    int32_t *starts, *first, *last;
+};
 // Tile `i` of the launch: expert e, weight rows 128 g .., activation rows r0 .. r0 + n - 1.
 struct Tile {
     int e, g, r0, n;
 };
 template <int BN>
-__device__ __forceinline__ Tile tile_at(const MxParams &p, const int32_t *starts, int i) {
+__device__ __forceinline__ Tile tile_at(const MxParams &p, const Where &w, int i) {
     int lo = 0, hi = p.E;                                  // starts[e] * G <= i < starts[e + 1] * G
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (starts[mid] * p.G <= i)
+        if (w.starts[mid] * p.G <= i)
             lo = mid;
         else
             hi = mid;
     }
-    const int nt = starts[lo + 1] - starts[lo], local = i - starts[lo] * p.G;
+    const int nt = w.starts[lo + 1] - w.starts[lo], local = i - w.starts[lo] * p.G;
     Tile t;
     t.e = lo;
     t.g = local / nt;
-    const int k = local - t.g * nt, r0 = p.offsets ? p.offsets[lo] : 0, r1 = p.offsets ? p.offsets[lo + 1] : p.R;
-    t.r0 = r0 + k * BN;
-    t.n = min(BN, r1 - t.r0);
+    t.r0 = w.first[lo] + (local - t.g * nt) * BN;
+    t.n = min(BN, w.last[lo] - t.r0);
     return t;
 }
 
@@ -203,23 +255,27 @@ __device__ __forceinline__ Tile tile_at(const MxParams &p, const int32_t *starts
 // ---------------------------------------------------------------------------
 template <int BN, bool GATED>
 __global__ void __launch_bounds__(THREADS, 1)
-    mx_product_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const MxParams p) {
+    mx_product_kernel(const __grid_constant__ CUtensorMap map_x, const MxParams p) {
     using C = Cfg<BN, GATED>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bars);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NUM_BARS);
-    int32_t *starts = reinterpret_cast<int32_t *>(smem + C::starts);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Where where;
+    where.starts = reinterpret_cast<int32_t *>(smem + C::starts);
+    where.first = where.starts + MAX_E + 4;
+    where.last = where.first + MAX_E + 4;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int split = p.split, rank = (int)blockIdx.x % split, cluster = (int)blockIdx.x / split, clusters = (int)gridDim.x / split;
     auto bar = [&](int i) { return smem_addr(bars + i); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::ST; i++) {
-            mbar_init(bar(FULL + i), 1 + (C::NB > 1 ? 2 : 1));
+            mbar_init(bar(RAW + i), 1);
+            mbar_init(bar(FULL + i), 1);
             mbar_init(bar(EMPTY + i), 1);
         }
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < C::SETS; i++) {
             mbar_init(bar(ACC_FULL + i), 1);
             mbar_init(bar(ACC_EMPTY + i), EPI_WARPS);
         }
@@ -242,6 +298,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             int tiles = 0;
             if (e < p.E) {
                 const int r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.R;
+                where.first[e] = r0;
+                where.last[e] = r1;
                 if (r0 < 0 || r1 < r0 || r1 > p.R) {
                     atomicOr(p.status, STATUS_RANGE);
                 } else {
@@ -254,158 +312,230 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int u = __shfl_up_sync(0xffffffffu, s, d);
                 if (lane >= d) s += u;
             }
-            if (e < p.E) starts[e] = before + s - tiles;
+            if (e < p.E) where.starts[e] = before + s - tiles;
             before += __shfl_sync(0xffffffffu, s, 31);
         }
-        if (lane == 0) starts[p.E] = before;
+        if (lane == 0) where.starts[p.E] = before;
     }
     fence_before();
     __syncthreads();
     if (split > 1) cluster_sync();            // every CTA's barriers are there before others arrive on them
     fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tiles = starts[p.E] * p.G;
+    const int tiles = where.starts[p.E] * p.G;
     const int kt0 = (int)((int64_t)p.KT * rank / split), nk = (int)((int64_t)p.KT * (rank + 1) / split) - kt0;
     bool failed = false;
-
     if (warp == 0) {
         // ------------------------------------------------------------------ copies
-        int step = 0;
-        for (int i = cluster; i < tiles && !failed; i += clusters) {
-            const Tile t = tile_at<BN>(p, starts, i);
-            const int boxes = (t.n + C::BOX - 1) / C::BOX, quads = (t.n + 3) / 4;
-            int4 idx[C::NB];
-            if (p.rows) {
-#pragma unroll
-                for (int u = 0; u < C::NB; u++) {
-                    int r[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int c = (u * 32 + lane) * 4 + j;
-                        r[j] = c < t.n ? p.rows[t.r0 + c] : (int)p.x_rows;
-                        if (r[j] < 0 || r[j] > p.x_rows || (r[j] == p.x_rows && c < t.n)) {
-                            atomicOr(p.status, STATUS_RANGE);
-                            r[j] = (int)p.x_rows;                 // past the end: zeros
+        set_registers<C::BIG, false>();
+        if (elect()) {
+            Ring<C::ST> ring;
+            int filled = 0;
+            for (int i = cluster; i < tiles && !failed; i += clusters) {
+                const Tile t = tile_at<BN>(p, where, i);
+                const uint8_t *w = p.w + (((int64_t)t.e * C::NA * p.G + t.g) * p.KT + kt0) * MX_TILE_BYTES;
+                const int64_t up = (int64_t)p.G * p.KT * MX_TILE_BYTES;    // from the gate's tile to the up matrix's
+                const int parts = p.rows ? 0 : t.n > C::BOX ? C::PARTS : 1;
+                const uint32_t bytes = (uint32_t)(C::NA * MX_TILE_BYTES + parts * C::BOX * 128);
+                for (int k = 0; k < nk; k++, w += MX_TILE_BYTES, ring.next()) {
+                    if (filled == C::ST) {
+                        if (!mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) {
+                            failed = true;
+                            break;
                         }
+                    } else {
+                        filled++;
                     }
-                    idx[u] = make_int4(r[0], r[1], r[2], r[3]);
-                }
-            }
-            // (the weights' copy counts the bytes that it reads, not the room that it fills)
-            const uint32_t bytes = (uint32_t)(C::NA * (MX_TILE_CODES + MX_TILE_SCALES) + (p.rows ? quads * 512 : boxes * C::BOX * 128));
-            for (int k = 0; k < nk; k++, step++) {
-                const int st = step % C::ST, kt = kt0 + k;
-                if (step >= C::ST && !mbar_wait(bar(EMPTY + st), (uint32_t)((step / C::ST - 1) & 1), p.status)) failed = true;
-                if (__any_sync(0xffffffffu, failed)) {
-                    failed = true;
-                    break;
-                }
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(FULL + st), bytes);
+                    const uint32_t raw = bar(RAW + ring.st);
+                    mbar_arrive_expect_tx(raw, bytes);
 #pragma unroll
-                    for (int a = 0; a < C::NA; a++) {
-                        const int64_t tile = ((int64_t)(t.e * C::NA + a) * p.G + t.g) * p.KT + kt;
-                        copy_2d(smem_addr(smem + C::a + (st * C::NA + a) * A_BYTES), &map_w, 0, (int)(tile * MX_TILE), bar(FULL + st));
-                        bulk_g2s(smem_addr(smem + C::sfa + (st * C::NA + a) * MX_TILE_SCALES), p.w_scales + tile * MX_TILE_SCALES,
-                                 MX_TILE_SCALES, bar(FULL + st));
-                    }
-                    if (!p.rows)
-                        for (int u = 0; u < boxes; u++)
-                            copy_2d(smem_addr(smem + C::b + st * C::B_STAGE + u * C::BOX * 128), &map_x, kt * MX_TILE, t.r0 + u * C::BOX,
-                                    bar(FULL + st));
-                }
-                __syncwarp();
-                if (p.rows) {
+                    for (int a = 0; a < C::NA; a++)
+                        bulk_g2s(smem_addr(smem + C::a) + (uint32_t)((ring.st * C::NA + a) * A_SLOT + A_BYTES - MX_TILE_CODES), w + a * up,
+                                 MX_TILE_BYTES, raw);
 #pragma unroll
-                    for (int u = 0; u < C::NB; u++)
-                        if (u * 32 + lane < quads)
-                            copy_rows4(smem_addr(smem + C::b + st * C::B_STAGE + (u * 32 + lane) * 512), &map_x, kt * MX_TILE, idx[u],
-                                       bar(FULL + st));
+                    for (int u = 0; u < C::PARTS; u++)
+                        if (u < parts)
+                            copy_2d(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE + u * C::BOX * 128), &map_x, (kt0 + k) * MX_TILE,
+                                    t.r0 + u * C::BOX, raw);
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMAs
-        int step = 0, chunk = 0;
-        for (int i = cluster; i < tiles && !failed; i += clusters) {
-            const Tile t = tile_at<BN>(p, starts, i);
-            const int n = (t.n + 15) & ~15;
-            for (int k = 0; k < nk; k++, step++) {
-                const int st = step % C::ST, set = chunk & 1;
-                if (k % FLUSH == 0 && chunk >= 2 && !mbar_wait(bar(ACC_EMPTY + set), (uint32_t)((chunk / 2 - 1) & 1), p.status))
-                    failed = true;
-                if (!failed && !mbar_wait(bar(FULL + st), (uint32_t)((step / C::ST) & 1), p.status)) failed = true;
-                if (__any_sync(0xffffffffu, failed)) {
-                    failed = true;
-                    break;
-                }
-                fence_after();
-                if (lane == 0) {
-                    const uint32_t acc = tmem + (uint32_t)(set * C::ACC), sf = tmem + (uint32_t)(C::SF + st * C::SF_STAGE);
-#pragma unroll
-                    for (int a = 0; a < C::NA; a++)
-                        copy_scales(sf + 4 * a, scales_desc(smem_addr(smem + C::sfa + (st * C::NA + a) * MX_TILE_SCALES)));
-#pragma unroll
-                    for (int u = 0; u < C::NB; u++)
-                        if (u * 128 < n)
-                            copy_scales(sf + 4 * (C::NA + u), scales_desc(smem_addr(smem + C::sfb + (st * C::NB + u) * 512)));
-                    const uint64_t bd = operand_desc(smem_addr(smem + C::b + st * C::B_STAGE));
-#pragma unroll
-                    for (int a = 0; a < C::NA; a++) {
-                        const uint64_t ad = operand_desc(smem_addr(smem + C::a + (st * C::NA + a) * A_BYTES));
-#pragma unroll
-                        for (int kk = 0; kk < 4; kk++)     // 32 columns: 32 bytes further in both operands
-                            mma_mx(acc + a * BN, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), mx_idesc(n, kk), sf + 4 * a,
-                                   sf + 4 * C::NA, k % FLUSH != 0 || kk > 0);
-                    }
-                    commit(bar(EMPTY + st));
-                    if (k % FLUSH == FLUSH - 1 || k == nk - 1) commit(bar(ACC_FULL + set));
-                }
-                __syncwarp();
-                if (k % FLUSH == FLUSH - 1 || k == nk - 1) chunk++;
-            }
-        }
-    } else if (warp < 4) {
-        // ------------------------------------------------------------------ the activations' scales
-        const int u = warp - 2;                            // rows 128 u .. of the tile
-        if (u < C::NB) {
-            int step = 0;
+        set_registers<C::BIG, false>();
+        if (elect()) {
+            Ring<C::ST> ring;
+            Ring<C::SETS> set;
+            int chunks = 0;
             for (int i = cluster; i < tiles && !failed; i += clusters) {
-                const Tile t = tile_at<BN>(p, starts, i);
-                const uint8_t *row[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int c = u * 128 + j * 32 + lane;
-                    int64_t r = -1;
-                    if (c < t.n) r = p.rows ? p.rows[t.r0 + c] : t.r0 + c;
-                    row[j] = r >= 0 && r < p.x_rows ? p.x_scales + r * p.S : nullptr;
-                }
-                for (int k = 0; k < nk; k++, step++) {
-                    const int st = step % C::ST, kt = kt0 + k;
-                    uint32_t w[4];
-                    // scale bytes past the row's end belong to columns of zeros, but must not be NaN
-                    const int left = p.K / QK - kt * 4;
-                    const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
-#pragma unroll
-                    for (int j = 0; j < 4; j++) w[j] = row[j] ? *reinterpret_cast<const uint32_t *>(row[j] + kt * 4) & mask : 0u;
-                    if (step >= C::ST && !mbar_wait(bar(EMPTY + st), (uint32_t)((step / C::ST - 1) & 1), p.status)) failed = true;
-                    if (__any_sync(0xffffffffu, failed)) {
+                const Tile t = tile_at<BN>(p, where, i);
+                const int n = (t.n + 15) & ~15;
+                const uint32_t idesc = mx_idesc(n);
+                for (int k = 0; k < nk; k++, ring.next()) {
+                    const int in_chunk = k % FLUSH;
+                    if (in_chunk == 0) {
+                        if (chunks == C::SETS) {
+                            if (!mbar_wait(bar(ACC_EMPTY + set.st), set.turn ^ 1, p.status)) failed = true;
+                        } else {
+                            chunks++;
+                        }
+                    }
+                    // (whoever arrived there had waited for the stage's copies)
+                    if (failed || !mbar_wait(bar(FULL + ring.st), ring.turn, p.status)) {
                         failed = true;
                         break;
                     }
-                    *reinterpret_cast<uint4 *>(smem + C::sfb + (st * C::NB + u) * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(FULL + st));
+                    fence_after();
+                    const uint32_t acc = tmem + (uint32_t)(set.st * C::ACC), sf = tmem + (uint32_t)(C::SF + ring.st * C::SF_STAGE);
+                    const uint32_t as = smem_addr(smem + C::a) + (uint32_t)(ring.st * C::NA * A_SLOT);
+#pragma unroll
+                    for (int a = 0; a < C::NA; a++) copy_scales(sf + 4 * a, scales_desc(as + a * A_SLOT + A_BYTES));
+#pragma unroll
+                    for (int u = 0; u < C::NB; u++)
+                        if (u == 0 || u * 128 < n)
+                            copy_scales(sf + 4 * (C::NA + u), scales_desc(smem_addr(smem + C::sfb) + (uint32_t)((ring.st * C::NB + u) * 512)));
+                    const uint64_t bd = operand_desc(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE));
+#pragma unroll
+                    for (int a = 0; a < C::NA; a++) {
+                        const uint64_t ad = operand_desc(as + a * A_SLOT);
+#pragma unroll
+                        for (int kk = 0; kk < 4; kk++)     // 32 columns: 32 bytes further in both operands, the next scale byte
+                            mma_mx(acc + a * BN, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc + (uint32_t)kk * ((1u << 4) | (1u << 29)),
+                                   sf + 4 * a, sf + 4 * C::NA, in_chunk > 0 || kk > 0);
+                    }
+                    commit(bar(EMPTY + ring.st));
+                    if (in_chunk == FLUSH - 1 || k == nk - 1) {
+                        commit(bar(ACC_FULL + set.st));
+                        set.next();
+                    }
                 }
             }
         }
-    } else {
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------------ spreading, the activations' scales
+        set_registers<C::BIG, false>();
+        // This warp's next stage: step k of tile i, step `at` of the launch.  The scale bytes of its rows (row 32 j +
+        // lane of the tile; -1: none) are loaded one of its stages ahead.
+        int i = cluster, k = warp - 12, from[C::NR];
+        uint32_t next[C::NR];
+        Ring<C::ST> ring;
+        for (int j = 0; j < k; j++) ring.next();
+        Tile t{};
+        auto rows_of = [&] {
+            t = tile_at<BN>(p, where, i);
+#pragma unroll
+            for (int j = 0; j < C::NR; j++) {
+                const int c = j * 32 + lane;
+                from[j] = -1;
+                if (c < t.n) {
+                    from[j] = p.rows ? p.rows[t.r0 + c] : t.r0 + c;
+                    if (from[j] < 0 || from[j] >= p.x_rows) {
+                        atomicOr(p.status, STATUS_RANGE);
+                        from[j] = -1;
+                    }
+                }
+            }
+        };
+        auto load = [&] {
+            // bytes past the row's end belong to columns of zeros, but must not be NaN
+            const int left = p.K / QK - (kt0 + k) * 4;
+            const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+#pragma unroll
+            for (int j = 0; j < C::NR; j++)
+                next[j] = from[j] < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (int64_t)from[j] * p.S) + kt0 + k) & mask;
+        };
+        // to the stage `by` steps further, if there is one
+        auto advance = [&] {
+            bool other = false;
+            while (k >= nk && i < tiles) {
+                k -= nk;
+                i += clusters;
+                other = true;
+            }
+            if (i >= tiles) return false;
+            if (other) rows_of();
+            load();
+            return true;
+        };
+        bool more = cluster < tiles;
+        if (more) {
+            rows_of();
+            more = advance();
+            if (more) load();
+        }
+        // the places of 32 codes: row 8 j + lane / 4, columns 32 (lane % 4) ..
+        const int r8 = lane >> 2, c0 = 2 * (lane & 3);
+        const uint32_t to0 = (uint32_t)(r8 * 128 + ((c0 ^ r8) << 4)), to1 = (uint32_t)(r8 * 128 + (((c0 + 1) ^ r8) << 4));
+        bool first = true;                                  // turn of the ring: no stage is in use yet
+        while (more && !failed) {
+            uint32_t now[C::NR];
+#pragma unroll
+            for (int j = 0; j < C::NR; j++) now[j] = next[j];
+            uint8_t *const slot = smem + C::a + ring.st * C::NA * A_SLOT;
+            // The stage's last MMAs are done: its place is free for gathered rows, and its copies' barrier, which
+            // another warp may have waited on the turn before, is at this turn (a parity tells two turns apart,
+            // not three).
+            if (!first && !mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) break;
+            if (p.rows) {
+                // 16 bytes, piece lane % 8, of the tile's rows lane / 8, lane / 8 + 4, ..
+                const int col = (kt0 + k) * MX_TILE + (lane & 7) * 16;
+                const uint32_t b = smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE);
+#pragma unroll 4
+                for (int c = lane >> 3; c < t.n; c += 4) {
+                    const int r = __ldg(p.rows + t.r0 + c);
+                    const bool there = r >= 0 && r < p.x_rows && col < p.K;
+                    copy16(b + (uint32_t)(c * 128 + (((lane & 7) ^ (c & 7)) << 4)), p.x_codes + (there ? (int64_t)r * p.K + col : 0), there);
+                }
+                copy_group();
+            }
+            const int st = ring.st;
+            const uint32_t turn = ring.turn;
+            k += SPREAD_WARPS;
+#pragma unroll
+            for (int j = 0; j < SPREAD_WARPS; j++) {
+                ring.next();
+                if (ring.st == 0) first = false;
+            }
+            more = advance();
+            if (!mbar_wait(bar(RAW + st), turn, p.status)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) break;
+#pragma unroll
+            for (int a = 0; a < C::NA; a++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {               // 64 rows at a time
+                    uint8_t *tile = slot + a * A_SLOT;
+                    uint4 v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[j] = lds128(tile + (A_BYTES - MX_TILE_CODES) + h * 4096 + j * 512 + lane * 16);
+                    __syncwarp();                           // all of what the second half's place holds is read
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        *reinterpret_cast<uint2 *>(tile + to0 + (h * 8 + j) * 1024) = make_uint2(v[j].x, v[j].y);
+                        *reinterpret_cast<uint2 *>(tile + to1 + (h * 8 + j) * 1024) = make_uint2(v[j].z, v[j].w);
+                    }
+                }
+#pragma unroll
+            for (int u = 0; u < C::NB; u++) {
+                auto word = [&](int j) { return j < C::NR ? now[j < C::NR ? j : 0] : 0u; };
+                *reinterpret_cast<uint4 *>(smem + C::sfb + (st * C::NB + u) * 512 + lane * 16) =
+                    make_uint4(word(4 * u), word(4 * u + 1), word(4 * u + 2), word(4 * u + 3));
+            }
+            if (p.rows) copy_wait<0>();
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(FULL + st));
+        }
+    } else if (warp >= 4) {
         // ------------------------------------------------------------------ sums, output
+        set_registers<C::BIG, true>();
         const int q = warp & 3, half = (warp - 4) >> 2;    // tensor-memory lanes 32 q .., column chunks half, half + 2, ..
-        int chunk = 0, turn = 0;
+        int turn = 0;
+        Ring<C::SETS> set;
         for (int i = cluster; i < tiles && !failed; i += clusters, turn++) {
-            const Tile t = tile_at<BN>(p, starts, i);
+            const Tile t = tile_at<BN>(p, where, i);
             const int cols = (t.n + C::CW - 1) / C::CW;    // chunks in use
             float acc[C::NA][C::MINE][C::CW];
 #pragma unroll
@@ -414,25 +544,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < C::MINE; j++)
 #pragma unroll
                     for (int c = 0; c < C::CW; c++) acc[a][j][c] = 0.0f;
-            for (int k = 0; k < nk; k += FLUSH, chunk++) {
-                const int set = chunk & 1;
-                if (!failed && !mbar_wait(bar(ACC_FULL + set), (uint32_t)((chunk / 2) & 1), p.status)) failed = true;
+            for (int k = 0; k < nk; k += FLUSH, set.next()) {
+                if (!mbar_wait(bar(ACC_FULL + set.st), set.turn, p.status)) failed = true;
                 failed = __any_sync(0xffffffffu, failed);
                 if (failed) break;
                 fence_after();
+                const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(set.st * C::ACC + half * C::CW);
+                // two reads of tensor memory under way at a time
 #pragma unroll
-                for (int a = 0; a < C::NA; a++)
+                for (int j = 0; j < C::MINE; j += 2 / C::NA) {
+                    constexpr int W = C::CW, X = 2 / C::NA;
+                    uint32_t v[X][C::NA][W];
 #pragma unroll
-                    for (int j = 0; j < C::MINE; j++)
-                        if (2 * j + half < cols) {
-                            float v[C::CW];
-                            read_acc<C::CW>(tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(set * C::ACC + a * BN + (2 * j + half) * C::CW), v);
+                    for (int x = 0; x < X; x++)
 #pragma unroll
-                            for (int c = 0; c < C::CW; c++) acc[a][j][c] += v[c];
-                        }
+                        for (int a = 0; a < C::NA; a++)
+                            if (j + x < C::MINE && 2 * (j + x) + half < cols) read_acc<W>(at + (uint32_t)(a * BN + 2 * (j + x) * W), v[x][a]);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int x = 0; x < X; x++)
+#pragma unroll
+                        for (int a = 0; a < C::NA; a++)
+                            if (j + x < C::MINE && 2 * (j + x) + half < cols)
+#pragma unroll
+                                for (int c = 0; c < W; c++) acc[a][j + x < C::MINE ? j + x : 0][c] += keep(v[x][a][c]);
+                }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(ACC_EMPTY + set));
+                if (lane == 0) mbar_arrive(bar(ACC_EMPTY + set.st));
             }
             if (failed) break;
             if (C::MAX_SPLIT > 1 && split > 1) {
@@ -496,21 +635,37 @@ __global__ void __launch_bounds__(THREADS, 1)
             } else {
                 // a warp's 32 lanes are one block of 32 output values of each column's row; N is a
                 // multiple of 32, so the block is there as a whole or not at all
-                if (t.g * MX_TILE + 32 * q < p.N)
+                if (t.g * MX_TILE + 32 * q < p.N) {
+                    uint8_t *const codes = p.codes + (int64_t)t.r0 * p.N + t.g * MX_TILE + 32 * q + (lane & ~3);
+                    uint8_t *const scales = p.scales + (int64_t)t.r0 * p.So + t.g * 4 + q;
 #pragma unroll
                     for (int j = 0; j < C::MINE; j++)
 #pragma unroll
-                        for (int c = 0; c < C::CW; c++) {
+                        for (int c = 0; c < C::CW; c += 4) {
                             const int col = (2 * j + half) * C::CW + c;
-                            if (col < t.n) {
-                                const float gate = acc[0][j][c], v = gate / (1.0f + expf(-gate)) * acc[1][j][c];
+                            if (col >= t.n) continue;
+                            uint32_t word = 0;             // this lane's code in each of four columns
+                            uint32_t bytes = 0;            // their scales
+#pragma unroll
+                            for (int x = 0; x < 4; x++) {
+                                const float v = swish(acc[0][j][c + x]) * acc[1][j][c + x];
                                 const int b = mx_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu), false);
                                 const float inv = mx_inverse(b);
-                                const int64_t r = t.r0 + col;
-                                p.codes[r * p.N + n] = (uint8_t)(inv == 0.0f ? 0u : e4m3x2(v * inv, 0.0f));
-                                if (lane == 0) p.scales[r * p.So + t.g * 4 + q] = (uint8_t)b;
+                                word |= (inv == 0.0f ? 0u : e4m3x2(v * inv, 0.0f)) << (8 * x);
+                                bytes |= (uint32_t)b << (8 * x);
+                            }
+                            // four lanes turn their 4 x 4 codes: lane l & 3 then has column l & 3's four
+                            uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
+                            word = lane & 1 ? __byte_perm(other, word, 0x7351) : __byte_perm(word, other, 0x6240);
+                            other = __shfl_xor_sync(0xffffffffu, word, 2);
+                            word = lane & 2 ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
+                            const int mine = col + (lane & 3);
+                            if (mine < t.n) {
+                                *reinterpret_cast<uint32_t *>(codes + (int64_t)mine * p.N) = word;
+                                if (lane < 4) scales[(int64_t)mine * p.So] = (uint8_t)(bytes >> (8 * lane));
                             }
                         }
+                }
                 // the scales' padding, by the warp of the row's last block
                 const int last = p.N / QK - 1;
                 if (t.g * 4 + q == last)
@@ -523,6 +678,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
             }
         }
+    } else {
+        set_registers<C::BIG, false>();
     }
     __syncwarp();
     fence_before();
@@ -540,8 +697,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-gq_status encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner, int64_t outer, int64_t stride,
-                 int box_rows) {
+// rows of K bytes; boxes of 128 bytes x box_rows rows, 128-byte swizzle, zeros outside
+gq_status encode(CUtensorMap *map, const void *base, int64_t rows, int64_t K, int box_rows) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -550,20 +707,21 @@ gq_status encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, i
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (!g_encode) return fail(GQ_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
-    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride};
+    const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K};
     const cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = g_encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(GQ_ERR_CUDA, "cuTensorMapEncodeTiled (mx) failed (%d)", (int)r);
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GQ_ERR_CUDA, "cuTensorMapEncodeTiled (mx rows) failed (%d)", (int)r);
     return GQ_OK;
 }
 
 constexpr int MAX_DEV = 64;
 
 template <int BN, bool GATED>
-gq_status launch(MxParams p, const void *rep, const gq_mx_rows &x, int64_t tiles128, int64_t most_tiles, cudaStream_t s) {
+gq_status launch(MxParams p, const gq_mx_rows &x, int64_t most_tiles, cudaStream_t s) {
     using C = Cfg<BN, GATED>;
     static std::atomic<bool> allowed[MAX_DEV];
     auto kernel = mx_product_kernel<BN, GATED>;
@@ -575,10 +733,8 @@ gq_status launch(MxParams p, const void *rep, const gq_mx_rows &x, int64_t tiles
         if (st != GQ_OK) return st;
         if (dev >= 0 && dev < MAX_DEV) allowed[dev].store(true, std::memory_order_release);
     }
-    CUtensorMap mw, mx;
-    st = encode(&mw, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, rep, MX_TILE, tiles128 * MX_TILE, MX_TILE / 2, MX_TILE);
-    if (st != GQ_OK) return st;
-    st = encode(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x.codes, p.K, x.rows, p.K, p.rows ? 1 : C::BOX);
+    CUtensorMap mx;
+    st = encode(&mx, x.codes, x.rows, p.K, C::BOX);
     if (st != GQ_OK) return st;
 
     // K shared out where the tiles leave SMs idle, two stages a CTA at least
@@ -600,7 +756,7 @@ gq_status launch(MxParams p, const void *rep, const gq_mx_rows &x, int64_t tiles
     cfg.numAttrs = split > 1 ? 2 : 1;
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(most_tiles, sms / split));
     cfg.gridDim = dim3((unsigned)(clusters * split));
-    return check_cuda(cudaLaunchKernelEx(&cfg, kernel, mw, mx, p), "mx product launch");
+    return check_cuda(cudaLaunchKernelEx(&cfg, kernel, mx, p), "mx product launch");
 }
 
 }  // namespace
@@ -619,21 +775,21 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     p.G = (int)((N + MX_TILE - 1) / MX_TILE), p.KT = (int)((K + MX_TILE - 1) / MX_TILE);
     p.S = (int)gq_mx_scale_cols(K), p.So = gated ? (int)gq_mx_scale_cols(N) : 0;
     p.dst = dst, p.codes = static_cast<uint8_t *>(codes), p.scales = scales, p.x_scales = x.scales;
-    const int64_t count = (int64_t)p.E * (gated ? 2 : 1), tiles128 = count * p.G * p.KT;
-    p.w_scales = static_cast<const uint8_t *>(rep) + tiles128 * MX_TILE_CODES;
+    p.w = static_cast<const uint8_t *>(rep);
+    p.x_codes = static_cast<const uint8_t *>(x.codes);
 
     // Rows per tile by the rows that an expert has on average (of the experts that can have any).
     const int64_t some = std::min<int64_t>(p.E, p.R), mean = (p.R + some - 1) / some;
     auto most = [&](int bn) { return ((plan ? some : 0) + (p.R + bn - 1) / bn) * p.G; };
     if (most(16) >= (1LL << 31)) return fail(GQ_ERR_INVALID_ARG, "R=%lld rows of N=%lld are too many", (long long)p.R, (long long)N);
     if (gated) {
-        if (mean <= 16) return launch<16, true>(p, rep, x, tiles128, most(16), s);
-        if (mean <= 64) return launch<64, true>(p, rep, x, tiles128, most(64), s);
-        return launch<112, true>(p, rep, x, tiles128, most(112), s);
+        if (mean <= 16) return launch<16, true>(p, x, most(16), s);
+        if (mean <= 64) return launch<64, true>(p, x, most(64), s);
+        return launch<112, true>(p, x, most(112), s);
     }
-    if (mean <= 16) return launch<16, false>(p, rep, x, tiles128, most(16), s);
-    if (mean <= 64) return launch<64, false>(p, rep, x, tiles128, most(64), s);
-    return launch<192, false>(p, rep, x, tiles128, most(192), s);
+    if (mean <= 16) return launch<16, false>(p, x, most(16), s);
+    if (mean <= 64) return launch<64, false>(p, x, most(64), s);
+    return launch<192, false>(p, x, most(192), s);
 }
 
 }  // namespace gq

@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(256) repack_mxfp4_kernel(const uint8_t *__rest
                 v = *reinterpret_cast<const uint4 *>(codes + (row * K + k) / 2);
                 b = scales[row * S + k / 32];
             }
-            *reinterpret_cast<uint4 *>(out + tile * MX_TILE_CODES + r * 64 + j * 16) = v;
-            out[tiles * MX_TILE_CODES + tile * MX_TILE_SCALES + (r & 31) * 16 + (r >> 5) * 4 + j] = b;
+            *reinterpret_cast<uint4 *>(out + tile * MX_TILE_BYTES + r * 64 + j * 16) = v;
+            out[tile * MX_TILE_BYTES + MX_TILE_CODES + (r & 31) * 16 + (r >> 5) * 4 + j] = b;
         }
     }
 }
