@@ -3,24 +3,21 @@
 //
 // dst^T = W . X^T: a tile is 128 weight rows (the MMA's M, tensor-memory lanes) by up to BN rows of
 // activations (its N, tensor-memory columns; an MMA is as wide as its tile's rows need, in steps of
-// 16).  kind::mxf8f6f4 multiplies the codes as they are and each block of 32 by its two powers of
-// two, so nothing is converted on the way:
-//   warp 0     one thread copies: the weights' tile (packed codes, scales) by a bulk copy, the activations'
-//              codes by a tensor copy;
-//   warps 12 .. 15  spread the weights' codes, each warp every fourth stage (a stage is mostly waiting: for the
-//              copies, for the loads, for the fence, so four of them overlap).  This kind reads 16 4-bit
-//              codes from the first 8 of 16 bytes.  The packed tile arrives in the second half of the 16 KB that it
-//              will take; its first half moves to the free first half, then the second over the place.
-//              (A tensor copy that spreads codes on the way moves 8 bytes a cycle, a quarter of what device
-//              memory gives.)  They also bring the activations' scale bytes into the order that tensor memory
-//              wants, and, where a plan names the rows, their codes, by asynchronous 16-byte copies;
-//   warp 1     one thread issues: per stage of 128 columns, copies of the scales into tensor memory and 4
-//              MMAs (8 for the gated unit, whose gate and up tiles share the activations).  The thread
-//              is elected, not picked by its lane: the compiler then keeps the descriptors in uniform registers,
-//              which halves the cost of an instruction (measured: 80 to 39 cycles per MMA of 16 columns);
+// 16).  kind::mxf8f6f4 multiplies the codes and each block of 32 by its two powers of two.  What bounds a
+// full tile is shared memory's 128 bytes a cycle, so the weights go through it once, packed, and reach the
+// MMAs in tensor memory:
+//   warp 0     one thread copies, some stages of 128 columns ahead: the weights' tile (packed codes, scales) by a
+//              bulk copy, the activations' codes by a tensor copy;
+//   warps 2, 3     instead of the latter, where a plan names the rows: 16-byte asynchronous copies;
+//   warps 12 .. 15  a weight row per thread: 64 bytes of packed codes become 128 e4m3 codes by moving bits (sign,
+//              exponent and fraction to their places give 2^-6 of the value; the tiles' scale bytes are stored
+//              6 higher) and go to tensor memory, and so do the scales of both operands;
+//   warp 1     one thread issues 4 MMAs a stage (8 for the gated unit, whose gate and up tiles share the
+//              activations).  The thread is elected, not picked by its lane: the compiler then keeps the
+//              descriptors in uniform registers (measured: 39 cycles per MMA of 16 columns, not 80);
 //   warps 4 .. 11  take the sums over: the tensor cores' accumulators cut off what does not fit 24 bits, so
-//              every 4 stages (512 columns) they are added, rounded, to f32 registers, while the
-//              next stages go to another set of accumulators; then they store the tile.
+//              every few stages they are added, rounded, to f32 registers, while the next stages go
+//              to another set of accumulators; then they store the tile.
 // CTAs take tiles in turn (persistent), those of one expert's weight rows next to each other.  With few
 // tiles a cluster of 2 or 4 CTAs shares a tile's columns; the first adds the others' sums in order.
 #include <cuda.h>
@@ -38,62 +35,65 @@ namespace {
 
 constexpr int THREADS = 512;
 constexpr int EPI_WARPS = 8;
-constexpr int SPREAD_WARPS = 4;              // each takes every fourth stage
-constexpr int FLUSH = 4;                     // stages per take-over of the accumulators
-constexpr int A_BYTES = MX_TILE * MX_TILE;   // a weight tile in shared memory: one byte's room per code
-constexpr int A_SLOT = A_BYTES + 1024;       // and its scales, 1024-aligned
+constexpr int SPREAD_WARPS = 4;              // 32 weight rows each
+constexpr int GATHER_WARPS = 2;
 constexpr int MAX_E = 1024;
-constexpr int MAX_STAGES = 8, MAX_SETS = 4;
+constexpr int MAX_STAGES = 16, MAX_SLOTS = 8, MAX_SETS = 4;
 constexpr int FEW_REGS = 88, MANY_REGS = 168;   // per thread, of 128 at launch: 2 x 88 + 2 x 168 = 4 x 128
 
 // BN: rows of activations per tile.  GATED: two weight tiles (gate, up) per stage.
 template <int BN, bool GATED>
 struct Cfg {
     static constexpr int NA = GATED ? 2 : 1;
-    static constexpr int NB = (BN + 127) / 128;             // 512-byte pieces of activation scales
-    static constexpr int ST = GATED ? 4 : BN <= 64 ? 8 : 5;
     static constexpr bool BIG = BN > 64;                    // more sums per thread than an even share of registers holds
-    static constexpr int NR = (BN + 31) / 32;               // activation rows of a lane
+    static constexpr int ST = BN <= 16 ? (GATED ? 8 : 16) : BN <= 64 ? (GATED ? 7 : 10) : 6;   // stages in shared memory
     static constexpr int PARTS = BN > 64 ? 2 : 1;           // tensor copies of a tile's activations, BN / PARTS rows each
     static constexpr int BOX = BN / PARTS;
     static constexpr int CW = BN <= 16 ? 8 : 16;            // columns per read of tensor memory
     static constexpr int CHUNKS = BN / CW;
     static constexpr int MINE = (CHUNKS + 1) / 2;           // chunks of a warpgroup
     static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;
-    // tensor memory: sets of accumulators, then the scales of every stage
+    // Tensor memory: sets of accumulators, then slots of a stage's weights and scales.  The gated unit's large
+    // tile has one set only; its accumulators are taken over every 16 stages (2048 columns; what is cut
+    // off meanwhile, 2^-24 of the sums 64 times at most, is far below its output's 2^-4), gate before up, so
+    // that the next gate MMAs wait for half of it.
     static constexpr int ACC = NA * BN;
-    static constexpr int SF_STAGE = 4 * (NA + NB);
-    static constexpr int SETS = 4 * ACC + ST * SF_STAGE <= 512 ? 4 : 2;
-    static constexpr int SF = SETS * ACC;
-    static constexpr int COLS_USED = SF + ST * SF_STAGE;
-    static constexpr int COLS = COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
+    static constexpr int SETS = GATED ? (BN <= 16 ? 4 : BN <= 64 ? 2 : 1) : (BN <= 64 ? 4 : 2);
+    static constexpr int FLUSH = SETS == 1 ? 16 : 4;        // stages per take-over of the accumulators
+    static constexpr int NR = (BN + 31) / 32;               // scales of activation rows: columns, words of a lane
+    static constexpr int SFB = NR <= 1 ? 4 : NR <= 4 ? 4 : 8;
+    static constexpr int SLOT = NA * 36 + SFB;              // 32 columns of codes and 4 of scales per weight tile
+    static constexpr int NS = BN <= 16 ? (GATED ? 4 : 8) : BN <= 64 ? (GATED ? 3 : 6) : 3;
+    static constexpr int SLOTS = SETS * ACC;                // their first column
+    static constexpr int COLS_USED = SLOTS + NS * SLOT;
+    static constexpr int COLS = COLS_USED <= 256 ? 256 : 512;
     static_assert(COLS_USED <= 512, "tensor memory");
     static_assert(BOX % 8 == 0 && BN % 16 == 0, "tile rows");
+    static_assert(NS < ST && NS <= MAX_SLOTS && ST <= MAX_STAGES && SETS <= MAX_SETS, "barriers");
     // shared memory from a 1024-aligned base
     static constexpr int B_STAGE = BN * 128;
-    static constexpr int a = 0;
-    static constexpr int b = a + ST * NA * A_SLOT;
-    static constexpr int sfb = b + ST * B_STAGE;
-    static constexpr int part = sfb + ST * NB * 512;
+    static constexpr int b = 0;
+    static constexpr int w = b + ST * B_STAGE;
+    static constexpr int part = w + ST * NA * MX_TILE_BYTES;
     static constexpr int PART_BYTES = NA * BN * MX_TILE * 4;
     static constexpr int starts = part + (MAX_SPLIT - 1) * PART_BYTES;
     static constexpr int bars = starts + 3 * (MAX_E + 4) * 4;
-    static constexpr int total = bars + 320;
+    static constexpr int total = bars + 640;
     static_assert(total + 1024 <= 227 * 1024, "shared memory");
-    static_assert(ST <= MAX_STAGES, "barriers");
 };
 
 enum : int {
     RAW = 0,                     // a stage's copies have landed
-    FULL = RAW + MAX_STAGES,     // its weights are spread, its activations' scales written
-    EMPTY = FULL + MAX_STAGES,   // its MMAs are done
-    ACC_FULL = EMPTY + MAX_STAGES,
-    ACC_EMPTY = ACC_FULL + MAX_SETS,
-    PART_FULL = ACC_EMPTY + MAX_SETS,
+    GATHERED = RAW + MAX_STAGES, // and so have its gathered rows
+    EMPTY = GATHERED + MAX_STAGES,   // its MMAs are done
+    FULL = EMPTY + MAX_STAGES,   // a slot's weights and scales are in tensor memory
+    ACC_FULL = FULL + MAX_SLOTS,
+    ACC_EMPTY = ACC_FULL + MAX_SETS,         // gate and up apart
+    PART_FULL = ACC_EMPTY + 2 * MAX_SETS,
     PART_EMPTY,
     NUM_BARS
 };
-static_assert(NUM_BARS * 8 + 8 <= 320, "barrier area");
+static_assert(NUM_BARS * 8 + 8 <= 640, "barrier area");
 
 struct MxParams {
     const uint8_t *w;              // tiles
@@ -116,25 +116,40 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)2 << 61;
 }
-// 32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
-// kind::mxf8f6f4: A e2m1 (5), B e4m3 (0), both K-major, scales ue8m0, f32 sums; the scale bytes'
+// kind::mxf8f6f4: A and B e4m3 (0), both K-major, scales ue8m0, f32 sums; the scale bytes'
 // places (0 .. 3) go to bits 4 and 29
 __device__ __forceinline__ uint32_t mx_idesc(int n) {
-    return 5u << 7 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24;
+    return (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24;
 }
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+// A, D and the scales in tensor memory
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], [%1], %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// one 32-bit column per value, this warp's 32 lanes
+template <int W>
+__device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[W]) {
+    if constexpr (W == 1)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
+    else if constexpr (W == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+    else if constexpr (W == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+}
+// Eight codes as the tiles hold them (byte i: code i below, code i + 4 above) -> e4m3 of 2^-6 of their values:
+// sign to bit 7, exponent and fraction to bits 2 .. 4 (0.5, e2m1's subnormal, becomes one too).
+__device__ __forceinline__ void spread8(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    lo = ((w << 4) & 0x80808080u) | ((w << 2) & 0x1C1C1C1Cu);
+    hi = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -272,13 +287,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::ST; i++) {
             mbar_init(bar(RAW + i), 1);
-            mbar_init(bar(FULL + i), 1);
+            mbar_init(bar(GATHERED + i), GATHER_WARPS);
             mbar_init(bar(EMPTY + i), 1);
         }
-        for (int i = 0; i < C::SETS; i++) {
-            mbar_init(bar(ACC_FULL + i), 1);
-            mbar_init(bar(ACC_EMPTY + i), EPI_WARPS);
-        }
+        for (int i = 0; i < C::NS; i++) mbar_init(bar(FULL + i), SPREAD_WARPS);
+        for (int i = 0; i < C::SETS; i++) mbar_init(bar(ACC_FULL + i), 1);
+        for (int i = 0; i < C::SETS * C::NA; i++) mbar_init(bar(ACC_EMPTY + i), EPI_WARPS);
         mbar_init(bar(PART_FULL), (split - 1) * EPI_WARPS + (split == 1));
         mbar_init(bar(PART_EMPTY), EPI_WARPS);
     }
@@ -350,8 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     mbar_arrive_expect_tx(raw, bytes);
 #pragma unroll
                     for (int a = 0; a < C::NA; a++)
-                        bulk_g2s(smem_addr(smem + C::a) + (uint32_t)((ring.st * C::NA + a) * A_SLOT + A_BYTES - MX_TILE_CODES), w + a * up,
-                                 MX_TILE_BYTES, raw);
+                        bulk_g2s(smem_addr(smem + C::w) + (uint32_t)((ring.st * C::NA + a) * MX_TILE_BYTES), w + a * up, MX_TILE_BYTES, raw);
 #pragma unroll
                     for (int u = 0; u < C::PARTS; u++)
                         if (u < parts)
@@ -365,70 +378,113 @@ __global__ void __launch_bounds__(THREADS, 1)
         set_registers<C::BIG, false>();
         if (elect()) {
             Ring<C::ST> ring;
+            Ring<C::NS> slot;
             Ring<C::SETS> set;
             int chunks = 0;
             for (int i = cluster; i < tiles && !failed; i += clusters) {
                 const Tile t = tile_at<BN>(p, where, i);
-                const int n = (t.n + 15) & ~15;
-                const uint32_t idesc = mx_idesc(n);
-                for (int k = 0; k < nk; k++, ring.next()) {
-                    const int in_chunk = k % FLUSH;
-                    if (in_chunk == 0) {
-                        if (chunks == C::SETS) {
-                            if (!mbar_wait(bar(ACC_EMPTY + set.st), set.turn ^ 1, p.status)) failed = true;
-                        } else {
-                            chunks++;
-                        }
-                    }
+                const uint32_t idesc = mx_idesc((t.n + 15) & ~15);
+                for (int k = 0; k < nk; k++, ring.next(), slot.next()) {
+                    const int in_chunk = k % C::FLUSH;
                     // (whoever arrived there had waited for the stage's copies)
-                    if (failed || !mbar_wait(bar(FULL + ring.st), ring.turn, p.status)) {
-                        failed = true;
-                        break;
-                    }
-                    fence_after();
-                    const uint32_t acc = tmem + (uint32_t)(set.st * C::ACC), sf = tmem + (uint32_t)(C::SF + ring.st * C::SF_STAGE);
-                    const uint32_t as = smem_addr(smem + C::a) + (uint32_t)(ring.st * C::NA * A_SLOT);
-#pragma unroll
-                    for (int a = 0; a < C::NA; a++) copy_scales(sf + 4 * a, scales_desc(as + a * A_SLOT + A_BYTES));
-#pragma unroll
-                    for (int u = 0; u < C::NB; u++)
-                        if (u == 0 || u * 128 < n)
-                            copy_scales(sf + 4 * (C::NA + u), scales_desc(smem_addr(smem + C::sfb) + (uint32_t)((ring.st * C::NB + u) * 512)));
+                    if (!mbar_wait(bar(FULL + slot.st), slot.turn, p.status)) failed = true;
+                    if (p.rows && !failed && !mbar_wait(bar(GATHERED + ring.st), ring.turn, p.status)) failed = true;
+                    const uint32_t acc = tmem + (uint32_t)(set.st * C::ACC), sl = tmem + (uint32_t)(C::SLOTS + slot.st * C::SLOT);
                     const uint64_t bd = operand_desc(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE));
 #pragma unroll
                     for (int a = 0; a < C::NA; a++) {
-                        const uint64_t ad = operand_desc(as + a * A_SLOT);
+                        if (in_chunk == 0 && chunks == C::SETS && !failed &&
+                            !mbar_wait(bar(ACC_EMPTY + set.st * C::NA + a), set.turn ^ 1, p.status))
+                            failed = true;
+                        if (failed) break;
+                        fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < 4; kk++)     // 32 columns: 32 bytes further in both operands, the next scale byte
-                            mma_mx(acc + a * BN, ad + (uint64_t)(kk * 2), bd + (uint64_t)(kk * 2), idesc + (uint32_t)kk * ((1u << 4) | (1u << 29)),
-                                   sf + 4 * a, sf + 4 * C::NA, in_chunk > 0 || kk > 0);
+                        for (int kk = 0; kk < 4; kk++)     // 32 columns: 8 of tensor memory, 32 bytes of the activations, the next scale byte
+                            mma_mx(acc + a * BN, sl + (uint32_t)(a * 32 + kk * 8), bd + (uint64_t)(kk * 2),
+                                   idesc + (uint32_t)kk * ((1u << 4) | (1u << 29)), sl + (uint32_t)(C::NA * 32 + a * 4),
+                                   sl + (uint32_t)(C::NA * 36), in_chunk > 0 || kk > 0);
                     }
+                    if (failed) break;
                     commit(bar(EMPTY + ring.st));
-                    if (in_chunk == FLUSH - 1 || k == nk - 1) {
+                    if (in_chunk == C::FLUSH - 1 || k == nk - 1) {
                         commit(bar(ACC_FULL + set.st));
                         set.next();
+                        if (chunks < C::SETS) chunks++;
                     }
                 }
             }
         }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------------ spreading, the activations' scales
+    } else if (warp < 4) {
+        // ------------------------------------------------------------------ gathered rows
         set_registers<C::BIG, false>();
-        // This warp's next stage: step k of tile i, step `at` of the launch.  The scale bytes of its rows (row 32 j +
-        // lane of the tile; -1: none) are loaded one of its stages ahead.
-        int i = cluster, k = warp - 12, from[C::NR];
+        if (p.rows) {
+            // Thread x copies 16 bytes, piece x % 8, of the tile's rows x / 8, x / 8 + 8, ..; two stages are under
+            // way before the first is waited for.
+            constexpr int ROWS = BN / 8, AHEAD = 2;
+            const int x = (warp - 2) * 32 + lane;
+            int from[ROWS], filled = 0;
+            Ring<C::ST> ring, done;
+            int under_way = 0;
+            auto finish = [&] {
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(GATHERED + done.st));
+                done.next();
+                under_way--;
+            };
+            for (int i = cluster; i < tiles && !failed; i += clusters) {
+                const Tile t = tile_at<BN>(p, where, i);
+#pragma unroll
+                for (int j = 0; j < ROWS; j++) {
+                    const int c = j * 8 + (x >> 3);
+                    const int r = c < t.n ? __ldg(p.rows + t.r0 + c) : -1;
+                    from[j] = r >= 0 && r < p.x_rows ? r : -1;
+                }
+                for (int k = 0; k < nk; k++, ring.next()) {
+                    if (filled == C::ST) {
+                        if (!mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
+                        failed = __any_sync(0xffffffffu, failed);
+                        if (failed) break;
+                    } else {
+                        filled++;
+                    }
+                    const int col = (kt0 + k) * MX_TILE + (x & 7) * 16;
+                    const uint32_t to = smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE + (x >> 3) * 128 + (((x & 7) ^ (x >> 3)) << 4));
+#pragma unroll
+                    for (int j = 0; j < ROWS; j++)
+                        if (j * 8 < t.n) {
+                            const bool there = from[j] >= 0 && col < p.K;
+                            copy16(to + j * 1024, p.x_codes + (there ? (int64_t)from[j] * p.K + col : 0), there);
+                        }
+                    copy_group();
+                    if (++under_way > AHEAD) {
+                        copy_wait<AHEAD>();
+                        finish();
+                    }
+                }
+            }
+            if (!failed) {
+                copy_wait<0>();
+                while (under_way > 0) finish();
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------------ weights and scales into tensor memory
+        set_registers<C::BIG, false>();
+        const int q = warp - 12;                           // tensor-memory lanes, weight rows 32 q ..
+        // The scales of activation row 32 j + lane of the tile (-1: none), loaded a stage ahead.  Every warp brings
+        // all of them: each quarter of the lanes holds a copy.
+        int from[C::NR];
         uint32_t next[C::NR];
-        Ring<C::ST> ring;
-        for (int j = 0; j < k; j++) ring.next();
-        Tile t{};
-        auto rows_of = [&] {
-            t = tile_at<BN>(p, where, i);
+        constexpr int WB = C::NR == 3 ? 4 : C::NR > 4 ? 8 : C::NR;
+        auto rows_of = [&](int i) {
+            const Tile t = tile_at<BN>(p, where, i);
 #pragma unroll
             for (int j = 0; j < C::NR; j++) {
                 const int c = j * 32 + lane;
                 from[j] = -1;
                 if (c < t.n) {
-                    from[j] = p.rows ? p.rows[t.r0 + c] : t.r0 + c;
+                    from[j] = p.rows ? __ldg(p.rows + t.r0 + c) : t.r0 + c;
                     if (from[j] < 0 || from[j] >= p.x_rows) {
                         atomicOr(p.status, STATUS_RANGE);
                         from[j] = -1;
@@ -436,97 +492,72 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         };
-        auto load = [&] {
-            // bytes past the row's end belong to columns of zeros, but must not be NaN
-            const int left = p.K / QK - (kt0 + k) * 4;
-            const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+        auto load = [&](int kt) {
 #pragma unroll
             for (int j = 0; j < C::NR; j++)
-                next[j] = from[j] < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (int64_t)from[j] * p.S) + kt0 + k) & mask;
+                next[j] = from[j] < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (int64_t)from[j] * p.S) + kt);
         };
-        // to the stage `by` steps further, if there is one
-        auto advance = [&] {
-            bool other = false;
-            while (k >= nk && i < tiles) {
-                k -= nk;
-                i += clusters;
-                other = true;
-            }
-            if (i >= tiles) return false;
-            if (other) rows_of();
-            load();
-            return true;
-        };
-        bool more = cluster < tiles;
-        if (more) {
-            rows_of();
-            more = advance();
-            if (more) load();
+        if (cluster < tiles) {
+            rows_of(cluster);
+            load(kt0);
         }
-        // the places of 32 codes: row 8 j + lane / 4, columns 32 (lane % 4) ..
-        const int r8 = lane >> 2, c0 = 2 * (lane & 3);
-        const uint32_t to0 = (uint32_t)(r8 * 128 + ((c0 ^ r8) << 4)), to1 = (uint32_t)(r8 * 128 + (((c0 + 1) ^ r8) << 4));
-        bool first = true;                                  // turn of the ring: no stage is in use yet
-        while (more && !failed) {
-            uint32_t now[C::NR];
+        Ring<C::ST> ring, freed;                           // this stage; the one whose MMAs read the slot last
+        Ring<C::NS> slot;
+        int filled = 0;
+        for (int i = cluster; i < tiles && !failed; i += clusters) {
+            for (int k = 0; k < nk; k++, ring.next(), slot.next()) {
+                const int kt = kt0 + k;
+                uint32_t sfb[WB];
+                // bytes past the row's end belong to columns of zeros, but must not be NaN
+                const int left = p.K / QK - kt * 4;
+                const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
 #pragma unroll
-            for (int j = 0; j < C::NR; j++) now[j] = next[j];
-            uint8_t *const slot = smem + C::a + ring.st * C::NA * A_SLOT;
-            // The stage's last MMAs are done: its place is free for gathered rows, and its copies' barrier, which
-            // another warp may have waited on the turn before, is at this turn (a parity tells two turns apart,
-            // not three).
-            if (!first && !mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
-            failed = __any_sync(0xffffffffu, failed);
-            if (failed) break;
-            if (p.rows) {
-                // 16 bytes, piece lane % 8, of the tile's rows lane / 8, lane / 8 + 4, ..
-                const int col = (kt0 + k) * MX_TILE + (lane & 7) * 16;
-                const uint32_t b = smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE);
-#pragma unroll 4
-                for (int c = lane >> 3; c < t.n; c += 4) {
-                    const int r = __ldg(p.rows + t.r0 + c);
-                    const bool there = r >= 0 && r < p.x_rows && col < p.K;
-                    copy16(b + (uint32_t)(c * 128 + (((lane & 7) ^ (c & 7)) << 4)), p.x_codes + (there ? (int64_t)r * p.K + col : 0), there);
+                for (int j = 0; j < WB; j++) sfb[j] = j < C::NR ? next[j < C::NR ? j : 0] & mask : 0u;
+                if (k + 1 < nk) {
+                    load(kt + 1);
+                } else if (i + clusters < tiles) {
+                    rows_of(i + clusters);
+                    load(kt0);
                 }
-                copy_group();
-            }
-            const int st = ring.st;
-            const uint32_t turn = ring.turn;
-            k += SPREAD_WARPS;
+                if (!mbar_wait(bar(RAW + ring.st), ring.turn, p.status)) failed = true;
+                const uint8_t *raw = smem + C::w + ring.st * C::NA * MX_TILE_BYTES;
+                uint4 v[C::NA][4], sfa[C::NA];
 #pragma unroll
-            for (int j = 0; j < SPREAD_WARPS; j++) {
-                ring.next();
-                if (ring.st == 0) first = false;
-            }
-            more = advance();
-            if (!mbar_wait(bar(RAW + st), turn, p.status)) failed = true;
-            failed = __any_sync(0xffffffffu, failed);
-            if (failed) break;
+                for (int a = 0; a < C::NA; a++) {
 #pragma unroll
-            for (int a = 0; a < C::NA; a++)
+                    for (int j = 0; j < 4; j++) v[a][j] = lds128(raw + a * MX_TILE_BYTES + j * 2048 + (q * 32 + lane) * 16);
+                    sfa[a] = lds128(raw + a * MX_TILE_BYTES + MX_TILE_CODES + lane * 16);
+                }
+                if (filled == C::NS) {
+                    if (!failed && !mbar_wait(bar(EMPTY + freed.st), freed.turn, p.status)) failed = true;
+                    freed.next();
+                } else {
+                    filled++;
+                }
+                failed = __any_sync(0xffffffffu, failed);
+                if (failed) break;
+                fence_after();
+                const uint32_t sl = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(C::SLOTS + slot.st * C::SLOT);
 #pragma unroll
-                for (int h = 0; h < 2; h++) {               // 64 rows at a time
-                    uint8_t *tile = slot + a * A_SLOT;
-                    uint4 v[8];
+                for (int a = 0; a < C::NA; a++) {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) v[j] = lds128(tile + (A_BYTES - MX_TILE_CODES) + h * 4096 + j * 512 + lane * 16);
-                    __syncwarp();                           // all of what the second half's place holds is read
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        *reinterpret_cast<uint2 *>(tile + to0 + (h * 8 + j) * 1024) = make_uint2(v[j].x, v[j].y);
-                        *reinterpret_cast<uint2 *>(tile + to1 + (h * 8 + j) * 1024) = make_uint2(v[j].z, v[j].w);
+                    for (int j = 0; j < 4; j++) {
+                        uint32_t c[8];
+                        spread8(v[a][j].x, c[0], c[1]);
+                        spread8(v[a][j].y, c[2], c[3]);
+                        spread8(v[a][j].z, c[4], c[5]);
+                        spread8(v[a][j].w, c[6], c[7]);
+                        write_tmem<8>(sl + (uint32_t)(a * 32 + j * 8), c);
                     }
+                    const uint32_t s4[4] = {sfa[a].x, sfa[a].y, sfa[a].z, sfa[a].w};
+                    write_tmem<4>(sl + (uint32_t)(C::NA * 32 + a * 4), s4);
                 }
-#pragma unroll
-            for (int u = 0; u < C::NB; u++) {
-                auto word = [&](int j) { return j < C::NR ? now[j < C::NR ? j : 0] : 0u; };
-                *reinterpret_cast<uint4 *>(smem + C::sfb + (st * C::NB + u) * 512 + lane * 16) =
-                    make_uint4(word(4 * u), word(4 * u + 1), word(4 * u + 2), word(4 * u + 3));
+                write_tmem<WB>(sl + (uint32_t)(C::NA * 36), sfb);
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(FULL + slot.st));
             }
-            if (p.rows) copy_wait<0>();
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(FULL + st));
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------------ sums, output
@@ -544,34 +575,32 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int j = 0; j < C::MINE; j++)
 #pragma unroll
                     for (int c = 0; c < C::CW; c++) acc[a][j][c] = 0.0f;
-            for (int k = 0; k < nk; k += FLUSH, set.next()) {
+            for (int k = 0; k < nk; k += C::FLUSH, set.next()) {
                 if (!mbar_wait(bar(ACC_FULL + set.st), set.turn, p.status)) failed = true;
                 failed = __any_sync(0xffffffffu, failed);
                 if (failed) break;
                 fence_after();
-                const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(set.st * C::ACC + half * C::CW);
-                // two reads of tensor memory under way at a time
 #pragma unroll
-                for (int j = 0; j < C::MINE; j += 2 / C::NA) {
-                    constexpr int W = C::CW, X = 2 / C::NA;
-                    uint32_t v[X][C::NA][W];
+                for (int a = 0; a < C::NA; a++) {
+                    const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(set.st * C::ACC + a * BN + half * C::CW);
+                    // two reads of tensor memory under way at a time
 #pragma unroll
-                    for (int x = 0; x < X; x++)
+                    for (int j = 0; j < C::MINE; j += 2) {
+                        uint32_t v[2][C::CW];
 #pragma unroll
-                        for (int a = 0; a < C::NA; a++)
-                            if (j + x < C::MINE && 2 * (j + x) + half < cols) read_acc<W>(at + (uint32_t)(a * BN + 2 * (j + x) * W), v[x][a]);
-                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        for (int x = 0; x < 2; x++)
+                            if (j + x < C::MINE && 2 * (j + x) + half < cols) read_acc<C::CW>(at + (uint32_t)(2 * (j + x) * C::CW), v[x]);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int x = 0; x < X; x++)
-#pragma unroll
-                        for (int a = 0; a < C::NA; a++)
+                        for (int x = 0; x < 2; x++)
                             if (j + x < C::MINE && 2 * (j + x) + half < cols)
 #pragma unroll
-                                for (int c = 0; c < W; c++) acc[a][j + x < C::MINE ? j + x : 0][c] += keep(v[x][a][c]);
+                                for (int c = 0; c < C::CW; c++) acc[a][j + x < C::MINE ? j + x : 0][c] += keep(v[x][c]);
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(ACC_EMPTY + set.st * C::NA + a));
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(ACC_EMPTY + set.st));
             }
             if (failed) break;
             if (C::MAX_SPLIT > 1 && split > 1) {
@@ -785,11 +814,11 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     if (gated) {
         if (mean <= 16) return launch<16, true>(p, x, most(16), s);
         if (mean <= 64) return launch<64, true>(p, x, most(64), s);
-        return launch<112, true>(p, x, most(112), s);
+        return launch<128, true>(p, x, most(128), s);
     }
     if (mean <= 16) return launch<16, false>(p, x, most(16), s);
     if (mean <= 64) return launch<64, false>(p, x, most(64), s);
-    return launch<192, false>(p, x, most(192), s);
+    return launch<176, false>(p, x, most(176), s);
 }
 
 }  // namespace gq

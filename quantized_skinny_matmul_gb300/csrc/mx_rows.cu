@@ -80,27 +80,39 @@ __global__ void __launch_bounds__(Q_THREADS) dequantize_mx_kernel(const uint8_t 
 // ---------------------------------------------------------------------------
 // 4-bit weights into tiles
 // ---------------------------------------------------------------------------
-// One CTA per tile; a thread copies 16 bytes of codes (32 values, one scale) twice.
+// One CTA per tile; a thread takes 16 bytes of codes (32 values, one scale) twice.  Of each eight codes, the
+// first four go to the low nibbles of the tile's four bytes, the others to the high ones.
+__device__ __forceinline__ uint32_t by_fours(uint32_t w) {
+    uint32_t lo = w & 0xFFFFu, hi = w >> 16;      // codes 0 .. 3, 4 .. 7, one per nibble
+    lo = (lo | lo << 8) & 0x00FF00FFu;
+    lo = (lo | lo << 4) & 0x0F0F0F0Fu;
+    hi = (hi | hi << 8) & 0x00FF00FFu;
+    hi = (hi | hi << 4) & 0x0F0F0F0Fu;
+    return lo | hi << 4;
+}
 __global__ void __launch_bounds__(256) repack_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                            uint8_t *__restrict__ out, int64_t tiles, int64_t N, int64_t K,
                                                            int G, int KT, int S) {
+    pdl_wait();
+    pdl_launch_dependents();
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int t = (int)(tile % KT);
         const int64_t cg = tile / KT;
         const int g = (int)(cg % G);
         const int64_t c = cg / G;
+        uint8_t *to = out + tile * MX_TILE_BYTES;
         for (int i = threadIdx.x; i < MX_TILE * 4; i += 256) {
             const int r = i >> 2, j = i & 3;
             const int64_t n = (int64_t)g * MX_TILE + r, k = (int64_t)t * MX_TILE + 32 * j;
             uint4 v = make_uint4(0, 0, 0, 0);
-            uint8_t b = 0;
+            int b = 0;
             if (n < N && k < K) {
                 const int64_t row = c * N + n;
                 v = *reinterpret_cast<const uint4 *>(codes + (row * K + k) / 2);
-                b = scales[row * S + k / 32];
+                b = min(scales[row * S + k / 32] + 6, 255);
             }
-            *reinterpret_cast<uint4 *>(out + tile * MX_TILE_BYTES + r * 64 + j * 16) = v;
-            out[tile * MX_TILE_BYTES + MX_TILE_CODES + (r & 31) * 16 + (r >> 5) * 4 + j] = b;
+            *reinterpret_cast<uint4 *>(to + j * 2048 + r * 16) = make_uint4(by_fours(v.x), by_fours(v.y), by_fours(v.z), by_fours(v.w));
+            to[MX_TILE_CODES + (r & 31) * 16 + (r >> 5) * 4 + j] = (uint8_t)b;
         }
     }
 }
@@ -326,11 +338,12 @@ gq_status launch_dequantize_mx(const void *codes, const uint8_t *scales, bool e2
 
 gq_status launch_repack_mxfp4(const void *codes, const uint8_t *scales, void *rep, int64_t count, int64_t N, int64_t K,
                               cudaStream_t s) {
-    const int G = (int)((N + MX_TILE - 1) / MX_TILE), KT = (int)((K + MX_TILE - 1) / MX_TILE);
-    const int64_t tiles = count * G * KT;
-    repack_mxfp4_kernel<<<(unsigned)std::min<int64_t>(tiles, 1 << 20), 256, 0, s>>>(
-        static_cast<const uint8_t *>(codes), scales, static_cast<uint8_t *>(rep), tiles, N, K, G, KT, (int)gq_mx_scale_cols(K));
-    return check_cuda(cudaGetLastError(), "mxfp4 repack launch");
+    int G = (int)((N + MX_TILE - 1) / MX_TILE), KT = (int)((K + MX_TILE - 1) / MX_TILE);
+    int64_t tiles = count * G * KT;
+    int S = (int)gq_mx_scale_cols(K);
+    void *args[] = {&codes, &scales, &rep, &tiles, &N, &K, &G, &KT, &S};
+    return launch_pdl((const void *)repack_mxfp4_kernel, dim3((unsigned)std::min<int64_t>(tiles, 1 << 20)), dim3(256), 0, s, args,
+                      "mxfp4 repack launch");
 }
 
 gq_status launch_rms_norm_mx(const void *x, int64_t ldx, const void *res, int64_t ldr, bool bf16, const float *w,
