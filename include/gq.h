@@ -575,10 +575,10 @@ gq_status gq_rms_norm_mx(const void *x, int64_t ldx, const void *residual, int64
  * (codes [count * N][K / 2], scales [count * N][S]), copied once into tiles of 128 rows x 128
  * columns: tile (c, g, t) of matrix c, rows 128 g .. and columns 128 t .. is number
  * (c * ceil(N/128) + g) * ceil(K/128) + t, 8704 bytes: the codes of row r, columns 32 j .. 32 j + 31 in
- * the 16 bytes from j * 2048 + r * 16 on, of each eight of them codes 0 .. 3 in the low nibbles of four bytes
- * and 4 .. 7 in the high ones; then, from byte 8192, the scales, the four bytes of row r at (r % 32) * 16 + (r / 32)
- * * 4, each stored 6 higher (255 at most: scales from 2^122 on count as NaN).  Padding is 0.  The result must
- * not overlap the inputs. */
+ * the 16 bytes from j * 2048 + r * 16 on, of each eight of them codes 0 .. 3 in bits 2 .. 5 of the four bytes
+ * of a little-endian word and 4 .. 7 in its bits 6 .. 9, 14 .. 17, 22 .. 25 and 30, 31, 0, 1; then, from byte 8192, the
+ * scales, the four bytes of row r at (r % 32) * 16 + (r / 32) * 4.  Padding is 0.  The result must not overlap
+ * the inputs. */
 size_t gq_mxfp4_repacked_bytes(int64_t count, int64_t N, int64_t K);   /* 0 for sizes out of range */
 gq_status gq_repack_mxfp4(const void *codes, const uint8_t *scales, void *repacked, int64_t count, int64_t N,
                           int64_t K, cudaStream_t stream);

@@ -9,9 +9,9 @@
 //   warp 0     one thread copies, some stages of 128 columns ahead: the weights' tile (packed codes, scales) by a
 //              bulk copy, the activations' codes by a tensor copy;
 //   warps 2, 3     instead of the latter, where a plan names the rows: 16-byte asynchronous copies;
-//   warps 12 .. 15  a weight row per thread: 64 bytes of packed codes become 128 e4m3 codes by moving bits (sign,
-//              exponent and fraction to their places give 2^-6 of the value; the tiles' scale bytes are stored
-//              6 higher) and go to tensor memory, and so do the scales of both operands;
+//   warps 12 .. 15  a weight row per thread: 64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of
+//              each (the form of 4-bit operands in tensor memory), and go there, and so do the scales of both
+//              operands.  The tiles hold the codes so that three instructions place eight of them;
 //   warp 1     one thread issues 4 MMAs a stage (8 for the gated unit, whose gate and up tiles share the
 //              activations).  The thread is elected, not picked by its lane: the compiler then keeps the
 //              descriptors in uniform registers (measured: 39 cycles per MMA of 16 columns, not 80);
@@ -116,18 +116,18 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)2 << 61;
 }
-// kind::mxf8f6f4: A and B e4m3 (0), both K-major, scales ue8m0, f32 sums; the scale bytes'
+// kind::mxf8f6f4: A e2m1 (5), B e4m3 (0), both K-major, scales ue8m0, f32 sums; the scale bytes'
 // places (0 .. 3) go to bits 4 and 29
 __device__ __forceinline__ uint32_t mx_idesc(int n) {
-    return (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24;
+    return 5u << 7 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(MX_TILE >> 4) << 24;
 }
-// A, D and the scales in tensor memory
-__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+// A, D and the scales in tensor memory; the descriptor of B in two halves (the low one holds the address)
+__device__ __forceinline__ void mma_mx(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], [%1], %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %7, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], [%1], b, %4, [%5], [%6], p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 // one 32-bit column per value, this warp's 32 lanes
@@ -145,11 +145,11 @@ __device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[W
                      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                      : "memory");
 }
-// Eight codes as the tiles hold them (byte i: code i below, code i + 4 above) -> e4m3 of 2^-6 of their values:
-// sign to bit 7, exponent and fraction to bits 2 .. 4 (0.5, e2m1's subnormal, becomes one too).
+// Eight codes as the tiles hold them (0 .. 3 in bits 2 .. 5 of the bytes, 4 .. 7 in bits 6 .. 9 from each byte on, the
+// last around the word's end), each into bits 2 .. 5 of a byte.
 __device__ __forceinline__ void spread8(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    lo = ((w << 4) & 0x80808080u) | ((w << 2) & 0x1C1C1C1Cu);
-    hi = (w & 0x80808080u) | ((w >> 2) & 0x1C1C1C1Cu);
+    lo = w & 0x3C3C3C3Cu;
+    hi = __funnelshift_r(w, w, 4) & 0x3C3C3C3Cu;
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -177,6 +177,11 @@ __device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_gro
 template <int LEFT>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
 }
 // A place in the ring of stages and the parity of its turn.
 template <int ST>
@@ -335,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     if (split > 1) cluster_sync();            // every CTA's barriers are there before others arrive on them
     fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int tiles = where.starts[p.E] * p.G;
     const int kt0 = (int)((int64_t)p.KT * rank / split), nk = (int)((int64_t)p.KT * (rank + 1) / split) - kt0;
     bool failed = false;
@@ -380,17 +385,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             Ring<C::ST> ring;
             Ring<C::NS> slot;
             Ring<C::SETS> set;
+            const uint32_t full = bar(FULL), empty = bar(EMPTY), slots = tmem + (uint32_t)C::SLOTS;
+            const uint64_t bdesc = operand_desc(smem_addr(smem + C::b));
+            const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
             int chunks = 0;
             for (int i = cluster; i < tiles && !failed; i += clusters) {
                 const Tile t = tile_at<BN>(p, where, i);
-                const uint32_t idesc = mx_idesc((t.n + 15) & ~15);
-                for (int k = 0; k < nk; k++, ring.next(), slot.next()) {
-                    const int in_chunk = k % C::FLUSH;
+                uint32_t idesc[4];                         // of the scale bytes' four places
+#pragma unroll
+                for (int kk = 0; kk < 4; kk++) idesc[kk] = mx_idesc((t.n + 15) & ~15) + (uint32_t)kk * ((1u << 4) | (1u << 29));
+                int in_chunk = 0;
+                for (int k = 0; k < nk; k++) {
                     // (whoever arrived there had waited for the stage's copies)
-                    if (!mbar_wait(bar(FULL + slot.st), slot.turn, p.status)) failed = true;
+                    if (!mbar_wait(full + slot.st * 8, slot.turn, p.status)) failed = true;
                     if (p.rows && !failed && !mbar_wait(bar(GATHERED + ring.st), ring.turn, p.status)) failed = true;
-                    const uint32_t acc = tmem + (uint32_t)(set.st * C::ACC), sl = tmem + (uint32_t)(C::SLOTS + slot.st * C::SLOT);
-                    const uint64_t bd = operand_desc(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE));
+                    const uint32_t sl = slots + (uint32_t)(slot.st * C::SLOT), acc = tmem + (uint32_t)(set.st * C::ACC);
+                    const uint32_t bd = b_lo + (uint32_t)(ring.st * (C::B_STAGE >> 4));
 #pragma unroll
                     for (int a = 0; a < C::NA; a++) {
                         if (in_chunk == 0 && chunks == C::SETS && !failed &&
@@ -400,15 +410,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                         fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; kk++)     // 32 columns: 8 of tensor memory, 32 bytes of the activations, the next scale byte
-                            mma_mx(acc + a * BN, sl + (uint32_t)(a * 32 + kk * 8), bd + (uint64_t)(kk * 2),
-                                   idesc + (uint32_t)kk * ((1u << 4) | (1u << 29)), sl + (uint32_t)(C::NA * 32 + a * 4),
+                            mma_mx(acc + a * BN, sl + (uint32_t)(a * 32 + kk * 8), bd + kk * 2, b_hi, idesc[kk], sl + (uint32_t)(C::NA * 32 + a * 4),
                                    sl + (uint32_t)(C::NA * 36), in_chunk > 0 || kk > 0);
                     }
                     if (failed) break;
-                    commit(bar(EMPTY + ring.st));
-                    if (in_chunk == C::FLUSH - 1 || k == nk - 1) {
+                    commit(empty + ring.st * 8);
+                    ring.next();
+                    slot.next();
+                    if (++in_chunk == C::FLUSH || k == nk - 1) {
                         commit(bar(ACC_FULL + set.st));
                         set.next();
+                        in_chunk = 0;
                         if (chunks < C::SETS) chunks++;
                     }
                 }
@@ -472,55 +484,54 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ------------------------------------------------------------------ weights and scales into tensor memory
         set_registers<C::BIG, false>();
         const int q = warp - 12;                           // tensor-memory lanes, weight rows 32 q ..
-        // The scales of activation row 32 j + lane of the tile (-1: none), loaded a stage ahead.  Every warp brings
-        // all of them: each quarter of the lanes holds a copy.
-        int from[C::NR];
-        uint32_t next[C::NR];
+        // The scales of activation row 32 j + lane of the tile, loaded a stage ahead (rows that are not there: those of
+        // row 0, put out by a mask).  Every warp brings all of them: each quarter of the lanes holds a copy.
+        const uint32_t *from[C::NR];
+        uint32_t next[C::NR], there = 0, there_now;
         constexpr int WB = C::NR == 3 ? 4 : C::NR > 4 ? 8 : C::NR;
         auto rows_of = [&](int i) {
             const Tile t = tile_at<BN>(p, where, i);
+            there = 0;
 #pragma unroll
             for (int j = 0; j < C::NR; j++) {
                 const int c = j * 32 + lane;
-                from[j] = -1;
+                int r = -1;
                 if (c < t.n) {
-                    from[j] = p.rows ? __ldg(p.rows + t.r0 + c) : t.r0 + c;
-                    if (from[j] < 0 || from[j] >= p.x_rows) {
-                        atomicOr(p.status, STATUS_RANGE);
-                        from[j] = -1;
-                    }
+                    r = p.rows ? __ldg(p.rows + t.r0 + c) : t.r0 + c;
+                    if (r < 0 || r >= p.x_rows) atomicOr(p.status, STATUS_RANGE), r = -1;
                 }
+                there |= (r >= 0 ? 1u : 0u) << j;
+                from[j] = reinterpret_cast<const uint32_t *>(p.x_scales + (r >= 0 ? (int64_t)r * p.S : 0)) + kt0;
             }
         };
-        auto load = [&](int kt) {
+        auto load = [&] {
 #pragma unroll
-            for (int j = 0; j < C::NR; j++)
-                next[j] = from[j] < 0 ? 0u : __ldg(reinterpret_cast<const uint32_t *>(p.x_scales + (int64_t)from[j] * p.S) + kt);
+            for (int j = 0; j < C::NR; j++) next[j] = __ldg(from[j]++);
         };
         if (cluster < tiles) {
             rows_of(cluster);
-            load(kt0);
+            load();
         }
         Ring<C::ST> ring, freed;                           // this stage; the one whose MMAs read the slot last
         Ring<C::NS> slot;
+        const uint32_t raw0 = smem_addr(smem + C::w), raw_bar = bar(RAW), empty = bar(EMPTY), full = bar(FULL);
+        const uint32_t sl0 = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)C::SLOTS;
+        const int blocks = p.K / QK - kt0 * 4;             // scale bytes of this CTA's columns
         int filled = 0;
         for (int i = cluster; i < tiles && !failed; i += clusters) {
-            for (int k = 0; k < nk; k++, ring.next(), slot.next()) {
-                const int kt = kt0 + k;
+            for (int k = 0; k < nk; k++) {
                 uint32_t sfb[WB];
-                // bytes past the row's end belong to columns of zeros, but must not be NaN
-                const int left = p.K / QK - kt * 4;
-                const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+                there_now = there;
 #pragma unroll
-                for (int j = 0; j < WB; j++) sfb[j] = j < C::NR ? next[j < C::NR ? j : 0] & mask : 0u;
+                for (int j = 0; j < WB; j++) sfb[j] = j < C::NR ? next[j < C::NR ? j : 0] : 0u;
                 if (k + 1 < nk) {
-                    load(kt + 1);
+                    load();
                 } else if (i + clusters < tiles) {
                     rows_of(i + clusters);
-                    load(kt0);
+                    load();
                 }
-                if (!mbar_wait(bar(RAW + ring.st), ring.turn, p.status)) failed = true;
-                const uint8_t *raw = smem + C::w + ring.st * C::NA * MX_TILE_BYTES;
+                if (!mbar_wait(raw_bar + ring.st * 8, ring.turn, p.status)) failed = true;
+                const uint32_t raw = raw0 + (uint32_t)(ring.st * C::NA * MX_TILE_BYTES);
                 uint4 v[C::NA][4], sfa[C::NA];
 #pragma unroll
                 for (int a = 0; a < C::NA; a++) {
@@ -529,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     sfa[a] = lds128(raw + a * MX_TILE_BYTES + MX_TILE_CODES + lane * 16);
                 }
                 if (filled == C::NS) {
-                    if (!failed && !mbar_wait(bar(EMPTY + freed.st), freed.turn, p.status)) failed = true;
+                    if (!failed && !mbar_wait(empty + freed.st * 8, freed.turn, p.status)) failed = true;
                     freed.next();
                 } else {
                     filled++;
@@ -537,7 +548,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 failed = __any_sync(0xffffffffu, failed);
                 if (failed) break;
                 fence_after();
-                const uint32_t sl = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(C::SLOTS + slot.st * C::SLOT);
+                // bytes past the row's end belong to columns of zeros, but must not be NaN
+                const int left = blocks - k * 4;
+                const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+#pragma unroll
+                for (int j = 0; j < C::NR; j++) sfb[j] &= there_now >> j & 1u ? mask : 0u;
+                const uint32_t sl = sl0 + (uint32_t)(slot.st * C::SLOT);
 #pragma unroll
                 for (int a = 0; a < C::NA; a++) {
 #pragma unroll
@@ -556,7 +572,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(FULL + slot.st));
+                if (lane == 0) mbar_arrive(full + slot.st * 8);
+                ring.next();
+                slot.next();
             }
         }
     } else if (warp >= 4) {

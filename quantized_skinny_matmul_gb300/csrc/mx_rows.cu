@@ -81,14 +81,14 @@ __global__ void __launch_bounds__(Q_THREADS) dequantize_mx_kernel(const uint8_t 
 // 4-bit weights into tiles
 // ---------------------------------------------------------------------------
 // One CTA per tile; a thread takes 16 bytes of codes (32 values, one scale) twice.  Of each eight codes, the
-// first four go to the low nibbles of the tile's four bytes, the others to the high ones.
+// first four go to bits 2 .. 5 of the four bytes, the others to bits 6 .. 9 from each byte on (around the end).
 __device__ __forceinline__ uint32_t by_fours(uint32_t w) {
     uint32_t lo = w & 0xFFFFu, hi = w >> 16;      // codes 0 .. 3, 4 .. 7, one per nibble
     lo = (lo | lo << 8) & 0x00FF00FFu;
     lo = (lo | lo << 4) & 0x0F0F0F0Fu;
     hi = (hi | hi << 8) & 0x00FF00FFu;
     hi = (hi | hi << 4) & 0x0F0F0F0Fu;
-    return lo | hi << 4;
+    return lo << 2 | __funnelshift_l(hi, hi, 6);
 }
 __global__ void __launch_bounds__(256) repack_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                            uint8_t *__restrict__ out, int64_t tiles, int64_t N, int64_t K,
@@ -105,14 +105,14 @@ __global__ void __launch_bounds__(256) repack_mxfp4_kernel(const uint8_t *__rest
             const int r = i >> 2, j = i & 3;
             const int64_t n = (int64_t)g * MX_TILE + r, k = (int64_t)t * MX_TILE + 32 * j;
             uint4 v = make_uint4(0, 0, 0, 0);
-            int b = 0;
+            uint8_t b = 0;
             if (n < N && k < K) {
                 const int64_t row = c * N + n;
                 v = *reinterpret_cast<const uint4 *>(codes + (row * K + k) / 2);
-                b = min(scales[row * S + k / 32] + 6, 255);
+                b = scales[row * S + k / 32];
             }
             *reinterpret_cast<uint4 *>(to + j * 2048 + r * 16) = make_uint4(by_fours(v.x), by_fours(v.y), by_fours(v.z), by_fours(v.w));
-            to[MX_TILE_CODES + (r & 31) * 16 + (r >> 5) * 4 + j] = (uint8_t)b;
+            to[MX_TILE_CODES + (r & 31) * 16 + (r >> 5) * 4 + j] = b;
         }
     }
 }
