@@ -7,9 +7,11 @@
 // full tile is shared memory's 128 bytes a cycle, so the weights go through it once, packed, and reach the
 // MMAs in tensor memory:
 //   warp 0     one thread copies, some stages of 128 columns ahead: the weights' tile (packed codes, scales) by a
-//              bulk copy, the activations' codes by a tensor copy;
-//   warps 2, 3     instead of the latter, where a plan names the rows: 16-byte asynchronous copies;
-//   warps 12 .. 15  a weight row per thread: 64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of
+//              bulk copy, the activations' codes by a tensor copy, of four rows at a time where a plan names
+//              them (16-row tiles; for larger ones that would be too many copies for a thread, and a kernel in front
+//              brings the rows into the plan's order);
+//   warps 2, 3     copy the activations' scales;
+//   warps 12 .. 19  two teams, for every other stage each (a stage is mostly latency).  A weight row per thread: 64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of
 //              each (the form of 4-bit operands in tensor memory), and go there, and so do the scales of both
 //              operands.  The tiles hold the codes so that three instructions place eight of them;
 //   warp 1     one thread issues 4 MMAs a stage (8 for the gated unit, whose gate and up tiles share the
@@ -33,25 +35,26 @@
 namespace gq {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 640;
 constexpr int EPI_WARPS = 8;
-constexpr int SPREAD_WARPS = 4;              // 32 weight rows each
-constexpr int GATHER_WARPS = 2;
+constexpr int SPREAD_WARPS = 4;              // of a team, 32 weight rows each
+constexpr int SCALE_WARPS = 2;
 constexpr int MAX_E = 1024;
 constexpr int MAX_STAGES = 16, MAX_SLOTS = 8, MAX_SETS = 4;
-constexpr int FEW_REGS = 88, MANY_REGS = 168;   // per thread, of 128 at launch: 2 x 88 + 2 x 168 = 4 x 128
+constexpr int FEW_REGS = 56, MANY_REGS = 152;   // per thread, of 96 at launch: 3 x 56 + 2 x 152 < 5 x 96
 
 // BN: rows of activations per tile.  GATED: two weight tiles (gate, up) per stage.
 template <int BN, bool GATED>
 struct Cfg {
     static constexpr int NA = GATED ? 2 : 1;
-    static constexpr bool BIG = BN > 64;                    // more sums per thread than an even share of registers holds
-    static constexpr int ST = BN <= 16 ? (GATED ? 8 : 16) : BN <= 64 ? (GATED ? 7 : 10) : 6;   // stages in shared memory
+    static constexpr int ST = BN <= 16 ? (GATED ? 8 : 16) : BN <= 64 ? (GATED ? 6 : 10) : 6;   // stages in shared memory
     static constexpr int PARTS = BN > 64 ? 2 : 1;           // tensor copies of a tile's activations, BN / PARTS rows each
     static constexpr int BOX = BN / PARTS;
     static constexpr int CW = BN <= 16 ? 8 : 16;            // columns per read of tensor memory
     static constexpr int CHUNKS = BN / CW;
     static constexpr int MINE = (CHUNKS + 1) / 2;           // chunks of a warpgroup
+    static constexpr bool BIG = NA * MINE * CW >= 64;       // more sums per thread than an even share of registers holds
+    static constexpr bool GATHERS = BN <= 16;
     static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;
     // Tensor memory: sets of accumulators, then slots of a stage's weights and scales.  The gated unit's large
     // tile has one set only; its accumulators are taken over every 16 stages (2048 columns; what is cut
@@ -69,31 +72,33 @@ struct Cfg {
     static constexpr int COLS = COLS_USED <= 256 ? 256 : 512;
     static_assert(COLS_USED <= 512, "tensor memory");
     static_assert(BOX % 8 == 0 && BN % 16 == 0, "tile rows");
-    static_assert(NS < ST && NS <= MAX_SLOTS && ST <= MAX_STAGES && SETS <= MAX_SETS, "barriers");
+    static_assert(ST % 2 == 0 && NS < ST && NS <= MAX_SLOTS && ST <= MAX_STAGES && SETS <= MAX_SETS, "barriers");
     // shared memory from a 1024-aligned base
     static constexpr int B_STAGE = BN * 128;
     static constexpr int b = 0;
     static constexpr int w = b + ST * B_STAGE;
     static constexpr int part = w + ST * NA * MX_TILE_BYTES;
     static constexpr int PART_BYTES = NA * BN * MX_TILE * 4;
-    static constexpr int starts = part + (MAX_SPLIT - 1) * PART_BYTES;
+    static constexpr int SB_STAGE = NR * 32 * 4;            // a stage's scales of the activation rows
+    static constexpr int sb = part + (MAX_SPLIT - 1) * PART_BYTES;
+    static constexpr int starts = sb + ST * SB_STAGE;
     static constexpr int bars = starts + 3 * (MAX_E + 4) * 4;
-    static constexpr int total = bars + 640;
+    static constexpr int total = bars + 768;
     static_assert(total + 1024 <= 227 * 1024, "shared memory");
 };
 
 enum : int {
     RAW = 0,                     // a stage's copies have landed
-    GATHERED = RAW + MAX_STAGES, // and so have its gathered rows
-    EMPTY = GATHERED + MAX_STAGES,   // its MMAs are done
+    EMPTY = RAW + MAX_STAGES,    // its MMAs are done
     FULL = EMPTY + MAX_STAGES,   // a slot's weights and scales are in tensor memory
     ACC_FULL = FULL + MAX_SLOTS,
     ACC_EMPTY = ACC_FULL + MAX_SETS,         // gate and up apart
-    PART_FULL = ACC_EMPTY + 2 * MAX_SETS,
+    SCALES = ACC_EMPTY + 2 * MAX_SETS,   // a stage's scales of activations have landed
+    PART_FULL = SCALES + MAX_STAGES,
     PART_EMPTY,
     NUM_BARS
 };
-static_assert(NUM_BARS * 8 + 8 <= 640, "barrier area");
+static_assert(NUM_BARS * 8 + 8 <= 768, "barrier area");
 
 struct MxParams {
     const uint8_t *w;              // tiles
@@ -102,7 +107,7 @@ struct MxParams {
     void *dst;
     uint8_t *codes, *scales;       // gated: the output's
     unsigned int *status;
-    const uint8_t *x_codes;        // for gathered rows
+    int lo, hi, base;              // rows of the plan that this launch does; which of them is row 0 of x
     int64_t ldd, x_rows;
     int N, K, KT, G, S, So;        // S, So: scale bytes per row of x and of the gated output
     int E, R, split, bf16;
@@ -137,6 +142,13 @@ __device__ __forceinline__ void write_tmem(uint32_t taddr, const uint32_t (&r)[W
         asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
     else if constexpr (W == 2)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+    else if constexpr (W == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+                taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+            "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
     else if constexpr (W == 4)
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                      : "memory");
@@ -163,26 +175,41 @@ __device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap *map, in
         ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
+// four rows of 128 bytes
+__device__ __forceinline__ void copy_rows4(uint32_t dst, const CUtensorMap *map, int c0, int4 r, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+        : "memory");
+}
 // one lane of the warp
 __device__ __forceinline__ bool elect() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// 16 bytes, zeros unless `there`
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// 4 bytes, zeros unless `there`
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void copy_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+// this thread's copies so far will arrive there (once) when they are done
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+// Whether a phase is over, without waiting.  Asked ahead of time: an answer takes over a hundred cycles.
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) { return mbar_try_wait(bar, parity); }
 // A place in the ring of stages and the parity of its turn.
 template <int ST>
 struct Ring {
@@ -212,6 +239,8 @@ __device__ __forceinline__ void read_acc(uint32_t taddr, uint32_t (&r)[W]) {
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr));
 }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 // a value read from tensor memory, not used before the wait in front of this
 __device__ __forceinline__ float keep(uint32_t r) {
     asm volatile("" : "+r"(r));
@@ -292,8 +321,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::ST; i++) {
             mbar_init(bar(RAW + i), 1);
-            mbar_init(bar(GATHERED + i), GATHER_WARPS);
             mbar_init(bar(EMPTY + i), 1);
+            mbar_init(bar(SCALES + i), SCALE_WARPS * 32);
         }
         for (int i = 0; i < C::NS; i++) mbar_init(bar(FULL + i), SPREAD_WARPS);
         for (int i = 0; i < C::SETS; i++) mbar_init(bar(ACC_FULL + i), 1);
@@ -316,14 +345,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int e = e0 + lane;
             int tiles = 0;
             if (e < p.E) {
-                const int r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.R;
-                where.first[e] = r0;
-                where.last[e] = r1;
+                int r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.R;
                 if (r0 < 0 || r1 < r0 || r1 > p.R) {
                     atomicOr(p.status, STATUS_RANGE);
-                } else {
-                    tiles = (r1 - r0 + BN - 1) / BN;
+                    r0 = r1 = 0;
                 }
+                r0 = max(r0, p.lo);
+                r1 = min(r1, p.hi);
+                where.first[e] = r0;
+                where.last[e] = r1;
+                if (r1 > r0) tiles = (r1 - r0 + BN - 1) / BN;
             }
             int s = tiles;
 #pragma unroll
@@ -354,8 +385,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const Tile t = tile_at<BN>(p, where, i);
                 const uint8_t *w = p.w + (((int64_t)t.e * C::NA * p.G + t.g) * p.KT + kt0) * MX_TILE_BYTES;
                 const int64_t up = (int64_t)p.G * p.KT * MX_TILE_BYTES;    // from the gate's tile to the up matrix's
-                const int parts = p.rows ? 0 : t.n > C::BOX ? C::PARTS : 1;
+                const int parts = t.n > C::BOX ? C::PARTS : 1;
                 const uint32_t bytes = (uint32_t)(C::NA * MX_TILE_BYTES + parts * C::BOX * 128);
+                int4 from[4];                              // gathered rows; past the tile and outside x: zeros
+                if (C::GATHERS && p.rows)
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        int r[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            r[j] = u * 4 + j < t.n ? __ldg(p.rows + t.r0 + u * 4 + j) : (int)p.x_rows;
+                            if (r[j] < 0 || r[j] > p.x_rows) r[j] = (int)p.x_rows;
+                        }
+                        from[u] = make_int4(r[0], r[1], r[2], r[3]);
+                    }
                 for (int k = 0; k < nk; k++, w += MX_TILE_BYTES, ring.next()) {
                     if (filled == C::ST) {
                         if (!mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) {
@@ -370,11 +413,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int a = 0; a < C::NA; a++)
                         bulk_g2s(smem_addr(smem + C::w) + (uint32_t)((ring.st * C::NA + a) * MX_TILE_BYTES), w + a * up, MX_TILE_BYTES, raw);
+                    if (C::GATHERS && p.rows) {
+#pragma unroll
+                        for (int u = 0; u < 4; u++)
+                            copy_rows4(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE + u * 512), &map_x, (kt0 + k) * MX_TILE, from[u], raw);
+                        continue;
+                    }
 #pragma unroll
                     for (int u = 0; u < C::PARTS; u++)
                         if (u < parts)
                             copy_2d(smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE + u * C::BOX * 128), &map_x, (kt0 + k) * MX_TILE,
-                                    t.r0 + u * C::BOX, raw);
+                                    t.r0 - p.base + u * C::BOX, raw);
                 }
             }
         }
@@ -389,6 +438,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint64_t bdesc = operand_desc(smem_addr(smem + C::b));
             const uint32_t b_lo = (uint32_t)bdesc, b_hi = (uint32_t)(bdesc >> 32);
             int chunks = 0;
+            bool full_ready = false;
             for (int i = cluster; i < tiles && !failed; i += clusters) {
                 const Tile t = tile_at<BN>(p, where, i);
                 uint32_t idesc[4];                         // of the scale bytes' four places
@@ -397,8 +447,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 int in_chunk = 0;
                 for (int k = 0; k < nk; k++) {
                     // (whoever arrived there had waited for the stage's copies)
-                    if (!mbar_wait(full + slot.st * 8, slot.turn, p.status)) failed = true;
-                    if (p.rows && !failed && !mbar_wait(bar(GATHERED + ring.st), ring.turn, p.status)) failed = true;
+                    if (!full_ready && !mbar_wait(full + slot.st * 8, slot.turn, p.status)) failed = true;
                     const uint32_t sl = slots + (uint32_t)(slot.st * C::SLOT), acc = tmem + (uint32_t)(set.st * C::ACC);
                     const uint32_t bd = b_lo + (uint32_t)(ring.st * (C::B_STAGE >> 4));
 #pragma unroll
@@ -417,6 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     commit(empty + ring.st * 8);
                     ring.next();
                     slot.next();
+                    full_ready = ready(full + slot.st * 8, slot.turn);
                     if (++in_chunk == C::FLUSH || k == nk - 1) {
                         commit(bar(ACC_FULL + set.st));
                         set.next();
@@ -427,157 +477,130 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
     } else if (warp < 4) {
-        // ------------------------------------------------------------------ gathered rows
+        // ------------------------------------------------------------------ the activations' scales
         set_registers<C::BIG, false>();
-        if (p.rows) {
-            // Thread x copies 16 bytes, piece x % 8, of the tile's rows x / 8, x / 8 + 8, ..; two stages are under
-            // way before the first is waited for.
-            constexpr int ROWS = BN / 8, AHEAD = 2;
-            const int x = (warp - 2) * 32 + lane;
-            int from[ROWS], filled = 0;
-            Ring<C::ST> ring, done;
-            int under_way = 0;
-            auto finish = [&] {
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(GATHERED + done.st));
-                done.next();
-                under_way--;
-            };
-            for (int i = cluster; i < tiles && !failed; i += clusters) {
-                const Tile t = tile_at<BN>(p, where, i);
-#pragma unroll
-                for (int j = 0; j < ROWS; j++) {
-                    const int c = j * 8 + (x >> 3);
-                    const int r = c < t.n ? __ldg(p.rows + t.r0 + c) : -1;
-                    from[j] = r >= 0 && r < p.x_rows ? r : -1;
-                }
-                for (int k = 0; k < nk; k++, ring.next()) {
-                    if (filled == C::ST) {
-                        if (!mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
-                        failed = __any_sync(0xffffffffu, failed);
-                        if (failed) break;
-                    } else {
-                        filled++;
-                    }
-                    const int col = (kt0 + k) * MX_TILE + (x & 7) * 16;
-                    const uint32_t to = smem_addr(smem + C::b) + (uint32_t)(ring.st * C::B_STAGE + (x >> 3) * 128 + (((x & 7) ^ (x >> 3)) << 4));
-#pragma unroll
-                    for (int j = 0; j < ROWS; j++)
-                        if (j * 8 < t.n) {
-                            const bool there = from[j] >= 0 && col < p.K;
-                            copy16(to + j * 1024, p.x_codes + (there ? (int64_t)from[j] * p.K + col : 0), there);
-                        }
-                    copy_group();
-                    if (++under_way > AHEAD) {
-                        copy_wait<AHEAD>();
-                        finish();
-                    }
-                }
+        const int x = (warp - 2) * 32 + lane;
+        constexpr int SROWS = (C::NR * 32 + 63) / 64;      // thread x copies the scales of the tile's rows x, x + 64, ..
+        int scale_row[SROWS], filled = 0;
+        Ring<C::ST> ring;
+        bool free = false;
+        auto row = [&](const Tile &t, int c) {             // the tile's row c in x, or -1
+            int r = -1;
+            if (c < t.n) {
+                r = p.rows ? __ldg(p.rows + t.r0 + c) : t.r0 - p.base + c;
+                if (r < 0 || r >= p.x_rows) atomicOr(p.status, STATUS_RANGE), r = -1;
             }
-            if (!failed) {
-                copy_wait<0>();
-                while (under_way > 0) finish();
-            }
-        }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------------ weights and scales into tensor memory
-        set_registers<C::BIG, false>();
-        const int q = warp - 12;                           // tensor-memory lanes, weight rows 32 q ..
-        // The scales of activation row 32 j + lane of the tile, loaded a stage ahead (rows that are not there: those of
-        // row 0, put out by a mask).  Every warp brings all of them: each quarter of the lanes holds a copy.
-        const uint32_t *from[C::NR];
-        uint32_t next[C::NR], there = 0, there_now;
-        constexpr int WB = C::NR == 3 ? 4 : C::NR > 4 ? 8 : C::NR;
-        auto rows_of = [&](int i) {
-            const Tile t = tile_at<BN>(p, where, i);
-            there = 0;
-#pragma unroll
-            for (int j = 0; j < C::NR; j++) {
-                const int c = j * 32 + lane;
-                int r = -1;
-                if (c < t.n) {
-                    r = p.rows ? __ldg(p.rows + t.r0 + c) : t.r0 + c;
-                    if (r < 0 || r >= p.x_rows) atomicOr(p.status, STATUS_RANGE), r = -1;
-                }
-                there |= (r >= 0 ? 1u : 0u) << j;
-                from[j] = reinterpret_cast<const uint32_t *>(p.x_scales + (r >= 0 ? (int64_t)r * p.S : 0)) + kt0;
-            }
+            return r;
         };
-        auto load = [&] {
-#pragma unroll
-            for (int j = 0; j < C::NR; j++) next[j] = __ldg(from[j]++);
-        };
-        if (cluster < tiles) {
-            rows_of(cluster);
-            load();
-        }
-        Ring<C::ST> ring, freed;                           // this stage; the one whose MMAs read the slot last
-        Ring<C::NS> slot;
-        const uint32_t raw0 = smem_addr(smem + C::w), raw_bar = bar(RAW), empty = bar(EMPTY), full = bar(FULL);
-        const uint32_t sl0 = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)C::SLOTS;
-        const int blocks = p.K / QK - kt0 * 4;             // scale bytes of this CTA's columns
-        int filled = 0;
         for (int i = cluster; i < tiles && !failed; i += clusters) {
+            const Tile t = tile_at<BN>(p, where, i);
+#pragma unroll
+            for (int j = 0; j < SROWS; j++) scale_row[j] = row(t, j * 64 + x);
             for (int k = 0; k < nk; k++) {
-                uint32_t sfb[WB];
-                there_now = there;
-#pragma unroll
-                for (int j = 0; j < WB; j++) sfb[j] = j < C::NR ? next[j < C::NR ? j : 0] : 0u;
-                if (k + 1 < nk) {
-                    load();
-                } else if (i + clusters < tiles) {
-                    rows_of(i + clusters);
-                    load();
-                }
-                if (!mbar_wait(raw_bar + ring.st * 8, ring.turn, p.status)) failed = true;
-                const uint32_t raw = raw0 + (uint32_t)(ring.st * C::NA * MX_TILE_BYTES);
-                uint4 v[C::NA][4], sfa[C::NA];
-#pragma unroll
-                for (int a = 0; a < C::NA; a++) {
-#pragma unroll
-                    for (int j = 0; j < 4; j++) v[a][j] = lds128(raw + a * MX_TILE_BYTES + j * 2048 + (q * 32 + lane) * 16);
-                    sfa[a] = lds128(raw + a * MX_TILE_BYTES + MX_TILE_CODES + lane * 16);
-                }
-                if (filled == C::NS) {
-                    if (!failed && !mbar_wait(empty + freed.st * 8, freed.turn, p.status)) failed = true;
-                    freed.next();
+                const int kt = kt0 + k;
+                if (filled == C::ST) {
+                    if (!free && !mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
+                    failed = __any_sync(0xffffffffu, failed);
+                    if (failed) break;
                 } else {
                     filled++;
                 }
-                failed = __any_sync(0xffffffffu, failed);
-                if (failed) break;
-                fence_after();
-                // bytes past the row's end belong to columns of zeros, but must not be NaN
-                const int left = blocks - k * 4;
-                const uint32_t mask = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1u;
+                const uint32_t scales = smem_addr(smem + C::sb) + (uint32_t)(ring.st * C::SB_STAGE + x * 4);
 #pragma unroll
-                for (int j = 0; j < C::NR; j++) sfb[j] &= there_now >> j & 1u ? mask : 0u;
-                const uint32_t sl = sl0 + (uint32_t)(slot.st * C::SLOT);
-#pragma unroll
-                for (int a = 0; a < C::NA; a++) {
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        uint32_t c[8];
-                        spread8(v[a][j].x, c[0], c[1]);
-                        spread8(v[a][j].y, c[2], c[3]);
-                        spread8(v[a][j].z, c[4], c[5]);
-                        spread8(v[a][j].w, c[6], c[7]);
-                        write_tmem<8>(sl + (uint32_t)(a * 32 + j * 8), c);
-                    }
-                    const uint32_t s4[4] = {sfa[a].x, sfa[a].y, sfa[a].z, sfa[a].w};
-                    write_tmem<4>(sl + (uint32_t)(C::NA * 32 + a * 4), s4);
-                }
-                write_tmem<WB>(sl + (uint32_t)(C::NA * 36), sfb);
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + slot.st * 8);
+                for (int j = 0; j < SROWS; j++)
+                    if (j * 64 + x < C::NR * 32)
+                        copy4(scales + j * 256, p.x_scales + (scale_row[j] >= 0 ? (int64_t)scale_row[j] * p.S + kt * 4 : 0), scale_row[j] >= 0);
+                arrive_copied(bar(SCALES + ring.st));
                 ring.next();
-                slot.next();
+                free = filled == C::ST && ready(bar(EMPTY + ring.st), ring.turn ^ 1);
             }
         }
-    } else if (warp >= 4) {
+        copy_wait();                                    // (nothing of this CTA's shared memory is under way at its end)
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------------ weights and scales into tensor memory
+        set_registers<C::BIG, false>();
+        const int q = warp & 3, team = (warp - 12) >> 2;   // tensor-memory lanes, weight rows 32 q ..; every other stage
+        constexpr int WB = C::NR == 3 ? 4 : C::NR > 4 ? 8 : C::NR;
+        const int steps = cluster < tiles ? (tiles - cluster + clusters - 1) / clusters * nk : 0;
+        const int blocks = p.K / QK - kt0 * 4;             // scale bytes of this CTA's columns
+        const uint32_t raw0 = smem_addr(smem + C::w) + (uint32_t)((q * 32 + lane) * 16), sb0 = smem_addr(smem + C::sb) + (uint32_t)(lane * 4);
+        const uint32_t raw_bar = bar(RAW), scales_bar = bar(SCALES), empty = bar(EMPTY), full = bar(FULL);
+        const uint32_t sl0 = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)C::SLOTS;
+        Ring<C::ST> ring, freed;                           // this stage; the one whose MMAs read the slot last
+        Ring<C::NS> slot;
+        int k = 0;
+        if (team) {
+            ring.next();
+            slot.next();
+            if (++k == nk) k = 0;
+        }
+        // The stage NS before this one; for the first ones there is none.
+        auto to_freed = [&](int step) {
+            const int f = step - C::NS;
+            freed.st = f % C::ST, freed.turn = (uint32_t)(f / C::ST) & 1;
+        };
+        bool raw_ready = false, scales_ready = false, slot_ready = true;
+        for (int step = team; step < steps; step += 2) {
+            if (!raw_ready && !mbar_wait(raw_bar + ring.st * 8, ring.turn, p.status)) failed = true;
+            if (!scales_ready && !failed && !mbar_wait(scales_bar + ring.st * 8, ring.turn, p.status)) failed = true;
+            if (!slot_ready && !failed && !mbar_wait(empty + freed.st * 8, freed.turn, p.status)) failed = true;
+            failed = __any_sync(0xffffffffu, failed);
+            if (failed) break;
+            fence_after();
+            const uint32_t raw = raw0 + (uint32_t)(ring.st * C::NA * MX_TILE_BYTES), sl = sl0 + (uint32_t)(slot.st * C::SLOT);
+            // every warp takes the scales of all activation rows (row 32 j + lane): each quarter of tensor memory's lanes
+            // holds a copy
+            uint32_t sfb[WB];
+#pragma unroll
+            for (int j = 0; j < WB; j++) sfb[j] = j < C::NR ? lds32(sb0 + (uint32_t)(ring.st * C::SB_STAGE + j * 128)) : 0u;
+            uint4 v[4], sfa[C::NA];
+#pragma unroll
+            for (int a = 0; a < C::NA; a++) {
+                sfa[a] = lds128(raw + a * MX_TILE_BYTES + MX_TILE_CODES - q * 512);
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] = lds128(raw + a * MX_TILE_BYTES + j * 2048);
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    uint32_t c[16];
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        spread8(v[j + h].x, c[8 * h], c[8 * h + 1]);
+                        spread8(v[j + h].y, c[8 * h + 2], c[8 * h + 3]);
+                        spread8(v[j + h].z, c[8 * h + 4], c[8 * h + 5]);
+                        spread8(v[j + h].w, c[8 * h + 6], c[8 * h + 7]);
+                    }
+                    write_tmem<16>(sl + (uint32_t)(a * 32 + j * 8), c);
+                }
+                const uint32_t s4[4] = {sfa[a].x, sfa[a].y, sfa[a].z, sfa[a].w};
+                write_tmem<4>(sl + (uint32_t)(C::NA * 32 + a * 4), s4);
+            }
+            // bytes past the row's end belong to columns of zeros, but must not be NaN
+            const int left = blocks - k * 4;
+            if (left < 4)
+#pragma unroll
+                for (int j = 0; j < C::NR; j++) sfb[j] &= (1u << (8 * left)) - 1u;
+            write_tmem<WB>(sl + (uint32_t)(C::NA * 36), sfb);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + slot.st * 8);
+            ring.next();
+            ring.next();
+            slot.next();
+            slot.next();
+            if (++k == nk) k = 0;
+            if (++k == nk) k = 0;
+            if (step + 2 < steps) {
+                // (this team's stage before that one in the ring is done with: ST is even)
+                raw_ready = ready(raw_bar + ring.st * 8, ring.turn);
+                scales_ready = ready(scales_bar + ring.st * 8, ring.turn);
+                if (step + 2 >= C::NS) {
+                    to_freed(step + 2);
+                    slot_ready = ready(empty + freed.st * 8, freed.turn);
+                }
+            }
+        }
+    } else {
         // ------------------------------------------------------------------ sums, output
         set_registers<C::BIG, true>();
         const int q = warp & 3, half = (warp - 4) >> 2;    // tensor-memory lanes 32 q .., column chunks half, half + 2, ..
@@ -601,16 +624,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int a = 0; a < C::NA; a++) {
                     const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(set.st * C::ACC + a * BN + half * C::CW);
-                    // two reads of tensor memory under way at a time
+                    // two reads of tensor memory under way at a time (where registers allow it)
+                    constexpr int X = C::NA * C::MINE * C::CW > 96 ? 1 : 2;
 #pragma unroll
-                    for (int j = 0; j < C::MINE; j += 2) {
-                        uint32_t v[2][C::CW];
+                    for (int j = 0; j < C::MINE; j += X) {
+                        uint32_t v[X][C::CW];
 #pragma unroll
-                        for (int x = 0; x < 2; x++)
+                        for (int x = 0; x < X; x++)
                             if (j + x < C::MINE && 2 * (j + x) + half < cols) read_acc<C::CW>(at + (uint32_t)(2 * (j + x) * C::CW), v[x]);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                        for (int x = 0; x < 2; x++)
+                        for (int x = 0; x < X; x++)
                             if (j + x < C::MINE && 2 * (j + x) + half < cols)
 #pragma unroll
                                 for (int c = 0; c < C::CW; c++) acc[a][j + x < C::MINE ? j + x : 0][c] += keep(v[x][c]);
@@ -665,68 +689,81 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const int n = t.g * MX_TILE + 32 * q + lane;
             if constexpr (!GATED) {
-                if (n < p.N)
+                if (n < p.N) {
+                    auto store = [&](auto *dst) {
+                        const int64_t ldd = p.ldd;
+                        dst += (int64_t)(t.r0 + half * C::CW) * ldd + n;
 #pragma unroll
-                    for (int j = 0; j < C::MINE; j++)
+                        for (int j = 0; j < C::MINE; j++)
 #pragma unroll
-                        for (int c = 0; c < C::CW; c++) {
-                            const int col = (2 * j + half) * C::CW + c;
-                            if (col < t.n) {
-                                const int64_t at = (int64_t)(t.r0 + col) * p.ldd + n;
-                                if (p.bf16)
-                                    static_cast<__nv_bfloat16 *>(p.dst)[at] = __float2bfloat16_rn(acc[0][j][c]);
-                                else
-                                    static_cast<float *>(p.dst)[at] = acc[0][j][c];
-                            }
-                        }
+                            for (int c = 0; c < C::CW; c++)
+                                if ((2 * j + half) * C::CW + c < t.n) put(dst + (2 * j * C::CW + c) * ldd, acc[0][j][c]);
+                    };
+                    if (p.bf16)
+                        store(static_cast<__nv_bfloat16 *>(p.dst));
+                    else
+                        store(static_cast<float *>(p.dst));
+                }
             } else {
                 // a warp's 32 lanes are one block of 32 output values of each column's row; N is a
                 // multiple of 32, so the block is there as a whole or not at all
-                if (t.g * MX_TILE + 32 * q < p.N) {
-                    uint8_t *const codes = p.codes + (int64_t)t.r0 * p.N + t.g * MX_TILE + 32 * q + (lane & ~3);
-                    uint8_t *const scales = p.scales + (int64_t)t.r0 * p.So + t.g * 4 + q;
+                const int block = t.g * 4 + q, last = p.N / QK - 1;
+                if (block <= last) {
+                    // lane l writes four codes of column l % 4, and lane l < 4 its scale
+                    const int64_t first = t.r0 + half * C::CW + (lane & 3);
+                    uint8_t *const codes = p.codes + first * p.N + block * 32 + (lane & ~3);
+                    uint8_t *const scales = p.scales + first * p.So + block;
 #pragma unroll
                     for (int j = 0; j < C::MINE; j++)
 #pragma unroll
                         for (int c = 0; c < C::CW; c += 4) {
                             const int col = (2 * j + half) * C::CW + c;
                             if (col >= t.n) continue;
-                            uint32_t word = 0;             // this lane's code in each of four columns
-                            uint32_t bytes = 0;            // their scales
+                            float v[4];
+                            uint32_t top[4];
 #pragma unroll
-                            for (int x = 0; x < 4; x++) {
-                                const float v = swish(acc[0][j][c + x]) * acc[1][j][c + x];
-                                const int b = mx_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu), false);
-                                const float inv = mx_inverse(b);
-                                word |= (inv == 0.0f ? 0u : e4m3x2(v * inv, 0.0f)) << (8 * x);
-                                bytes |= (uint32_t)b << (8 * x);
+                            for (int x = 0; x < 4; x++) v[x] = swish(acc[0][j][c + x]) * acc[1][j][c + x];
+                            // the largest magnitude, rounded up to 7/4 times a power of two where above it: its exponent, less
+                            // 8, is the scale byte (mx_scale_byte), and 262 less that of the scale's inverse
+#pragma unroll
+                            for (int x = 0; x < 4; x++) top[x] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[x]) & 0x7FFFFFFFu) + 0x1FFFFFu;
+                            bool odd = false;              // a block that is tiny, infinite or NaN
+#pragma unroll
+                            for (int x = 0; x < 4; x++) odd |= top[x] - (9u << 23) >= (246u << 23);
+                            uint32_t word, bytes;
+                            if (odd) {
+                                word = bytes = 0;
+#pragma unroll
+                                for (int x = 0; x < 4; x++) {
+                                    const int b = mx_scale_byte(top[x] - 0x1FFFFFu, false);
+                                    const float inv = mx_inverse(b);
+                                    word |= (inv == 0.0f ? 0u : e4m3x2(v[x] * inv, 0.0f)) << (8 * x);
+                                    bytes |= (uint32_t)b << (8 * x);
+                                }
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < 4; x++) v[x] *= __uint_as_float((262u << 23) - (top[x] & 0x7F800000u));
+                                word = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
+                                const uint32_t mine = lane & 2 ? (lane & 1 ? top[3] : top[2]) : (lane & 1 ? top[1] : top[0]);
+                                bytes = ((mine >> 23) - 8) << (8 * (lane & 3));
                             }
                             // four lanes turn their 4 x 4 codes: lane l & 3 then has column l & 3's four
                             uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
-                            word = lane & 1 ? __byte_perm(other, word, 0x7351) : __byte_perm(word, other, 0x6240);
+                            word = __byte_perm(word, other, lane & 1 ? 0x3715 : 0x6240);
                             other = __shfl_xor_sync(0xffffffffu, word, 2);
-                            word = lane & 2 ? __byte_perm(other, word, 0x7632) : __byte_perm(word, other, 0x5410);
-                            const int mine = col + (lane & 3);
-                            if (mine < t.n) {
-                                *reinterpret_cast<uint32_t *>(codes + (int64_t)mine * p.N) = word;
-                                if (lane < 4) scales[(int64_t)mine * p.So] = (uint8_t)(bytes >> (8 * lane));
+                            word = __byte_perm(word, other, lane & 2 ? 0x3276 : 0x5410);
+                            if (col + (lane & 3) < t.n) {
+                                *reinterpret_cast<uint32_t *>(codes + (2 * j * C::CW + c) * (int64_t)p.N) = word;
+                                if (lane < 4) scales[(2 * j * C::CW + c) * (int64_t)p.So] = (uint8_t)(bytes >> (8 * lane));
                             }
                         }
                 }
-                // the scales' padding, by the warp of the row's last block
-                const int last = p.N / QK - 1;
-                if (t.g * 4 + q == last)
-#pragma unroll
-                    for (int j = 0; j < C::MINE; j++)
-#pragma unroll
-                        for (int c = 0; c < C::CW; c++) {
-                            const int col = (2 * j + half) * C::CW + c;
-                            if (col < t.n && last + 1 + lane < p.So) p.scales[(int64_t)(t.r0 + col) * p.So + last + 1 + lane] = 0;
-                        }
+                // the scales' padding, by the warps of the rows' last block
+                if (block == last && last + 1 + lane < p.So)
+#pragma unroll 1
+                    for (int col = half; col < t.n; col += 2) p.scales[(int64_t)(t.r0 + col) * p.So + last + 1 + lane] = 0;
             }
         }
-    } else {
-        set_registers<C::BIG, false>();
     }
     __syncwarp();
     fence_before();
@@ -738,9 +775,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+// Rows lo .. hi - 1 of the plan, as far as they are in use, brought into its order: codes and scales, 16 bytes a thread and
+// turn.  A row whose index is out of range becomes zeros.
+__global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                                                          const int32_t *__restrict__ rows, const int32_t *__restrict__ used,
+                                                          uint8_t *__restrict__ to_codes, uint8_t *__restrict__ to_scales, int lo, int hi,
+                                                          int64_t x_rows, int K, int S, unsigned int *status) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int end = min(hi, *used), pieces = K / 16, all = pieces + S / 16;
+    // a warp takes rows in turn, two at a time
+    const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
+    for (int r = lo + (int)(blockIdx.x * 8 + (threadIdx.x >> 5)); r < end; r += warps) {
+        const int from = __ldg(rows + r);
+        const bool there = from >= 0 && from < x_rows;
+        if (!there && lane == 0) atomicOr(status, STATUS_RANGE);
+        const uint4 *c = reinterpret_cast<const uint4 *>(codes + (int64_t)(there ? from : 0) * K);
+        const uint4 *b = reinterpret_cast<const uint4 *>(scales + (int64_t)(there ? from : 0) * S);
+        uint4 *tc = reinterpret_cast<uint4 *>(to_codes + (int64_t)(r - lo) * K), *tb = reinterpret_cast<uint4 *>(to_scales + (int64_t)(r - lo) * S);
+#pragma unroll 4
+        for (int i = lane; i < all; i += 32) {
+            const uint4 v = there ? __ldg(i < pieces ? c + i : b + (i - pieces)) : make_uint4(0u, 0u, 0u, 0u);
+            *(i < pieces ? tc + i : tb + (i - pieces)) = v;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+constexpr int64_t GATHER_BYTES = 512LL << 20;   // of rows brought into order at a time
+
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
@@ -781,7 +846,7 @@ gq_status launch(MxParams p, const gq_mx_rows &x, int64_t most_tiles, cudaStream
         if (dev >= 0 && dev < MAX_DEV) allowed[dev].store(true, std::memory_order_release);
     }
     CUtensorMap mx;
-    st = encode(&mx, x.codes, x.rows, p.K, C::BOX);
+    st = encode(&mx, x.codes, x.rows, p.K, p.rows ? 1 : C::BOX);
     if (st != GQ_OK) return st;
 
     // K shared out where the tiles leave SMs idle, two stages a CTA at least
@@ -823,20 +888,49 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     p.S = (int)gq_mx_scale_cols(K), p.So = gated ? (int)gq_mx_scale_cols(N) : 0;
     p.dst = dst, p.codes = static_cast<uint8_t *>(codes), p.scales = scales, p.x_scales = x.scales;
     p.w = static_cast<const uint8_t *>(rep);
-    p.x_codes = static_cast<const uint8_t *>(x.codes);
+    p.lo = 0, p.hi = p.R;
 
     // Rows per tile by the rows that an expert has on average (of the experts that can have any).
     const int64_t some = std::min<int64_t>(p.E, p.R), mean = (p.R + some - 1) / some;
     auto most = [&](int bn) { return ((plan ? some : 0) + (p.R + bn - 1) / bn) * p.G; };
     if (most(16) >= (1LL << 31)) return fail(GQ_ERR_INVALID_ARG, "R=%lld rows of N=%lld are too many", (long long)p.R, (long long)N);
-    if (gated) {
-        if (mean <= 16) return launch<16, true>(p, x, most(16), s);
-        if (mean <= 64) return launch<64, true>(p, x, most(64), s);
-        return launch<128, true>(p, x, most(128), s);
+    auto run = [&](const gq_mx_rows &rows) {
+        if (gated) {
+            if (mean <= 16) return launch<16, true>(p, rows, most(16), s);
+            if (mean <= 64) return launch<64, true>(p, rows, most(64), s);
+            return launch<128, true>(p, rows, most(128), s);
+        }
+        if (mean <= 16) return launch<16, false>(p, rows, most(16), s);
+        if (mean <= 64) return launch<64, false>(p, rows, most(64), s);
+        return launch<176, false>(p, rows, most(176), s);
+    };
+    if (!p.rows || mean <= 16) return run(x);
+    // the rows in the plan's order, as many at a time as the workspace's share holds; the kernel sees them as rows lo .. of an
+    // array that begins lo rows earlier
+    const int64_t row_bytes = K + p.S, some_rows = std::min<int64_t>(p.R, std::max<int64_t>(1, GATHER_BYTES / row_bytes));
+    Workspace ws;
+    gq_status st = get_workspace(s, 0, (size_t)(some_rows * row_bytes), &ws);
+    if (st != GQ_OK) return st;
+    const int32_t *from = p.rows, *used = p.offsets + p.E;
+    uint8_t *codes_to = ws.data, *scales_to = ws.data + some_rows * K;
+    p.rows = nullptr;
+    for (int64_t lo = 0; lo < p.R; lo += some_rows) {
+        int l = (int)lo, h = (int)std::min<int64_t>(p.R, lo + some_rows), k = (int)K, S = p.S;
+        int64_t x_rows = x.rows;
+        const void *xc = x.codes;
+        const uint8_t *xs = x.scales;
+        unsigned int *status = p.status;
+        void *args[] = {&xc, &xs, &from, &used, &codes_to, &scales_to, &l, &h, &x_rows, &k, &S, &status};
+        st = launch_pdl((const void *)gather_rows_kernel, dim3((unsigned)std::min<int64_t>((h - l + 7) / 8, 8LL * sm_count())), dim3(256), 0, s,
+                        args, "gather rows launch");
+        if (st != GQ_OK) return st;
+        p.lo = l, p.hi = h, p.base = l;
+        p.x_scales = scales_to;
+        p.x_rows = h - l;
+        st = run(gq_mx_rows{h - l, codes_to, scales_to});
+        if (st != GQ_OK) return st;
     }
-    if (mean <= 16) return launch<16, false>(p, x, most(16), s);
-    if (mean <= 64) return launch<64, false>(p, x, most(64), s);
-    return launch<176, false>(p, x, most(176), s);
+    return GQ_OK;
 }
 
 }  // namespace gq
