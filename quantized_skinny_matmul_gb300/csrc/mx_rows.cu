@@ -13,67 +13,93 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int Q_THREADS = 256;
 
-// One group of 8 values per thread and turn; the K / 8 groups of a row are a multiple of four, so
-// the four lanes of a block are in one row and all there.
+// Quotients of 31-bit numbers by a number known at launch: n * mul >> shift, with mul = ceil(2^shift / d) and shift = 31 +
+// ceil(log2 d), for which the error stays below 1 / d.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+    __device__ __forceinline__ uint32_t of(uint32_t n) const { return (uint32_t)((uint64_t)n * mul >> shift); }
+};
+Divisor divisor(uint32_t d) {
+    int l = 0;
+    while ((1u << l) < d) l++;
+    return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), 31 + l};
+}
+
+// One group of 8 values per thread, U of them in flight; the K / 8 groups of a row are a multiple of four, so the four lanes of
+// a block are in one row and all there.
 template <typename T, bool E2M1>
 __global__ void __launch_bounds__(Q_THREADS) quantize_mx_kernel(const T *__restrict__ x, int64_t ldx, uint8_t *__restrict__ codes,
-                                                                uint8_t *__restrict__ scales, int64_t groups, int per_row,
-                                                                int S) {
+                                                                uint8_t *__restrict__ scales, uint32_t groups, uint32_t per_row,
+                                                                Divisor by_row, int S) {
+    constexpr int U = sizeof(T) == 4 ? 2 : 4;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t stride = (int64_t)gridDim.x * Q_THREADS;
-    for (int64_t first = (int64_t)blockIdx.x * Q_THREADS; first < groups; first += stride) {
-        const int64_t i = first + threadIdx.x;
-        const bool live = i < groups;
-        const int64_t row = live ? i / per_row : 0;
-        const int g = live ? (int)(i - row * per_row) : 0;
-        float v[8];
-        load8(x + row * ldx + g * 8, v);
-        const int b = mx_scale_byte(block_amax(v), E2M1);
-        const uint2 c = codes8<E2M1>(v, mx_inverse(b));
-        if (!live) continue;
-        if (E2M1)
-            *reinterpret_cast<uint32_t *>(codes + (row * per_row + g) * 4) = c.x;
-        else
-            *reinterpret_cast<uint2 *>(codes + (row * per_row + g) * 8) = c;
-        if ((g & 3) == 0) scales[row * S + (g >> 2)] = (uint8_t)b;
-        // the row's last block also writes the padding
-        if (g == per_row - 4)
-            for (int j = per_row / 4; j < S; j++) scales[row * S + j] = 0;
+    const uint32_t stride = gridDim.x * Q_THREADS;
+    for (uint32_t first = blockIdx.x * Q_THREADS; first < groups; first += U * stride) {
+        float v[U][8];
+        uint32_t row[U], g[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint32_t i = first + u * stride + threadIdx.x;
+            row[u] = i < groups ? by_row.of(i) : 0;
+            g[u] = i < groups ? i - row[u] * per_row : 0;
+            load8(x + (int64_t)row[u] * ldx + g[u] * 8, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int b = mx_scale_byte(block_amax(v[u]), E2M1);
+            const uint2 c = codes8<E2M1>(v[u], mx_inverse(b));
+            if (first + u * stride + threadIdx.x >= groups) continue;
+            const int64_t i = (int64_t)row[u] * per_row + g[u];
+            if (E2M1)
+                *reinterpret_cast<uint32_t *>(codes + i * 4) = c.x;
+            else
+                *reinterpret_cast<uint2 *>(codes + i * 8) = c;
+            if ((g[u] & 3) == 0) scales[(int64_t)row[u] * S + (g[u] >> 2)] = (uint8_t)b;
+            // the row's last block also writes the padding
+            if (g[u] == per_row - 4)
+                for (int j = per_row / 4; j < S; j++) scales[(int64_t)row[u] * S + j] = 0;
+        }
     }
 }
 
 template <typename T, bool E2M1>
 __global__ void __launch_bounds__(Q_THREADS) dequantize_mx_kernel(const uint8_t *__restrict__ codes,
                                                                   const uint8_t *__restrict__ scales, T *__restrict__ y,
-                                                                  int64_t groups, int per_row, int S) {
+                                                                  uint32_t groups, uint32_t per_row, Divisor by_row, int S) {
+    constexpr int U = 4;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t stride = (int64_t)gridDim.x * Q_THREADS;
-    for (int64_t i = (int64_t)blockIdx.x * Q_THREADS + threadIdx.x; i < groups; i += stride) {
-        const int64_t row = i / per_row;
-        const int g = (int)(i - row * per_row);
-        const float p = mx_power(scales[row * S + (g >> 2)]);
-        float v[8];
-        if (E2M1) {
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + i * 4);
+    const uint32_t stride = gridDim.x * Q_THREADS;
+    for (uint32_t first = blockIdx.x * Q_THREADS + threadIdx.x; first < groups; first += U * stride) {
+        uint2 w[U];
+        int b[U];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                // sign, exponent and fraction in their places of an f16 are the value times 2^-14
-                const uint32_t n = w >> (4 * j) & 15u;
-                v[j] = __half2float(__ushort_as_half((unsigned short)((n & 8u) << 12 | (n & 7u) << 9))) * 16384.0f * p;
-            }
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(codes + i * 8);
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                // e4m3 likewise, times 2^-8; code 0x7F is a NaN
-                const uint32_t n = (j < 4 ? w.x : w.y) >> (8 * (j & 3)) & 255u;
-                v[j] = __half2float(__ushort_as_half((unsigned short)((n & 128u) << 8 | (n & 127u) << 7))) * 256.0f * p;
-                if ((n & 127u) == 127u) v[j] = __uint_as_float(0x7FFFFFFFu);
-            }
+        for (int u = 0; u < U; u++) {
+            const uint32_t i = first + u * stride < groups ? first + u * stride : first, row = by_row.of(i);
+            w[u] = E2M1 ? make_uint2(__ldg(reinterpret_cast<const uint32_t *>(codes) + i), 0u) : __ldg(reinterpret_cast<const uint2 *>(codes) + i);
+            b[u] = __ldg(scales + (int64_t)row * S + ((i - row * per_row) >> 2));
         }
-        store8(y + i * 8, v);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (first + u * stride >= groups) break;
+            const float p = mx_power(b[u]);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                // two codes to two f16, exactly (NaN codes included)
+                uint32_t h;
+                const uint32_t c = E2M1 ? w[u].x >> (8 * j) & 0xFFu : (j < 2 ? w[u].x : w[u].y) >> (16 * (j & 1)) & 0xFFFFu;
+                if (E2M1)
+                    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(c));
+                else
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+                v[2 * j] = half_lo(h) * p;
+                v[2 * j + 1] = half_hi(h) * p;
+            }
+            store8(y + (int64_t)(first + u * stride) * 8, v);
+        }
     }
 }
 
@@ -163,6 +189,29 @@ __device__ __forceinline__ Two two_rsqrt(Two a) {
     return fast_two_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
 }
 
+// Pairs of f32, an operation on both at once.
+__device__ __forceinline__ uint64_t pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 struct NormParams {
     const void *x, *res;
     const float *w;
@@ -173,39 +222,75 @@ struct NormParams {
     int K, S, y_bf16;
 };
 
-// One CTA per row (in turn).  Thread t holds the groups of 8 values t, t + T, .. (C of them at most)
-// from the load to the output, so that the row is read once.
-template <typename T, int C>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
+// One CTA per row (in turn).  Thread t holds the groups of 8 values t, t + T, .. (C of them at most) from the load to the
+// output, so that the row is read once, and their weights over all its rows.  What the codes are is decided
+// exactly, mostly without exact arithmetic: a scaled value h w r 2^(127 - b) formed in f32 is within 2^-22 of
+// itself, so if it gives the same code with 2^-21 more and with 2^-21 less (and so does the largest its scale), that is the
+// code; else (3 in 1000 times) the warp forms its values in two terms.  r, which all of them share, is in two terms always.
+template <typename T, int C, int MOST>
+__global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormParams p) {
     __shared__ Two part[32];
+    const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint64_t minus = pack(-1.0f, -1.0f);
     pdl_wait();
     pdl_launch_dependents();
-    const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float w[C][8];
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[c][i] = 1.0f;
+        const int g = threadIdx.x + c * blockDim.x;
+        if (p.w && g < groups) load8(p.w + g * 8, w[c]);
+    }
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         const T *res = static_cast<const T *>(p.res) + row * p.ldr;
         float h[C][8];
-        Two sum{0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
-            if (g >= groups) continue;
-            load8(x + g * 8, h[c]);
-            if (p.res) {
-                float r[8];
-                load8(res + g * 8, r);
 #pragma unroll
-                for (int i = 0; i < 8; i++) h[c][i] = sizeof(T) == 4 ? h[c][i] + r[i] : __bfloat162float(__float2bfloat16_rn(h[c][i] + r[i]));
+            for (int i = 0; i < 8; i++) h[c][i] = 0.0f;
+            if (g < groups) load8(x + g * 8, h[c]);
+        }
+        if (p.res) {
+            float r[C][8];
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const int g = threadIdx.x + c * blockDim.x;
+#pragma unroll
+                for (int i = 0; i < 8; i++) r[c][i] = 0.0f;
+                if (g < groups) load8(res + g * 8, r[c]);
             }
-            if (p.h) store8(static_cast<T *>(p.h) + row * p.ldh + g * 8, h[c]);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const Two sq = two_prod(h[c][i], h[c][i]);
-                const Two s = two_sum(sum.hi, sq.hi);
-                sum = {s.hi, sum.lo + (s.lo + sq.lo)};
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) h[c][i] = sizeof(T) == 4 ? h[c][i] + r[c][i] : __bfloat162float(__float2bfloat16_rn(h[c][i] + r[c][i]));
+        }
+        // the sum of squares in two terms, two values at a time: hi + lo, and what each addition to hi cuts off (the
+        // squares of bf16 values are exact; those of f32 values leave a second term too)
+        uint64_t hi = 0, lo = 0;
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const int g = threadIdx.x + c * blockDim.x;
+            if (p.h && g < groups) store8(static_cast<T *>(p.h) + row * p.ldh + g * 8, h[c]);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const uint64_t v = pack(h[c][i], h[c][i + 1]), neg = mul2(v, mul2(v, minus));       // -square
+                if (sizeof(T) == 4) lo = add2(lo, fma2(v, v, neg));
+                const uint64_t s = fma2(neg, minus, hi), t = fma2(hi, minus, s);                     // hi + square; what arrived of it
+                lo = add2(lo, fma2(fma2(t, minus, s), minus, hi));                                    // what hi lost
+                lo = fma2(add2(neg, t), minus, lo);                                                   // what the square lost
+                hi = s;
             }
         }
-        sum = fast_two_sum(sum.hi, sum.lo);
+        Two sum;
+        {
+            float a, b, d, e;
+            unpack(hi, a, b);
+            unpack(lo, d, e);
+            sum = add(fast_two_sum(a, d), fast_two_sum(b, e));
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
@@ -213,9 +298,9 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             if (lane == 0) part[warp] = sum;
             __syncthreads();
             sum = lane < warps ? part[lane] : Two{0.0f, 0.0f};
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
+            for (int d = 1; d < warps; d <<= 1)
                 sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+            sum = Two{__shfl_sync(0xffffffffu, sum.hi, 0), __shfl_sync(0xffffffffu, sum.lo, 0)};
             __syncthreads();
         }
         // mean = sum / K: the quotient of the first terms, and what it leaves over
@@ -228,28 +313,44 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             // a warp's lanes leave together but at the row's end, where whole blocks of four lanes do
             const bool live = g < groups;
             if (!__any_sync(0xffffffffu, live)) continue;
-            float w[8], odd[8], near[8];
-            if (p.w && live) {
-                load8(p.w + g * 8, w);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) w[i] = 1.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const Two y = mul(two_prod(live ? h[c][i] : 0.0f, w[i]), r);
-                near[i] = y.hi;
-                odd[i] = to_odd(y);
-            }
             if (p.y && live) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) y[i] = mul(two_prod(h[c][i], w[c][i]), r).hi;
                 if (p.y_bf16)
-                    store8(static_cast<__nv_bfloat16 *>(p.y) + row * p.K + g * 8, near);
+                    store8(static_cast<__nv_bfloat16 *>(p.y) + row * p.K + g * 8, y);
                 else
-                    store8(static_cast<float *>(p.y) + row * p.K + g * 8, near);
+                    store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
             }
             if (!p.codes) continue;
-            const int b = mx_scale_byte(block_amax(odd), false);
-            const uint2 code = codes8<false>(odd, mx_inverse(b));
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = h[c][i] * w[c][i];
+            const float most = __uint_as_float(block_amax(v)) * r.hi;
+            const uint32_t below = __float_as_uint(most * (1.0f - 0x1p-21f)), above = __float_as_uint(most * (1.0f + 0x1p-21f));
+            int b = mx_scale_byte(above, false);
+            const float inv = mx_inverse(b) * r.hi, less = inv * (1.0f - 0x1p-21f), more = inv * (1.0f + 0x1p-21f);
+            uint2 code, other;
+            {
+                uint32_t lo4[4], hi4[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    lo4[i] = e4m3x2(v[2 * i] * less, v[2 * i + 1] * less);
+                    hi4[i] = e4m3x2(v[2 * i] * more, v[2 * i + 1] * more);
+                }
+                code = make_uint2(lo4[0] | lo4[1] << 16, lo4[2] | lo4[3] << 16);
+                other = make_uint2(hi4[0] | hi4[1] << 16, hi4[2] | hi4[3] << 16);
+            }
+            // (tiny, infinite and NaN blocks too: there the f32 values are not that close)
+            const bool sure = code.x == other.x && code.y == other.y && mx_scale_byte(below, false) == b && b > 0 && b < 255 &&
+                              inv < 0x1p100f && r.hi > 0x1p-100f && most > 0x1p-90f;
+            if (__any_sync(0xffffffffu, live && !sure)) {
+                float odd[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) odd[i] = to_odd(mul(two_prod(h[c][i], w[c][i]), r));
+                b = mx_scale_byte(block_amax(odd), false);
+                code = codes8<false>(odd, mx_inverse(b));
+            }
             if (live) {
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = code;
                 if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = (uint8_t)b;
@@ -292,48 +393,66 @@ unsigned grid_for(int64_t work, int threads) {
     return (unsigned)std::min<int64_t>((work + threads - 1) / threads, (int64_t)sm_count() * (2048 / threads));
 }
 
-template <typename T, int C>
+template <typename T, int C, int MOST>
 gq_status norm_launch(const NormParams &p, int threads, cudaStream_t s) {
     NormParams q = p;
     void *args[] = {&q};
-    const int64_t fit = (int64_t)sm_count() * std::max(1, 2048 / threads);
-    return launch_pdl((const void *)rms_norm_kernel<T, C>, dim3((unsigned)std::min<int64_t>(p.M, fit)), dim3(threads), 0, s, args,
+    const int64_t fit = (int64_t)sm_count() * std::max(1, (C == 4 ? 640 : 1024) / threads);     // by the registers of each form
+    return launch_pdl((const void *)rms_norm_kernel<T, C, MOST>, dim3((unsigned)std::min<int64_t>(p.M, fit)), dim3(threads), 0, s, args,
                       "norm launch");
 }
 
 // One group of 8 values per thread keeps a lone row's chain short; where rows abound (several for each
-// SM) threads take up to four groups, for fewer and longer turns.
+// SM) threads take four groups, for fewer and longer turns, up to 256 of them.
 template <typename T>
 gq_status norm_width(const NormParams &p, cudaStream_t s) {
     const int groups = p.K / 8;
-    int c = p.M >= 4LL * sm_count() && groups >= 128 ? 4 : 1;
-    while (c < 4 && (groups + c - 1) / c > 1024) c *= 2;
+    int c = p.M >= 4LL * sm_count() && groups >= 128 && groups <= 1024 ? 4 : 1;
+    while ((groups + c - 1) / c > 1024) c *= 2;
     const int threads = ((groups + c - 1) / c + 31) / 32 * 32;
-    if (c == 1) return norm_launch<T, 1>(p, threads, s);
-    if (c == 2) return norm_launch<T, 2>(p, threads, s);
-    return norm_launch<T, 4>(p, threads, s);
+    if (c == 1) return norm_launch<T, 1, 1024>(p, threads, s);
+    if (c == 2) return norm_launch<T, 2, 1024>(p, threads, s);
+    return threads <= 256 ? norm_launch<T, 4, 256>(p, threads, s) : norm_launch<T, 4, 1024>(p, threads, s);
 }
 
 }  // namespace
 
 gq_status launch_quantize_mx(const void *x, int64_t ldx, bool bf16, bool e2m1, void *codes, uint8_t *scales, int64_t M,
                              int64_t K, cudaStream_t s) {
-    int per_row = (int)(K / 8), S = (int)gq_mx_scale_cols(K);
-    int64_t groups = M * per_row;
-    void *args[] = {&x, &ldx, &codes, &scales, &groups, &per_row, &S};
+    uint32_t per_row = (uint32_t)(K / 8);
+    int S = (int)gq_mx_scale_cols(K);
+    Divisor by_row = divisor(per_row);
+    const int64_t most = std::max<int64_t>(1, ((1LL << 30) - 1) / per_row);      // rows of a launch: 31-bit numbers of groups
     const void *fn = bf16 ? (e2m1 ? (const void *)quantize_mx_kernel<__nv_bfloat16, true> : (const void *)quantize_mx_kernel<__nv_bfloat16, false>)
                           : (e2m1 ? (const void *)quantize_mx_kernel<float, true> : (const void *)quantize_mx_kernel<float, false>);
-    return launch_pdl(fn, dim3(grid_for(groups, Q_THREADS)), dim3(Q_THREADS), 0, s, args, "mx quantize launch");
+    for (int64_t m = 0; m < M; m += most) {
+        uint32_t groups = (uint32_t)(std::min(most, M - m) * per_row);
+        const uint8_t *from = static_cast<const uint8_t *>(x) + m * ldx * (bf16 ? 2 : 4);
+        uint8_t *to = static_cast<uint8_t *>(codes) + m * K / (e2m1 ? 2 : 1), *to_scales = scales + m * S;
+        void *args[] = {&from, &ldx, &to, &to_scales, &groups, &per_row, &by_row, &S};
+        gq_status st = launch_pdl(fn, dim3(grid_for(groups, Q_THREADS)), dim3(Q_THREADS), 0, s, args, "mx quantize launch");
+        if (st != GQ_OK) return st;
+    }
+    return GQ_OK;
 }
 
 gq_status launch_dequantize_mx(const void *codes, const uint8_t *scales, bool e2m1, void *y, bool bf16, int64_t M,
                                int64_t K, cudaStream_t s) {
-    int per_row = (int)(K / 8), S = (int)gq_mx_scale_cols(K);
-    int64_t groups = M * per_row;
-    void *args[] = {&codes, &scales, &y, &groups, &per_row, &S};
+    uint32_t per_row = (uint32_t)(K / 8);
+    int S = (int)gq_mx_scale_cols(K);
+    Divisor by_row = divisor(per_row);
+    const int64_t most = std::max<int64_t>(1, ((1LL << 30) - 1) / per_row);
     const void *fn = bf16 ? (e2m1 ? (const void *)dequantize_mx_kernel<__nv_bfloat16, true> : (const void *)dequantize_mx_kernel<__nv_bfloat16, false>)
                           : (e2m1 ? (const void *)dequantize_mx_kernel<float, true> : (const void *)dequantize_mx_kernel<float, false>);
-    return launch_pdl(fn, dim3(grid_for(groups, Q_THREADS)), dim3(Q_THREADS), 0, s, args, "mx dequantize launch");
+    for (int64_t m = 0; m < M; m += most) {
+        uint32_t groups = (uint32_t)(std::min(most, M - m) * per_row);
+        const uint8_t *from = static_cast<const uint8_t *>(codes) + m * K / (e2m1 ? 2 : 1), *from_scales = scales + m * S;
+        uint8_t *to = static_cast<uint8_t *>(y) + m * K * (bf16 ? 2 : 4);
+        void *args[] = {&from, &from_scales, &to, &groups, &per_row, &by_row, &S};
+        gq_status st = launch_pdl(fn, dim3(grid_for(groups, Q_THREADS)), dim3(Q_THREADS), 0, s, args, "mx dequantize launch");
+        if (st != GQ_OK) return st;
+    }
+    return GQ_OK;
 }
 
 gq_status launch_repack_mxfp4(const void *codes, const uint8_t *scales, void *rep, int64_t count, int64_t N, int64_t K,

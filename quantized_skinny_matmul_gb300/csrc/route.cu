@@ -4,13 +4,15 @@
 // 32-bit keys, one warp-wide maximum and one minimum of indices per chosen expert.  Without a bias
 // the order of the scores is the order of the logits, which are exact.  With one (and for the groups'
 // sums) the f32 values carry a rounding error: where two values that decide something are closer than
-// its bound, the warp does the token again in 64 bits (a few tokens in ten thousand).
+// its bound (about one token in a hundred with a bias), the warp takes the 32 best candidates, one per lane, and
+// ranks them by their values in 64 bits; where that does not settle it (the groups' sums are close, or more than
+// 32 candidates are), it does the whole token in 64 bits.
 //
 // The plan is a counting sort, stable in the tokens.  Up to 32 tokens: one CTA does all of it.  More:
 // each CTA counts the choices of its chunk of tokens per expert into the workspace (about one chunk
 // per SM, so that the counts of all chunks, which every CTA of the second kernel reads, stay small), and the
 // second kernel places each chunk's choices behind those of the chunks before it.  No atomics on
-// memory, so nothing depends on timing.
+// memory, so nothing depends on timing.  Both are bound by instructions, not by memory.
 #include <algorithm>
 
 #include "mx.cuh"
@@ -31,6 +33,7 @@ struct RouteParams {
     unsigned int *status;
     int64_t ldl;
     int E, k, T, chunk, sigmoid, groups, top_groups, group_best, renormalize, bf16;
+    int lanes;                       // that look through a group
     float factor;
 };
 
@@ -60,151 +63,249 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// Which groups take part, as a bit each, from the choice values c[e] in shared memory: lane g looks
-// through group g.  `gap` receives the distance between the worst group that does and the best that
-// does not.
+// The two largest of two pairs.
 template <typename F>
-__device__ __forceinline__ uint32_t best_groups(const F *c, int E, int groups, int top, int best, int lane, F &gap) {
-    const int n = E / groups;
+__device__ __forceinline__ void best_two(F &a, F &b, F c, F d) {
+    const F lo = a < c ? a : c;
+    a = a < c ? c : a;
+    b = b < d ? d : b;
+    b = lo < b ? b : lo;
+}
+
+// Which groups take part, as a bit each, from the choice values in shared memory.  32 / P lanes look through a group, P the
+// power of two from `groups` on; expert e's value is at e + (e / n) * (32 / P), so that lanes of different groups use
+// different banks.  `gap` receives the distance between the worst group that takes part and the best that does not.
+template <typename F>
+__device__ __forceinline__ uint32_t best_groups(const F *c, int n, int groups, int lanes, int top, int best, int lane, F &gap) {
     const F none = -(F)INFINITY;
+    const int g = lane / lanes;
     F a = none, b = none;
-    if (lane < groups)
-        for (int j = 0; j < n; j++) {
-            int at = j + lane;                       // a start of its own: no two lanes in one bank
-            if (at >= n) at %= n;
-            const F v = c[lane * n + at];
-            b = v > a ? a : v > b ? v : b;
-            a = v > a ? v : a;
-        }
+    if (g < groups)
+        for (int j = lane % lanes; j < n; j += lanes) best_two<F>(a, b, c[g * (n + lanes) + j], none);
+    for (int d = 1; d < lanes; d <<= 1) {
+        const F oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
+        best_two<F>(a, b, oa, ob);
+    }
     const F value = best == 2 && n > 1 ? a + b : a;
     int rank = 0;
-    for (int g = 0; g < groups; g++) {
-        const F v = __shfl_sync(0xffffffffu, value, g);
-        rank += v > value || (v == value && g < lane);
+    for (int h = 0; h < groups; h++) {
+        const F v = __shfl_sync(0xffffffffu, value, h * lanes);
+        rank += v > value || (v == value && h < g);
     }
-    const bool in = lane < groups && rank < top;
-    F worst = in ? value : (F)INFINITY, other = !in && lane < groups ? value : none;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const F w = __shfl_xor_sync(0xffffffffu, worst, d), o = __shfl_xor_sync(0xffffffffu, other, d);
-        worst = w < worst ? w : worst;
-        other = o > other ? o : other;
-    }
-    gap = worst - other;
-    return __ballot_sync(0xffffffffu, in);
+    const bool in = g < groups && rank < top;
+    // ranks are all different: the worst that takes part has rank top - 1, the best other rank top
+    const uint32_t w = __ballot_sync(0xffffffffu, g < groups && rank == top - 1), o = __ballot_sync(0xffffffffu, g < groups && rank == top);
+    gap = __shfl_sync(0xffffffffu, value, __ffs((int)w) - 1) - __shfl_sync(0xffffffffu, value, __ffs((int)o) - 1);
+    // one bit per group
+    uint32_t bits = __ballot_sync(0xffffffffu, in), out = 0;
+    if (lanes == 1) return bits;
+    for (int h = 0; h < groups; h++) out |= (bits >> (h * lanes) & 1u) << h;
+    return out;
 }
 
-// One token.  Lane j < k returns the j-th choice (its expert and logit); m and the sum of exponentials as
-// the caller computed them.  F is float (with the checks of close values: `close` is set) or double.
-template <int V, typename F>
-__device__ __forceinline__ void choose(const RouteParams &p, const float (&z)[V], float m, F sum, F *shared, int lane, int &id,
-                                       float &zid, bool &close) {
-    constexpr bool FAST = sizeof(F) == 4;
-    auto score = [&](float x) -> F {
-        if (p.sigmoid) return (F)1 / ((F)1 + (FAST ? (F)expf(-x) : (F)exp(-(double)x)));
-        return m == -INFINITY ? (F)0 : (FAST ? (F)expf(x - m) : (F)exp((double)x - (double)m)) / sum;
-    };
-    const bool grouped = p.top_groups < p.groups;
-    // bounds of the f32 errors: a score's relative one, and a sum's
-    const F rel = p.sigmoid ? (F)0x1p-21 : (F)0x1p-18;
-    const F most = p.sigmoid ? (F)1 : m == -INFINITY ? (F)0 : (F)1 / sum;
+__device__ __forceinline__ double score64(const RouteParams &p, float z, float m, double sum) {
+    if (p.sigmoid) return 1.0 / (1.0 + exp(-(double)z));
+    return m == -INFINITY ? 0.0 : exp((double)z - (double)m) / sum;
+}
+
+__device__ __forceinline__ float logit(const RouteParams &p, int64_t t, int e) {
+    const float z = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[t * p.ldl + e])
+                           : static_cast<const float *>(p.logits)[t * p.ldl + e];
+    return isnan(z) ? -INFINITY : z;
+}
+
+// The sum of the exponentials of token t, in 64 bits.
+__device__ __noinline__ double sum64(const RouteParams &p, int64_t t, float m, int lane) {
+    double sum = 0.0;
+    if (p.sigmoid || m == -INFINITY) return 1.0;
+    for (int e = lane; e < p.E; e += 32) sum += exp((double)logit(p, t, e) - (double)m);
+    return warp_sum(sum);
+}
+
+// Token t in 64 bits, from the start; lane j < k returns the j-th choice.  An expert's value is computed again for each
+// choice: this path is for few tokens, and short.
+__device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, double sum, double *shared, int lane) {
     uint32_t allowed = 0xffffffffu;
-    F c[V];
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-        const int e = i * 32 + lane;
-        // without a bias, and where no sums are compared, the logits decide
-        c[i] = p.bias ? (e < p.E ? score(z[i]) + (F)p.bias[e] : (F)0) : (F)z[i];
+    const int n = p.E / p.groups;
+    if (p.top_groups < p.groups) {
+        for (int e = lane; e < p.E; e += 32) {
+            const float z = logit(p, t, e);
+            // without a bias, and where no sums are compared, the logits decide
+            shared[e + e / n * p.lanes] = p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : p.group_best == 2 ? score64(p, z, m, sum) : (double)z;
+        }
+        __syncwarp();
+        double gap;
+        allowed = best_groups<double>(shared, n, p.groups, p.lanes, p.top_groups, p.group_best, lane, gap);
+        __syncwarp();
     }
+    uint64_t last_key = ~0ull;
+    int last = -1, id = -1;
+    for (int j = 0; j < p.k; j++) {
+        uint64_t key = 0;
+        int at = 0x7fffffff;
+        for (int e = lane; e < p.E; e += 32) {
+            if (!(allowed >> (e / n) & 1u)) continue;
+            const float z = logit(p, t, e);
+            const uint64_t c = order64((p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : (double)z) + 0.0);
+            // behind the last choice in the order of values, then indices
+            if ((c < last_key || (c == last_key && e > last)) && c > key) key = c, at = e;
+        }
+        const uint64_t top = warp_max64(key);
+        const int e = (int)__reduce_min_sync(0xffffffffu, key == top ? (uint32_t)at : 0x7fffffffu);
+        if (lane == j) id = e;
+        last_key = top;
+        last = e;
+    }
+    return id;
+}
+
+// One token.  Lane j < k returns the j-th choice.  z: the lane's logits; m and sum: their maximum and the sum of the
+// exponentials (softmax); bias, group: of the lane's experts.
+template <int V>
+__device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const float (&z)[V], const float (&bias)[V], const int (&group)[V], float m,
+                                      float sum, double *shared, int lane) {
+    const bool grouped = p.top_groups < p.groups, sums = !p.bias && p.group_best == 2;
+    const float inverse = p.sigmoid ? 1.0f : m == -INFINITY ? 0.0f : 1.0f / sum;
+    // The fast exponential and reciprocal: a sigmoid is off by 2e-7 at most; a softmax score by its rounded argument and
+    // sum, 2^-18 of the largest score at most.  Two values that differ by more than `tol` (and the rounding of the sums
+    // with a bias) are in order.
+    const float tol = p.sigmoid ? 0x1p-20f : inverse * 0x1p-17f;
+    auto score = [&](float x) {
+        float e, r;
+        if (p.sigmoid) {
+            asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+            asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+            return r;
+        }
+        if (m == -INFINITY) return 0.0f;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"((x - m) * 1.4426950408889634f));
+        return e * inverse;
+    };
+    float c[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) c[i] = p.bias ? score(z[i]) + bias[i] : z[i];
+    uint32_t allowed = 0xffffffffu;
     if (grouped) {
-        const bool sums = !p.bias && p.group_best == 2;
+        float *values = reinterpret_cast<float *>(shared);
 #pragma unroll
         for (int i = 0; i < V; i++)
-            if (i * 32 + lane < p.E) shared[i * 32 + lane] = sums ? score(z[i]) : c[i];
+            if (i * 32 + lane < p.E) values[i * 32 + lane + group[i] * p.lanes] = sums ? score(z[i]) : c[i];
         __syncwarp();
-        F gap;
-        allowed = best_groups<F>(shared, p.E, p.groups, p.top_groups, p.group_best, lane, gap);
+        float gap;
+        allowed = best_groups<float>(values, p.E / p.groups, p.groups, p.lanes, p.top_groups, p.group_best, lane, gap);
         __syncwarp();
-        if (FAST && (p.bias || sums)) {
-            float size = 0.0f;                       // the largest magnitude among the biases
+        if (p.bias || sums) {
+            float size = 0.0f;
             if (p.bias)
 #pragma unroll
-                for (int i = 0; i < V; i++)
-                    if (i * 32 + lane < p.E) size = fmaxf(size, fabsf((float)c[i]));
+                for (int i = 0; i < V; i++) size = fmaxf(size, fabsf(c[i]));
             size = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
-            close |= !((float)gap > 4.0f * (float)(rel * most) + 0x1p-20f * size);
+            if (!(gap > 2.0f * tol + 0x1p-20f * size)) return choose64(p, t, m, sum64(p, t, m, lane), shared, lane);
         }
     }
-    const int per_group = p.E / p.groups;
-    using Key = typename std::conditional<FAST, uint32_t, uint64_t>::type;
-    Key key[V];
+    uint32_t key[V], best = 0;
+    int at = 0;
 #pragma unroll
     for (int i = 0; i < V; i++) {
-        const int e = i * 32 + lane;
-        const bool in = e < p.E && (!grouped || (allowed >> (e / per_group) & 1u));
-        if constexpr (FAST)
-            key[i] = in ? order32(c[i] + 0.0f) : 0u;
-        else
-            key[i] = in ? order64(c[i] + 0.0) : 0ull;
+        key[i] = i * 32 + lane < p.E && (allowed >> group[i] & 1u) ? order32(c[i] + 0.0f) : 0u;
+        if (key[i] > best) best = key[i], at = i;
     }
-    Key best = 0;
-    int at = 0;
-    auto local = [&] {
-        best = 0;
+    int id = -1;
+    float value = 0.0f;                       // of the lane's candidate
+    int found = 0;
+    auto next = [&] {                         // the best that is left goes to lane `found`; false if there is none
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0) return false;
+        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
+        if (lane == found) id = e, value = unorder32(top);
+        if (lane == (e & 31)) {
+            best = 0;
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            if (key[i] > best) best = key[i], at = i;
-    };
-    local();
-    float before = INFINITY;
-    for (int j = 0; j <= p.k; j++) {
-        // the choice after the last only says how far it is from it
-        if (j == p.k && !(FAST && p.bias)) break;
-        Key top;
-        if constexpr (FAST)
-            top = __reduce_max_sync(0xffffffffu, best);
-        else
-            top = warp_max64(best);
-        if (top == 0) break;
-        if constexpr (FAST) {
-            if (p.bias) {
-                const float v = unorder32(top);
-                close |= !(before - v > 2.0f * (float)(rel * most) + 0x1p-21f * (fabsf(v) + (j ? fabsf(before) : 0.0f)));
-                before = v;
+            for (int i = 0; i < V; i++) {
+                if (i == (e >> 5)) key[i] = 0;
+                if (key[i] > best) best = key[i], at = i;
             }
         }
-        if (j == p.k) break;
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-        float mine = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            if (i == (e >> 5)) mine = z[i];
-        const float chosen = __shfl_sync(0xffffffffu, mine, e & 31);
-        if (lane == j) id = e, zid = chosen;
-        if (lane == (e & 31)) {
-#pragma unroll
-            for (int i = 0; i < V; i++)
-                if (i == (e >> 5)) key[i] = 0;
-            local();
-        }
         __syncwarp();
+        found++;
+        return true;
+    };
+    while (found < p.k && next()) {
     }
+    if (!p.bias) return id;
+    // the choice after the last says how far it is from it
+    const int chosen = found;
+    const bool one_more = found < 32 && next();
+    float after = __shfl_down_sync(0xffffffffu, value, 1);
+    if (chosen == 32) {                       // (all lanes are taken: the best that is left)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (lane == 31) after = top ? unorder32(top) : -INFINITY;
+    } else if (!one_more && lane == chosen - 1) {
+        after = -INFINITY;
+    }
+    const bool close = lane < chosen && !(value - after > tol + 0x1p-21f * (fabsf(value) + (after > -INFINITY ? fabsf(after) : 0.0f)));
+    if (!__any_sync(0xffffffffu, close)) return id;
+    // 32 candidates, ranked by their values in 64 bits
+    while (found < 32 && next()) {
+    }
+    const double s = sum64(p, t, m, lane);
+    double exact = -INFINITY;
+    if (lane < found) exact = score64(p, logit(p, t, id), m, s) + (double)p.bias[id];
+    int rank = 0;
+    for (int j = 0; j < found; j++) {
+        const double v = __shfl_sync(0xffffffffu, exact, j);
+        const int e = __shfl_sync(0xffffffffu, id, j);
+        rank += v > exact || (v == exact && e < id);
+    }
+    // what was not taken is below the last candidate's f32 value: it must not reach up to the last choice
+    const uint32_t left = __reduce_max_sync(0xffffffffu, best);
+    if (left) {
+        const uint32_t w = __ballot_sync(0xffffffffu, lane < found && rank == p.k - 1);
+        const double lowest = __shfl_sync(0xffffffffu, exact, __ffs((int)w) - 1);
+        const float most = unorder32(left);
+        if (!(lowest - (double)most > (double)(tol + 0x1p-21f * (fabsf(most) + fabsf((float)lowest))))) return choose64(p, t, m, s, shared, lane);
+    }
+    // to the lanes of their ranks
+    int out = -1;
+    for (int j = 0; j < found; j++) {
+        const int r = __shfl_sync(0xffffffffu, rank, j), e = __shfl_sync(0xffffffffu, id, j);
+        if (r == lane && lane < p.k) out = e;
+    }
+    return out;
 }
 
-// Stable places for n choices in order (32 at a time, by one warp): base[e] is where expert e's next row goes.
-__device__ __forceinline__ void place(const int32_t *ids, int n, int64_t first, int k, int32_t *base, int32_t *rows,
-                                      int32_t *pos, int lane) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        const int e = i < n ? ids[i] : -1;
+// Stable places for n choices in order, by all warps of the CTA; base[e] is where expert e's next row goes, and per_warp has room for
+// a byte per expert and warp.  Each warp ranks 32 choices among themselves and counts them per expert; a prefix over
+// the warps' counts gives each its base.
+__device__ __forceinline__ void place(const int32_t *ids, int n, int64_t first, int k, int E, int32_t *base, uint8_t *per_warp, int32_t *rows,
+                                      int32_t *pos) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    for (int i0 = 0; i0 < n; i0 += blockDim.x) {
+        for (int j = threadIdx.x; j < (warps * E + 3) / 4; j += blockDim.x) reinterpret_cast<uint32_t *>(per_warp)[j] = 0;
+        __syncthreads();
+        const int i = i0 + threadIdx.x, e = i < n ? ids[i] : -1;
         const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const int r = e < 0 ? -1 : base[e] + __popc(same & ((1u << lane) - 1u));
-        __syncwarp();
-        if (e >= 0 && (same >> lane) == 1u) base[e] = r + 1;      // the last lane of its expert
-        __syncwarp();
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        if (e >= 0 && rank == 0) per_warp[warp * E + e] = (uint8_t)__popc(same);
+        __syncthreads();
+        int at = 0;
+        if (e >= 0) {
+            at = base[e];
+            for (int w = 0; w < warp; w++) at += per_warp[w * E + e];
+        }
         if (i < n) {
-            pos[first + i] = r;
-            if (r >= 0) rows[r] = (int32_t)((first + i) / k);
+            pos[first + i] = e < 0 ? -1 : at + rank;
+            if (e >= 0) rows[at + rank] = (int32_t)((uint32_t)(first + i) / (uint32_t)k);
+        }
+        if (i0 + (int)blockDim.x < n) {
+            __syncthreads();
+            // the last warp of each expert moves its base
+            for (int x = threadIdx.x; x < E; x += blockDim.x) {
+                int all = 0;
+                for (int w = 0; w < warps; w++) all += per_warp[w * E + x];
+                base[x] += all;
+            }
+            __syncthreads();
         }
     }
 }
@@ -244,10 +345,17 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
     const int words = (p.E + 3) / 4 * 4;
     int32_t *list = counts + words;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    double *shared = reinterpret_cast<double *>(list + (p.pos ? (SOLO_TOKENS * p.k + 3) / 4 * 4 : 0)) + (size_t)warp * p.E;
+    // choice values by group, for warps that need them: E and a few more per group
+    double *shared = reinterpret_cast<double *>(list + (p.pos ? (SOLO_TOKENS * p.k + 3) / 4 * 4 : 0)) + (size_t)warp * (p.E + p.groups * p.lanes);
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) counts[e] = 0;
+    int group[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) group[i] = (i * 32 + lane) / (p.E / p.groups) & 31;
     pdl_wait();
     pdl_launch_dependents();
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) bias[i] = p.bias && i * 32 + lane < p.E ? p.bias[i * 32 + lane] : 0.0f;
     __syncthreads();
     const int used = tokens_used(p.used, p.T, p.status);
     const int t0 = blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
@@ -259,12 +367,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
             float z[V], m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                const int e = i * 32 + lane;
-                z[i] = -INFINITY;
-                if (e < p.E)
-                    z[i] = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[t * p.ldl + e])
-                                  : static_cast<const float *>(p.logits)[t * p.ldl + e];
-                if (isnan(z[i])) z[i] = -INFINITY;
+                z[i] = i * 32 + lane < p.E ? logit(p, t, i * 32 + lane) : -INFINITY;
                 m = fmaxf(m, z[i]);
             }
             float sum = 1.0f;
@@ -277,26 +380,11 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
                     sum = warp_sum(sum);
                 }
             }
-            float zid = -INFINITY;
-            bool close = false;
-            choose<V, float>(p, z, m, sum, reinterpret_cast<float *>(shared), lane, id, zid, close);
-            if (__any_sync(0xffffffffu, close)) {
-                double sum64 = 1.0;
-                if (!p.sigmoid && m > -INFINITY) {
-                    sum64 = 0.0;
-#pragma unroll 1
-                    for (int i = 0; i < V; i++) {
-                        float x = 0.0f;
-#pragma unroll
-                        for (int u = 0; u < V; u++)
-                            if (u == i) x = z[u];
-                        sum64 += exp((double)x - (double)m);
-                    }
-                    sum64 = warp_sum(sum64);
-                }
-                choose<V, double>(p, z, m, sum64, shared, lane, id, zid, close);
+            id = choose<V>(p, t, z, bias, group, m, sum, shared, lane);
+            if (lane < p.k) {
+                const float chosen = logit(p, t, id);
+                w = p.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : m > -INFINITY ? expf(chosen - m) / sum : 0.0f;
             }
-            if (lane < p.k) w = p.sigmoid ? 1.0f / (1.0f + expf(-zid)) : m > -INFINITY ? expf(zid - m) / sum : 0.0f;
             if (p.renormalize) {
                 const float all = warp_sum(w);
                 if (all > 0.0f) w /= all;
@@ -313,54 +401,63 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
     if (!counted) return;
     __syncthreads();
     if (p.pos) {
-        if (warp != 0) return;
-        const int total = scan(counts, p.E, lane);
-        for (int e = lane; e < p.E; e += 32) p.offsets[e] = counts[e];
-        if (lane == 0) p.offsets[p.E] = total;
-        __syncwarp();
-        place(list, (t1 - t0) * p.k, 0, p.k, counts, p.rows, p.pos, lane);
+        if (warp == 0) {
+            const int total = scan(counts, p.E, lane);
+            for (int e = lane; e < p.E; e += 32) p.offsets[e] = counts[e];
+            if (lane == 0) p.offsets[p.E] = total;
+        }
+        __syncthreads();
+        // (the choices are made: the groups' room serves the warps' counts)
+        place(list, (t1 - t0) * p.k, 0, p.k, p.E, counts, reinterpret_cast<uint8_t *>(list + (SOLO_TOKENS * p.k + 3) / 4 * 4), p.rows, p.pos);
     } else {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.counts[(int64_t)blockIdx.x * p.E + e] = counts[e];
     }
 }
 
-// CTA c places the choices of chunk c.
-__global__ void __launch_bounds__(256) plan_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
-                                                   int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
-                                                   int32_t *__restrict__ pos, int E, int k, int T, int chunk, int chunks) {
+// CTA c places the choices of chunk c.  Four threads sum an expert's counts over the chunks.
+constexpr int PLAN_THREADS = 512;
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
+                                                            int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
+                                                            int32_t *__restrict__ pos, int E, int k, int T, int chunk, int chunks) {
     extern __shared__ __align__(16) uint8_t smem[];
     int32_t *base = reinterpret_cast<int32_t *>(smem), *before = base + E;
+    uint8_t *per_warp = reinterpret_cast<uint8_t *>(before + E);
+    for (int e = threadIdx.x; e < 2 * E; e += PLAN_THREADS) base[e] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    for (int e = threadIdx.x; e < E; e += 256) {
+    __syncthreads();
+    const int parts = max(1, PLAN_THREADS / E);
+    for (int x = threadIdx.x; x < E * parts; x += PLAN_THREADS) {
+        const int e = x % E, part = x / E;
         int all = 0, mine = 0;
 #pragma unroll 8
-        for (int c = 0; c < chunks; c++) {
+        for (int c = part; c < chunks; c += parts) {
             const int v = counts[(int64_t)c * E + e];
             all += v;
             mine += c < (int)blockIdx.x ? v : 0;
         }
-        base[e] = all;
-        before[e] = mine;
+        atomicAdd(&base[e], all);
+        atomicAdd(&before[e], mine);
     }
     __syncthreads();
-    if (threadIdx.x >= 32) return;
-    const int lane = threadIdx.x;
-    const int total = scan(base, E, lane);
-    for (int e = lane; e < E; e += 32) {
-        if (blockIdx.x == 0) offsets[e] = base[e];
-        base[e] += before[e];
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, total = scan(base, E, lane);
+        for (int e = lane; e < E; e += 32) {
+            if (blockIdx.x == 0) offsets[e] = base[e];
+            base[e] += before[e];
+        }
+        if (blockIdx.x == 0 && lane == 0) offsets[E] = total;
     }
-    if (blockIdx.x == 0 && lane == 0) offsets[E] = total;
-    __syncwarp();
+    __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * chunk * k;
     const int n = (min((int)(blockIdx.x + 1) * chunk, T) - (int)blockIdx.x * chunk) * k;
-    place(ids + first, n, first, k, base, rows, pos, lane);
+    place(ids + first, n, first, k, E, base, per_warp, rows, pos);
 }
 
 template <int V>
 gq_status route_launch(RouteParams p, int chunks, size_t fixed, cudaStream_t s) {
-    const size_t per_warp = p.top_groups < p.groups ? (size_t)p.E * 8 : 0;
+    // values by group in 64 bits; the solo CTA's counts of each warp (a byte per expert) lie over them
+    const size_t per_warp = p.top_groups < p.groups ? (size_t)(p.E + p.groups * p.lanes) * 8 : p.pos ? (size_t)(p.E + 7) / 4 * 4 : 0;
     int warps = std::min(route_threads(V) / 32, p.chunk);
     if (per_warp) warps = std::max<int>(1, std::min<int64_t>(warps, (int64_t)((48 * 1024 - fixed) / per_warp)));
     warps = (p.chunk + (p.chunk + warps - 1) / warps - 1) / ((p.chunk + warps - 1) / warps);   // as many turns, no idle warps
@@ -377,6 +474,9 @@ gq_status launch_route(const gq_router &r, const void *logits, int64_t ldl, bool
     p.E = (int)r.E, p.k = (int)r.top_k, p.T = (int)T, p.sigmoid = r.score == GQ_SCORE_SIGMOID;
     p.groups = (int)r.groups, p.top_groups = (int)r.top_groups, p.group_best = (int)r.group_best;
     p.renormalize = r.renormalize != 0, p.bf16 = bf16, p.factor = r.factor;
+    int P = 1;
+    while (P < p.groups) P *= 2;
+    p.lanes = 32 / P;
     p.status = device_status_word();
     if (!p.status) return fail(GQ_ERR_CUDA, "device status word unavailable");
     const bool solo = pos && T <= SOLO_TOKENS;
@@ -402,7 +502,7 @@ gq_status launch_route(const gq_router &r, const void *logits, int64_t ldl, bool
     int E = p.E, k = p.k, TT = p.T, chunk = p.chunk, nch = chunks;
     const int32_t *cids = ids, *counts = p.counts;
     void *args[] = {&cids, &counts, &offsets, &rows, &pos, &E, &k, &TT, &chunk, &nch};
-    return launch_pdl((const void *)plan_kernel, dim3(chunks), dim3(256), (size_t)E * 8, s, args, "plan launch");
+    return launch_pdl((const void *)plan_kernel, dim3(chunks), dim3(PLAN_THREADS), (size_t)E * 8 + (size_t)E * (PLAN_THREADS / 32) + 16, s, args, "plan launch");
 }
 
 }  // namespace gq
