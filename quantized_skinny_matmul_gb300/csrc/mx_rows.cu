@@ -189,29 +189,6 @@ __device__ __forceinline__ Two two_rsqrt(Two a) {
     return fast_two_sum(r, r * fmaf(0.375f * e, e, 0.5f * e));
 }
 
-// Pairs of f32, an operation on both at once.
-__device__ __forceinline__ uint64_t pack(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 struct NormParams {
     const void *x, *res;
     const float *w;
@@ -222,132 +199,125 @@ struct NormParams {
     int K, S, y_bf16;
 };
 
+// Group g of 8 values of h = x + residual, rounded to T.
+template <typename T>
+__device__ __forceinline__ void load_h(const T *x, const T *res, int g, float (&h)[8]) {
+    load8(x + g * 8, h);
+    if (!res) return;
+    float r[8];
+    load8(res + g * 8, r);
+#pragma unroll
+    for (int i = 0; i < 8; i++) h[i] = sizeof(T) == 4 ? h[i] + r[i] : __bfloat162float(__float2bfloat16_rn(h[i] + r[i]));
+}
+
+// 1 / sqrt(mean(h^2) + eps) of a row in two terms, by one warp.
+template <typename T>
+__device__ __noinline__ Two exact_r(const NormParams &p, const T *x, const T *res, int lane) {
+    Two sum{0.0f, 0.0f};
+    for (int g = lane; g < p.K / 8; g += 32) {
+        float h[8];
+        load_h(x, res, g, h);
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum = add(sum, two_prod(h[i], h[i]));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+    // mean = sum / K: the quotient of the first terms, and what it leaves over
+    const float k = (float)p.K, q = sum.hi / k;
+    return two_rsqrt(add(fast_two_sum(q, (fmaf(-q, k, sum.hi) + sum.lo) / k), Two{p.eps_hi, p.eps_lo}));
+}
+
 // One CTA per row (in turn).  Thread t holds the groups of 8 values t, t + T, .. (C of them at most) from the load to the
-// output, so that the row is read once, and their weights over all its rows.  What the codes are is decided
-// exactly, mostly without exact arithmetic: a scaled value h w r 2^(127 - b) formed in f32 is within 2^-22 of
-// itself, so if it gives the same code with 2^-21 more and with 2^-21 less (and so does the largest its scale), that is the
-// code; else (3 in 1000 times) the warp forms its values in two terms.  r, which all of them share, is in two terms always.
-template <typename T, int C, int MOST>
-__global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormParams p) {
-    __shared__ Two part[32];
+// output, so that the row is read once.  The codes are those of the exact y, mostly without exact arithmetic.
+// In f32, with positive terms only, the sum of squares is off by 17 roundings at most (4 additions in a thread, 3 levels
+// there, 5 in the warp, 5 over the warps), which counts half in r, and a scaled value h w r 2^(127 - b) by 14 in
+// all, less than 2^-20 of itself.  So if it gives the same code with 2^-20 more and with 2^-20 less (and so does the
+// largest its scale), that is the code; else (one group of 256 values in 200) the warp forms r and its values in
+// two terms, reading the row again.
+template <typename T, int C>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
+    __shared__ float part[32];
     const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const uint64_t minus = pack(-1.0f, -1.0f);
     pdl_wait();
     pdl_launch_dependents();
-    float w[C][8];
-#pragma unroll
-    for (int c = 0; c < C; c++) {
-#pragma unroll
-        for (int i = 0; i < 8; i++) w[c][i] = 1.0f;
-        const int g = threadIdx.x + c * blockDim.x;
-        if (p.w && g < groups) load8(p.w + g * 8, w[c]);
-    }
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
-        const T *res = static_cast<const T *>(p.res) + row * p.ldr;
+        const T *res = p.res ? static_cast<const T *>(p.res) + row * p.ldr : nullptr;
         float h[C][8];
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
 #pragma unroll
             for (int i = 0; i < 8; i++) h[c][i] = 0.0f;
-            if (g < groups) load8(x + g * 8, h[c]);
+            if (g < groups) load_h(x, res, g, h[c]);
         }
-        if (p.res) {
-            float r[C][8];
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                const int g = threadIdx.x + c * blockDim.x;
-#pragma unroll
-                for (int i = 0; i < 8; i++) r[c][i] = 0.0f;
-                if (g < groups) load8(res + g * 8, r[c]);
-            }
-#pragma unroll
-            for (int c = 0; c < C; c++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) h[c][i] = sizeof(T) == 4 ? h[c][i] + r[c][i] : __bfloat162float(__float2bfloat16_rn(h[c][i] + r[c][i]));
-        }
-        // the sum of squares in two terms, two values at a time: hi + lo, and what each addition to hi cuts off (the
-        // squares of bf16 values are exact; those of f32 values leave a second term too)
-        uint64_t hi = 0, lo = 0;
+        float sq[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
             if (p.h && g < groups) store8(static_cast<T *>(p.h) + row * p.ldh + g * 8, h[c]);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const uint64_t v = pack(h[c][i], h[c][i + 1]), neg = mul2(v, mul2(v, minus));       // -square
-                if (sizeof(T) == 4) lo = add2(lo, fma2(v, v, neg));
-                const uint64_t s = fma2(neg, minus, hi), t = fma2(hi, minus, s);                     // hi + square; what arrived of it
-                lo = add2(lo, fma2(fma2(t, minus, s), minus, hi));                                    // what hi lost
-                lo = fma2(add2(neg, t), minus, lo);                                                   // what the square lost
-                hi = s;
-            }
+            for (int i = 0; i < 8; i++) sq[i] = fmaf(h[c][i], h[c][i], sq[i]);
         }
-        Two sum;
-        {
-            float a, b, d, e;
-            unpack(hi, a, b);
-            unpack(lo, d, e);
-            sum = add(fast_two_sum(a, d), fast_two_sum(b, e));
-        }
+        float sum = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (warps > 1) {
             if (lane == 0) part[warp] = sum;
             __syncthreads();
-            sum = lane < warps ? part[lane] : Two{0.0f, 0.0f};
-            for (int d = 1; d < warps; d <<= 1)
-                sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
-            sum = Two{__shfl_sync(0xffffffffu, sum.hi, 0), __shfl_sync(0xffffffffu, sum.lo, 0)};
-            __syncthreads();
+            sum = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
-        // mean = sum / K: the quotient of the first terms, and what it leaves over
-        const float k = (float)p.K, q = sum.hi / k;
-        const Two mean = fast_two_sum(q, (fmaf(-q, k, sum.hi) + sum.lo) / k);
-        const Two r = two_rsqrt(add(mean, Two{p.eps_hi, p.eps_lo}));
+        const float mean = sum / (float)p.K + p.eps_hi;
+        float r;
+        asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(mean));
+        r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.0f), r);          // to a unit
+        bool exact = false;
+        Two r2;
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
             // a warp's lanes leave together but at the row's end, where whole blocks of four lanes do
             const bool live = g < groups;
             if (!__any_sync(0xffffffffu, live)) continue;
+            float w[8], v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = 1.0f;
+            if (p.w && live) load8(p.w + g * 8, w);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = h[c][i] * w[i];
             if (p.y && live) {
                 float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) y[i] = mul(two_prod(h[c][i], w[c][i]), r).hi;
+                for (int i = 0; i < 8; i++) y[i] = v[i] * r;
                 if (p.y_bf16)
                     store8(static_cast<__nv_bfloat16 *>(p.y) + row * p.K + g * 8, y);
                 else
                     store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
             }
             if (!p.codes) continue;
-            float v[8];
+            const float most = __uint_as_float(block_amax(v)) * r;
+            int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
+            const float inv = mx_inverse(b) * r, less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
+            uint32_t lo[4], hi[4];
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = h[c][i] * w[c][i];
-            const float most = __uint_as_float(block_amax(v)) * r.hi;
-            const uint32_t below = __float_as_uint(most * (1.0f - 0x1p-21f)), above = __float_as_uint(most * (1.0f + 0x1p-21f));
-            int b = mx_scale_byte(above, false);
-            const float inv = mx_inverse(b) * r.hi, less = inv * (1.0f - 0x1p-21f), more = inv * (1.0f + 0x1p-21f);
-            uint2 code, other;
-            {
-                uint32_t lo4[4], hi4[4];
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    lo4[i] = e4m3x2(v[2 * i] * less, v[2 * i + 1] * less);
-                    hi4[i] = e4m3x2(v[2 * i] * more, v[2 * i + 1] * more);
-                }
-                code = make_uint2(lo4[0] | lo4[1] << 16, lo4[2] | lo4[3] << 16);
-                other = make_uint2(hi4[0] | hi4[1] << 16, hi4[2] | hi4[3] << 16);
+            for (int i = 0; i < 4; i++) {
+                lo[i] = e4m3x2(v[2 * i] * less, v[2 * i + 1] * less);
+                hi[i] = e4m3x2(v[2 * i] * more, v[2 * i + 1] * more);
             }
-            // (tiny, infinite and NaN blocks too: there the f32 values are not that close)
-            const bool sure = code.x == other.x && code.y == other.y && mx_scale_byte(below, false) == b && b > 0 && b < 255 &&
-                              inv < 0x1p100f && r.hi > 0x1p-100f && most > 0x1p-90f;
+            uint2 code = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            // (tiny, infinite and NaN blocks are not sure: there the f32 values are not that close)
+            const bool sure = code.x == (hi[0] | hi[1] << 16) && code.y == (hi[2] | hi[3] << 16) &&
+                              mx_scale_byte(__float_as_uint(most * (1.0f - 0x1p-20f)), false) == b && b > 0 && b < 255 && inv < 0x1p100f &&
+                              r > 0x1p-60f && most > 0x1p-90f;
             if (__any_sync(0xffffffffu, live && !sure)) {
+                if (!exact) r2 = exact_r<T>(p, x, res, lane);
+                exact = true;
                 float odd[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) odd[i] = to_odd(mul(two_prod(h[c][i], w[c][i]), r));
+                for (int i = 0; i < 8; i++) odd[i] = to_odd(mul(two_prod(h[c][i], w[i]), r2));
                 b = mx_scale_byte(block_amax(odd), false);
                 code = codes8<false>(odd, mx_inverse(b));
             }
@@ -357,6 +327,7 @@ __global__ void __launch_bounds__(MOST) rms_norm_kernel(const NormParams p) {
             }
         }
         if (p.codes && threadIdx.x < p.S - p.K / 32) p.scales[row * p.S + p.K / 32 + threadIdx.x] = 0;
+        if (warps > 1) __syncthreads();                            // `part` is free
     }
 }
 
@@ -393,26 +364,26 @@ unsigned grid_for(int64_t work, int threads) {
     return (unsigned)std::min<int64_t>((work + threads - 1) / threads, (int64_t)sm_count() * (2048 / threads));
 }
 
-template <typename T, int C, int MOST>
+template <typename T, int C>
 gq_status norm_launch(const NormParams &p, int threads, cudaStream_t s) {
     NormParams q = p;
     void *args[] = {&q};
-    const int64_t fit = (int64_t)sm_count() * std::max(1, (C == 4 ? 640 : 1024) / threads);     // by the registers of each form
-    return launch_pdl((const void *)rms_norm_kernel<T, C, MOST>, dim3((unsigned)std::min<int64_t>(p.M, fit)), dim3(threads), 0, s, args,
+    const int64_t fit = (int64_t)sm_count() * std::max(1, 1024 / threads);       // 64 registers
+    return launch_pdl((const void *)rms_norm_kernel<T, C>, dim3((unsigned)std::min<int64_t>(p.M, fit)), dim3(threads), 0, s, args,
                       "norm launch");
 }
 
 // One group of 8 values per thread keeps a lone row's chain short; where rows abound (several for each
-// SM) threads take four groups, for fewer and longer turns, up to 256 of them.
+// SM) threads take two, for fewer and longer turns.
 template <typename T>
 gq_status norm_width(const NormParams &p, cudaStream_t s) {
     const int groups = p.K / 8;
-    int c = p.M >= 4LL * sm_count() && groups >= 128 && groups <= 1024 ? 4 : 1;
+    int c = p.M >= 4LL * sm_count() && groups >= 64 ? 2 : 1;
     while ((groups + c - 1) / c > 1024) c *= 2;
     const int threads = ((groups + c - 1) / c + 31) / 32 * 32;
-    if (c == 1) return norm_launch<T, 1, 1024>(p, threads, s);
-    if (c == 2) return norm_launch<T, 2, 1024>(p, threads, s);
-    return threads <= 256 ? norm_launch<T, 4, 256>(p, threads, s) : norm_launch<T, 4, 1024>(p, threads, s);
+    if (c == 1) return norm_launch<T, 1>(p, threads, s);
+    if (c == 2) return norm_launch<T, 2>(p, threads, s);
+    return norm_launch<T, 4>(p, threads, s);
 }
 
 }  // namespace

@@ -1,10 +1,10 @@
 // route.cu -- routing to experts: scores, the choice of top_k, and the rows sorted by expert.
 //
-// One warp per token; lane l holds the logits of experts l, l + 32, ..  A choice is made on ordered
-// 32-bit keys, one warp-wide maximum and one minimum of indices per chosen expert.  Without a bias
-// the order of the scores is the order of the logits, which are exact.  With one (and for the groups'
-// sums) the f32 values carry a rounding error: where two values that decide something are closer than
-// its bound (about one token in a hundred with a bias), the warp takes the 32 best candidates, one per lane, and
+// One warp per token; lane l holds the values of experts l, l + 32, .. as ordered 32-bit keys, whose lowest bits say which of
+// the lane's experts it is, and sorts them; a choice then costs a warp-wide maximum of the lanes' first keys, and the lane that
+// had it moves up.  Without a bias the order of the scores is the order of the logits.  Keys lack some bits, and with a bias
+// (and for the groups' sums) f32 values carry a rounding error: where two values that decide something are closer
+// than its bound (about one token in a hundred with a bias), the warp takes the 32 best candidates, one per lane, and
 // ranks them by their values in 64 bits; where that does not settle it (the groups' sums are close, or more than
 // 32 candidates are), it does the whole token in 64 bits.
 //
@@ -108,6 +108,8 @@ __device__ __forceinline__ double score64(const RouteParams &p, float z, float m
     return m == -INFINITY ? 0.0 : exp((double)z - (double)m) / sum;
 }
 
+__device__ __forceinline__ float plain(float z) { return isnan(z) ? -INFINITY : z; }
+__device__ __forceinline__ float plain(__nv_bfloat16 z) { return plain(__bfloat162float(z)); }
 __device__ __forceinline__ float logit(const RouteParams &p, int64_t t, int e) {
     const float z = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[t * p.ldl + e])
                            : static_cast<const float *>(p.logits)[t * p.ldl + e];
@@ -159,11 +161,31 @@ __device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, d
     return id;
 }
 
+// Sorts N keys of a lane, the largest first: a bitonic network.
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[N]) {
+#pragma unroll
+    for (int size = 2; size <= N; size *= 2)
+#pragma unroll
+        for (int step = size / 2; step > 0; step /= 2)
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const int j = i ^ step;
+                if (j > i) {
+                    const uint32_t hi = max(key[i], key[j]), lo = min(key[i], key[j]);
+                    key[i] = (i & size) == 0 || size == N ? hi : lo;
+                    key[j] = (i & size) == 0 || size == N ? lo : hi;
+                }
+            }
+}
+
 // One token.  Lane j < k returns the j-th choice.  z: the lane's logits; m and sum: their maximum and the sum of the
 // exponentials (softmax); bias, group: of the lane's experts.
-template <int V>
+template <int V, typename T>
 __device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const float (&z)[V], const float (&bias)[V], const int (&group)[V], float m,
                                       float sum, double *shared, int lane) {
+    // the lowest bits of a key: the lane's experts counted from the last, so that of equal values the lowest index is first
+    constexpr uint32_t SLOT = V - 1;
     const bool grouped = p.top_groups < p.groups, sums = !p.bias && p.group_best == 2;
     const float inverse = p.sigmoid ? 1.0f : m == -INFINITY ? 0.0f : 1.0f / sum;
     // The fast exponential and reciprocal: a sigmoid is off by 2e-7 at most; a softmax score by its rounded argument and
@@ -203,68 +225,69 @@ __device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const flo
             if (!(gap > 2.0f * tol + 0x1p-20f * size)) return choose64(p, t, m, sum64(p, t, m, lane), shared, lane);
         }
     }
-    uint32_t key[V], best = 0;
-    int at = 0;
+    uint32_t key[V];
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        key[i] = i * 32 + lane < p.E && (allowed >> group[i] & 1u) ? order32(c[i] + 0.0f) : 0u;
-        if (key[i] > best) best = key[i], at = i;
-    }
+    for (int i = 0; i < V; i++)
+        key[i] = i * 32 + lane < p.E && (allowed >> group[i] & 1u) ? (order32(c[i] + 0.0f) & ~SLOT) | (SLOT - i) : 0u;
+    sort_keys<V>(key);
     int id = -1;
-    float value = 0.0f;                       // of the lane's candidate
+    uint32_t mine = 0;                        // the lane's candidate
     int found = 0;
     auto next = [&] {                         // the best that is left goes to lane `found`; false if there is none
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top == 0) return false;
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-        if (lane == found) id = e, value = unorder32(top);
-        if (lane == (e & 31)) {
-            best = 0;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+        if (top <= SLOT) return false;
+        // equal keys are of the same place in different lanes: the lowest lane has the lowest index
+        const int from = __ffs((int)__ballot_sync(0xffffffffu, key[0] == top)) - 1;
+        if (lane == found) id = (int)(SLOT - (top & SLOT)) * 32 + from, mine = top;
+        if (lane == from) {
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                if (i == (e >> 5)) key[i] = 0;
-                if (key[i] > best) best = key[i], at = i;
-            }
+            for (int i = 0; i + 1 < V; i++) key[i] = key[i + 1];
+            key[V - 1] = 0;
         }
-        __syncwarp();
         found++;
         return true;
     };
     while (found < p.k && next()) {
     }
-    if (!p.bias) return id;
+    // bf16 logits without a bias: keys lack nothing
+    if (!p.bias && sizeof(T) == 2) return id;
     // the choice after the last says how far it is from it
     const int chosen = found;
     const bool one_more = found < 32 && next();
-    float after = __shfl_down_sync(0xffffffffu, value, 1);
+    uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1);
     if (chosen == 32) {                       // (all lanes are taken: the best that is left)
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (lane == 31) after = top ? unorder32(top) : -INFINITY;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+        if (lane == 31) after = top;
     } else if (!one_more && lane == chosen - 1) {
-        after = -INFINITY;
+        after = 0;
     }
-    const bool close = lane < chosen && !(value - after > tol + 0x1p-21f * (fabsf(value) + (after > -INFINITY ? fabsf(after) : 0.0f)));
-    if (!__any_sync(0xffffffffu, close)) return id;
+    // a key's value is up to 32 units of the last place below its expert's
+    auto apart = [&](uint32_t hi, uint32_t lo) {
+        if (lo <= SLOT) return true;
+        const float a = unorder32(hi & ~SLOT), b = unorder32(lo & ~SLOT);
+        if (!p.bias) return (hi & ~SLOT) != (lo & ~SLOT);
+        return a - b > tol + (0x1p-21f + V * 0x1p-23f) * (fabsf(a) + fabsf(b));
+    };
+    if (!__any_sync(0xffffffffu, lane < chosen && !apart(mine, after))) return id;
     // 32 candidates, ranked by their values in 64 bits
     while (found < 32 && next()) {
     }
     const double s = sum64(p, t, m, lane);
     double exact = -INFINITY;
-    if (lane < found) exact = score64(p, logit(p, t, id), m, s) + (double)p.bias[id];
+    if (lane < found) {
+        const float x = logit(p, t, id);
+        exact = p.bias ? score64(p, x, m, s) + (double)p.bias[id] : (double)x;
+    }
     int rank = 0;
     for (int j = 0; j < found; j++) {
         const double v = __shfl_sync(0xffffffffu, exact, j);
         const int e = __shfl_sync(0xffffffffu, id, j);
         rank += v > exact || (v == exact && e < id);
     }
-    // what was not taken is below the last candidate's f32 value: it must not reach up to the last choice
-    const uint32_t left = __reduce_max_sync(0xffffffffu, best);
-    if (left) {
-        const uint32_t w = __ballot_sync(0xffffffffu, lane < found && rank == p.k - 1);
-        const double lowest = __shfl_sync(0xffffffffu, exact, __ffs((int)w) - 1);
-        const float most = unorder32(left);
-        if (!(lowest - (double)most > (double)(tol + 0x1p-21f * (fabsf(most) + fabsf((float)lowest))))) return choose64(p, t, m, s, shared, lane);
-    }
+    // what was not taken must be below the last choice
+    const uint32_t left = __reduce_max_sync(0xffffffffu, key[0]);
+    const uint32_t w = __ballot_sync(0xffffffffu, lane < found && rank == p.k - 1);
+    if (!apart(__shfl_sync(0xffffffffu, mine, __ffs((int)w) - 1), left)) return choose64(p, t, m, s, shared, lane);
     // to the lanes of their ranks
     int out = -1;
     for (int j = 0; j < found; j++) {
@@ -338,7 +361,7 @@ __device__ __forceinline__ int tokens_used(const int32_t *used, int T, unsigned 
 constexpr int route_threads(int V) { return V <= 8 ? 1024 : 512; }
 
 // Dynamic shared memory: E counts, SOLO_TOKENS * k ids (solo), then, with groups, E doubles per warp.
-template <int V>
+template <int V, typename T>
 __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RouteParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     int32_t *counts = reinterpret_cast<int32_t *>(smem);
@@ -364,10 +387,11 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
         int id = -1;
         float w = 0.0f;
         if (t < used) {
+            const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
             float z[V], m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                z[i] = i * 32 + lane < p.E ? logit(p, t, i * 32 + lane) : -INFINITY;
+                z[i] = i * 32 + lane < p.E ? plain(row[i * 32 + lane]) : -INFINITY;
                 m = fmaxf(m, z[i]);
             }
             float sum = 1.0f;
@@ -380,9 +404,9 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
                     sum = warp_sum(sum);
                 }
             }
-            id = choose<V>(p, t, z, bias, group, m, sum, shared, lane);
+            id = choose<V, T>(p, t, z, bias, group, m, sum, shared, lane);
             if (lane < p.k) {
-                const float chosen = logit(p, t, id);
+                const float chosen = plain(row[id]);
                 w = p.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : m > -INFINITY ? expf(chosen - m) / sum : 0.0f;
             }
             if (p.renormalize) {
@@ -462,7 +486,8 @@ gq_status route_launch(RouteParams p, int chunks, size_t fixed, cudaStream_t s) 
     if (per_warp) warps = std::max<int>(1, std::min<int64_t>(warps, (int64_t)((48 * 1024 - fixed) / per_warp)));
     warps = (p.chunk + (p.chunk + warps - 1) / warps - 1) / ((p.chunk + warps - 1) / warps);   // as many turns, no idle warps
     void *args[] = {&p};
-    return launch_pdl((const void *)route_kernel<V>, dim3(chunks), dim3(32 * warps), fixed + warps * per_warp, s, args, "route launch");
+    const void *fn = p.bf16 ? (const void *)route_kernel<V, __nv_bfloat16> : (const void *)route_kernel<V, float>;
+    return launch_pdl(fn, dim3(chunks), dim3(32 * warps), fixed + warps * per_warp, s, args, "route launch");
 }
 
 }  // namespace
