@@ -934,17 +934,28 @@ def kv_pages_evict(cache: KVPages, weights, budget: int, keep_first: int = 1, ke
 # ---------------------------------------------------------------------------
 # microscaled formats, routing, experts
 # ---------------------------------------------------------------------------
+# (a call on few rows takes the GPU some microseconds, so what a call costs on the host counts here: a torch.empty is
+# 1.5 us, a launch 2 to 3 us)
+def _torch():
+    """torch, and its types as gq_type, once."""
+    global _th, _types, _float32, _bfloat16, _uint8, _int32
+    import torch
+    _th, _types = torch, {torch.float32: GQ_TYPE_F32, torch.bfloat16: GQ_TYPE_BF16}
+    _float32, _bfloat16, _uint8, _int32 = torch.float32, torch.bfloat16, torch.uint8, torch.int32
+    return torch
+
+
+_th = _types = _bfloat16 = _uint8 = _int32 = None
+
+
 def _mx_type(dtype, name: str) -> int:
     """gq_type of a torch dtype."""
-    if not _types:
-        import torch
-        _types.update({torch.float32: GQ_TYPE_F32, torch.bfloat16: GQ_TYPE_BF16})
-    if dtype not in _types:
+    if _types is None:
+        _torch()
+    t = _types.get(dtype)
+    if t is None:
         raise ValueError(f"{name}: expected float32 or bfloat16, got {dtype}")
-    return _types[dtype]
-
-
-_types = {}
+    return t
 
 
 def _cuda(t, dtype: str, shape, name: str) -> int:
@@ -956,9 +967,10 @@ def _cuda(t, dtype: str, shape, name: str) -> int:
 
 def _matrix(x, name: str):
     """(rows, columns, row stride, gq_type) of a CUDA matrix whose rows are contiguous."""
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError(f"{name}: expected a CUDA matrix, got {tuple(x.shape)}")
-    (M, K), (ld, one) = x.shape, x.stride()
+    shape = x.shape
+    if not x.is_cuda or len(shape) != 2:
+        raise ValueError(f"{name}: expected a CUDA matrix, got {tuple(shape)}")
+    (M, K), (ld, one) = shape, x.stride()
     if one != 1 and K > 1:
         raise ValueError(f"{name}: each row must be contiguous")
     return M, K, ld if M > 1 else K, _mx_type(x.dtype, name)
@@ -967,18 +979,52 @@ def _matrix(x, name: str):
 class MXRows:
     """Rows in microscaled blocks: codes uint8 [rows, K] (e4m3) or [rows, K / 2] (e2m1), scales uint8 [rows, S]."""
 
+    __slots__ = ("kind", "rows", "K", "codes_ptr", "scales_ptr", "_codes", "_scales", "_buffer", "_struct")
+
     def __init__(self, codes, scales, kind: int = GQ_MX_E4M3):
         rows, width = codes.shape
         self.kind, self.rows, self.K = kind, rows, width * (2 if kind == GQ_MX_E2M1 else 1)
-        c = _cuda(codes, "uint8", codes.shape, "codes")
-        s = _cuda(scales, "uint8", (rows, gq_mx_scale_cols(self.K)), "scales")
-        self.codes, self.scales, self.struct = codes, scales, MXRowsStruct(rows, c, s)
+        self.codes_ptr = _cuda(codes, "uint8", codes.shape, "codes")
+        self.scales_ptr = _cuda(scales, "uint8", (rows, gq_mx_scale_cols(self.K)), "scales")
+        self._codes, self._scales, self._buffer, self._struct = codes, scales, None, None
 
     @classmethod
     def empty(cls, rows: int, K: int, kind: int = GQ_MX_E4M3, device="cuda"):
-        import torch
-        return cls(torch.empty((rows, K // 2 if kind == GQ_MX_E2M1 else K), dtype=torch.uint8, device=device),
-                   torch.empty((rows, gq_mx_scale_cols(K)), dtype=torch.uint8, device=device), kind)
+        """Room for rows of K values: one tensor that holds the codes, then the scales."""
+        if K <= 0 or K % 32 or rows <= 0:
+            raise ValueError(f"expected rows of a multiple of 32 values, got {(rows, K)}")
+        self = cls.__new__(cls)
+        width = K // 2 if kind == GQ_MX_E2M1 else K
+        self._buffer = (_th or _torch()).empty(rows * (width + (K + 511) // 512 * 16), dtype=_uint8, device=device)
+        self.kind, self.rows, self.K = kind, rows, K
+        self.codes_ptr = self._buffer.data_ptr()
+        self.scales_ptr = self.codes_ptr + rows * width
+        self._codes = self._scales = self._struct = None
+        return self
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            n = self.scales_ptr - self.codes_ptr
+            self._codes = self._buffer[:n].view(self.rows, n // self.rows)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._buffer[self.scales_ptr - self.codes_ptr:].view(self.rows, -1)
+        return self._scales
+
+    @property
+    def device(self):
+        return (self._codes if self._buffer is None else self._buffer).device
+
+    @property
+    def by_ref(self):
+        """The gq_mx_rows, for a call."""
+        if self._struct is None:
+            self._struct = ctypes.pointer(MXRowsStruct(self.rows, self.codes_ptr, self.scales_ptr))
+        return self._struct
 
 
 class MXWeights:
@@ -986,19 +1032,29 @@ class MXWeights:
 
     def __init__(self, data, count: int, N: int, K: int):
         self.address = _cuda(data, "uint8", (gq_mxfp4_repacked_bytes(count, N, K),), "data")
-        self.data, self.count, self.N, self.K = data, count, N, K
+        self.data, self.device, self.count, self.N, self.K = data, data.device, count, N, K
 
 
 class ExpertPlan:
     """Rows sorted by expert (gq_expert_rows): offsets int32 [E + 1], the token of each row, the row of each choice [T, top_k]."""
 
     def __init__(self, offsets, rows, pos):
-        self.offsets, self.rows, self.pos = offsets, rows, pos
-        self.E, self.R = offsets.shape[0] - 1, rows.shape[0]
-        o = _cuda(offsets, "int32", (self.E + 1,), "offsets")
-        r = _cuda(rows, "int32", (self.R,), "rows")
+        _cuda(offsets, "int32", offsets.shape[:1], "offsets")
+        _cuda(rows, "int32", rows.shape[:1], "rows")
         _cuda(pos, "int32", pos.shape, "pos")
-        self.gathered, self.in_order = ExpertRowsStruct(self.E, self.R, o, r), ExpertRowsStruct(self.E, self.R, o, None)
+        self._set(offsets, rows, pos, offsets.shape[0] - 1, rows.shape[0])
+
+    def _set(self, offsets, rows, pos, E: int, R: int):
+        self.offsets, self.rows, self.pos, self.E, self.R = offsets, rows, pos, E, R
+        self._gathered = self._in_order = None
+
+    def by_ref(self, gather: bool):
+        """The gq_expert_rows, for a call: with the rows to gather, or without."""
+        if self._gathered is None:
+            o, r = self.offsets.data_ptr(), self.rows.data_ptr()
+            self._gathered = ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, r))
+            self._in_order = ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, None))
+        return self._gathered if gather else self._in_order
 
 
 class Router:
@@ -1012,23 +1068,28 @@ class Router:
         self.E, self.top_k, self.bias = E, top_k, bias
         self.struct = RouterStruct(E, top_k, scores[score], groups, top_groups, group_best, renormalize, factor,
                                    None if bias is None else _cuda(bias, "float32", (E,), "bias"))
+        self.by_ref = ctypes.pointer(self.struct)
 
 
 def quantize_mx(x, kind: int = GQ_MX_E4M3) -> MXRows:
     """Rows f32 or bf16 [M, K] in microscaled blocks."""
     M, K, ld, t = _matrix(x, "x")
     out = MXRows.empty(M, K, kind, x.device)
-    _check(lib().gq_quantize_mx(x.data_ptr(), ld, t, kind, out.struct.codes, out.struct.scales, M, K, _current_stream()),
-           "gq_quantize_mx")
+    status = lib().gq_quantize_mx(x.data_ptr(), ld, t, kind, out.codes_ptr, out.scales_ptr, M, K, _current_stream())
+    if status:
+        _check(status, "gq_quantize_mx")
     return out
 
 
 def dequantize_mx(rows: MXRows, dtype=None):
     """The values of microscaled rows, f32 (or bf16) [rows, K]."""
-    import torch
-    y = torch.empty((rows.rows, rows.K), dtype=dtype or torch.float32, device=rows.codes.device)
-    _check(lib().gq_dequantize_mx(rows.struct.codes, rows.struct.scales, rows.kind, y.data_ptr(), _mx_type(y.dtype, "dtype"),
-                                  rows.rows, rows.K, _current_stream()), "gq_dequantize_mx")
+    th = _th or _torch()
+    dtype = dtype or _float32
+    t = _mx_type(dtype, "dtype")
+    y = th.empty((rows.rows, rows.K), dtype=dtype, device=rows.device)
+    status = lib().gq_dequantize_mx(rows.codes_ptr, rows.scales_ptr, rows.kind, y.data_ptr(), t, rows.rows, rows.K, _current_stream())
+    if status:
+        _check(status, "gq_dequantize_mx")
     return y
 
 
@@ -1055,7 +1116,19 @@ def _operands(w: MXWeights, x: MXRows, plan, gather: bool, parts: int):
         if gather:
             raise ValueError("gather: there is no plan")
         return x.rows, None
-    return plan.R, ctypes.byref(plan.gathered if gather else plan.in_order)
+    return plan.R, plan.by_ref(gather)
+
+
+def _output(out, rows: int, N: int, dtype, device):
+    """(tensor, row stride, gq_type) of an output [rows, N]: `out` if given, else a new one."""
+    if out is None:
+        dtype = dtype or _f32()
+        t = _mx_type(dtype, "dtype")
+        return _th.empty((rows, N), dtype=dtype, device=device), N, t
+    Ro, No, ld, t = _matrix(out, "out")
+    if Ro != rows or No != N:
+        raise ValueError(f"out: expected shape {(rows, N)}, got {(Ro, No)}")
+    return out, ld, t
 
 
 def mul_mat_mxfp4(w: MXWeights, x, plan: ExpertPlan = None, gather: bool = False, dtype=None, out=None):
@@ -1064,88 +1137,87 @@ def mul_mat_mxfp4(w: MXWeights, x, plan: ExpertPlan = None, gather: bool = False
     With a plan, row r is the product of x's row plan.rows[r] (gather) or r with the weights of its expert;
     rows from plan.offsets[E] on are left as they are.
     """
-    import torch
     if isinstance(x, MXRows):
         R, ref = _operands(w, x, plan, gather, 1)
+        out, ldd, otype = _output(out, R, w.N, dtype, w.device)
+        status = lib().gq_mul_mat_mxfp4_mx(w.address, x.by_ref, ref, out.data_ptr(), ldd, otype, w.N, w.K, _current_stream())
     else:
         R, K, ldx, xtype = _matrix(x, "x")
-        if plan is not None or K != w.K or w.count != 1:
+        if plan is not None or gather or K != w.K or w.count != 1:
             raise ValueError(f"x: expected rows of K = {w.K} and one matrix without a plan, got K = {K} and {w.count}")
-    if out is None:
-        out = torch.empty((R, w.N), dtype=dtype or torch.float32, device=w.data.device)
-    Ro, N, ldd, otype = _matrix(out, "out")
-    if Ro != R or N != w.N:
-        raise ValueError(f"out: expected shape {(R, w.N)}, got {(Ro, N)}")
-    if isinstance(x, MXRows):
-        _check(lib().gq_mul_mat_mxfp4_mx(w.address, ctypes.byref(x.struct), ref, out.data_ptr(), ldd, otype, N, w.K, _current_stream()),
-               "gq_mul_mat_mxfp4_mx")
-    else:
-        _check(lib().gq_mul_mat_mxfp4(w.address, x.data_ptr(), ldx, xtype, out.data_ptr(), ldd, otype, R, N, w.K, _current_stream()),
-               "gq_mul_mat_mxfp4")
+        out, ldd, otype = _output(out, R, w.N, dtype, w.device)
+        status = lib().gq_mul_mat_mxfp4(w.address, x.data_ptr(), ldx, xtype, out.data_ptr(), ldd, otype, R, w.N, K, _current_stream())
+    if status:
+        _check(status, "gq_mul_mat_mxfp4")
     return out
 
 
 def swiglu_mxfp4(w: MXWeights, x: MXRows, plan: ExpertPlan = None, gather: bool = False) -> MXRows:
     """silu(x Wg^T) * (x Wu^T) in e4m3 blocks; w holds Wg and Wu, each [F, K], one after the other (for each expert)."""
     R, ref = _operands(w, x, plan, gather, 2)
-    out = MXRows.empty(R, w.N, GQ_MX_E4M3, w.data.device)
-    _check(lib().gq_swiglu_mxfp4_mx(w.address, ctypes.byref(x.struct), ref, out.struct.codes, out.struct.scales, w.N, w.K,
-                                    _current_stream()), "gq_swiglu_mxfp4_mx")
+    out = MXRows.empty(R, w.N, GQ_MX_E4M3, w.device)
+    status = lib().gq_swiglu_mxfp4_mx(w.address, x.by_ref, ref, out.codes_ptr, out.scales_ptr, w.N, w.K, _current_stream())
+    if status:
+        _check(status, "gq_swiglu_mxfp4_mx")
     return out
 
 
 def rms_norm_mx(x, weight, eps: float, residual=None, y_dtype=None):
     """(h, blocks): h = x + residual (x itself without one) and the e4m3 blocks of its norm; with y_dtype (h, blocks, y)."""
-    import torch
     M, K, ldx, t = _matrix(x, "x")
     w = None if weight is None else _cuda(weight, "float32", (K,), "weight")
-    h, res, ldr, ldh = x, None, K, K
+    device = x.device
+    h, y, res, ldr, h_ptr, y_ptr, yt = x, None, None, K, None, None, GQ_TYPE_F32
     if residual is not None:
         Mr, Kr, ldr, tr = _matrix(residual, "residual")
-        if (Mr, Kr, tr) != (M, K, t):
+        if Mr != M or Kr != K or tr != t:
             raise ValueError(f"residual: expected {x.dtype} {(M, K)}, got {residual.dtype} {(Mr, Kr)}")
-        h, res = torch.empty((M, K), dtype=x.dtype, device=x.device), residual.data_ptr()
-    y = None if y_dtype is None else torch.empty((M, K), dtype=y_dtype, device=x.device)
-    out = MXRows.empty(M, K, GQ_MX_E4M3, x.device)
-    _check(lib().gq_rms_norm_mx(x.data_ptr(), ldx, res, ldr, t, w, eps, None if res is None else h.data_ptr(), ldh,
-                                None if y is None else y.data_ptr(), GQ_TYPE_F32 if y is None else _mx_type(y_dtype, "y_dtype"),
-                                out.struct.codes, out.struct.scales, M, K, _current_stream()), "gq_rms_norm_mx")
+        h, res = _th.empty((M, K), dtype=x.dtype, device=device), residual.data_ptr()
+        h_ptr = h.data_ptr()
+    if y_dtype is not None:
+        yt = _mx_type(y_dtype, "y_dtype")
+        y = _th.empty((M, K), dtype=y_dtype, device=device)
+        y_ptr = y.data_ptr()
+    out = MXRows.empty(M, K, GQ_MX_E4M3, device)
+    status = lib().gq_rms_norm_mx(x.data_ptr(), ldx, res, ldr, t, w, eps, h_ptr, K, y_ptr, yt, out.codes_ptr, out.scales_ptr, M, K,
+                                  _current_stream())
+    if status:
+        _check(status, "gq_rms_norm_mx")
     return (h, out) if y is None else (h, out, y)
 
 
 def route(logits, router: Router, used=None):
     """(ids, weights, plan) of f32 or bf16 logits [T, E]; `used`: int32 [1], tokens from it on are padding."""
-    import torch
     T, E, ldl, t = _matrix(logits, "logits")
     if E != router.E:
         raise ValueError(f"logits: expected {router.E} experts, got {E}")
-    k, dev = router.top_k, logits.device
+    k, dev, empty = router.top_k, logits.device, _th.empty
     u = None if used is None else _cuda(used, "int32", (1,), "used")
-    ids, pos = (torch.empty((T, k), dtype=torch.int32, device=dev) for _ in range(2))
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    plan = ExpertPlan(torch.empty(E + 1, dtype=torch.int32, device=dev), torch.empty(T * k, dtype=torch.int32, device=dev), pos)
-    _check(lib().gq_route(ctypes.byref(router.struct), logits.data_ptr(), ldl, t, u, ids.data_ptr(), weights.data_ptr(),
-                          plan.offsets.data_ptr(), plan.rows.data_ptr(), pos.data_ptr(), T, _current_stream()), "gq_route")
+    ids, pos = empty((T, k), dtype=_int32, device=dev), empty((T, k), dtype=_int32, device=dev)
+    rows, offsets = empty(T * k, dtype=_int32, device=dev), empty(E + 1, dtype=_int32, device=dev)
+    weights = empty((T, k), dtype=_float32, device=dev)
+    status = lib().gq_route(router.by_ref, logits.data_ptr(), ldl, t, u, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+                            rows.data_ptr(), pos.data_ptr(), T, _current_stream())
+    if status:
+        _check(status, "gq_route")
+    plan = ExpertPlan.__new__(ExpertPlan)
+    plan._set(offsets, rows, pos, E, T * k)
     return ids, weights, plan
 
 
 def experts_combine(y, plan: ExpertPlan, weights, residual=None, dtype=None, out=None):
     """residual + the weighted sum of each token's rows of y (f32 [R, N]): f32 (or `dtype`) [T, N]."""
-    import torch
     T, k = plan.pos.shape
     R, N = y.shape
     a, w = _cuda(y, "float32", (plan.R, N), "y"), _cuda(weights, "float32", (T, k), "weights")
     res, ldr, rtype = None, N, GQ_TYPE_F32
     if residual is not None:
         Tr, Nr, ldr, rtype = _matrix(residual, "residual")
-        if (Tr, Nr) != (T, N):
+        if Tr != T or Nr != N:
             raise ValueError(f"residual: expected shape {(T, N)}, got {(Tr, Nr)}")
         res = residual.data_ptr()
-    if out is None:
-        out = torch.empty((T, N), dtype=dtype or torch.float32, device=y.device)
-    To, No, ldo, otype = _matrix(out, "out")
-    if (To, No) != (T, N):
-        raise ValueError(f"out: expected shape {(T, N)}, got {(To, No)}")
-    _check(lib().gq_experts_combine(a, R, plan.pos.data_ptr(), w, k, res, ldr, rtype, out.data_ptr(), ldo, otype, T, N,
-                                    _current_stream()), "gq_experts_combine")
+    out, ldo, otype = _output(out, T, N, dtype, y.device)
+    status = lib().gq_experts_combine(a, R, plan.pos.data_ptr(), w, k, res, ldr, rtype, out.data_ptr(), ldo, otype, T, N, _current_stream())
+    if status:
+        _check(status, "gq_experts_combine")
     return out

@@ -199,15 +199,39 @@ struct NormParams {
     int K, S, y_bf16;
 };
 
+// Eight values as they lie in memory, and the sum of two such, rounded to the type: as it is stored, and widened.
+template <typename T>
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; i++) v[i] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ void store(T *p) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; i++) reinterpret_cast<uint4 *>(p)[i] = v[i];
+    }
+    __device__ __forceinline__ void widen(float (&f)[8]) const { load8(reinterpret_cast<const T *>(v), f); }
+    __device__ __forceinline__ void add(const Raw &o) {
+        float a[8], b[8];
+        widen(a);
+        o.widen(b);
+#pragma unroll
+        for (int i = 0; i < 8; i++) a[i] += b[i];
+        store8(reinterpret_cast<T *>(v), a);
+    }
+};
+
 // Group g of 8 values of h = x + residual, rounded to T.
 template <typename T>
 __device__ __forceinline__ void load_h(const T *x, const T *res, int g, float (&h)[8]) {
-    load8(x + g * 8, h);
-    if (!res) return;
-    float r[8];
-    load8(res + g * 8, r);
-#pragma unroll
-    for (int i = 0; i < 8; i++) h[i] = sizeof(T) == 4 ? h[i] + r[i] : __bfloat162float(__float2bfloat16_rn(h[i] + r[i]));
+    Raw<T> a, b;
+    a.load(x + g * 8);
+    if (res) {
+        b.load(res + g * 8);
+        a.add(b);
+    }
+    a.widen(h);
 }
 
 // 1 / sqrt(mean(h^2) + eps) of a row in two terms, by one warp.
@@ -241,6 +265,20 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
+    // a row's loads are under way while the one before it is worked on
+    Raw<T> rx[C], rr[C];
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const int g = threadIdx.x + c * blockDim.x;
+            if (g >= groups) continue;
+            rx[c].load(static_cast<const T *>(p.x) + row * p.ldx + g * 8);
+            if (p.res) rr[c].load(static_cast<const T *>(p.res) + row * p.ldr + g * 8);
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < C; c++) rx[c] = rr[c] = Raw<T>{};
+    if (blockIdx.x < p.M) load(blockIdx.x);
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         const T *res = p.res ? static_cast<const T *>(p.res) + row * p.ldr : nullptr;
@@ -248,15 +286,14 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
-#pragma unroll
-            for (int i = 0; i < 8; i++) h[c][i] = 0.0f;
-            if (g < groups) load_h(x, res, g, h[c]);
+            if (p.res) rx[c].add(rr[c]);
+            if (p.h && g < groups) rx[c].store(static_cast<T *>(p.h) + row * p.ldh + g * 8);
+            rx[c].widen(h[c]);
         }
+        if (row + gridDim.x < p.M) load(row + gridDim.x);
         float sq[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            const int g = threadIdx.x + c * blockDim.x;
-            if (p.h && g < groups) store8(static_cast<T *>(p.h) + row * p.ldh + g * 8, h[c]);
 #pragma unroll
             for (int i = 0; i < 8; i++) sq[i] = fmaf(h[c][i], h[c][i], sq[i]);
         }
@@ -298,7 +335,11 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
                     store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
             }
             if (!p.codes) continue;
-            const float most = __uint_as_float(block_amax(v)) * r;
+            float most = 0.0f;                             // (a NaN or infinity of h has made r NaN or 0)
+#pragma unroll
+            for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[i]));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2)) * r;
             int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
             const float inv = mx_inverse(b) * r, less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
             uint32_t lo[4], hi[4];
@@ -309,7 +350,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             }
             uint2 code = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             // (tiny, infinite and NaN blocks are not sure: there the f32 values are not that close)
-            const bool sure = code.x == (hi[0] | hi[1] << 16) && code.y == (hi[2] | hi[3] << 16) &&
+            const bool sure = ((lo[0] ^ hi[0]) | (lo[1] ^ hi[1]) | (lo[2] ^ hi[2]) | (lo[3] ^ hi[3])) == 0 &&
                               mx_scale_byte(__float_as_uint(most * (1.0f - 0x1p-20f)), false) == b && b > 0 && b < 255 && inv < 0x1p100f &&
                               r > 0x1p-60f && most > 0x1p-90f;
             if (__any_sync(0xffffffffu, live && !sure)) {

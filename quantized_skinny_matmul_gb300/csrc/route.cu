@@ -33,7 +33,8 @@ struct RouteParams {
     unsigned int *status;
     int64_t ldl;
     int E, k, T, chunk, sigmoid, groups, top_groups, group_best, renormalize, bf16;
-    int lanes;                       // that look through a group
+    int lanes, log_lanes;            // that look through a group
+    int per_group;                   // E / groups
     float factor;
 };
 
@@ -76,12 +77,12 @@ __device__ __forceinline__ void best_two(F &a, F &b, F c, F d) {
 // power of two from `groups` on; expert e's value is at e + (e / n) * (32 / P), so that lanes of different groups use
 // different banks.  `gap` receives the distance between the worst group that takes part and the best that does not.
 template <typename F>
-__device__ __forceinline__ uint32_t best_groups(const F *c, int n, int groups, int lanes, int top, int best, int lane, F &gap) {
+__device__ __forceinline__ uint32_t best_groups(const F *c, int n, int groups, int log_lanes, int top, int best, int lane, F &gap) {
     const F none = -(F)INFINITY;
-    const int g = lane / lanes;
+    const int g = lane >> log_lanes, lanes = 1 << log_lanes;
     F a = none, b = none;
     if (g < groups)
-        for (int j = lane % lanes; j < n; j += lanes) best_two<F>(a, b, c[g * (n + lanes) + j], none);
+        for (int j = lane & (lanes - 1); j < n; j += lanes) best_two<F>(a, b, c[g * (n + lanes) + j], none);
     for (int d = 1; d < lanes; d <<= 1) {
         const F oa = __shfl_xor_sync(0xffffffffu, a, d), ob = __shfl_xor_sync(0xffffffffu, b, d);
         best_two<F>(a, b, oa, ob);
@@ -137,7 +138,7 @@ __device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, d
         }
         __syncwarp();
         double gap;
-        allowed = best_groups<double>(shared, n, p.groups, p.lanes, p.top_groups, p.group_best, lane, gap);
+        allowed = best_groups<double>(shared, n, p.groups, p.log_lanes, p.top_groups, p.group_best, lane, gap);
         __syncwarp();
     }
     uint64_t last_key = ~0ull;
@@ -214,7 +215,7 @@ __device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const flo
             if (i * 32 + lane < p.E) values[i * 32 + lane + group[i] * p.lanes] = sums ? score(z[i]) : c[i];
         __syncwarp();
         float gap;
-        allowed = best_groups<float>(values, p.E / p.groups, p.groups, p.lanes, p.top_groups, p.group_best, lane, gap);
+        allowed = best_groups<float>(values, p.per_group, p.groups, p.log_lanes, p.top_groups, p.group_best, lane, gap);
         __syncwarp();
         if (p.bias || sums) {
             float size = 0.0f;
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
 }
 
 // CTA c places the choices of chunk c.  Four threads sum an expert's counts over the chunks.
-constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_THREADS = 1024;
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const int32_t *__restrict__ ids, const int32_t *__restrict__ counts,
                                                             int32_t *__restrict__ offsets, int32_t *__restrict__ rows,
                                                             int32_t *__restrict__ pos, int E, int k, int T, int chunk, int chunks) {
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const int32_t *__res
     for (int x = threadIdx.x; x < E * parts; x += PLAN_THREADS) {
         const int e = x % E, part = x / E;
         int all = 0, mine = 0;
-#pragma unroll 8
+#pragma unroll 16
         for (int c = part; c < chunks; c += parts) {
             const int v = counts[(int64_t)c * E + e];
             all += v;
@@ -464,13 +465,36 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const int32_t *__res
         atomicAdd(&before[e], mine);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, total = scan(base, E, lane);
-        for (int e = lane; e < E; e += 32) {
-            if (blockIdx.x == 0) offsets[e] = base[e];
-            base[e] += before[e];
+    {
+        // exclusive sums over the experts: E <= PLAN_THREADS, one each
+        __shared__ int32_t sums[32];
+        const int e = threadIdx.x, lane = e & 31, warp = e >> 5, v = e < E ? base[e] : 0;
+        int s = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += u;
         }
-        if (blockIdx.x == 0 && lane == 0) offsets[E] = total;
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            int t = sums[lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, t, d);
+                if (lane >= d) t += u;
+            }
+            sums[lane] = t;
+        }
+        __syncthreads();
+        if (warp > 0) s += sums[warp - 1];
+        if (e < E) {
+            if (blockIdx.x == 0) {
+                offsets[e] = s - v;
+                if (e == E - 1) offsets[E] = s;
+            }
+            base[e] = s - v + before[e];
+        }
     }
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * chunk * k;
@@ -502,6 +526,8 @@ gq_status launch_route(const gq_router &r, const void *logits, int64_t ldl, bool
     int P = 1;
     while (P < p.groups) P *= 2;
     p.lanes = 32 / P;
+    while ((1 << p.log_lanes) < p.lanes) p.log_lanes++;
+    p.per_group = p.E / p.groups;
     p.status = device_status_word();
     if (!p.status) return fail(GQ_ERR_CUDA, "device status word unavailable");
     const bool solo = pos && T <= SOLO_TOKENS;
