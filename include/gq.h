@@ -556,7 +556,7 @@ size_t gq_mx_scale_cols(int64_t K);   /* ceil(K / 512) * 16; 0 if K <= 0 or K % 
 gq_status gq_quantize_mx(const void *x, int64_t ldx, gq_type type, gq_mx_kind kind, void *codes, uint8_t *scales,
                          int64_t M, int64_t K, cudaStream_t stream);
 /* The values that codes and scales stand for, into y [M][K] of `type` (exact but for values below
- * 2^-126 and, in bf16, below 2^-133 steps; NaN for scale 255). */
+ * 2^-126 and, in bf16, below 2^-133 steps; infinite from 2^128 on; NaN for scale 255). */
 gq_status gq_dequantize_mx(const void *codes, const uint8_t *scales, gq_mx_kind kind, void *y, gq_type type,
                            int64_t M, int64_t K, cudaStream_t stream);
 
