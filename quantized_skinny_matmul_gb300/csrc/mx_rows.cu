@@ -222,46 +222,16 @@ struct Raw {
     }
 };
 
-// Group g of 8 values of h = x + residual, rounded to T.
-template <typename T>
-__device__ __forceinline__ void load_h(const T *x, const T *res, int g, float (&h)[8]) {
-    Raw<T> a, b;
-    a.load(x + g * 8);
-    if (res) {
-        b.load(res + g * 8);
-        a.add(b);
-    }
-    a.widen(h);
-}
-
-// 1 / sqrt(mean(h^2) + eps) of a row in two terms, by one warp.
-template <typename T>
-__device__ __noinline__ Two exact_r(const NormParams &p, const T *x, const T *res, int lane) {
-    Two sum{0.0f, 0.0f};
-    for (int g = lane; g < p.K / 8; g += 32) {
-        float h[8];
-        load_h(x, res, g, h);
-#pragma unroll
-        for (int i = 0; i < 8; i++) sum = add(sum, two_prod(h[i], h[i]));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        sum = add(sum, Two{__shfl_xor_sync(0xffffffffu, sum.hi, d), __shfl_xor_sync(0xffffffffu, sum.lo, d)});
-    // mean = sum / K: the quotient of the first terms, and what it leaves over
-    const float k = (float)p.K, q = sum.hi / k;
-    return two_rsqrt(add(fast_two_sum(q, (fmaf(-q, k, sum.hi) + sum.lo) / k), Two{p.eps_hi, p.eps_lo}));
-}
-
 // One CTA per row (in turn).  Thread t holds the groups of 8 values t, t + T, .. (C of them at most) from the load to the
 // output, so that the row is read once.  The codes are those of the exact y, mostly without exact arithmetic.
 // In f32, with positive terms only, the sum of squares is off by 17 roundings at most (4 additions in a thread, 3 levels
 // there, 5 in the warp, 5 over the warps), which counts half in r, and a scaled value h w r 2^(127 - b) by 14 in
 // all, less than 2^-20 of itself.  So if it gives the same code with 2^-20 more and with 2^-20 less (and so does the
-// largest its scale), that is the code; else (one group of 256 values in 200) the warp forms r and its values in
-// two terms, reading the row again.
+// largest its scale), that is the code; if one value of the row does not (one row of 4096 in ten), the CTA forms the sum, r and
+// the row's values again in two terms, from what it holds.
 template <typename T, int C>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
-    __shared__ float part[32];
+    __shared__ Two part[32];
     const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
@@ -280,30 +250,30 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     for (int c = 0; c < C; c++) rx[c] = rr[c] = Raw<T>{};
     if (blockIdx.x < p.M) load(blockIdx.x);
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-        const T *x = static_cast<const T *>(p.x) + row * p.ldx;
-        const T *res = p.res ? static_cast<const T *>(p.res) + row * p.ldr : nullptr;
-        float h[C][8];
+        Raw<T> h[C];
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
             if (p.res) rx[c].add(rr[c]);
-            if (p.h && g < groups) rx[c].store(static_cast<T *>(p.h) + row * p.ldh + g * 8);
-            rx[c].widen(h[c]);
+            h[c] = rx[c];
+            if (p.h && g < groups) h[c].store(static_cast<T *>(p.h) + row * p.ldh + g * 8);
         }
         if (row + gridDim.x < p.M) load(row + gridDim.x);
         float sq[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < C; c++) {
+            float v[8];
+            h[c].widen(v);
 #pragma unroll
-            for (int i = 0; i < 8; i++) sq[i] = fmaf(h[c][i], h[c][i], sq[i]);
+            for (int i = 0; i < 8; i++) sq[i] = fmaf(v[i], v[i], sq[i]);
         }
         float sum = ((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7]));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (warps > 1) {
-            if (lane == 0) part[warp] = sum;
+            if (lane == 0) part[warp].hi = sum;
             __syncthreads();
-            sum = lane < warps ? part[lane] : 0.0f;
+            sum = lane < warps ? part[lane].hi : 0.0f;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         }
@@ -311,8 +281,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         float r;
         asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(mean));
         r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.0f), r);          // to a unit
-        bool exact = false;
-        Two r2;
+        bool unsure = false;
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
@@ -320,11 +289,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             const bool live = g < groups;
             if (!__any_sync(0xffffffffu, live)) continue;
             float w[8], v[8];
+            h[c].widen(v);
+            if (p.w) {
+                load8(p.w + (live ? g * 8 : 0), w);
 #pragma unroll
-            for (int i = 0; i < 8; i++) w[i] = 1.0f;
-            if (p.w && live) load8(p.w + g * 8, w);
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = h[c][i] * w[i];
+                for (int i = 0; i < 8; i++) v[i] *= w[i];
+            }
             if (p.y && live) {
                 float y[8];
 #pragma unroll
@@ -340,35 +310,75 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[i]));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2)) * r;
-            int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
+            const int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
             const float inv = mx_inverse(b) * r, less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
-            uint32_t lo[4], hi[4];
+            uint32_t lo[4], differ = 0;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 lo[i] = e4m3x2(v[2 * i] * less, v[2 * i + 1] * less);
-                hi[i] = e4m3x2(v[2 * i] * more, v[2 * i + 1] * more);
+                differ |= lo[i] ^ e4m3x2(v[2 * i] * more, v[2 * i + 1] * more);
             }
-            uint2 code = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             // (tiny, infinite and NaN blocks are not sure: there the f32 values are not that close)
-            const bool sure = ((lo[0] ^ hi[0]) | (lo[1] ^ hi[1]) | (lo[2] ^ hi[2]) | (lo[3] ^ hi[3])) == 0 &&
-                              mx_scale_byte(__float_as_uint(most * (1.0f - 0x1p-20f)), false) == b && b > 0 && b < 255 && inv < 0x1p100f &&
-                              r > 0x1p-60f && most > 0x1p-90f;
-            if (__any_sync(0xffffffffu, live && !sure)) {
-                if (!exact) r2 = exact_r<T>(p, x, res, lane);
-                exact = true;
-                float odd[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) odd[i] = to_odd(mul(two_prod(h[c][i], w[i]), r2));
-                b = mx_scale_byte(block_amax(odd), false);
-                code = codes8<false>(odd, mx_inverse(b));
+            const bool sure = differ == 0 && mx_scale_byte(__float_as_uint(most * (1.0f - 0x1p-20f)), false) == b && b > 0 && b < 255 &&
+                              inv < 0x1p100f && r > 0x1p-60f && most > 0x1p-90f;
+            if (live) {
+                unsure |= !sure;
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = (uint8_t)b;
             }
+        }
+        if (p.codes && threadIdx.x < p.S - p.K / 32) p.scales[row * p.S + p.K / 32 + threadIdx.x] = 0;
+        // (the barrier also frees `part`)
+        if (!(warps > 1 ? __syncthreads_or(unsure) : __any_sync(0xffffffffu, unsure))) continue;
+        Two total{0.0f, 0.0f};
+#pragma unroll 1
+        for (int i = 0; i < 8; i++) {
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                float v[8], x = 0.0f;
+                h[c].widen(v);
+#pragma unroll
+                for (int u = 0; u < 8; u++)
+                    if (u == i) x = v[u];
+                const Two square = two_prod(x, x), next = two_sum(total.hi, square.hi);
+                total = {next.hi, total.lo + (next.lo + square.lo)};
+            }
+        }
+        total = fast_two_sum(total.hi, total.lo);
+#pragma unroll 1
+        for (int d = 16; d > 0; d >>= 1)
+            total = add(total, Two{__shfl_xor_sync(0xffffffffu, total.hi, d), __shfl_xor_sync(0xffffffffu, total.lo, d)});
+        if (warps > 1) {
+            if (lane == 0) part[warp] = total;
+            __syncthreads();
+            total = lane < warps ? part[lane] : Two{0.0f, 0.0f};
+#pragma unroll 1
+            for (int d = 16; d > 0; d >>= 1)
+                total = add(total, Two{__shfl_xor_sync(0xffffffffu, total.hi, d), __shfl_xor_sync(0xffffffffu, total.lo, d)});
+        }
+        // mean = total / K: the quotient of the first terms, and what it leaves over
+        const float k = (float)p.K, q = total.hi / k;
+        const Two r2 = two_rsqrt(add(fast_two_sum(q, (fmaf(-q, k, total.hi) + total.lo) / k), Two{p.eps_hi, p.eps_lo}));
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const int g = threadIdx.x + c * blockDim.x;
+            const bool live = g < groups;
+            if (!__any_sync(0xffffffffu, live)) continue;
+            float v[8], w[8];
+            h[c].widen(v);
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = 1.0f;
+            if (p.w) load8(p.w + (live ? g * 8 : 0), w);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = to_odd(mul(two_prod(v[i], w[i]), r2));
+            const int b = mx_scale_byte(block_amax(v), false);
+            const uint2 code = codes8<false>(v, mx_inverse(b));
             if (live) {
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = code;
                 if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = (uint8_t)b;
             }
         }
-        if (p.codes && threadIdx.x < p.S - p.K / 32) p.scales[row * p.S + p.K / 32 + threadIdx.x] = 0;
-        if (warps > 1) __syncthreads();                            // `part` is free
+        if (warps > 1) __syncthreads();                    // `part` is free
     }
 }
 

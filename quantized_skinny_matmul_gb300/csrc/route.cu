@@ -125,17 +125,20 @@ __device__ __noinline__ double sum64(const RouteParams &p, int64_t t, float m, i
     return warp_sum(sum);
 }
 
-// Token t in 64 bits, from the start; lane j < k returns the j-th choice.  An expert's value is computed again for each
-// choice: this path is for few tokens, and short.
+// Token t in 64 bits, from the start; lane j < k returns the j-th choice.  With groups the experts' values are formed once,
+// in shared memory (a few microseconds: this GPU has few 64-bit units); without, again for each choice (for tokens with more
+// than 32 values closer than f32 can tell).
 __device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, double sum, double *shared, int lane) {
     uint32_t allowed = 0xffffffffu;
-    const int n = p.E / p.groups;
-    if (p.top_groups < p.groups) {
-        for (int e = lane; e < p.E; e += 32) {
-            const float z = logit(p, t, e);
-            // without a bias, and where no sums are compared, the logits decide
-            shared[e + e / n * p.lanes] = p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : p.group_best == 2 ? score64(p, z, m, sum) : (double)z;
-        }
+    const int n = p.per_group;
+    const bool grouped = p.top_groups < p.groups, sums = !p.bias && p.group_best == 2;
+    // without a bias, and where no sums are compared, the logits decide
+    auto value = [&](int e) {
+        const float z = logit(p, t, e);
+        return p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : (double)z;
+    };
+    if (grouped) {
+        for (int e = lane; e < p.E; e += 32) shared[e + e / n * p.lanes] = sums ? score64(p, logit(p, t, e), m, sum) : value(e);
         __syncwarp();
         double gap;
         allowed = best_groups<double>(shared, n, p.groups, p.log_lanes, p.top_groups, p.group_best, lane, gap);
@@ -148,12 +151,12 @@ __device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, d
         int at = 0x7fffffff;
         for (int e = lane; e < p.E; e += 32) {
             if (!(allowed >> (e / n) & 1u)) continue;
-            const float z = logit(p, t, e);
-            const uint64_t c = order64((p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : (double)z) + 0.0);
+            const uint64_t c = order64((grouped && !sums ? shared[e + e / n * p.lanes] : value(e)) + 0.0);
             // behind the last choice in the order of values, then indices
             if ((c < last_key || (c == last_key && e > last)) && c > key) key = c, at = e;
         }
         const uint64_t top = warp_max64(key);
+        if (top == 0) break;
         const int e = (int)__reduce_min_sync(0xffffffffu, key == top ? (uint32_t)at : 0x7fffffffu);
         if (lane == j) id = e;
         last_key = top;
@@ -407,7 +410,9 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
             }
             id = choose<V, T>(p, t, z, bias, group, m, sum, shared, lane);
             if (lane < p.k) {
-                const float chosen = plain(row[id]);
+                // (a bias that is not finite could leave a place empty)
+                id = (uint32_t)id < (uint32_t)p.E ? id : -1;
+                const float chosen = id < 0 ? -INFINITY : plain(row[id]);
                 w = p.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : m > -INFINITY ? expf(chosen - m) / sum : 0.0f;
             }
             if (p.renormalize) {
