@@ -209,7 +209,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     return v;
 }
 // Whether a phase is over, without waiting.  Asked ahead of time: an answer takes over a hundred cycles.
-__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) { return mbar_try_wait(bar, parity); }
+__device__ __forceinline__ bool ready(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // A place in the ring of stages and the parity of its turn.
 template <int ST>
 struct Ring {
@@ -688,22 +693,40 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int z = 1; z < split; z++) arrive_remote(map_shared_rank_addr(bar(PART_EMPTY), (uint32_t)z));
             }
             const int n = t.g * MX_TILE + 32 * q + lane;
+            // Chunk by chunk, the sums moved up by one chunk each time: what the loop's body works on is always chunk 0.
+            // (All chunks written out are more code than the instruction caches hold, and every tile would fetch it
+            // again: 276 us for 32760 rows of the gated unit, 167 for its way back.)
+            auto next_chunk = [&] {
+#pragma unroll
+                for (int a = 0; a < C::NA; a++)
+#pragma unroll
+                    for (int j = 0; j + 1 < C::MINE; j++)
+#pragma unroll
+                        for (int c = 0; c < C::CW; c++) acc[a][j][c] = acc[a][j + 1][c];
+            };
             if constexpr (!GATED) {
-                if (n < p.N) {
-                    auto store = [&](auto *dst) {
-                        const int64_t ldd = p.ldd;
-                        dst += (int64_t)(t.r0 + half * C::CW) * ldd + n;
+                auto store = [&](auto *dst) {
+                    const int64_t ldd = p.ldd;
+                    dst += (int64_t)(t.r0 + half * C::CW) * ldd + n;
+#pragma unroll 1
+                    for (int col = half * C::CW; col < t.n; col += 2 * C::CW, dst += C::CW * ldd) {
+                        if (n < p.N) {
+                            if (col + C::CW <= t.n) {
 #pragma unroll
-                        for (int j = 0; j < C::MINE; j++)
+                                for (int c = 0; c < C::CW; c++, dst += ldd) put(dst, acc[0][0][c]);
+                            } else {
 #pragma unroll
-                            for (int c = 0; c < C::CW; c++)
-                                if ((2 * j + half) * C::CW + c < t.n) put(dst + (2 * j * C::CW + c) * ldd, acc[0][j][c]);
-                    };
-                    if (p.bf16)
-                        store(static_cast<__nv_bfloat16 *>(p.dst));
-                    else
-                        store(static_cast<float *>(p.dst));
-                }
+                                for (int c = 0; c < C::CW; c++, dst += ldd)
+                                    if (col + c < t.n) put(dst, acc[0][0][c]);
+                            }
+                        }
+                        next_chunk();
+                    }
+                };
+                if (p.bf16)
+                    store(static_cast<__nv_bfloat16 *>(p.dst));
+                else
+                    store(static_cast<float *>(p.dst));
             } else {
                 // a warp's 32 lanes are one block of 32 output values of each column's row; N is a
                 // multiple of 32, so the block is there as a whole or not at all
@@ -711,52 +734,55 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (block <= last) {
                     // lane l writes four codes of column l % 4, and lane l < 4 its scale
                     const int64_t first = t.r0 + half * C::CW + (lane & 3);
-                    uint8_t *const codes = p.codes + first * p.N + block * 32 + (lane & ~3);
-                    uint8_t *const scales = p.scales + first * p.So + block;
+                    uint8_t *codes = p.codes + first * p.N + block * 32 + (lane & ~3);
+                    uint8_t *scales = p.scales + first * p.So + block;
+#pragma unroll 1
+                    for (int col = half * C::CW; col < t.n; col += 2 * C::CW) {
+                        float(&v)[C::CW] = acc[0][0];
+                        uint32_t top[C::CW], most = 0;
 #pragma unroll
-                    for (int j = 0; j < C::MINE; j++)
+                        for (int c = 0; c < C::CW; c++) v[c] = swish(v[c]) * acc[1][0][c];
+#pragma unroll
+                        for (int c = 0; c < C::CW; c++) {
+                            top[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[c]) & 0x7FFFFFFFu);
+                            most = max(most, top[c]);
+                        }
 #pragma unroll
                         for (int c = 0; c < C::CW; c += 4) {
-                            const int col = (2 * j + half) * C::CW + c;
-                            if (col >= t.n) continue;
-                            float v[4];
-                            uint32_t top[4];
-#pragma unroll
-                            for (int x = 0; x < 4; x++) v[x] = swish(acc[0][j][c + x]) * acc[1][j][c + x];
                             // the largest magnitude, rounded up to 7/4 times a power of two where above it: its exponent, less
                             // 8, is the scale byte (mx_scale_byte), and 262 less that of the scale's inverse
+                            uint32_t e[4];
 #pragma unroll
-                            for (int x = 0; x < 4; x++) top[x] = __reduce_max_sync(0xffffffffu, __float_as_uint(v[x]) & 0x7FFFFFFFu) + 0x1FFFFFu;
-                            bool odd = false;              // a block that is tiny, infinite or NaN
+                            for (int x = 0; x < 4; x++) {
+                                e[x] = max((top[c + x] + 0x1FFFFFu) >> 23, 8u);
+                                v[c + x] *= __uint_as_float((262u - e[x]) << 23);
+                            }
+                            uint32_t word = e4m3x2(v[c], v[c + 1]) | e4m3x2(v[c + 2], v[c + 3]) << 16;
+                            uint32_t byte = (lane & 2 ? (lane & 1 ? e[3] : e[2]) : (lane & 1 ? e[1] : e[0])) - 8;
+                            if (most >= 0x7F800000u) {     // blocks with an infinity or a NaN
 #pragma unroll
-                            for (int x = 0; x < 4; x++) odd |= top[x] - (9u << 23) >= (246u << 23);
-                            uint32_t word, bytes;
-                            if (odd) {
-                                word = bytes = 0;
-#pragma unroll
-                                for (int x = 0; x < 4; x++) {
-                                    const int b = mx_scale_byte(top[x] - 0x1FFFFFu, false);
-                                    const float inv = mx_inverse(b);
-                                    word |= (inv == 0.0f ? 0u : e4m3x2(v[x] * inv, 0.0f)) << (8 * x);
-                                    bytes |= (uint32_t)b << (8 * x);
-                                }
-                            } else {
-#pragma unroll
-                                for (int x = 0; x < 4; x++) v[x] *= __uint_as_float((262u << 23) - (top[x] & 0x7F800000u));
-                                word = e4m3x2(v[0], v[1]) | e4m3x2(v[2], v[3]) << 16;
-                                const uint32_t mine = lane & 2 ? (lane & 1 ? top[3] : top[2]) : (lane & 1 ? top[1] : top[0]);
-                                bytes = ((mine >> 23) - 8) << (8 * (lane & 3));
+                                for (int x = 0; x < 4; x++)
+                                    if (top[c + x] >= 0x7F800000u) {
+                                        word &= ~(0xFFu << (8 * x));
+                                        if ((lane & 3) == x) byte = 255;
+                                    }
                             }
                             // four lanes turn their 4 x 4 codes: lane l & 3 then has column l & 3's four
                             uint32_t other = __shfl_xor_sync(0xffffffffu, word, 1);
                             word = __byte_perm(word, other, lane & 1 ? 0x3715 : 0x6240);
                             other = __shfl_xor_sync(0xffffffffu, word, 2);
                             word = __byte_perm(word, other, lane & 2 ? 0x3276 : 0x5410);
-                            if (col + (lane & 3) < t.n) {
-                                *reinterpret_cast<uint32_t *>(codes + (2 * j * C::CW + c) * (int64_t)p.N) = word;
-                                if (lane < 4) scales[(2 * j * C::CW + c) * (int64_t)p.So] = (uint8_t)(bytes >> (8 * lane));
+                            if (col + c + (lane & 3) < t.n) {
+                                *reinterpret_cast<uint32_t *>(codes) = word;
+                                if (lane < 4) *scales = (uint8_t)byte;
                             }
+                            codes += 4 * (int64_t)p.N;
+                            scales += 4 * (int64_t)p.So;
                         }
+                        codes += C::CW * (int64_t)p.N;
+                        scales += C::CW * (int64_t)p.So;
+                        next_chunk();
+                    }
                 }
                 // the scales' padding, by the warps of the rows' last block
                 if (block == last && last + 1 + lane < p.So)
