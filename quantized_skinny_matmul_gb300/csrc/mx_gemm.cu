@@ -268,12 +268,14 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsi
     return false;
 }
 
-// x / (1 + exp(-x)); the exponential and the reciprocal are the fast ones, off by a few units of f32.
+// x / (1 + exp(-x)); the exponential and the reciprocal are the fast ones, off by a few units of f32.  Both
+// flush denormals: of the exponential that leaves 1 + 0, and the reciprocal is taken of a quarter of the sum, so that
+// it has none.
 __device__ __forceinline__ float swish(float x) {
     float e, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return x * r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
+    return x * (0.25f * r);
 }
 
 // Where tiles lie, in shared memory: starts[e] tiles of BN rows (for one group of weight rows) come before
