@@ -385,26 +385,37 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
 // ---------------------------------------------------------------------------
 // the sum over a token's experts
 // ---------------------------------------------------------------------------
+// Eight columns per thread.  Bound by the rows' bytes; four of them are under way at a time, so that one token's
+// eight experts are two latencies, not eight.
 template <typename TR, typename TO>
 __global__ void __launch_bounds__(256) experts_combine_kernel(const float *__restrict__ y, int64_t R, const int32_t *__restrict__ pos,
                                                               const float *__restrict__ w, int k, const TR *res, int64_t ldr,
-                                                              TO *out, int64_t ldo, int64_t groups, int per_row) {
+                                                              TO *out, int64_t ldo, uint32_t groups, uint32_t per_row, Divisor by_row) {
+    constexpr int U = 4;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < groups; i += stride) {
-        const int64_t t = i / per_row;
-        const int g = (int)(i - t * per_row);
+    const uint32_t stride = gridDim.x * 256;
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < groups; i += stride) {
+        const uint32_t t = by_row.of(i), g = i - t * per_row;
+        const int32_t *const at = pos + (int64_t)t * k;
+        const float *const by = w + (int64_t)t * k;
         float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (res) load8(res + t * ldr + g * 8, acc);
-        for (int j = 0; j < k; j++) {
-            const int64_t r = pos[t * k + j];
-            if (r < 0 || r >= R) continue;
-            const float a = w[t * k + j];
-            float v[8];
-            load8(y + (r * per_row + g) * 8, v);
+        for (int j = 0; j < k; j += U) {
+            bool there[U];
+            float a[U], v[U][8];
 #pragma unroll
-            for (int u = 0; u < 8; u++) acc[u] = fmaf(a, v[u], acc[u]);
+            for (int x = 0; x < U; x++) {
+                const int64_t r = j + x < k ? at[j + x] : -1;
+                there[x] = r >= 0 && r < R;
+                a[x] = there[x] ? by[j + x] : 0.0f;
+                if (there[x]) load8(y + (r * per_row + g) * 8, v[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < U; x++)
+                if (there[x])
+#pragma unroll
+                    for (int u = 0; u < 8; u++) acc[u] = fmaf(a[x], v[x][u], acc[u]);
         }
         store8(out + t * ldo + g * 8, acc);
     }
@@ -501,13 +512,24 @@ gq_status launch_rms_norm_mx(const void *x, int64_t ldx, const void *res, int64_
 gq_status launch_experts_combine(const float *y, int64_t R, const int32_t *pos, const float *w, int64_t k, const void *res,
                                  int64_t ldr, bool res_bf16, void *out, int64_t ldo, bool bf16, int64_t T, int64_t N,
                                  cudaStream_t s) {
-    int per_row = (int)(N / 8), kk = (int)k;
-    int64_t groups = T * per_row;
-    void *args[] = {&y, &R, &pos, &w, &kk, &res, &ldr, &out, &ldo, &groups, &per_row};
+    uint32_t per_row = (uint32_t)(N / 8);
+    int kk = (int)k;
+    Divisor by_row = divisor(per_row);
+    const int64_t most = std::max<int64_t>(1, ((1LL << 30) - 1) / per_row);      // tokens of a launch, as above
     using B = __nv_bfloat16;
     const void *fn = res_bf16 ? (bf16 ? (const void *)experts_combine_kernel<B, B> : (const void *)experts_combine_kernel<B, float>)
                               : (bf16 ? (const void *)experts_combine_kernel<float, B> : (const void *)experts_combine_kernel<float, float>);
-    return launch_pdl(fn, dim3(grid_for(groups, 256)), dim3(256), 0, s, args, "experts combine launch");
+    for (int64_t m = 0; m < T; m += most) {
+        uint32_t groups = (uint32_t)(std::min(most, T - m) * per_row);
+        const int32_t *at = pos + m * k;
+        const float *by = w + m * k;
+        const uint8_t *from = res ? static_cast<const uint8_t *>(res) + m * ldr * (res_bf16 ? 2 : 4) : nullptr;
+        uint8_t *to = static_cast<uint8_t *>(out) + m * ldo * (bf16 ? 2 : 4);
+        void *args[] = {&y, &R, &at, &by, &kk, &from, &ldr, &to, &ldo, &groups, &per_row, &by_row};
+        gq_status st = launch_pdl(fn, dim3(grid_for(groups, 256)), dim3(256), 0, s, args, "experts combine launch");
+        if (st != GQ_OK) return st;
+    }
+    return GQ_OK;
 }
 
 }  // namespace gq
