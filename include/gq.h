@@ -604,7 +604,7 @@ typedef struct gq_expert_rows {
 } gq_expert_rows;
 
 /* dst = X . W^T with X in e4m3 blocks and W in repacked 4-bit blocks: products are exact, sums f32
- * (the tensor cores' partial sums are taken up by rounded f32 additions every 512 columns).  dst row r
+ * (the tensor cores' partial sums are taken up by rounded f32 additions every 2048 columns at the latest).  dst row r
  * at dst + r * ldd, N values of `type` (rounded once), ldd >= N.  Without a plan W is one matrix and
  * row m of dst is row m of x; with one W holds E matrices and row r of dst is the product of
  * its row of x with its expert's matrix.  Results do not depend on timing.  A plan with `rows` and more than 16 rows
