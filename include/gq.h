@@ -594,7 +594,7 @@ typedef struct gq_mx_rows {
  * (offsets int32 [E + 1] on the device).  R is the room for rows on the host's side; rows from
  * offsets[E] on are neither read nor written.  With `rows` (int32 [R]) row r of the product reads
  * row rows[r] of the activations, without it row r.  An expert whose offsets are out of range
- * (negative, decreasing, past R) has no rows, a row whose index is outside the activations reads
+ * (negative, decreasing, past R, or begin in front of the end of an earlier expert that is not) has no rows, a row whose index is outside the activations reads
  * as zeros, and either makes the next gq_last_error() return GQ_ERR_INVALID_ARG.
  * E 1 .. 1024, R < 2^30. */
 typedef struct gq_expert_rows {

@@ -350,14 +350,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
     if (warp == 0) {
-        // tiles of BN rows in front of each expert
-        int before = 0;
+        // tiles of BN rows in front of each expert; ranges are disjoint, so that the host's count of tiles bounds them
+        int before = 0, end = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            int tiles = 0;
+            int tiles = 0, r0 = 0, r1 = 0, most = 0;
             if (e < p.E) {
-                int r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.R;
-                if (r0 < 0 || r1 < r0 || r1 > p.R) {
+                r0 = p.offsets ? p.offsets[e] : 0, r1 = p.offsets ? p.offsets[e + 1] : p.R;
+                if (r0 >= 0 && r1 >= r0 && r1 <= p.R) most = r1;
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, most, d);
+                if (lane >= d) most = max(most, u);
+            }
+            int front = __shfl_up_sync(0xffffffffu, most, 1);      // the largest end of the experts in front
+            front = lane ? max(front, end) : end;
+            end = max(end, __shfl_sync(0xffffffffu, most, 31));
+            if (e < p.E) {
+                if (r0 < front || r1 < r0 || r1 > p.R) {
                     atomicOr(p.status, STATUS_RANGE);
                     r0 = r1 = 0;
                 }

@@ -456,6 +456,30 @@ def test_combine(rtype, otype, T, k, N):
         assert torch.equal(gq.experts_combine(dev(y), plan, dev(w), residual=res, out=res), got)     # in place
 
 
+@pytest.mark.parametrize("E,mean", [(5, 3), (70, 2), (5, 20)])
+def test_ranges_that_overlap_belong_to_the_first_expert(E, mean):
+    """Offsets that go back: no row is computed for two experts, and the experts behind keep theirs."""
+    N, K = 130, 96
+    w, W = weights(1, E, N, K)
+    R = E * mean
+    x, X = mx(rows(2, R, K)[1])
+    off = np.arange(E + 1, dtype=np.int32) * mean
+    off[E - 2] = 0                                       # expert E - 3 has less than none, expert E - 2 what others have
+    plan = gq.ExpertPlan(dev(off), dev(np.arange(R, dtype=np.int32)), dev(np.zeros((1, 1), np.int32)))
+    for gather in (True, False):
+        out = torch.full((R, N), 5.0, device="cuda")
+        gq.mul_mat_mxfp4(w, x, plan, gather=gather, out=out)
+        assert gq.gq_last_error() == gq.GQ_ERR_INVALID_ARG
+        for e in range(E):
+            r = slice(e * mean, (e + 1) * mean)
+            if e in (E - 3, E - 2):
+                assert (out[r] == 5).all()
+                continue
+            want, S = ref.product(X[r], W[e])
+            near(out[r], want, ref.product_tolerance(K) * S, f"expert {e}")
+    assert gq.gq_last_error() == gq.GQ_OK
+
+
 class Block:
     """norm, router, experts, sum: one feed-forward layer of experts, as it is used."""
 
