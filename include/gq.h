@@ -607,7 +607,7 @@ typedef struct gq_expert_rows {
  * (the tensor cores' partial sums are taken up by rounded f32 additions every 2048 columns at the latest).  dst row r
  * at dst + r * ldd, N values of `type` (rounded once), ldd >= N.  Without a plan W is one matrix and
  * row m of dst is row m of x; with one W holds E matrices and row r of dst is the product of
- * its row of x with its expert's matrix.  Results do not depend on timing.  A plan with `rows` and more than 16 rows
+ * its row of x with its expert's matrix.  Results do not depend on timing.  A plan with `rows` and more than 14 rows
  * for an expert on average uses the stream's workspace, up to 512 MB (grown on demand, as for the products above;
  * GQ_ERR_NO_MEMORY while the stream is captured: run the call once before capturing). */
 gq_status gq_mul_mat_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *dst,

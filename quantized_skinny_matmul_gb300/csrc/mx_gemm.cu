@@ -55,7 +55,7 @@ struct Cfg {
     static constexpr int MINE = (CHUNKS + 1) / 2;           // chunks of a warpgroup
     static constexpr bool BIG = NA * MINE * CW >= 64;       // more sums per thread than an even share of registers holds
     static constexpr bool GATHERS = BN <= 16;
-    static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;
+    static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;      // (for 64 rows two: 17 rows 9.7 us against 10.1, 65 rows 10.9 against 10.6)
     // Tensor memory: sets of accumulators, then slots of a stage's weights and scales.  The gated unit's large
     // tile has one set only; its accumulators are taken over every 16 stages (2048 columns; what is cut
     // off meanwhile, 2^-24 of the sums 64 times at most, is far below its output's 2^-4), gate before up, so
@@ -892,7 +892,8 @@ gq_status launch(MxParams p, const gq_mx_rows &x, int64_t most_tiles, cudaStream
     st = encode(&mx, x.codes, x.rows, p.K, p.rows ? 1 : C::BOX);
     if (st != GQ_OK) return st;
 
-    // K shared out where the tiles leave SMs idle, two stages a CTA at least
+    // K shared out where the tiles leave SMs idle, two stages a CTA at least ([4096, 4096], a row: 8.5 us by four, 9.1 by
+    // two, 9.8 by one)
     const int sms = sm_count();
     int split = 1;
     while (split < C::MAX_SPLIT && most_tiles * 2 * split <= sms && p.KT / (2 * split) >= 2) split *= 2;
@@ -933,21 +934,27 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     p.w = static_cast<const uint8_t *>(rep);
     p.lo = 0, p.hi = p.R;
 
-    // Rows per tile by the rows that an expert has on average (of the experts that can have any).
+    // Rows per tile by the rows that an expert has on average (of the experts that can have any).  Its rows vary about
+    // that, so with a plan a tile is taken for means up to seven eighths of it: 32 experts of [2816, 2048], us:
+    //   mean    8 rows 24.4; 10: 24.6, by tiles of 64 28.4; 14: 28.8, 28.0 (gated 21.0, 25.9); 16: 33.1, 29.1 (26.0, 26.3)
+    //   mean    40: 30.6, by larger tiles 35.9; 48: 31.4, 36.9 (29.0, 30.5); 56: 35.0, 36.9 (29.1, 29.9); 64: 42.4, 37.6 (34.6, 30.6)
+    // And tiles of 64 rows where all of them run at once ([4096, 4096]: 65 rows 10.6 us against 12.3, 256 rows 10.8 against 14.9).
+    // One row by tiles of 16 8.5 us, of 64 9.9.
     const int64_t some = std::min<int64_t>(p.E, p.R), mean = (p.R + some - 1) / some;
     auto most = [&](int bn) { return ((plan ? some : 0) + (p.R + bn - 1) / bn) * p.G; };
     if (most(16) >= (1LL << 31)) return fail(GQ_ERR_INVALID_ARG, "R=%lld rows of N=%lld are too many", (long long)p.R, (long long)N);
+    const bool few = mean <= (plan ? 14 : 16), medium = mean <= (plan ? 56 : 64) || most(64) <= sm_count();
     auto run = [&](const gq_mx_rows &rows) {
         if (gated) {
-            if (mean <= 16) return launch<16, true>(p, rows, most(16), s);
-            if (mean <= 64) return launch<64, true>(p, rows, most(64), s);
+            if (few) return launch<16, true>(p, rows, most(16), s);
+            if (medium) return launch<64, true>(p, rows, most(64), s);
             return launch<128, true>(p, rows, most(128), s);
         }
-        if (mean <= 16) return launch<16, false>(p, rows, most(16), s);
-        if (mean <= 64) return launch<64, false>(p, rows, most(64), s);
+        if (few) return launch<16, false>(p, rows, most(16), s);
+        if (medium) return launch<64, false>(p, rows, most(64), s);
         return launch<176, false>(p, rows, most(176), s);
     };
-    if (!p.rows || mean <= 16) return run(x);
+    if (!p.rows || few) return run(x);
     // the rows in the plan's order, as many at a time as the workspace's share holds; the kernel sees them as rows lo .. of an
     // array that begins lo rows earlier
     const int64_t row_bytes = K + p.S, some_rows = std::min<int64_t>(p.R, std::max<int64_t>(1, GATHER_BYTES / row_bytes));
