@@ -22,6 +22,10 @@
 //              to another set of accumulators; then they store the tile.
 // CTAs take tiles in turn (persistent), those of one expert's weight rows next to each other.  With few
 // tiles a cluster of 2 or 4 CTAs shares a tile's columns; the first adds the others' sums in order.
+//
+// Measured: 2047 rows by [4096, 11008] 81 us, 2.3 PFLOP/s, 13 TB/s from L2 (each CTA fetches its own operands: that bounds the
+// large tiles; the tensor pipe is busy for 48 %); 61 tokens on 8 of 64 experts of [2816, 2048] 48 us, 4.2 TB/s from memory
+// (a stage's latencies); a row by [4096, 4096] 6.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -711,8 +715,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const int n = t.g * MX_TILE + 32 * q + lane;
             // Chunk by chunk, the sums moved up by one chunk each time: what the loop's body works on is always chunk 0.
-            // (All chunks written out are more code than the instruction caches hold, and every tile would fetch it
-            // again: 276 us for 32760 rows of the gated unit, 167 for its way back.)
+            // (All chunks written out are more code than the instruction caches hold, and every tile fetches it
+            // again: 32760 rows of the gated unit and back 537 us in all, so 427.)
             auto next_chunk = [&] {
 #pragma unroll
                 for (int a = 0; a < C::NA; a++)
@@ -819,7 +823,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Rows lo .. hi - 1 of the plan, as far as they are in use, brought into its order: codes and scales, 16 bytes a thread and
-// turn.  A row whose index is out of range becomes zeros.
+// turn.  A row whose index is out of range becomes zeros.  18 us for 32760 rows of 2048; four-row copies by the product's one
+// copying thread keep up with tiles of 16 rows only.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                           const int32_t *__restrict__ rows, const int32_t *__restrict__ used,
                                                           uint8_t *__restrict__ to_codes, uint8_t *__restrict__ to_scales, int lo, int hi,
