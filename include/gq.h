@@ -614,8 +614,9 @@ gq_status gq_mul_mat_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const g
                               int64_t ldd, gq_type type, int64_t N, int64_t K, cudaStream_t stream);
 
 /* The same for rows of f32 or bf16 (strides as in gq_quantize_mx), quantized to e4m3 blocks inside
- * the call, in the stream's workspace (grown on demand, as for the products above; GQ_ERR_NO_MEMORY
- * while the stream is captured: run the call once before capturing). */
+ * the call, for M > 2 in the stream's workspace (grown on demand, as for the products above; GQ_ERR_NO_MEMORY
+ * while the stream is captured: run the call once before capturing).  Bit for bit the product of the blocks of
+ * gq_quantize_mx. */
 gq_status gq_mul_mat_mxfp4(const void *repacked, const void *x, int64_t ldx, gq_type xtype, void *dst, int64_t ldd,
                            gq_type type, int64_t M, int64_t N, int64_t K, cudaStream_t stream);
 

@@ -175,6 +175,10 @@ gq_status gq_mul_mat_mxfp4(const void *repacked, const void *x, int64_t ldx, gq_
     GQ_TRY(check_ptr(x, "x"));
     GQ_TRY(check_ptr(dst, "dst"));
     GQ_TRY(check_device());
+    if (M <= MX_FEW_ROWS) {
+        GQ_TRY(launch_mx_product_few(repacked, x, ldx, xtype == GQ_TYPE_BF16, dst, ldd, type == GQ_TYPE_BF16, M, N, K, stream));
+        return ok();
+    }
     Workspace ws;
     const size_t scales = (size_t)M * gq_mx_scale_cols(K);
     GQ_TRY(get_workspace(stream, 0, scales + (size_t)M * K, &ws));

@@ -10,7 +10,7 @@
 //              bulk copy, the activations' codes by a tensor copy, of four rows at a time where a plan names
 //              them (16-row tiles; for larger ones that would be too many copies for a thread, and a kernel in front
 //              brings the rows into the plan's order);
-//   warps 2, 3     copy the activations' scales;
+//   warps 2, 3     copy the activations' scales (of one or two rows of values: quantize them);
 //   warps 12 .. 19  two teams, for every other stage each (a stage is mostly latency).  A weight row per thread: 64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of
 //              each (the form of 4-bit operands in tensor memory), and go there, and so do the scales of both
 //              operands.  The tiles hold the codes so that three instructions place eight of them;
@@ -59,6 +59,7 @@ struct Cfg {
     static constexpr int MINE = (CHUNKS + 1) / 2;           // chunks of a warpgroup
     static constexpr bool BIG = NA * MINE * CW >= 64;       // more sums per thread than an even share of registers holds
     static constexpr bool GATHERS = BN <= 16;
+    static constexpr bool QUANTIZES = BN <= 16 && !GATED;   // takes rows of f32 or bf16 too
     static constexpr int MAX_SPLIT = BN <= 16 ? 4 : 1;      // (for 64 rows two: 17 rows 9.7 us against 10.1, 65 rows 10.9 against 10.6)
     // Tensor memory: sets of accumulators, then slots of a stage's weights and scales.  The gated unit's large
     // tile has one set only; its accumulators are taken over every 16 stages (2048 columns; what is cut
@@ -119,6 +120,9 @@ struct MxParams {
     int64_t ldd, x_rows;
     int N, K, KT, G, S, So;        // S, So: scale bytes per row of x and of the gated output
     int E, R, split, bf16;
+    const void *values;            // rows to quantize (no plan, at most MX_FEW_ROWS), instead of x's codes and scales
+    int64_t ldv;
+    int values_bf16;
 };
 
 // ---------------------------------------------------------------------------
@@ -412,7 +416,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint8_t *w = p.w + (((int64_t)t.e * C::NA * p.G + t.g) * p.KT + kt0) * MX_TILE_BYTES;
                 const int64_t up = (int64_t)p.G * p.KT * MX_TILE_BYTES;    // from the gate's tile to the up matrix's
                 const int parts = t.n > C::BOX ? C::PARTS : 1;
-                const uint32_t bytes = (uint32_t)(C::NA * MX_TILE_BYTES + parts * C::BOX * 128);
+                const bool quantizes = C::QUANTIZES && p.values;
+                const uint32_t bytes = (uint32_t)(C::NA * MX_TILE_BYTES + (quantizes ? 0 : parts * C::BOX * 128));
                 int4 from[4];                              // gathered rows; past the tile and outside x: zeros
                 if (C::GATHERS && p.rows)
 #pragma unroll
@@ -439,6 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int a = 0; a < C::NA; a++)
                         bulk_g2s(smem_addr(smem + C::w) + (uint32_t)((ring.st * C::NA + a) * MX_TILE_BYTES), w + a * up, MX_TILE_BYTES, raw);
+                    if (quantizes) continue;
                     if (C::GATHERS && p.rows) {
 #pragma unroll
                         for (int u = 0; u < 4; u++)
@@ -518,27 +524,86 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return r;
         };
-        for (int i = cluster; i < tiles && !failed; i += clusters) {
-            const Tile t = tile_at<BN>(p, where, i);
+        // One or two rows that are not quantized yet: these threads write the codes too, those of 8 stages at a time (a quarter
+        // of a block each, four times), the next ones' values under way.  Rows past them hold anything: their columns of the sums
+        // are not stored.
+        auto quantize = [&](const auto *values) {
+            constexpr int many = 8;
+            const int r = (x >> 4) & 1, block = (x >> 2) & 3;      // row, block of the stage (u * 2 + x / 32)
+            for (int i = cluster; i < tiles && !failed; i += clusters) {
+                const Tile t = tile_at<BN>(p, where, i);
+                float v[4][8];
+                auto load = [&](int k) {
 #pragma unroll
-            for (int j = 0; j < SROWS; j++) scale_row[j] = row(t, j * 64 + x);
-            for (int k = 0; k < nk; k++) {
-                const int kt = kt0 + k;
-                if (filled == C::ST) {
-                    if (!free && !mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
+                    for (int u = 0; u < 4; u++) {
+                        const int stage = k + u * 2 + (x >> 5), col = (kt0 + stage) * MX_TILE + block * QK + (x & 3) * 8;
+#pragma unroll
+                        for (int c = 0; c < 8; c++) v[u][c] = 0.0f;
+                        if (stage < nk && r < t.n && col < p.K) load8(values + (t.r0 + r) * p.ldv + col, v[u]);
+                    }
+                };
+                load(0);
+                for (int k = 0; k < nk; k += many) {
+                    uint2 code[4];
+                    int byte[4];
+#pragma unroll
+                    for (int u = 0; u < 4; u++) {
+                        byte[u] = mx_scale_byte(block_amax(v[u]), false);
+                        code[u] = codes8<false>(v[u], mx_inverse(byte[u]));
+                    }
+                    const int stages = min(many, nk - k);
+                    if (k + many < nk) load(k + many);
+                    Ring<C::ST> at = ring;
+                    for (int j = 0; j < stages; j++, at.next()) {
+                        if (filled < C::ST)
+                            filled++;
+                        else if (!failed && !mbar_wait(bar(EMPTY + at.st), at.turn ^ 1, p.status))
+                            failed = true;
+                    }
                     failed = __any_sync(0xffffffffu, failed);
                     if (failed) break;
-                } else {
-                    filled++;
-                }
-                const uint32_t scales = smem_addr(smem + C::sb) + (uint32_t)(ring.st * C::SB_STAGE + x * 4);
 #pragma unroll
-                for (int j = 0; j < SROWS; j++)
-                    if (j * 64 + x < C::NR * 32)
-                        copy4(scales + j * 256, p.x_scales + (scale_row[j] >= 0 ? (int64_t)scale_row[j] * p.S + kt * 4 : 0), scale_row[j] >= 0);
-                arrive_copied(bar(SCALES + ring.st));
-                ring.next();
-                free = filled == C::ST && ready(bar(EMPTY + ring.st), ring.turn ^ 1);
+                    for (int u = 0; u < 4; u++) {
+                        const int j = u * 2 + (x >> 5), st = ring.st + j < C::ST ? ring.st + j : ring.st + j - C::ST;
+                        if (j >= stages) continue;
+                        // (16 bytes' place in a row of 128: swizzled by the row)
+                        uint8_t *const to = smem + C::b + st * C::B_STAGE + r * 128 + ((block * 2 + ((x & 3) >> 1)) ^ r) * 16;
+                        *reinterpret_cast<uint2 *>(to + (x & 1) * 8) = code[u];
+                        if ((x & 3) == 0) smem[C::sb + st * C::SB_STAGE + r * 4 + block] = (uint8_t)byte[u];
+                    }
+                    fence_proxy_async_shared();            // (the MMAs read the codes)
+                    for (int j = 0; j < stages; j++, ring.next()) mbar_arrive(bar(SCALES + ring.st));
+                }
+            }
+        };
+        if (C::QUANTIZES && p.values) {
+            if (p.values_bf16)
+                quantize(static_cast<const __nv_bfloat16 *>(p.values));
+            else
+                quantize(static_cast<const float *>(p.values));
+        } else {
+            for (int i = cluster; i < tiles && !failed; i += clusters) {
+                const Tile t = tile_at<BN>(p, where, i);
+#pragma unroll
+                for (int j = 0; j < SROWS; j++) scale_row[j] = row(t, j * 64 + x);
+                for (int k = 0; k < nk; k++) {
+                    const int kt = kt0 + k;
+                    if (filled == C::ST) {
+                        if (!free && !mbar_wait(bar(EMPTY + ring.st), ring.turn ^ 1, p.status)) failed = true;
+                        failed = __any_sync(0xffffffffu, failed);
+                        if (failed) break;
+                    } else {
+                        filled++;
+                    }
+                    const uint32_t scales = smem_addr(smem + C::sb) + (uint32_t)(ring.st * C::SB_STAGE + x * 4);
+#pragma unroll
+                    for (int j = 0; j < SROWS; j++)
+                        if (j * 64 + x < C::NR * 32)
+                            copy4(scales + j * 256, p.x_scales + (scale_row[j] >= 0 ? (int64_t)scale_row[j] * p.S + kt * 4 : 0), scale_row[j] >= 0);
+                    arrive_copied(bar(SCALES + ring.st));
+                    ring.next();
+                    free = filled == C::ST && ready(bar(EMPTY + ring.st), ring.turn ^ 1);
+                }
             }
         }
         copy_wait();                                    // (nothing of this CTA's shared memory is under way at its end)
@@ -894,8 +959,12 @@ gq_status launch(MxParams p, const gq_mx_rows &x, int64_t most_tiles, cudaStream
         if (dev >= 0 && dev < MAX_DEV) allowed[dev].store(true, std::memory_order_release);
     }
     CUtensorMap mx;
-    st = encode(&mx, x.codes, x.rows, p.K, p.rows ? 1 : C::BOX);
-    if (st != GQ_OK) return st;
+    if (p.values) {
+        mx = {};                                           // (nothing is copied by it)
+    } else {
+        st = encode(&mx, x.codes, x.rows, p.K, p.rows ? 1 : C::BOX);
+        if (st != GQ_OK) return st;
+    }
 
     // K shared out where the tiles leave SMs idle, two stages a CTA at least ([4096, 4096], a row: 8.5 us by four, 9.1 by
     // two, 9.8 by one)
@@ -920,24 +989,44 @@ gq_status launch(MxParams p, const gq_mx_rows &x, int64_t most_tiles, cudaStream
     return check_cuda(cudaLaunchKernelEx(&cfg, kernel, mx, p), "mx product launch");
 }
 
+// What a product's operands do not decide.
+gq_status product_params(MxParams *p, const void *rep, int64_t N, int64_t K, int64_t x_rows) {
+    *p = MxParams{};
+    p->status = device_status_word();
+    if (!p->status) return fail(GQ_ERR_CUDA, "device status word unavailable");
+    p->N = (int)N, p->K = (int)K, p->x_rows = x_rows;
+    p->G = (int)((N + MX_TILE - 1) / MX_TILE), p->KT = (int)((K + MX_TILE - 1) / MX_TILE);
+    p->S = (int)gq_mx_scale_cols(K);
+    p->w = static_cast<const uint8_t *>(rep);
+    return GQ_OK;
+}
+
 }  // namespace
+
+gq_status launch_mx_product_few(const void *rep, const void *values, int64_t ldv, bool values_bf16, void *dst, int64_t ldd, bool bf16,
+                                int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+    MxParams p;
+    const gq_status st = product_params(&p, rep, N, K, M);
+    if (st != GQ_OK) return st;
+    p.E = 1, p.R = p.hi = (int)M;
+    p.values = values, p.ldv = ldv, p.values_bf16 = values_bf16;
+    p.dst = dst, p.ldd = ldd, p.bf16 = bf16;
+    return launch<16, false>(p, gq_mx_rows{M, nullptr, nullptr}, p.G, s);
+}
 
 gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_expert_rows *plan, void *dst, int64_t ldd,
                             bool bf16, void *codes, uint8_t *scales, int64_t N, int64_t K, cudaStream_t s) {
-    MxParams p{};
-    p.status = device_status_word();
-    if (!p.status) return fail(GQ_ERR_CUDA, "device status word unavailable");
+    MxParams p;
+    gq_status st = product_params(&p, rep, N, K, x.rows);
+    if (st != GQ_OK) return st;
     const bool gated = codes != nullptr;
     p.E = plan ? (int)plan->E : 1;
     p.R = plan ? (int)plan->R : (int)x.rows;
     p.offsets = plan ? plan->offsets : nullptr;
     p.rows = plan ? plan->rows : nullptr;
-    p.N = (int)N, p.K = (int)K, p.bf16 = bf16, p.ldd = ldd, p.x_rows = x.rows;
-    p.G = (int)((N + MX_TILE - 1) / MX_TILE), p.KT = (int)((K + MX_TILE - 1) / MX_TILE);
-    p.S = (int)gq_mx_scale_cols(K), p.So = gated ? (int)gq_mx_scale_cols(N) : 0;
+    p.bf16 = bf16, p.ldd = ldd, p.So = gated ? (int)gq_mx_scale_cols(N) : 0;
     p.dst = dst, p.codes = static_cast<uint8_t *>(codes), p.scales = scales, p.x_scales = x.scales;
-    p.w = static_cast<const uint8_t *>(rep);
-    p.lo = 0, p.hi = p.R;
+    p.hi = p.R;
 
     // Rows per tile by the rows that an expert has on average (of the experts that can have any).  Its rows vary about
     // that, so with a plan a tile is taken for means up to seven eighths of it: 32 experts of [2816, 2048], us:
@@ -964,7 +1053,7 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     // array that begins lo rows earlier
     const int64_t row_bytes = K + p.S, some_rows = std::min<int64_t>(p.R, std::max<int64_t>(1, GATHER_BYTES / row_bytes));
     Workspace ws;
-    gq_status st = get_workspace(s, 0, (size_t)(some_rows * row_bytes), &ws);
+    st = get_workspace(s, 0, (size_t)(some_rows * row_bytes), &ws);
     if (st != GQ_OK) return st;
     const int32_t *from = p.rows, *used = p.offsets + p.E;
     uint8_t *codes_to = ws.data, *scales_to = ws.data + some_rows * K;

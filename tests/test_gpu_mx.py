@@ -456,6 +456,42 @@ def test_combine(rtype, otype, T, k, N):
         assert torch.equal(gq.experts_combine(dev(y), plan, dev(w), residual=res, out=res), got)     # in place
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 7, 8, 9, 16, 17])
+def test_product_of_values_is_the_product_of_their_blocks(M, dtype):
+    """Bit for bit, however the rows are quantized on the way: short, ragged and long rows, one tile and many, special blocks."""
+    for N, K, ld in ((1, 32, 32), (130, 96, 104), (300, 992, 992), (128 * 3, 4096 + 160, 4256 + 8), (20011, 320, 320), (130, 15008, 15008)):
+        w, _ = weights(M, 1, N, K)
+        room = torch.randn((M, ld), generator=torch.Generator("cuda").manual_seed(K + M), device="cuda")
+        room[:, K:] = float("nan")                       # between the rows
+        x = room.to(dtype)[:, :K]
+        x[M // 2, :32] = 0
+        x[0, 32:64] *= 1e-38
+        if K > 64 and M > 1:
+            x[M - 1, 64 + M] = float("inf")
+        got = gq.mul_mat_mxfp4(w, x)
+        want = gq.mul_mat_mxfp4(w, gq.quantize_mx(x))
+        assert torch.equal(torch.nan_to_num(got, nan=7.5), torch.nan_to_num(want, nan=7.5)), (N, K)
+        assert torch.isnan(want[:M - 1]).sum() == 0 and (M == 1 or K <= 64 or torch.isnan(want[M - 1]).all())
+    assert gq.gq_last_error() == gq.GQ_OK
+
+
+def test_product_of_few_values_needs_no_workspace():
+    """Captured on a stream that never ran a product."""
+    w, _ = weights(3, 1, 256, 512)
+    x = torch.randn((2, 512), device="cuda")
+    want = gq.mul_mat_mxfp4(w, x)
+    out = torch.zeros_like(want)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        gq.mul_mat_mxfp4(w, x, out=out)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("E,mean", [(5, 3), (70, 2), (5, 20)])
 def test_ranges_that_overlap_belong_to_the_first_expert(E, mean):
     """Offsets that go back: no row is computed for two experts, and the experts behind keep theirs."""
