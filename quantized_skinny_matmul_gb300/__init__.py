@@ -976,17 +976,21 @@ def _matrix(x, name: str):
     return M, K, ld if M > 1 else K, _mx_type(x.dtype, name)
 
 
-class MXRows:
-    """Rows in microscaled blocks: codes uint8 [rows, K] (e4m3) or [rows, K / 2] (e2m1), scales uint8 [rows, S]."""
+class _Fixed:
+    """What calls are given pointers and sizes of: its fields stay as they were made."""
 
-    __slots__ = ("kind", "rows", "K", "codes_ptr", "scales_ptr", "_codes", "_scales", "_buffer", "_struct")
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be changed; make a new {type(self).__name__}")
+
+
+class MXRows(_Fixed):
+    """Rows in microscaled blocks: codes uint8 [rows, K] (e4m3) or [rows, K / 2] (e2m1), scales uint8 [rows, S]."""
 
     def __init__(self, codes, scales, kind: int = GQ_MX_E4M3):
         rows, width = codes.shape
-        self.kind, self.rows, self.K = kind, rows, width * (2 if kind == GQ_MX_E2M1 else 1)
-        self.codes_ptr = _cuda(codes, "uint8", codes.shape, "codes")
-        self.scales_ptr = _cuda(scales, "uint8", (rows, gq_mx_scale_cols(self.K)), "scales")
-        self._codes, self._scales, self._buffer, self._struct = codes, scales, None, None
+        K = width * (2 if kind == GQ_MX_E2M1 else 1)
+        c, s = _cuda(codes, "uint8", codes.shape, "codes"), _cuda(scales, "uint8", (rows, gq_mx_scale_cols(K)), "scales")
+        self.__dict__.update(kind=kind, rows=rows, K=K, codes_ptr=c, scales_ptr=s, _codes=codes, _scales=scales, _buffer=None, _struct=None)
 
     @classmethod
     def empty(cls, rows: int, K: int, kind: int = GQ_MX_E4M3, device="cuda"):
@@ -995,24 +999,23 @@ class MXRows:
             raise ValueError(f"expected rows of a multiple of 32 values, got {(rows, K)}")
         self = cls.__new__(cls)
         width = K // 2 if kind == GQ_MX_E2M1 else K
-        self._buffer = (_th or _torch()).empty(rows * (width + (K + 511) // 512 * 16), dtype=_uint8, device=device)
-        self.kind, self.rows, self.K = kind, rows, K
-        self.codes_ptr = self._buffer.data_ptr()
-        self.scales_ptr = self.codes_ptr + rows * width
-        self._codes = self._scales = self._struct = None
+        buffer = (_th or _torch()).empty(rows * (width + (K + 511) // 512 * 16), dtype=_uint8, device=device)
+        at = buffer.data_ptr()
+        self.__dict__.update(kind=kind, rows=rows, K=K, codes_ptr=at, scales_ptr=at + rows * width, _codes=None, _scales=None,
+                             _buffer=buffer, _struct=None)
         return self
 
     @property
     def codes(self):
         if self._codes is None:
             n = self.scales_ptr - self.codes_ptr
-            self._codes = self._buffer[:n].view(self.rows, n // self.rows)
+            self.__dict__["_codes"] = self._buffer[:n].view(self.rows, n // self.rows)
         return self._codes
 
     @property
     def scales(self):
         if self._scales is None:
-            self._scales = self._buffer[self.scales_ptr - self.codes_ptr:].view(self.rows, -1)
+            self.__dict__["_scales"] = self._buffer[self.scales_ptr - self.codes_ptr:].view(self.rows, -1)
         return self._scales
 
     @property
@@ -1023,19 +1026,19 @@ class MXRows:
     def by_ref(self):
         """The gq_mx_rows, for a call."""
         if self._struct is None:
-            self._struct = ctypes.pointer(MXRowsStruct(self.rows, self.codes_ptr, self.scales_ptr))
+            self.__dict__["_struct"] = ctypes.pointer(MXRowsStruct(self.rows, self.codes_ptr, self.scales_ptr))
         return self._struct
 
 
-class MXWeights:
+class MXWeights(_Fixed):
     """`count` repacked 4-bit matrices [N, K] (gq_repack_mxfp4)."""
 
     def __init__(self, data, count: int, N: int, K: int):
-        self.address = _cuda(data, "uint8", (gq_mxfp4_repacked_bytes(count, N, K),), "data")
-        self.data, self.device, self.count, self.N, self.K = data, data.device, count, N, K
+        address = _cuda(data, "uint8", (gq_mxfp4_repacked_bytes(count, N, K),), "data")
+        self.__dict__.update(address=address, data=data, device=data.device, count=count, N=N, K=K)
 
 
-class ExpertPlan:
+class ExpertPlan(_Fixed):
     """Rows sorted by expert (gq_expert_rows): offsets int32 [E + 1], the token of each row, the row of each choice [T, top_k]."""
 
     def __init__(self, offsets, rows, pos):
@@ -1045,19 +1048,18 @@ class ExpertPlan:
         self._set(offsets, rows, pos, offsets.shape[0] - 1, rows.shape[0])
 
     def _set(self, offsets, rows, pos, E: int, R: int):
-        self.offsets, self.rows, self.pos, self.E, self.R = offsets, rows, pos, E, R
-        self._gathered = self._in_order = None
+        self.__dict__.update(offsets=offsets, rows=rows, pos=pos, E=E, R=R, _gathered=None, _in_order=None)
 
     def by_ref(self, gather: bool):
         """The gq_expert_rows, for a call: with the rows to gather, or without."""
         if self._gathered is None:
             o, r = self.offsets.data_ptr(), self.rows.data_ptr()
-            self._gathered = ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, r))
-            self._in_order = ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, None))
+            self.__dict__.update(_gathered=ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, r)),
+                                 _in_order=ctypes.pointer(ExpertRowsStruct(self.E, self.R, o, None)))
         return self._gathered if gather else self._in_order
 
 
-class Router:
+class Router(_Fixed):
     """How tokens choose their experts (gq_router)."""
 
     def __init__(self, E: int, top_k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups: int = 1,
@@ -1065,10 +1067,9 @@ class Router:
         scores = {"softmax": GQ_SCORE_SOFTMAX, "sigmoid": GQ_SCORE_SIGMOID}
         if score not in scores:
             raise ValueError(f"score: expected softmax or sigmoid, got {score}")
-        self.E, self.top_k, self.bias = E, top_k, bias
-        self.struct = RouterStruct(E, top_k, scores[score], groups, top_groups, group_best, renormalize, factor,
-                                   None if bias is None else _cuda(bias, "float32", (E,), "bias"))
-        self.by_ref = ctypes.pointer(self.struct)
+        struct = RouterStruct(E, top_k, scores[score], groups, top_groups, group_best, renormalize, factor,
+                              None if bias is None else _cuda(bias, "float32", (E,), "bias"))
+        self.__dict__.update(E=E, top_k=top_k, bias=bias, struct=struct, by_ref=ctypes.pointer(struct))
 
 
 def quantize_mx(x, kind: int = GQ_MX_E4M3) -> MXRows:

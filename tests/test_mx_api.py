@@ -161,3 +161,17 @@ def test_binding_objects(lib):
         gq.quantize_mx(OnGpu(torch.zeros((64, 3)).T))
     with pytest.raises(ValueError, match="residual"):
         gq.rms_norm_mx(OnGpu(torch.zeros((3, 64))), None, 1e-5, residual=OnGpu(torch.zeros((3, 64), dtype=torch.bfloat16)))
+
+
+def test_what_calls_point_at_cannot_be_changed(lib):
+    """The structs hold addresses and sizes: a field that could be assigned would leave them behind."""
+    x = gq.MXRows.empty(5, 64, E4M3, "cpu")
+    p = gq.ExpertPlan(*(OnGpu(torch.zeros(n, dtype=torch.int32)) for n in ((5,), (12,), (6, 2))))
+    r = gq.Router(8, 2)
+    for thing, names in ((x, ("rows", "K", "kind", "codes", "scales", "codes_ptr")), (p, ("E", "R", "offsets", "rows", "pos")),
+                         (r, ("E", "top_k", "bias", "struct"))):
+        for name in names:
+            before = getattr(thing, name)
+            with pytest.raises(AttributeError):
+                setattr(thing, name, 3)
+            assert getattr(thing, name) is before
