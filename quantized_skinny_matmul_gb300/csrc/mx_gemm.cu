@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t *__restr
     pdl_wait();
     pdl_launch_dependents();
     const int end = min(hi, *used), pieces = K / 16, all = pieces + S / 16;
-    // a warp takes rows in turn, two at a time
+    // a warp takes rows in turn
     const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
     for (int r = lo + (int)(blockIdx.x * 8 + (threadIdx.x >> 5)); r < end; r += warps) {
         const int from = __ldg(rows + r);
