@@ -591,11 +591,12 @@ typedef struct gq_mx_rows {
 } gq_mx_rows;
 
 /* Which rows go to which expert: row r, offsets[e] <= r < offsets[e + 1], belongs to expert e
- * (offsets int32 [E + 1] on the device).  R is the room for rows on the host's side; rows from
- * offsets[E] on are neither read nor written.  With `rows` (int32 [R]) row r of the product reads
- * row rows[r] of the activations, without it row r.  An expert whose offsets are out of range
- * (negative, decreasing, past R, or begin in front of the end of an earlier expert that is not) has no rows, a row whose index is outside the activations reads
- * as zeros, and either makes the next gq_last_error() return GQ_ERR_INVALID_ARG.
+ * (offsets int32 [E + 1] on the device).  R is the room for rows on the host's side; rows that belong to
+ * no expert (those from offsets[E] on, and those in front of offsets[0]) are neither read nor written.
+ * With `rows` (int32 [R]) row r of the product reads row rows[r] of the activations, without it row r.
+ * An expert whose offsets are out of range (negative, decreasing, past R, or beginning in front of the end of an
+ * earlier expert that is not) has no rows, the others keep theirs; a row whose index is outside the activations
+ * reads as zeros; either makes the next gq_last_error() return GQ_ERR_INVALID_ARG.
  * E 1 .. 1024, R < 2^30. */
 typedef struct gq_expert_rows {
     int64_t E, R;

@@ -887,19 +887,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-// Rows lo .. hi - 1 of the plan, as far as they are in use, brought into its order: codes and scales, 16 bytes a thread and
+// Rows lo .. hi - 1 of the plan, as far as experts have them, brought into its order: codes and scales, 16 bytes a thread and
 // turn.  A row whose index is out of range becomes zeros.  18 us for 32760 rows of 2048; four-row copies by the product's one
-// copying thread keep up with tiles of 16 rows only.
+// copying thread keep up with tiles of 16 rows only.  What experts have is from the first begin to the largest end of the
+// ranges that are in [0, R], as the product sees them (one that overlaps an earlier range it refuses, but such a row does no
+// harm here): with offsets that go back at the end, offsets[E] is not the largest.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                                                          const int32_t *__restrict__ rows, const int32_t *__restrict__ used,
+                                                          const int32_t *__restrict__ rows, const int32_t *__restrict__ offsets,
                                                           uint8_t *__restrict__ to_codes, uint8_t *__restrict__ to_scales, int lo, int hi,
-                                                          int64_t x_rows, int K, int S, unsigned int *status) {
+                                                          int E, int R, int64_t x_rows, int K, int S, unsigned int *status) {
+    __shared__ int range[2];                               // R - first begin, largest end
+    if (threadIdx.x < 2) range[threadIdx.x] = 0;
     pdl_wait();
     pdl_launch_dependents();
-    const int end = min(hi, *used), pieces = K / 16, all = pieces + S / 16;
+    __syncthreads();
+    int from_end = 0, last = 0;
+    for (int e = threadIdx.x; e < E; e += 256) {
+        const int r0 = __ldg(offsets + e), r1 = __ldg(offsets + e + 1);
+        if (r0 >= 0 && r1 > r0 && r1 <= R) from_end = max(from_end, R - r0), last = max(last, r1);
+    }
+    from_end = (int)__reduce_max_sync(0xffffffffu, (uint32_t)from_end);
+    last = (int)__reduce_max_sync(0xffffffffu, (uint32_t)last);
+    if ((threadIdx.x & 31) == 0 && last > 0) atomicMax(&range[0], from_end), atomicMax(&range[1], last);
+    __syncthreads();
+    const int begin = max(lo, R - range[0]), end = min(hi, range[1]), pieces = K / 16, all = pieces + S / 16;
     // a warp takes rows in turn
     const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
-    for (int r = lo + (int)(blockIdx.x * 8 + (threadIdx.x >> 5)); r < end; r += warps) {
+    for (int r = begin + (int)(blockIdx.x * 8 + (threadIdx.x >> 5)); r < end; r += warps) {
         const int from = __ldg(rows + r);
         const bool there = from >= 0 && from < x_rows;
         if (!there && lane == 0) atomicOr(status, STATUS_RANGE);
@@ -1055,16 +1069,16 @@ gq_status launch_mx_product(const void *rep, const gq_mx_rows &x, const gq_exper
     Workspace ws;
     st = get_workspace(s, 0, (size_t)(some_rows * row_bytes), &ws);
     if (st != GQ_OK) return st;
-    const int32_t *from = p.rows, *used = p.offsets + p.E;
+    const int32_t *from = p.rows, *offsets = p.offsets;
     uint8_t *codes_to = ws.data, *scales_to = ws.data + some_rows * K;
     p.rows = nullptr;
     for (int64_t lo = 0; lo < p.R; lo += some_rows) {
-        int l = (int)lo, h = (int)std::min<int64_t>(p.R, lo + some_rows), k = (int)K, S = p.S;
+        int l = (int)lo, h = (int)std::min<int64_t>(p.R, lo + some_rows), E = p.E, R = p.R, k = (int)K, S = p.S;
         int64_t x_rows = x.rows;
         const void *xc = x.codes;
         const uint8_t *xs = x.scales;
         unsigned int *status = p.status;
-        void *args[] = {&xc, &xs, &from, &used, &codes_to, &scales_to, &l, &h, &x_rows, &k, &S, &status};
+        void *args[] = {&xc, &xs, &from, &offsets, &codes_to, &scales_to, &l, &h, &E, &R, &x_rows, &k, &S, &status};
         st = launch_pdl((const void *)gather_rows_kernel, dim3((unsigned)std::min<int64_t>((h - l + 7) / 8, 8LL * sm_count())), dim3(256), 0, s,
                         args, "gather rows launch");
         if (st != GQ_OK) return st;
