@@ -564,8 +564,10 @@ gq_status gq_dequantize_mx(const void *codes, const uint8_t *scales, gq_mx_kind 
  * one), y_j = h_j * weight_j / sqrt(mean(h^2) + eps).  x, residual and h are rows of `type` at
  * stride ldx, ldr, ldh (as in gq_quantize_mx); weight f32 [K] or NULL (1).  Outputs, each optional
  * (at least one): h (NULL: not kept; h may be x or residual), y [M][K] of `ytype`, and the e4m3
- * blocks of y, codes with scales.  The blocks are those of the exact y: where f32 does not settle a code or a scale,
- * it is decided in two f32 terms (48 bits).  y itself is formed in f32, within 2^-20 of itself, and rounded to ytype.
+ * blocks of y, codes with scales.  The blocks are those of the exact y: where f32 does not settle
+ * a code or a scale, it is decided in two f32 terms (48 bits), and in 64 bits where squares, sums or products leave the
+ * range of f32 (a row whose root mean square is not between 2^-30 and 2^60; a block of very large or small y).  y itself is
+ * formed in f32, within 2^-20 of itself or 2^-120, and rounded to ytype.
  * K up to 32768. */
 gq_status gq_rms_norm_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr, gq_type type,
                          const float *weight, double eps, void *h, int64_t ldh, void *y, gq_type ytype,

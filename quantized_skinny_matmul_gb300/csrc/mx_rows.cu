@@ -197,6 +197,7 @@ struct NormParams {
     void *h, *y, *codes;
     uint8_t *scales;
     int64_t ldx, ldr, ldh, M;
+    double eps;
     float eps_hi, eps_lo;
     int K, S, y_bf16;
 };
@@ -224,6 +225,91 @@ struct Raw {
     }
 };
 
+// The norm of one row in 64 bits, by all of a CTA: for rows that leave the range in which f32 decides (below).  The squares
+// of any f32 values, their sum and any product h w r are normal numbers of 64 bits.  h is read again, where this thread
+// wrote it if it is kept.  This GPU has few 64-bit units: 20 us for a row of 4096.
+template <typename T>
+__device__ __noinline__ void norm_row64(const NormParams &p, int64_t row, double *part) {
+    const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    auto load = [&](int g, float (&v)[8]) {
+        Raw<T> h;
+        if (p.h) {
+            h.load(static_cast<const T *>(p.h) + row * p.ldh + g * 8);
+        } else {
+            h.load(static_cast<const T *>(p.x) + row * p.ldx + g * 8);
+            if (p.res) {
+                Raw<T> r;
+                r.load(static_cast<const T *>(p.res) + row * p.ldr + g * 8);
+                h.add(r);
+            }
+        }
+        h.widen(v);
+    };
+    double sum = 0.0;
+#pragma unroll 1
+    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+        float v[8];
+        load(g, v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += (double)v[i] * (double)v[i];
+    }
+#pragma unroll 1
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (warps > 1) {
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = lane < warps ? part[lane] : 0.0;
+#pragma unroll 1
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        __syncthreads();                                   // `part` is free
+    }
+    const double r = 1.0 / sqrt(sum / (double)p.K + p.eps);
+#pragma unroll 1
+    for (int g0 = 0; g0 < groups; g0 += blockDim.x) {
+        const int g = g0 + threadIdx.x;
+        const bool live = g < groups;
+        float h[8], w[8];
+        double v[8];
+        double most = 0.0;                                 // infinity for blocks with a NaN, too
+        load(live ? g : 0, h);
+        if (p.w) load8(p.w + (live ? g * 8 : 0), w);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            v[i] = (p.w ? (double)h[i] * (double)w[i] : (double)h[i]) * r;
+            const double a = fabs(v[i]);
+            most = a < INFINITY ? fmax(most, a) : INFINITY;
+        }
+        most = fmax(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmax(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        if (!live) continue;
+        if (p.y) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) y[i] = (float)v[i];
+            if (p.y_bf16)
+                store8(static_cast<__nv_bfloat16 *>(p.y) + row * p.K + g * 8, y);
+            else
+                store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
+        }
+        if (!p.codes) continue;
+        // as mx_scale_byte, and 2^(127 - b); what is scaled is cut to f32 with its last bit set if anything was cut off, so that
+        // the code's rounding decides as if it saw all of it
+        const int64_t bits = __double_as_longlong(most);
+        const int e = (int)(bits >> 52);
+        const int b = e == 2047 ? 255 : max(e - 1023 + 127 - 8 + ((bits & 0xFFFFFFFFFFFFF) > 0xC000000000000), 0);
+        const double inverse = __longlong_as_double((int64_t)(b == 255 ? 0 : 1023 + 127 - b) << 52);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const double x = v[i] * inverse;
+            f[i] = __double2float_rz(x);
+            if ((double)f[i] != x) f[i] = __uint_as_float(__float_as_uint(f[i]) | 1u);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = codes8<false>(f, b == 255 ? 0.0f : 1.0f);
+        if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = (uint8_t)b;
+    }
+}
+
 // One CTA per row (in turn).  Thread t holds the groups of 8 values t, t + T, .. (C of them at most) from the load to the
 // output, so that the row is read once.  The codes are those of the exact y, mostly without exact arithmetic.
 // In f32, with positive terms only, the sum of squares is off by 17 roundings at most (4 additions in a thread, 3 levels
@@ -231,9 +317,20 @@ struct Raw {
 // all, less than 2^-20 of itself.  So if it gives the same code with 2^-20 more and with 2^-20 less (and so does the
 // largest its scale), that is the code; if one value of the row does not (one row of 4096 in ten), the CTA forms the sum, r and
 // the row's values again in two terms, from what it holds.
+// That counts roundings, not what falls out of f32's range.  With r between 2^-60 and 2^30 the mean of squares is between 2^-60
+// and 2^120: the sum is finite, and squares that fell below 2^-126 are off by 2^-150 each.  With a block's largest y between
+// 2^-60 and 2^126 (2^-90 for one that f32 decides) its largest h w is finite and above 2^-90 (2^-120), and what its values and
+// their second terms lose at 2^-150 is far below a code's step.  Rows with another r or another block are done in 64 bits,
+// when the CTA is through with the others: a call within the loop would cost all rows registers (8191 rows 64 us, not 53).
+// But blocks of zeros have their codes as they are, if a factor of each value is 0, and a row with a NaN is NaN.
+// `later` has a bit for each of a CTA's turns, which some turns share past 2048 of them.
+constexpr float R_MIN = 0x1p-60f, R_MAX = 0x1p30f, Y_MIN = 0x1p-60f, Y_MAX = 0x1p126f;
+constexpr int LATER = 2048;
 template <typename T, int C>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
-    __shared__ Two part[32];
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ __align__(8) Two part[32];
+    __shared__ uint32_t later[LATER / 32];                 // which of the CTA's rows are left for the end, if any
+    bool some_later = false;
     const int groups = p.K / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
@@ -283,7 +380,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         float r;
         asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(mean));
         r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.0f), r);          // to a unit
-        bool unsure = false;
+        bool wide = !(r > R_MIN && r < R_MAX), unsure = false;    // (true for NaN)
 #pragma unroll
         for (int c = 0; c < C; c++) {
             const int g = threadIdx.x + c * blockDim.x;
@@ -306,14 +403,17 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
                 else
                     store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
             }
-            if (!p.codes) continue;
             float most = 0.0f;                             // (a NaN or infinity of h has made r NaN or 0)
 #pragma unroll
             for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[i]));
+            if (!p.codes) {
+                wide |= live && !(most * r > Y_MIN && most * r < Y_MAX);
+                continue;
+            }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2)) * r;
             const int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
-            const float inv = mx_inverse(b) * r, less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
+            const float inv = fminf(mx_inverse(b) * r, 0x1p126f), less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
             uint32_t lo[4], differ = 0;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -322,16 +422,60 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
             }
             // (tiny, infinite and NaN blocks are not sure: there the f32 values are not that close)
             const bool sure = differ == 0 && mx_scale_byte(__float_as_uint(most * (1.0f - 0x1p-20f)), false) == b && b > 0 && b < 255 &&
-                              inv < 0x1p100f && r > 0x1p-60f && most > 0x1p-90f;
+                              inv < 0x1p100f && most > 0x1p-90f;
             if (live) {
-                unsure |= !sure;
+                unsure |= !sure && most > 0.0f;
+                wide |= !sure && !(most > Y_MIN && most < Y_MAX);
                 *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                 if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = (uint8_t)b;
             }
         }
         if (p.codes && threadIdx.x < p.S - p.K / 32) p.scales[row * p.S + p.K / 32 + threadIdx.x] = 0;
         // (the barrier also frees `part`)
-        if (!(warps > 1 ? __syncthreads_or(unsure) : __any_sync(0xffffffffu, unsure))) continue;
+        if (!(warps > 1 ? __syncthreads_or(unsure || wide) : __any_sync(0xffffffffu, unsure || wide))) continue;
+        if (warps > 1 ? __syncthreads_or(wide) : __any_sync(0xffffffffu, wide)) {
+            if (isnan(mean)) {                             // a NaN among h: the row is NaN, y is already
+                if (p.codes)
+                    for (int g = threadIdx.x; g < groups; g += blockDim.x) {
+                        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.codes) + row * p.K + g * 8) = make_uint2(0u, 0u);
+                        if ((g & 3) == 0) p.scales[row * p.S + (g >> 2)] = 255;
+                    }
+                continue;
+            }
+            // (blocks of zeros that are there because a factor of each is have their codes)
+            wide = !(r > R_MIN && r < R_MAX);
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const int g = threadIdx.x + c * blockDim.x;
+                float v[8], w[8], most = 0.0f;
+                h[c].widen(v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) w[i] = 1.0f;
+                if (p.w) load8(p.w + (g < groups ? g * 8 : 0), w);
+                bool zeros = true;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    zeros = zeros && (v[i] == 0.0f || w[i] == 0.0f);
+                    most = fmaxf(most, fabsf(v[i] * w[i]));
+                }
+                if (p.codes) {
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                }
+                wide |= g < groups && !zeros && !(most * r > Y_MIN && most * r < Y_MAX);
+            }
+            if (warps > 1 ? __syncthreads_or(wide) : __any_sync(0xffffffffu, wide)) {
+                if (threadIdx.x == 0) {
+                    if (!some_later)
+                        for (int i = 0; i < LATER / 32; i++) later[i] = 0;
+                    const int turn = (int)((row - blockIdx.x) / gridDim.x) % LATER;
+                    later[turn >> 5] |= 1u << (turn & 31);
+                }
+                some_later = true;
+                continue;
+            }
+            if (!(warps > 1 ? __syncthreads_or(unsure) : __any_sync(0xffffffffu, unsure))) continue;
+        }
         Two total{0.0f, 0.0f};
 #pragma unroll 1
         for (int i = 0; i < 8; i++) {
@@ -382,6 +526,11 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         }
         if (warps > 1) __syncthreads();                    // `part` is free
     }
+    if (!some_later) return;
+    __syncthreads();
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, turn = (turn + 1) % LATER)
+        if (later[turn >> 5] >> (turn & 31) & 1u) norm_row64<T>(p, row, reinterpret_cast<double *>(part));
 }
 
 // ---------------------------------------------------------------------------
@@ -506,7 +655,7 @@ gq_status launch_rms_norm_mx(const void *x, int64_t ldx, const void *res, int64_
     NormParams p{};
     p.x = x, p.res = res, p.w = w, p.h = h, p.y = y, p.codes = codes, p.scales = scales;
     p.ldx = ldx, p.ldr = ldr, p.ldh = ldh, p.M = M;
-    p.eps_hi = (float)eps, p.eps_lo = (float)(eps - (double)p.eps_hi);
+    p.eps = eps, p.eps_hi = (float)eps, p.eps_lo = (float)(eps - (double)p.eps_hi);
     p.K = (int)K, p.S = (int)gq_mx_scale_cols(K), p.y_bf16 = y_bf16;
     return bf16 ? norm_width<__nv_bfloat16>(p, s) : norm_width<float>(p, s);
 }

@@ -10,9 +10,10 @@ import torch
 
 import mx_ref as ref
 import quantized_skinny_matmul_gb300 as gq
-from test_gpu_mx import built, dev, mx, near, rows, weights  # noqa: F401 (built: a fixture)
+from test_gpu_mx import DT, U, built, dev, host, mx, near, rows, weights  # noqa: F401 (built: a fixture)
 
 pytestmark = pytest.mark.gpu
+FLT_MAX = float(np.finfo(np.float32).max)
 E = 4
 
 
@@ -73,3 +74,109 @@ def test_rows_in_front_of_the_first_expert(mean):
         want, S = ref.product(X[token[r]], W[e])
         near(out[r], want, ref.product_tolerance(K) * S, f"expert {e}")
     assert (out[:front] == 5).all() and (out[R - 5:] == 5).all()
+
+
+# ---- the norm ------------------------------------------------------------------------------------
+
+
+def check_norm(x, w, eps, dtype="f32"):
+    """Codes (signs too), scales and y of rows on the GPU."""
+    t = dev(x, DT[dtype])
+    K = t.shape[1]
+    _, q, y = gq.rms_norm_mx(t, w, eps, y_dtype=torch.float32)
+    _, only, _ = gq.rms_norm_mx(t, w, eps, residual=torch.zeros_like(t), y_dtype=torch.bfloat16)
+    alone = torch.empty_like(y)
+    gq.gq_rms_norm_mx(t, K, None, K, gq.GQ_TYPE_BF16 if dtype == "bf16" else gq.GQ_TYPE_F32, w, eps, None, K, alone, gq.GQ_TYPE_F32, None,
+                      None, len(t), K)
+    with np.errstate(all="ignore"):
+        want = ref.norm(host(t), None if w is None else host(w), eps)
+        codes, b = ref.quantize(want, ref.E4M3)
+    assert np.array_equal(host(q.scales)[:, :K // 32], b)
+    zero = want == 0
+    assert np.array_equal(np.where(zero, 0, host(q.codes)), np.where(zero, 0, codes))
+    assert not (host(q.codes)[zero] & 127).any()
+    nonzero = torch.from_numpy(host(t) != 0).cuda()                        # (a sum with +0 makes a -0 of x +0)
+    assert torch.equal(only.codes[nonzero], q.codes[nonzero]) and torch.equal(only.scales, q.scales)
+    inside = np.abs(want) <= FLT_MAX * (1 - 2.0 ** -19)
+    for v in (y, alone):
+        v = host(v)
+        near(v[inside], want[inside], (2.0 ** -20 + U) * np.abs(want[inside]) + 2.0 ** -120)
+        assert np.array_equal(np.isnan(v), np.isnan(want))
+        large = np.abs(want) > FLT_MAX * (1 + 2.0 ** -19)
+        assert np.array_equal(v[large], np.sign(want[large]) * np.inf)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-40, 1e-60, 1e300])
+@pytest.mark.parametrize("K", [32, 160, 4096])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_of_any_magnitude(dtype, K, eps):
+    """Rows whose squares leave the range of f32, at either end."""
+    size = [1e-44, 1e-42, 1e-38, 1e-30, 1e-25, 1e-21, 1e-19, 1e-15, 1e-12, 1.0, 1e12, 1e15, 1e17, 1e18, 1e19, 1e30, 3e37]
+    x = np.random.default_rng(K).standard_normal((3, len(size), K)) * np.array(size)[None, :, None]
+    x = np.clip(x.reshape(-1, K), -3.3e38, 3.3e38).astype(np.float32)
+    host_rows = host(dev(x, DT[dtype]))
+    x = x[(host_rows != 0).any(-1)]                                        # (a row of zeros with eps 0 is the next test's)
+    check_norm(x, None, eps, dtype)
+    check_norm(x, dev(1 + 0.3 * np.random.default_rng(1).standard_normal(K).astype(np.float32)), eps, dtype)
+
+
+@pytest.mark.parametrize("K", [32, 160, 4096])
+def test_norm_of_uneven_rows_and_zeros(K):
+    rng = np.random.default_rng(K)
+    x = rng.standard_normal((8, K)).astype(np.float32)
+    x[0, 3] = 3e38                                                         # one value far above the others
+    x[1, :] *= 1e-38
+    x[1, 5] = 1.0
+    x[2, :16] = 3e38
+    x[2, 16:] = 1e-44
+    x[3] = 0
+    x[4] = -0.0
+    x[4, 9] = 1e-30
+    x[5, ::2] = 0                                                          # zeros in between, and whole blocks of them
+    x[6, :-32] = 0
+    x[7] = np.where(rng.random(K) < 0.5, -2, 2)                            # exactly 1 and -1 with eps 0
+    for eps in (1e-6, 1e-60):
+        check_norm(x, None, eps)
+    check_norm(np.delete(x, 3, 0), None, 0.0)
+    q = gq.rms_norm_mx(dev(x), None, 0.0)[1]                               # 0 / 0
+    assert (q.scales[3, :K // 32] == 255).all() and not q.codes[3].any() and (q.scales[[0, 1, 2, 4, 5, 6, 7], :K // 32] != 255).all()
+
+
+def test_norm_with_weights_of_any_magnitude():
+    K = 32768
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((6, K)).astype(np.float32)
+    w = rng.standard_normal(K).astype(np.float32)
+    w[:32], w[32:64], w[64:96], w[96:128], w[128] = w[:32] * 1e30, w[32:64] * 1e-30, 0, 1e-44, FLT_MAX
+    x[1] *= 1e15
+    x[2] *= 1e-15
+    x[3] *= 1e-36
+    x[4] *= 1e30
+    x[5] = 0
+    x[5, 128], x[5, 7] = 1e25, -1e20                                       # y is 181 times the largest f32
+    for eps in (0.0, 1e-6):
+        check_norm(x, dev(w), eps)
+    check_norm(x[:, :4096], dev(w[:4096]), 0.0)
+
+
+@pytest.mark.parametrize("M, K", [(6000, 64), (3100, 1024), (700, 4096), (330, 16416)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norm_where_each_cta_takes_several_rows(M, K, dtype):
+    """More rows than CTAs are resident, of ordinary and of extreme size in turn."""
+    x = np.random.default_rng(M).standard_normal((M, K)).astype(np.float32)
+    size = np.ones(M)
+    size[3::11], size[5::13], size[-2:], size[7::17] = 1e20, 1e-22, 1e25, 0
+    x = (x * size[:, None]).astype(np.float32)
+    t, r = dev(x, DT[dtype]), dev(np.roll(x, 1, 1), DT[dtype])
+    want_h = (t.float() + r.float()).to(DT[dtype])
+    h, q = gq.rms_norm_mx(t, None, 1e-12, residual=r)
+    assert torch.equal(h, want_h)
+    want = ref.norm(host(want_h), None, 1e-12)
+    codes, b = ref.quantize(want, ref.E4M3)
+    assert np.array_equal(host(q.scales)[:, :K // 32], b)
+    assert np.array_equal(np.where(want == 0, 0, host(q.codes)), np.where(want == 0, 0, codes))
+    # in place: a CTA reads its next rows while it writes this one's sum
+    out = gq.MXRows.empty(M, K)
+    code = gq.GQ_TYPE_BF16 if dtype == "bf16" else gq.GQ_TYPE_F32
+    gq.gq_rms_norm_mx(t, K, r, K, code, None, 1e-12, t, K, None, gq.GQ_TYPE_F32, out.codes, out.scales, M, K)
+    assert torch.equal(t, want_h) and torch.equal(out.codes, q.codes) and torch.equal(out.scales, q.scales)
