@@ -225,6 +225,13 @@ struct Raw {
     }
 };
 
+// The larger, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The norm of one row in 64 bits, by all of a CTA: for rows that leave the range in which f32 decides (below).  The squares
 // of any f32 values, their sum and any product h w r are normal numbers of 64 bits.  h is read again, where this thread
 // wrote it if it is kept.  This GPU has few 64-bit units: 20 us for a row of 4096.
@@ -403,15 +410,15 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
                 else
                     store8(static_cast<float *>(p.y) + row * p.K + g * 8, y);
             }
-            float most = 0.0f;                             // (a NaN or infinity of h has made r NaN or 0)
+            float most = 0.0f;                             // NaN if any is: a weight may be, where r is not
 #pragma unroll
-            for (int i = 0; i < 8; i++) most = fmaxf(most, fabsf(v[i]));
+            for (int i = 0; i < 8; i++) most = max_nan(most, fabsf(v[i]));
             if (!p.codes) {
                 wide |= live && !(most * r > Y_MIN && most * r < Y_MAX);
                 continue;
             }
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2)) * r;
+            most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2)) * r;
             const int b = mx_scale_byte(__float_as_uint(most * (1.0f + 0x1p-20f)), false);
             const float inv = fminf(mx_inverse(b) * r, 0x1p126f), less = inv * (1.0f - 0x1p-20f), more = inv * (1.0f + 0x1p-20f);
             uint32_t lo[4], differ = 0;
@@ -455,12 +462,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
                 bool zeros = true;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    zeros = zeros && (v[i] == 0.0f || w[i] == 0.0f);
-                    most = fmaxf(most, fabsf(v[i] * w[i]));
+                    zeros = zeros && v[i] * w[i] == 0.0f && (v[i] == 0.0f || w[i] == 0.0f);
+                    most = max_nan(most, fabsf(v[i] * w[i]));
                 }
                 if (p.codes) {
-                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
                 }
                 wide |= g < groups && !zeros && !(most * r > Y_MIN && most * r < Y_MAX);
             }

@@ -159,6 +159,20 @@ def test_norm_with_weights_of_any_magnitude():
     check_norm(x[:, :4096], dev(w[:4096]), 0.0)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_norm_with_a_weight_that_is_not_finite(bad):
+    """Its block, and that alone, holds no numbers, whatever the other columns of the row are."""
+    K = 1024
+    x = np.random.default_rng(4).standard_normal((300, K)).astype(np.float32)
+    w = np.ones(K, np.float32)
+    w[700] = bad
+    q = gq.rms_norm_mx(dev(x), dev(w), 1e-6)[1]
+    with np.errstate(all="ignore"):
+        codes, b = ref.quantize(ref.norm(x, w, 1e-6), ref.E4M3)
+    assert (b == 255).sum() == 300
+    assert np.array_equal(host(q.scales)[:, :K // 32], b) and np.array_equal(host(q.codes), codes)
+
+
 @pytest.mark.parametrize("M, K", [(6000, 64), (3100, 1024), (700, 4096), (330, 16416)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_norm_where_each_cta_takes_several_rows(M, K, dtype):
