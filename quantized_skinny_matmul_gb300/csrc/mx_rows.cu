@@ -523,7 +523,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
             for (int i = 0; i < 8; i++) w[i] = 1.0f;
             if (p.w) load8(p.w + (live ? g * 8 : 0), w);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = to_odd(mul(two_prod(v[i], w[i]), r2));
+            for (int i = 0; i < 8; i++) {
+                const Two hw = two_prod(v[i], w[i]);
+                v[i] = hw.hi == 0.0f ? hw.hi : to_odd(mul(hw, r2));      // (a sum of terms would make +0 of -0)
+            }
             const int b = mx_scale_byte(block_amax(v), false);
             const uint2 code = codes8<false>(v, mx_inverse(b));
             if (live) {

@@ -173,6 +173,15 @@ def test_norm_with_a_weight_that_is_not_finite(bad):
     assert np.array_equal(host(q.scales)[:, :K // 32], b) and np.array_equal(host(q.codes), codes)
 
 
+def test_the_sign_of_zeros_does_not_depend_on_the_row():
+    """-0 has the code of -0, in rows that f32 decides and in rows that need more."""
+    x = np.random.default_rng(5).standard_normal((300, 1024)).astype(np.float32)
+    x[:, 3::7] = -0.0
+    x[:, 5::7] = 0.0
+    q = gq.rms_norm_mx(dev(x), None, 1e-6)[1]
+    assert np.array_equal(host(q.codes), ref.quantize(ref.norm(x, None, 1e-6), ref.E4M3)[0])
+
+
 @pytest.mark.parametrize("M, K", [(6000, 64), (3100, 1024), (700, 4096), (330, 16416)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_norm_where_each_cta_takes_several_rows(M, K, dtype):
