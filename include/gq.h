@@ -637,8 +637,9 @@ gq_status gq_swiglu_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq
  * the largest c are chosen, largest first; equal values: the lower index, of groups too.
  * Their weights are the scores p, divided by their sum if renormalize is set (left as they are
  * if the sum is 0), times factor.  The choice is that of exact arithmetic: values that f32 cannot tell
- * apart are compared in 64 bits.  An expert whose logit is -infinity has score 0; a NaN
- * logit counts as -infinity; a row without a finite logit has weights 0 (softmax).
+ * apart are compared in 64 bits; the weights are formed in f32.  Among logits and biases NaN counts as -infinity and
+ * +infinity as the largest finite f32.  An expert whose logit is -infinity has score 0; a row whose logits all are has
+ * weights 0 (softmax).  An expert whose bias is -infinity is chosen only when there is no other.
  * E 1 .. 1024, top_k 1 .. 32, 1 to 32 groups that divide E, top_k <= top_groups * E / groups. */
 typedef enum { GQ_SCORE_SOFTMAX = 0, GQ_SCORE_SIGMOID = 1 } gq_score;
 typedef struct gq_router {

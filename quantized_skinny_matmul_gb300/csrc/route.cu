@@ -15,6 +15,7 @@
 // memory, so nothing depends on timing.  Both are bound by instructions, not by memory: 8192 tokens, 8 of 256
 // experts by sigmoid scores with a bias in 4 of 8 groups, take 27 us and 12 us (their bytes 1.4).
 #include <algorithm>
+#include <cfloat>
 
 #include "mx.cuh"
 
@@ -110,12 +111,12 @@ __device__ __forceinline__ double score64(const RouteParams &p, float z, float m
     return m == -INFINITY ? 0.0 : exp((double)z - (double)m) / sum;
 }
 
-__device__ __forceinline__ float plain(float z) { return isnan(z) ? -INFINITY : z; }
+// A logit or a bias as it counts: NaN as -infinity, +infinity as the largest finite number.  So no sum, difference or score of two
+// such is NaN, but for the difference of two -infinities.
+__device__ __forceinline__ float plain(float z) { return fminf(fmaxf(z, -INFINITY), FLT_MAX); }   // (fmaxf drops a NaN)
 __device__ __forceinline__ float plain(__nv_bfloat16 z) { return plain(__bfloat162float(z)); }
 __device__ __forceinline__ float logit(const RouteParams &p, int64_t t, int e) {
-    const float z = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[t * p.ldl + e])
-                           : static_cast<const float *>(p.logits)[t * p.ldl + e];
-    return isnan(z) ? -INFINITY : z;
+    return p.bf16 ? plain(static_cast<const __nv_bfloat16 *>(p.logits)[t * p.ldl + e]) : plain(static_cast<const float *>(p.logits)[t * p.ldl + e]);
 }
 
 // The sum of the exponentials of token t, in 64 bits.
@@ -136,7 +137,7 @@ __device__ __noinline__ int choose64(const RouteParams &p, int64_t t, float m, d
     // without a bias, and where no sums are compared, the logits decide
     auto value = [&](int e) {
         const float z = logit(p, t, e);
-        return p.bias ? score64(p, z, m, sum) + (double)p.bias[e] : (double)z;
+        return p.bias ? score64(p, z, m, sum) + (double)plain(p.bias[e]) : (double)z;
     };
     if (grouped) {
         for (int e = lane; e < p.E; e += 32) shared[e + e / n * p.lanes] = sums ? score64(p, logit(p, t, e), m, sum) : value(e);
@@ -227,7 +228,8 @@ __device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const flo
 #pragma unroll
                 for (int i = 0; i < V; i++) size = fmaxf(size, fabsf(c[i]));
             size = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
-            if (!(gap > 2.0f * tol + 0x1p-20f * size)) return choose64(p, t, m, sum64(p, t, m, lane), shared, lane);
+            // (two of the largest values would overflow in a sum of f32)
+            if (!(gap > 2.0f * tol + 0x1p-20f * size) || size > 0x1p126f) return choose64(p, t, m, sum64(p, t, m, lane), shared, lane);
         }
     }
     uint32_t key[V];
@@ -281,7 +283,7 @@ __device__ __forceinline__ int choose(const RouteParams &p, int64_t t, const flo
     double exact = -INFINITY;
     if (lane < found) {
         const float x = logit(p, t, id);
-        exact = p.bias ? score64(p, x, m, s) + (double)p.bias[id] : (double)x;
+        exact = p.bias ? score64(p, x, m, s) + (double)plain(p.bias[id]) : (double)x;
     }
     int rank = 0;
     for (int j = 0; j < found; j++) {
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
     pdl_launch_dependents();
     float bias[V];
 #pragma unroll
-    for (int i = 0; i < V; i++) bias[i] = p.bias && i * 32 + lane < p.E ? p.bias[i * 32 + lane] : 0.0f;
+    for (int i = 0; i < V; i++) bias[i] = p.bias && i * 32 + lane < p.E ? plain(p.bias[i * 32 + lane]) : 0.0f;
     __syncthreads();
     const int used = tokens_used(p.used, p.T, p.status);
     const int t0 = blockIdx.x * p.chunk, t1 = min(t0 + p.chunk, p.T);
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
             }
             id = choose<V, T>(p, t, z, bias, group, m, sum, shared, lane);
             if (lane < p.k) {
-                // (a bias that is not finite could leave a place empty)
+                // (no value is NaN, so every place is filled; a mistake in that would not read out of bounds)
                 id = (uint32_t)id < (uint32_t)p.E ? id : -1;
                 const float chosen = id < 0 ? -INFINITY : plain(row[id]);
                 w = p.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : m > -INFINITY ? expf(chosen - m) / sum : 0.0f;

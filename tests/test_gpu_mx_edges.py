@@ -10,7 +10,7 @@ import torch
 
 import mx_ref as ref
 import quantized_skinny_matmul_gb300 as gq
-from test_gpu_mx import DT, U, built, dev, host, mx, near, rows, weights  # noqa: F401 (built: a fixture)
+from test_gpu_mx import DT, U, built, dev, host, mx, near, router, rows, weights  # noqa: F401 (built: a fixture)
 
 pytestmark = pytest.mark.gpu
 FLT_MAX = float(np.finfo(np.float32).max)
@@ -203,3 +203,38 @@ def test_norm_where_each_cta_takes_several_rows(M, K, dtype):
     code = gq.GQ_TYPE_BF16 if dtype == "bf16" else gq.GQ_TYPE_F32
     gq.gq_rms_norm_mx(t, K, r, K, code, None, 1e-12, t, K, None, gq.GQ_TYPE_F32, out.codes, out.scales, M, K)
     assert torch.equal(t, want_h) and torch.equal(out.codes, q.codes) and torch.equal(out.scales, q.scales)
+
+
+# ---- routing --------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [20, 100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n, k", [(64, 6), (40, 32)])
+@pytest.mark.parametrize("best", [0, 1, 2])
+def test_route_of_values_that_are_not_finite(T, score, n, k, best, dtype):
+    """+infinity counts as the largest finite number, NaN as -infinity, among logits and biases: each token has top_k experts."""
+    rng = np.random.default_rng(T)
+    z = rng.integers(-3, 3, (T, n)).astype(np.float32)
+    z[1, 5], z[2, [3, 30]], z[3], z[4, :] = np.inf, np.inf, np.inf, -np.inf
+    z[4, 9], z[5, ::2], z[6, 7], z[6, 8], z[7], z[8] = np.inf, -np.inf, np.nan, np.inf, np.nan, -np.inf
+    z[9, :12], z[10, 11], z[10, 12] = np.inf, 3e38, np.inf
+    finite = (0.1 * rng.standard_normal(n)).astype(np.float32)
+    masked, odd, large = finite.copy(), finite.copy(), finite.copy()
+    masked[[0, 5, 17, 30]] = -np.inf
+    odd[[3, 20]], odd[[9, 33]], odd[12] = np.inf, np.nan, -np.inf
+    large[[2, 8, 21]] = 3e38
+    opt = dict(groups=4, top_groups=4 if k > 20 else 2, best=best) if best else {}
+    t = dev(z, DT[dtype])
+    clean = np.where(np.isnan(host(t)), -np.inf, np.minimum(host(t), FLT_MAX))
+    for bias in (None, finite, masked, odd, large):
+        exact = None if bias is None else np.where(np.isnan(bias), -np.inf, np.minimum(bias.astype(np.float64), FLT_MAX))
+        ids, w, plan = gq.route(t, router(dict(E=n, k=k, score=score, bias=None if bias is None else dev(bias), **opt)))
+        with np.errstate(all="ignore"):
+            want, ww = ref.route(clean, k, score, exact, **opt)
+        assert np.array_equal(host(ids), want)
+        # arguments of the exponential are small whole numbers, or leave 0
+        near(w, ww, (6 + n / 32 + 16) * U * np.abs(ww) + 1e-38)
+        off, rows_, pos = ref.plan(want, n)
+        assert np.array_equal(host(plan.offsets), off) and np.array_equal(host(plan.pos), pos) and np.array_equal(host(plan.rows), rows_)
