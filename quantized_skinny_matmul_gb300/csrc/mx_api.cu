@@ -215,7 +215,7 @@ gq_status gq_route(const gq_router *router, const void *logits, int64_t ldl, gq_
                     (long long)(r.top_groups * (r.E / r.groups)), (long long)r.top_k);
     if (!std::isfinite(r.factor)) return fail(GQ_ERR_INVALID_ARG, "factor is not finite");
     GQ_TRY(check_type(type, "type"));
-    if (T <= 0 || T * r.top_k >= (1LL << 30)) return fail(GQ_ERR_INVALID_ARG, "T must be positive, T * top_k below 2^30 (got %lld)", (long long)T);
+    if (T <= 0 || T >= (1LL << 30) || T * r.top_k >= (1LL << 30)) return fail(GQ_ERR_INVALID_ARG, "T must be positive, T * top_k below 2^30 (got %lld)", (long long)T);
     if (ldl < r.E || ldl > (1LL << 31)) return fail(GQ_ERR_INVALID_ARG, "ldl=%lld must be at least E=%lld", (long long)ldl, (long long)r.E);
     GQ_TRY(check_ptr(logits, "logits"));
     if (r.bias) GQ_TRY(check_ptr(r.bias, "bias"));
