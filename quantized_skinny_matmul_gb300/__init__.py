@@ -1121,7 +1121,7 @@ def _operands(w: MXWeights, x: MXRows, plan, gather: bool, parts: int):
 
 
 def _output(out, rows: int, N: int, dtype, device):
-    """(tensor, row stride, gq_type) of an output [rows, N]: `out` if given, else a new one."""
+    """(tensor, row stride, gq_type) of an output [rows, N]: `out` if given (of `dtype`, if that is too), else a new one."""
     if out is None:
         dtype = dtype or _f32()
         t = _mx_type(dtype, "dtype")
@@ -1129,6 +1129,8 @@ def _output(out, rows: int, N: int, dtype, device):
     Ro, No, ld, t = _matrix(out, "out")
     if Ro != rows or No != N:
         raise ValueError(f"out: expected shape {(rows, N)}, got {(Ro, No)}")
+    if dtype is not None and dtype != out.dtype:
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
     return out, ld, t
 
 
