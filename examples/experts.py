@@ -47,29 +47,29 @@ class Layer:
 
 
 def check(layer, out, parts, tokens):
-    """How far the first `tokens` rows are off their 64-bit values, from the blocks as they are."""
+    """How far the first `tokens` rows are off their 64-bit values, from the blocks as they are (NaN if anything is)."""
     h, blocks, ids, weights, plan, act = parts
     A, pos = gq.dequantize_mx(act).double(), plan.pos.tolist()
     N, K = layer.down.N, layer.down.K
-    worst = 0.0
+    worst = []
     W = gq.dequantize_mx(layer.down_blocks).view(-1, N, K)
     for t in range(tokens):
         want = h[t].double()
         for j, e in enumerate(ids[t].tolist()):
             want = want + weights[t, j].double() * (W[e].double() @ A[pos[t][j]])
-        worst = max(worst, float((out[t].double() - want).abs().max() / want.abs().max()))
+        worst.append((out[t].double() - want).abs().max() / want.abs().max())
     # the gated units in e4m3: half a step is 2^-4 of a value, or of its block's smallest normal one; what is
     # beyond that, of the block's largest value
     X, U = gq.dequantize_mx(blocks), gq.dequantize_mx(layer.up_blocks).view(-1, 2, layer.up.N, layer.up.K)
-    unit = 0.0
+    unit = []
     for t in range(tokens):
         for j, e in enumerate(ids[t].tolist()):
             g, u = (U[e].double() @ X[t].double())
             v = torch.nn.functional.silu(g) * u
             top = v.view(-1, 32).abs().amax(-1, keepdim=True).expand(-1, 32).reshape(-1)
             off = (A[pos[t][j]] - v).abs() - torch.maximum(v.abs(), top * 2.0 ** -13) / 16
-            unit = max(unit, float((off / top).max()))
-    return worst, unit
+            unit.append((off / top.clamp(min=1e-30)).max().clamp(min=0.0))
+    return tuple(float(torch.stack(x).max()) if x else 0.0 for x in (worst, unit))
 
 
 def run(hidden=2048, inner=1408, experts=64, top_k=8, prompt=500, steps=100, room=8):

@@ -3,6 +3,8 @@ any magnitude, values that are not finite, and sizes that take several turns, sl
 
 Codes, scales, chosen experts and plans have to be equal to the definitions in 64 bits; bounds of sums as in test_gpu_mx.py.
 """
+import importlib.util
+import os
 
 import numpy as np
 import pytest
@@ -238,3 +240,25 @@ def test_route_of_values_that_are_not_finite(T, score, n, k, best, dtype):
         near(w, ww, (6 + n / 32 + 16) * U * np.abs(ww) + 1e-38)
         off, rows_, pos = ref.plan(want, n)
         assert np.array_equal(host(plan.offsets), off) and np.array_equal(host(plan.pos), pos) and np.array_equal(host(plan.rows), rows_)
+
+
+# ---- the example ------------------------------------------------------------------------------------
+
+
+def test_the_example_sees_outputs_that_are_no_numbers():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "experts.py")
+    spec = importlib.util.spec_from_file_location("experts_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    layer = example.Layer(256, 96, 8, 2)
+    x = torch.randn((5, 256), generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    out, parts = layer.forward(x, torch.zeros_like(x))
+    worst, unit = example.check(layer, out, parts, 5)
+    assert worst < 1e-4 and unit < 5e-4
+    broken = out.clone()
+    broken[2, 17] = float("nan")
+    assert not example.check(layer, broken, parts, 5)[0] < 1e-4
+    assert not example.check(layer, torch.full_like(out, float("nan")), parts, 5)[0] < 1e-4
+    parts[-1].scales[3, 1] = 255
+    worst, unit = example.check(layer, out, parts, 5)
+    assert not worst < 1e-4 and not unit < 5e-4
