@@ -207,6 +207,24 @@ def test_norm_where_each_cta_takes_several_rows(M, K, dtype):
     assert torch.equal(t, want_h) and torch.equal(out.codes, q.codes) and torch.equal(out.scales, q.scales)
 
 
+def test_norm_of_rows_that_share_a_mark():
+    """A CTA marks the rows that it leaves for its end in 2048 bits: past 2048 turns, some share one."""
+    K, turns = 32, 2048
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count * 32
+    M = ctas * turns + 3 * ctas + 5
+    x = torch.randn((M, K), generator=torch.Generator("cuda").manual_seed(0), device="cuda").bfloat16()
+    wide = [0, 7, ctas + 3, ctas * turns + 1, ctas * (turns + 2) + 9, M - 1]
+    x[wide] *= 1e25
+    q = gq.rms_norm_mx(x, None, 1e-6)[1]
+    at = torch.tensor(sorted(set(wide) | {(r + d) % M for r in wide for d in (1, ctas, ctas * turns, M - ctas * turns)}), device="cuda")
+    want = ref.norm(host(x[at]), None, 1e-6)
+    codes, b = ref.quantize(want, ref.E4M3)
+    zero = want == 0
+    assert np.array_equal(host(q.scales[at])[:, :1], b) and np.array_equal(np.where(zero, 0, host(q.codes[at])), np.where(zero, 0, codes))
+    part = gq.rms_norm_mx(x[-2 * ctas:], None, 1e-6)[1]
+    assert torch.equal(q.codes[-2 * ctas:], part.codes) and torch.equal(q.scales[-2 * ctas:], part.scales)
+
+
 # ---- routing --------------------------------------------------------------------------------------
 
 
@@ -262,3 +280,59 @@ def test_the_example_sees_outputs_that_are_no_numbers():
     parts[-1].scales[3, 1] = 255
     worst, unit = example.check(layer, out, parts, 5)
     assert not worst < 1e-4 and not unit < 5e-4
+
+
+# ---- sizes that take several slices or launches -------------------------------------------------------
+
+
+def test_gathered_rows_in_slices():
+    """More rows than the workspace's share of 512 MB holds: a second slice begins in the middle of an expert."""
+    K, N, T = 32, 8, 1000
+    n = (512 << 20) // (K + 16)
+    R = n + 100000
+    off = np.array([0, 5000000, n + 40000, n + 40000, R - 9])
+    w, W = weights(1, 4, N, K)
+    x, X = mx(rows(2, T, K)[1])
+    gen = torch.Generator("cuda").manual_seed(0)
+    token = torch.randint(0, T, (R,), generator=gen, device="cuda", dtype=torch.int32)
+    plan = gq.ExpertPlan(dev(off.astype(np.int32)), token, dev(np.zeros((1, 1), np.int32)))
+    out = torch.full((R, N), 5.0, device="cuda")
+    gq.mul_mat_mxfp4(w, x, plan, gather=True, out=out)
+    assert gq.gq_last_error() == gq.GQ_OK
+    for e in range(4):
+        want, S = ref.product(X, W[e])
+        r = slice(int(off[e]), int(off[e + 1]))
+        i = token[r].long()
+        assert ((out[r].double() - dev(want)[i]).abs() <= dev(ref.product_tolerance(K) * S)[i]).all(), e
+    assert (out[R - 9:] == 5).all()
+
+
+def test_rows_that_take_several_launches():
+    """A launch of rows numbers 2^30 groups of eight values: quantization, reading back and the sum over experts go on behind them."""
+    K = 4096
+    n = ((1 << 30) - 1) // (K // 8)
+    M = n + 5
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(0))
+    q = gq.quantize_mx(x)
+    parts = [slice(0, 6), slice(n - 3, M)]
+    for r in parts:
+        p = gq.quantize_mx(x[r])
+        assert torch.equal(q.codes[r], p.codes) and torch.equal(q.scales[r], p.scales)
+    back = gq.dequantize_mx(q, torch.bfloat16)
+    for r in parts:
+        assert torch.equal(back[r], gq.dequantize_mx(gq.quantize_mx(x[r]), torch.bfloat16))
+    del back, q
+    e = gq.quantize_mx(x, gq.GQ_MX_E2M1)
+    for r in parts:
+        assert torch.equal(e.codes[r], gq.quantize_mx(x[r], gq.GQ_MX_E2M1).codes)
+    del e
+    y = torch.randn((7, K), device="cuda")
+    pos = torch.randint(0, 7, (M, 2), device="cuda", dtype=torch.int32)
+    w = torch.rand((M, 2), device="cuda")
+    ints = lambda m: torch.zeros(m, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = gq.experts_combine(y, gq.ExpertPlan(ints(2), ints(7), pos), w, residual=x, dtype=torch.bfloat16)
+    for r in parts:
+        p = gq.ExpertPlan(ints(2), ints(7), pos[r].contiguous())
+        assert torch.equal(out[r], gq.experts_combine(y, p, w[r].contiguous(), residual=x[r], dtype=torch.bfloat16))
+    del x, out
+    torch.cuda.empty_cache()
