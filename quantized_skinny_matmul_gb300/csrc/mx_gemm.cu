@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int filled = 0;
             for (int i = cluster; i < tiles && !failed; i += clusters) {
                 const Tile t = tile_at<BN>(p, where, i);
+                GQ_DCHECK(t.e < p.E && t.g < p.G && t.n > 0 && t.r0 >= p.lo && t.r0 + t.n <= p.hi, p.status);
                 const uint8_t *w = p.w + (((int64_t)t.e * C::NA * p.G + t.g) * p.KT + kt0) * MX_TILE_BYTES;
                 const int64_t up = (int64_t)p.G * p.KT * MX_TILE_BYTES;    // from the gate's tile to the up matrix's
                 const int parts = t.n > C::BOX ? C::PARTS : 1;
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     } else {
                         filled++;
                     }
+                    GQ_DCHECK(kt >= 0 && kt < p.KT && kt * 4 < p.S, p.status);
                     const uint32_t scales = smem_addr(smem + C::sb) + (uint32_t)(ring.st * C::SB_STAGE + x * 4);
 #pragma unroll
                     for (int j = 0; j < SROWS; j++)
@@ -699,6 +701,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Ring<C::SETS> set;
         for (int i = cluster; i < tiles && !failed; i += clusters, turn++) {
             const Tile t = tile_at<BN>(p, where, i);
+            GQ_DCHECK(t.n <= BN && t.r0 >= 0 && t.r0 + t.n <= p.R && t.g * MX_TILE < p.N, p.status);
             const int cols = (t.n + C::CW - 1) / C::CW;    // chunks in use
             float acc[C::NA][C::MINE][C::CW];
 #pragma unroll
@@ -914,6 +917,7 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint8_t *__restr
     // a warp takes rows in turn
     const int lane = threadIdx.x & 31, warps = gridDim.x * 8;
     for (int r = begin + (int)(blockIdx.x * 8 + (threadIdx.x >> 5)); r < end; r += warps) {
+        GQ_DCHECK(r >= lo && r < hi, status);
         const int from = __ldg(rows + r);
         const bool there = from >= 0 && from < x_rows;
         if (!there && lane == 0) atomicOr(status, STATUS_RANGE);

@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(route_threads(V)) route_kernel(const RoutePara
             id = choose<V, T>(p, t, z, bias, group, m, sum, shared, lane);
             if (lane < p.k) {
                 // (no value is NaN, so every place is filled; a mistake in that would not read out of bounds)
+                GQ_DCHECK((uint32_t)id < (uint32_t)p.E, p.status);
                 id = (uint32_t)id < (uint32_t)p.E ? id : -1;
                 const float chosen = id < 0 ? -INFINITY : plain(row[id]);
                 w = p.sigmoid ? 1.0f / (1.0f + expf(-chosen)) : m > -INFINITY ? expf(chosen - m) / sum : 0.0f;
