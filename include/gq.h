@@ -87,10 +87,10 @@ const char *gq_last_error_message(void);
 
 /* Sticky device-side status of the current device: GQ_ERR_TIMEOUT if a kernel
  * gave up a bounded wait since the last call, else GQ_ERR_DEVICE_CHECK if a
- * bounds check of a GQ_DEBUG build failed (a library bug; those builds check the
- * indices the kernels derive from their arguments and never trap), else
- * GQ_ERR_INVALID_ARG if a length or position read on the device was out of range
- * (the KV-cache calls), else GQ_OK; reading clears it and, after a timeout, re-zeroes the
+ * bounds check of a GQ_DEBUG build failed (a library bug; in those builds the products, the
+ * INT8 cache's attention and the router check the indices they derive and never trap), else
+ * GQ_ERR_INVALID_ARG if a length, position, offset or row index read on the device was out of
+ * range (the KV-cache calls, plans and routing), else GQ_OK; reading clears it and, after a timeout, re-zeroes the
  * workspace counters of the device.  Synchronizes the current device first. */
 gq_status gq_last_error(void);
 
@@ -351,7 +351,8 @@ gq_status gq_mul_mat_q4_0_f32_noalloc(const void *q4_repacked, const float *src1
  * enqueued right before a product never writes that product's weights (true in
  * a decode loop, where weights are written once at load time); the GEMV then
  * reads the weights before that wait.  Default 0: weights are read only after
- * every earlier kernel in the stream has finished.  Process-wide. */
+ * every earlier kernel in the stream has finished.  Process-wide.  The products of
+ * microscaled weights (below) always wait. */
 gq_status gq_set_static_weights(int enable);
 int gq_get_static_weights(void);
 
@@ -611,7 +612,7 @@ typedef struct gq_expert_rows {
  * at dst + r * ldd, N values of `type` (rounded once), ldd >= N.  Without a plan W is one matrix and
  * row m of dst is row m of x; with one W holds E matrices and row r of dst is the product of
  * its row of x with its expert's matrix.  Results do not depend on timing.  A plan with `rows` and more than 14 rows
- * for an expert on average uses the stream's workspace, up to 512 MB (grown on demand, as for the products above;
+ * for an expert on average uses up to 512 MB of the stream's workspace (grown on demand, as for the products above;
  * GQ_ERR_NO_MEMORY while the stream is captured: run the call once before capturing). */
 gq_status gq_mul_mat_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *dst,
                               int64_t ldd, gq_type type, int64_t N, int64_t K, cudaStream_t stream);
@@ -626,7 +627,9 @@ gq_status gq_mul_mat_mxfp4(const void *repacked, const void *x, int64_t ldx, gq_
 /* A gated unit: gate = X . Wg^T, up = X . Wu^T, and out = silu(gate) * up = gate / (1 + exp(-gate)) * up
  * in e4m3 blocks (codes [R][F], scales [R][gq_mx_scale_cols(F)]; R the rows of x without a plan).
  * Repacked weights: for each expert (or once) the matrix Wg [F][K], then Wu [F][K], so 2 E (or 2) matrices in
- * gq_repack_mxfp4.  F a multiple of 32.  gate and up are f32 sums as above. */
+ * gq_repack_mxfp4.  F a multiple of 32.  gate and up are f32 sums as above; silu is formed in f32, within
+ * (1.25 |gate| + 10) 2^-24 of itself, and is 0 for gates below -88.7.  (This form only: no biases, no clamped or scaled
+ * gates, gate and up as two matrices, not row by row in turn.) */
 gq_status gq_swiglu_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *codes,
                              uint8_t *scales, int64_t F, int64_t K, cudaStream_t stream);
 

@@ -39,7 +39,8 @@ gq_status check_ptr4(const void *p, const char *name) {
 }
 
 // the operands of a product: activations, plan, sizes
-gq_status check_product(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, int64_t N, int64_t K, int64_t parts) {
+gq_status check_product(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, int64_t N, int64_t K,
+                        int64_t parts) {
     GQ_TRY(check_sizes(1, N, K));
     if (!x) return fail(GQ_ERR_INVALID_ARG, "x is NULL");
     if (x->rows <= 0 || x->rows >= (1LL << 30)) return fail(GQ_ERR_INVALID_ARG, "x->rows must be in [1, 2^30) (got %lld)", (long long)x->rows);
@@ -130,7 +131,7 @@ gq_status gq_rms_norm_mx(const void *x, int64_t ldx, const void *residual, int64
 size_t gq_mxfp4_repacked_bytes(int64_t count, int64_t N, int64_t K) {
     if (count <= 0 || N <= 0 || K <= 0 || K % QK || N > (1LL << 30) || K > (1LL << 30) || count > 2048) return 0;
     const int64_t G = (N + MX_TILE - 1) / MX_TILE, KT = (K + MX_TILE - 1) / MX_TILE;
-    // tile rows are 32-bit coordinates of a tensor copy
+    // 2^24 tiles are 146 GB; their numbers stay far within 32 bits
     if (G * KT > (1LL << 24) || count * G * KT >= (1LL << 24)) return 0;
     return (size_t)(count * G * KT) * (MX_TILE_CODES + MX_TILE_SCALES);
 }
@@ -139,7 +140,8 @@ gq_status gq_repack_mxfp4(const void *codes, const uint8_t *scales, void *repack
                           int64_t K, cudaStream_t stream) {
     GQ_TRY(check_sizes(1, N, K));
     const size_t bytes = gq_mxfp4_repacked_bytes(count, N, K);
-    if (!bytes) return fail(GQ_ERR_INVALID_ARG, "count=%lld matrices of %lld x %lld: out of range", (long long)count, (long long)N, (long long)K);
+    if (!bytes)
+        return fail(GQ_ERR_INVALID_ARG, "count=%lld matrices of %lld x %lld: out of range", (long long)count, (long long)N, (long long)K);
     GQ_TRY(check_ptr(codes, "codes"));
     GQ_TRY(check_ptr(scales, "scales"));
     GQ_TRY(check_ptr(repacked, "repacked"));
@@ -205,17 +207,20 @@ gq_status gq_route(const gq_router *router, const void *logits, int64_t ldl, gq_
     if (!router) return fail(GQ_ERR_INVALID_ARG, "router is NULL");
     const gq_router &r = *router;
     if (r.E < 1 || r.E > 1024) return fail(GQ_ERR_INVALID_ARG, "E must be in [1, 1024] (got %lld)", (long long)r.E);
-    if (r.score != GQ_SCORE_SOFTMAX && r.score != GQ_SCORE_SIGMOID) return fail(GQ_ERR_INVALID_ARG, "score=%lld is no gq_score", (long long)r.score);
+    if (r.score != GQ_SCORE_SOFTMAX && r.score != GQ_SCORE_SIGMOID)
+        return fail(GQ_ERR_INVALID_ARG, "score=%lld is no gq_score", (long long)r.score);
     if (r.groups < 1 || r.groups > 32 || r.E % r.groups || r.top_groups < 1 || r.top_groups > r.groups)
         return fail(GQ_ERR_INVALID_ARG, "need 1 to 32 groups that divide E=%lld, and top_groups of them (got %lld, %lld)", (long long)r.E,
                     (long long)r.groups, (long long)r.top_groups);
-    if (r.group_best != 1 && r.group_best != 2) return fail(GQ_ERR_INVALID_ARG, "group_best must be 1 or 2 (got %lld)", (long long)r.group_best);
+    if (r.group_best != 1 && r.group_best != 2)
+        return fail(GQ_ERR_INVALID_ARG, "group_best must be 1 or 2 (got %lld)", (long long)r.group_best);
     if (r.top_k < 1 || r.top_k > 32 || r.top_k > r.top_groups * (r.E / r.groups))
         return fail(GQ_ERR_INVALID_ARG, "top_k must be in [1, 32] and at most the %lld experts that can be chosen (got %lld)",
                     (long long)(r.top_groups * (r.E / r.groups)), (long long)r.top_k);
     if (!std::isfinite(r.factor)) return fail(GQ_ERR_INVALID_ARG, "factor is not finite");
     GQ_TRY(check_type(type, "type"));
-    if (T <= 0 || T >= (1LL << 30) || T * r.top_k >= (1LL << 30)) return fail(GQ_ERR_INVALID_ARG, "T must be positive, T * top_k below 2^30 (got %lld)", (long long)T);
+    if (T <= 0 || T >= (1LL << 30) || T * r.top_k >= (1LL << 30))
+        return fail(GQ_ERR_INVALID_ARG, "T must be positive, T * top_k below 2^30 (got %lld)", (long long)T);
     if (ldl < r.E || ldl > (1LL << 31)) return fail(GQ_ERR_INVALID_ARG, "ldl=%lld must be at least E=%lld", (long long)ldl, (long long)r.E);
     GQ_TRY(check_ptr(logits, "logits"));
     if (r.bias) GQ_TRY(check_ptr(r.bias, "bias"));

@@ -11,9 +11,10 @@
 //              them (16-row tiles; for larger ones that would be too many copies for a thread, and a kernel in front
 //              brings the rows into the plan's order);
 //   warps 2, 3     copy the activations' scales (of one or two rows of values: quantize them);
-//   warps 12 .. 19  two teams, for every other stage each (a stage is mostly latency).  A weight row per thread: 64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of
-//              each (the form of 4-bit operands in tensor memory), and go there, and so do the scales of both
-//              operands.  The tiles hold the codes so that three instructions place eight of them;
+//   warps 12 .. 19  two teams, for every other stage each (a stage is mostly latency).  A weight row per thread:
+//              64 bytes of packed codes become 128 bytes, a code in bits 2 .. 5 of each (the form of 4-bit operands
+//              in tensor memory), and go there, and so do the scales of both operands.  The tiles hold the codes so
+//              that three instructions place eight of them;
 //   warp 1     one thread issues 4 MMAs a stage (8 for the gated unit, whose gate and up tiles share the
 //              activations).  The thread is elected, not picked by its lane: the compiler then keeps the
 //              descriptors in uniform registers (measured: 39 cycles per MMA of 16 columns, not 80);
@@ -23,9 +24,10 @@
 // CTAs take tiles in turn (persistent), those of one expert's weight rows next to each other.  With few
 // tiles a cluster of 2 or 4 CTAs shares a tile's columns; the first adds the others' sums in order.
 //
-// Measured: 2047 rows by [4096, 11008] 81 us, 2.3 PFLOP/s, 13 TB/s from L2 (each CTA fetches its own operands: that bounds the
-// large tiles; the tensor pipe is busy for 48 %); 61 tokens on 8 of 64 experts of [2816, 2048] 48 us, 4.2 TB/s from memory
-// (a stage's latencies); a row by [4096, 4096] 6.5 us.
+// Measured, products of blocks in a captured graph, weights from memory: 2047 rows by [4096, 11008] 75 us, 2.5 PFLOP/s (81
+// under ncu: 13 TB/s from L2, as each CTA fetches its own operands, which bounds the large tiles; the tensor pipe is busy for
+// 48 %); 61 tokens on 8 of 64 experts of [2816, 2048] 50 us, 4.0 TB/s from memory (a stage's latencies); a row by
+// [4096, 4096] 8.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -280,9 +282,10 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, unsi
     return false;
 }
 
-// x / (1 + exp(-x)); the exponential and the reciprocal are the fast ones, off by a few units of f32.  Both
+// x / (1 + exp(-x)), within (1.25 |x| + 10) 2^-24 of itself: the exponential's argument is a rounded product with a rounded
+// log2(e), off by 1.22 |x| 2^-24 in e's exponent, the fast exponential by 2^-22 and the reciprocal by 2^-23.  Both
 // flush denormals: of the exponential that leaves 1 + 0, and the reciprocal is taken of a quarter of the sum, so that
-// it has none.
+// it has none.  From -88.73 down the exponential is infinite and this 0, where x exp(x) is 2.6e-37 or less.
 __device__ __forceinline__ float swish(float x) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
@@ -891,7 +894,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Rows lo .. hi - 1 of the plan, as far as experts have them, brought into its order: codes and scales, 16 bytes a thread and
-// turn.  A row whose index is out of range becomes zeros.  18 us for 32760 rows of 2048; four-row copies by the product's one
+// turn.  A row whose index is out of range becomes zeros.  19 us for 32760 rows of 2048; four-row copies by the product's one
 // copying thread keep up with tiles of 16 rows only.  What experts have is from the first begin to the largest end of the
 // ranges that are in [0, R], as the product sees them (one that overlaps an earlier range it refuses, but such a row does no
 // harm here): with offsets that go back at the end, offsets[E] is not the largest.

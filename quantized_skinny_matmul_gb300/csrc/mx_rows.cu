@@ -1,8 +1,8 @@
 // mx_rows.cu -- rows of microscaled values: quantization, reading back, the tiles of 4-bit
 // weights, the root-mean-square norm with its output in blocks, and the sum over a token's experts.
 // A thread takes eight values (16 or 32 bytes), four lanes a block.  The bounds are memory, for the norm also instructions:
-// f32 weights of [11008, 4096] to 4 bits in 33 us cold (5.8 TB/s), the norm of 8191 bf16 rows of 4096 with residual 65 us
-// (3.9 TB/s), the sum over 8 experts of 4095 tokens 46 us (6.4 TB/s).
+// f32 weights of [11008, 4096] to 4 bits in 33 us cold (5.8 TB/s), into tiles 11 us (4.5 TB/s), the norm of 8191 bf16 rows of
+// 4096 with residual 53 us in a captured graph (4.4 TB/s; 65 cold), the sum over 8 experts of 4095 tokens 46 us (6.4 TB/s).
 #include <algorithm>
 
 #include "mx.cuh"
@@ -596,8 +596,9 @@ gq_status norm_launch(const NormParams &p, int threads, cudaStream_t s) {
                       "norm launch");
 }
 
-// One group of 8 values per thread keeps a lone row's chain short; where rows abound (several for each
-// SM) threads take two, for fewer and longer turns.  Rows of more than 16384 values need four.
+// One group of 8 values per thread keeps a lone row's chain short (a row of 4096 2.8 us, by two 3.9); where rows abound
+// (several for each SM) threads take two, for fewer and longer turns (8191 bf16 rows 53 us, by one 62; f32, more registers, 99
+// and 96).  Rows of more than 16384 values need four.
 template <typename T>
 gq_status norm_width(const NormParams &p, cudaStream_t s) {
     const int groups = p.K / 8;
