@@ -565,10 +565,10 @@ gq_status gq_dequantize_mx(const void *codes, const uint8_t *scales, gq_mx_kind 
  * one), y_j = h_j * weight_j / sqrt(mean(h^2) + eps).  x, residual and h are rows of `type` at
  * stride ldx, ldr, ldh (as in gq_quantize_mx); weight f32 [K] or NULL (1).  Outputs, each optional
  * (at least one): h (NULL: not kept; h may be x or residual), y [M][K] of `ytype`, and the e4m3
- * blocks of y, codes with scales.  The blocks are those of the exact y: where f32 does not settle
- * a code or a scale, it is decided in two f32 terms (48 bits), and in 64 bits where squares, sums or products leave the
- * range of f32 (a row whose root mean square is not between 2^-30 and 2^60; a block of very large or small y).  y itself is
- * formed in f32, within 2^-20 of itself or 2^-120, and rounded to ytype.
+ * blocks of y, codes with scales.  The blocks are those of the exact y: where f32 does not settle a code or a scale,
+ * it is decided in two f32 terms (48 bits), and in 64 bits where squares, sums or products leave the range of f32 (a
+ * row whose root mean square is not between 2^-30 and 2^60, a block of very large or small y).  y itself is formed in
+ * f32, within 2^-20 of itself or 2^-120, and rounded to ytype.
  * K up to 32768. */
 gq_status gq_rms_norm_mx(const void *x, int64_t ldx, const void *residual, int64_t ldr, gq_type type,
                          const float *weight, double eps, void *h, int64_t ldh, void *y, gq_type ytype,
@@ -627,9 +627,9 @@ gq_status gq_mul_mat_mxfp4(const void *repacked, const void *x, int64_t ldx, gq_
 /* A gated unit: gate = X . Wg^T, up = X . Wu^T, and out = silu(gate) * up = gate / (1 + exp(-gate)) * up
  * in e4m3 blocks (codes [R][F], scales [R][gq_mx_scale_cols(F)]; R the rows of x without a plan).
  * Repacked weights: for each expert (or once) the matrix Wg [F][K], then Wu [F][K], so 2 E (or 2) matrices in
- * gq_repack_mxfp4.  F a multiple of 32.  gate and up are f32 sums as above; silu is formed in f32, within
- * (1.25 |gate| + 10) 2^-24 of itself, and is 0 for gates below -88.7.  (This form only: no biases, no clamped or scaled
- * gates, gate and up as two matrices, not row by row in turn.) */
+ * gq_repack_mxfp4.  F a multiple of 32.  gate and up are f32 sums as above; silu is formed in f32,
+ * within (1.25 |gate| + 10) 2^-24 of itself, and is 0 for gates below -88.7.  (This form only: no biases, no
+ * clamped or scaled gates, gate and up as two matrices, not row by row in turn.) */
 gq_status gq_swiglu_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq_expert_rows *plan, void *codes,
                              uint8_t *scales, int64_t F, int64_t K, cudaStream_t stream);
 
@@ -640,9 +640,9 @@ gq_status gq_swiglu_mxfp4_mx(const void *repacked, const gq_mx_rows *x, const gq
  * the largest c are chosen, largest first; equal values: the lower index, of groups too.
  * Their weights are the scores p, divided by their sum if renormalize is set (left as they are
  * if the sum is 0), times factor.  The choice is that of exact arithmetic: values that f32 cannot tell
- * apart are compared in 64 bits; the weights are formed in f32.  Among logits and biases NaN counts as -infinity and
- * +infinity as the largest finite f32.  An expert whose logit is -infinity has score 0; a row whose logits all are has
- * weights 0 (softmax).  An expert whose bias is -infinity is chosen only when there is no other.
+ * apart are compared in 64 bits; the weights are formed in f32.  Among logits and biases NaN counts as -infinity
+ * and +infinity as the largest finite f32.  An expert whose logit is -infinity has score 0; a row whose logits all
+ * are has weights 0 (softmax).  An expert whose bias is -infinity is chosen only when there is no other.
  * E 1 .. 1024, top_k 1 .. 32, 1 to 32 groups that divide E, top_k <= top_groups * E / groups. */
 typedef enum { GQ_SCORE_SOFTMAX = 0, GQ_SCORE_SIGMOID = 1 } gq_score;
 typedef struct gq_router {
